@@ -21,6 +21,13 @@
  *       out, queued in order on one stream.
  *   paged_decode_check_tables
  *       validation of the block-table entries a decode run reads.
+ *   paged_kv_tables
+ *       block tables, slot maps and lengths of a step, made on the GPU.
+ *   paged_latent_append / paged_latent_decode_plan / _run
+ *       latent attention in its absorbed form: one cached row per token for
+ *       all heads, written to a paged pool and decoded over it.
+ *   batch_latent_prefill_plan / batch_latent_prefill_run
+ *       its expanded form: ragged prefill with a shared rotary key part.
  *   paged_kv_gather
  *       test hook: copies paged K or V rows to a dense buffer through the same
  *       page addressing the decode kernels use.
@@ -69,8 +76,9 @@ extern "C" {
 #define PKA_ERR_UNSUPPORTED (-2)          /* valid on the pages, not built here        */
 #define PKA_ERR_WORKSPACE_TOO_SMALL (-3)  /* workspace_bytes below the plan's need     */
 #define PKA_ERR_CUDA (-4)                 /* a CUDA runtime/driver call failed         */
-#define PKA_ERR_DEVICE_BOUNDS (-5)        /* a block-table entry outside the pool      */
+#define PKA_ERR_DEVICE_BOUNDS (-5)        /* a block-table or slot entry outside the pool */
 #define PKA_ERR_DEVICE_TIMEOUT (-6)       /* a kernel gave up on a bounded wait        */
+#define PKA_ERR_DEVICE_CAPACITY (-7)      /* paged_kv_tables: a step that does not fit */
 
 /* ---- enums ------------------------------------------------------------- */
 #define PKA_DTYPE_BF16 0
@@ -547,6 +555,252 @@ int batch_prefill_run(const pka_prefill_plan* plan, const void* q, int64_t q_str
                       int64_t q_stride_head, const void* k, const void* v, int64_t kv_stride_tok,
                       int64_t kv_stride_head, void* out, float* lse, void* workspace,
                       size_t workspace_bytes, void* stream);
+
+/* ======================================================================== */
+/* Page tables and slot maps on the GPU                                      */
+/* ======================================================================== */
+
+/*
+ * Give a step's new tokens their pages and slots: grows the block tables from
+ * a list of free pages and writes one cache slot per new token, all on the
+ * device (no host copy of the lengths is needed, so the call may be captured).
+ *
+ * kv_lens       int32 [batch_size] device: tokens of each request cached so
+ *               far; its table row holds their ceil(kv_len / page_size) pages.
+ * new_lens      int32 [batch_size] device: tokens the step adds (0 allowed).
+ * batch_size    1 <= B <= 16384.
+ * free_pages    int32 [num_free] device: free page ids; entries from
+ *               free_head[0] on are taken in order, requests in batch order
+ *               (so the result does not depend on scheduling).
+ * free_head     int32 [1] device.
+ * page_size     1 .. 65536.
+ * block_tables  int32 [B, max_pages_per_seq] device, row stride bt_row_stride:
+ *               entries ceil(kv/ps) .. ceil((kv+new)/ps) - 1 are written,
+ *               every other entry is left as it was.
+ * seq_lens      int32 [B] device, out: kv_len + new_len.
+ * qo_indptr     int32 [B + 1] device, out: cumulative new_lens from 0.
+ * slot_map      int64 [num_slots] device, out: for new token t of the batch
+ *               (request order) page * page_size + slot in page; -1 at and
+ *               behind the last new token.  num_slots >= 1.
+ * free_head_out int32 [1] device, out: free_head plus the pages taken.
+ * status        NULL or int32 [1] device status word (pka_status_check).
+ *
+ * A step that does not fit -- a negative length, a request longer than
+ * max_pages_per_seq pages or 2^31 - 1 tokens, more tokens than num_slots, more
+ * pages than free_pages has left, a negative free_head -- changes nothing: the
+ * tables stay, seq_lens repeats kv_lens, qo_indptr is all 0, slot_map all -1,
+ * free_head_out repeats free_head, and the status word gets its capacity bit
+ * (PKA_ERR_DEVICE_CAPACITY).  Page ids are not checked here: a bad one shows
+ * up in paged_latent_append or paged_decode_check_tables.
+ * Outputs must not overlap the inputs (checked by address): to step a captured
+ * loop, copy seq_lens over kv_lens and free_head_out over free_head.
+ */
+int paged_kv_tables(const int32_t* kv_lens, const int32_t* new_lens, int32_t batch_size,
+                    const int32_t* free_pages, int32_t num_free, const int32_t* free_head,
+                    int32_t page_size, int32_t* block_tables, int64_t bt_row_stride,
+                    int32_t max_pages_per_seq, int32_t* seq_lens, int32_t* qo_indptr,
+                    int64_t* slot_map, int64_t num_slots, int32_t* free_head_out, int32_t* status,
+                    void* stream);
+
+/*
+ * Wait for `stream`, then read and clear a caller-owned status word, as
+ * paged_decode_plan_check does for a plan's: PKA_OK, PKA_ERR_DEVICE_CAPACITY
+ * (paged_kv_tables), PKA_ERR_DEVICE_BOUNDS (paged_latent_append) or
+ * PKA_ERR_DEVICE_TIMEOUT.  Synchronises; not for capture.
+ */
+int pka_status_check(int32_t* status_dev, void* stream);
+
+/* ======================================================================== */
+/* Latent attention                                                          */
+/* ======================================================================== */
+
+/*
+ * Latent attention keeps one row per token for all heads: latent_dim values
+ * that every head reads as its key and as its value, followed by rope_dim
+ * rotary key values.  The paged latent pool is [num_pages, page_size,
+ * latent_dim + rope_dim] bf16 or f16, element (page, slot, d) at
+ * pages + page*stride_page + slot*(latent_dim + rope_dim) + d, stride_page a
+ * multiple of 8, the base 16-byte aligned.
+ *
+ * Write new rows into the pool: row t, [latent[t] | rope[t]], goes to slot
+ * slot_map[t] = page * page_size + slot in page (paged_kv_tables).
+ * latent     the pool's type, (t, d) at latent + t*latent_stride + d.
+ * rope       (t, d) at rope + t*rope_stride + d, rotated already.  Both 16-byte
+ *            aligned with strides that are multiples of 8.
+ * slot_map   int64 [num_tokens] device; a negative entry skips its row.  An
+ *            entry at or past num_pages * page_size skips it too and sets the
+ *            slot bit of the status word (PKA_ERR_DEVICE_BOUNDS).  Entries
+ *            must be distinct: of two rows for one slot either may remain, or
+ *            parts of both.
+ * latent_dim, rope_dim  multiples of 8, rope_dim may be 0 (rope then NULL).
+ * status     NULL or int32 [1] device status word (pka_status_check).
+ */
+int paged_latent_append(const void* latent, int64_t latent_stride, const void* rope,
+                        int64_t rope_stride, int32_t latent_dim, int32_t rope_dim,
+                        const int64_t* slot_map, int64_t num_tokens, void* pages,
+                        int64_t num_pages, int32_t page_size, int64_t stride_page, int32_t dtype,
+                        int32_t* status, void* stream);
+
+/*
+ * Absorbed decode over a paged latent pool.  With q the query already
+ * multiplied by the key projection (latent_dim values) and its rotary part
+ * behind it, per row and head
+ *   s_j = scale * q . pages[token j],  p = softmax(s),
+ *   out = output_scale * sum_j p_j * pages[token j][0 .. latent_dim)
+ * which the caller multiplies by the value projection.
+ *
+ * batch_size  B.  num_heads 1 .. 1024: all heads share the one cached row.
+ * latent_dim  256 or 512.  rope_dim 64.
+ * page_size   a multiple of 8 in [8, 256].
+ * max_pages_per_seq, num_pages, q_len, flags, num_sms as for paged_decode_plan;
+ *             num_heads * rows per request <= 65536.
+ * mask        PKA_MASK_DENSE or PKA_MASK_CAUSAL (row i of L sees keys
+ *             0 .. n-L+i; a row that sees none gives 0 and an LSE of -inf).
+ * scale       finite; there is no default, the absorbed form hides
+ *             the head size it stands for.
+ * freeze_seq_lens  nonzero: the plan keeps the host lengths.  Zero: a run reads
+ *             the live lengths, each clamped to [0, the planned length].
+ * dtype       PKA_DTYPE_BF16 or PKA_DTYPE_F16: q and the pool.
+ * out_dtype   PKA_DTYPE_BF16, PKA_DTYPE_F16 or PKA_DTYPE_F32.
+ */
+typedef struct pka_latent_desc {
+  int32_t batch_size;
+  int32_t num_heads;
+  int32_t latent_dim;
+  int32_t rope_dim;
+  int32_t page_size;
+  int32_t max_pages_per_seq;
+  int64_t num_pages;
+  int32_t dtype;
+  int32_t out_dtype;
+  int32_t q_len;
+  int32_t mask;
+  float scale;
+  float output_scale;
+  int32_t return_lse;
+  int32_t freeze_seq_lens;
+  int32_t num_sms;
+  int32_t flags;
+} pka_latent_desc;
+
+typedef struct pka_latent_plan pka_latent_plan; /* opaque latent decode plan */
+
+/* Summary of a latent decode plan. */
+typedef struct pka_latent_plan_info {
+  int32_t num_segments;     /* runs of key tiles: each is one CTA per row block      */
+  int32_t num_items;        /* pieces of requests in them                             */
+  int32_t num_split;        /* requests cut into more than one piece                  */
+  int32_t row_tile;         /* query rows (token, head) of a CTA: 16, 32 or 64        */
+  int32_t row_blocks;       /* CTAs side by side over a request's rows                */
+  int32_t partial_rows;     /* fp32 partial rows in the workspace                     */
+  int64_t workspace_bytes;
+  int32_t total_q;
+  int32_t num_sms;
+} pka_latent_plan_info;
+
+/*
+ * Build a latent decode plan from host copies of the lengths (before capture).
+ * seq_lens_kv_host [B], each in [0, C * page_size].
+ * qo_indptr_host   NULL (fixed q_len) or [B+1]: cumulative query offsets from
+ *                  0, non-decreasing.  A request without rows writes nothing.
+ */
+int paged_latent_decode_plan(pka_latent_plan** plan_out, const pka_latent_desc* desc,
+                             const int32_t* seq_lens_kv_host, const int32_t* qo_indptr_host,
+                             size_t* workspace_bytes_out, void* stream);
+
+/* Re-plan in place for a new batch, as paged_decode_plan_update does. */
+int paged_latent_decode_plan_update(pka_latent_plan* plan, int32_t batch_size,
+                                    const int32_t* seq_lens_kv_host,
+                                    const int32_t* qo_indptr_host, size_t* workspace_bytes_out,
+                                    void* stream);
+
+/* Free a plan (NULL is ignored); no run that uses it may still execute. */
+void paged_latent_decode_plan_destroy(pka_latent_plan* plan);
+
+int paged_latent_decode_plan_info(const pka_latent_plan* plan, pka_latent_plan_info* info);
+
+/*
+ * Copy the plan's host arrays out (for tests of the planner).  items
+ * [num_items * 4] int32: (request, first 64-key tile, end tile, partial state
+ * index inside the request or -1 when it is whole); segments [num_segments + 1]:
+ * each segment's first item.  Either may be NULL.
+ */
+int paged_latent_decode_plan_export(const pka_latent_plan* plan, int32_t* items,
+                                    int32_t* segments);
+
+/* As paged_decode_plan_check, for the latent plan's device status word. */
+int paged_latent_decode_plan_check(const pka_latent_plan* plan, void* stream);
+
+/*
+ * Run the planned latent decode.
+ * q          the plan's dtype, rows [total_q] x [num_heads] x (latent_dim +
+ *            rope_dim), (t, h, d) at q + t*q_stride_tok + h*q_stride_head + d;
+ *            16-byte aligned, strides multiples of 8.
+ * pages      the latent pool, stride_page as above.
+ * block_tables, bt_row_stride, seq_lens_kv_dev as for paged_decode_run.
+ *            Entries past a request's last page are not read; cache rows past
+ *            its last token may hold anything, infinities and NaN included.
+ *            An entry outside [0, num_pages) reads as zeros, never out of
+ *            bounds.
+ * out        [total_q, num_heads, latent_dim] contiguous, out_dtype, 16-byte
+ *            aligned; rows past total_q are not touched.
+ * lse        NULL or fp32 [total_q, num_heads]: log2 of the sum over the row's
+ *            keys of exp(scale * q . k).  Required when the plan has return_lse.
+ * workspace  at least the plan's workspace_bytes, 256-byte aligned: the split
+ *            requests' partial states.  Runs that may overlap on the GPU need a
+ *            workspace each; they may share the plan.
+ */
+int paged_latent_decode_run(const pka_latent_plan* plan, const void* q, int64_t q_stride_tok,
+                            int64_t q_stride_head, const void* pages, int64_t stride_page,
+                            const int32_t* block_tables, int64_t bt_row_stride,
+                            const int32_t* seq_lens_kv_dev, void* out, float* lse,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Expanded prefill: ragged attention whose heads have a key of nope_dim values
+ * of their own and rope_dim rotary values that all heads share, and a value of
+ * value_dim:  s = sm_scale * (q[0 .. nope) . k_nope + q[nope ..) . k_rope).
+ *
+ * nope_dim    128.  rope_dim 64.  value_dim 128.
+ * num_heads   query and key/value heads alike.
+ * mask, output_scale, return_lse, flags, dtype, out_dtype as for
+ *             batch_prefill_plan; sm_scale NaN selects 1/sqrt(nope + rope).
+ */
+typedef struct pka_latent_prefill_desc {
+  int32_t batch_size;
+  int32_t num_heads;
+  int32_t nope_dim;
+  int32_t rope_dim;
+  int32_t value_dim;
+  int32_t dtype;
+  int32_t out_dtype;
+  int32_t mask;
+  float sm_scale;
+  float output_scale;
+  int32_t return_lse;
+  int32_t flags;
+} pka_latent_prefill_desc;
+
+/* The plan is a prefill plan: batch_prefill_plan_check and
+ * batch_prefill_plan_destroy take it, batch_prefill_run does not. */
+int batch_latent_prefill_plan(pka_prefill_plan** plan_out, const pka_latent_prefill_desc* desc,
+                              const int32_t* qo_indptr_host, const int32_t* kv_indptr_host,
+                              int32_t* num_tiles_out, void* stream);
+
+/*
+ * q       [total_q, H, nope + rope]: (t, h, d) at q + t*q_stride_tok + h*q_stride_head + d.
+ * k_nope, v  [total_kv, H, nope] and [total_kv, H, value]: (t, h, d) at
+ *         base + t*kv_stride_tok + h*kv_stride_head + d, one set of strides for
+ *         both (they may be the two parts of one projection's output).
+ * k_rope  [total_kv, rope]: (t, d) at k_rope + t*rope_stride + d.
+ *         All strides multiples of 8 elements, bases 16-byte aligned.
+ * out     [total_q, H, value] contiguous, out_dtype, 16-byte aligned.
+ * lse     NULL or fp32 [total_q, H] base-2 LSE (required with return_lse).
+ */
+int batch_latent_prefill_run(const pka_prefill_plan* plan, const void* q, int64_t q_stride_tok,
+                             int64_t q_stride_head, const void* k_nope, const void* k_rope,
+                             int64_t rope_stride, const void* v, int64_t kv_stride_tok,
+                             int64_t kv_stride_head, void* out, float* lse, void* stream);
 
 /* ======================================================================== */
 /* Test hook                                                                 */

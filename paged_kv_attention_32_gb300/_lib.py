@@ -17,6 +17,7 @@ PKA_ERR_WORKSPACE_TOO_SMALL = -3
 PKA_ERR_CUDA = -4
 PKA_ERR_DEVICE_BOUNDS = -5
 PKA_ERR_DEVICE_TIMEOUT = -6
+PKA_ERR_DEVICE_CAPACITY = -7
 
 PKA_DTYPE_BF16, PKA_DTYPE_F16, PKA_DTYPE_F32 = 0, 1, 2
 PKA_MASK_DENSE, PKA_MASK_CAUSAL, PKA_MASK_VARIABLE_WINDOW = 0, 1, 2
@@ -34,6 +35,11 @@ EXPORTED = (
     "attn_merge_lse",
     "batch_prefill_plan", "batch_prefill_plan_fixed", "batch_prefill_plan_destroy", "batch_prefill_plan_check",
     "batch_prefill_run",
+    "paged_kv_tables", "pka_status_check", "paged_latent_append",
+    "paged_latent_decode_plan", "paged_latent_decode_plan_update",
+    "paged_latent_decode_plan_destroy", "paged_latent_decode_plan_info",
+    "paged_latent_decode_plan_export", "paged_latent_decode_plan_check",
+    "paged_latent_decode_run", "batch_latent_prefill_plan", "batch_latent_prefill_run",
     "paged_kv_gather", "pka_wait_timeout_probe",
 )
 
@@ -86,6 +92,39 @@ class PrefillDesc(ctypes.Structure):
     ]
 
 
+class LatentDesc(ctypes.Structure):
+    _fields_ = [
+        ("batch_size", ctypes.c_int32), ("num_heads", ctypes.c_int32),
+        ("latent_dim", ctypes.c_int32), ("rope_dim", ctypes.c_int32),
+        ("page_size", ctypes.c_int32), ("max_pages_per_seq", ctypes.c_int32),
+        ("num_pages", ctypes.c_int64), ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+        ("q_len", ctypes.c_int32), ("mask", ctypes.c_int32), ("scale", ctypes.c_float),
+        ("output_scale", ctypes.c_float), ("return_lse", ctypes.c_int32),
+        ("freeze_seq_lens", ctypes.c_int32), ("num_sms", ctypes.c_int32),
+        ("flags", ctypes.c_int32),
+    ]
+
+
+class LatentPlanInfo(ctypes.Structure):
+    _fields_ = [
+        ("num_segments", ctypes.c_int32), ("num_items", ctypes.c_int32),
+        ("num_split", ctypes.c_int32), ("row_tile", ctypes.c_int32),
+        ("row_blocks", ctypes.c_int32), ("partial_rows", ctypes.c_int32),
+        ("workspace_bytes", ctypes.c_int64), ("total_q", ctypes.c_int32),
+        ("num_sms", ctypes.c_int32),
+    ]
+
+
+class LatentPrefillDesc(ctypes.Structure):
+    _fields_ = [
+        ("batch_size", ctypes.c_int32), ("num_heads", ctypes.c_int32),
+        ("nope_dim", ctypes.c_int32), ("rope_dim", ctypes.c_int32),
+        ("value_dim", ctypes.c_int32), ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+        ("mask", ctypes.c_int32), ("sm_scale", ctypes.c_float), ("output_scale", ctypes.c_float),
+        ("return_lse", ctypes.c_int32), ("flags", ctypes.c_int32),
+    ]
+
+
 _vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 _pi32 = ctypes.POINTER(ctypes.c_int32)
 
@@ -118,6 +157,26 @@ _SIGS = {
     "batch_prefill_plan_check": (ctypes.c_int, [_vp, _vp]),
     "batch_prefill_run": (ctypes.c_int, [_vp, _vp, _i64, _i64, _vp, _vp, _i64, _i64, _vp, _vp,
                                          _vp, _sz, _vp]),
+    "paged_kv_tables": (ctypes.c_int, [_vp, _vp, _i32, _vp, _i32, _vp, _i32, _vp, _i64, _i32, _vp,
+                                       _vp, _vp, _i64, _vp, _vp, _vp]),
+    "pka_status_check": (ctypes.c_int, [_vp, _vp]),
+    "paged_latent_append": (ctypes.c_int, [_vp, _i64, _vp, _i64, _i32, _i32, _vp, _i64, _vp, _i64,
+                                           _i32, _i64, _i32, _vp, _vp]),
+    "paged_latent_decode_plan": (ctypes.c_int, [ctypes.POINTER(_vp), ctypes.POINTER(LatentDesc),
+                                                _pi32, _pi32, ctypes.POINTER(_sz), _vp]),
+    "paged_latent_decode_plan_update": (ctypes.c_int, [_vp, _i32, _pi32, _pi32,
+                                                       ctypes.POINTER(_sz), _vp]),
+    "paged_latent_decode_plan_destroy": (None, [_vp]),
+    "paged_latent_decode_plan_info": (ctypes.c_int, [_vp, ctypes.POINTER(LatentPlanInfo)]),
+    "paged_latent_decode_plan_export": (ctypes.c_int, [_vp, _pi32, _pi32]),
+    "paged_latent_decode_plan_check": (ctypes.c_int, [_vp, _vp]),
+    "paged_latent_decode_run": (ctypes.c_int, [_vp, _vp, _i64, _i64, _vp, _i64, _vp, _i64, _vp,
+                                               _vp, _vp, _vp, _sz, _vp]),
+    "batch_latent_prefill_plan": (ctypes.c_int, [ctypes.POINTER(_vp),
+                                                 ctypes.POINTER(LatentPrefillDesc), _pi32, _pi32,
+                                                 _pi32, _vp]),
+    "batch_latent_prefill_run": (ctypes.c_int, [_vp, _vp, _i64, _i64, _vp, _vp, _i64, _vp, _i64,
+                                                _i64, _vp, _vp, _vp]),
     "paged_kv_gather": (ctypes.c_int, [_vp, _i64, _i64, _i64, _i32, _i32, _i32, _vp, _i64, _i32,
                                        _i32, _i32, _i32, _vp, _vp]),
     "pka_wait_timeout_probe": (ctypes.c_int, [_vp, _vp, _i64, _vp]),

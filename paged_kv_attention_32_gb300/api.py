@@ -7,6 +7,7 @@ every computation happens in ``libpka.so``.  There is no CPU path.
 
 import ctypes
 import math
+from collections import namedtuple
 
 import torch
 
@@ -462,6 +463,339 @@ def batch_prefill_run(plan, q, k, v, out=None, lse=None, stream=None):
                                    None, 0, _stream(stream))
     L.check(rc, "batch_prefill_run")
     return (out, lse) if plan.desc.return_lse else out
+
+
+def _on_device(**tensors):
+    """Every given tensor is a CUDA tensor of the current device (the library launches there)."""
+    want = torch.device("cuda", torch.cuda.current_device())
+    for name, t in tensors.items():
+        if t is not None and t.device != want:
+            raise ValueError(f"{name} is on {t.device}, the current device is {want}")
+
+
+def _typed(dtype, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.dtype != dtype:
+            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+
+
+def _dense(**tensors):
+    for name, t in tensors.items():
+        if t is not None and not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+
+
+def check_status(status, stream=None):
+    """Synchronise, read and clear a status word (a device int32 tensor given to
+    ``paged_kv_tables`` or ``paged_latent_append``); raises on what it reports."""
+    _typed(torch.int32, status=status)
+    _on_device(status=status)
+    L.check(L.lib().pka_status_check(_ptr(status), _stream(stream)), "check_status")
+
+
+KvTables = namedtuple("KvTables", "seq_lens qo_indptr slot_map free_head")
+
+
+def paged_kv_tables(kv_lens, new_lens, free_pages, free_head, block_tables, *, page_size,
+                    num_slots=None, seq_lens=None, qo_indptr=None, slot_map=None,
+                    free_head_out=None, status=None, stream=None):
+    """Give a step's new tokens their pages and cache slots, on the GPU (see pka.h).
+
+    ``kv_lens``, ``new_lens`` int32 ``[B]``; ``free_pages`` int32 with ``free_head`` int32
+    ``[1]`` its first unused entry; ``block_tables`` int32 ``[B, C]`` grows in place.
+    ``num_slots``: length of the slot map when none is passed (the step's token budget).
+    Returns ``KvTables(seq_lens, qo_indptr, slot_map, free_head)``: the new lengths, the
+    query offsets ``[B + 1]``, one int64 slot per new token (-1 behind the last) and the
+    advanced head.  A step that does not fit changes nothing and sets ``status``
+    (``check_status``)."""
+    _typed(torch.int32, kv_lens=kv_lens, new_lens=new_lens, free_pages=free_pages,
+           free_head=free_head, block_tables=block_tables, seq_lens=seq_lens,
+           qo_indptr=qo_indptr, free_head_out=free_head_out, status=status)
+    _typed(torch.int64, slot_map=slot_map)
+    _on_device(kv_lens=kv_lens, new_lens=new_lens, free_pages=free_pages, free_head=free_head,
+               block_tables=block_tables, seq_lens=seq_lens, qo_indptr=qo_indptr,
+               slot_map=slot_map, free_head_out=free_head_out, status=status)
+    _dense(kv_lens=kv_lens, new_lens=new_lens, free_pages=free_pages, seq_lens=seq_lens,
+           qo_indptr=qo_indptr, slot_map=slot_map)
+    B = kv_lens.numel()
+    if block_tables.dim() != 2 or block_tables.shape[0] != B or new_lens.numel() != B:
+        raise ValueError("kv_lens, new_lens and block_tables must have one row per request")
+    if block_tables.stride(-1) != 1:
+        raise ValueError("block_tables rows must be dense")
+    if free_head.numel() != 1:
+        raise ValueError("free_head must hold one entry")
+    dev = kv_lens.device
+    if slot_map is None:
+        if num_slots is None:
+            raise ValueError("num_slots is required when no slot_map is passed")
+        slot_map = torch.empty(num_slots, dtype=torch.int64, device=dev)
+    elif num_slots is not None and num_slots != slot_map.numel():
+        raise ValueError("num_slots differs from the length of slot_map")
+    if seq_lens is None:
+        seq_lens = torch.empty(B, dtype=torch.int32, device=dev)
+    if qo_indptr is None:
+        qo_indptr = torch.empty(B + 1, dtype=torch.int32, device=dev)
+    if free_head_out is None:
+        free_head_out = torch.empty(1, dtype=torch.int32, device=dev)
+    if seq_lens.numel() != B or qo_indptr.numel() != B + 1 or free_head_out.numel() != 1:
+        raise ValueError("seq_lens needs B entries, qo_indptr B + 1, free_head_out one")
+    rc = L.lib().paged_kv_tables(
+        _ptr(kv_lens), _ptr(new_lens), B, _ptr(free_pages), free_pages.numel(), _ptr(free_head),
+        page_size, _ptr(block_tables), max(block_tables.stride(0), block_tables.shape[1]),
+        block_tables.shape[1], _ptr(seq_lens), _ptr(qo_indptr), _ptr(slot_map), slot_map.numel(),
+        _ptr(free_head_out), _ptr(status), _stream(stream))
+    L.check(rc, "paged_kv_tables")
+    return KvTables(seq_lens, qo_indptr, slot_map, free_head_out)
+
+
+def _check_latent_pool(pages):
+    if pages.dim() != 3 or pages.stride(2) != 1 or pages.stride(1) != pages.shape[2]:
+        raise ValueError("pages must be [num_pages, page_size, dim] with dense slots")
+
+
+def _page_stride(pages):
+    return pages.stride(0) if pages.shape[0] > 1 else pages.shape[1] * pages.shape[2]
+
+
+def paged_latent_append(latent, rope, slot_map, pages, status=None, stream=None):
+    """Write rows ``[latent | rope]`` into a paged latent pool (see pka.h): ``latent``
+    ``[T, latent_dim]``, ``rope`` ``[T, rope_dim]`` (or None), ``slot_map`` int64 ``[T]``
+    (negative entries skip their row), ``pages`` ``[num_pages, page_size, latent_dim +
+    rope_dim]``, updated in place and returned.  A slot past the pool is skipped and
+    reported in ``status`` (``check_status``)."""
+    if pages.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError(f"pages must be bfloat16 or float16, got {pages.dtype}")
+    _typed(pages.dtype, latent=latent, rope=rope)
+    _typed(torch.int64, slot_map=slot_map)
+    _typed(torch.int32, status=status)
+    _on_device(latent=latent, rope=rope, slot_map=slot_map, pages=pages, status=status)
+    _dense(slot_map=slot_map)
+    _check_latent_pool(pages)
+    T, dl = latent.shape
+    dr = 0 if rope is None else rope.shape[1]
+    if slot_map.numel() != T or (rope is not None and rope.shape[0] != T):
+        raise ValueError("latent, rope and slot_map must have one row per token")
+    if dl + dr != pages.shape[2]:
+        raise ValueError(f"rows of {dl} + {dr} values, the pool's have {pages.shape[2]}")
+    if T == 0:
+        return pages
+    if latent.stride(1) != 1 or (rope is not None and rope.stride(1) != 1):
+        raise ValueError("latent and rope must have a dense last dimension")
+    rc = L.lib().paged_latent_append(
+        _ptr(latent), latent.stride(0), _ptr(rope), 0 if rope is None else rope.stride(0), dl, dr,
+        _ptr(slot_map), T, _ptr(pages), pages.shape[0], pages.shape[1], _page_stride(pages),
+        _DTYPES[pages.dtype], _ptr(status), _stream(stream))
+    L.check(rc, "paged_latent_append")
+    return pages
+
+
+class LatentDecodePlan:
+    """Owns a ``pka_latent_plan*``; freed with ``paged_latent_decode_plan_destroy``."""
+
+    def __init__(self, handle, desc, workspace_bytes):
+        self.handle = handle
+        self.desc = desc
+        self.workspace_bytes = workspace_bytes
+        self.total_q = self.info["total_q"]
+
+    @property
+    def info(self):
+        inf = L.LatentPlanInfo()
+        L.check(L.lib().paged_latent_decode_plan_info(self.handle, ctypes.byref(inf)), "plan_info")
+        return {f: getattr(inf, f) for f, _ in L.LatentPlanInfo._fields_}
+
+    def export(self):
+        """Host copies of the plan: items (request, first tile, end tile, partial index)
+        and each segment's first item, with the item count behind them."""
+        inf = self.info
+        items = torch.zeros((max(1, inf["num_items"]), 4), dtype=torch.int32)
+        segs = torch.zeros(inf["num_segments"] + 1, dtype=torch.int32)
+        L.check(L.lib().paged_latent_decode_plan_export(
+            self.handle, ctypes.cast(items.data_ptr(), L._pi32),
+            ctypes.cast(segs.data_ptr(), L._pi32)), "plan_export")
+        return [tuple(r) for r in items[: inf["num_items"]].tolist()], segs.tolist()
+
+    def update(self, seq_lens_kv, qo_indptr=None, stream=None):
+        """Re-plan in place for a new batch (``paged_latent_decode_plan_update``)."""
+        seq_t, seq_p = _host_i32(seq_lens_kv)
+        ind_t, ind_p = _host_i32(qo_indptr)
+        if ind_t is not None and ind_t.numel() != seq_t.numel() + 1:
+            raise ValueError("qo_indptr must have one entry more than seq_lens_kv")
+        ws = ctypes.c_size_t()
+        host_only = bool(self.desc.flags & L.PKA_PLAN_HOST_ONLY)
+        rc = L.lib().paged_latent_decode_plan_update(
+            self.handle, seq_t.numel(), seq_p, ind_p, ctypes.byref(ws),
+            None if host_only else _stream(stream))
+        L.check(rc, "paged_latent_decode_plan_update")
+        self.desc.batch_size = seq_t.numel()
+        self.workspace_bytes = ws.value
+        self.total_q = self.info["total_q"]
+        return self
+
+    def check(self, stream=None):
+        """Synchronise and read the device status word (raises on a kernel timeout)."""
+        L.check(L.lib().paged_latent_decode_plan_check(self.handle, _stream(stream)), "plan_check")
+
+    def __del__(self):
+        h, self.handle = getattr(self, "handle", None), None
+        if h:
+            L.lib().paged_latent_decode_plan_destroy(h)
+
+
+def paged_latent_decode_plan(seq_lens_kv, *, num_heads, page_size, max_pages_per_seq, num_pages,
+                             scale, latent_dim=512, rope_dim=64, qo_indptr=None, q_len=1,
+                             causal=False, output_scale=1.0, return_lse=False,
+                             freeze_seq_lens=True, num_sms=0, host_only=False,
+                             dtype=torch.bfloat16, out_dtype=None, stream=None):
+    """Plan an absorbed latent decode from host copies of the lengths (see pka.h).
+    ``scale`` has no default: the head size it comes from is not visible here."""
+    in_code, out_code = _dtype_codes(dtype, out_dtype)
+    seq_t, seq_p = _host_i32(seq_lens_kv)
+    ind_t, ind_p = _host_i32(qo_indptr)
+    if ind_t is not None and ind_t.numel() != seq_t.numel() + 1:
+        raise ValueError("qo_indptr must have one entry more than seq_lens_kv")
+    d = L.LatentDesc(
+        batch_size=seq_t.numel(), num_heads=num_heads, latent_dim=latent_dim, rope_dim=rope_dim,
+        page_size=page_size, max_pages_per_seq=max_pages_per_seq, num_pages=num_pages,
+        dtype=in_code, out_dtype=out_code, q_len=q_len,
+        mask=L.PKA_MASK_CAUSAL if causal else L.PKA_MASK_DENSE, scale=scale,
+        output_scale=output_scale, return_lse=int(bool(return_lse)),
+        freeze_seq_lens=int(bool(freeze_seq_lens)), num_sms=num_sms,
+        flags=L.PKA_PLAN_HOST_ONLY if host_only else 0)
+    h = ctypes.c_void_p()
+    ws = ctypes.c_size_t()
+    rc = L.lib().paged_latent_decode_plan(ctypes.byref(h), ctypes.byref(d), seq_p, ind_p,
+                                          ctypes.byref(ws),
+                                          None if host_only else _stream(stream))
+    L.check(rc, "paged_latent_decode_plan")
+    return LatentDecodePlan(h, d, ws.value)
+
+
+def paged_latent_decode_run(plan, q, pages, block_tables, seq_lens_kv=None, out=None, lse=None,
+                            workspace=None, stream=None):
+    """Run a planned latent decode: ``q`` ``[T, H, latent_dim + rope_dim]``, ``pages``
+    ``[num_pages, page_size, latent_dim + rope_dim]``.  Returns ``out``
+    ``[T, H, latent_dim]`` (and the base-2 ``lse`` ``[T, H]`` when the plan returns it);
+    rows of a given ``out`` past the plan's are left as they were."""
+    d = plan.desc
+    _typed(_TORCH[d.dtype], q=q, pages=pages)
+    _typed(torch.int32, block_tables=block_tables, seq_lens_kv=seq_lens_kv)
+    _typed(_TORCH[d.out_dtype], out=out)
+    _typed(torch.float32, lse=lse)
+    _on_device(q=q, pages=pages, block_tables=block_tables, seq_lens_kv=seq_lens_kv, out=out,
+               lse=lse, workspace=workspace)
+    _dense(seq_lens_kv=seq_lens_kv, out=out, lse=lse, workspace=workspace)
+    _check_latent_pool(pages)
+    D = d.latent_dim + d.rope_dim
+    T = q.shape[0]
+    if q.dim() != 3 or tuple(q.shape[1:]) != (d.num_heads, D) or T < plan.total_q:
+        raise ValueError(f"q must be [>= {plan.total_q}, {d.num_heads}, {D}], got {tuple(q.shape)}")
+    if q.stride(-1) != 1:
+        raise ValueError("q must have a dense last dimension")
+    if tuple(pages.shape) != (d.num_pages, d.page_size, D):
+        raise ValueError(f"pages must be [{d.num_pages}, {d.page_size}, {D}], "
+                         f"got {tuple(pages.shape)}")
+    if block_tables.stride(-1) != 1 or block_tables.shape[0] < d.batch_size or \
+            block_tables.shape[1] < d.max_pages_per_seq:
+        raise ValueError("block_tables needs dense rows, one of at least max_pages_per_seq "
+                         "entries per request")
+    if seq_lens_kv is not None and seq_lens_kv.numel() < d.batch_size:
+        raise ValueError("seq_lens_kv needs one entry per request")
+    if out is None:
+        out = torch.empty((T, d.num_heads, d.latent_dim), dtype=_TORCH[d.out_dtype],
+                          device=q.device)
+    if d.return_lse and lse is None:
+        lse = torch.empty((T, d.num_heads), dtype=torch.float32, device=q.device)
+    if out.dim() != 3 or tuple(out.shape[1:]) != (d.num_heads, d.latent_dim) or \
+            out.shape[0] < plan.total_q:
+        raise ValueError("out must be [T, num_heads, latent_dim]")
+    if lse is not None and (lse.dim() != 2 or lse.shape[1] != d.num_heads or
+                            lse.shape[0] < plan.total_q):
+        raise ValueError("lse must be [T, num_heads]")
+    if workspace is None and plan.workspace_bytes > 0:
+        workspace = torch.empty(plan.workspace_bytes, dtype=torch.uint8, device=q.device)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    rc = L.lib().paged_latent_decode_run(
+        plan.handle, _ptr(q), q.stride(0), q.stride(1), _ptr(pages), _page_stride(pages),
+        _ptr(block_tables), max(block_tables.stride(0), block_tables.shape[1]),
+        _ptr(seq_lens_kv), _ptr(out), _ptr(lse), _ptr(workspace), ws_bytes, _stream(stream))
+    L.check(rc, "paged_latent_decode_run")
+    return (out, lse) if d.return_lse else out
+
+
+class LatentPrefillPlan(PrefillPlan):
+    """A prefill plan for ``batch_latent_prefill_run``."""
+
+
+def batch_latent_prefill_plan(qo_indptr, kv_indptr, *, num_heads, nope_dim=128, rope_dim=64,
+                              value_dim=128, causal=True, sm_scale=None, output_scale=1.0,
+                              return_lse=False, host_only=False, dtype=torch.bfloat16,
+                              out_dtype=None, stream=None):
+    """Plan an expanded latent prefill from host copies of the offsets (see pka.h)."""
+    in_code, out_code = _dtype_codes(dtype, out_dtype)
+    qo_t, qo_p = _host_i32(qo_indptr)
+    kv_t, kv_p = _host_i32(kv_indptr)
+    if qo_t.numel() != kv_t.numel():
+        raise ValueError("qo_indptr and kv_indptr must have the same length")
+    d = L.LatentPrefillDesc(
+        batch_size=qo_t.numel() - 1, num_heads=num_heads, nope_dim=nope_dim, rope_dim=rope_dim,
+        value_dim=value_dim, dtype=in_code, out_dtype=out_code,
+        mask=L.PKA_MASK_CAUSAL if causal else L.PKA_MASK_DENSE,
+        sm_scale=float("nan") if sm_scale is None else sm_scale, output_scale=output_scale,
+        return_lse=int(bool(return_lse)), flags=L.PKA_PLAN_HOST_ONLY if host_only else 0)
+    h = ctypes.c_void_p()
+    nt = ctypes.c_int32()
+    rc = L.lib().batch_latent_prefill_plan(ctypes.byref(h), ctypes.byref(d), qo_p, kv_p,
+                                           ctypes.byref(nt),
+                                           _stream(stream) if not host_only else None)
+    L.check(rc, "batch_latent_prefill_plan")
+    plan = LatentPrefillPlan(h, d, nt.value)
+    plan.total_q, plan.total_kv = int(qo_t[-1]), int(kv_t[-1])
+    return plan
+
+
+def batch_latent_prefill_run(plan, q, k_nope, k_rope, v, out=None, lse=None, stream=None):
+    """Run a planned latent prefill: ``q`` ``[Tq, H, nope + rope]``, ``k_nope``
+    ``[Tk, H, nope]`` and ``v`` ``[Tk, H, value]`` with the same strides (the two parts of
+    one projection's output, or two tensors alike), ``k_rope`` ``[Tk, rope]`` shared by the
+    heads.  Returns ``out`` ``[Tq, H, value]`` (and ``lse`` when the plan returns it)."""
+    d = plan.desc
+    if not isinstance(plan, LatentPrefillPlan):
+        raise ValueError("the plan was not made by batch_latent_prefill_plan")
+    _typed(_TORCH[d.dtype], q=q, k_nope=k_nope, k_rope=k_rope, v=v)
+    _typed(_TORCH[d.out_dtype], out=out)
+    _typed(torch.float32, lse=lse)
+    _on_device(q=q, k_nope=k_nope, k_rope=k_rope, v=v, out=out, lse=lse)
+    _dense(out=out, lse=lse)
+    H, D = d.num_heads, d.nope_dim + d.rope_dim
+    if q.dim() != 3 or tuple(q.shape[1:]) != (H, D) or q.shape[0] < plan.total_q:
+        raise ValueError(f"q must be [>= {plan.total_q}, {H}, {D}], got {tuple(q.shape)}")
+    for name, t, w in (("k_nope", k_nope, d.nope_dim), ("v", v, d.value_dim)):
+        if t.dim() != 3 or tuple(t.shape[1:]) != (H, w) or t.shape[0] < plan.total_kv:
+            raise ValueError(f"{name} must be [>= {plan.total_kv}, {H}, {w}], got {tuple(t.shape)}")
+    if k_rope.dim() != 2 or k_rope.shape[1] != d.rope_dim or k_rope.shape[0] < plan.total_kv:
+        raise ValueError(f"k_rope must be [>= {plan.total_kv}, {d.rope_dim}], "
+                         f"got {tuple(k_rope.shape)}")
+    for name, t in (("q", q), ("k_nope", k_nope), ("k_rope", k_rope), ("v", v)):
+        if t.stride(-1) != 1:
+            raise ValueError(f"{name} must have a dense last dimension")
+    if plan.total_kv > 0 and tuple(k_nope.stride()) != tuple(v.stride()):
+        raise ValueError("k_nope and v must have the same strides")
+    T = q.shape[0]
+    if out is None:
+        out = torch.empty((T, H, d.value_dim), dtype=_TORCH[d.out_dtype], device=q.device)
+    if d.return_lse and lse is None:
+        lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
+    if out.dim() != 3 or tuple(out.shape[1:]) != (H, d.value_dim) or out.shape[0] < plan.total_q:
+        raise ValueError("out must be [Tq, H, value_dim]")
+    if lse is not None and (lse.dim() != 2 or lse.shape[1] != H or lse.shape[0] < plan.total_q):
+        raise ValueError("lse must be [Tq, H]")
+    rc = L.lib().batch_latent_prefill_run(
+        plan.handle, _ptr(q), q.stride(0), q.stride(1), _ptr(k_nope), _ptr(k_rope),
+        k_rope.stride(0), _ptr(v), k_nope.stride(0), k_nope.stride(1), _ptr(out), _ptr(lse),
+        _stream(stream))
+    L.check(rc, "batch_latent_prefill_run")
+    return (out, lse) if d.return_lse else out
 
 
 def paged_kv_gather(pages, block_tables, request, kv_head, tok_begin, tok_end, out=None,

@@ -8,8 +8,6 @@
 #include <new>
 #include <string>
 
-#include <nvtx3/nvToolsExt.h>
-
 #include "host_common.h"
 #include "kernels.h"
 #include "plan.h"
@@ -36,24 +34,41 @@ void clear_error() { g_last_error.clear(); }
 
 const char* last_error() { return g_last_error.c_str(); }
 
+int check_device(int plan_device) {
+  int dev = -1;
+  PKA_CUDA_TRY(cudaGetDevice(&dev), "cudaGetDevice");
+  PKA_CHECK_ARG(dev == plan_device, "plan was made on device %d, current device is %d",
+                plan_device, dev);
+  return PKA_OK;
+}
+
+int read_status(int32_t* d_status, cudaStream_t stream) {
+  int32_t st = 0;
+  PKA_CUDA_TRY(cudaMemcpyAsync(&st, d_status, sizeof(st), cudaMemcpyDeviceToHost, stream),
+               "cudaMemcpyAsync(status)");
+  PKA_CUDA_TRY(cudaStreamSynchronize(stream), "cudaStreamSynchronize");
+  PKA_CUDA_TRY(cudaMemsetAsync(d_status, 0, sizeof(int32_t), stream), "cudaMemsetAsync(status)");
+  PKA_CUDA_TRY(cudaStreamSynchronize(stream), "cudaStreamSynchronize");
+  if (st & STATUS_WAIT_TIMEOUT)
+    return fail(PKA_ERR_DEVICE_TIMEOUT, "a kernel gave up on a bounded wait (status 0x%x)", st);
+  if (st & STATUS_PAGE_BOUNDS)
+    return fail(PKA_ERR_DEVICE_BOUNDS,
+                "a block-table entry a run would read is outside [0, num_pages) (status 0x%x)",
+                st);
+  if (st & STATUS_SLOT_BOUNDS)
+    return fail(PKA_ERR_DEVICE_BOUNDS, "a slot map entry is outside the pool (status 0x%x)", st);
+  if (st & STATUS_CAPACITY)
+    return fail(PKA_ERR_DEVICE_CAPACITY,
+                "a step's tokens do not fit the free pages, a table row or the slot map, or a "
+                "length is negative (status 0x%x)", st);
+  return PKA_OK;
+}
+
 }  // namespace pka
 
 using namespace pka;
 
 namespace {
-
-bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
-
-// An NVTX range over an entry point, so that the plan and run calls show up by
-// name on a profiler's timeline (a no-op call when no tool is attached).
-struct NvtxRange {
-  explicit NvtxRange(const char* name) { nvtxRangePushA(name); }
-  ~NvtxRange() { nvtxRangePop(); }
-  NvtxRange(const NvtxRange&) = delete;
-  NvtxRange& operator=(const NvtxRange&) = delete;
-};
-
-size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
 int upload_decode_plan(pka_plan& p, cudaStream_t stream) {
   const size_t n_items = p.items.size() * sizeof(WorkItem);
@@ -167,30 +182,6 @@ int upload_prefill_plan(pka_prefill_plan& p, cudaStream_t stream) {
                  "cudaMemcpyAsync(row order)");
   }
   PKA_CUDA_TRY(cudaMemsetAsync(base + off_status, 0, 256, stream), "cudaMemsetAsync(status)");
-  return PKA_OK;
-}
-
-int check_device(int plan_device) {
-  int dev = -1;
-  PKA_CUDA_TRY(cudaGetDevice(&dev), "cudaGetDevice");
-  PKA_CHECK_ARG(dev == plan_device, "plan was made on device %d, current device is %d",
-                plan_device, dev);
-  return PKA_OK;
-}
-
-int read_status(int32_t* d_status, cudaStream_t stream) {
-  int32_t st = 0;
-  PKA_CUDA_TRY(cudaMemcpyAsync(&st, d_status, sizeof(st), cudaMemcpyDeviceToHost, stream),
-               "cudaMemcpyAsync(status)");
-  PKA_CUDA_TRY(cudaStreamSynchronize(stream), "cudaStreamSynchronize");
-  PKA_CUDA_TRY(cudaMemsetAsync(d_status, 0, sizeof(int32_t), stream), "cudaMemsetAsync(status)");
-  PKA_CUDA_TRY(cudaStreamSynchronize(stream), "cudaStreamSynchronize");
-  if (st & STATUS_WAIT_TIMEOUT)
-    return fail(PKA_ERR_DEVICE_TIMEOUT, "a kernel gave up on a bounded wait (status 0x%x)", st);
-  if (st & STATUS_PAGE_BOUNDS)
-    return fail(PKA_ERR_DEVICE_BOUNDS,
-                "a block-table entry a run would read is outside [0, num_pages) (status 0x%x)",
-                st);
   return PKA_OK;
 }
 
@@ -628,6 +619,7 @@ int batch_prefill_run(const pka_prefill_plan* p, const void* q, int64_t q_stride
   (void)workspace;
   (void)workspace_bytes;
   PKA_CHECK_ARG(p != nullptr, "plan must not be NULL");
+  PKA_CHECK_ARG(!p->latent, "the plan was made by batch_latent_prefill_plan");
   PKA_CHECK_ARG(p->dev_buf != nullptr, "plan was built with PKA_PLAN_HOST_ONLY and cannot run");
   PKA_CHECK_ARG(q && k && v && out, "q, k, v and out must not be NULL");
   PKA_CHECK_ARG(!p->desc.return_lse || lse != nullptr, "the plan returns the LSE: lse is NULL");
@@ -727,6 +719,13 @@ int paged_decode_check_tables(const pka_plan* p, const int32_t* block_tables,
                              bt_row_stride, p->desc.freeze_seq_lens ? nullptr : seq_lens_kv_dev,
                              p->ps, p->desc.num_pages, p->d_status,
                              static_cast<cudaStream_t>(stream));
+}
+
+int pka_status_check(int32_t* status_dev, void* stream) {
+  clear_error();
+  PKA_CHECK_ARG(status_dev != nullptr && aligned(status_dev, 4),
+                "status_dev must be a 4-byte aligned device pointer");
+  return read_status(status_dev, static_cast<cudaStream_t>(stream));
 }
 
 int pka_wait_timeout_probe(const pka_plan* plan, int32_t* status_dev, int64_t limit_ns,

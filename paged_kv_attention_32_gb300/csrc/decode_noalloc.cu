@@ -28,7 +28,6 @@ constexpr int kMaxDevices = 256;
 std::mutex g_setup_mu;
 void* g_scratch_addr[kMaxDevices] = {};
 
-size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // Device address of the scratch array on `dev` (the current device), looked
 // up once per device.  In host code the symbol is only a stand-in: kernels

@@ -9,6 +9,7 @@
 #include <string>
 
 #include <cuda_runtime.h>
+#include <nvtx3/nvToolsExt.h>
 
 #include "pka.h"
 
@@ -39,6 +40,28 @@ inline cudaError_t set_smem_once(Kernel kern, int bytes, std::atomic<uint64_t>& 
 inline int cuda_fail(cudaError_t e, const char* what) {
   return fail(PKA_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
+
+inline bool aligned(const void* p, uintptr_t n) {
+  return (reinterpret_cast<uintptr_t>(p) % n) == 0;
+}
+
+inline size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
+
+// An NVTX range over an entry point, so that the plan and run calls show up by
+// name on a profiler's timeline (a no-op call when no tool is attached).
+struct NvtxRange {
+  explicit NvtxRange(const char* name) { nvtxRangePushA(name); }
+  ~NvtxRange() { nvtxRangePop(); }
+  NvtxRange(const NvtxRange&) = delete;
+  NvtxRange& operator=(const NvtxRange&) = delete;
+};
+
+// PKA_OK when `plan_device` is the current device.
+int check_device(int plan_device);
+
+// Waits for `stream`, reads and clears a device status word, and maps its bits
+// to an error code.
+int read_status(int32_t* d_status, cudaStream_t stream);
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 

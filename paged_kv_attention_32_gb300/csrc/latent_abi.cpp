@@ -1,0 +1,448 @@
+// extern "C" entry points of page tables and latent attention: argument
+// checks, plan ownership, launch dispatch.
+#include <algorithm>
+#include <climits>
+#include <cmath>
+#include <cstring>
+#include <exception>
+#include <new>
+
+#include "host_common.h"
+#include "latent.h"
+#include "tmap.h"
+
+using namespace pka;
+
+namespace {
+
+// Runs `f`, turning a C++ exception (a host allocation that failed) into an error code.
+template <typename F>
+int guarded(F&& f) {
+  try {
+    return f();
+  } catch (const std::exception& e) {
+    return fail(PKA_ERR_INVALID_ARG, "host error: %s", e.what());
+  }
+}
+
+// Whether two byte ranges share a byte.
+bool overlap(const void* p, size_t n, const void* q, size_t m) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return a < b + m && b < a + n;
+}
+
+// One asynchronous copy of the plan's arrays from a pinned image, which is
+// rewritten only after the copy that last read it has completed.
+int upload_latent_plan(pka_latent_plan& p, cudaStream_t stream) {
+  const size_t n_items = p.items.size() * sizeof(LatentItem);
+  const size_t n_segs = p.segments.size() * sizeof(int32_t);
+  const size_t n_reqs = p.reqs.size() * sizeof(LatentReq);
+  const size_t n_splits = p.splits.size() * sizeof(int32_t);
+  const size_t off_segs = up256(n_items), off_reqs = off_segs + up256(n_segs);
+  const size_t off_splits = off_reqs + up256(n_reqs), off_status = off_splits + up256(n_splits);
+  const size_t total = off_status + 256;
+  if (p.stage_done != nullptr)
+    PKA_CUDA_TRY(cudaEventSynchronize(p.stage_done), "cudaEventSynchronize(plan upload)");
+  if (p.dev_buf == nullptr || total > p.dev_capacity) {
+    if (p.dev_buf != nullptr) {
+      PKA_CUDA_TRY(cudaFree(p.dev_buf), "cudaFree(latent plan)");
+      p.dev_buf = nullptr;
+    }
+    if (p.host_stage != nullptr) {
+      PKA_CUDA_TRY(cudaFreeHost(p.host_stage), "cudaFreeHost(plan image)");
+      p.host_stage = nullptr;
+    }
+    const size_t cap = std::max<size_t>(4096, total + total / 2);
+    PKA_CUDA_TRY(cudaGetDevice(&p.device), "cudaGetDevice");
+    PKA_CUDA_TRY(cudaMalloc(&p.dev_buf, cap), "cudaMalloc(latent plan)");
+    p.dev_capacity = cap;
+    PKA_CUDA_TRY(cudaMallocHost(&p.host_stage, cap), "cudaMallocHost(plan image)");
+  }
+  uint8_t* base = static_cast<uint8_t*>(p.dev_buf);
+  p.d_items = reinterpret_cast<const LatentItem*>(base);
+  p.d_segments = reinterpret_cast<const int32_t*>(base + off_segs);
+  p.d_reqs = reinterpret_cast<const LatentReq*>(base + off_reqs);
+  p.d_splits = reinterpret_cast<const int32_t*>(base + off_splits);
+  p.d_status = reinterpret_cast<int32_t*>(base + off_status);
+  uint8_t* img = static_cast<uint8_t*>(p.host_stage);
+  if (n_items) std::memcpy(img, p.items.data(), n_items);
+  std::memcpy(img + off_segs, p.segments.data(), n_segs);
+  std::memcpy(img + off_reqs, p.reqs.data(), n_reqs);
+  if (n_splits) std::memcpy(img + off_splits, p.splits.data(), n_splits);
+  std::memset(img + off_status, 0, 256);
+  PKA_CUDA_TRY(cudaMemcpyAsync(base, img, total, cudaMemcpyHostToDevice, stream),
+               "cudaMemcpyAsync(latent plan)");
+  if (p.stage_done == nullptr)
+    PKA_CUDA_TRY(cudaEventCreateWithFlags(&p.stage_done, cudaEventDisableTiming),
+                 "cudaEventCreate(plan upload)");
+  PKA_CUDA_TRY(cudaEventRecord(p.stage_done, stream), "cudaEventRecord(plan upload)");
+  return PKA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+// ---------------------------------------------------------------------------
+// page tables
+// ---------------------------------------------------------------------------
+
+int paged_kv_tables(const int32_t* kv_lens, const int32_t* new_lens, int32_t batch_size,
+                    const int32_t* free_pages, int32_t num_free, const int32_t* free_head,
+                    int32_t page_size, int32_t* block_tables, int64_t bt_row_stride,
+                    int32_t max_pages_per_seq, int32_t* seq_lens, int32_t* qo_indptr,
+                    int64_t* slot_map, int64_t num_slots, int32_t* free_head_out, int32_t* status,
+                    void* stream) {
+  NvtxRange nvtx_range("pka::paged_kv_tables");
+  clear_error();
+  PKA_CHECK_ARG(kv_lens && new_lens && free_head && block_tables && seq_lens && qo_indptr &&
+                    slot_map && free_head_out,
+                "only free_pages (with num_free 0) and status may be NULL");
+  PKA_CHECK_ARG(batch_size >= 1, "batch_size must be >= 1 (got %d)", batch_size);
+  PKA_CHECK_ARG(num_free >= 0 && (free_pages != nullptr || num_free == 0),
+                "num_free must be >= 0 and free_pages not NULL");
+  PKA_CHECK_ARG(page_size >= 1 && page_size <= 65536, "page_size must be in [1, 65536] (got %d)",
+                page_size);
+  PKA_CHECK_ARG(max_pages_per_seq >= 1 && bt_row_stride >= max_pages_per_seq,
+                "block_tables rows of %d entries, row stride %lld", max_pages_per_seq,
+                (long long)bt_row_stride);
+  PKA_CHECK_ARG(num_slots >= 1, "num_slots must be >= 1 (got %lld)", (long long)num_slots);
+  for (const void* p : {(const void*)kv_lens, (const void*)new_lens, (const void*)free_pages,
+                        (const void*)free_head, (const void*)block_tables, (const void*)seq_lens,
+                        (const void*)qo_indptr, (const void*)free_head_out, (const void*)status})
+    PKA_CHECK_ARG(aligned(p, 4), "int32 arrays must be 4-byte aligned");
+  PKA_CHECK_ARG(aligned(slot_map, 8), "slot_map must be 8-byte aligned");
+  struct Range {
+    const void* p;
+    size_t n;
+  };
+  const size_t B = (size_t)batch_size;
+  const Range ins[] = {{kv_lens, B * 4}, {new_lens, B * 4}, {free_pages, (size_t)num_free * 4},
+                       {free_head, 4}};
+  const Range outs[] = {{block_tables, ((B - 1) * (size_t)bt_row_stride + max_pages_per_seq) * 4},
+                        {seq_lens, B * 4}, {qo_indptr, (B + 1) * 4},
+                        {slot_map, (size_t)num_slots * 8}, {free_head_out, 4}};
+  for (const Range& o : outs) {
+    for (const Range& i : ins)
+      PKA_CHECK_ARG(i.n == 0 || !overlap(o.p, o.n, i.p, i.n), "an output overlaps an input");
+    for (const Range& u : outs)
+      PKA_CHECK_ARG(&u == &o || !overlap(o.p, o.n, u.p, u.n), "two outputs overlap");
+  }
+  return launch_kv_tables(kv_lens, new_lens, batch_size, free_pages, num_free, free_head,
+                          page_size, block_tables, bt_row_stride, max_pages_per_seq, seq_lens,
+                          qo_indptr, slot_map, num_slots, free_head_out, status,
+                          static_cast<cudaStream_t>(stream));
+}
+
+// ---------------------------------------------------------------------------
+// latent cache
+// ---------------------------------------------------------------------------
+
+int paged_latent_append(const void* latent, int64_t latent_stride, const void* rope,
+                        int64_t rope_stride, int32_t latent_dim, int32_t rope_dim,
+                        const int64_t* slot_map, int64_t num_tokens, void* pages,
+                        int64_t num_pages, int32_t page_size, int64_t stride_page, int32_t dtype,
+                        int32_t* status, void* stream) {
+  NvtxRange nvtx_range("pka::paged_latent_append");
+  clear_error();
+  PKA_CHECK_ARG(latent && slot_map && pages, "latent, slot_map and pages must not be NULL");
+  if (dtype != PKA_DTYPE_BF16 && dtype != PKA_DTYPE_F16)
+    return fail(PKA_ERR_UNSUPPORTED, "the pool must be bf16 or f16 (dtype %d)", dtype);
+  PKA_CHECK_ARG(latent_dim >= 8 && latent_dim % 8 == 0 && latent_dim <= 65536,
+                "latent_dim must be a multiple of 8 in [8, 65536] (got %d)", latent_dim);
+  PKA_CHECK_ARG(rope_dim >= 0 && rope_dim % 8 == 0 && rope_dim <= 65536 &&
+                    (rope_dim == 0) == (rope == nullptr),
+                "rope_dim must be a multiple of 8 in [0, 65536], rope NULL only with 0 (got %d)",
+                rope_dim);
+  PKA_CHECK_ARG(num_tokens >= 0 && num_pages >= 1 && page_size >= 1,
+                "num_tokens must be >= 0, num_pages and page_size >= 1");
+  PKA_CHECK_ARG(num_pages <= INT64_MAX / page_size / 65536, "the pool is too large");
+  PKA_CHECK_ARG(latent_stride >= 0 && rope_stride >= 0 && latent_stride % 8 == 0 &&
+                    rope_stride % 8 == 0 && stride_page % 8 == 0,
+                "strides must be non-negative multiples of 8 elements");
+  PKA_CHECK_ARG(stride_page >= (int64_t)page_size * (latent_dim + rope_dim),
+                "stride_page (%lld) is smaller than a page", (long long)stride_page);
+  PKA_CHECK_ARG(aligned(latent, 16) && aligned(rope, 16) && aligned(pages, 16) &&
+                    aligned(slot_map, 8) && aligned(status, 4),
+                "latent, rope and pages must be 16-byte aligned, slot_map 8-byte aligned");
+  PKA_CHECK_ARG(num_tokens <= (INT64_MAX / 2) / ((latent_dim + rope_dim) / 8), "too many tokens");
+  return launch_latent_append(latent, latent_stride, rope, rope_stride, latent_dim, rope_dim,
+                              slot_map, num_tokens, pages, num_pages, page_size, stride_page,
+                              status, static_cast<cudaStream_t>(stream));
+}
+
+// ---------------------------------------------------------------------------
+// latent decode
+// ---------------------------------------------------------------------------
+
+int paged_latent_decode_plan(pka_latent_plan** plan_out, const pka_latent_desc* desc,
+                             const int32_t* seq_lens_kv_host, const int32_t* qo_indptr_host,
+                             size_t* workspace_bytes_out, void* stream) {
+  NvtxRange nvtx_range("pka::paged_latent_decode_plan");
+  clear_error();
+  PKA_CHECK_ARG(plan_out != nullptr && desc != nullptr, "plan_out and desc must not be NULL");
+  *plan_out = nullptr;
+  pka_latent_plan* p = new (std::nothrow) pka_latent_plan();
+  if (p == nullptr) return fail(PKA_ERR_INVALID_ARG, "out of host memory");
+  int rc = guarded([&] { return build_latent_plan(*p, *desc, seq_lens_kv_host, qo_indptr_host); });
+  if (rc == PKA_OK && !(desc->flags & PKA_PLAN_HOST_ONLY))
+    rc = upload_latent_plan(*p, static_cast<cudaStream_t>(stream));
+  if (rc != PKA_OK) {
+    paged_latent_decode_plan_destroy(p);
+    return rc;
+  }
+  if (workspace_bytes_out) *workspace_bytes_out = (size_t)p->workspace_bytes;
+  *plan_out = p;
+  return PKA_OK;
+}
+
+int paged_latent_decode_plan_update(pka_latent_plan* p, int32_t batch_size,
+                                    const int32_t* seq_lens_kv_host,
+                                    const int32_t* qo_indptr_host, size_t* workspace_bytes_out,
+                                    void* stream) {
+  NvtxRange nvtx_range("pka::paged_latent_decode_plan_update");
+  clear_error();
+  PKA_CHECK_ARG(p != nullptr, "plan must not be NULL");
+  const bool host_only = p->desc.flags & PKA_PLAN_HOST_ONLY;
+  if (!host_only) {
+    const int rc = check_device(p->device);
+    if (rc != PKA_OK) return rc;
+  }
+  int rc = guarded([&] {
+    pka_latent_desc d = p->desc;
+    d.batch_size = batch_size;
+    pka_latent_plan fresh;
+    const int r = build_latent_plan(fresh, d, seq_lens_kv_host, qo_indptr_host);
+    if (r != PKA_OK) return r;   // the old plan stays as it was
+    fresh.dev_buf = p->dev_buf;
+    fresh.dev_capacity = p->dev_capacity;
+    fresh.device = p->device;
+    fresh.host_stage = p->host_stage;
+    fresh.stage_done = p->stage_done;
+    *p = std::move(fresh);
+    return PKA_OK;
+  });
+  if (rc != PKA_OK) return rc;
+  if (!host_only) {
+    rc = upload_latent_plan(*p, static_cast<cudaStream_t>(stream));
+    if (rc != PKA_OK) return rc;
+  }
+  if (workspace_bytes_out) *workspace_bytes_out = (size_t)p->workspace_bytes;
+  return PKA_OK;
+}
+
+void paged_latent_decode_plan_destroy(pka_latent_plan* plan) {
+  if (plan == nullptr) return;
+  if (plan->stage_done != nullptr) {
+    cudaEventSynchronize(plan->stage_done);   // the image is not freed under a pending copy
+    cudaEventDestroy(plan->stage_done);
+  }
+  if (plan->host_stage != nullptr) cudaFreeHost(plan->host_stage);
+  if (plan->dev_buf != nullptr) cudaFree(plan->dev_buf);
+  delete plan;
+}
+
+int paged_latent_decode_plan_info(const pka_latent_plan* p, pka_latent_plan_info* info) {
+  clear_error();
+  PKA_CHECK_ARG(p != nullptr && info != nullptr, "plan and info must not be NULL");
+  info->num_segments = (int32_t)p->segments.size() - 1;
+  info->num_items = (int32_t)p->items.size();
+  info->num_split = (int32_t)p->splits.size();
+  info->row_tile = p->row_tile;
+  info->row_blocks = p->row_blocks;
+  info->partial_rows = p->partial_rows;
+  info->workspace_bytes = p->workspace_bytes;
+  info->total_q = p->total_q;
+  info->num_sms = p->desc.num_sms;
+  return PKA_OK;
+}
+
+int paged_latent_decode_plan_export(const pka_latent_plan* p, int32_t* items, int32_t* segments) {
+  clear_error();
+  PKA_CHECK_ARG(p != nullptr, "plan must not be NULL");
+  if (items != nullptr && !p->items.empty())
+    std::memcpy(items, p->items.data(), p->items.size() * sizeof(LatentItem));
+  if (segments != nullptr)
+    std::memcpy(segments, p->segments.data(), p->segments.size() * sizeof(int32_t));
+  return PKA_OK;
+}
+
+int paged_latent_decode_plan_check(const pka_latent_plan* p, void* stream) {
+  clear_error();
+  PKA_CHECK_ARG(p != nullptr && p->d_status != nullptr, "plan has no device state");
+  return read_status(p->d_status, static_cast<cudaStream_t>(stream));
+}
+
+int paged_latent_decode_run(const pka_latent_plan* p, const void* q, int64_t q_stride_tok,
+                            int64_t q_stride_head, const void* pages, int64_t stride_page,
+                            const int32_t* block_tables, int64_t bt_row_stride,
+                            const int32_t* seq_lens_kv_dev, void* out, float* lse,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+  NvtxRange nvtx_range("pka::paged_latent_decode_run");
+  clear_error();
+  PKA_CHECK_ARG(p != nullptr, "plan must not be NULL");
+  PKA_CHECK_ARG(p->dev_buf != nullptr, "plan was built with PKA_PLAN_HOST_ONLY and cannot run");
+  const pka_latent_desc& d = p->desc;
+  PKA_CHECK_ARG(q && pages && block_tables && out,
+                "q, pages, block_tables and out must not be NULL");
+  PKA_CHECK_ARG(d.freeze_seq_lens || seq_lens_kv_dev != nullptr,
+                "seq_lens_kv_dev is required when the plan does not freeze the lengths");
+  PKA_CHECK_ARG(!d.return_lse || lse != nullptr, "the plan returns the LSE: lse is NULL");
+  PKA_CHECK_ARG(aligned(q, 16) && q_stride_tok % 8 == 0 && q_stride_head % 8 == 0 &&
+                    q_stride_tok >= 0 && q_stride_head >= 0,
+                "q must be 16-byte aligned with non-negative strides that are multiples of 8");
+  PKA_CHECK_ARG(aligned(pages, 16) && stride_page % 8 == 0, "pages must be 16-byte aligned with "
+                "a stride_page that is a multiple of 8");
+  PKA_CHECK_ARG(stride_page >= (int64_t)d.page_size * (d.latent_dim + d.rope_dim),
+                "stride_page (%lld) is smaller than a page", (long long)stride_page);
+  PKA_CHECK_ARG(aligned(out, 16) && aligned(lse, 4) && aligned(block_tables, 4) &&
+                    aligned(seq_lens_kv_dev, 4),
+                "out must be 16-byte aligned, lse, block_tables and lengths 4-byte aligned");
+  PKA_CHECK_ARG(bt_row_stride >= d.max_pages_per_seq,
+                "bt_row_stride (%lld) is smaller than the table width %d",
+                (long long)bt_row_stride, d.max_pages_per_seq);
+  if (p->workspace_bytes > 0) {
+    if (workspace == nullptr || workspace_bytes < (size_t)p->workspace_bytes)
+      return fail(PKA_ERR_WORKSPACE_TOO_SMALL, "workspace of %zu bytes, the plan needs %lld",
+                  workspace_bytes, (long long)p->workspace_bytes);
+    PKA_CHECK_ARG(aligned(workspace, 256), "workspace must be 256-byte aligned");
+  }
+  const int rc = check_device(p->device);
+  if (rc != PKA_OK) return rc;
+  LatentArgs a{};
+  a.q = q;
+  a.q_stride_tok = q_stride_tok;
+  a.q_stride_head = q_stride_head;
+  a.block_tables = block_tables;
+  a.bt_row_stride = bt_row_stride;
+  a.seq_lens_live = d.freeze_seq_lens ? nullptr : seq_lens_kv_dev;
+  a.out = out;
+  a.lse = d.return_lse ? lse : nullptr;
+  a.ws_o = static_cast<float*>(workspace);
+  a.ws_lse = workspace ? reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) +
+                                                  p->ws_lse_offset)
+                       : nullptr;
+  a.items = p->d_items;
+  a.segments = p->d_segments;
+  a.reqs = p->d_reqs;
+  a.splits = p->d_splits;
+  a.status = p->d_status;
+  a.num_segments = (int32_t)p->segments.size() - 1;
+  a.num_items = (int32_t)p->items.size();
+  a.num_splits = (int32_t)p->splits.size();
+  a.row_blocks = p->row_blocks;
+  a.max_rows = p->max_rows;
+  a.num_heads = d.num_heads;
+  a.page_size = d.page_size;
+  a.box_rows = 8;
+  while (a.box_rows < kLatentTile && d.page_size % (2 * a.box_rows) == 0) a.box_rows *= 2;
+  a.num_pages = (int32_t)d.num_pages;
+  a.causal = d.mask == PKA_MASK_CAUSAL;
+  a.scale_log2 = d.scale * 1.4426950408889634f;
+  a.output_scale = d.output_scale;
+  a.out_dtype = d.out_dtype;
+  return launch_latent_decode(*p, a, pages, stride_page, static_cast<cudaStream_t>(stream));
+}
+
+// ---------------------------------------------------------------------------
+// latent prefill
+// ---------------------------------------------------------------------------
+
+int batch_latent_prefill_plan(pka_prefill_plan** plan_out, const pka_latent_prefill_desc* desc,
+                              const int32_t* qo_indptr_host, const int32_t* kv_indptr_host,
+                              int32_t* num_tiles_out, void* stream) {
+  clear_error();
+  PKA_CHECK_ARG(plan_out != nullptr && desc != nullptr, "plan_out and desc must not be NULL");
+  *plan_out = nullptr;
+  if (desc->nope_dim != 128 || desc->rope_dim != kLatentRopeDim || desc->value_dim != 128)
+    return fail(PKA_ERR_UNSUPPORTED, "latent prefill takes heads of 128 + %d key and 128 value "
+                "dimensions (got %d + %d, %d)", kLatentRopeDim, desc->nope_dim, desc->rope_dim,
+                desc->value_dim);
+  PKA_CHECK_ARG(desc->mask == PKA_MASK_DENSE || desc->mask == PKA_MASK_CAUSAL, "unknown mask %d",
+                desc->mask);
+  pka_prefill_desc d{};
+  d.batch_size = desc->batch_size;
+  d.num_qo_heads = desc->num_heads;
+  d.num_kv_heads = desc->num_heads;
+  d.head_dim = 128;
+  d.dtype = desc->dtype;
+  d.mask = desc->mask;
+  d.window_left = -1;
+  d.sm_scale = std::isnan(desc->sm_scale) ? 1.0f / std::sqrt(128.0f + kLatentRopeDim) : desc->sm_scale;
+  d.output_scale = desc->output_scale;
+  d.return_lse = desc->return_lse;
+  d.flags = desc->flags;
+  d.out_dtype = desc->out_dtype;
+  pka_prefill_plan* p = nullptr;
+  const int rc = guarded([&] {
+    return batch_prefill_plan(&p, &d, qo_indptr_host, kv_indptr_host, nullptr, num_tiles_out,
+                              stream);
+  });
+  if (rc != PKA_OK) return rc;
+  p->latent = true;
+  *plan_out = p;
+  return PKA_OK;
+}
+
+int batch_latent_prefill_run(const pka_prefill_plan* p, const void* q, int64_t q_stride_tok,
+                             int64_t q_stride_head, const void* k_nope, const void* k_rope,
+                             int64_t rope_stride, const void* v, int64_t kv_stride_tok,
+                             int64_t kv_stride_head, void* out, float* lse, void* stream) {
+  NvtxRange nvtx_range("pka::batch_latent_prefill_run");
+  clear_error();
+  PKA_CHECK_ARG(p != nullptr, "plan must not be NULL");
+  PKA_CHECK_ARG(p->latent, "the plan was made by batch_prefill_plan");
+  PKA_CHECK_ARG(p->dev_buf != nullptr, "plan was built with PKA_PLAN_HOST_ONLY and cannot run");
+  PKA_CHECK_ARG(q && k_nope && k_rope && v && out,
+                "q, k_nope, k_rope, v and out must not be NULL");
+  PKA_CHECK_ARG(!p->desc.return_lse || lse != nullptr, "the plan returns the LSE: lse is NULL");
+  PKA_CHECK_ARG(aligned(out, 16) && aligned(lse, 4), "out must be 16-byte aligned, lse 4-byte");
+  for (int64_t s : {q_stride_tok, q_stride_head, rope_stride, kv_stride_tok, kv_stride_head})
+    PKA_CHECK_ARG(s > 0 && s % 8 == 0, "strides must be positive multiples of 8 elements");
+  int rc = check_device(p->device);
+  if (rc != PKA_OK) return rc;
+  if (p->tiles.empty()) return PKA_OK;
+  CUtensorMap qmap, kmap, rmap, vmap;
+  const uint64_t H = (uint64_t)p->Hq, nk = (uint64_t)p->total_kv;
+  const uint32_t qbox[3] = {64, 1, 128}, kbox[3] = {64, 1, 64};
+  {
+    const uint64_t dims[3] = {192, H, (uint64_t)p->total_q};
+    const uint64_t strides[2] = {(uint64_t)q_stride_head * 2, (uint64_t)q_stride_tok * 2};
+    rc = encode_bf16_map(&qmap, q, 3, dims, strides, qbox);
+    if (rc != PKA_OK) return rc;
+  }
+  {
+    const uint64_t dims[3] = {128, H, nk};
+    const uint64_t strides[2] = {(uint64_t)kv_stride_head * 2, (uint64_t)kv_stride_tok * 2};
+    rc = encode_bf16_map(&kmap, k_nope, 3, dims, strides, kbox);
+    if (rc != PKA_OK) return rc;
+    rc = encode_bf16_map(&vmap, v, 3, dims, strides, kbox);
+    if (rc != PKA_OK) return rc;
+  }
+  {
+    const uint64_t dims[3] = {64, 1, nk};
+    const uint64_t strides[2] = {128, (uint64_t)rope_stride * 2};
+    rc = encode_bf16_map(&rmap, k_rope, 3, dims, strides, kbox);
+    if (rc != PKA_OK) return rc;
+  }
+  PrefillArgs a{};
+  a.q = q;
+  a.q_stride_tok = q_stride_tok;
+  a.q_stride_head = q_stride_head;
+  a.out = out;
+  a.lse = p->desc.return_lse ? lse : nullptr;
+  a.tiles = p->d_tiles;
+  a.status = p->d_status;
+  a.num_tiles = (int32_t)p->tiles.size();
+  a.num_qo_heads = p->Hq;
+  a.num_kv_heads = p->Hkv;
+  a.group = 1;
+  a.causal = p->desc.mask == PKA_MASK_CAUSAL;
+  a.window_left = -1;
+  a.scale_log2 = p->scale * 1.4426950408889634f;
+  a.output_scale = p->desc.output_scale;
+  a.out_dtype = p->desc.out_dtype;
+  return launch_latent_prefill(*p, a, qmap, kmap, rmap, vmap, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

@@ -68,6 +68,8 @@ struct DecodeArgs {
 enum : int32_t {
   STATUS_WAIT_TIMEOUT = 1,  // an mbarrier wait hit its iteration limit
   STATUS_PAGE_BOUNDS = 2,   // paged_decode_check_tables found an entry outside [0, num_pages)
+  STATUS_CAPACITY = 4,      // paged_kv_tables: a step that does not fit
+  STATUS_SLOT_BOUNDS = 8,   // paged_latent_append: a slot past the pool
 };
 
 }  // namespace pka

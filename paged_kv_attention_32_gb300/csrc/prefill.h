@@ -69,6 +69,7 @@ struct pka_prefill_plan {
   const int32_t* d_row_map = nullptr;
   int32_t* d_status = nullptr;
   int device = -1;
+  bool latent = false;   // made by batch_latent_prefill_plan: run by its own entry point
 };
 
 namespace pka {
