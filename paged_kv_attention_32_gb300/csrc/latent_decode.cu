@@ -8,6 +8,9 @@
 #include "device_common.cuh"
 #include "host_common.h"
 #include "latent.h"
+#include "prefill_softmax.cuh"
+#include "tcgen05.cuh"
+#include "tmap.h"
 
 namespace pka {
 
@@ -15,92 +18,501 @@ using namespace dev;
 
 namespace {
 
-// One CTA per (piece, query row): each warp takes every fourth key with the
-// row's values spread over its lanes, and keeps a running maximum and sum.
-template <int DL, bool F16>
-__global__ void __launch_bounds__(128)
-latent_decode_rows_kernel(const __grid_constant__ LatentArgs a, const uint16_t* pages,
-                          int64_t stride_page) {
-  constexpr int D = DL + kLatentRopeDim, V = D / 64;   // 32-bit words of a row per lane
-  __shared__ float s_o[4][DL];
-  __shared__ float s_m[4], s_l[4];
-  const LatentItem it = a.items[blockIdx.x];
-  const LatentReq rq = a.reqs[it.request];
-  const int r = blockIdx.y;
-  if (r >= rq.q_len * a.num_heads) return;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int i = r / a.num_heads, h = r % a.num_heads;
-  int kv = rq.kv_len;
-  if (a.seq_lens_live != nullptr) kv = min(max(__ldg(a.seq_lens_live + it.request), 0), kv);
-  const int seen = a.causal ? min(kv, kv - rq.q_len + i + 1) : kv;
-  const int k0 = it.tile_lo * kLatentTile, k1 = min(it.tile_hi * kLatentTile, seen);
-  const int64_t t = rq.q_start + i;
-  const uint32_t* q = reinterpret_cast<const uint32_t*>(
-      static_cast<const uint16_t*>(a.q) + t * a.q_stride_tok + h * a.q_stride_head);
-  float2 qv[V];
+// ---- the decode kernel -----------------------------------------------------------
+
+constexpr int kThreads = 192;
+constexpr float kRescaleThreshold = 8.0f;
+constexpr uint32_t kSmemLimit = 232448;   // dynamic shared memory of one CTA
+
+// Shared memory and TMEM of latent_dim DL with N query rows.
+template <int DL, int N>
+struct Geo {
+  static constexpr int NC = DL / 64 + 1;                // 64-column chunks of a cached row
+  static constexpr uint32_t kGroup = NC * 1024;         // 8 keys: NC atoms of 8 x 128 bytes
+  static constexpr uint32_t kTile = 8 * kGroup;         // 64 keys
+  static constexpr uint32_t kQChunk = N * 128;          // 64 columns of the queries
+  static constexpr uint32_t kQ = NC * kQChunk;
+  static constexpr uint32_t kP = N * 128;               // N rows of 64 weights
+  static constexpr uint32_t kMisc = 256 + (8 + 3) * N * 4;
+  static constexpr int NP = kSmemLimit - kMisc - kQ - kP >= 2 * kTile + kP ? 2 : 1;
+  static constexpr int kRoom = (kSmemLimit - kMisc - kQ - NP * kP) / kTile;
+  static constexpr int NS = kRoom < 4 ? kRoom : 4;      // stages of 64 keys
+  static constexpr uint32_t kOffK = 0;
+  static constexpr uint32_t kOffQ = kOffK + NS * kTile;
+  static constexpr uint32_t kOffP = kOffQ + kQ;
+  static constexpr uint32_t kOffMisc = kOffP + NP * kP;
+  static constexpr uint32_t kSmem = kOffMisc + kMisc;
+  static constexpr uint32_t kColS = (DL / 128) * N;     // O blocks, then the two S buffers
+  static constexpr uint32_t kCols = kColS + 2 * N;
+  static constexpr uint32_t kTmemCols = kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
+  static_assert(NS >= 2 && kSmem <= kSmemLimit, "two stages of keys");
+};
+
+// mbarriers.  T counts a CTA's tiles over all its pieces: stage T % NS, S and
+// P V barriers T & 1.  No wait is more than one phase ahead of its barrier: S(T)
+// is issued after P V(T - 2), so whoever saw S(T) knows P V(T - 2) complete.
+enum {
+  L_KFULL = 0, L_KEMPTY = 4, L_SFULL = 8, L_PFULL = 10, L_PV = 12, L_QFULL = 14, L_OFREE = 15,
+  L_MMADONE = 16, L_COUNT = 17
+};
+static_assert(L_COUNT * 8 + 4 + 16 <= 256, "barriers, TMEM address, failure flags");
+
+__device__ __forceinline__ void bar_sync_softmax() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+// Max or sum over the eight lanes that share lane % 4, of C values each.  The
+// lanes trade halves, so that each ends with C / 8 (at least one) totals: value
+// index first_value(lane) on.
+template <int C, typename Op>
+__device__ __forceinline__ void reduce_rows(float* x, int lane, Op op) {
+  int n = C;
 #pragma unroll
-  for (int v = 0; v < V; ++v) qv[v] = unpack2<F16>(__ldg(q + v * 32 + lane));
-  float m = neg_inf(), l = 0.f;
-  float2 o[V - 1];
+  for (int d = 16; d >= 4; d >>= 1) {
+    if (n > 1) {
+      n >>= 1;
+      const bool up = lane & d;
 #pragma unroll
-  for (int v = 0; v < V - 1; ++v) o[v] = make_float2(0.f, 0.f);
-  const int32_t* table = a.block_tables + (int64_t)it.request * a.bt_row_stride;
-  for (int k = k0 + warp; k < k1; k += 4) {
-    const int page = __ldg(table + k / a.page_size);
-    float2 x[V];
-    if (page >= 0 && page < a.num_pages) {
-      const uint32_t* row = reinterpret_cast<const uint32_t*>(
-          pages + page * stride_page + (int64_t)(k % a.page_size) * D);
-#pragma unroll
-      for (int v = 0; v < V; ++v) x[v] = unpack2<F16>(__ldg(row + v * 32 + lane));
+      for (int i = 0; i < C / 2; ++i)
+        if (i < n) {
+          const float mine = up ? x[i + n] : x[i], other = up ? x[i] : x[i + n];
+          x[i] = op(mine, __shfl_xor_sync(0xffffffffu, other, d));
+        }
     } else {
-#pragma unroll
-      for (int v = 0; v < V; ++v) x[v] = make_float2(0.f, 0.f);
-    }
-    float s = 0.f;
-#pragma unroll
-    for (int v = 0; v < V; ++v) s += qv[v].x * x[v].x + qv[v].y * x[v].y;
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-    s *= a.scale_log2;
-    const float mn = fmaxf(m, s), sc = ex2(m - mn), p = ex2(s - mn);
-    m = mn;
-    l = l * sc + p;
-#pragma unroll
-    for (int v = 0; v < V - 1; ++v) {
-      o[v].x = o[v].x * sc + p * x[v].x;
-      o[v].y = o[v].y * sc + p * x[v].y;
+      x[0] = op(x[0], __shfl_xor_sync(0xffffffffu, x[0], d));
     }
   }
-#pragma unroll
-  for (int v = 0; v < V - 1; ++v) {
-    s_o[warp][v * 64 + lane * 2] = o[v].x;
-    s_o[warp][v * 64 + lane * 2 + 1] = o[v].y;
+}
+template <int C>
+__device__ __forceinline__ int first_value(int lane) {
+  const int b4 = (lane >> 4) & 1, b3 = (lane >> 3) & 1, b2 = (lane >> 2) & 1;
+  return C == 16 ? 8 * b4 + 4 * b3 + 2 * b2 : C == 8 ? 4 * b4 + 2 * b3 + b2 : 2 * b4 + b3;
+}
+
+// What a CTA needs to know of its piece.
+struct Piece {
+  LatentReq rq;
+  int request, kv, tile0, n, part, row0, rows;   // rows: live rows of the CTA's row block
+  __device__ __forceinline__ Piece(const LatentArgs& a, int item, int row_block, int row_tile) {
+    const LatentItem it = a.items[item];
+    rq = a.reqs[it.request];
+    request = it.request;
+    part = it.part;
+    kv = rq.kv_len;
+    if (a.seq_lens_live != nullptr) kv = min(max(__ldg(a.seq_lens_live + request), 0), kv);
+    row0 = row_block * row_tile;
+    rows = min(row_tile, rq.q_len * a.num_heads - row0);
+    tile0 = it.tile_lo;
+    n = rows > 0 ? max(0, min(it.tile_hi, (kv + kLatentTile - 1) / kLatentTile) - tile0) : 0;
   }
-  if (lane == 0) {
-    s_m[warp] = m;
-    s_l[warp] = l;
-  }
-  __syncthreads();
-  const float mm = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
-  float w[4], ll = 0.f;
-#pragma unroll
-  for (int x = 0; x < 4; ++x) {
-    w[x] = s_m[x] == neg_inf() ? 0.f : ex2(s_m[x] - mm);
-    ll += w[x] * s_l[x];
-  }
-  const bool whole = it.part < 0;
-  const int64_t prow = rq.part_base + (int64_t)max(it.part, 0) * rq.q_len * a.num_heads + r;
-  const float inv = ll > 0.f ? (whole ? a.output_scale : 1.f) / ll : 0.f;
-  for (int dd = tid; dd < DL; dd += 128) {
-    const float v = (w[0] * s_o[0][dd] + w[1] * s_o[1][dd] + w[2] * s_o[2][dd] + w[3] * s_o[3][dd]) * inv;
-    if (whole) store_out1(a.out, (t * a.num_heads + h) * DL + dd, v, a.out_dtype);
-    else a.ws_o[prow * DL + dd] = v;
-  }
+};
+
+template <int DL, int N, bool F16>
+__global__ void __launch_bounds__(kThreads, 1)
+latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant__ CUtensorMap tmk) {
+  using G = Geo<DL, N>;
+  constexpr int NC = G::NC, NS = G::NS, NP = G::NP, C = N / 4;
+  constexpr uint32_t kIdescQK = idesc_bf16_f32(64, N, 0, 0, F16);
+  constexpr uint32_t kIdescPV = idesc_bf16_f32(128, N, 1, 0, F16);
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sbase = smem_u32(smem);
+  uint8_t* misc = smem + G::kOffMisc;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + L_COUNT * 8);
+  volatile int* s_fail = reinterpret_cast<volatile int*>(tmem_slot + 1);   // [3]
+  float* s_max = reinterpret_cast<float*>(misc + 256);   // [2][4 warps][N]
+  float* s_col = s_max + 8 * N;                          // [N] rescale factors, then 1 / l
+  float* s_ref = s_col + N;                              // [N] reference maxima
+  int* s_seen = reinterpret_cast<int*>(s_ref + N);       // [N] keys each row sees
+  auto bar = [&](int i) -> uint32_t { return sbase + G::kOffMisc + 8u * (uint32_t)i; };
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int seg = blockIdx.x / a.row_blocks, rb = blockIdx.x % a.row_blocks;
+  const int item0 = __ldg(a.segments + seg), item1 = __ldg(a.segments + seg + 1);
+
   if (tid == 0) {
-    const float lse = ll > 0.f ? mm + log2f(ll) : neg_inf();
-    if (!whole) a.ws_lse[prow] = lse;
-    else if (a.lse != nullptr) a.lse[t * a.num_heads + h] = lse;
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(bar(L_KFULL + s), 1);
+      mbar_init(bar(L_KEMPTY + s), 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(bar(L_SFULL + s), 1);
+      mbar_init(bar(L_PFULL + s), 128);
+      mbar_init(bar(L_PV + s), 1);
+    }
+    mbar_init(bar(L_QFULL), 128);
+    mbar_init(bar(L_OFREE), 128);
+    mbar_init(bar(L_MMADONE), 1);
+    for (int i = 0; i < 3; ++i) s_fail[i] = 0;
+    fence_barrier_init();
+  }
+  if (warp == 5) {
+    tmem_alloc(smem_u32(tmem_slot), G::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 4) {
+    // ---------------- TMA producer: lane i copies box i of a tile ----------------
+    if (lane == 0) tma_prefetch_desc(&tmk);
+    const int boxes = kLatentTile / a.box_rows;
+    const uint32_t dst0 = sbase + G::kOffK + (uint32_t)lane * (uint32_t)(a.box_rows / 8) * G::kGroup;
+    int T = 0;
+    bool ok = true;
+    for (int item = item0; ok && item < item1; ++item) {
+      const Piece pc(a, item, rb, N);
+      const int32_t* table = a.block_tables + (int64_t)pc.request * a.bt_row_stride;
+      for (int j = 0; j < pc.n; ++j, ++T) {
+        const int st = T % NS, tok = (pc.tile0 + j) * kLatentTile + lane * a.box_rows;
+        // a box past the last token reads as zeros: its page lies outside the pool
+        const int page = lane < boxes && tok < pc.kv ? __ldg(table + tok / a.page_size) : a.num_pages;
+        if (T >= NS && !warp_wait(bar(L_KEMPTY + st), (uint32_t)((T / NS - 1) & 1), a.status)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) mbar_arrive_expect_tx(bar(L_KFULL + st), G::kTile);
+        __syncwarp();
+        if (lane < boxes)
+          tma_load_5d(dst0 + (uint32_t)st * G::kTile, &tmk, bar(L_KFULL + st), 0, 0, 0,
+                      (tok % a.page_size) / 8, page);
+        __syncwarp();
+      }
+    }
+    if (!ok)   // give the copies already issued a bounded chance to land
+      for (int i = max(0, T - NS); i < T; ++i)
+        mbar_wait(bar(L_KFULL + i % NS), (uint32_t)((i / NS) & 1), nullptr);
+  } else if (warp == 5) {
+    // ---------------- MMA issuer ----------------
+    int T = 0, I = 0;   // tiles and non-empty pieces before this one
+    bool ok = true;
+    for (int item = item0; ok && item < item1; ++item) {
+      const Piece pc(a, item, rb, N);
+      if (pc.n == 0) continue;
+      ok = warp_wait(bar(L_QFULL), (uint32_t)(I & 1), a.status);
+      int qk = 0, pv = 0;   // tiles whose S / whose P V was issued
+      uint64_t t0 = 0;
+      while (ok && pv < pc.n) {
+        // S runs at most two tiles ahead of P V, and never makes a ready P V wait
+        // for keys that are still on their way (P V is what frees a stage)
+        const int k = T + qk, p = T + pv;
+        if (qk < pc.n && qk <= pv + 1 &&
+            __all_sync(0xffffffffu, mbar_test_wait(bar(L_KFULL + k % NS), (uint32_t)((k / NS) & 1)))) {
+          const uint32_t kb = sbase + G::kOffK + (uint32_t)(k % NS) * G::kTile;
+          const int live = pc.kv - (pc.tile0 + qk) * kLatentTile;
+          if (live < kLatentTile) {
+            // rows past the last token may hold anything, and 0 * inf is not 0:
+            // clear them (copies past the last token brought zeros already)
+            const int end = (live + a.box_rows - 1) / a.box_rows * a.box_rows;
+            for (int r = live; r < end; ++r)
+              for (int c = lane; c < NC * 8; c += 32)
+                *reinterpret_cast<uint4*>(smem + G::kOffK + (uint32_t)(k % NS) * G::kTile +
+                                          (uint32_t)(r >> 3) * G::kGroup + (uint32_t)(c >> 3) * 1024u +
+                                          (uint32_t)(r & 7) * 128u + (uint32_t)(c & 7) * 16u) =
+                    make_uint4(0u, 0u, 0u, 0u);
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+          tc_fence_after();
+          const uint32_t d = tmem + G::kColS + (uint32_t)(k & 1) * N;
+#pragma unroll
+          for (int c = 0; c < NC; ++c)   // 64 keys x N rows += 64 columns of each
+            umma_ss_k4(d, smem_desc_sw128(kb + (uint32_t)c * 1024u, 16u, G::kGroup),
+                       smem_desc_sw128(sbase + G::kOffQ + (uint32_t)c * G::kQChunk, 16u, 1024u),
+                       kIdescQK, c > 0 ? 1u : 0u);
+          umma_commit_elect(bar(L_SFULL + (k & 1)));
+          ++qk;
+          t0 = 0;
+          continue;
+        }
+        if (pv < qk &&
+            __all_sync(0xffffffffu, mbar_test_wait(bar(L_PFULL + (p & 1)), (uint32_t)((p >> 1) & 1)))) {
+          if (pv == 0 && I > 0 && !(ok = warp_wait(bar(L_OFREE), (uint32_t)((I - 1) & 1), a.status)))
+            break;
+          tc_fence_after();
+          const uint32_t kb = sbase + G::kOffK + (uint32_t)(p % NS) * G::kTile;
+          const uint32_t pb = sbase + G::kOffP + (uint32_t)(p % NP) * G::kP;
+#pragma unroll
+          for (int blk = 0; blk < DL / 128; ++blk)   // 128 dims x N rows += 64 keys
+            umma_ss_k4_steps<2 * (int)G::kGroup / 16, 2>(
+                tmem + (uint32_t)blk * N,
+                smem_desc_sw128(kb + (uint32_t)blk * 2048u, 1024u, G::kGroup),
+                smem_desc_sw128(pb, 16u, 1024u), kIdescPV, pv > 0 ? 1u : 0u);
+          umma_commit_elect(bar(L_PV + (p & 1)));
+          umma_commit_elect(bar(L_KEMPTY + p % NS));
+          ++pv;
+          t0 = 0;
+          continue;
+        }
+        const uint64_t now = global_timer_ns();
+        if (t0 == 0) t0 = now;
+        if (!__all_sync(0xffffffffu, now - t0 <= kWaitLimitNs)) {
+          if (lane == 0) atomicOr(a.status, STATUS_WAIT_TIMEOUT);
+          ok = false;
+        }
+      }
+      T += pc.n;
+      ++I;
+    }
+    umma_commit_elect(bar(L_MMADONE));
+    warp_wait(bar(L_MMADONE), 0, a.status);   // nothing of ours still runs on the tensor core
+  } else {
+    // ---------------- softmax and output: warps 0-3 ----------------
+    const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
+    const int col0 = 2 * (lane & 3);   // this thread's columns: 8j + col0 + {0, 1}
+    const float sl2 = a.scale_log2;
+
+    // the queries of a piece into shared memory, N rows of NC swizzled chunks
+    auto load_q = [&](const Piece& pc) {
+      constexpr int V = NC * 8;   // 16-byte pieces of a row
+#pragma unroll 4
+      for (int i = tid; i < N * V; i += 128) {
+        const int r = i / V, c = i % V;
+        uint4 x = make_uint4(0u, 0u, 0u, 0u);
+        if (r < pc.rows) {
+          const int tok = (pc.row0 + r) / a.num_heads, h = (pc.row0 + r) % a.num_heads;
+          x = __ldg(reinterpret_cast<const uint4*>(
+                        static_cast<const uint16_t*>(a.q) + (int64_t)(pc.rq.q_start + tok) * a.q_stride_tok +
+                        (int64_t)h * a.q_stride_head) + c);
+        }
+        *reinterpret_cast<uint4*>(smem + G::kOffQ + (uint32_t)(c >> 3) * G::kQChunk +
+                                  swz128((uint32_t)r, (uint32_t)(c & 7))) = x;
+      }
+      fence_proxy_async_smem();   // generic writes -> the tensor core's operand reads
+      mbar_arrive(bar(L_QFULL));
+    };
+    // the next piece that has tiles, from `item` on
+    auto next_q = [&](int item) {
+      for (; item < item1; ++item) {
+        const Piece pc(a, item, rb, N);
+        if (pc.n > 0) {
+          load_q(pc);
+          return;
+        }
+      }
+    };
+    next_q(item0);
+
+    int T = 0;
+    bool ok = true;
+    for (int item = item0; ok && item < item1; ++item) {
+      const Piece pc(a, item, rb, N);
+      if (pc.rows <= 0) continue;
+      const bool whole = pc.part < 0;
+      const int64_t orow = (int64_t)pc.rq.q_start * a.num_heads + pc.row0;   // first output row
+      const int64_t prow = (int64_t)pc.rq.part_base +
+                           (int64_t)max(pc.part, 0) * pc.rq.q_len * a.num_heads + pc.row0;
+      if (pc.n == 0) {   // no keys here: zero rows, or a piece that weighs nothing
+        for (int i = tid; i < pc.rows; i += 128) {
+          if (!whole) a.ws_lse[prow + i] = neg_inf();
+          else if (a.lse != nullptr) a.lse[orow + i] = neg_inf();
+        }
+        if (whole)
+          for (int i = tid; i < pc.rows * DL; i += 128) store_out1(a.out, orow * DL + i, 0.f, a.out_dtype);
+        continue;
+      }
+      if (tid < N) {
+        const int tok = (pc.row0 + tid) / a.num_heads;
+        s_seen[tid] = a.causal ? min(pc.kv, pc.kv - pc.rq.q_len + tok + 1) : pc.kv;
+      }
+      // the first row of the block sees the fewest keys; s_seen is read behind
+      // the barrier of the first tile
+      const int seen_min =
+          a.causal ? min(pc.kv, pc.kv - pc.rq.q_len + pc.row0 / a.num_heads + 1) : pc.kv;
+      float m[C], l[C];
+#pragma unroll
+      for (int q = 0; q < C; ++q) {
+        m[q] = neg_inf();
+        l[q] = 0.f;
+      }
+      bar_sync_softmax();
+      for (int j = 0; j < pc.n; ++j, ++T) {
+        const int key0 = (pc.tile0 + j) * kLatentTile;
+        const bool got = warp_wait(bar(L_SFULL + (T & 1)), (uint32_t)((T >> 1) & 1), a.status);
+        if (!got) s_fail[T & 1] = 1;
+        tc_fence_after();
+        uint32_t s[N / 2];
+        const uint32_t s_tm = tmem + lane_off + G::kColS + (uint32_t)(T & 1) * N;
+        if constexpr (N == 16) tmem_ld_frag2(s_tm, s);
+        else if constexpr (N == 32) tmem_ld_frag4(s_tm, s);
+        else tmem_ld_frag8(s_tm, s);
+        tmem_wait_ld();
+        reg_fence<N / 2>(s);
+        float x[N / 2];
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) x[i] = __uint_as_float(s[i]) * sl2;
+        if (key0 + kLatentTile > seen_min) {
+          const int k = key0 + warp * 16 + (lane >> 2);
+#pragma unroll
+          for (int jj = 0; jj < N / 8; ++jj)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int seen = s_seen[8 * jj + col0 + e];
+              if (k >= seen) x[4 * jj + e] = neg_inf();
+              if (k + 8 >= seen) x[4 * jj + 2 + e] = neg_inf();
+            }
+        }
+        // row maxima over the tile's 64 keys: lanes, then warps
+        float mx[C];
+#pragma unroll
+        for (int q = 0; q < C; ++q)
+          mx[q] = fmaxf(x[4 * (q >> 1) + (q & 1)], x[4 * (q >> 1) + 2 + (q & 1)]);
+        reduce_rows<C>(mx, lane, [](float u, float v) { return fmaxf(u, v); });
+        float* wm = s_max + (T & 1) * 4 * N;
+        {
+          float* w = wm + warp * N + (lane & 3) * C + first_value<C>(lane);
+          w[0] = mx[0];
+          if constexpr (C == 16) w[1] = mx[1];
+        }
+        bar_sync_softmax();
+        if (s_fail[T & 1]) {
+          ok = false;
+          break;
+        }
+#pragma unroll
+        for (int q = 0; q < C; q += 4) {
+          float4 u = *reinterpret_cast<const float4*>(wm + (lane & 3) * C + q);
+#pragma unroll
+          for (int w = 1; w < 4; ++w) {
+            const float4 v = *reinterpret_cast<const float4*>(wm + w * N + (lane & 3) * C + q);
+            u = make_float4(fmaxf(u.x, v.x), fmaxf(u.y, v.y), fmaxf(u.z, v.z), fmaxf(u.w, v.w));
+          }
+          mx[q] = u.x;
+          mx[q + 1] = u.y;
+          mx[q + 2] = u.z;
+          mx[q + 3] = u.w;
+        }
+        // lazy rescale: the reference moves only when a maximum grew by more than
+        // 2^8; a row without visible keys so far still has O = 0 and takes its
+        // first reference without one.  Every warp holds the same maxima, so all
+        // four decide alike.
+        float al[C];
+        bool rescale = false;
+#pragma unroll
+        for (int q = 0; q < C; ++q) {
+          const bool grow = mx[q] > m[q] + kRescaleThreshold;
+          al[q] = grow && m[q] != neg_inf() ? ex2(m[q] - mx[q]) : 1.f;
+          rescale = rescale || (grow && m[q] != neg_inf());
+          if (grow) m[q] = mx[q];
+        }
+        if (j > 0 && __any_sync(0xffffffffu, rescale)) {
+          if (!warp_wait(bar(L_PV + ((T - 1) & 1)), (uint32_t)(((T - 1) >> 1) & 1), a.status))
+            s_fail[2] = 1;
+          tc_fence_after();
+          if (warp == 0 && lane < 4)
+#pragma unroll
+            for (int q = 0; q < C; ++q) s_col[8 * (q >> 1) + col0 + (q & 1)] = al[q];
+          bar_sync_softmax();
+          if (s_fail[2]) {
+            ok = false;
+            break;
+          }
+#pragma unroll
+          for (int q = 0; q < C; ++q) l[q] *= al[q];
+#pragma unroll 1
+          for (int c = 0; c < DL / 128 * N; c += 16) {
+            uint32_t r[16];
+            tmem_ld16(tmem + lane_off + (uint32_t)c, r);
+            tmem_wait_ld();
+            reg_fence<16>(r);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              r[i] = __float_as_uint(__uint_as_float(r[i]) * s_col[(c + i) % N]);
+            tmem_st16(tmem + lane_off + (uint32_t)c, r);
+          }
+          tmem_wait_st();
+          bar_sync_softmax();   // s_col is free again
+        }
+        // p = exp2(x - m), summed in 32 bits, rounded to the inputs' format for P V
+        float neg[C];
+#pragma unroll
+        for (int q = 0; q < C; ++q) neg[q] = m[q] == neg_inf() ? 0.f : -m[q];
+#pragma unroll
+        for (int jj = 0; jj < N / 8; ++jj)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float p0 = ex2(x[4 * jj + e] + neg[2 * jj + e]);
+            const float p1 = ex2(x[4 * jj + 2 + e] + neg[2 * jj + e]);
+            l[2 * jj + e] += p0 + p1;
+            x[4 * jj + e] = p0;
+            x[4 * jj + 2 + e] = p1;
+          }
+        // with two P buffers, S(T) complete means P V(T - 2) complete: buffer free
+        if (NP == 1 && j > 0 &&
+            !warp_wait(bar(L_PV + ((T - 1) & 1)), (uint32_t)(((T - 1) >> 1) & 1), a.status))
+          s_fail[(T + 1) & 1] = 1;   // seen behind the next tile's barrier, or at the end
+        const uint32_t pb = sbase + G::kOffP + (uint32_t)(T % NP) * G::kP;
+#pragma unroll
+        for (int jj = 0; jj < N / 8; jj += 2) {
+          // matrices: rows 8jj.. keys 0-7 and 8-15 of the warp, rows 8(jj + 1).. alike
+          const int mt = lane >> 3;
+          const uint32_t row = (uint32_t)(8 * (jj + (mt >> 1)) + (lane & 7));
+          stmatrix_x4_trans(pb + swz128(row, (uint32_t)(2 * warp + (mt & 1))),
+                            pack2<F16>(x[4 * jj], x[4 * jj + 1]),
+                            pack2<F16>(x[4 * jj + 2], x[4 * jj + 3]),
+                            pack2<F16>(x[4 * jj + 4], x[4 * jj + 5]),
+                            pack2<F16>(x[4 * jj + 6], x[4 * jj + 7]));
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        mbar_arrive(bar(L_PFULL + (T & 1)));
+      }
+      if (!ok) break;
+      next_q(item + 1);   // the last S is complete: the query buffer is free
+
+      // ---- output: O^T / l, one latent dimension per thread and row block ----
+      reduce_rows<C>(l, lane, [](float u, float v) { return u + v; });
+      float* s_sum = s_max + (T & 1) * 4 * N;   // the half the last tile did not use
+      {
+        const int q = (lane & 3) * C + first_value<C>(lane);
+        s_sum[warp * N + q] = l[0];
+        if constexpr (C == 16) s_sum[warp * N + q + 1] = l[1];
+      }
+      if (warp == 0 && lane < 4)
+#pragma unroll
+        for (int q = 0; q < C; ++q) s_ref[8 * (q >> 1) + col0 + (q & 1)] = m[q];
+      if (!warp_wait(bar(L_PV + ((T - 1) & 1)), (uint32_t)(((T - 1) >> 1) & 1), a.status)) s_fail[2] = 1;
+      bar_sync_softmax();
+      if (s_fail[2]) {
+        ok = false;
+        break;
+      }
+      if (tid < N) {
+        const int q = ((tid & 7) >> 1) * C + 2 * (tid >> 3) + (tid & 1);   // column tid in s_sum
+        const float sum = (s_sum[q] + s_sum[N + q]) + (s_sum[2 * N + q] + s_sum[3 * N + q]);
+        s_col[tid] = sum > 0.f ? (whole ? a.output_scale : 1.f) / sum : 0.f;
+        if (tid < pc.rows) {
+          const float lse = sum > 0.f ? s_ref[tid] + log2f(sum) : neg_inf();
+          if (!whole) a.ws_lse[prow + tid] = lse;
+          else if (a.lse != nullptr) a.lse[orow + tid] = lse;
+        }
+      }
+      bar_sync_softmax();
+      tc_fence_after();
+#pragma unroll 1
+      for (int c = 0; c < DL / 128 * N; c += 16) {
+        uint32_t r[16];
+        tmem_ld16(tmem + lane_off + (uint32_t)c, r);
+        tmem_wait_ld();
+        reg_fence<16>(r);
+        const int n0 = c % N, d = c / N * 128 + warp * 32 + lane;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (n0 + i < pc.rows) {
+            const float v = __uint_as_float(r[i]) * s_col[n0 + i];
+            if (whole) store_out1(a.out, (orow + n0 + i) * DL + d, v, a.out_dtype);
+            else a.ws_o[(prow + n0 + i) * DL + d] = v;
+          }
+      }
+      tc_fence_before();
+      mbar_arrive(bar(L_OFREE));
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 5) {
+    tc_fence_after();
+    tmem_dealloc(tmem, G::kTmemCols);
   }
 }
 
@@ -154,15 +566,23 @@ latent_merge_kernel(const __grid_constant__ LatentArgs a) {
   if (x == 0 && a.lse != nullptr) a.lse[row] = sum > 0.f ? m + log2f(sum) : neg_inf();
 }
 
-template <int DL>
-int launch(const pka_latent_plan& plan, const LatentArgs& a, const void* pages, int64_t stride_page,
+template <int DL, int N, bool F16>
+cudaError_t launch_tiles(const LatentArgs& a, const CUtensorMap& map, cudaStream_t stream) {
+  auto kern = latent_decode_kernel<DL, N, F16>;
+  static std::atomic<uint64_t> smem_set{0};   // devices whose limit was raised
+  const cudaError_t e = set_smem_once(kern, (int)Geo<DL, N>::kSmem, smem_set);
+  if (e != cudaSuccess) return e;
+  kern<<<(unsigned)(a.num_segments * a.row_blocks), kThreads, Geo<DL, N>::kSmem, stream>>>(a, map);
+  return cudaGetLastError();
+}
+
+template <int DL, bool F16>
+int launch(const pka_latent_plan& plan, const LatentArgs& a, const CUtensorMap& map,
            cudaStream_t stream) {
-  const dim3 grid((unsigned)a.num_items, (unsigned)a.max_rows);
-  auto kern = plan.desc.dtype == PKA_DTYPE_F16 ? latent_decode_rows_kernel<DL, true>
-                                               : latent_decode_rows_kernel<DL, false>;
-  kern<<<grid, 128, 0, stream>>>(a, static_cast<const uint16_t*>(pages), stride_page);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return cuda_fail(e, "latent decode kernel launch");
+  cudaError_t e = plan.row_tile == 16   ? launch_tiles<DL, 16, F16>(a, map, stream)
+                  : plan.row_tile == 32 ? launch_tiles<DL, 32, F16>(a, map, stream)
+                                        : launch_tiles<DL, 64, F16>(a, map, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "latent_decode_kernel launch");
   if (a.num_splits > 0) {
     latent_merge_kernel<DL><<<(unsigned)(a.num_splits * a.max_rows), DL, 0, stream>>>(a);
     e = cudaGetLastError();
@@ -176,8 +596,22 @@ int launch(const pka_latent_plan& plan, const LatentArgs& a, const void* pages, 
 int launch_latent_decode(const pka_latent_plan& plan, const LatentArgs& a, const void* pages,
                          int64_t stride_page, cudaStream_t stream) {
   if (a.num_items == 0) return PKA_OK;
-  return plan.desc.latent_dim == 512 ? launch<512>(plan, a, pages, stride_page, stream)
-                                     : launch<256>(plan, a, pages, stride_page, stream);
+  // The pool as (64 columns, slot in 8, column chunk, slot / 8, page): one box of
+  // box_rows slots lands as groups of 8 keys, each NC swizzled 8 x 128 byte atoms.
+  // Groups are evenly spaced whatever the page size, so a tile of 64 keys from
+  // any number of pages is one operand, as keys (K-major) and as values (MN-major).
+  const uint64_t row = (uint64_t)(plan.desc.latent_dim + plan.desc.rope_dim) * 2;
+  const uint32_t nc = (uint32_t)plan.desc.latent_dim / 64 + 1;
+  const uint64_t dims[5] = {64, 8, nc, (uint64_t)plan.desc.page_size / 8, (uint64_t)plan.desc.num_pages};
+  const uint64_t strides[4] = {row, 128, 8 * row, (uint64_t)stride_page * 2};
+  const uint32_t box[5] = {64, 8, nc, (uint32_t)a.box_rows / 8, 1};
+  CUtensorMap map;
+  const int rc = encode_bf16_map(&map, pages, 5, dims, strides, box);
+  if (rc != PKA_OK) return rc;
+  const bool f16 = plan.desc.dtype == PKA_DTYPE_F16;
+  if (plan.desc.latent_dim == 512)
+    return f16 ? launch<512, true>(plan, a, map, stream) : launch<512, false>(plan, a, map, stream);
+  return f16 ? launch<256, true>(plan, a, map, stream) : launch<256, false>(plan, a, map, stream);
 }
 
 }  // namespace pka
