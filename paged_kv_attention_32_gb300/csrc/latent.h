@@ -58,6 +58,7 @@ struct LatentArgs {
   int32_t num_heads;
   int32_t page_size;
   int32_t box_rows;              // cache rows of one copy (divides page_size and 64)
+  int32_t q_box;                 // query heads of one copy, 0: queries by plain loads
   int32_t num_pages;
   int32_t causal;
   float scale_log2;              // scale * log2(e)

@@ -2,6 +2,7 @@
 // values, p = softmax(s), o = sum_j p_j row_j[0 .. latent_dim), all heads over
 // the same cached rows.
 #include <algorithm>
+#include <type_traits>
 
 #include <cuda_bf16.h>
 
@@ -20,7 +21,6 @@ namespace {
 
 // ---- the decode kernel -----------------------------------------------------------
 
-constexpr int kThreads = 192;
 constexpr float kRescaleThreshold = 8.0f;
 constexpr uint32_t kSmemLimit = 232448;   // dynamic shared memory of one CTA
 
@@ -28,10 +28,12 @@ constexpr uint32_t kSmemLimit = 232448;   // dynamic shared memory of one CTA
 template <int DL, int N>
 struct Geo {
   static constexpr int NC = DL / 64 + 1;                // 64-column chunks of a cached row
+  static constexpr int SG = N >= 32 ? 2 : 1;            // softmax groups of four warps
+  static constexpr int NG = N / SG;                     // query rows of one
+  static constexpr int kThreads = 64 + 128 * SG;
   static constexpr uint32_t kGroup = NC * 1024;         // 8 keys: NC atoms of 8 x 128 bytes
   static constexpr uint32_t kTile = 8 * kGroup;         // 64 keys
-  static constexpr uint32_t kQChunk = N * 128;          // 64 columns of the queries
-  static constexpr uint32_t kQ = NC * kQChunk;
+  static constexpr uint32_t kQ = N / 8 * kGroup;        // the queries, laid out like keys
   static constexpr uint32_t kP = N * 128;               // N rows of 64 weights
   static constexpr uint32_t kMisc = 256 + (8 + 3) * N * 4;
   static constexpr int NP = kSmemLimit - kMisc - kQ - kP >= 2 * kTile + kP ? 2 : 1;
@@ -52,12 +54,15 @@ struct Geo {
 // P V barriers T & 1.  No wait is more than one phase ahead of its barrier: S(T)
 // is issued after P V(T - 2), so whoever saw S(T) knows P V(T - 2) complete.
 enum {
-  L_KFULL = 0, L_KEMPTY = 4, L_SFULL = 8, L_PFULL = 10, L_PV = 12, L_QFULL = 14, L_OFREE = 15,
-  L_MMADONE = 16, L_COUNT = 17
+  L_KFULL = 0, L_KEMPTY = 4, L_SFULL = 8, L_PFULL = 10, L_PV = 12, L_QFULL = 14, L_QFREE = 15,
+  L_OFREE = 16, L_MMADONE = 17, L_COUNT = 18
 };
-static_assert(L_COUNT * 8 + 4 + 16 <= 256, "barriers, TMEM address, failure flags");
+static_assert(L_COUNT * 8 + 4 + 24 <= 256, "barriers, TMEM address, failure flags");
 
-__device__ __forceinline__ void bar_sync_softmax() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// Barrier of the four warps of softmax group g.
+__device__ __forceinline__ void bar_sync_group(int g) {
+  asm volatile("bar.sync %0, 128;" ::"r"(g + 1) : "memory");
+}
 
 // Max or sum over the eight lanes that share lane % 4, of C values each.  The
 // lanes trade halves, so that each ends with C / 8 (at least one) totals: value
@@ -84,7 +89,7 @@ __device__ __forceinline__ void reduce_rows(float* x, int lane, Op op) {
 template <int C>
 __device__ __forceinline__ int first_value(int lane) {
   const int b4 = (lane >> 4) & 1, b3 = (lane >> 3) & 1, b2 = (lane >> 2) & 1;
-  return C == 16 ? 8 * b4 + 4 * b3 + 2 * b2 : C == 8 ? 4 * b4 + 2 * b3 + b2 : 2 * b4 + b3;
+  return C == 8 ? 4 * b4 + 2 * b3 + b2 : 2 * b4 + b3;
 }
 
 // What a CTA needs to know of its piece.
@@ -105,25 +110,81 @@ struct Piece {
   }
 };
 
+// Four values of each of 16 columns: r[i] of lane d holds column i of dimension
+// d; afterwards v[k] holds column 4k + lane % 4 of dimensions 4 (lane / 4) on.
+__device__ __forceinline__ void transpose_quads(const float* r, float4* v, int lane) {
+  const bool odd = lane & 1, high = lane & 2;
+  float2 u[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float got = __shfl_xor_sync(0xffffffffu, odd ? r[2 * i] : r[2 * i + 1], 1);
+    u[i] = odd ? make_float2(got, r[2 * i + 1]) : make_float2(r[2 * i], got);
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 keep = high ? u[2 * k + 1] : u[2 * k], send = high ? u[2 * k] : u[2 * k + 1];
+    const float2 got = make_float2(__shfl_xor_sync(0xffffffffu, send.x, 2),
+                                   __shfl_xor_sync(0xffffffffu, send.y, 2));
+    v[k] = high ? make_float4(got.x, got.y, keep.x, keep.y) : make_float4(keep.x, keep.y, got.x, got.y);
+  }
+}
+
+// 16 consecutive columns of TMEM (one dimension per lane) times their factors,
+// as rows of the output: row n0 + i of `out`, `base` being row 0's first
+// dimension of this warp.
+template <typename T, int DL>
+__device__ __forceinline__ void store_columns(uint32_t taddr, const float* factor, int live, T* base,
+                                              int lane) {
+  uint32_t r[16];
+  tmem_ld16(taddr, r);
+  float f[16];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float4 x = reinterpret_cast<const float4*>(factor)[i];
+    f[4 * i] = x.x;
+    f[4 * i + 1] = x.y;
+    f[4 * i + 2] = x.z;
+    f[4 * i + 3] = x.w;
+  }
+  tmem_wait_ld();
+  reg_fence<16>(r);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) f[i] *= __uint_as_float(r[i]);
+  float4 v[4];
+  transpose_quads(f, v, lane);
+  T* dst = base + (lane & 3) * DL + (lane >> 2) * 4;
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (4 * k + (lane & 3) < live) {
+      if constexpr (sizeof(T) == 4) {
+        *reinterpret_cast<float4*>(dst + 4 * k * DL) = v[k];
+      } else {
+        constexpr bool F = std::is_same<T, __half>::value;
+        *reinterpret_cast<uint2*>(dst + 4 * k * DL) = make_uint2(pack2<F>(v[k].x, v[k].y), pack2<F>(v[k].z, v[k].w));
+      }
+    }
+}
+
 template <int DL, int N, bool F16>
-__global__ void __launch_bounds__(kThreads, 1)
-latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant__ CUtensorMap tmk) {
+__global__ void __launch_bounds__(Geo<DL, N>::kThreads, 1)
+latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant__ CUtensorMap tmk,
+                     const __grid_constant__ CUtensorMap tmq) {
   using G = Geo<DL, N>;
-  constexpr int NC = G::NC, NS = G::NS, NP = G::NP, C = N / 4;
+  constexpr int NC = G::NC, NS = G::NS, NP = G::NP, SG = G::SG, NG = G::NG, C = NG / 4;
   constexpr uint32_t kIdescQK = idesc_bf16_f32(64, N, 0, 0, F16);
   constexpr uint32_t kIdescPV = idesc_bf16_f32(128, N, 1, 0, F16);
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
   uint8_t* misc = smem + G::kOffMisc;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + L_COUNT * 8);
-  volatile int* s_fail = reinterpret_cast<volatile int*>(tmem_slot + 1);   // [3]
-  float* s_max = reinterpret_cast<float*>(misc + 256);   // [2][4 warps][N]
+  float* s_max = reinterpret_cast<float*>(misc + 256);   // [SG][2][4 warps][NG]
   float* s_col = s_max + 8 * N;                          // [N] rescale factors, then 1 / l
   float* s_ref = s_col + N;                              // [N] reference maxima
   int* s_seen = reinterpret_cast<int*>(s_ref + N);       // [N] keys each row sees
   auto bar = [&](int i) -> uint32_t { return sbase + G::kOffMisc + 8u * (uint32_t)i; };
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = tid >> 5;   // 0: copies, 1: tensor core, then the softmax groups
   const int seg = blockIdx.x / a.row_blocks, rb = blockIdx.x % a.row_blocks;
   const int item0 = __ldg(a.segments + seg), item1 = __ldg(a.segments + seg + 1);
 
@@ -134,16 +195,17 @@ latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar(L_SFULL + s), 1);
-      mbar_init(bar(L_PFULL + s), 128);
+      mbar_init(bar(L_PFULL + s), 128 * SG);
       mbar_init(bar(L_PV + s), 1);
     }
-    mbar_init(bar(L_QFULL), 128);
-    mbar_init(bar(L_OFREE), 128);
+    mbar_init(bar(L_QFULL), a.q_box > 0 ? 1 : 128 * SG);
+    mbar_init(bar(L_QFREE), 1);
+    mbar_init(bar(L_OFREE), 128 * SG);
     mbar_init(bar(L_MMADONE), 1);
-    for (int i = 0; i < 3; ++i) s_fail[i] = 0;
+    for (int i = 0; i < 6; ++i) tmem_slot[1 + i] = 0;   // failure flags
     fence_barrier_init();
   }
-  if (warp == 5) {
+  if (warp == 1) {
     tmem_alloc(smem_u32(tmem_slot), G::kTmemCols);
     tmem_relinquish();
   }
@@ -151,17 +213,35 @@ latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  // the merge's CTAs may start taking free SMs; they wait for this grid's end
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  if (warp == 4) {
-    // ---------------- TMA producer: lane i copies box i of a tile ----------------
-    if (lane == 0) tma_prefetch_desc(&tmk);
+  if (warp == 0) {
+    // ---------------- TMA producer: lane i copies box i ----------------
+    if (lane == 0) {
+      tma_prefetch_desc(&tmk);
+      tma_prefetch_desc(&tmq);
+    }
     const int boxes = kLatentTile / a.box_rows;
     const uint32_t dst0 = sbase + G::kOffK + (uint32_t)lane * (uint32_t)(a.box_rows / 8) * G::kGroup;
-    int T = 0;
+    int T = 0, I = 0;
     bool ok = true;
     for (int item = item0; ok && item < item1; ++item) {
       const Piece pc(a, item, rb, N);
+      if (pc.n == 0) continue;
       const int32_t* table = a.block_tables + (int64_t)pc.request * a.bt_row_stride;
+      if (a.q_box > 0) {   // whole groups of 8 heads: the queries come by TMA too
+        if (I > 0 && !(ok = warp_wait(bar(L_QFREE), (uint32_t)((I - 1) & 1), a.status))) break;
+        if (lane == 0) mbar_arrive_expect_tx(bar(L_QFULL), G::kQ);
+        __syncwarp();
+        if (lane < N / a.q_box) {   // rows past the request's last are copied, and never stored
+          const int r = pc.row0 + lane * a.q_box;
+          tma_load_5d(sbase + G::kOffQ + (uint32_t)(lane * a.q_box / 8) * G::kGroup, &tmq, bar(L_QFULL), 0,
+                      0, 0, r % a.num_heads / 8, pc.rq.q_start + r / a.num_heads);
+        }
+        __syncwarp();
+      }
+      ++I;
       for (int j = 0; j < pc.n; ++j, ++T) {
         const int st = T % NS, tok = (pc.tile0 + j) * kLatentTile + lane * a.box_rows;
         // a box past the last token reads as zeros: its page lies outside the pool
@@ -178,10 +258,12 @@ latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant
         __syncwarp();
       }
     }
-    if (!ok)   // give the copies already issued a bounded chance to land
+    if (!ok) {   // give the copies already issued a bounded chance to land
       for (int i = max(0, T - NS); i < T; ++i)
         mbar_wait(bar(L_KFULL + i % NS), (uint32_t)((i / NS) & 1), nullptr);
-  } else if (warp == 5) {
+      if (a.q_box > 0 && I > 0) mbar_wait(bar(L_QFULL), (uint32_t)((I - 1) & 1), nullptr);
+    }
+  } else if (warp == 1) {
     // ---------------- MMA issuer ----------------
     int T = 0, I = 0;   // tiles and non-empty pieces before this one
     bool ok = true;
@@ -217,10 +299,10 @@ latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant
 #pragma unroll
           for (int c = 0; c < NC; ++c)   // 64 keys x N rows += 64 columns of each
             umma_ss_k4(d, smem_desc_sw128(kb + (uint32_t)c * 1024u, 16u, G::kGroup),
-                       smem_desc_sw128(sbase + G::kOffQ + (uint32_t)c * G::kQChunk, 16u, 1024u),
+                       smem_desc_sw128(sbase + G::kOffQ + (uint32_t)c * 1024u, 16u, G::kGroup),
                        kIdescQK, c > 0 ? 1u : 0u);
           umma_commit_elect(bar(L_SFULL + (k & 1)));
-          ++qk;
+          if (++qk == pc.n) umma_commit_elect(bar(L_QFREE));
           t0 = 0;
           continue;
         }
@@ -237,8 +319,8 @@ latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant
                 tmem + (uint32_t)blk * N,
                 smem_desc_sw128(kb + (uint32_t)blk * 2048u, 1024u, G::kGroup),
                 smem_desc_sw128(pb, 16u, 1024u), kIdescPV, pv > 0 ? 1u : 0u);
-          umma_commit_elect(bar(L_PV + (p & 1)));
           umma_commit_elect(bar(L_KEMPTY + p % NS));
+          umma_commit_elect(bar(L_PV + (p & 1)));
           ++pv;
           t0 = 0;
           continue;
@@ -256,16 +338,21 @@ latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant
     umma_commit_elect(bar(L_MMADONE));
     warp_wait(bar(L_MMADONE), 0, a.status);   // nothing of ours still runs on the tensor core
   } else {
-    // ---------------- softmax and output: warps 0-3 ----------------
-    const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
-    const int col0 = 2 * (lane & 3);   // this thread's columns: 8j + col0 + {0, 1}
+    // ---------------- softmax and output: group g takes rows g NG .. ----------------
+    const int g = (warp - 2) >> 2, quad = warp & 3;     // TMEM lanes 32 quad .. + 31
+    const int gt = ((warp - 2) & 3) * 32 + lane;        // thread of the group
+    const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+    const int col0 = 2 * (lane & 3);   // this thread's columns: g NG + 8j + col0 + {0, 1}
+    const int gc = g * NG;
     const float sl2 = a.scale_log2;
+    volatile int* s_fail = reinterpret_cast<volatile int*>(tmem_slot + 1 + 3 * g);
+    float* g_max = s_max + g * 8 * NG;
 
-    // the queries of a piece into shared memory, N rows of NC swizzled chunks
+    // queries by plain loads (heads not a multiple of 8), laid out like keys
     auto load_q = [&](const Piece& pc) {
       constexpr int V = NC * 8;   // 16-byte pieces of a row
 #pragma unroll 4
-      for (int i = tid; i < N * V; i += 128) {
+      for (int i = g * 128 + gt; i < N * V; i += 128 * SG) {
         const int r = i / V, c = i % V;
         uint4 x = make_uint4(0u, 0u, 0u, 0u);
         if (r < pc.rows) {
@@ -274,17 +361,23 @@ latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant
                         static_cast<const uint16_t*>(a.q) + (int64_t)(pc.rq.q_start + tok) * a.q_stride_tok +
                         (int64_t)h * a.q_stride_head) + c);
         }
-        *reinterpret_cast<uint4*>(smem + G::kOffQ + (uint32_t)(c >> 3) * G::kQChunk +
-                                  swz128((uint32_t)r, (uint32_t)(c & 7))) = x;
+        *reinterpret_cast<uint4*>(smem + G::kOffQ + (uint32_t)(r >> 3) * G::kGroup +
+                                  (uint32_t)(c >> 3) * 1024u +
+                                  swz128((uint32_t)(r & 7), (uint32_t)(c & 7))) = x;
       }
       fence_proxy_async_smem();   // generic writes -> the tensor core's operand reads
       mbar_arrive(bar(L_QFULL));
     };
-    // the next piece that has tiles, from `item` on
+    // the next piece that has tiles, from `item` on; the last S of the one before
+    // is complete for this thread's group, and QFREE says so for both
+    int I = 0;
+    bool ok = true;
     auto next_q = [&](int item) {
+      if (a.q_box > 0) return;
       for (; item < item1; ++item) {
         const Piece pc(a, item, rb, N);
         if (pc.n > 0) {
+          if (I > 0 && !warp_wait(bar(L_QFREE), (uint32_t)((I - 1) & 1), a.status)) s_fail[2] = 1;
           load_q(pc);
           return;
         }
@@ -293,7 +386,6 @@ latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant
     next_q(item0);
 
     int T = 0;
-    bool ok = true;
     for (int item = item0; ok && item < item1; ++item) {
       const Piece pc(a, item, rb, N);
       if (pc.rows <= 0) continue;
@@ -302,20 +394,20 @@ latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant
       const int64_t prow = (int64_t)pc.rq.part_base +
                            (int64_t)max(pc.part, 0) * pc.rq.q_len * a.num_heads + pc.row0;
       if (pc.n == 0) {   // no keys here: zero rows, or a piece that weighs nothing
-        for (int i = tid; i < pc.rows; i += 128) {
+        for (int i = g * 128 + gt; i < pc.rows; i += 128 * SG) {
           if (!whole) a.ws_lse[prow + i] = neg_inf();
           else if (a.lse != nullptr) a.lse[orow + i] = neg_inf();
         }
         if (whole)
-          for (int i = tid; i < pc.rows * DL; i += 128) store_out1(a.out, orow * DL + i, 0.f, a.out_dtype);
+          for (int i = g * 128 + gt; i < pc.rows * DL; i += 128 * SG)
+            store_out1(a.out, orow * DL + i, 0.f, a.out_dtype);
         continue;
       }
-      if (tid < N) {
-        const int tok = (pc.row0 + tid) / a.num_heads;
-        s_seen[tid] = a.causal ? min(pc.kv, pc.kv - pc.rq.q_len + tok + 1) : pc.kv;
+      if (gt < NG) {
+        const int tok = (pc.row0 + gc + gt) / a.num_heads;
+        s_seen[gc + gt] = a.causal ? min(pc.kv, pc.kv - pc.rq.q_len + tok + 1) : pc.kv;
       }
-      // the first row of the block sees the fewest keys; s_seen is read behind
-      // the barrier of the first tile
+      // the first row of the block sees the fewest keys
       const int seen_min =
           a.causal ? min(pc.kv, pc.kv - pc.rq.q_len + pc.row0 / a.num_heads + 1) : pc.kv;
       float m[C], l[C];
@@ -324,29 +416,27 @@ latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant
         m[q] = neg_inf();
         l[q] = 0.f;
       }
-      bar_sync_softmax();
+      bar_sync_group(g);
       for (int j = 0; j < pc.n; ++j, ++T) {
         const int key0 = (pc.tile0 + j) * kLatentTile;
-        const bool got = warp_wait(bar(L_SFULL + (T & 1)), (uint32_t)((T >> 1) & 1), a.status);
-        if (!got) s_fail[T & 1] = 1;
+        if (!warp_wait(bar(L_SFULL + (T & 1)), (uint32_t)((T >> 1) & 1), a.status)) s_fail[T & 1] = 1;
         tc_fence_after();
-        uint32_t s[N / 2];
-        const uint32_t s_tm = tmem + lane_off + G::kColS + (uint32_t)(T & 1) * N;
-        if constexpr (N == 16) tmem_ld_frag2(s_tm, s);
-        else if constexpr (N == 32) tmem_ld_frag4(s_tm, s);
-        else tmem_ld_frag8(s_tm, s);
+        uint32_t s[NG / 2];
+        const uint32_t s_tm = tmem + lane_off + G::kColS + (uint32_t)(T & 1) * N + (uint32_t)gc;
+        if constexpr (NG == 16) tmem_ld_frag2(s_tm, s);
+        else tmem_ld_frag4(s_tm, s);
         tmem_wait_ld();
-        reg_fence<N / 2>(s);
-        float x[N / 2];
+        reg_fence<NG / 2>(s);
+        float x[NG / 2];
 #pragma unroll
-        for (int i = 0; i < N / 2; ++i) x[i] = __uint_as_float(s[i]) * sl2;
+        for (int i = 0; i < NG / 2; ++i) x[i] = __uint_as_float(s[i]) * sl2;
         if (key0 + kLatentTile > seen_min) {
-          const int k = key0 + warp * 16 + (lane >> 2);
+          const int k = key0 + quad * 16 + (lane >> 2);
 #pragma unroll
-          for (int jj = 0; jj < N / 8; ++jj)
+          for (int jj = 0; jj < NG / 8; ++jj)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const int seen = s_seen[8 * jj + col0 + e];
+              const int seen = s_seen[gc + 8 * jj + col0 + e];
               if (k >= seen) x[4 * jj + e] = neg_inf();
               if (k + 8 >= seen) x[4 * jj + 2 + e] = neg_inf();
             }
@@ -357,13 +447,9 @@ latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant
         for (int q = 0; q < C; ++q)
           mx[q] = fmaxf(x[4 * (q >> 1) + (q & 1)], x[4 * (q >> 1) + 2 + (q & 1)]);
         reduce_rows<C>(mx, lane, [](float u, float v) { return fmaxf(u, v); });
-        float* wm = s_max + (T & 1) * 4 * N;
-        {
-          float* w = wm + warp * N + (lane & 3) * C + first_value<C>(lane);
-          w[0] = mx[0];
-          if constexpr (C == 16) w[1] = mx[1];
-        }
-        bar_sync_softmax();
+        float* wm = g_max + (T & 1) * 4 * NG;
+        wm[quad * NG + (lane & 3) * C + first_value<C>(lane)] = mx[0];
+        bar_sync_group(g);
         if (s_fail[T & 1]) {
           ok = false;
           break;
@@ -373,7 +459,7 @@ latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant
           float4 u = *reinterpret_cast<const float4*>(wm + (lane & 3) * C + q);
 #pragma unroll
           for (int w = 1; w < 4; ++w) {
-            const float4 v = *reinterpret_cast<const float4*>(wm + w * N + (lane & 3) * C + q);
+            const float4 v = *reinterpret_cast<const float4*>(wm + w * NG + (lane & 3) * C + q);
             u = make_float4(fmaxf(u.x, v.x), fmaxf(u.y, v.y), fmaxf(u.z, v.z), fmaxf(u.w, v.w));
           }
           mx[q] = u.x;
@@ -382,71 +468,72 @@ latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant
           mx[q + 3] = u.w;
         }
         // lazy rescale: the reference moves only when a maximum grew by more than
-        // 2^8; a row without visible keys so far still has O = 0 and takes its
-        // first reference without one.  Every warp holds the same maxima, so all
-        // four decide alike.
-        float al[C];
-        bool rescale = false;
+        // 2^8.  Every warp of the group holds the same maxima, so all decide alike.
+        bool grow = false;
 #pragma unroll
-        for (int q = 0; q < C; ++q) {
-          const bool grow = mx[q] > m[q] + kRescaleThreshold;
-          al[q] = grow && m[q] != neg_inf() ? ex2(m[q] - mx[q]) : 1.f;
-          rescale = rescale || (grow && m[q] != neg_inf());
-          if (grow) m[q] = mx[q];
-        }
-        if (j > 0 && __any_sync(0xffffffffu, rescale)) {
-          if (!warp_wait(bar(L_PV + ((T - 1) & 1)), (uint32_t)(((T - 1) >> 1) & 1), a.status))
-            s_fail[2] = 1;
-          tc_fence_after();
-          if (warp == 0 && lane < 4)
+        for (int q = 0; q < C; ++q) grow = grow || mx[q] > m[q] + kRescaleThreshold;
+        if (__any_sync(0xffffffffu, grow)) {
+          // a row without visible keys so far still has O = 0 and l = 0 and takes
+          // its first reference without a rescale
+          float al[C];
+          bool rescale = false;
 #pragma unroll
-            for (int q = 0; q < C; ++q) s_col[8 * (q >> 1) + col0 + (q & 1)] = al[q];
-          bar_sync_softmax();
-          if (s_fail[2]) {
-            ok = false;
-            break;
+          for (int q = 0; q < C; ++q) {
+            const bool up = mx[q] > m[q] + kRescaleThreshold, had = m[q] != neg_inf();
+            al[q] = up && had ? ex2(m[q] - mx[q]) : 1.f;
+            rescale = rescale || (up && had);
+            if (up) m[q] = mx[q];
           }
+          if (__any_sync(0xffffffffu, rescale)) {
+            if (!warp_wait(bar(L_PV + ((T - 1) & 1)), (uint32_t)(((T - 1) >> 1) & 1), a.status))
+              s_fail[2] = 1;
+            tc_fence_after();
+            if (gt < 4)
 #pragma unroll
-          for (int q = 0; q < C; ++q) l[q] *= al[q];
+              for (int q = 0; q < C; ++q) s_col[gc + 8 * (q >> 1) + col0 + (q & 1)] = al[q];
+            bar_sync_group(g);
+            if (s_fail[2]) {
+              ok = false;
+              break;
+            }
+#pragma unroll
+            for (int q = 0; q < C; ++q) l[q] *= al[q];
 #pragma unroll 1
-          for (int c = 0; c < DL / 128 * N; c += 16) {
-            uint32_t r[16];
-            tmem_ld16(tmem + lane_off + (uint32_t)c, r);
-            tmem_wait_ld();
-            reg_fence<16>(r);
+            for (int c = 0; c < DL / 128 * NG; c += 16) {
+              uint32_t r[16];
+              const uint32_t o_tm = tmem + lane_off + (uint32_t)(c / NG * N + gc + c % NG);
+              tmem_ld16(o_tm, r);
+              tmem_wait_ld();
+              reg_fence<16>(r);
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              r[i] = __float_as_uint(__uint_as_float(r[i]) * s_col[(c + i) % N]);
-            tmem_st16(tmem + lane_off + (uint32_t)c, r);
+              for (int i = 0; i < 16; ++i)
+                r[i] = __float_as_uint(__uint_as_float(r[i]) * s_col[gc + c % NG + i]);
+              tmem_st16(o_tm, r);
+            }
+            tmem_wait_st();
+            bar_sync_group(g);   // s_col is free again
           }
-          tmem_wait_st();
-          bar_sync_softmax();   // s_col is free again
         }
         // p = exp2(x - m), summed in 32 bits, rounded to the inputs' format for P V
-        float neg[C];
 #pragma unroll
-        for (int q = 0; q < C; ++q) neg[q] = m[q] == neg_inf() ? 0.f : -m[q];
-#pragma unroll
-        for (int jj = 0; jj < N / 8; ++jj)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float p0 = ex2(x[4 * jj + e] + neg[2 * jj + e]);
-            const float p1 = ex2(x[4 * jj + 2 + e] + neg[2 * jj + e]);
-            l[2 * jj + e] += p0 + p1;
-            x[4 * jj + e] = p0;
-            x[4 * jj + 2 + e] = p1;
-          }
+        for (int q = 0; q < C; ++q) {
+          const float neg = m[q] == neg_inf() ? 0.f : -m[q];
+          const int i = 4 * (q >> 1) + (q & 1);
+          x[i] = ex2(x[i] + neg);
+          x[i + 2] = ex2(x[i + 2] + neg);
+          l[q] += x[i] + x[i + 2];
+        }
         // with two P buffers, S(T) complete means P V(T - 2) complete: buffer free
         if (NP == 1 && j > 0 &&
             !warp_wait(bar(L_PV + ((T - 1) & 1)), (uint32_t)(((T - 1) >> 1) & 1), a.status))
           s_fail[(T + 1) & 1] = 1;   // seen behind the next tile's barrier, or at the end
         const uint32_t pb = sbase + G::kOffP + (uint32_t)(T % NP) * G::kP;
 #pragma unroll
-        for (int jj = 0; jj < N / 8; jj += 2) {
+        for (int jj = 0; jj < NG / 8; jj += 2) {
           // matrices: rows 8jj.. keys 0-7 and 8-15 of the warp, rows 8(jj + 1).. alike
           const int mt = lane >> 3;
-          const uint32_t row = (uint32_t)(8 * (jj + (mt >> 1)) + (lane & 7));
-          stmatrix_x4_trans(pb + swz128(row, (uint32_t)(2 * warp + (mt & 1))),
+          const uint32_t row = (uint32_t)(gc + 8 * (jj + (mt >> 1)) + (lane & 7));
+          stmatrix_x4_trans(pb + swz128(row, (uint32_t)(2 * quad + (mt & 1))),
                             pack2<F16>(x[4 * jj], x[4 * jj + 1]),
                             pack2<F16>(x[4 * jj + 2], x[4 * jj + 3]),
                             pack2<F16>(x[4 * jj + 4], x[4 * jj + 5]),
@@ -457,52 +544,49 @@ latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant
         mbar_arrive(bar(L_PFULL + (T & 1)));
       }
       if (!ok) break;
-      next_q(item + 1);   // the last S is complete: the query buffer is free
+      ++I;
+      next_q(item + 1);
 
-      // ---- output: O^T / l, one latent dimension per thread and row block ----
+      // ---- output: O^T / l, one latent dimension per lane of a 128-wide block ----
       reduce_rows<C>(l, lane, [](float u, float v) { return u + v; });
-      float* s_sum = s_max + (T & 1) * 4 * N;   // the half the last tile did not use
-      {
-        const int q = (lane & 3) * C + first_value<C>(lane);
-        s_sum[warp * N + q] = l[0];
-        if constexpr (C == 16) s_sum[warp * N + q + 1] = l[1];
-      }
-      if (warp == 0 && lane < 4)
+      float* s_sum = g_max + (T & 1) * 4 * NG;   // the half the last tile did not use
+      s_sum[quad * NG + (lane & 3) * C + first_value<C>(lane)] = l[0];
+      if (gt < 4)
 #pragma unroll
-        for (int q = 0; q < C; ++q) s_ref[8 * (q >> 1) + col0 + (q & 1)] = m[q];
+        for (int q = 0; q < C; ++q) s_ref[gc + 8 * (q >> 1) + col0 + (q & 1)] = m[q];
       if (!warp_wait(bar(L_PV + ((T - 1) & 1)), (uint32_t)(((T - 1) >> 1) & 1), a.status)) s_fail[2] = 1;
-      bar_sync_softmax();
+      bar_sync_group(g);
       if (s_fail[2]) {
         ok = false;
         break;
       }
-      if (tid < N) {
-        const int q = ((tid & 7) >> 1) * C + 2 * (tid >> 3) + (tid & 1);   // column tid in s_sum
-        const float sum = (s_sum[q] + s_sum[N + q]) + (s_sum[2 * N + q] + s_sum[3 * N + q]);
-        s_col[tid] = sum > 0.f ? (whole ? a.output_scale : 1.f) / sum : 0.f;
-        if (tid < pc.rows) {
-          const float lse = sum > 0.f ? s_ref[tid] + log2f(sum) : neg_inf();
-          if (!whole) a.ws_lse[prow + tid] = lse;
-          else if (a.lse != nullptr) a.lse[orow + tid] = lse;
+      if (gt < NG) {
+        const int q = ((gt & 7) >> 1) * C + 2 * (gt >> 3) + (gt & 1);   // column gt in s_sum
+        const float sum = (s_sum[q] + s_sum[NG + q]) + (s_sum[2 * NG + q] + s_sum[3 * NG + q]);
+        const int n = gc + gt;
+        s_col[n] = sum > 0.f ? (whole ? a.output_scale : 1.f) / sum : 0.f;
+        if (n < pc.rows) {
+          const float lse = sum > 0.f ? s_ref[n] + log2f(sum) : neg_inf();
+          if (!whole) a.ws_lse[prow + n] = lse;
+          else if (a.lse != nullptr) a.lse[orow + n] = lse;
         }
       }
-      bar_sync_softmax();
+      bar_sync_group(g);
       tc_fence_after();
+      auto write = [&](auto* out, int64_t row) {
+        out += (row + gc) * DL + quad * 32;
 #pragma unroll 1
-      for (int c = 0; c < DL / 128 * N; c += 16) {
-        uint32_t r[16];
-        tmem_ld16(tmem + lane_off + (uint32_t)c, r);
-        tmem_wait_ld();
-        reg_fence<16>(r);
-        const int n0 = c % N, d = c / N * 128 + warp * 32 + lane;
+        for (int blk = 0; blk < DL / 128; ++blk)
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (n0 + i < pc.rows) {
-            const float v = __uint_as_float(r[i]) * s_col[n0 + i];
-            if (whole) store_out1(a.out, (orow + n0 + i) * DL + d, v, a.out_dtype);
-            else a.ws_o[(prow + n0 + i) * DL + d] = v;
-          }
-      }
+          for (int n = 0; n < NG; n += 16)
+            store_columns<typename std::remove_pointer<decltype(out)>::type, DL>(
+                tmem + lane_off + (uint32_t)(blk * N + gc + n), s_col + gc + n, pc.rows - gc - n,
+                out + n * DL + blk * 128, lane);
+      };
+      if (!whole) write(a.ws_o, prow);
+      else if (a.out_dtype == PKA_DTYPE_F32) write(static_cast<float*>(a.out), orow);
+      else if (a.out_dtype == PKA_DTYPE_F16) write(static_cast<__half*>(a.out), orow);
+      else write(static_cast<__nv_bfloat16*>(a.out), orow);
       tc_fence_before();
       mbar_arrive(bar(L_OFREE));
     }
@@ -510,45 +594,65 @@ latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 5) {
+  if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, G::kTmemCols);
   }
 }
 
 // The pieces of a cut request: out = sum_c w_c o_c / sum_c w_c with
-// w_c = 2^(lse_c - max), one CTA per row.  Four thread groups take every
-// fourth piece, so the loads of many pieces are in flight at once.
+// w_c = 2^(lse_c - max), one CTA per row.  The weights are made once, a piece
+// per thread; then four thread groups take every fourth piece, eight rows in
+// flight each.  Launched while the decode still runs, it waits for that grid.
+constexpr int kMaxPieces = 1024;
+
 template <int DL>
 __global__ void __launch_bounds__(DL)
 latent_merge_kernel(const __grid_constant__ LatentArgs a) {
   constexpr int T = DL / 4;   // threads of a group: four values each
   __shared__ float4 s_o[3][T];
-  const int b = a.splits[blockIdx.x / a.max_rows], r = blockIdx.x % a.max_rows;
+  __shared__ float s_w[kMaxPieces];
+  __shared__ float s_red[DL / 32];
+  const int b = __ldg(a.splits + blockIdx.x / a.max_rows), r = blockIdx.x % a.max_rows;
   const LatentReq rq = a.reqs[b];
-  const int rows = rq.q_len * a.num_heads;
+  const int rows = rq.q_len * a.num_heads, tid = threadIdx.x;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (r >= rows) return;
-  const int g = threadIdx.x / T, x = threadIdx.x % T;
+  const int64_t p0 = rq.part_base + r;
+  auto reduce = [&](float v, auto op) -> float {   // over the CTA
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, d));
+    __syncthreads();
+    if ((tid & 31) == 0) s_red[tid >> 5] = v;
+    __syncthreads();
+    v = s_red[0];
+#pragma unroll
+    for (int w = 1; w < DL / 32; ++w) v = op(v, s_red[w]);
+    return v;
+  };
   float m = neg_inf();
-  for (int c = 0; c < rq.n_parts; ++c)
-    m = fmaxf(m, __ldg(a.ws_lse + rq.part_base + (int64_t)c * rows + r));
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int c = tid; c < rq.n_parts; c += DL) {
+    s_w[c] = __ldcg(a.ws_lse + p0 + (int64_t)c * rows);
+    m = fmaxf(m, s_w[c]);
+  }
+  m = reduce(m, [](float u, float v) { return fmaxf(u, v); });
   float sum = 0.f;
-  if (m != neg_inf()) {
-    for (int c = 0; c < rq.n_parts; ++c)
-      sum += ex2(__ldg(a.ws_lse + rq.part_base + (int64_t)c * rows + r) - m);
-#pragma unroll 4
-    for (int c = g; c < rq.n_parts; c += 4) {
-      const int64_t prow = rq.part_base + (int64_t)c * rows + r;
-      const float lse = __ldg(a.ws_lse + prow);
-      if (lse == neg_inf()) continue;   // a piece without keys has no output rows
-      const float w = ex2(lse - m);
-      const float4 v = __ldg(reinterpret_cast<const float4*>(a.ws_o + prow * DL) + x);
-      o.x += w * v.x;
-      o.y += w * v.y;
-      o.z += w * v.z;
-      o.w += w * v.w;
-    }
+  for (int c = tid; c < rq.n_parts; c += DL) {
+    s_w[c] = s_w[c] == neg_inf() ? 0.f : ex2(s_w[c] - m);
+    sum += s_w[c];
+  }
+  sum = reduce(sum, [](float u, float v) { return u + v; });
+  const int g = tid / T, x = tid % T;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int c = g; c < rq.n_parts; c += 4) {
+    const float w = s_w[c];
+    if (w == 0.f) continue;   // a piece without keys has no output rows
+    const float4 v = __ldcg(reinterpret_cast<const float4*>(a.ws_o + (p0 + (int64_t)c * rows) * DL) + x);
+    o.x += w * v.x;
+    o.y += w * v.y;
+    o.z += w * v.z;
+    o.w += w * v.w;
   }
   if (g > 0) s_o[g - 1][x] = o;
   __syncthreads();
@@ -560,32 +664,42 @@ latent_merge_kernel(const __grid_constant__ LatentArgs a) {
     o.z += s_o[k][x].z;
     o.w += s_o[k][x].w;
   }
-  const int64_t row = ((int64_t)rq.q_start + r / a.num_heads) * a.num_heads + r % a.num_heads;
+  const int64_t row = (int64_t)rq.q_start * a.num_heads + r;
   const float v[4] = {o.x, o.y, o.z, o.w};
   store_out<4>(a.out, row * DL + x * 4, v, sum > 0.f ? a.output_scale / sum : 0.f, a.out_dtype);
   if (x == 0 && a.lse != nullptr) a.lse[row] = sum > 0.f ? m + log2f(sum) : neg_inf();
 }
 
 template <int DL, int N, bool F16>
-cudaError_t launch_tiles(const LatentArgs& a, const CUtensorMap& map, cudaStream_t stream) {
+cudaError_t launch_tiles(const LatentArgs& a, const CUtensorMap& map, const CUtensorMap& qmap,
+                         cudaStream_t stream) {
   auto kern = latent_decode_kernel<DL, N, F16>;
   static std::atomic<uint64_t> smem_set{0};   // devices whose limit was raised
   const cudaError_t e = set_smem_once(kern, (int)Geo<DL, N>::kSmem, smem_set);
   if (e != cudaSuccess) return e;
-  kern<<<(unsigned)(a.num_segments * a.row_blocks), kThreads, Geo<DL, N>::kSmem, stream>>>(a, map);
+  kern<<<(unsigned)(a.num_segments * a.row_blocks), Geo<DL, N>::kThreads, Geo<DL, N>::kSmem, stream>>>(
+      a, map, qmap);
   return cudaGetLastError();
 }
 
 template <int DL, bool F16>
 int launch(const pka_latent_plan& plan, const LatentArgs& a, const CUtensorMap& map,
-           cudaStream_t stream) {
-  cudaError_t e = plan.row_tile == 16   ? launch_tiles<DL, 16, F16>(a, map, stream)
-                  : plan.row_tile == 32 ? launch_tiles<DL, 32, F16>(a, map, stream)
-                                        : launch_tiles<DL, 64, F16>(a, map, stream);
+           const CUtensorMap& qmap, cudaStream_t stream) {
+  cudaError_t e = plan.row_tile == 16   ? launch_tiles<DL, 16, F16>(a, map, qmap, stream)
+                  : plan.row_tile == 32 ? launch_tiles<DL, 32, F16>(a, map, qmap, stream)
+                                        : launch_tiles<DL, 64, F16>(a, map, qmap, stream);
   if (e != cudaSuccess) return cuda_fail(e, "latent_decode_kernel launch");
   if (a.num_splits > 0) {
-    latent_merge_kernel<DL><<<(unsigned)(a.num_splits * a.max_rows), DL, 0, stream>>>(a);
-    e = cudaGetLastError();
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(a.num_splits * a.max_rows));
+    cfg.blockDim = dim3(DL);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, latent_merge_kernel<DL>, a);
     if (e != cudaSuccess) return cuda_fail(e, "latent_merge_kernel launch");
   }
   return PKA_OK;
@@ -593,9 +707,10 @@ int launch(const pka_latent_plan& plan, const LatentArgs& a, const CUtensorMap& 
 
 }  // namespace
 
-int launch_latent_decode(const pka_latent_plan& plan, const LatentArgs& a, const void* pages,
+int launch_latent_decode(const pka_latent_plan& plan, const LatentArgs& args, const void* pages,
                          int64_t stride_page, cudaStream_t stream) {
-  if (a.num_items == 0) return PKA_OK;
+  if (args.num_items == 0) return PKA_OK;
+  LatentArgs a = args;
   // The pool as (64 columns, slot in 8, column chunk, slot / 8, page): one box of
   // box_rows slots lands as groups of 8 keys, each NC swizzled 8 x 128 byte atoms.
   // Groups are evenly spaced whatever the page size, so a tile of 64 keys from
@@ -605,13 +720,27 @@ int launch_latent_decode(const pka_latent_plan& plan, const LatentArgs& a, const
   const uint64_t dims[5] = {64, 8, nc, (uint64_t)plan.desc.page_size / 8, (uint64_t)plan.desc.num_pages};
   const uint64_t strides[4] = {row, 128, 8 * row, (uint64_t)stride_page * 2};
   const uint32_t box[5] = {64, 8, nc, (uint32_t)a.box_rows / 8, 1};
-  CUtensorMap map;
-  const int rc = encode_bf16_map(&map, pages, 5, dims, strides, box);
+  CUtensorMap map, qmap;
+  int rc = encode_bf16_map(&map, pages, 5, dims, strides, box);
   if (rc != PKA_OK) return rc;
+  // The queries alike, where heads come in groups of 8: (64 columns, head in 8,
+  // chunk, head / 8, token), boxes of q_box heads that stay inside a token.
+  qmap = map;
+  a.q_box = 0;
+  if (a.num_heads % 8 == 0 && a.q_stride_head > 0 && (a.q_stride_tok > 0 || plan.total_q == 1)) {
+    a.q_box = plan.row_tile;
+    while (a.num_heads % a.q_box != 0) a.q_box /= 2;
+    const uint64_t hs = (uint64_t)a.q_stride_head * 2;
+    const uint64_t qd[5] = {64, 8, nc, (uint64_t)a.num_heads / 8, (uint64_t)plan.total_q};
+    const uint64_t qs[4] = {hs, 128, 8 * hs, std::max((uint64_t)a.q_stride_tok * 2, (uint64_t)16)};
+    const uint32_t qb[5] = {64, 8, nc, (uint32_t)a.q_box / 8, 1};
+    rc = encode_bf16_map(&qmap, a.q, 5, qd, qs, qb);
+    if (rc != PKA_OK) return rc;
+  }
   const bool f16 = plan.desc.dtype == PKA_DTYPE_F16;
   if (plan.desc.latent_dim == 512)
-    return f16 ? launch<512, true>(plan, a, map, stream) : launch<512, false>(plan, a, map, stream);
-  return f16 ? launch<256, true>(plan, a, map, stream) : launch<256, false>(plan, a, map, stream);
+    return f16 ? launch<512, true>(plan, a, map, qmap, stream) : launch<512, false>(plan, a, map, qmap, stream);
+  return f16 ? launch<256, true>(plan, a, map, qmap, stream) : launch<256, false>(plan, a, map, qmap, stream);
 }
 
 }  // namespace pka
