@@ -71,7 +71,7 @@ struct LatentArgs {
 struct pka_latent_plan {
   pka_latent_desc desc;       // normalised copy
   int32_t total_q = 0, max_rows = 0, row_tile = 0, row_blocks = 0;
-  int32_t partial_rows = 0;
+  int32_t partial_rows = 0, max_parts = 0;
   int64_t workspace_bytes = 0;
   int64_t ws_lse_offset = 0;
   std::vector<pka::LatentItem> items;

@@ -24,40 +24,54 @@ namespace {
 constexpr float kRescaleThreshold = 8.0f;
 constexpr uint32_t kSmemLimit = 232448;   // dynamic shared memory of one CTA
 
-// Shared memory and TMEM of latent_dim DL with N query rows.
+// Shared memory and TMEM of latent_dim DL with N query rows.  A stage is a tile
+// of 64 keys: groups of 8 keys, each NC swizzled atoms of 8 x 128 bytes.  Its
+// rotary atoms are dead once S is complete, and the weights of the tile (N / 8
+// atoms of 8 rows x 64 keys, the same spacing) are written over them.
 template <int DL, int N>
 struct Geo {
-  static constexpr int NC = DL / 64 + 1;                // 64-column chunks of a cached row
+  static constexpr int NB = DL / 128;                   // 128-wide latent blocks of a row
+  static constexpr int NC = DL / 64 + 1;                // 64-column chunks of a row
   static constexpr int SG = N >= 32 ? 2 : 1;            // softmax groups of four warps
   static constexpr int NG = N / SG;                     // query rows of one
-  static constexpr int kThreads = 64 + 128 * SG;
-  static constexpr uint32_t kGroup = NC * 1024;         // 8 keys: NC atoms of 8 x 128 bytes
-  static constexpr uint32_t kTile = 8 * kGroup;         // 64 keys
+  static constexpr int kThreads = 96 + 128 * SG;
+  static constexpr uint32_t kGroup = NC * 1024;
+  static constexpr uint32_t kTile = 8 * kGroup;
   static constexpr uint32_t kQ = N / 8 * kGroup;        // the queries, laid out like keys
-  static constexpr uint32_t kP = N * 128;               // N rows of 64 weights
-  static constexpr uint32_t kMisc = 256 + (8 + 3) * N * 4;
-  static constexpr int NP = kSmemLimit - kMisc - kQ - kP >= 2 * kTile + kP ? 2 : 1;
-  static constexpr int kRoom = (kSmemLimit - kMisc - kQ - NP * kP) / kTile;
-  static constexpr int NS = kRoom < 4 ? kRoom : 4;      // stages of 64 keys
-  static constexpr uint32_t kOffK = 0;
-  static constexpr uint32_t kOffQ = kOffK + NS * kTile;
-  static constexpr uint32_t kOffP = kOffQ + kQ;
-  static constexpr uint32_t kOffMisc = kOffP + NP * kP;
+  static constexpr uint32_t kMisc = 512 + (8 + 2) * N * 4;
+  static constexpr int kFit = (kSmemLimit - kMisc - kQ) / kTile;
+  static constexpr int NS = kFit < 4 ? kFit : 4;        // stages
+  static constexpr uint32_t kOffQ = NS * kTile;
+  static constexpr uint32_t kOffMisc = kOffQ + kQ;
   static constexpr uint32_t kSmem = kOffMisc + kMisc;
-  static constexpr uint32_t kColS = (DL / 128) * N;     // O blocks, then the two S buffers
+  static constexpr uint32_t kOffP = (NC - 1) * 1024;    // inside a stage
+  static constexpr uint32_t kColS = NB * N;             // O blocks, then the two S buffers
   static constexpr uint32_t kCols = kColS + 2 * N;
   static constexpr uint32_t kTmemCols = kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
-  static_assert(NS >= 2 && kSmem <= kSmemLimit, "two stages of keys");
+  static_assert(NS >= 2 && kSmem <= kSmemLimit, "two stages");
 };
 
-// mbarriers.  T counts a CTA's tiles over all its pieces: stage T % NS, S and
-// P V barriers T & 1.  No wait is more than one phase ahead of its barrier: S(T)
-// is issued after P V(T - 2), so whoever saw S(T) knows P V(T - 2) complete.
+// mbarriers.  T counts a CTA's tiles over all its pieces: S, P and P V barriers
+// T & 1.  No barrier runs a phase past one that somebody still has to see: S(T)
+// is issued once P(T - 2) is written, P(T) written once P V(T - 2) is complete.
 enum {
   L_KFULL = 0, L_KEMPTY = 4, L_SFULL = 8, L_PFULL = 10, L_PV = 12, L_QFULL = 14, L_QFREE = 15,
-  L_OFREE = 16, L_MMADONE = 17, L_COUNT = 18
+  L_OFREE = 16, L_SDONE = 17, L_ODONE = 18, L_COUNT = 19
 };
-static_assert(L_COUNT * 8 + 4 + 24 <= 256, "barriers, TMEM address, failure flags");
+static_assert(L_COUNT * 8 + 4 + 24 <= 512, "barriers, TMEM address, failure flags");
+
+// A position in a ring of N slots and the parity of its round.
+template <int N>
+struct Ring {
+  int slot = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == N) {
+      slot = 0;
+      parity ^= 1u;
+    }
+  }
+};
 
 // Barrier of the four warps of softmax group g.
 __device__ __forceinline__ void bar_sync_group(int g) {
@@ -91,6 +105,10 @@ __device__ __forceinline__ int first_value(int lane) {
   const int b4 = (lane >> 4) & 1, b3 = (lane >> 3) & 1, b2 = (lane >> 2) & 1;
   return C == 8 ? 4 * b4 + 2 * b3 + b2 : 2 * b4 + b3;
 }
+
+struct LatentMaps {
+  CUtensorMap pool, q;
+};
 
 // What a CTA needs to know of its piece.
 struct Piece {
@@ -129,62 +147,64 @@ __device__ __forceinline__ void transpose_quads(const float* r, float4* v, int l
   }
 }
 
-// 16 consecutive columns of TMEM (one dimension per lane) times their factors,
-// as rows of the output: row n0 + i of `out`, `base` being row 0's first
-// dimension of this warp.
-template <typename T, int DL>
+// NG consecutive columns of TMEM (one dimension per lane) times their factors,
+// as rows of the output: column i to row i, `base` being row 0's first dimension
+// of this warp.
+template <typename T, int DL, int NG>
 __device__ __forceinline__ void store_columns(uint32_t taddr, const float* factor, int live, T* base,
                                               int lane) {
-  uint32_t r[16];
-  tmem_ld16(taddr, r);
-  float f[16];
+  uint32_t r[NG];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float4 x = reinterpret_cast<const float4*>(factor)[i];
-    f[4 * i] = x.x;
-    f[4 * i + 1] = x.y;
-    f[4 * i + 2] = x.z;
-    f[4 * i + 3] = x.w;
-  }
+  for (int n = 0; n < NG; n += 16) tmem_ld16(taddr + (uint32_t)n, r + n);
   tmem_wait_ld();
-  reg_fence<16>(r);
-#pragma unroll
-  for (int i = 0; i < 16; ++i) f[i] *= __uint_as_float(r[i]);
-  float4 v[4];
-  transpose_quads(f, v, lane);
+  reg_fence<NG>(r);
   T* dst = base + (lane & 3) * DL + (lane >> 2) * 4;
 #pragma unroll
-  for (int k = 0; k < 4; ++k)
-    if (4 * k + (lane & 3) < live) {
-      if constexpr (sizeof(T) == 4) {
-        *reinterpret_cast<float4*>(dst + 4 * k * DL) = v[k];
-      } else {
-        constexpr bool F = std::is_same<T, __half>::value;
-        *reinterpret_cast<uint2*>(dst + 4 * k * DL) = make_uint2(pack2<F>(v[k].x, v[k].y), pack2<F>(v[k].z, v[k].w));
-      }
+  for (int n = 0; n < NG; n += 16) {
+    float f[16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 x = reinterpret_cast<const float4*>(factor + n)[i];
+      f[4 * i] = x.x * __uint_as_float(r[n + 4 * i]);
+      f[4 * i + 1] = x.y * __uint_as_float(r[n + 4 * i + 1]);
+      f[4 * i + 2] = x.z * __uint_as_float(r[n + 4 * i + 2]);
+      f[4 * i + 3] = x.w * __uint_as_float(r[n + 4 * i + 3]);
     }
+    float4 v[4];
+    transpose_quads(f, v, lane);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (n + 4 * k + (lane & 3) < live) {
+        T* to = dst + (n + 4 * k) * DL;
+        if constexpr (sizeof(T) == 4) {
+          *reinterpret_cast<float4*>(to) = v[k];
+        } else {
+          constexpr bool F = std::is_same<T, __half>::value;
+          *reinterpret_cast<uint2*>(to) = make_uint2(pack2<F>(v[k].x, v[k].y), pack2<F>(v[k].z, v[k].w));
+        }
+      }
+  }
 }
 
 template <int DL, int N, bool F16>
 __global__ void __launch_bounds__(Geo<DL, N>::kThreads, 1)
-latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant__ CUtensorMap tmk,
-                     const __grid_constant__ CUtensorMap tmq) {
+latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant__ LatentMaps maps) {
   using G = Geo<DL, N>;
-  constexpr int NC = G::NC, NS = G::NS, NP = G::NP, SG = G::SG, NG = G::NG, C = NG / 4;
+  constexpr int NB = G::NB, NC = G::NC, NS = G::NS, SG = G::SG, NG = G::NG, C = NG / 4;
   constexpr uint32_t kIdescQK = idesc_bf16_f32(64, N, 0, 0, F16);
   constexpr uint32_t kIdescPV = idesc_bf16_f32(128, N, 1, 0, F16);
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
   uint8_t* misc = smem + G::kOffMisc;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + L_COUNT * 8);
-  float* s_max = reinterpret_cast<float*>(misc + 256);   // [SG][2][4 warps][NG]
+  float* s_max = reinterpret_cast<float*>(misc + 512);   // [SG][2][4 warps][NG]
   float* s_col = s_max + 8 * N;                          // [N] rescale factors, then 1 / l
-  float* s_ref = s_col + N;                              // [N] reference maxima
-  int* s_seen = reinterpret_cast<int*>(s_ref + N);       // [N] keys each row sees
+  int* s_seen = reinterpret_cast<int*>(s_col + N);       // [N] keys each row sees
+  float* s_ref = s_col + N;                              // then the rows' reference maxima
   auto bar = [&](int i) -> uint32_t { return sbase + G::kOffMisc + 8u * (uint32_t)i; };
 
   const int tid = threadIdx.x, lane = tid & 31;
-  const int warp = tid >> 5;   // 0: copies, 1: tensor core, then the softmax groups
+  const int warp = tid >> 5;   // 0: copies, 1: S, 2: P V, then the softmax groups
   const int seg = blockIdx.x / a.row_blocks, rb = blockIdx.x % a.row_blocks;
   const int item0 = __ldg(a.segments + seg), item1 = __ldg(a.segments + seg + 1);
 
@@ -201,7 +221,8 @@ latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant
     mbar_init(bar(L_QFULL), a.q_box > 0 ? 1 : 128 * SG);
     mbar_init(bar(L_QFREE), 1);
     mbar_init(bar(L_OFREE), 128 * SG);
-    mbar_init(bar(L_MMADONE), 1);
+    mbar_init(bar(L_SDONE), 1);
+    mbar_init(bar(L_ODONE), 1);
     for (int i = 0; i < 6; ++i) tmem_slot[1 + i] = 0;   // failure flags
     fence_barrier_init();
   }
@@ -217,130 +238,131 @@ latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   if (warp == 0) {
-    // ---------------- TMA producer: lane i copies box i ----------------
-    if (lane == 0) {
-      tma_prefetch_desc(&tmk);
-      tma_prefetch_desc(&tmq);
-    }
-    const int boxes = kLatentTile / a.box_rows;
-    const uint32_t dst0 = sbase + G::kOffK + (uint32_t)lane * (uint32_t)(a.box_rows / 8) * G::kGroup;
-    int T = 0, I = 0;
+    // ---------------- TMA producer: lane i copies box i of a tile ----------------
+    if (lane < 2) tma_prefetch_desc(lane == 0 ? &maps.pool : &maps.q);
+    const int boxes = kLatentTile / a.box_rows, groups = a.box_rows / 8;
+    Ring<NS> kp;
+    int nk = 0, I = 0;   // stages filled so far, pieces
     bool ok = true;
     for (int item = item0; ok && item < item1; ++item) {
       const Piece pc(a, item, rb, N);
       if (pc.n == 0) continue;
       const int32_t* table = a.block_tables + (int64_t)pc.request * a.bt_row_stride;
+      // a box past the last token reads as zeros: its page lies outside the pool
+      auto page_of = [&](int tok) {
+        return lane < boxes && tok < pc.kv ? __ldg(table + tok / a.page_size) : a.num_pages;
+      };
+      const int tok0 = pc.tile0 * kLatentTile + lane * a.box_rows;
       if (a.q_box > 0) {   // whole groups of 8 heads: the queries come by TMA too
         if (I > 0 && !(ok = warp_wait(bar(L_QFREE), (uint32_t)((I - 1) & 1), a.status))) break;
         if (lane == 0) mbar_arrive_expect_tx(bar(L_QFULL), G::kQ);
         __syncwarp();
         if (lane < N / a.q_box) {   // rows past the request's last are copied, and never stored
           const int r = pc.row0 + lane * a.q_box;
-          tma_load_5d(sbase + G::kOffQ + (uint32_t)(lane * a.q_box / 8) * G::kGroup, &tmq, bar(L_QFULL), 0,
+          tma_load_5d(sbase + G::kOffQ + (uint32_t)(lane * a.q_box / 8) * G::kGroup, &maps.q, bar(L_QFULL), 0,
                       0, 0, r % a.num_heads / 8, pc.rq.q_start + r / a.num_heads);
         }
         __syncwarp();
       }
       ++I;
-      for (int j = 0; j < pc.n; ++j, ++T) {
-        const int st = T % NS, tok = (pc.tile0 + j) * kLatentTile + lane * a.box_rows;
-        // a box past the last token reads as zeros: its page lies outside the pool
-        const int page = lane < boxes && tok < pc.kv ? __ldg(table + tok / a.page_size) : a.num_pages;
-        if (T >= NS && !warp_wait(bar(L_KEMPTY + st), (uint32_t)((T / NS - 1) & 1), a.status)) {
-          ok = false;
-          break;
-        }
-        if (lane == 0) mbar_arrive_expect_tx(bar(L_KFULL + st), G::kTile);
+      int next = page_of(tok0);
+      for (int j = 0; j < pc.n; ++j) {
+        const int tok = tok0 + j * kLatentTile, page = next;
+        next = page_of(tok + kLatentTile);
+        if (nk >= NS && !(ok = warp_wait(bar(L_KEMPTY + kp.slot), kp.parity ^ 1u, a.status))) break;
+        if (lane == 0) mbar_arrive_expect_tx(bar(L_KFULL + kp.slot), G::kTile);
         __syncwarp();
         if (lane < boxes)
-          tma_load_5d(dst0 + (uint32_t)st * G::kTile, &tmk, bar(L_KFULL + st), 0, 0, 0,
-                      (tok % a.page_size) / 8, page);
+          tma_load_5d(sbase + (uint32_t)kp.slot * G::kTile + (uint32_t)(lane * groups) * G::kGroup, &maps.pool,
+                      bar(L_KFULL + kp.slot), 0, 0, 0, tok % a.page_size / 8, page);
         __syncwarp();
+        kp.next();
+        ++nk;
       }
     }
     if (!ok) {   // give the copies already issued a bounded chance to land
-      for (int i = max(0, T - NS); i < T; ++i)
+      for (int i = max(0, nk - NS); i < nk; ++i)
         mbar_wait(bar(L_KFULL + i % NS), (uint32_t)((i / NS) & 1), nullptr);
       if (a.q_box > 0 && I > 0) mbar_wait(bar(L_QFULL), (uint32_t)((I - 1) & 1), nullptr);
     }
   } else if (warp == 1) {
-    // ---------------- MMA issuer ----------------
+    // ---------------- issues S^T = K Q^T ----------------
+    // Its own warp, so that neither products of keys that are still on their way
+    // hold up a ready P V nor the other way round.
+    const uint64_t dk = smem_desc_sw128(sbase, 16u, G::kGroup);
+    const uint64_t dq = smem_desc_sw128(sbase + G::kOffQ, 16u, G::kGroup);
+    Ring<NS> kp;
     int T = 0, I = 0;   // tiles and non-empty pieces before this one
     bool ok = true;
     for (int item = item0; ok && item < item1; ++item) {
       const Piece pc(a, item, rb, N);
       if (pc.n == 0) continue;
       ok = warp_wait(bar(L_QFULL), (uint32_t)(I & 1), a.status);
-      int qk = 0, pv = 0;   // tiles whose S / whose P V was issued
-      uint64_t t0 = 0;
-      while (ok && pv < pc.n) {
-        // S runs at most two tiles ahead of P V, and never makes a ready P V wait
-        // for keys that are still on their way (P V is what frees a stage)
-        const int k = T + qk, p = T + pv;
-        if (qk < pc.n && qk <= pv + 1 &&
-            __all_sync(0xffffffffu, mbar_test_wait(bar(L_KFULL + k % NS), (uint32_t)((k / NS) & 1)))) {
-          const uint32_t kb = sbase + G::kOffK + (uint32_t)(k % NS) * G::kTile;
-          const int live = pc.kv - (pc.tile0 + qk) * kLatentTile;
-          if (live < kLatentTile) {
-            // rows past the last token may hold anything, and 0 * inf is not 0:
-            // clear them (copies past the last token brought zeros already)
-            const int end = (live + a.box_rows - 1) / a.box_rows * a.box_rows;
-            for (int r = live; r < end; ++r)
-              for (int c = lane; c < NC * 8; c += 32)
-                *reinterpret_cast<uint4*>(smem + G::kOffK + (uint32_t)(k % NS) * G::kTile +
-                                          (uint32_t)(r >> 3) * G::kGroup + (uint32_t)(c >> 3) * 1024u +
-                                          (uint32_t)(r & 7) * 128u + (uint32_t)(c & 7) * 16u) =
-                    make_uint4(0u, 0u, 0u, 0u);
-            fence_proxy_async_smem();
-            __syncwarp();
+      ++I;
+      for (int j = 0; ok && j < pc.n; ++j, ++T) {
+        // P(T - 2) written means S(T - 2) read: this S buffer is free
+        ok = (T < 2 || warp_wait(bar(L_PFULL + (T & 1)), (uint32_t)(((T >> 1) - 1) & 1), a.status)) &&
+             warp_wait(bar(L_KFULL + kp.slot), kp.parity, a.status);
+        if (!ok) break;
+        const int live = pc.kv - (pc.tile0 + j) * kLatentTile;
+        if (live < kLatentTile) {
+          // rows past the last token may hold anything, and 0 * inf is not 0:
+          // clear them to the end of their box (boxes past it brought zeros)
+          const int end = (live + a.box_rows - 1) / a.box_rows * a.box_rows;
+          for (int i = lane; i < (end - live) * NC * 8; i += 32) {
+            const int r = live + i / (NC * 8), c = i % (NC * 8);
+            *reinterpret_cast<uint4*>(smem + (uint32_t)kp.slot * G::kTile + (uint32_t)(r >> 3) * G::kGroup +
+                                      (uint32_t)(c >> 3) * 1024u + (uint32_t)(r & 7) * 128u +
+                                      (uint32_t)(c & 7) * 16u) = make_uint4(0u, 0u, 0u, 0u);
           }
-          tc_fence_after();
-          const uint32_t d = tmem + G::kColS + (uint32_t)(k & 1) * N;
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        tc_fence_after();
+        const uint32_t d = tmem + G::kColS + (uint32_t)(T & 1) * N;
+        const uint64_t dkt = dk + (uint32_t)kp.slot * (G::kTile / 16);
 #pragma unroll
-          for (int c = 0; c < NC; ++c)   // 64 keys x N rows += 64 columns of each
-            umma_ss_k4(d, smem_desc_sw128(kb + (uint32_t)c * 1024u, 16u, G::kGroup),
-                       smem_desc_sw128(sbase + G::kOffQ + (uint32_t)c * 1024u, 16u, G::kGroup),
-                       kIdescQK, c > 0 ? 1u : 0u);
-          umma_commit_elect(bar(L_SFULL + (k & 1)));
-          if (++qk == pc.n) umma_commit_elect(bar(L_QFREE));
-          t0 = 0;
-          continue;
-        }
-        if (pv < qk &&
-            __all_sync(0xffffffffu, mbar_test_wait(bar(L_PFULL + (p & 1)), (uint32_t)((p >> 1) & 1)))) {
-          if (pv == 0 && I > 0 && !(ok = warp_wait(bar(L_OFREE), (uint32_t)((I - 1) & 1), a.status)))
-            break;
-          tc_fence_after();
-          const uint32_t kb = sbase + G::kOffK + (uint32_t)(p % NS) * G::kTile;
-          const uint32_t pb = sbase + G::kOffP + (uint32_t)(p % NP) * G::kP;
-#pragma unroll
-          for (int blk = 0; blk < DL / 128; ++blk)   // 128 dims x N rows += 64 keys
-            umma_ss_k4_steps<2 * (int)G::kGroup / 16, 2>(
-                tmem + (uint32_t)blk * N,
-                smem_desc_sw128(kb + (uint32_t)blk * 2048u, 1024u, G::kGroup),
-                smem_desc_sw128(pb, 16u, 1024u), kIdescPV, pv > 0 ? 1u : 0u);
-          umma_commit_elect(bar(L_KEMPTY + p % NS));
-          umma_commit_elect(bar(L_PV + (p & 1)));
-          ++pv;
-          t0 = 0;
-          continue;
-        }
-        const uint64_t now = global_timer_ns();
-        if (t0 == 0) t0 = now;
-        if (!__all_sync(0xffffffffu, now - t0 <= kWaitLimitNs)) {
-          if (lane == 0) atomicOr(a.status, STATUS_WAIT_TIMEOUT);
-          ok = false;
-        }
+        for (int c = 0; c < NC; ++c)   // 64 keys x N rows += 64 columns of each
+          umma_ss_k4(d, dkt + c * 64, dq + c * 64, kIdescQK, c > 0 ? 1u : 0u);
+        umma_commit_elect(bar(L_SFULL + (T & 1)));
+        kp.next();
       }
-      T += pc.n;
+      if (ok) umma_commit_elect(bar(L_QFREE));
+    }
+    umma_commit_elect(bar(L_SDONE));
+    warp_wait(bar(L_SDONE), 0, a.status);   // nothing of this warp's still runs on the tensor core
+  } else if (warp == 2) {
+    // ---------------- issues O^T += V^T P^T ----------------
+    const uint64_t dv = smem_desc_sw128(sbase, 1024u, G::kGroup);
+    const uint64_t dp = smem_desc_sw128(sbase + G::kOffP, 16u, G::kGroup);
+    Ring<NS> kp;
+    int T = 0, I = 0;
+    bool ok = true;
+    for (int item = item0; ok && item < item1; ++item) {
+      const Piece pc(a, item, rb, N);
+      if (pc.n == 0) continue;
+      for (int j = 0; j < pc.n; ++j, ++T) {
+        ok = warp_wait(bar(L_PFULL + (T & 1)), (uint32_t)((T >> 1) & 1), a.status);
+        if (ok && j == 0 && I > 0) ok = warp_wait(bar(L_OFREE), (uint32_t)((I - 1) & 1), a.status);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t stage = (uint32_t)kp.slot * (G::kTile / 16);
+#pragma unroll
+        for (int b = 0; b < NB; ++b)   // 128 dims x N rows += 64 keys
+          umma_ss_k4_steps<2 * (int)G::kGroup / 16, 2>(tmem + (uint32_t)b * N, dv + stage + b * 128, dp + stage,
+                                                       kIdescPV, j > 0 ? 1u : 0u);
+        umma_commit_elect(bar(L_KEMPTY + kp.slot));
+        umma_commit_elect(bar(L_PV + (T & 1)));
+        kp.next();
+      }
       ++I;
     }
-    umma_commit_elect(bar(L_MMADONE));
-    warp_wait(bar(L_MMADONE), 0, a.status);   // nothing of ours still runs on the tensor core
+    umma_commit_elect(bar(L_ODONE));
+    warp_wait(bar(L_ODONE), 0, a.status);
   } else {
     // ---------------- softmax and output: group g takes rows g NG .. ----------------
-    const int g = (warp - 2) >> 2, quad = warp & 3;     // TMEM lanes 32 quad .. + 31
-    const int gt = ((warp - 2) & 3) * 32 + lane;        // thread of the group
+    const int g = (warp - 3) >> 2, quad = warp & 3;     // TMEM lanes 32 quad .. + 31
+    const int gt = ((warp - 3) & 3) * 32 + lane;        // thread of the group
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
     const int col0 = 2 * (lane & 3);   // this thread's columns: g NG + 8j + col0 + {0, 1}
     const int gc = g * NG;
@@ -350,7 +372,7 @@ latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant
 
     // queries by plain loads (heads not a multiple of 8), laid out like keys
     auto load_q = [&](const Piece& pc) {
-      constexpr int V = NC * 8;   // 16-byte pieces of a row
+      constexpr int V = (DL + kLatentRopeDim) / 8;   // 16-byte pieces of a row
 #pragma unroll 4
       for (int i = g * 128 + gt; i < N * V; i += 128 * SG) {
         const int r = i / V, c = i % V;
@@ -361,8 +383,7 @@ latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant
                         static_cast<const uint16_t*>(a.q) + (int64_t)(pc.rq.q_start + tok) * a.q_stride_tok +
                         (int64_t)h * a.q_stride_head) + c);
         }
-        *reinterpret_cast<uint4*>(smem + G::kOffQ + (uint32_t)(r >> 3) * G::kGroup +
-                                  (uint32_t)(c >> 3) * 1024u +
+        *reinterpret_cast<uint4*>(smem + G::kOffQ + (uint32_t)(r >> 3) * G::kGroup + (uint32_t)(c >> 3) * 1024u +
                                   swz128((uint32_t)(r & 7), (uint32_t)(c & 7))) = x;
       }
       fence_proxy_async_smem();   // generic writes -> the tensor core's operand reads
@@ -385,6 +406,7 @@ latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant
     };
     next_q(item0);
 
+    Ring<NS> kp;
     int T = 0;
     for (int item = item0; ok && item < item1; ++item) {
       const Piece pc(a, item, rb, N);
@@ -523,17 +545,19 @@ latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant
           x[i + 2] = ex2(x[i + 2] + neg);
           l[q] += x[i] + x[i + 2];
         }
-        // with two P buffers, S(T) complete means P V(T - 2) complete: buffer free
-        if (NP == 1 && j > 0 &&
-            !warp_wait(bar(L_PV + ((T - 1) & 1)), (uint32_t)(((T - 1) >> 1) & 1), a.status))
-          s_fail[(T + 1) & 1] = 1;   // seen behind the next tile's barrier, or at the end
-        const uint32_t pb = sbase + G::kOffP + (uint32_t)(T % NP) * G::kP;
+        // P(T) only once P V(T - 2) is complete (nearly always it is): nobody then
+        // waits for a phase of the P and P V barriers that is not the next one
+        if (T >= 2 && !warp_wait(bar(L_PV + (T & 1)), (uint32_t)(((T >> 1) - 1) & 1), a.status))
+          s_fail[(T + 1) & 1] = 1;   // seen behind the next tile's barrier
+        // it takes the place of the tile's rotary columns
+        const uint32_t pb = sbase + (uint32_t)kp.slot * G::kTile + G::kOffP;
+        kp.next();
 #pragma unroll
         for (int jj = 0; jj < NG / 8; jj += 2) {
           // matrices: rows 8jj.. keys 0-7 and 8-15 of the warp, rows 8(jj + 1).. alike
           const int mt = lane >> 3;
           const uint32_t row = (uint32_t)(gc + 8 * (jj + (mt >> 1)) + (lane & 7));
-          stmatrix_x4_trans(pb + swz128(row, (uint32_t)(2 * quad + (mt & 1))),
+          stmatrix_x4_trans(pb + (row >> 3) * G::kGroup + swz128(row & 7, (uint32_t)(2 * quad + (mt & 1))),
                             pack2<F16>(x[4 * jj], x[4 * jj + 1]),
                             pack2<F16>(x[4 * jj + 2], x[4 * jj + 3]),
                             pack2<F16>(x[4 * jj + 4], x[4 * jj + 5]),
@@ -577,11 +601,8 @@ latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant
         out += (row + gc) * DL + quad * 32;
 #pragma unroll 1
         for (int blk = 0; blk < DL / 128; ++blk)
-#pragma unroll
-          for (int n = 0; n < NG; n += 16)
-            store_columns<typename std::remove_pointer<decltype(out)>::type, DL>(
-                tmem + lane_off + (uint32_t)(blk * N + gc + n), s_col + gc + n, pc.rows - gc - n,
-                out + n * DL + blk * 128, lane);
+          store_columns<typename std::remove_pointer<decltype(out)>::type, DL, NG>(
+              tmem + lane_off + (uint32_t)(blk * N + gc), s_col + gc, pc.rows - gc, out + blk * 128, lane);
       };
       if (!whole) write(a.ws_o, prow);
       else if (a.out_dtype == PKA_DTYPE_F32) write(static_cast<float*>(a.out), orow);
@@ -601,68 +622,77 @@ latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant
 }
 
 // The pieces of a cut request: out = sum_c w_c o_c / sum_c w_c with
-// w_c = 2^(lse_c - max), one CTA per row.  The weights are made once, a piece
-// per thread; then four thread groups take every fourth piece, eight rows in
-// flight each.  Launched while the decode still runs, it waits for that grid.
-constexpr int kMaxPieces = 1024;
+// w_c = 2^(lse_c - max).  A CTA of 128 threads takes a row, four values a thread
+// and eight pieces in flight; a row of more than kFewPieces is shared out to
+// DL / 128 CTAs of 128 dimensions whose four warps take every fourth piece.
+// Every warp makes the weights for itself, a piece per lane.  Launched while
+// the decode still runs, it waits for that grid's end.
+constexpr int kFewPieces = 16;
 
 template <int DL>
-__global__ void __launch_bounds__(DL)
+__global__ void __launch_bounds__(128)
 latent_merge_kernel(const __grid_constant__ LatentArgs a) {
-  constexpr int T = DL / 4;   // threads of a group: four values each
-  __shared__ float4 s_o[3][T];
-  __shared__ float s_w[kMaxPieces];
-  __shared__ float s_red[DL / 32];
+  __shared__ float4 s_o[3][32];
   const int b = __ldg(a.splits + blockIdx.x / a.max_rows), r = blockIdx.x % a.max_rows;
   const LatentReq rq = a.reqs[b];
-  const int rows = rq.q_len * a.num_heads, tid = threadIdx.x;
+  const int rows = rq.q_len * a.num_heads, tid = threadIdx.x, lane = tid & 31;
+  const bool shared = rq.n_parts > kFewPieces;
+  const int slab = blockIdx.y;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (r >= rows) return;
+  if (r >= rows || (!shared && slab > 0) || (!shared && tid >= DL / 4)) return;
+  const int g = shared ? tid >> 5 : 0, step = shared ? 4 : 1;
+  const int x = shared ? slab * 32 + lane : tid;
   const int64_t p0 = rq.part_base + r;
-  auto reduce = [&](float v, auto op) -> float {   // over the CTA
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, d));
-    __syncthreads();
-    if ((tid & 31) == 0) s_red[tid >> 5] = v;
-    __syncthreads();
-    v = s_red[0];
-#pragma unroll
-    for (int w = 1; w < DL / 32; ++w) v = op(v, s_red[w]);
-    return v;
+  auto lse_of = [&](int c) {
+    return c < rq.n_parts ? __ldcg(a.ws_lse + p0 + (int64_t)c * rows) : neg_inf();
   };
-  float m = neg_inf();
-  for (int c = tid; c < rq.n_parts; c += DL) {
-    s_w[c] = __ldcg(a.ws_lse + p0 + (int64_t)c * rows);
-    m = fmaxf(m, s_w[c]);
-  }
-  m = reduce(m, [](float u, float v) { return fmaxf(u, v); });
-  float sum = 0.f;
-  for (int c = tid; c < rq.n_parts; c += DL) {
-    s_w[c] = s_w[c] == neg_inf() ? 0.f : ex2(s_w[c] - m);
-    sum += s_w[c];
-  }
-  sum = reduce(sum, [](float u, float v) { return u + v; });
-  const int g = tid / T, x = tid % T;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-  for (int c = g; c < rq.n_parts; c += 4) {
-    const float w = s_w[c];
-    if (w == 0.f) continue;   // a piece without keys has no output rows
-    const float4 v = __ldcg(reinterpret_cast<const float4*>(a.ws_o + (p0 + (int64_t)c * rows) * DL) + x);
-    o.x += w * v.x;
-    o.y += w * v.y;
-    o.z += w * v.z;
-    o.w += w * v.w;
-  }
-  if (g > 0) s_o[g - 1][x] = o;
-  __syncthreads();
-  if (g > 0) return;
+  const float first = lse_of(lane);
+  float m = first;
+  for (int c = lane + 32; c < rq.n_parts; c += 32) m = fmaxf(m, lse_of(c));
 #pragma unroll
-  for (int k = 0; k < 3; ++k) {
-    o.x += s_o[k][x].x;
-    o.y += s_o[k][x].y;
-    o.z += s_o[k][x].z;
-    o.w += s_o[k][x].w;
+  for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+  float sum = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (m != neg_inf()) {
+    for (int c0 = 0; c0 < rq.n_parts; c0 += 32) {
+      const float w = ex2((c0 == 0 ? first : lse_of(c0 + lane)) - m);   // 0 without keys
+      sum += w;
+      const int n = min(32, rq.n_parts - c0);
+      const float4* src = reinterpret_cast<const float4*>(a.ws_o + (p0 + (int64_t)c0 * rows) * DL) + x;
+      for (int k0 = g; k0 < n; k0 += 8 * step) {
+        float wk[8];
+        float4 v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int k = k0 + i * step;
+          wk[i] = __shfl_sync(0xffffffffu, w, k & 31);
+          if (k >= n) wk[i] = 0.f;
+          // a piece without keys has no output rows
+          v[i] = wk[i] != 0.f ? __ldcg(src + (int64_t)k * rows * (DL / 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          o.x += wk[i] * v[i].x;
+          o.y += wk[i] * v[i].y;
+          o.z += wk[i] * v[i].z;
+          o.w += wk[i] * v[i].w;
+        }
+      }
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  }
+  if (shared) {
+    if (g > 0) s_o[g - 1][lane] = o;
+    __syncthreads();
+    if (g > 0) return;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      o.x += s_o[k][lane].x;
+      o.y += s_o[k][lane].y;
+      o.z += s_o[k][lane].z;
+      o.w += s_o[k][lane].w;
+    }
   }
   const int64_t row = (int64_t)rq.q_start * a.num_heads + r;
   const float v[4] = {o.x, o.y, o.z, o.w};
@@ -671,28 +701,27 @@ latent_merge_kernel(const __grid_constant__ LatentArgs a) {
 }
 
 template <int DL, int N, bool F16>
-cudaError_t launch_tiles(const LatentArgs& a, const CUtensorMap& map, const CUtensorMap& qmap,
-                         cudaStream_t stream) {
+cudaError_t launch_tiles(const LatentArgs& a, const LatentMaps& maps, cudaStream_t stream) {
   auto kern = latent_decode_kernel<DL, N, F16>;
   static std::atomic<uint64_t> smem_set{0};   // devices whose limit was raised
   const cudaError_t e = set_smem_once(kern, (int)Geo<DL, N>::kSmem, smem_set);
   if (e != cudaSuccess) return e;
   kern<<<(unsigned)(a.num_segments * a.row_blocks), Geo<DL, N>::kThreads, Geo<DL, N>::kSmem, stream>>>(
-      a, map, qmap);
+      a, maps);
   return cudaGetLastError();
 }
 
 template <int DL, bool F16>
-int launch(const pka_latent_plan& plan, const LatentArgs& a, const CUtensorMap& map,
-           const CUtensorMap& qmap, cudaStream_t stream) {
-  cudaError_t e = plan.row_tile == 16   ? launch_tiles<DL, 16, F16>(a, map, qmap, stream)
-                  : plan.row_tile == 32 ? launch_tiles<DL, 32, F16>(a, map, qmap, stream)
-                                        : launch_tiles<DL, 64, F16>(a, map, qmap, stream);
+int launch(const pka_latent_plan& plan, const LatentArgs& a, const LatentMaps& maps,
+           cudaStream_t stream) {
+  cudaError_t e = plan.row_tile == 16   ? launch_tiles<DL, 16, F16>(a, maps, stream)
+                  : plan.row_tile == 32 ? launch_tiles<DL, 32, F16>(a, maps, stream)
+                                        : launch_tiles<DL, 64, F16>(a, maps, stream);
   if (e != cudaSuccess) return cuda_fail(e, "latent_decode_kernel launch");
   if (a.num_splits > 0) {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(a.num_splits * a.max_rows));
-    cfg.blockDim = dim3(DL);
+    cfg.gridDim = dim3((unsigned)(a.num_splits * a.max_rows), plan.max_parts > kFewPieces ? DL / 128 : 1);
+    cfg.blockDim = dim3(128);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -712,35 +741,38 @@ int launch_latent_decode(const pka_latent_plan& plan, const LatentArgs& args, co
   if (args.num_items == 0) return PKA_OK;
   LatentArgs a = args;
   // The pool as (64 columns, slot in 8, column chunk, slot / 8, page): one box of
-  // box_rows slots lands as groups of 8 keys, each NC swizzled 8 x 128 byte atoms.
-  // Groups are evenly spaced whatever the page size, so a tile of 64 keys from
-  // any number of pages is one operand, as keys (K-major) and as values (MN-major).
+  // box_rows whole rows lands as groups of 8 keys, each a swizzled 8 x 128 byte
+  // atom per chunk.  Groups are evenly spaced whatever the page size, so 64 keys
+  // from any number of pages are one operand, as keys (K-major) and as values
+  // (MN-major).
   const uint64_t row = (uint64_t)(plan.desc.latent_dim + plan.desc.rope_dim) * 2;
   const uint32_t nc = (uint32_t)plan.desc.latent_dim / 64 + 1;
-  const uint64_t dims[5] = {64, 8, nc, (uint64_t)plan.desc.page_size / 8, (uint64_t)plan.desc.num_pages};
-  const uint64_t strides[4] = {row, 128, 8 * row, (uint64_t)stride_page * 2};
-  const uint32_t box[5] = {64, 8, nc, (uint32_t)a.box_rows / 8, 1};
-  CUtensorMap map, qmap;
-  int rc = encode_bf16_map(&map, pages, 5, dims, strides, box);
-  if (rc != PKA_OK) return rc;
+  LatentMaps maps;
+  {
+    const uint64_t dims[5] = {64, 8, nc, (uint64_t)plan.desc.page_size / 8, (uint64_t)plan.desc.num_pages};
+    const uint64_t strides[4] = {row, 128, 8 * row, (uint64_t)stride_page * 2};
+    const uint32_t box[5] = {64, 8, nc, (uint32_t)a.box_rows / 8, 1};
+    const int rc = encode_bf16_map(&maps.pool, pages, 5, dims, strides, box);
+    if (rc != PKA_OK) return rc;
+  }
   // The queries alike, where heads come in groups of 8: (64 columns, head in 8,
   // chunk, head / 8, token), boxes of q_box heads that stay inside a token.
-  qmap = map;
   a.q_box = 0;
+  maps.q = maps.pool;
   if (a.num_heads % 8 == 0 && a.q_stride_head > 0 && (a.q_stride_tok > 0 || plan.total_q == 1)) {
     a.q_box = plan.row_tile;
     while (a.num_heads % a.q_box != 0) a.q_box /= 2;
     const uint64_t hs = (uint64_t)a.q_stride_head * 2;
-    const uint64_t qd[5] = {64, 8, nc, (uint64_t)a.num_heads / 8, (uint64_t)plan.total_q};
-    const uint64_t qs[4] = {hs, 128, 8 * hs, std::max((uint64_t)a.q_stride_tok * 2, (uint64_t)16)};
-    const uint32_t qb[5] = {64, 8, nc, (uint32_t)a.q_box / 8, 1};
-    rc = encode_bf16_map(&qmap, a.q, 5, qd, qs, qb);
+    const uint64_t dims[5] = {64, 8, nc, (uint64_t)a.num_heads / 8, (uint64_t)plan.total_q};
+    const uint64_t strides[4] = {hs, 128, 8 * hs, std::max((uint64_t)a.q_stride_tok * 2, (uint64_t)16)};
+    const uint32_t box[5] = {64, 8, nc, (uint32_t)a.q_box / 8, 1};
+    const int rc = encode_bf16_map(&maps.q, a.q, 5, dims, strides, box);
     if (rc != PKA_OK) return rc;
   }
   const bool f16 = plan.desc.dtype == PKA_DTYPE_F16;
   if (plan.desc.latent_dim == 512)
-    return f16 ? launch<512, true>(plan, a, map, qmap, stream) : launch<512, false>(plan, a, map, qmap, stream);
-  return f16 ? launch<256, true>(plan, a, map, qmap, stream) : launch<256, false>(plan, a, map, qmap, stream);
+    return f16 ? launch<512, true>(plan, a, maps, stream) : launch<512, false>(plan, a, maps, stream);
+  return f16 ? launch<256, true>(plan, a, maps, stream) : launch<256, false>(plan, a, maps, stream);
 }
 
 }  // namespace pka

@@ -136,9 +136,11 @@ int build_latent_plan(pka_latent_plan& p, const pka_latent_desc& d_in, const int
   for (LatentItem& it : p.items)
     if (count[it.request] > 1) it.part = p.reqs[it.request].n_parts++;
   p.splits.clear();
+  p.max_parts = 0;
   int64_t prow = 0;
   for (int32_t b = 0; b < B; ++b) {
     LatentReq& r = p.reqs[b];
+    p.max_parts = std::max(p.max_parts, r.n_parts);
     if (r.n_parts > 1) {
       r.part_base = (int32_t)prow;
       prow += (int64_t)r.n_parts * r.q_len * H;
