@@ -16,8 +16,8 @@ from . import _lib as L
 
 def _stream(stream):
     """cudaStream_t as an int (ctypes passes ints to void* parameters as is)."""
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:   # the current stream's handle, without a Stream object around it
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -465,21 +465,19 @@ def batch_prefill_run(plan, q, k, v, out=None, lse=None, stream=None):
     return (out, lse) if plan.desc.return_lse else out
 
 
-def _on_device(**tensors):
-    """Every given tensor is a CUDA tensor of the current device (the library launches there)."""
-    want = torch.device("cuda", torch.cuda.current_device())
+def _check_tensors(dtype, **tensors):
+    """Every given tensor has this type and lies on the current device, where the library
+    launches.  One pass: this runs on every call of a serving loop."""
+    dev = torch.cuda.current_device()
     for name, t in tensors.items():
-        if t is not None and t.device != want:
-            raise ValueError(f"{name} is on {t.device}, the current device is {want}")
+        if t is not None:
+            if t.dtype is not dtype:
+                raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+            if t.get_device() != dev:
+                raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
 
 
-def _typed(dtype, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.dtype != dtype:
-            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-
-
-def _dense(**tensors):
+def _contiguous(**tensors):
     for name, t in tensors.items():
         if t is not None and not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
@@ -488,8 +486,7 @@ def _dense(**tensors):
 def check_status(status, stream=None):
     """Synchronise, read and clear a status word (a device int32 tensor given to
     ``paged_kv_tables`` or ``paged_latent_append``); raises on what it reports."""
-    _typed(torch.int32, status=status)
-    _on_device(status=status)
+    _check_tensors(torch.int32, status=status)
     L.check(L.lib().pka_status_check(_ptr(status), _stream(stream)), "check_status")
 
 
@@ -508,53 +505,58 @@ def paged_kv_tables(kv_lens, new_lens, free_pages, free_head, block_tables, *, p
     query offsets ``[B + 1]``, one int64 slot per new token (-1 behind the last) and the
     advanced head.  A step that does not fit changes nothing and sets ``status``
     (``check_status``)."""
-    _typed(torch.int32, kv_lens=kv_lens, new_lens=new_lens, free_pages=free_pages,
-           free_head=free_head, block_tables=block_tables, seq_lens=seq_lens,
-           qo_indptr=qo_indptr, free_head_out=free_head_out, status=status)
-    _typed(torch.int64, slot_map=slot_map)
-    _on_device(kv_lens=kv_lens, new_lens=new_lens, free_pages=free_pages, free_head=free_head,
-               block_tables=block_tables, seq_lens=seq_lens, qo_indptr=qo_indptr,
-               slot_map=slot_map, free_head_out=free_head_out, status=status)
-    _dense(kv_lens=kv_lens, new_lens=new_lens, free_pages=free_pages, seq_lens=seq_lens,
-           qo_indptr=qo_indptr, slot_map=slot_map)
+    _check_tensors(torch.int32, kv_lens=kv_lens, new_lens=new_lens, free_pages=free_pages,
+                   free_head=free_head, block_tables=block_tables, seq_lens=seq_lens,
+                   qo_indptr=qo_indptr, free_head_out=free_head_out, status=status)
+    _contiguous(kv_lens=kv_lens, new_lens=new_lens, free_pages=free_pages)
     B = kv_lens.numel()
     if block_tables.dim() != 2 or block_tables.shape[0] != B or new_lens.numel() != B:
         raise ValueError("kv_lens, new_lens and block_tables must have one row per request")
-    if block_tables.stride(-1) != 1:
+    width = block_tables.shape[1]
+    row, col = block_tables.stride()
+    if col != 1:
         raise ValueError("block_tables rows must be dense")
     if free_head.numel() != 1:
         raise ValueError("free_head must hold one entry")
-    dev = kv_lens.device
     if slot_map is None:
         if num_slots is None:
             raise ValueError("num_slots is required when no slot_map is passed")
-        slot_map = torch.empty(num_slots, dtype=torch.int64, device=dev)
-    elif num_slots is not None and num_slots != slot_map.numel():
-        raise ValueError("num_slots differs from the length of slot_map")
+        slot_map = torch.empty(num_slots, dtype=torch.int64, device=kv_lens.device)
+    else:
+        _check_tensors(torch.int64, slot_map=slot_map)
+        _contiguous(slot_map=slot_map)
+        if num_slots is not None and num_slots != slot_map.numel():
+            raise ValueError("num_slots differs from the length of slot_map")
+        num_slots = slot_map.numel()
     if seq_lens is None:
-        seq_lens = torch.empty(B, dtype=torch.int32, device=dev)
+        seq_lens = torch.empty_like(kv_lens)
+    elif seq_lens.numel() != B or not seq_lens.is_contiguous():
+        raise ValueError("seq_lens must hold B contiguous entries")
     if qo_indptr is None:
-        qo_indptr = torch.empty(B + 1, dtype=torch.int32, device=dev)
+        qo_indptr = kv_lens.new_empty(B + 1)
+    elif qo_indptr.numel() != B + 1 or not qo_indptr.is_contiguous():
+        raise ValueError("qo_indptr must hold B + 1 contiguous entries")
     if free_head_out is None:
-        free_head_out = torch.empty(1, dtype=torch.int32, device=dev)
-    if seq_lens.numel() != B or qo_indptr.numel() != B + 1 or free_head_out.numel() != 1:
-        raise ValueError("seq_lens needs B entries, qo_indptr B + 1, free_head_out one")
+        free_head_out = torch.empty_like(free_head)
+    elif free_head_out.numel() != 1:
+        raise ValueError("free_head_out must hold one entry")
     rc = L.lib().paged_kv_tables(
-        _ptr(kv_lens), _ptr(new_lens), B, _ptr(free_pages), free_pages.numel(), _ptr(free_head),
-        page_size, _ptr(block_tables), max(block_tables.stride(0), block_tables.shape[1]),
-        block_tables.shape[1], _ptr(seq_lens), _ptr(qo_indptr), _ptr(slot_map), slot_map.numel(),
-        _ptr(free_head_out), _ptr(status), _stream(stream))
+        kv_lens.data_ptr(), new_lens.data_ptr(), B, free_pages.data_ptr(), free_pages.numel(),
+        free_head.data_ptr(), page_size, block_tables.data_ptr(), row if row > width else width,
+        width, seq_lens.data_ptr(), qo_indptr.data_ptr(), slot_map.data_ptr(), num_slots,
+        free_head_out.data_ptr(), _ptr(status), _stream(stream))
     L.check(rc, "paged_kv_tables")
     return KvTables(seq_lens, qo_indptr, slot_map, free_head_out)
 
 
-def _check_latent_pool(pages):
-    if pages.dim() != 3 or pages.stride(2) != 1 or pages.stride(1) != pages.shape[2]:
-        raise ValueError("pages must be [num_pages, page_size, dim] with dense slots")
-
-
-def _page_stride(pages):
-    return pages.stride(0) if pages.shape[0] > 1 else pages.shape[1] * pages.shape[2]
+def _latent_page_stride(pages):
+    """Page stride of a latent pool whose slots are dense rows."""
+    if pages.dim() == 3:
+        n, ps, dim = pages.shape
+        page, slot, col = pages.stride()
+        if col == 1 and slot == dim:
+            return page if n > 1 else ps * dim
+    raise ValueError("pages must be [num_pages, page_size, dim] with dense slots")
 
 
 def paged_latent_append(latent, rope, slot_map, pages, status=None, stream=None):
@@ -563,28 +565,36 @@ def paged_latent_append(latent, rope, slot_map, pages, status=None, stream=None)
     (negative entries skip their row), ``pages`` ``[num_pages, page_size, latent_dim +
     rope_dim]``, updated in place and returned.  A slot past the pool is skipped and
     reported in ``status`` (``check_status``)."""
-    if pages.dtype not in (torch.bfloat16, torch.float16):
-        raise ValueError(f"pages must be bfloat16 or float16, got {pages.dtype}")
-    _typed(pages.dtype, latent=latent, rope=rope)
-    _typed(torch.int64, slot_map=slot_map)
-    _typed(torch.int32, status=status)
-    _on_device(latent=latent, rope=rope, slot_map=slot_map, pages=pages, status=status)
-    _dense(slot_map=slot_map)
-    _check_latent_pool(pages)
+    dtype = pages.dtype
+    if dtype is not torch.bfloat16 and dtype is not torch.float16:
+        raise ValueError(f"pages must be bfloat16 or float16, got {dtype}")
+    _check_tensors(dtype, latent=latent, rope=rope, pages=pages)
+    _check_tensors(torch.int64, slot_map=slot_map)
+    page_stride = _latent_page_stride(pages)
+    n_pages, ps, dim = pages.shape
+    if latent.dim() != 2 or (rope is not None and rope.dim() != 2):
+        raise ValueError("latent and rope must be [T, dim]")
     T, dl = latent.shape
-    dr = 0 if rope is None else rope.shape[1]
-    if slot_map.numel() != T or (rope is not None and rope.shape[0] != T):
-        raise ValueError("latent, rope and slot_map must have one row per token")
-    if dl + dr != pages.shape[2]:
-        raise ValueError(f"rows of {dl} + {dr} values, the pool's have {pages.shape[2]}")
+    ls, lc = latent.stride()
+    dr = rs = 0
+    if rope is not None:
+        rows, dr = rope.shape
+        rs, rc = rope.stride()
+        if rows != T or (rc != 1 and T > 0):
+            raise ValueError("rope needs one row per token, with a dense last dimension")
+    if slot_map.numel() != T or not slot_map.is_contiguous():
+        raise ValueError("slot_map needs one contiguous entry per token")
+    if dl + dr != dim:
+        raise ValueError(f"rows of {dl} + {dr} values, the pool's have {dim}")
     if T == 0:
         return pages
-    if latent.stride(1) != 1 or (rope is not None and rope.stride(1) != 1):
-        raise ValueError("latent and rope must have a dense last dimension")
+    if lc != 1:
+        raise ValueError("latent must have a dense last dimension")
+    if status is not None:
+        _check_tensors(torch.int32, status=status)
     rc = L.lib().paged_latent_append(
-        _ptr(latent), latent.stride(0), _ptr(rope), 0 if rope is None else rope.stride(0), dl, dr,
-        _ptr(slot_map), T, _ptr(pages), pages.shape[0], pages.shape[1], _page_stride(pages),
-        _DTYPES[pages.dtype], _ptr(status), _stream(stream))
+        latent.data_ptr(), ls, _ptr(rope), rs, dl, dr, slot_map.data_ptr(), T, pages.data_ptr(),
+        n_pages, ps, page_stride, _DTYPES[dtype], _ptr(status), _stream(stream))
     L.check(rc, "paged_latent_append")
     return pages
 
@@ -597,6 +607,12 @@ class LatentDecodePlan:
         self.desc = desc
         self.workspace_bytes = workspace_bytes
         self.total_q = self.info["total_q"]
+        # what every run compares its tensors with
+        self.dtype, self.out_dtype = _TORCH[desc.dtype], _TORCH[desc.out_dtype]
+        self.row = (desc.num_heads, desc.latent_dim + desc.rope_dim)
+        self.out_row = (desc.num_heads, desc.latent_dim)
+        self.pages_shape = (desc.num_pages, desc.page_size, desc.latent_dim + desc.rope_dim)
+        self.table_width, self.return_lse = desc.max_pages_per_seq, bool(desc.return_lse)
 
     @property
     def info(self):
@@ -677,54 +693,67 @@ def paged_latent_decode_run(plan, q, pages, block_tables, seq_lens_kv=None, out=
     ``[num_pages, page_size, latent_dim + rope_dim]``.  Returns ``out``
     ``[T, H, latent_dim]`` (and the base-2 ``lse`` ``[T, H]`` when the plan returns it);
     rows of a given ``out`` past the plan's are left as they were."""
-    d = plan.desc
-    _typed(_TORCH[d.dtype], q=q, pages=pages)
-    _typed(torch.int32, block_tables=block_tables, seq_lens_kv=seq_lens_kv)
-    _typed(_TORCH[d.out_dtype], out=out)
-    _typed(torch.float32, lse=lse)
-    _on_device(q=q, pages=pages, block_tables=block_tables, seq_lens_kv=seq_lens_kv, out=out,
-               lse=lse, workspace=workspace)
-    _dense(seq_lens_kv=seq_lens_kv, out=out, lse=lse, workspace=workspace)
-    _check_latent_pool(pages)
-    D = d.latent_dim + d.rope_dim
+    _check_tensors(plan.dtype, q=q, pages=pages)
+    _check_tensors(torch.int32, block_tables=block_tables, seq_lens_kv=seq_lens_kv)
+    need, B = plan.total_q, plan.desc.batch_size
+    if q.dim() != 3 or q.shape[1:] != plan.row or q.shape[0] < need:
+        raise ValueError(f"q must be [>= {need}, {plan.row[0]}, {plan.row[1]}], "
+                         f"got {tuple(q.shape)}")
     T = q.shape[0]
-    if q.dim() != 3 or tuple(q.shape[1:]) != (d.num_heads, D) or T < plan.total_q:
-        raise ValueError(f"q must be [>= {plan.total_q}, {d.num_heads}, {D}], got {tuple(q.shape)}")
-    if q.stride(-1) != 1:
+    q_tok, q_head, q_col = q.stride()
+    if q_col != 1:
         raise ValueError("q must have a dense last dimension")
-    if tuple(pages.shape) != (d.num_pages, d.page_size, D):
-        raise ValueError(f"pages must be [{d.num_pages}, {d.page_size}, {D}], "
-                         f"got {tuple(pages.shape)}")
-    if block_tables.stride(-1) != 1 or block_tables.shape[0] < d.batch_size or \
-            block_tables.shape[1] < d.max_pages_per_seq:
+    page_stride = _latent_page_stride(pages)
+    if pages.shape != plan.pages_shape:
+        raise ValueError(f"pages must be {list(plan.pages_shape)}, got {tuple(pages.shape)}")
+    if block_tables.dim() != 2 or block_tables.shape[0] < B or \
+            block_tables.shape[1] < plan.table_width or block_tables.stride(1) != 1:
         raise ValueError("block_tables needs dense rows, one of at least max_pages_per_seq "
                          "entries per request")
-    if seq_lens_kv is not None and seq_lens_kv.numel() < d.batch_size:
-        raise ValueError("seq_lens_kv needs one entry per request")
+    row, width = block_tables.stride(0), block_tables.shape[1]
+    if seq_lens_kv is not None and (seq_lens_kv.numel() < B or not seq_lens_kv.is_contiguous()):
+        raise ValueError("seq_lens_kv needs one contiguous entry per request")
     if out is None:
-        out = torch.empty((T, d.num_heads, d.latent_dim), dtype=_TORCH[d.out_dtype],
-                          device=q.device)
-    if d.return_lse and lse is None:
-        lse = torch.empty((T, d.num_heads), dtype=torch.float32, device=q.device)
-    if out.dim() != 3 or tuple(out.shape[1:]) != (d.num_heads, d.latent_dim) or \
-            out.shape[0] < plan.total_q:
-        raise ValueError("out must be [T, num_heads, latent_dim]")
-    if lse is not None and (lse.dim() != 2 or lse.shape[1] != d.num_heads or
-                            lse.shape[0] < plan.total_q):
-        raise ValueError("lse must be [T, num_heads]")
-    if workspace is None and plan.workspace_bytes > 0:
-        workspace = torch.empty(plan.workspace_bytes, dtype=torch.uint8, device=q.device)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        out = torch.empty((T,) + plan.out_row, dtype=plan.out_dtype, device=q.device)
+    else:
+        _check_tensors(plan.out_dtype, out=out)
+        _contiguous(out=out)
+        if out.dim() != 3 or out.shape[1:] != plan.out_row or out.shape[0] < need:
+            raise ValueError("out must be [T, num_heads, latent_dim]")
+    if lse is not None:
+        _check_tensors(torch.float32, lse=lse)
+        _contiguous(lse=lse)
+        if lse.dim() != 2 or lse.shape[1] != plan.row[0] or lse.shape[0] < need:
+            raise ValueError("lse must be [T, num_heads]")
+    elif plan.return_lse:
+        lse = torch.empty((T, plan.row[0]), dtype=torch.float32, device=q.device)
+    ws_bytes = 0
+    if workspace is not None:
+        _check_tensors(workspace.dtype, workspace=workspace)
+        _contiguous(workspace=workspace)
+        ws_bytes = workspace.numel() * workspace.element_size()
+    elif plan.workspace_bytes > 0:
+        ws_bytes = plan.workspace_bytes
+        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
     rc = L.lib().paged_latent_decode_run(
-        plan.handle, _ptr(q), q.stride(0), q.stride(1), _ptr(pages), _page_stride(pages),
-        _ptr(block_tables), max(block_tables.stride(0), block_tables.shape[1]),
-        _ptr(seq_lens_kv), _ptr(out), _ptr(lse), _ptr(workspace), ws_bytes, _stream(stream))
+        plan.handle, q.data_ptr(), q_tok, q_head, pages.data_ptr(), page_stride,
+        block_tables.data_ptr(), row if row > width else width, _ptr(seq_lens_kv),
+        out.data_ptr(), _ptr(lse), _ptr(workspace), ws_bytes, _stream(stream))
     L.check(rc, "paged_latent_decode_run")
-    return (out, lse) if d.return_lse else out
+    return (out, lse) if plan.return_lse else out
 
 
 class LatentPrefillPlan(PrefillPlan):
     """A prefill plan for ``batch_latent_prefill_run``."""
+
+    def __init__(self, handle, desc, num_tiles, total_q, total_kv):
+        super().__init__(handle, desc, num_tiles)
+        self.total_q, self.total_kv = total_q, total_kv
+        # what every run compares its tensors with
+        self.dtype, self.out_dtype = _TORCH[desc.dtype], _TORCH[desc.out_dtype]
+        self.q_row = (desc.num_heads, desc.nope_dim + desc.rope_dim)
+        self.k_row, self.v_row = (desc.num_heads, desc.nope_dim), (desc.num_heads, desc.value_dim)
+        self.rope_dim, self.return_lse = desc.rope_dim, bool(desc.return_lse)
 
 
 def batch_latent_prefill_plan(qo_indptr, kv_indptr, *, num_heads, nope_dim=128, rope_dim=64,
@@ -749,9 +778,7 @@ def batch_latent_prefill_plan(qo_indptr, kv_indptr, *, num_heads, nope_dim=128, 
                                            ctypes.byref(nt),
                                            _stream(stream) if not host_only else None)
     L.check(rc, "batch_latent_prefill_plan")
-    plan = LatentPrefillPlan(h, d, nt.value)
-    plan.total_q, plan.total_kv = int(qo_t[-1]), int(kv_t[-1])
-    return plan
+    return LatentPrefillPlan(h, d, nt.value, int(qo_t[-1]), int(kv_t[-1]))
 
 
 def batch_latent_prefill_run(plan, q, k_nope, k_rope, v, out=None, lse=None, stream=None):
@@ -759,43 +786,48 @@ def batch_latent_prefill_run(plan, q, k_nope, k_rope, v, out=None, lse=None, str
     ``[Tk, H, nope]`` and ``v`` ``[Tk, H, value]`` with the same strides (the two parts of
     one projection's output, or two tensors alike), ``k_rope`` ``[Tk, rope]`` shared by the
     heads.  Returns ``out`` ``[Tq, H, value]`` (and ``lse`` when the plan returns it)."""
-    d = plan.desc
     if not isinstance(plan, LatentPrefillPlan):
         raise ValueError("the plan was not made by batch_latent_prefill_plan")
-    _typed(_TORCH[d.dtype], q=q, k_nope=k_nope, k_rope=k_rope, v=v)
-    _typed(_TORCH[d.out_dtype], out=out)
-    _typed(torch.float32, lse=lse)
-    _on_device(q=q, k_nope=k_nope, k_rope=k_rope, v=v, out=out, lse=lse)
-    _dense(out=out, lse=lse)
-    H, D = d.num_heads, d.nope_dim + d.rope_dim
-    if q.dim() != 3 or tuple(q.shape[1:]) != (H, D) or q.shape[0] < plan.total_q:
-        raise ValueError(f"q must be [>= {plan.total_q}, {H}, {D}], got {tuple(q.shape)}")
-    for name, t, w in (("k_nope", k_nope, d.nope_dim), ("v", v, d.value_dim)):
-        if t.dim() != 3 or tuple(t.shape[1:]) != (H, w) or t.shape[0] < plan.total_kv:
-            raise ValueError(f"{name} must be [>= {plan.total_kv}, {H}, {w}], got {tuple(t.shape)}")
-    if k_rope.dim() != 2 or k_rope.shape[1] != d.rope_dim or k_rope.shape[0] < plan.total_kv:
-        raise ValueError(f"k_rope must be [>= {plan.total_kv}, {d.rope_dim}], "
+    _check_tensors(plan.dtype, q=q, k_nope=k_nope, k_rope=k_rope, v=v)
+    need, need_kv = plan.total_q, plan.total_kv
+    if q.dim() != 3 or q.shape[1:] != plan.q_row or q.shape[0] < need:
+        raise ValueError(f"q must be [>= {need}, {plan.q_row[0]}, {plan.q_row[1]}], "
+                         f"got {tuple(q.shape)}")
+    if k_nope.dim() != 3 or k_nope.shape[1:] != plan.k_row or k_nope.shape[0] < need_kv or \
+            v.dim() != 3 or v.shape[1:] != plan.v_row or v.shape[0] < need_kv:
+        raise ValueError(f"k_nope and v must be [>= {need_kv}, {plan.k_row[0]}, ..] with rows of "
+                         f"{plan.k_row[1]} and {plan.v_row[1]}, got {tuple(k_nope.shape)} and "
+                         f"{tuple(v.shape)}")
+    if k_rope.dim() != 2 or k_rope.shape[1] != plan.rope_dim or k_rope.shape[0] < need_kv:
+        raise ValueError(f"k_rope must be [>= {need_kv}, {plan.rope_dim}], "
                          f"got {tuple(k_rope.shape)}")
-    for name, t in (("q", q), ("k_nope", k_nope), ("k_rope", k_rope), ("v", v)):
-        if t.stride(-1) != 1:
-            raise ValueError(f"{name} must have a dense last dimension")
-    if plan.total_kv > 0 and tuple(k_nope.stride()) != tuple(v.stride()):
+    q_tok, q_head, q_col = q.stride()
+    k_strides = k_nope.stride()
+    rope_tok, rope_col = k_rope.stride()
+    if q_col != 1 or k_strides[2] != 1 or rope_col != 1:
+        raise ValueError("q, k_nope and k_rope must have a dense last dimension")
+    if k_strides != v.stride():
         raise ValueError("k_nope and v must have the same strides")
     T = q.shape[0]
     if out is None:
-        out = torch.empty((T, H, d.value_dim), dtype=_TORCH[d.out_dtype], device=q.device)
-    if d.return_lse and lse is None:
-        lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
-    if out.dim() != 3 or tuple(out.shape[1:]) != (H, d.value_dim) or out.shape[0] < plan.total_q:
-        raise ValueError("out must be [Tq, H, value_dim]")
-    if lse is not None and (lse.dim() != 2 or lse.shape[1] != H or lse.shape[0] < plan.total_q):
-        raise ValueError("lse must be [Tq, H]")
+        out = torch.empty((T,) + plan.v_row, dtype=plan.out_dtype, device=q.device)
+    else:
+        _check_tensors(plan.out_dtype, out=out)
+        _contiguous(out=out)
+        if out.dim() != 3 or out.shape[1:] != plan.v_row or out.shape[0] < need:
+            raise ValueError("out must be [Tq, H, value_dim]")
+    if lse is not None:
+        _check_tensors(torch.float32, lse=lse)
+        _contiguous(lse=lse)
+        if lse.dim() != 2 or lse.shape[1] != plan.q_row[0] or lse.shape[0] < need:
+            raise ValueError("lse must be [Tq, H]")
+    elif plan.return_lse:
+        lse = torch.empty((T, plan.q_row[0]), dtype=torch.float32, device=q.device)
     rc = L.lib().batch_latent_prefill_run(
-        plan.handle, _ptr(q), q.stride(0), q.stride(1), _ptr(k_nope), _ptr(k_rope),
-        k_rope.stride(0), _ptr(v), k_nope.stride(0), k_nope.stride(1), _ptr(out), _ptr(lse),
-        _stream(stream))
+        plan.handle, q.data_ptr(), q_tok, q_head, k_nope.data_ptr(), k_rope.data_ptr(), rope_tok,
+        v.data_ptr(), k_strides[0], k_strides[1], out.data_ptr(), _ptr(lse), _stream(stream))
     L.check(rc, "batch_latent_prefill_run")
-    return (out, lse) if d.return_lse else out
+    return (out, lse) if plan.return_lse else out
 
 
 def paged_kv_gather(pages, block_tables, request, kv_head, tok_begin, tok_end, out=None,
