@@ -39,7 +39,7 @@ constexpr int kTileQ = 128, kTileK = 64, kDV = 128;
 constexpr int kQBlocks = 3, kVBlocks = 2;   // 64-column blocks of a query or key row, of a value
 constexpr uint32_t kQBox = 16384;           // 128 rows x 128 bytes
 constexpr uint32_t kKBox = 8192;            // 64 rows x 128 bytes
-constexpr int kKBlocks = 6, kVStages = 1;
+constexpr int kKBlocks = 4, kVStages = 2;
 constexpr int kThreads = 192;
 constexpr float kRescaleThreshold = 8.0f;
 constexpr uint32_t kColO = 128, kTmemCols = 256;
