@@ -25,26 +25,29 @@ constexpr float kRescaleThreshold = 8.0f;
 constexpr uint32_t kSmemLimit = 232448;   // dynamic shared memory of one CTA
 
 // Shared memory and TMEM of latent_dim DL with N query rows.  A stage is a tile
-// of 64 keys: groups of 8 keys, each NC swizzled atoms of 8 x 128 bytes.  Its
-// rotary atoms are dead once S is complete, and the weights of the tile (N / 8
-// atoms of 8 rows x 64 keys, the same spacing) are written over them.
+// of 64 keys as blocks of 256 latent dimensions and one of the 64 rotary ones;
+// a block is groups of 8 keys, each 4 (rotary: 1) swizzled atoms of 8 x 128
+// bytes.  Every block has barriers of its own: scores start with the first that
+// lands, and a block is asked for again as soon as its own products are done.
+// The rotary block is dead once S is complete, and the weights of the tile (N
+// rows of 64, the same layout) are written over it.
 template <int DL, int N>
 struct Geo {
-  static constexpr int NB = DL / 128;                   // 128-wide latent blocks of a row
-  static constexpr int NC = DL / 64 + 1;                // 64-column chunks of a row
-  static constexpr int SG = N >= 32 ? 2 : 1;            // softmax groups of four warps
-  static constexpr int NG = N / SG;                     // query rows of one
+  static constexpr int NB = DL / 128;                   // 128-wide latent blocks of P V
+  static constexpr int NH = DL / 256;                   // 256-wide blocks of a stage
+  static constexpr int SG = N / 16;                     // softmax groups: four warps, 16 rows
   static constexpr int kThreads = 96 + 128 * SG;
-  static constexpr uint32_t kGroup = NC * 1024;
-  static constexpr uint32_t kTile = 8 * kGroup;
-  static constexpr uint32_t kQ = N / 8 * kGroup;        // the queries, laid out like keys
+  static constexpr uint32_t kBlock = 32768, kRope = 8192;
+  static constexpr uint32_t kTile = NH * kBlock + kRope;
+  static constexpr uint32_t kQBlock = N * 512;          // the queries, laid out like keys
+  static constexpr uint32_t kQ = NH * kQBlock + N * 128;
   static constexpr uint32_t kMisc = 512 + (8 + 2) * N * 4;
   static constexpr int kFit = (kSmemLimit - kMisc - kQ) / kTile;
   static constexpr int NS = kFit < 4 ? kFit : 4;        // stages
   static constexpr uint32_t kOffQ = NS * kTile;
   static constexpr uint32_t kOffMisc = kOffQ + kQ;
   static constexpr uint32_t kSmem = kOffMisc + kMisc;
-  static constexpr uint32_t kOffP = (NC - 1) * 1024;    // inside a stage
+  static constexpr uint32_t kOffR = NH * kBlock;        // inside a stage
   static constexpr uint32_t kColS = NB * N;             // O blocks, then the two S buffers
   static constexpr uint32_t kCols = kColS + 2 * N;
   static constexpr uint32_t kTmemCols = kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
@@ -55,10 +58,10 @@ struct Geo {
 // T & 1.  No barrier runs a phase past one that somebody still has to see: S(T)
 // is issued once P(T - 2) is written, P(T) written once P V(T - 2) is complete.
 enum {
-  L_KFULL = 0, L_KEMPTY = 4, L_SFULL = 8, L_PFULL = 10, L_PV = 12, L_QFULL = 14, L_QFREE = 15,
-  L_OFREE = 16, L_SDONE = 17, L_ODONE = 18, L_COUNT = 19
+  L_KFULL = 0, L_KEMPTY = 12, L_SFULL = 24, L_PFULL = 26, L_PV = 28, L_QFULL = 30, L_QFREE = 31,
+  L_OFREE = 32, L_SDONE = 33, L_ODONE = 34, L_COUNT = 35   // K: three blocks a stage at most
 };
-static_assert(L_COUNT * 8 + 4 + 24 <= 512, "barriers, TMEM address, failure flags");
+static_assert(L_COUNT * 8 + 4 + 48 <= 512, "barriers, TMEM address, failure flags");
 
 // A position in a ring of N slots and the parity of its round.
 template <int N>
@@ -107,7 +110,7 @@ __device__ __forceinline__ int first_value(int lane) {
 }
 
 struct LatentMaps {
-  CUtensorMap pool, q;
+  CUtensorMap pool, pool_rope, q, q_rope;
 };
 
 // What a CTA needs to know of its piece.
@@ -190,14 +193,14 @@ template <int DL, int N, bool F16>
 __global__ void __launch_bounds__(Geo<DL, N>::kThreads, 1)
 latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant__ LatentMaps maps) {
   using G = Geo<DL, N>;
-  constexpr int NB = G::NB, NC = G::NC, NS = G::NS, SG = G::SG, NG = G::NG, C = NG / 4;
+  constexpr int NB = G::NB, NH = G::NH, NS = G::NS, SG = G::SG, NG = 16, C = NG / 4;
   constexpr uint32_t kIdescQK = idesc_bf16_f32(64, N, 0, 0, F16);
   constexpr uint32_t kIdescPV = idesc_bf16_f32(128, N, 1, 0, F16);
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
   uint8_t* misc = smem + G::kOffMisc;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + L_COUNT * 8);
-  float* s_max = reinterpret_cast<float*>(misc + 512);   // [SG][2][4 warps][NG]
+  float* s_max = reinterpret_cast<float*>(misc + 512);   // [SG][2][4 warps][16]
   float* s_col = s_max + 8 * N;                          // [N] rescale factors, then 1 / l
   int* s_seen = reinterpret_cast<int*>(s_col + N);       // [N] keys each row sees
   float* s_ref = s_col + N;                              // then the rows' reference maxima
@@ -209,21 +212,21 @@ latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant
   const int item0 = __ldg(a.segments + seg), item1 = __ldg(a.segments + seg + 1);
 
   if (tid == 0) {
-    for (int s = 0; s < 4; ++s) {
+    for (int s = 0; s < 12; ++s) {
       mbar_init(bar(L_KFULL + s), 1);
       mbar_init(bar(L_KEMPTY + s), 1);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar(L_SFULL + s), 1);
-      mbar_init(bar(L_PFULL + s), 128 * SG);
+      mbar_init(bar(L_PFULL + s), 4 * SG);   // one arrival per softmax warp
       mbar_init(bar(L_PV + s), 1);
     }
-    mbar_init(bar(L_QFULL), a.q_box > 0 ? 1 : 128 * SG);
+    mbar_init(bar(L_QFULL), a.q_box > 0 ? 1 : 4 * SG);
     mbar_init(bar(L_QFREE), 1);
-    mbar_init(bar(L_OFREE), 128 * SG);
+    mbar_init(bar(L_OFREE), 4 * SG);
     mbar_init(bar(L_SDONE), 1);
     mbar_init(bar(L_ODONE), 1);
-    for (int i = 0; i < 6; ++i) tmem_slot[1 + i] = 0;   // failure flags
+    for (int i = 0; i < 3 * SG; ++i) tmem_slot[1 + i] = 0;   // failure flags
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -239,10 +242,11 @@ latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant
 
   if (warp == 0) {
     // ---------------- TMA producer: lane i copies box i of a tile ----------------
-    if (lane < 2) tma_prefetch_desc(lane == 0 ? &maps.pool : &maps.q);
+    if (lane < 4) tma_prefetch_desc(lane == 0 ? &maps.pool : lane == 1 ? &maps.pool_rope
+                                    : lane == 2 ? &maps.q : &maps.q_rope);
     const int boxes = kLatentTile / a.box_rows, groups = a.box_rows / 8;
     Ring<NS> kp;
-    int nk = 0, I = 0;   // stages filled so far, pieces
+    int nk = 0, blocks = 0, I = 0;   // stages and blocks asked for so far, pieces
     bool ok = true;
     for (int item = item0; ok && item < item1; ++item) {
       const Piece pc(a, item, rb, N);
@@ -259,8 +263,11 @@ latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant
         __syncwarp();
         if (lane < N / a.q_box) {   // rows past the request's last are copied, and never stored
           const int r = pc.row0 + lane * a.q_box;
-          tma_load_5d(sbase + G::kOffQ + (uint32_t)(lane * a.q_box / 8) * G::kGroup, &maps.q, bar(L_QFULL), 0,
-                      0, 0, r % a.num_heads / 8, pc.rq.q_start + r / a.num_heads);
+          const int h8 = r % a.num_heads / 8, t = pc.rq.q_start + r / a.num_heads;
+          const uint32_t g8 = (uint32_t)(lane * a.q_box / 8), dst = sbase + G::kOffQ;
+          for (int h = 0; h < NH; ++h)
+            tma_load_5d(dst + (uint32_t)h * G::kQBlock + g8 * 4096u, &maps.q, bar(L_QFULL), 0, 0, 4 * h, h8, t);
+          tma_load_5d(dst + NH * G::kQBlock + g8 * 1024u, &maps.q_rope, bar(L_QFULL), 0, 0, 4 * NH, h8, t);
         }
         __syncwarp();
       }
@@ -269,28 +276,51 @@ latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant
       for (int j = 0; j < pc.n; ++j) {
         const int tok = tok0 + j * kLatentTile, page = next;
         next = page_of(tok + kLatentTile);
-        if (nk >= NS && !(ok = warp_wait(bar(L_KEMPTY + kp.slot), kp.parity ^ 1u, a.status))) break;
-        if (lane == 0) mbar_arrive_expect_tx(bar(L_KFULL + kp.slot), G::kTile);
-        __syncwarp();
-        if (lane < boxes)
-          tma_load_5d(sbase + (uint32_t)kp.slot * G::kTile + (uint32_t)(lane * groups) * G::kGroup, &maps.pool,
-                      bar(L_KFULL + kp.slot), 0, 0, 0, tok % a.page_size / 8, page);
-        __syncwarp();
+        const int slot8 = tok % a.page_size / 8;
+        const uint32_t dst = sbase + (uint32_t)kp.slot * G::kTile;
+        for (int h = 0; h <= NH; ++h) {   // blocks in the order P V lets go of them
+          const int i = 3 * kp.slot + h;
+          if (nk >= NS && !(ok = warp_wait(bar(L_KEMPTY + i), kp.parity ^ 1u, a.status))) break;
+          if (lane == 0) mbar_arrive_expect_tx(bar(L_KFULL + i), h < NH ? G::kBlock : G::kRope);
+          __syncwarp();
+          if (lane < boxes)
+            tma_load_5d(dst + (uint32_t)h * G::kBlock + (uint32_t)(lane * groups) * (h < NH ? 4096u : 1024u),
+                        h < NH ? &maps.pool : &maps.pool_rope, bar(L_KFULL + i), 0, 0, 4 * h, slot8, page);
+          __syncwarp();
+          ++blocks;
+        }
+        if (!ok) break;
         kp.next();
         ++nk;
       }
     }
     if (!ok) {   // give the copies already issued a bounded chance to land
-      for (int i = max(0, nk - NS); i < nk; ++i)
-        mbar_wait(bar(L_KFULL + i % NS), (uint32_t)((i / NS) & 1), nullptr);
+      for (int i = max(0, blocks - NS * (NH + 1)); i < blocks; ++i)
+        mbar_wait(bar(L_KFULL + 3 * (i / (NH + 1) % NS) + i % (NH + 1)),
+                  (uint32_t)((i / (NH + 1) / NS) & 1), nullptr);
       if (a.q_box > 0 && I > 0) mbar_wait(bar(L_QFULL), (uint32_t)((I - 1) & 1), nullptr);
     }
   } else if (warp == 1) {
     // ---------------- issues S^T = K Q^T ----------------
     // Its own warp, so that neither products of keys that are still on their way
     // hold up a ready P V nor the other way round.
-    const uint64_t dk = smem_desc_sw128(sbase, 16u, G::kGroup);
-    const uint64_t dq = smem_desc_sw128(sbase + G::kOffQ, 16u, G::kGroup);
+    const uint64_t dk = smem_desc_sw128(sbase, 16u, 4096u);
+    const uint64_t dq = smem_desc_sw128(sbase + G::kOffQ, 16u, 4096u);
+    const uint64_t dkr = smem_desc_sw128(sbase + G::kOffR, 16u, 1024u);
+    const uint64_t dqr = smem_desc_sw128(sbase + G::kOffQ + NH * G::kQBlock, 16u, 1024u);
+    // rows past the last token may hold anything, and 0 * inf is not 0: clear them
+    // to the end of their box (boxes past it brought zeros)
+    auto clear_rows = [&](uint32_t off, int atoms, int live) {
+      const int end = (live + a.box_rows - 1) / a.box_rows * a.box_rows;
+      for (int i = lane; i < (end - live) * atoms * 8; i += 32) {
+        const int r = live + i / (atoms * 8), c = i % (atoms * 8);
+        *reinterpret_cast<uint4*>(smem + off + (uint32_t)((r >> 3) * atoms + (c >> 3)) * 1024u +
+                                  (uint32_t)(r & 7) * 128u + (uint32_t)(c & 7) * 16u) =
+            make_uint4(0u, 0u, 0u, 0u);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+    };
     Ring<NS> kp;
     int T = 0, I = 0;   // tiles and non-empty pieces before this one
     bool ok = true;
@@ -301,29 +331,24 @@ latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant
       ++I;
       for (int j = 0; ok && j < pc.n; ++j, ++T) {
         // P(T - 2) written means S(T - 2) read: this S buffer is free
-        ok = (T < 2 || warp_wait(bar(L_PFULL + (T & 1)), (uint32_t)(((T >> 1) - 1) & 1), a.status)) &&
-             warp_wait(bar(L_KFULL + kp.slot), kp.parity, a.status);
-        if (!ok) break;
+        ok = T < 2 || warp_wait(bar(L_PFULL + (T & 1)), (uint32_t)(((T >> 1) - 1) & 1), a.status);
         const int live = pc.kv - (pc.tile0 + j) * kLatentTile;
-        if (live < kLatentTile) {
-          // rows past the last token may hold anything, and 0 * inf is not 0:
-          // clear them to the end of their box (boxes past it brought zeros)
-          const int end = (live + a.box_rows - 1) / a.box_rows * a.box_rows;
-          for (int i = lane; i < (end - live) * NC * 8; i += 32) {
-            const int r = live + i / (NC * 8), c = i % (NC * 8);
-            *reinterpret_cast<uint4*>(smem + (uint32_t)kp.slot * G::kTile + (uint32_t)(r >> 3) * G::kGroup +
-                                      (uint32_t)(c >> 3) * 1024u + (uint32_t)(r & 7) * 128u +
-                                      (uint32_t)(c & 7) * 16u) = make_uint4(0u, 0u, 0u, 0u);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-        }
-        tc_fence_after();
-        const uint32_t d = tmem + G::kColS + (uint32_t)(T & 1) * N;
-        const uint64_t dkt = dk + (uint32_t)kp.slot * (G::kTile / 16);
+        const uint32_t d = tmem + G::kColS + (uint32_t)(T & 1) * N, off = (uint32_t)kp.slot * G::kTile;
 #pragma unroll
-        for (int c = 0; c < NC; ++c)   // 64 keys x N rows += 64 columns of each
-          umma_ss_k4(d, dkt + c * 64, dq + c * 64, kIdescQK, c > 0 ? 1u : 0u);
+        for (int h = 0; h <= NH; ++h) {   // 64 keys x N rows += 256 columns of each, then 64
+          ok = ok && warp_wait(bar(L_KFULL + 3 * kp.slot + h), kp.parity, a.status);
+          if (!ok) break;
+          if (live < kLatentTile) clear_rows(off + (uint32_t)h * G::kBlock, h < NH ? 4 : 1, live);
+          tc_fence_after();
+          if (h < NH) {
+            const uint64_t x = dk + (off + (uint32_t)h * G::kBlock) / 16, y = dq + h * (G::kQBlock / 16);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) umma_ss_k4(d, x + c * 64, y + c * 64, kIdescQK, h + c > 0 ? 1u : 0u);
+          } else {
+            umma_ss_k4(d, dkr + off / 16, dqr, kIdescQK, 1u);
+          }
+        }
+        if (!ok) break;
         umma_commit_elect(bar(L_SFULL + (T & 1)));
         kp.next();
       }
@@ -333,8 +358,8 @@ latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant
     warp_wait(bar(L_SDONE), 0, a.status);   // nothing of this warp's still runs on the tensor core
   } else if (warp == 2) {
     // ---------------- issues O^T += V^T P^T ----------------
-    const uint64_t dv = smem_desc_sw128(sbase, 1024u, G::kGroup);
-    const uint64_t dp = smem_desc_sw128(sbase + G::kOffP, 16u, G::kGroup);
+    const uint64_t dv = smem_desc_sw128(sbase, 1024u, 4096u);
+    const uint64_t dp = smem_desc_sw128(sbase + G::kOffR, 16u, 1024u);
     Ring<NS> kp;
     int T = 0, I = 0;
     bool ok = true;
@@ -346,12 +371,15 @@ latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant
         if (ok && j == 0 && I > 0) ok = warp_wait(bar(L_OFREE), (uint32_t)((I - 1) & 1), a.status);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t stage = (uint32_t)kp.slot * (G::kTile / 16);
+        const uint32_t off = (uint32_t)kp.slot * G::kTile;
 #pragma unroll
-        for (int b = 0; b < NB; ++b)   // 128 dims x N rows += 64 keys
-          umma_ss_k4_steps<2 * (int)G::kGroup / 16, 2>(tmem + (uint32_t)b * N, dv + stage + b * 128, dp + stage,
-                                                       kIdescPV, j > 0 ? 1u : 0u);
-        umma_commit_elect(bar(L_KEMPTY + kp.slot));
+        for (int b = 0; b < NB; ++b) {   // 128 dims x N rows += 64 keys
+          umma_ss_k4_steps<2 * 4096 / 16, 2>(tmem + (uint32_t)b * N,
+                                             dv + (off + (uint32_t)(b >> 1) * G::kBlock + (b & 1) * 2048u) / 16,
+                                             dp + off / 16, kIdescPV, j > 0 ? 1u : 0u);
+          if (b & 1) umma_commit_elect(bar(L_KEMPTY + 3 * kp.slot + (b >> 1)));
+        }
+        umma_commit_elect(bar(L_KEMPTY + 3 * kp.slot + NH));
         umma_commit_elect(bar(L_PV + (T & 1)));
         kp.next();
       }
@@ -383,11 +411,14 @@ latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant
                         static_cast<const uint16_t*>(a.q) + (int64_t)(pc.rq.q_start + tok) * a.q_stride_tok +
                         (int64_t)h * a.q_stride_head) + c);
         }
-        *reinterpret_cast<uint4*>(smem + G::kOffQ + (uint32_t)(r >> 3) * G::kGroup + (uint32_t)(c >> 3) * 1024u +
-                                  swz128((uint32_t)(r & 7), (uint32_t)(c & 7))) = x;
+        const uint32_t at = c < DL / 8 ? (uint32_t)(c >> 5) * G::kQBlock + (uint32_t)(r >> 3) * 4096u +
+                                             (uint32_t)((c >> 3) & 3) * 1024u
+                                       : NH * G::kQBlock + (uint32_t)(r >> 3) * 1024u;
+        *reinterpret_cast<uint4*>(smem + G::kOffQ + at + swz128((uint32_t)(r & 7), (uint32_t)(c & 7))) = x;
       }
       fence_proxy_async_smem();   // generic writes -> the tensor core's operand reads
-      mbar_arrive(bar(L_QFULL));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(L_QFULL));
     };
     // the next piece that has tiles, from `item` on; the last S of the one before
     // is complete for this thread's group, and QFREE says so for both
@@ -445,8 +476,7 @@ latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant
         tc_fence_after();
         uint32_t s[NG / 2];
         const uint32_t s_tm = tmem + lane_off + G::kColS + (uint32_t)(T & 1) * N + (uint32_t)gc;
-        if constexpr (NG == 16) tmem_ld_frag2(s_tm, s);
-        else tmem_ld_frag4(s_tm, s);
+        tmem_ld_frag2(s_tm, s);
         tmem_wait_ld();
         reg_fence<NG / 2>(s);
         float x[NG / 2];
@@ -550,14 +580,14 @@ latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant
         if (T >= 2 && !warp_wait(bar(L_PV + (T & 1)), (uint32_t)(((T >> 1) - 1) & 1), a.status))
           s_fail[(T + 1) & 1] = 1;   // seen behind the next tile's barrier
         // it takes the place of the tile's rotary columns
-        const uint32_t pb = sbase + (uint32_t)kp.slot * G::kTile + G::kOffP;
+        const uint32_t pb = sbase + (uint32_t)kp.slot * G::kTile + G::kOffR;
         kp.next();
 #pragma unroll
         for (int jj = 0; jj < NG / 8; jj += 2) {
           // matrices: rows 8jj.. keys 0-7 and 8-15 of the warp, rows 8(jj + 1).. alike
           const int mt = lane >> 3;
           const uint32_t row = (uint32_t)(gc + 8 * (jj + (mt >> 1)) + (lane & 7));
-          stmatrix_x4_trans(pb + (row >> 3) * G::kGroup + swz128(row & 7, (uint32_t)(2 * quad + (mt & 1))),
+          stmatrix_x4_trans(pb + swz128(row, (uint32_t)(2 * quad + (mt & 1))),
                             pack2<F16>(x[4 * jj], x[4 * jj + 1]),
                             pack2<F16>(x[4 * jj + 2], x[4 * jj + 3]),
                             pack2<F16>(x[4 * jj + 4], x[4 * jj + 5]),
@@ -565,7 +595,8 @@ latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant
         }
         fence_proxy_async_smem();
         tc_fence_before();
-        mbar_arrive(bar(L_PFULL + (T & 1)));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L_PFULL + (T & 1)));
       }
       if (!ok) break;
       ++I;
@@ -609,7 +640,8 @@ latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant
       else if (a.out_dtype == PKA_DTYPE_F16) write(static_cast<__half*>(a.out), orow);
       else write(static_cast<__nv_bfloat16*>(a.out), orow);
       tc_fence_before();
-      mbar_arrive(bar(L_OFREE));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(L_OFREE));
     }
   }
 
@@ -741,32 +773,37 @@ int launch_latent_decode(const pka_latent_plan& plan, const LatentArgs& args, co
   if (args.num_items == 0) return PKA_OK;
   LatentArgs a = args;
   // The pool as (64 columns, slot in 8, column chunk, slot / 8, page): one box of
-  // box_rows whole rows lands as groups of 8 keys, each a swizzled 8 x 128 byte
-  // atom per chunk.  Groups are evenly spaced whatever the page size, so 64 keys
-  // from any number of pages are one operand, as keys (K-major) and as values
-  // (MN-major).
+  // box_rows rows and four chunks (one for the rotary columns) lands as groups of
+  // 8 keys, each a swizzled 8 x 128 byte atom per chunk.  Groups are evenly spaced
+  // whatever the page size, so 64 keys from any number of pages are one operand,
+  // as keys (K-major) and as values (MN-major).
   const uint64_t row = (uint64_t)(plan.desc.latent_dim + plan.desc.rope_dim) * 2;
-  const uint32_t nc = (uint32_t)plan.desc.latent_dim / 64 + 1;
+  const uint64_t nc = (uint64_t)plan.desc.latent_dim / 64 + 1;
+  auto encode = [](CUtensorMap* four, CUtensorMap* one, const void* base, const uint64_t* dims,
+                   const uint64_t* strides, uint32_t groups) {
+    const uint32_t box4[5] = {64, 8, 4, groups, 1}, box1[5] = {64, 8, 1, groups, 1};
+    const int rc = encode_bf16_map(four, base, 5, dims, strides, box4);
+    return rc != PKA_OK ? rc : encode_bf16_map(one, base, 5, dims, strides, box1);
+  };
   LatentMaps maps;
   {
     const uint64_t dims[5] = {64, 8, nc, (uint64_t)plan.desc.page_size / 8, (uint64_t)plan.desc.num_pages};
     const uint64_t strides[4] = {row, 128, 8 * row, (uint64_t)stride_page * 2};
-    const uint32_t box[5] = {64, 8, nc, (uint32_t)a.box_rows / 8, 1};
-    const int rc = encode_bf16_map(&maps.pool, pages, 5, dims, strides, box);
+    const int rc = encode(&maps.pool, &maps.pool_rope, pages, dims, strides, (uint32_t)a.box_rows / 8);
     if (rc != PKA_OK) return rc;
   }
   // The queries alike, where heads come in groups of 8: (64 columns, head in 8,
   // chunk, head / 8, token), boxes of q_box heads that stay inside a token.
   a.q_box = 0;
   maps.q = maps.pool;
+  maps.q_rope = maps.pool;
   if (a.num_heads % 8 == 0 && a.q_stride_head > 0 && (a.q_stride_tok > 0 || plan.total_q == 1)) {
     a.q_box = plan.row_tile;
     while (a.num_heads % a.q_box != 0) a.q_box /= 2;
     const uint64_t hs = (uint64_t)a.q_stride_head * 2;
     const uint64_t dims[5] = {64, 8, nc, (uint64_t)a.num_heads / 8, (uint64_t)plan.total_q};
     const uint64_t strides[4] = {hs, 128, 8 * hs, std::max((uint64_t)a.q_stride_tok * 2, (uint64_t)16)};
-    const uint32_t box[5] = {64, 8, nc, (uint32_t)a.q_box / 8, 1};
-    const int rc = encode_bf16_map(&maps.q, a.q, 5, dims, strides, box);
+    const int rc = encode(&maps.q, &maps.q_rope, a.q, dims, strides, (uint32_t)a.q_box / 8);
     if (rc != PKA_OK) return rc;
   }
   const bool f16 = plan.desc.dtype == PKA_DTYPE_F16;
