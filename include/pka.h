@@ -782,7 +782,9 @@ typedef struct pka_latent_prefill_desc {
 } pka_latent_prefill_desc;
 
 /* The plan is a prefill plan: batch_prefill_plan_check and
- * batch_prefill_plan_destroy take it, batch_prefill_run does not. */
+ * batch_prefill_plan_destroy take it, batch_prefill_run does not.
+ * num_tiles_out receives the number of tiles of up to 256 rows of one request
+ * and head, a pair of CTAs each. */
 int batch_latent_prefill_plan(pka_prefill_plan** plan_out, const pka_latent_prefill_desc* desc,
                               const int32_t* qo_indptr_host, const int32_t* kv_indptr_host,
                               int32_t* num_tiles_out, void* stream);

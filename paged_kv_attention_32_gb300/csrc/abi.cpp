@@ -187,6 +187,23 @@ int upload_prefill_plan(pka_prefill_plan& p, cudaStream_t stream) {
 
 }  // namespace
 
+int pka::make_prefill_plan(pka_prefill_plan** plan_out, const pka_prefill_desc& desc,
+                           const int32_t* qo, const int32_t* kv, int32_t tile_q, bool by_head,
+                           int32_t* num_tiles_out, cudaStream_t stream) {
+  *plan_out = nullptr;
+  pka_prefill_plan* p = new (std::nothrow) pka_prefill_plan();
+  if (p == nullptr) return fail(PKA_ERR_INVALID_ARG, "out of host memory");
+  int rc = build_prefill_plan(*p, desc, qo, kv, nullptr, nullptr, tile_q, by_head);
+  if (rc == PKA_OK && !(desc.flags & PKA_PLAN_HOST_ONLY)) rc = upload_prefill_plan(*p, stream);
+  if (rc != PKA_OK) {
+    batch_prefill_plan_destroy(p);
+    return rc;
+  }
+  if (num_tiles_out) *num_tiles_out = (int32_t)p->tiles.size();
+  *plan_out = p;
+  return PKA_OK;
+}
+
 extern "C" {
 
 const char* pka_last_error(void) { return pka::last_error(); }
@@ -555,20 +572,10 @@ int batch_prefill_plan(pka_prefill_plan** plan_out, const pka_prefill_desc* desc
   NvtxRange nvtx_range("pka::batch_prefill_plan");
   clear_error();
   PKA_CHECK_ARG(plan_out != nullptr && desc != nullptr, "plan_out and desc must not be NULL");
-  *plan_out = nullptr;
-  pka_prefill_plan* p = new (std::nothrow) pka_prefill_plan();
-  if (p == nullptr) return fail(PKA_ERR_INVALID_ARG, "out of host memory");
-  int rc = build_prefill_plan(*p, *desc, qo_indptr_host, kv_indptr_host);
-  if (rc == PKA_OK && !(desc->flags & PKA_PLAN_HOST_ONLY))
-    rc = upload_prefill_plan(*p, static_cast<cudaStream_t>(stream));
-  if (rc != PKA_OK) {
-    batch_prefill_plan_destroy(p);
-    return rc;
-  }
-  if (workspace_bytes_out) *workspace_bytes_out = 0;
-  if (num_tiles_out) *num_tiles_out = (int32_t)p->tiles.size();
-  *plan_out = p;
-  return PKA_OK;
+  const int rc = make_prefill_plan(plan_out, *desc, qo_indptr_host, kv_indptr_host, 128, false,
+                                   num_tiles_out, static_cast<cudaStream_t>(stream));
+  if (rc == PKA_OK && workspace_bytes_out) *workspace_bytes_out = 0;
+  return rc;
 }
 
 int batch_prefill_plan_fixed(pka_prefill_plan** plan_out, const pka_prefill_desc* desc,

@@ -375,8 +375,8 @@ int batch_latent_prefill_plan(pka_prefill_plan** plan_out, const pka_latent_pref
   d.out_dtype = desc->out_dtype;
   pka_prefill_plan* p = nullptr;
   const int rc = guarded([&] {
-    return batch_prefill_plan(&p, &d, qo_indptr_host, kv_indptr_host, nullptr, num_tiles_out,
-                              stream);
+    return make_prefill_plan(&p, d, qo_indptr_host, kv_indptr_host, 256, true,
+                             num_tiles_out, static_cast<cudaStream_t>(stream));
   });
   if (rc != PKA_OK) return rc;
   p->latent = true;
@@ -404,7 +404,7 @@ int batch_latent_prefill_run(const pka_prefill_plan* p, const void* q, int64_t q
   if (p->tiles.empty()) return PKA_OK;
   CUtensorMap qmap, kmap, rmap, vmap;
   const uint64_t H = (uint64_t)p->Hq, nk = (uint64_t)p->total_kv;
-  const uint32_t qbox[3] = {64, 1, 128}, kbox[3] = {64, 1, 64};
+  const uint32_t qbox[3] = {64, 1, 128}, kbox[3] = {64, 1, 32}, vbox[3] = {64, 1, 64};
   {
     const uint64_t dims[3] = {192, H, (uint64_t)p->total_q};
     const uint64_t strides[2] = {(uint64_t)q_stride_head * 2, (uint64_t)q_stride_tok * 2};
@@ -416,7 +416,7 @@ int batch_latent_prefill_run(const pka_prefill_plan* p, const void* q, int64_t q
     const uint64_t strides[2] = {(uint64_t)kv_stride_head * 2, (uint64_t)kv_stride_tok * 2};
     rc = encode_bf16_map(&kmap, k_nope, 3, dims, strides, kbox);
     if (rc != PKA_OK) return rc;
-    rc = encode_bf16_map(&vmap, v, 3, dims, strides, kbox);
+    rc = encode_bf16_map(&vmap, v, 3, dims, strides, vbox);
     if (rc != PKA_OK) return rc;
   }
   {

@@ -79,7 +79,14 @@ namespace pka {
 // entry per packed query row), nullptr with the other masks.
 int build_prefill_plan(pka_prefill_plan& plan, const pka_prefill_desc& desc, const int32_t* qo,
                        const int32_t* kv, const int32_t* win_lo = nullptr,
-                       const int32_t* win_hi = nullptr);
+                       const int32_t* win_hi = nullptr, int32_t tile_q = 128,
+                       bool by_head = false);
+
+// Builds a packed prefill plan of tiles of tile_q rows and, unless it is a
+// host-only one, uploads it (batch_prefill_plan: 128, not by head).
+int make_prefill_plan(pka_prefill_plan** plan_out, const pka_prefill_desc& desc, const int32_t* qo,
+                      const int32_t* kv, int32_t tile_q, bool by_head, int32_t* num_tiles_out,
+                      cudaStream_t stream);
 
 // Launches the prefill kernel (one query head and 128 rows per CTA, 64-key
 // tiles; head_dim 128 or 256) over the plan's tiles.

@@ -15,12 +15,13 @@
 namespace pka {
 
 namespace {
-constexpr int kTileQ = 128;     // query rows per CTA
 constexpr int kTileK = 64;      // keys per K/V tile
 }  // namespace
 
 int build_prefill_plan(pka_prefill_plan& p, const pka_prefill_desc& d_in, const int32_t* qo,
-                       const int32_t* kv, const int32_t* win_lo, const int32_t* win_hi) {
+                       const int32_t* kv, const int32_t* win_lo, const int32_t* win_hi,
+                       int32_t tile_q, bool by_head) {
+  const int64_t kTileQ = tile_q;   // query rows per tile
   pka_prefill_desc d = d_in;
   PKA_CHECK_ARG(qo != nullptr && kv != nullptr, "qo_indptr_host and kv_indptr_host are required");
   PKA_CHECK_ARG(d.batch_size >= 1, "batch_size must be >= 1");
@@ -158,8 +159,19 @@ int build_prefill_plan(pka_prefill_plan& p, const pka_prefill_desc& d_in, const 
                                       (int32_t)lk});
     }
   }
-  std::stable_sort(p.tiles.begin(), p.tiles.end(),
-                   [](const PrefillTile& a, const PrefillTile& b) { return a.n_kv > b.n_kv; });
+  // Heaviest first.  By head (every query head has keys of its own): the tiles of
+  // one request and head side by side, heaviest first among them, so that they run
+  // at the same time and read their keys from HBM once; longest request first, so
+  // that the short ones fill the end.
+  if (by_head)
+    std::stable_sort(p.tiles.begin(), p.tiles.end(), [](const PrefillTile& a, const PrefillTile& b) {
+      if (a.lk != b.lk) return a.lk > b.lk;
+      if (a.k0 != b.k0) return a.k0 < b.k0;
+      return a.head != b.head ? a.head < b.head : a.n_kv > b.n_kv;
+    });
+  else
+    std::stable_sort(p.tiles.begin(), p.tiles.end(),
+                     [](const PrefillTile& a, const PrefillTile& b) { return a.n_kv > b.n_kv; });
   p.total_q = qo[B];
   p.total_kv = kv[B];
   PKA_CHECK_ARG(p.tiles.size() < (size_t)INT32_MAX, "too many prefill tiles");

@@ -142,7 +142,7 @@ def test_prefill_plan_rejects(kw, code):
 def test_prefill_plan_tiles():
     plan = api.batch_latent_prefill_plan([0, 300, 300, 310], [0, 300, 300, 400], num_heads=4,
                                          host_only=True)
-    assert plan.num_tiles == (3 + 1) * 4
+    assert plan.num_tiles == (2 + 1) * 4        # 256 rows of one head each
     with pytest.raises(ValueError, match="same length"):
         api.batch_latent_prefill_plan([0, 3], [0, 3, 4], num_heads=1, host_only=True)
 
