@@ -81,6 +81,20 @@ __device__ __forceinline__ void bar_sync_group(int g) {
   asm volatile("bar.sync %0, 128;" ::"r"(g + 1) : "memory");
 }
 
+// The same, true where `mine` is true in any thread of the group.
+__device__ __forceinline__ bool bar_any_group(int g, bool mine) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %2, 0;\n\t"
+      "barrier.cta.red.or.pred q, %1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"(g + 1), "r"((uint32_t)mine)
+      : "memory");
+  return any != 0;
+}
+
 // Max or sum over the eight lanes that share lane % 4, of C values each.  The
 // lanes trade halves, so that each ends with C / 8 (at least one) totals: value
 // index first_value(lane) on.
@@ -469,10 +483,14 @@ latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant
         m[q] = neg_inf();
         l[q] = 0.f;
       }
+      bool gave_up = false;
       bar_sync_group(g);
       for (int j = 0; j < pc.n; ++j, ++T) {
         const int key0 = (pc.tile0 + j) * kLatentTile;
-        if (!warp_wait(bar(L_SFULL + (T & 1)), (uint32_t)((T >> 1) & 1), a.status)) s_fail[T & 1] = 1;
+        if (!warp_wait(bar(L_SFULL + (T & 1)), (uint32_t)((T >> 1) & 1), a.status)) {
+          s_fail[T & 1] = 1;
+          gave_up = true;
+        }
         tc_fence_after();
         uint32_t s[NG / 2];
         const uint32_t s_tm = tmem + lane_off + G::kColS + (uint32_t)(T & 1) * N + (uint32_t)gc;
@@ -493,40 +511,45 @@ latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant
               if (k + 8 >= seen) x[4 * jj + 2 + e] = neg_inf();
             }
         }
-        // row maxima over the tile's 64 keys: lanes, then warps
-        float mx[C];
+        // Lazy rescale: the reference of a row moves only when a score is more than
+        // 2^8 above it, so most tiles need no maximum at all, just the word of every
+        // thread of the group that none of its scores is.
+        bool grow = gave_up;
 #pragma unroll
-        for (int q = 0; q < C; ++q)
-          mx[q] = fmaxf(x[4 * (q >> 1) + (q & 1)], x[4 * (q >> 1) + 2 + (q & 1)]);
-        reduce_rows<C>(mx, lane, [](float u, float v) { return fmaxf(u, v); });
-        float* wm = g_max + (T & 1) * 4 * NG;
-        wm[quad * NG + (lane & 3) * C + first_value<C>(lane)] = mx[0];
-        bar_sync_group(g);
-        if (s_fail[T & 1]) {
-          ok = false;
-          break;
+        for (int q = 0; q < C; ++q) {
+          const float top = fmaxf(x[4 * (q >> 1) + (q & 1)], x[4 * (q >> 1) + 2 + (q & 1)]);
+          grow = grow || top > m[q] + kRescaleThreshold;
         }
-#pragma unroll
-        for (int q = 0; q < C; q += 4) {
-          float4 u = *reinterpret_cast<const float4*>(wm + (lane & 3) * C + q);
-#pragma unroll
-          for (int w = 1; w < 4; ++w) {
-            const float4 v = *reinterpret_cast<const float4*>(wm + w * NG + (lane & 3) * C + q);
-            u = make_float4(fmaxf(u.x, v.x), fmaxf(u.y, v.y), fmaxf(u.z, v.z), fmaxf(u.w, v.w));
+        if (bar_any_group(g, grow)) {
+          if (s_fail[T & 1]) {
+            ok = false;
+            break;
           }
-          mx[q] = u.x;
-          mx[q + 1] = u.y;
-          mx[q + 2] = u.z;
-          mx[q + 3] = u.w;
-        }
-        // lazy rescale: the reference moves only when a maximum grew by more than
-        // 2^8.  Every warp of the group holds the same maxima, so all decide alike.
-        bool grow = false;
+          // row maxima over the tile's 64 keys: lanes, then warps
+          float mx[C];
 #pragma unroll
-        for (int q = 0; q < C; ++q) grow = grow || mx[q] > m[q] + kRescaleThreshold;
-        if (__any_sync(0xffffffffu, grow)) {
-          // a row without visible keys so far still has O = 0 and l = 0 and takes
-          // its first reference without a rescale
+          for (int q = 0; q < C; ++q)
+            mx[q] = fmaxf(x[4 * (q >> 1) + (q & 1)], x[4 * (q >> 1) + 2 + (q & 1)]);
+          reduce_rows<C>(mx, lane, [](float u, float v) { return fmaxf(u, v); });
+          float* wm = g_max + (T & 1) * 4 * NG;
+          wm[quad * NG + (lane & 3) * C + first_value<C>(lane)] = mx[0];
+          bar_sync_group(g);
+#pragma unroll
+          for (int q = 0; q < C; q += 4) {
+            float4 u = *reinterpret_cast<const float4*>(wm + (lane & 3) * C + q);
+#pragma unroll
+            for (int w = 1; w < 4; ++w) {
+              const float4 v = *reinterpret_cast<const float4*>(wm + w * NG + (lane & 3) * C + q);
+              u = make_float4(fmaxf(u.x, v.x), fmaxf(u.y, v.y), fmaxf(u.z, v.z), fmaxf(u.w, v.w));
+            }
+            mx[q] = u.x;
+            mx[q + 1] = u.y;
+            mx[q + 2] = u.z;
+            mx[q + 3] = u.w;
+          }
+          // Every warp of the group holds the same maxima, so all decide alike.  A row
+          // without visible keys so far still has O = 0 and l = 0 and takes its first
+          // reference without a rescale.
           float al[C];
           bool rescale = false;
 #pragma unroll
@@ -551,15 +574,14 @@ latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant
 #pragma unroll
             for (int q = 0; q < C; ++q) l[q] *= al[q];
 #pragma unroll 1
-            for (int c = 0; c < DL / 128 * NG; c += 16) {
-              uint32_t r[16];
-              const uint32_t o_tm = tmem + lane_off + (uint32_t)(c / NG * N + gc + c % NG);
+            for (int c = 0; c < NB; ++c) {
+              uint32_t r[NG];
+              const uint32_t o_tm = tmem + lane_off + (uint32_t)(c * N + gc);
               tmem_ld16(o_tm, r);
               tmem_wait_ld();
-              reg_fence<16>(r);
+              reg_fence<NG>(r);
 #pragma unroll
-              for (int i = 0; i < 16; ++i)
-                r[i] = __float_as_uint(__uint_as_float(r[i]) * s_col[gc + c % NG + i]);
+              for (int i = 0; i < NG; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * s_col[gc + i]);
               tmem_st16(o_tm, r);
             }
             tmem_wait_st();
@@ -577,8 +599,10 @@ latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant
         }
         // P(T) only once P V(T - 2) is complete (nearly always it is): nobody then
         // waits for a phase of the P and P V barriers that is not the next one
-        if (T >= 2 && !warp_wait(bar(L_PV + (T & 1)), (uint32_t)(((T >> 1) - 1) & 1), a.status))
+        if (T >= 2 && !warp_wait(bar(L_PV + (T & 1)), (uint32_t)(((T >> 1) - 1) & 1), a.status)) {
           s_fail[(T + 1) & 1] = 1;   // seen behind the next tile's barrier
+          gave_up = true;
+        }
         // it takes the place of the tile's rotary columns
         const uint32_t pb = sbase + (uint32_t)kp.slot * G::kTile + G::kOffR;
         kp.next();
