@@ -687,11 +687,12 @@ typedef struct pka_latent_plan pka_latent_plan; /* opaque latent decode plan */
 
 /* Summary of a latent decode plan. */
 typedef struct pka_latent_plan_info {
-  int32_t num_segments;     /* runs of key tiles: each is one CTA per row block      */
+  int32_t num_segments;     /* runs of key tiles: each is one CTA (a pair of them when
+                               row_tile is 128) per row block                          */
   int32_t num_items;        /* pieces of requests in them                             */
   int32_t num_split;        /* requests cut into more than one piece                  */
-  int32_t row_tile;         /* query rows (token, head) of a CTA: 16, 32 or 64        */
-  int32_t row_blocks;       /* CTAs side by side over a request's rows                */
+  int32_t row_tile;         /* query rows (token, head) of a row block: 16, 32, 64, 128 */
+  int32_t row_blocks;       /* row blocks side by side over a request's rows          */
   int32_t partial_rows;     /* fp32 partial rows in the workspace                     */
   int64_t workspace_bytes;
   int32_t total_q;

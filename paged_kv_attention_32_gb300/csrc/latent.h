@@ -102,6 +102,10 @@ int build_latent_plan(pka_latent_plan& plan, const pka_latent_desc& desc,
 int launch_latent_decode(const pka_latent_plan& plan, const LatentArgs& args, const void* pages,
                          int64_t stride_page, cudaStream_t stream);
 
+// The decode of plans whose row tile is 128, without the merge.
+int launch_latent_decode_pair(const pka_latent_plan& plan, const LatentArgs& args, const void* pages,
+                              int64_t stride_page, cudaStream_t stream);
+
 int launch_kv_tables(const int32_t* kv_lens, const int32_t* new_lens, int32_t batch,
                      const int32_t* free_pages, int32_t num_free, const int32_t* free_head,
                      int32_t page_size, int32_t* tables, int64_t row_stride, int32_t width,

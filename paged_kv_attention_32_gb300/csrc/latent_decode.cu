@@ -9,6 +9,7 @@
 #include "device_common.cuh"
 #include "host_common.h"
 #include "latent.h"
+#include "latent_decode.cuh"
 #include "prefill_softmax.cuh"
 #include "tcgen05.cuh"
 #include "tmap.h"
@@ -21,8 +22,6 @@ namespace {
 
 // ---- the decode kernel -----------------------------------------------------------
 
-constexpr float kRescaleThreshold = 8.0f;
-constexpr uint32_t kSmemLimit = 232448;   // dynamic shared memory of one CTA
 
 // Shared memory and TMEM of latent_dim DL with N query rows.  A stage is a tile
 // of 64 keys as blocks of 256 latent dimensions and one of the 64 rotary ones;
@@ -63,38 +62,6 @@ enum {
 };
 static_assert(L_COUNT * 8 + 4 + 48 <= 512, "barriers, TMEM address, failure flags");
 
-// A position in a ring of N slots and the parity of its round.
-template <int N>
-struct Ring {
-  int slot = 0;
-  uint32_t parity = 0;
-  __device__ __forceinline__ void next() {
-    if (++slot == N) {
-      slot = 0;
-      parity ^= 1u;
-    }
-  }
-};
-
-// Barrier of the four warps of softmax group g.
-__device__ __forceinline__ void bar_sync_group(int g) {
-  asm volatile("bar.sync %0, 128;" ::"r"(g + 1) : "memory");
-}
-
-// The same, true where `mine` is true in any thread of the group.
-__device__ __forceinline__ bool bar_any_group(int g, bool mine) {
-  uint32_t any;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %2, 0;\n\t"
-      "barrier.cta.red.or.pred q, %1, 128, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(any)
-      : "r"(g + 1), "r"((uint32_t)mine)
-      : "memory");
-  return any != 0;
-}
-
 // Max or sum over the eight lanes that share lane % 4, of C values each.  The
 // lanes trade halves, so that each ends with C / 8 (at least one) totals: value
 // index first_value(lane) on.
@@ -125,24 +92,6 @@ __device__ __forceinline__ int first_value(int lane) {
 
 struct LatentMaps {
   CUtensorMap pool, pool_rope, q, q_rope;
-};
-
-// What a CTA needs to know of its piece.
-struct Piece {
-  LatentReq rq;
-  int request, kv, tile0, n, part, row0, rows;   // rows: live rows of the CTA's row block
-  __device__ __forceinline__ Piece(const LatentArgs& a, int item, int row_block, int row_tile) {
-    const LatentItem it = a.items[item];
-    rq = a.reqs[it.request];
-    request = it.request;
-    part = it.part;
-    kv = rq.kv_len;
-    if (a.seq_lens_live != nullptr) kv = min(max(__ldg(a.seq_lens_live + request), 0), kv);
-    row0 = row_block * row_tile;
-    rows = min(row_tile, rq.q_len * a.num_heads - row0);
-    tile0 = it.tile_lo;
-    n = rows > 0 ? max(0, min(it.tile_hi, (kv + kLatentTile - 1) / kLatentTile) - tile0) : 0;
-  }
 };
 
 // Four values of each of 16 columns: r[i] of lane d holds column i of dimension
@@ -774,6 +723,11 @@ int launch(const pka_latent_plan& plan, const LatentArgs& a, const LatentMaps& m
                   : plan.row_tile == 32 ? launch_tiles<DL, 32, F16>(a, maps, stream)
                                         : launch_tiles<DL, 64, F16>(a, maps, stream);
   if (e != cudaSuccess) return cuda_fail(e, "latent_decode_kernel launch");
+  return PKA_OK;
+}
+
+template <int DL>
+int launch_merge(const pka_latent_plan& plan, const LatentArgs& a, cudaStream_t stream) {
   if (a.num_splits > 0) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(a.num_splits * a.max_rows), plan.max_parts > kFewPieces ? DL / 128 : 1);
@@ -784,7 +738,7 @@ int launch(const pka_latent_plan& plan, const LatentArgs& a, const LatentMaps& m
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, latent_merge_kernel<DL>, a);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, latent_merge_kernel<DL>, a);
     if (e != cudaSuccess) return cuda_fail(e, "latent_merge_kernel launch");
   }
   return PKA_OK;
@@ -792,9 +746,10 @@ int launch(const pka_latent_plan& plan, const LatentArgs& a, const LatentMaps& m
 
 }  // namespace
 
-int launch_latent_decode(const pka_latent_plan& plan, const LatentArgs& args, const void* pages,
-                         int64_t stride_page, cudaStream_t stream) {
-  if (args.num_items == 0) return PKA_OK;
+namespace {
+
+int launch_single(const pka_latent_plan& plan, const LatentArgs& args, const void* pages,
+                  int64_t stride_page, cudaStream_t stream) {
   LatentArgs a = args;
   // The pool as (64 columns, slot in 8, column chunk, slot / 8, page): one box of
   // box_rows rows and four chunks (one for the rotary columns) lands as groups of
@@ -834,6 +789,18 @@ int launch_latent_decode(const pka_latent_plan& plan, const LatentArgs& args, co
   if (plan.desc.latent_dim == 512)
     return f16 ? launch<512, true>(plan, a, maps, stream) : launch<512, false>(plan, a, maps, stream);
   return f16 ? launch<256, true>(plan, a, maps, stream) : launch<256, false>(plan, a, maps, stream);
+}
+
+}  // namespace
+
+int launch_latent_decode(const pka_latent_plan& plan, const LatentArgs& a, const void* pages,
+                         int64_t stride_page, cudaStream_t stream) {
+  if (a.num_items == 0) return PKA_OK;
+  const int rc = plan.row_tile == 128 ? launch_latent_decode_pair(plan, a, pages, stride_page, stream)
+                                      : launch_single(plan, a, pages, stride_page, stream);
+  if (rc != PKA_OK) return rc;
+  return plan.desc.latent_dim == 512 ? launch_merge<512>(plan, a, stream)
+                                     : launch_merge<256>(plan, a, stream);
 }
 
 }  // namespace pka

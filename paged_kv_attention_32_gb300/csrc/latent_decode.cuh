@@ -1,0 +1,64 @@
+// What the latent decode kernels share.
+#pragma once
+
+#include "device_common.cuh"
+#include "latent.h"
+
+namespace pka {
+namespace dev {
+
+constexpr float kRescaleThreshold = 8.0f;
+constexpr uint32_t kSmemLimit = 232448;   // dynamic shared memory of one CTA
+
+// A position in a ring of N slots and the parity of its round.
+template <int N>
+struct Ring {
+  int slot = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == N) {
+      slot = 0;
+      parity ^= 1u;
+    }
+  }
+};
+
+// Barrier of the four warps of softmax group g.
+__device__ __forceinline__ void bar_sync_group(int g) {
+  asm volatile("bar.sync %0, 128;" ::"r"(g + 1) : "memory");
+}
+
+// The same, true where `mine` is true in any thread of the group.
+__device__ __forceinline__ bool bar_any_group(int g, bool mine) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %2, 0;\n\t"
+      "barrier.cta.red.or.pred q, %1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"(g + 1), "r"((uint32_t)mine)
+      : "memory");
+  return any != 0;
+}
+
+// What a CTA needs to know of its piece.
+struct Piece {
+  LatentReq rq;
+  int request, kv, tile0, n, part, row0, rows;   // rows: live rows of the CTA's row block
+  __device__ __forceinline__ Piece(const LatentArgs& a, int item, int row_block, int row_tile) {
+    const LatentItem it = a.items[item];
+    rq = a.reqs[it.request];
+    request = it.request;
+    part = it.part;
+    kv = rq.kv_len;
+    if (a.seq_lens_live != nullptr) kv = min(max(__ldg(a.seq_lens_live + request), 0), kv);
+    row0 = row_block * row_tile;
+    rows = min(row_tile, rq.q_len * a.num_heads - row0);
+    tile0 = it.tile_lo;
+    n = rows > 0 ? max(0, min(it.tile_hi, (kv + kLatentTile - 1) / kLatentTile) - tile0) : 0;
+  }
+};
+
+}  // namespace dev
+}  // namespace pka

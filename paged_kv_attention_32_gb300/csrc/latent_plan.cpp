@@ -1,9 +1,9 @@
 // Host planner of the latent decode.
 //
 // All heads of a request read the same cached row, so a CTA takes a block of
-// up to 64 query rows (token, head) and streams keys past them.  Key tiles of
-// 64 are dealt to num_sms / row_blocks segments of equal cost, each one CTA
-// per row block for the whole run: requests are laid end to end and cut where a
+// up to 64 query rows (token, head), a pair of CTAs one of 128, and streams keys
+// past them.  Key tiles of 64 are dealt to as many segments of equal cost as there
+// are CTAs (pairs) per row block, each one of them for the whole run: requests are laid end to end and cut where a
 // segment is full, so at most two pieces of a segment belong to requests that
 // are cut, whatever the lengths.  A piece costs its tiles plus a fixed part
 // (its queries in, its output out).  The pieces of a cut request meet in a
@@ -93,11 +93,12 @@ int build_latent_plan(pka_latent_plan& p, const pka_latent_desc& d_in, const int
                 (long long)max_rows, kMaxRows);
   p.total_q = indptr == nullptr ? B * d.q_len : indptr[B];
   p.max_rows = (int32_t)max_rows;
-  p.row_tile = max_rows <= 16 ? 16 : max_rows <= 32 ? 32 : 64;
+  // up to 64 rows a CTA; more go to pairs of CTAs with 64 rows each
+  p.row_tile = max_rows <= 16 ? 16 : max_rows <= 32 ? 32 : max_rows <= 64 ? 64 : 128;
   p.row_blocks = (int32_t)std::max<int64_t>(1, ceil_div(max_rows, p.row_tile));
 
   // ---- segments: the smallest equal cost that fits the CTAs at hand ----
-  const int64_t max_segments = std::max(1, d.num_sms / p.row_blocks);
+  const int64_t max_segments = std::max(1, d.num_sms / (p.row_blocks * (p.row_tile == 128 ? 2 : 1)));
   int64_t target = std::max(ceil_div(cost, max_segments), kMinPiece + kItemCost);
   while (true) {
     p.items.clear();

@@ -268,7 +268,7 @@ def test_decode_split_over_the_length(num_sms, heads, dl):
 
 
 @pytest.mark.parametrize("live", [[2000, 5, 64], [1, 0, 63], [1999, 900, 0], [640, 128, 1]])
-@pytest.mark.parametrize("heads", [16, 64])
+@pytest.mark.parametrize("heads", [16, 64, 128])
 def test_decode_live_lengths(live, heads):
     check_decode([2000, 900, 64], [1] * 3, heads, live=live)
 
@@ -283,15 +283,31 @@ def test_decode_live_lengths_outside_the_plan_are_clamped():
     assert_within(out, lse, ref_decode(q, pages, table, [100, 0], [0, 1, 2], 512, 0.04, False, 1.0, BF))
 
 
+@pytest.mark.parametrize("heads", [16, 64])   # 32 and 128 rows a request
 @pytest.mark.parametrize("scale", [0.0, -0.05, 1.0, 40.0])
-def test_decode_scales(scale):
-    check_decode([1, 300, 77], [2] * 3, 16, scale=scale, causal=True, dl=256)
+def test_decode_scales(scale, heads):
+    check_decode([1, 300, 77], [2] * 3, heads, scale=scale, causal=True, dl=256)
 
 
-def test_decode_growing_scores_rescale_the_output():
+@pytest.mark.parametrize("heads,q_lens,dtype,out_dtype,dl,ps", [
+    (40, [2, 2, 2], BF, FP, 512, 8),          # 80 rows: the second CTA of a pair nearly empty
+    (33, [4, 4, 4], HF, BF, 256, 24),         # queries by plain loads, 132 rows: two row blocks
+    (130, [1, 1, 1], HF, HF, 512, 32),
+    (128, [3, 3, 3], BF, BF, 512, 256),       # three row blocks
+    (1024, [1, 1, 1], BF, HF, 256, 16),
+])
+def test_decode_many_rows(heads, q_lens, dtype, out_dtype, dl, ps):
+    check_decode([500, 63, 1], q_lens, heads, dl=dl, ps=ps, dtype=dtype, out_dtype=out_dtype,
+                 causal=True, out_scale=0.5)
+    check_decode([500, 64, 0], q_lens, heads, dl=dl, ps=ps, dtype=dtype, out_dtype=out_dtype,
+                 live=[401, 1, 0], num_sms=20)
+
+
+@pytest.mark.parametrize("heads", [16, 48, 100])
+def test_decode_growing_scores_rescale_the_output(heads):
     """Each key tile's scores tower over the last one's, so that every tile moves the
     running maximum and rescales what was summed before."""
-    kv, heads, dl = [1500], 16, 512
+    kv, dl = [1500], 512
     q, pages, table = decode_inputs(kv, [0, 1], heads, dl, 16, BF)
     d = torch.randn(dl + 64, device=DEV)
     d /= d.norm()
@@ -309,8 +325,9 @@ def test_decode_growing_scores_rescale_the_output():
         assert_within(out, lse, ref_decode(q, pages, table, kv, [0, 1], dl, 0.5, False, 1.0, BF))
 
 
-def test_decode_strided_arguments_and_rows_behind_the_batch():
-    kv, heads, dl, D = [90, 200], 12, 256, 320
+@pytest.mark.parametrize("heads", [12, 24, 70, 72])
+def test_decode_strided_arguments_and_rows_behind_the_batch(heads):
+    kv, dl, D = [90, 200], 256, 320
     q, pages, table = decode_inputs(kv, [0, 1, 2], heads, dl, 16, HF)
     qw = torch.zeros((4, heads, 3, D), dtype=HF, device=DEV)
     qw[:2, :, 1] = q
@@ -330,11 +347,12 @@ def test_decode_strided_arguments_and_rows_behind_the_batch():
     assert bool((out[2:] == 7).all()) and bool((lse[2:] == 7).all())
 
 
-def test_decode_bad_pages_read_as_zeros():
-    q, pages, table = decode_inputs([64, 64], [0, 1, 2], 16, 256, 16, BF, junk=0.0)
+@pytest.mark.parametrize("heads", [16, 80])
+def test_decode_bad_pages_read_as_zeros(heads):
+    q, pages, table = decode_inputs([64, 64], [0, 1, 2], heads, 256, 16, BF, junk=0.0)
     clean = table.clone()
     table[0, 1], table[1, 2] = pages.shape[0], -3
-    plan = api.paged_latent_decode_plan([64, 64], num_heads=16, page_size=16, scale=0.05,
+    plan = api.paged_latent_decode_plan([64, 64], num_heads=heads, page_size=16, scale=0.05,
                                         max_pages_per_seq=table.shape[1], latent_dim=256,
                                         num_pages=pages.shape[0], return_lse=True)
     out, lse = api.paged_latent_decode_run(plan, q, pages, table)
@@ -345,7 +363,8 @@ def test_decode_bad_pages_read_as_zeros():
                                        1.0, BF))
 
 
-def test_decode_pool_offsets_past_32_bits():
+@pytest.mark.parametrize("heads", [16, 128])
+def test_decode_pool_offsets_past_32_bits(heads):
     ps, D = 64, 576
     n_pages = 2 ** 32 // (ps * D) + 10
     pages = torch.full((n_pages, ps, D), float("nan"), dtype=BF, device=DEV)
@@ -353,18 +372,19 @@ def test_decode_pool_offsets_past_32_bits():
     for p in ids:
         pages[p] = torch.randn((ps, D), device=DEV).to(BF)
     table = i32([ids])
-    q = torch.randn((1, 16, D), device=DEV).to(BF)
-    plan = api.paged_latent_decode_plan([180], num_heads=16, page_size=ps, max_pages_per_seq=3,
+    q = torch.randn((1, heads, D), device=DEV).to(BF)
+    plan = api.paged_latent_decode_plan([180], num_heads=heads, page_size=ps, max_pages_per_seq=3,
                                         num_pages=n_pages, scale=0.04, return_lse=True)
     out, lse = api.paged_latent_decode_run(plan, q, pages, table)
     plan.check()
     assert_within(out, lse, ref_decode(q, pages, table, [180], [0, 1], 512, 0.04, False, 1.0, BF))
 
 
-def test_decode_gives_the_same_bits_again_and_in_two_streams():
+@pytest.mark.parametrize("heads", [32, 128])
+def test_decode_gives_the_same_bits_again_and_in_two_streams(heads):
     kv = [4000, 17, 900]
-    q, pages, table = decode_inputs(kv, [0, 1, 2, 3], 32, 512, 16, BF)
-    plan = api.paged_latent_decode_plan(kv, num_heads=32, page_size=16, scale=0.04,
+    q, pages, table = decode_inputs(kv, [0, 1, 2, 3], heads, 512, 16, BF)
+    plan = api.paged_latent_decode_plan(kv, num_heads=heads, page_size=16, scale=0.04,
                                         max_pages_per_seq=table.shape[1],
                                         num_pages=pages.shape[0], return_lse=True)
     first = api.paged_latent_decode_run(plan, q, pages, table)

@@ -34,9 +34,10 @@ def test_pieces_cover_every_request_once(heads, seed):
     items, segs = plan.export()
     inf = plan.info
     rows = max(b - a for a, b in zip(qo, qo[1:])) * heads
-    assert inf["row_tile"] == (16 if rows <= 16 else 32 if rows <= 32 else 64)
+    assert inf["row_tile"] == (16 if rows <= 16 else 32 if rows <= 32 else 64 if rows <= 64 else 128)
     assert inf["row_blocks"] == max(1, -(-rows // inf["row_tile"]))
-    assert inf["num_segments"] <= max(1, 152 // inf["row_blocks"])
+    ctas = inf["row_blocks"] * (2 if inf["row_tile"] == 128 else 1)
+    assert inf["num_segments"] <= max(1, 152 // ctas)
     assert segs[0] == 0 and segs[-1] == len(items) and all(a < b for a, b in zip(segs, segs[1:]))
     at, parts = {}, {}
     for b, lo, hi, part in items:
