@@ -214,12 +214,6 @@ latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant
     for (int item = item0; ok && item < item1; ++item) {
       const Piece pc(a, item, rb, N);
       if (pc.n == 0) continue;
-      const int32_t* table = a.block_tables + (int64_t)pc.request * a.bt_row_stride;
-      // a box past the last token reads as zeros: its page lies outside the pool
-      auto page_of = [&](int tok) {
-        return lane < boxes && tok < pc.kv ? __ldg(table + tok / a.page_size) : a.num_pages;
-      };
-      const int tok0 = pc.tile0 * kLatentTile + lane * a.box_rows;
       if (a.q_box > 0) {   // whole groups of 8 heads: the queries come by TMA too
         if (I > 0 && !(ok = warp_wait(bar(L_QFREE), (uint32_t)((I - 1) & 1), a.status))) break;
         if (lane == 0) mbar_arrive_expect_tx(bar(L_QFULL), G::kQ);
@@ -235,11 +229,10 @@ latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant
         __syncwarp();
       }
       ++I;
-      int next = page_of(tok0);
+      PageWalk walk(a, pc, lane * a.box_rows, lane < boxes);
       for (int j = 0; j < pc.n; ++j) {
-        const int tok = tok0 + j * kLatentTile, page = next;
-        next = page_of(tok + kLatentTile);
-        const int slot8 = tok % a.page_size / 8;
+        const int page = walk.page, slot8 = walk.slot / 8;
+        walk.next_tile();
         const uint32_t dst = sbase + (uint32_t)kp.slot * G::kTile;
         for (int h = 0; h <= NH; ++h) {   // blocks in the order P V lets go of them
           const int i = 3 * kp.slot + h;

@@ -60,5 +60,36 @@ struct Piece {
   }
 };
 
+// The page and slot of one token of every tile of a piece, 64 tokens apart: no
+// division per tile, and the next tile's table entry is asked for a tile ahead.
+// A token past the request's last is in page num_pages, outside the pool: a copy
+// from there brings zeros.
+struct PageWalk {
+  const int32_t* table;
+  int page, slot;                       // of the current tile's token
+  int tok, idx, kv, ps, step_pages, step_slots, none;
+  bool in;
+  __device__ __forceinline__ PageWalk(const LatentArgs& a, const Piece& pc, int offset, bool active)
+      : table(a.block_tables + (int64_t)pc.request * a.bt_row_stride), tok(pc.tile0 * kLatentTile + offset),
+        kv(pc.kv), ps(a.page_size), none(a.num_pages), in(active) {
+    idx = tok / ps;
+    slot = tok - idx * ps;
+    step_pages = kLatentTile / ps;
+    step_slots = kLatentTile - step_pages * ps;
+    page = entry();
+  }
+  __device__ __forceinline__ int entry() const { return in && tok < kv ? __ldg(table + idx) : none; }
+  __device__ __forceinline__ void next_tile() {
+    tok += kLatentTile;
+    idx += step_pages;
+    slot += step_slots;
+    if (slot >= ps) {
+      slot -= ps;
+      ++idx;
+    }
+    page = entry();
+  }
+};
+
 }  // namespace dev
 }  // namespace pka

@@ -13,10 +13,11 @@
 // pair 25, N=256 64.  The two halves overlap in a quarter of the tile, which
 // comes twice (from L2).
 // Each CTA's warps:
-//   0  copies of its own halves; the tile that holds the last key it clears past
-//      it in the values (0 * inf is not 0) before handing it over;
+//   0  copies queries and its half of the keys;   3  its half of the values, which
+//      in the tile that holds the last key it clears past it (0 * inf is not 0)
+//      before handing it over (one warp for both was what bounded the pair);
 //   1  in the leader: issues S for both CTAs;   2  in the leader: issues P V;
-//   3-6  softmax and output: TMEM lane i of a CTA is row i % 64, and lanes of
+//   4-7  softmax and output: TMEM lane i of a CTA is row i % 64, and lanes of
 //      64 on hold the second half of a tile's keys, of each 256 dimensions.
 // TMEM columns: O blocks of 256 dimensions (128 each), then two S buffers (32).
 #include <algorithm>
@@ -38,7 +39,7 @@ using namespace dev;
 
 namespace {
 
-constexpr int kThreads = 224;
+constexpr int kThreads = 256;
 constexpr int kRows = 64;   // query rows of a CTA
 
 template <int DL>
@@ -77,6 +78,14 @@ enum {
 };
 static_assert(R_COUNT * 8 + 4 + 12 <= 256, "barriers, TMEM address, failure flags");
 
+// When a wait gave up, copies still in flight land before the cluster leaves:
+// their barriers may be the other CTA's, so there is only time to go by.
+__device__ __forceinline__ void let_copies_land() {
+  const uint64_t t0 = global_timer_ns();
+  while (global_timer_ns() - t0 < 1000000ull) {
+  }
+}
+
 __device__ __forceinline__ bool warp_wait_pair(uint32_t bar, uint32_t parity, int32_t* status) {
   return __all_sync(0xffffffffu, mbar_wait_cluster(bar, parity, status));
 }
@@ -105,7 +114,7 @@ latent_decode_pair_kernel(const __grid_constant__ LatentArgs a, const __grid_con
 
   if (tid == 0) {
     for (int s = 0; s < 4; ++s) {
-      mbar_init(bar(R_KFULL + s), 2);
+      mbar_init(bar(R_KFULL + s), 1);   // the leader expects both CTAs' bytes
       mbar_init(bar(R_KEMPTY + s), 1);
       mbar_init(bar(R_VFULL + s), 2);
       mbar_init(bar(R_VEMPTY + s), 1);
@@ -115,7 +124,7 @@ latent_decode_pair_kernel(const __grid_constant__ LatentArgs a, const __grid_con
       mbar_init(bar(R_PFULL + s), 8);   // one arrival per softmax warp of the pair
       mbar_init(bar(R_PV + s), 1);
     }
-    mbar_init(bar(R_QFULL), a.q_box > 0 ? 2 : 8);
+    mbar_init(bar(R_QFULL), a.q_box > 0 ? 1 : 8);
     mbar_init(bar(R_QFREE), 1);
     mbar_init(bar(R_OFREE), 8);
     mbar_init(bar(R_SDONE), 1);
@@ -134,26 +143,18 @@ latent_decode_pair_kernel(const __grid_constant__ LatentArgs a, const __grid_con
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   if (warp == 0) {
-    // ---------------- TMA producer: lane i copies box i ----------------
-    if (lane < 3) tma_prefetch_desc(lane == 0 ? &maps.keys : lane == 1 ? &maps.values : &maps.q);
-    const int krows = min(a.box_rows, 32);   // cache rows of a key box
-    const int kboxes = 32 / krows, vboxes = kLatentTile / a.box_rows;
-    Ring<NS> kp, vp;
-    int nk = 0, nv = 0, I = 0, tails = 0;   // stages filled so far, pieces, cleared tiles
+    // ---------------- queries and keys: lane i copies box i ----------------
+    if (lane < 2) tma_prefetch_desc(lane == 0 ? &maps.keys : &maps.q);
+    const int krows = min(a.box_rows, 32), boxes = 32 / krows;   // cache rows of a key box
+    Ring<NS> kp;
+    int nk = 0, I = 0;   // stages filled so far, pieces
     bool ok = true;
     for (int item = item0; ok && item < item1; ++item) {
       const Piece pc(a, item, rb, 2 * kRows);
       if (pc.n == 0) continue;
-      const int32_t* table = a.block_tables + (int64_t)pc.request * a.bt_row_stride;
-      // a box past the last token reads as zeros: its page lies outside the pool
-      auto page_of = [&](int tok, int boxes) {
-        return lane < boxes && tok < pc.kv ? __ldg(table + tok / a.page_size) : a.num_pages;
-      };
-      const int tok_k = pc.tile0 * kLatentTile + (int)rank * 32 + lane * krows;
-      const int tok_v = pc.tile0 * kLatentTile + lane * a.box_rows;
       if (a.q_box > 0) {   // whole groups of 8 heads: the queries come by TMA too
         if (I > 0 && !(ok = warp_wait(bar(R_QFREE), (uint32_t)((I - 1) & 1), a.status))) break;
-        if (lane == 0) mbar_arrive_expect_tx_cluster(lead(R_QFULL), G::kQ);
+        if (lane == 0 && rank == 0) mbar_arrive_expect_tx(bar(R_QFULL), 2 * G::kQ);
         __syncwarp();
         if (lane < kRows / a.q_box) {   // rows past the request's last are copied, and never stored
           const int r = pc.row0 + (int)rank * kRows + lane * a.q_box;
@@ -163,41 +164,52 @@ latent_decode_pair_kernel(const __grid_constant__ LatentArgs a, const __grid_con
         __syncwarp();
       }
       ++I;
-      int next_k = page_of(tok_k, kboxes), next_v = page_of(tok_v, vboxes);
-      auto load_k = [&](int j) -> bool {
-        const int tok = tok_k + j * kLatentTile, page = next_k;
-        next_k = page_of(tok + kLatentTile, kboxes);
-        if (nk >= NS && !warp_wait(bar(R_KEMPTY + kp.slot), kp.parity ^ 1u, a.status)) return false;
-        const uint32_t full = lead(R_KFULL + kp.slot);
-        if (lane == 0) mbar_arrive_expect_tx_cluster(full, G::kK);
+      PageWalk walk(a, pc, (int)rank * 32 + lane * krows, lane < boxes);
+      for (int j = 0; j < pc.n; ++j) {
+        const int page = walk.page, slot8 = walk.slot / 8;
+        walk.next_tile();
+        if (nk >= NS && !(ok = warp_wait(bar(R_KEMPTY + kp.slot), kp.parity ^ 1u, a.status))) break;
+        if (lane == 0 && rank == 0) mbar_arrive_expect_tx(bar(R_KFULL + kp.slot), 2 * G::kK);
         __syncwarp();
-        if (lane < kboxes)
+        if (lane < boxes)
           tma_load_5d_pair(sbase + G::kOffK + (uint32_t)kp.slot * G::kK + (uint32_t)(lane * krows / 8) * G::kGroup,
-                           &maps.keys, full, 0, 0, 0, tok % a.page_size / 8, page);
+                           &maps.keys, lead(R_KFULL + kp.slot), 0, 0, 0, slot8, page);
         __syncwarp();
         kp.next();
         ++nk;
-        return true;
-      };
-      auto load_v = [&](int j) -> bool {
-        const int tok = tok_v + j * kLatentTile, page = next_v;
-        next_v = page_of(tok + kLatentTile, vboxes);
-        if (nv >= NS && !warp_wait(bar(R_VEMPTY + vp.slot), vp.parity ^ 1u, a.status)) return false;
+      }
+    }
+    if (!ok) let_copies_land();
+  } else if (warp == 3) {
+    // ---------------- values: lane i copies box i ----------------
+    if (lane == 0) tma_prefetch_desc(&maps.values);
+    const int boxes = kLatentTile / a.box_rows;
+    Ring<NS> vp;
+    int nv = 0, tails = 0;   // stages filled so far, cleared tiles
+    bool ok = true;
+    for (int item = item0; ok && item < item1; ++item) {
+      const Piece pc(a, item, rb, 2 * kRows);
+      if (pc.n == 0) continue;
+      PageWalk walk(a, pc, lane * a.box_rows, lane < boxes);
+      for (int j = 0; j < pc.n; ++j) {
+        const int page = walk.page, slot8 = walk.slot / 8;
+        walk.next_tile();
+        if (nv >= NS && !(ok = warp_wait(bar(R_VEMPTY + vp.slot), vp.parity ^ 1u, a.status))) break;
         const uint32_t off = G::kOffV + (uint32_t)vp.slot * G::kV, full = lead(R_VFULL + vp.slot);
         const int live = pc.kv - (pc.tile0 + j) * kLatentTile;
         const bool tail = live < kLatentTile;
         const uint32_t landed = tail ? map_to_rank(bar(R_TAIL), rank) : full;
         if (lane == 0) mbar_arrive_expect_tx_cluster(landed, G::kV);
         __syncwarp();
-        if (lane < vboxes)
+        if (lane < boxes)
           for (int d = 0; d < ND; ++d)
             tma_load_5d_pair(sbase + off + (uint32_t)d * 16384u + (uint32_t)(lane * a.box_rows / 8) * 2048u,
-                             &maps.values, landed, 0, 0, 4 * d + 2 * (int)rank, tok % a.page_size / 8, page);
+                             &maps.values, landed, 0, 0, 4 * d + 2 * (int)rank, slot8, page);
         __syncwarp();
         if (tail) {
           // rows past the last token may hold anything, and 0 * inf is not 0: clear
           // them to the end of their box (boxes past it brought zeros)
-          if (!warp_wait(bar(R_TAIL), (uint32_t)(tails & 1), a.status)) return false;
+          if (!(ok = warp_wait(bar(R_TAIL), (uint32_t)(tails & 1), a.status))) break;
           ++tails;
           const int end = (live + a.box_rows - 1) / a.box_rows * a.box_rows;
           for (int i = lane; i < (end - live) * ND * 16; i += 32) {
@@ -212,21 +224,9 @@ latent_decode_pair_kernel(const __grid_constant__ LatentArgs a, const __grid_con
         }
         vp.next();
         ++nv;
-        return true;
-      };
-      // order K0 K1 V0 K2 V1 ...
-      for (int j = 0; ok && j < pc.n + 1; ++j) {
-        if (j < pc.n) ok = load_k(j);
-        if (ok && j > 0) ok = load_v(j - 1);
       }
     }
-    // When a wait gave up, copies still in flight land before the cluster leaves:
-    // their barriers may be the other CTA's, so there is only time to go by.
-    if (!ok) {
-      const uint64_t t0 = global_timer_ns();
-      while (global_timer_ns() - t0 < 1000000ull) {
-      }
-    }
+    if (!ok) let_copies_land();
   } else if (warp == 1) {
     // ---------------- the leader's: issues S = Q K^T ----------------
     if (rank == 0) {
@@ -296,7 +296,7 @@ latent_decode_pair_kernel(const __grid_constant__ LatentArgs a, const __grid_con
     const int quad = warp & 3;                      // TMEM lanes 32 quad .. + 31
     const int row = (quad & 1) * 32 + lane, half = quad >> 1;
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
-    const int gt = tid - 96;                        // thread of the four warps
+    const int gt = tid - 128;                       // thread of the four warps
     const float sl2 = a.scale_log2;
 
     // queries by plain loads (heads not a multiple of 8), laid out like keys
