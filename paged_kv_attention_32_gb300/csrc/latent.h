@@ -15,6 +15,7 @@ namespace pka {
 
 constexpr int kLatentTile = 64;        // keys per tile of the latent decode
 constexpr int kLatentRopeDim = 64;
+constexpr int kLatentFewPieces = 8;    // pieces that one CTA merges for a whole row
 
 // A run of key tiles of one request (16 bytes, one aligned load).
 struct LatentItem {
@@ -48,11 +49,12 @@ struct LatentArgs {
   const LatentItem* items;
   const int32_t* segments;       // first item of each segment, then the item count
   const LatentReq* reqs;
-  const int32_t* splits;         // requests cut into several pieces
+  const LatentReq* splits;       // the requests cut into pieces, those of many first
   int32_t* status;
   int32_t num_segments;
   int32_t num_items;
   int32_t num_splits;
+  int32_t num_many;              // of them with more than kLatentFewPieces
   int32_t row_blocks;            // CTAs side by side over a request's rows
   int32_t max_rows;              // the most rows (token, head) of a request
   int32_t num_heads;
@@ -71,19 +73,19 @@ struct LatentArgs {
 struct pka_latent_plan {
   pka_latent_desc desc;       // normalised copy
   int32_t total_q = 0, max_rows = 0, row_tile = 0, row_blocks = 0;
-  int32_t partial_rows = 0, max_parts = 0;
+  int32_t partial_rows = 0, num_many = 0;
   int64_t workspace_bytes = 0;
   int64_t ws_lse_offset = 0;
   std::vector<pka::LatentItem> items;
-  std::vector<int32_t> segments, splits;
-  std::vector<pka::LatentReq> reqs;
+  std::vector<int32_t> segments;
+  std::vector<pka::LatentReq> reqs, splits;
   // one device allocation: items | segments | requests | splits | status word
   void* dev_buf = nullptr;
   size_t dev_capacity = 0;
   const pka::LatentItem* d_items = nullptr;
   const int32_t* d_segments = nullptr;
   const pka::LatentReq* d_reqs = nullptr;
-  const int32_t* d_splits = nullptr;
+  const pka::LatentReq* d_splits = nullptr;
   int32_t* d_status = nullptr;
   int device = -1;
   // pinned host image of dev_buf; stage_done marks when its last upload has read it

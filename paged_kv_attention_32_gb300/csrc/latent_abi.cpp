@@ -37,7 +37,7 @@ int upload_latent_plan(pka_latent_plan& p, cudaStream_t stream) {
   const size_t n_items = p.items.size() * sizeof(LatentItem);
   const size_t n_segs = p.segments.size() * sizeof(int32_t);
   const size_t n_reqs = p.reqs.size() * sizeof(LatentReq);
-  const size_t n_splits = p.splits.size() * sizeof(int32_t);
+  const size_t n_splits = p.splits.size() * sizeof(LatentReq);
   const size_t off_segs = up256(n_items), off_reqs = off_segs + up256(n_segs);
   const size_t off_splits = off_reqs + up256(n_reqs), off_status = off_splits + up256(n_splits);
   const size_t total = off_status + 256;
@@ -62,7 +62,7 @@ int upload_latent_plan(pka_latent_plan& p, cudaStream_t stream) {
   p.d_items = reinterpret_cast<const LatentItem*>(base);
   p.d_segments = reinterpret_cast<const int32_t*>(base + off_segs);
   p.d_reqs = reinterpret_cast<const LatentReq*>(base + off_reqs);
-  p.d_splits = reinterpret_cast<const int32_t*>(base + off_splits);
+  p.d_splits = reinterpret_cast<const LatentReq*>(base + off_splits);
   p.d_status = reinterpret_cast<int32_t*>(base + off_status);
   uint8_t* img = static_cast<uint8_t*>(p.host_stage);
   if (n_items) std::memcpy(img, p.items.data(), n_items);
@@ -330,6 +330,7 @@ int paged_latent_decode_run(const pka_latent_plan* p, const void* q, int64_t q_s
   a.num_segments = (int32_t)p->segments.size() - 1;
   a.num_items = (int32_t)p->items.size();
   a.num_splits = (int32_t)p->splits.size();
+  a.num_many = p->num_many;
   a.row_blocks = p->row_blocks;
   a.max_rows = p->max_rows;
   a.num_heads = d.num_heads;

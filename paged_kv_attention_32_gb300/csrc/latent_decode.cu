@@ -620,81 +620,115 @@ latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant
 }
 
 // The pieces of a cut request: out = sum_c w_c o_c / sum_c w_c with
-// w_c = 2^(lse_c - max).  A CTA of 128 threads takes a row, four values a thread
-// and eight pieces in flight; a row of more than kFewPieces is shared out to
-// DL / 128 CTAs of 128 dimensions whose four warps take every fourth piece.
-// Every warp makes the weights for itself, a piece per lane.  Launched while
-// the decode still runs, it waits for that grid's end.
-constexpr int kFewPieces = 16;
+// w_c = 2^(lse_c - max).  Bound by latency: a chain of dependent loads per row, so
+// little of it and many CTAs an SM.  A row of up to kLatentFewPieces (nearly all) is one
+// CTA's, four values a thread, and every LSE and four pieces at a time are asked for at once.
+// A row of more is shared out to DL / 32 CTAs of 32 dimensions, whose groups of
+// eight threads deal the pieces out; the planner lists such requests first.  Launched
+// while the decode still runs, it waits for that grid's end.
 
 template <int DL>
-__global__ void __launch_bounds__(128)
+__global__ void __launch_bounds__(DL / 4, 1280 / (DL / 4))
 latent_merge_kernel(const __grid_constant__ LatentArgs a) {
-  __shared__ float4 s_o[3][32];
-  const int b = __ldg(a.splits + blockIdx.x / a.max_rows), r = blockIdx.x % a.max_rows;
-  const LatentReq rq = a.reqs[b];
-  const int rows = rq.q_len * a.num_heads, tid = threadIdx.x, lane = tid & 31;
-  const bool shared = rq.n_parts > kFewPieces;
-  const int slab = blockIdx.y;
+  constexpr int T = DL / 4, GROUPS = T / 8, SLABS = DL / 32;
+  __shared__ float4 s_o[GROUPS - 1][8];
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int many_ctas = a.num_many * a.max_rows * SLABS;
+  const bool few = (int)blockIdx.x >= many_ctas;
+  const int slab = few ? 0 : blockIdx.x % SLABS;
+  const int at = few ? a.num_many * a.max_rows + (int)blockIdx.x - many_ctas : blockIdx.x / SLABS;
+  const int r = at % a.max_rows;
+  const LatentReq rq = a.splits[at / a.max_rows];
+  const int rows = rq.q_len * a.num_heads, n = rq.n_parts;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (r >= rows || (!shared && slab > 0) || (!shared && tid >= DL / 4)) return;
-  const int g = shared ? tid >> 5 : 0, step = shared ? 4 : 1;
-  const int x = shared ? slab * 32 + lane : tid;
-  const int64_t p0 = rq.part_base + r;
-  auto lse_of = [&](int c) {
-    return c < rq.n_parts ? __ldcg(a.ws_lse + p0 + (int64_t)c * rows) : neg_inf();
-  };
-  const float first = lse_of(lane);
-  float m = first;
-  for (int c = lane + 32; c < rq.n_parts; c += 32) m = fmaxf(m, lse_of(c));
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-  float sum = 0.f;
+  if (r >= rows) return;
+  const int64_t row = (int64_t)rq.q_start * a.num_heads + r, p0 = (int64_t)rq.part_base + r;
+  const float* lse = a.ws_lse + p0;
+  const int x = few ? tid : slab * 8 + (tid & 7);   // this thread's four dimensions
+  const float4* src = reinterpret_cast<const float4*>(a.ws_o + p0 * DL) + x;
+  float m = neg_inf(), sum = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (m != neg_inf()) {
-    for (int c0 = 0; c0 < rq.n_parts; c0 += 32) {
-      const float w = ex2((c0 == 0 ? first : lse_of(c0 + lane)) - m);   // 0 without keys
-      sum += w;
-      const int n = min(32, rq.n_parts - c0);
-      const float4* src = reinterpret_cast<const float4*>(a.ws_o + (p0 + (int64_t)c0 * rows) * DL) + x;
-      for (int k0 = g; k0 < n; k0 += 8 * step) {
-        float wk[8];
-        float4 v[8];
+  auto add = [&](float w, float4 v) {
+    o.x += w * v.x;
+    o.y += w * v.y;
+    o.z += w * v.z;
+    o.w += w * v.w;
+  };
+  // four pieces c0, c0 + step, ...: a piece without keys (LSE -inf) has no output
+  // rows, what lies there is not used
+  auto lse_of = [&](int c) { return c < n ? __ldcg(lse + (int64_t)c * rows) : neg_inf(); };
+  float s[4];
+  float4 v[4];
+  auto ask = [&](int c0, int step) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int k = k0 + i * step;
-          wk[i] = __shfl_sync(0xffffffffu, w, k & 31);
-          if (k >= n) wk[i] = 0.f;
-          // a piece without keys has no output rows
-          v[i] = wk[i] != 0.f ? __ldcg(src + (int64_t)k * rows * (DL / 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
+    for (int i = 0; i < 4; ++i) {
+      const int c = c0 + i * step;
+      v[i] = c < n ? __ldcg(src + (int64_t)c * rows * T) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  };
+  auto take = [&]() {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          o.x += wk[i] * v[i].x;
-          o.y += wk[i] * v[i].y;
-          o.z += wk[i] * v[i].z;
-          o.w += wk[i] * v[i].w;
-        }
+    for (int i = 0; i < 4; ++i)
+      if (s[i] != neg_inf()) add(ex2(s[i] - m), v[i]);
+  };
+  if (few) {
+    float more[4];   // the LSEs of pieces 4 .. 7
+    ask(0, 1);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[i] = lse_of(i);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) more[i] = lse_of(4 + i);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = fmaxf(m, fmaxf(s[i], more[i]));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      sum += s[i] == neg_inf() ? 0.f : ex2(s[i] - m);
+      sum += more[i] == neg_inf() ? 0.f : ex2(more[i] - m);
+    }
+    take();
+    if (n > 4) {
+      ask(4, 1);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[i] = more[i];
+      take();
+    }
+  } else {
+    const int g = tid >> 3;
+    ask(g, GROUPS);
+    // each warp for itself: four pieces a lane and round, a running maximum and sum
+    for (int c0 = 0; c0 < n; c0 += 128) {
+      float y[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int c = c0 + 32 * i + lane;
+        y[i] = lse_of(c);
       }
+      float top = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+      if (top > m) {
+        sum *= m == neg_inf() ? 0.f : ex2(m - top);
+        m = top;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum += y[i] == neg_inf() ? 0.f : ex2(y[i] - m);
     }
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-  }
-  if (shared) {
-    if (g > 0) s_o[g - 1][lane] = o;
+    for (int c0 = g; c0 < n; c0 += GROUPS * 4) {
+      if (c0 > g) ask(c0, GROUPS);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[i] = lse_of(c0 + i * GROUPS);
+      take();
+    }
+    if (g > 0) s_o[g - 1][tid & 7] = o;
     __syncthreads();
     if (g > 0) return;
 #pragma unroll
-    for (int k = 0; k < 3; ++k) {
-      o.x += s_o[k][lane].x;
-      o.y += s_o[k][lane].y;
-      o.z += s_o[k][lane].z;
-      o.w += s_o[k][lane].w;
-    }
+    for (int i = 0; i < GROUPS - 1; ++i) add(1.f, s_o[i][tid]);
   }
-  const int64_t row = (int64_t)rq.q_start * a.num_heads + r;
-  const float v[4] = {o.x, o.y, o.z, o.w};
-  store_out<4>(a.out, row * DL + x * 4, v, sum > 0.f ? a.output_scale / sum : 0.f, a.out_dtype);
+  const float f[4] = {o.x, o.y, o.z, o.w};
+  store_out<4>(a.out, row * DL + x * 4, f, sum > 0.f ? a.output_scale / sum : 0.f, a.out_dtype);
   if (x == 0 && a.lse != nullptr) a.lse[row] = sum > 0.f ? m + log2f(sum) : neg_inf();
 }
 
@@ -720,11 +754,11 @@ int launch(const pka_latent_plan& plan, const LatentArgs& a, const LatentMaps& m
 }
 
 template <int DL>
-int launch_merge(const pka_latent_plan& plan, const LatentArgs& a, cudaStream_t stream) {
+int launch_merge(const LatentArgs& a, cudaStream_t stream) {
   if (a.num_splits > 0) {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(a.num_splits * a.max_rows), plan.max_parts > kFewPieces ? DL / 128 : 1);
-    cfg.blockDim = dim3(128);
+    cfg.gridDim = dim3((unsigned)(a.num_splits + a.num_many * (DL / 32 - 1)) * (unsigned)a.max_rows);
+    cfg.blockDim = dim3(DL / 4);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -792,8 +826,7 @@ int launch_latent_decode(const pka_latent_plan& plan, const LatentArgs& a, const
   const int rc = plan.row_tile == 128 ? launch_latent_decode_pair(plan, a, pages, stride_page, stream)
                                       : launch_single(plan, a, pages, stride_page, stream);
   if (rc != PKA_OK) return rc;
-  return plan.desc.latent_dim == 512 ? launch_merge<512>(plan, a, stream)
-                                     : launch_merge<256>(plan, a, stream);
+  return plan.desc.latent_dim == 512 ? launch_merge<512>(a, stream) : launch_merge<256>(a, stream);
 }
 
 }  // namespace pka

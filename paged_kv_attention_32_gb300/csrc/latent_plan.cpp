@@ -137,18 +137,23 @@ int build_latent_plan(pka_latent_plan& p, const pka_latent_desc& d_in, const int
   for (LatentItem& it : p.items)
     if (count[it.request] > 1) it.part = p.reqs[it.request].n_parts++;
   p.splits.clear();
-  p.max_parts = 0;
   int64_t prow = 0;
   for (int32_t b = 0; b < B; ++b) {
     LatentReq& r = p.reqs[b];
-    p.max_parts = std::max(p.max_parts, r.n_parts);
     if (r.n_parts > 1) {
       r.part_base = (int32_t)prow;
       prow += (int64_t)r.n_parts * r.q_len * H;
       PKA_CHECK_ARG(prow <= (int64_t)INT32_MAX, "too many partial rows");
-      p.splits.push_back(b);
+      p.splits.push_back(r);
     }
   }
+  p.num_many = (int32_t)(std::stable_partition(p.splits.begin(), p.splits.end(),
+                                               [](const LatentReq& r) {
+                                                 return r.n_parts > kLatentFewPieces;
+                                               }) -
+                         p.splits.begin());
+  PKA_CHECK_ARG((int64_t)p.splits.size() * max_rows * (d.latent_dim / 32) <= INT32_MAX,
+                "too many rows of cut requests");
   p.partial_rows = (int32_t)prow;
   p.ws_lse_offset = ceil_div(prow * d.latent_dim * 4, 256) * 256;
   p.workspace_bytes = prow ? p.ws_lse_offset + prow * 4 : 0;
