@@ -5,8 +5,9 @@
 //   table[b, j]  = free[head + base_b + j - have_b],  have_b <= j < need_b
 //   slot_map[t]  = table[b, pos / ps] * ps + pos % ps, pos = kv_b + t - start_b
 // Every CTA scans the lengths itself (8 bytes a request, from L2 after the
-// first CTA) and keeps both prefix sums in shared memory, so one launch
-// without any wait between CTAs does the whole step; tokens and pages are
+// first CTA) and keeps them and both prefix sums in shared memory, so one launch
+// without any wait between CTAs does the whole step, with one dependent load
+// (a table entry or a free page) behind the first ones; tokens and pages are
 // then spread over all threads, each finding its request by binary search, so
 // one long request costs no more than many short ones.
 #include <algorithm>
@@ -20,7 +21,7 @@ namespace pka {
 namespace {
 
 constexpr int kThreads = 512;
-constexpr int kMaxBatch = 16384;   // two 32-bit prefix sums in 128 KB of shared memory
+constexpr int kMaxBatch = 16384;   // three 32-bit values each in 192 KB of shared memory
 
 // The last index b in [0, n) with start[b] <= x (start[0] = 0): requests that
 // add nothing share their start with their successor and are passed over.
@@ -53,9 +54,11 @@ kv_tables_kernel(const int32_t* __restrict__ kv_lens, const int32_t* __restrict_
   extern __shared__ uint32_t smem[];
   uint32_t* start = smem;           // [batch] tokens before the request
   uint32_t* base = smem + batch;    // [batch] fresh pages before it
+  int32_t* lens = reinterpret_cast<int32_t*>(smem) + 2 * batch;   // [batch] kv_lens
   __shared__ int64_t warp_tok[kThreads / 32], warp_pg[kThreads / 32];
   __shared__ int s_bad;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t head = __ldg(free_head);
   if (tid == 0) s_bad = 0;
   __syncthreads();
 
@@ -65,6 +68,7 @@ kv_tables_kernel(const int32_t* __restrict__ kv_lens, const int32_t* __restrict_
     int64_t nt = 0, np = 0;
     if (b < batch) {
       const int64_t kv = __ldg(kv_lens + b), nw = __ldg(new_lens + b);
+      lens[b] = (int32_t)kv;
       if (kv < 0 || nw < 0 || kv + nw > (int64_t)width * ps || kv + nw > 0x7fffffff) {
         s_bad = 1;
       } else {
@@ -96,7 +100,6 @@ kv_tables_kernel(const int32_t* __restrict__ kv_lens, const int32_t* __restrict_
     pg_sum += ap;
     __syncthreads();
   }
-  const int64_t head = __ldg(free_head);
   const bool bad = s_bad || tok_sum > num_slots || tok_sum > 0x7fffffff || head < 0 ||
                    head + pg_sum > num_free;
   const int64_t me = (int64_t)blockIdx.x * kThreads + tid, all = (int64_t)gridDim.x * kThreads;
@@ -107,12 +110,12 @@ kv_tables_kernel(const int32_t* __restrict__ kv_lens, const int32_t* __restrict_
   }
   for (int64_t b = me; b < batch; b += all) {
     qo_indptr[b] = bad ? 0 : (int32_t)start[b];
-    seq_lens[b] = __ldg(kv_lens + b) + (bad ? 0 : __ldg(new_lens + b));
+    seq_lens[b] = lens[b] + (bad ? 0 : __ldg(new_lens + b));
   }
   if (!bad) {
     for (int64_t p = me; p < pg_sum; p += all) {
       const int b = find_request(base, batch, (uint32_t)p);
-      const int have = (int)(((int64_t)__ldg(kv_lens + b) + ps - 1) / ps);
+      const int have = (int)(((uint32_t)lens[b] + (uint32_t)ps - 1u) / (uint32_t)ps);
       tables[b * row_stride + have + (p - base[b])] = __ldg(free_pages + head + p);
     }
   }
@@ -120,12 +123,13 @@ kv_tables_kernel(const int32_t* __restrict__ kv_lens, const int32_t* __restrict_
     int64_t slot = -1;
     if (!bad && t < tok_sum) {
       const int b = find_request(start, batch, (uint32_t)t);
-      const int64_t kv = __ldg(kv_lens + b), pos = kv + (t - start[b]);
-      const int page = (int)(pos / ps), have = (int)((kv + ps - 1) / ps);
+      // a request has at most 2^31 - 1 tokens: 32-bit unsigned positions
+      const uint32_t kv = (uint32_t)lens[b], pos = kv + ((uint32_t)t - start[b]);
+      const int page = (int)(pos / (uint32_t)ps), have = (int)((kv + (uint32_t)ps - 1u) / (uint32_t)ps);
       // entries below `have` are inputs of this call, the others come from the list
       const int32_t id = page < have ? tables[b * row_stride + page]
                                      : __ldg(free_pages + head + base[b] + (page - have));
-      slot = (int64_t)id * ps + pos % ps;
+      slot = (int64_t)id * ps + pos % (uint32_t)ps;
     }
     slot_map[t] = slot;
   }
@@ -141,11 +145,11 @@ int launch_kv_tables(const int32_t* kv_lens, const int32_t* new_lens, int32_t ba
   if (batch > kMaxBatch)
     return fail(PKA_ERR_UNSUPPORTED, "batch_size %d is above %d", batch, kMaxBatch);
   static std::atomic<uint64_t> smem_set{0};
-  cudaError_t e = set_smem_once(kv_tables_kernel, kMaxBatch * 8, smem_set);
+  cudaError_t e = set_smem_once(kv_tables_kernel, kMaxBatch * 12, smem_set);
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(kv_tables)");
   const int64_t work = std::max<int64_t>(num_slots, batch);
   const int grid = (int)std::min<int64_t>(ceil_div(work, kThreads), 152);
-  kv_tables_kernel<<<grid, kThreads, (size_t)batch * 8, stream>>>(
+  kv_tables_kernel<<<grid, kThreads, (size_t)batch * 12, stream>>>(
       kv_lens, new_lens, batch, free_pages, num_free, free_head, page_size, tables, row_stride,
       width, seq_lens, qo_indptr, slot_map, num_slots, free_head_out, status);
   e = cudaGetLastError();
