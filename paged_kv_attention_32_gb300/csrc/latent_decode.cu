@@ -113,42 +113,40 @@ __device__ __forceinline__ void transpose_quads(const float* r, float4* v, int l
   }
 }
 
-// NG consecutive columns of TMEM (one dimension per lane) times their factors,
-// as rows of the output: column i to row i, `base` being row 0's first dimension
-// of this warp.
-template <typename T, int DL, int NG>
+// 16 consecutive columns of TMEM (one dimension per lane) times their factors, as
+// rows of the output: column i to row i, `base` being row 0's first dimension of
+// this warp.  32-bit values go out as they lie, 128 bytes of a row a store; 16-bit
+// ones are turned first, so that a lane has four dimensions of a row.
+template <typename T, int DL>
 __device__ __forceinline__ void store_columns(uint32_t taddr, const float* factor, int live, T* base,
                                               int lane) {
-  uint32_t r[NG];
-#pragma unroll
-  for (int n = 0; n < NG; n += 16) tmem_ld16(taddr + (uint32_t)n, r + n);
+  uint32_t r[16];
+  tmem_ld16(taddr, r);
   tmem_wait_ld();
-  reg_fence<NG>(r);
-  T* dst = base + (lane & 3) * DL + (lane >> 2) * 4;
+  reg_fence<16>(r);
+  float f[16];
 #pragma unroll
-  for (int n = 0; n < NG; n += 16) {
-    float f[16];
+  for (int i = 0; i < 4; ++i) {
+    const float4 x = reinterpret_cast<const float4*>(factor)[i];
+    f[4 * i] = x.x * __uint_as_float(r[4 * i]);
+    f[4 * i + 1] = x.y * __uint_as_float(r[4 * i + 1]);
+    f[4 * i + 2] = x.z * __uint_as_float(r[4 * i + 2]);
+    f[4 * i + 3] = x.w * __uint_as_float(r[4 * i + 3]);
+  }
+  if constexpr (sizeof(T) == 4) {
+    T* dst = base + lane;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 x = reinterpret_cast<const float4*>(factor + n)[i];
-      f[4 * i] = x.x * __uint_as_float(r[n + 4 * i]);
-      f[4 * i + 1] = x.y * __uint_as_float(r[n + 4 * i + 1]);
-      f[4 * i + 2] = x.z * __uint_as_float(r[n + 4 * i + 2]);
-      f[4 * i + 3] = x.w * __uint_as_float(r[n + 4 * i + 3]);
-    }
+    for (int i = 0; i < 16; ++i)
+      if (i < live) dst[i * DL] = f[i];
+  } else {
     float4 v[4];
     transpose_quads(f, v, lane);
+    T* dst = base + (lane & 3) * DL + (lane >> 2) * 4;
+    constexpr bool F = std::is_same<T, __half>::value;
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      if (n + 4 * k + (lane & 3) < live) {
-        T* to = dst + (n + 4 * k) * DL;
-        if constexpr (sizeof(T) == 4) {
-          *reinterpret_cast<float4*>(to) = v[k];
-        } else {
-          constexpr bool F = std::is_same<T, __half>::value;
-          *reinterpret_cast<uint2*>(to) = make_uint2(pack2<F>(v[k].x, v[k].y), pack2<F>(v[k].z, v[k].w));
-        }
-      }
+      if (4 * k + (lane & 3) < live)
+        *reinterpret_cast<uint2*>(dst + 4 * k * DL) = make_uint2(pack2<F>(v[k].x, v[k].y), pack2<F>(v[k].z, v[k].w));
   }
 }
 
@@ -598,7 +596,7 @@ latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant
         out += (row + gc) * DL + quad * 32;
 #pragma unroll 1
         for (int blk = 0; blk < DL / 128; ++blk)
-          store_columns<typename std::remove_pointer<decltype(out)>::type, DL, NG>(
+          store_columns<typename std::remove_pointer<decltype(out)>::type, DL>(
               tmem + lane_off + (uint32_t)(blk * N + gc), s_col + gc, pc.rows - gc, out + blk * 128, lane);
       };
       if (!whole) write(a.ws_o, prow);
