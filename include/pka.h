@@ -631,7 +631,7 @@ int pka_status_check(int32_t* status_dev, void* stream);
  *            entry at or past num_pages * page_size skips it too and sets the
  *            slot bit of the status word (PKA_ERR_DEVICE_BOUNDS).  Entries
  *            must be distinct: of two rows for one slot either may remain, or
- *            parts of both.
+ *            parts of both.  latent and rope must not lie in the pool.
  * latent_dim, rope_dim  multiples of 8, rope_dim may be 0 (rope then NULL).
  * status     NULL or int32 [1] device status word (pka_status_check).
  */
@@ -702,6 +702,7 @@ typedef struct pka_latent_plan_info {
 /*
  * Build a latent decode plan from host copies of the lengths (before capture).
  * seq_lens_kv_host [B], each in [0, C * page_size].
+ *                  (and at most 2^31 - 257).
  * qo_indptr_host   NULL (fixed q_len) or [B+1]: cumulative query offsets from
  *                  0, non-decreasing.  A request without rows writes nothing.
  */

@@ -477,6 +477,15 @@ def _check_tensors(dtype, **tensors):
                 raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
 
 
+def _on_stream(stream):
+    """Makes ``stream`` current: the caching allocator hands a freed block out again in the
+    order of the stream it was made on, so what a call allocates for itself has to come from
+    the stream the call runs on."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream))
+    return torch.cuda.stream(stream)
+
+
 def _contiguous(**tensors):
     for name, t in tensors.items():
         if t is not None and not t.is_contiguous():
@@ -505,6 +514,12 @@ def paged_kv_tables(kv_lens, new_lens, free_pages, free_head, block_tables, *, p
     query offsets ``[B + 1]``, one int64 slot per new token (-1 behind the last) and the
     advanced head.  A step that does not fit changes nothing and sets ``status``
     (``check_status``)."""
+    if stream is not None:
+        with _on_stream(stream):
+            return paged_kv_tables(
+                kv_lens, new_lens, free_pages, free_head, block_tables, page_size=page_size,
+                num_slots=num_slots, seq_lens=seq_lens, qo_indptr=qo_indptr, slot_map=slot_map,
+                free_head_out=free_head_out, status=status)
     _check_tensors(torch.int32, kv_lens=kv_lens, new_lens=new_lens, free_pages=free_pages,
                    free_head=free_head, block_tables=block_tables, seq_lens=seq_lens,
                    qo_indptr=qo_indptr, free_head_out=free_head_out, status=status)
@@ -693,6 +708,10 @@ def paged_latent_decode_run(plan, q, pages, block_tables, seq_lens_kv=None, out=
     ``[num_pages, page_size, latent_dim + rope_dim]``.  Returns ``out``
     ``[T, H, latent_dim]`` (and the base-2 ``lse`` ``[T, H]`` when the plan returns it);
     rows of a given ``out`` past the plan's are left as they were."""
+    if stream is not None:
+        with _on_stream(stream):
+            return paged_latent_decode_run(plan, q, pages, block_tables, seq_lens_kv=seq_lens_kv,
+                                           out=out, lse=lse, workspace=workspace)
     _check_tensors(plan.dtype, q=q, pages=pages)
     _check_tensors(torch.int32, block_tables=block_tables, seq_lens_kv=seq_lens_kv)
     need, B = plan.total_q, plan.desc.batch_size
@@ -785,7 +804,11 @@ def batch_latent_prefill_run(plan, q, k_nope, k_rope, v, out=None, lse=None, str
     """Run a planned latent prefill: ``q`` ``[Tq, H, nope + rope]``, ``k_nope``
     ``[Tk, H, nope]`` and ``v`` ``[Tk, H, value]`` with the same strides (the two parts of
     one projection's output, or two tensors alike), ``k_rope`` ``[Tk, rope]`` shared by the
-    heads.  Returns ``out`` ``[Tq, H, value]`` (and ``lse`` when the plan returns it)."""
+    heads.  Returns ``out`` ``[Tq, H, value]`` (and ``lse`` when the plan returns it); rows of
+    a given ``out`` past the plan's are left as they were."""
+    if stream is not None:
+        with _on_stream(stream):
+            return batch_latent_prefill_run(plan, q, k_nope, k_rope, v, out=out, lse=lse)
     if not isinstance(plan, LatentPrefillPlan):
         raise ValueError("the plan was not made by batch_latent_prefill_plan")
     _check_tensors(plan.dtype, q=q, k_nope=k_nope, k_rope=k_rope, v=v)

@@ -28,7 +28,7 @@ int guarded(F&& f) {
 // Whether two byte ranges share a byte.
 bool overlap(const void* p, size_t n, const void* q, size_t m) {
   const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-  return a < b + m && b < a + n;
+  return n > 0 && m > 0 && a < b + m && b < a + n;
 }
 
 // One asynchronous copy of the plan's arrays from a pinned image, which is
@@ -121,10 +121,11 @@ int paged_kv_tables(const int32_t* kv_lens, const int32_t* new_lens, int32_t bat
                        {free_head, 4}};
   const Range outs[] = {{block_tables, ((B - 1) * (size_t)bt_row_stride + max_pages_per_seq) * 4},
                         {seq_lens, B * 4}, {qo_indptr, (B + 1) * 4},
-                        {slot_map, (size_t)num_slots * 8}, {free_head_out, 4}};
+                        {slot_map, (size_t)num_slots * 8}, {free_head_out, 4},
+                        {status, status != nullptr ? size_t(4) : 0}};
   for (const Range& o : outs) {
     for (const Range& i : ins)
-      PKA_CHECK_ARG(i.n == 0 || !overlap(o.p, o.n, i.p, i.n), "an output overlaps an input");
+      PKA_CHECK_ARG(!overlap(o.p, o.n, i.p, i.n), "an output overlaps an input");
     for (const Range& u : outs)
       PKA_CHECK_ARG(&u == &o || !overlap(o.p, o.n, u.p, u.n), "two outputs overlap");
   }

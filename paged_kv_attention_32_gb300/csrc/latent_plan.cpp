@@ -76,6 +76,8 @@ int build_latent_plan(pka_latent_plan& p, const pka_latent_desc& d_in, const int
     PKA_CHECK_ARG(n >= 0 && n <= (int64_t)d.max_pages_per_seq * d.page_size,
                   "request %d: kv_len %lld outside [0, %d pages x %d]", b, (long long)n,
                   d.max_pages_per_seq, d.page_size);
+    PKA_CHECK_ARG(n <= INT32_MAX - 4 * kLatentTile,   // positions a tile or two past it
+                  "request %d: kv_len %lld is too long", b, (long long)n);
     const int64_t l = indptr == nullptr ? d.q_len : (int64_t)indptr[b + 1] - indptr[b];
     PKA_CHECK_ARG(l >= 0, "qo_indptr must be non-decreasing (request %d)", b);
     LatentReq& r = p.reqs[b];

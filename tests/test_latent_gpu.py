@@ -65,6 +65,19 @@ def test_tables_follow_the_plain_form(kv, new, ps, slots):
     assert res.free_head.tolist() == [want[4]]
 
 
+def test_tables_of_the_largest_batch():
+    B, ps = 16384, 16
+    r = random.Random(4)
+    kv = [r.choice([0, 1, 15, 16, 40]) for _ in range(B)]
+    new = [r.choice([0, 1, 1, 17]) for _ in range(B)]
+    table, free, head, slots = tables_case(kv, new, ps, sum(new) + 100)
+    want = ref_tables(kv, new, free, head, table, ps, slots)
+    tab, res, status = run_tables(kv, new, table, free, head, ps, slots)
+    api.check_status(status)
+    assert tab.tolist() == want[0] and res.slot_map.tolist() == want[3]
+    assert res.qo_indptr.tolist() == want[2] and res.free_head.tolist() == [want[4]]
+
+
 def test_tables_slots_past_32_bits():
     table, ps = [[2 ** 31 - 1, -1]], 65536
     tab, res, _ = run_tables([65535], [2], table, [2 ** 31 - 2], 0, ps, 2)
@@ -114,6 +127,8 @@ def test_tables_rejects_overlapping_and_misplaced_arguments():
         api.paged_kv_tables(kv, new, free, head, tab, seq_lens=kv, **kw)
     with pytest.raises(L.PkaError, match="overlaps"):
         api.paged_kv_tables(kv, new, free, head, tab, free_head_out=head, **kw)
+    with pytest.raises(L.PkaError, match="overlap"):
+        api.paged_kv_tables(kv, new, free, head, tab, status=kv[:1], **kw)
     with pytest.raises(ValueError, match="cpu"):
         api.paged_kv_tables(kv.cpu(), new, free, head, tab, **kw)
     with pytest.raises(ValueError, match="int32"):
@@ -130,7 +145,7 @@ def test_tables_rejects_overlapping_and_misplaced_arguments():
 
 @pytest.mark.parametrize("tokens,dl,dr,ps,dtype", [
     (1, 512, 64, 16, BF), (33, 256, 64, 8, HF), (1000, 512, 64, 48, BF), (7, 8, 8, 3, HF),
-    (5, 72, 0, 1, BF)])
+    (5, 72, 0, 1, BF), (9001, 512, 64, 16, BF), (8193, 2048, 512, 7, HF), (3, 4096, 8, 2, BF)])
 def test_append_writes_rows_and_nothing_else(tokens, dl, dr, ps, dtype):
     g = torch.Generator(device=DEV).manual_seed(3)
     n_pages = tokens // ps + 4
@@ -401,6 +416,40 @@ def test_decode_gives_the_same_bits_again_and_in_two_streams(heads):
         assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
 
 
+@pytest.mark.parametrize("heads", [16, 128])
+def test_decode_split_requests_captured_and_on_a_given_stream(heads):
+    """The decode and the merge behind it, captured; replays on other lengths; and the same
+    call on a stream that is not the current one, its workspace made and freed there."""
+    kv = [6000, 40, 3000]
+    q, pages, table = decode_inputs(kv, [0, 1, 2, 3], heads, 512, 16, BF)
+    plan = api.paged_latent_decode_plan(kv, num_heads=heads, page_size=16, scale=0.04,
+                                        max_pages_per_seq=table.shape[1], return_lse=True,
+                                        num_pages=pages.shape[0], freeze_seq_lens=False)
+    assert plan.info["num_split"] >= 2
+    lens, out = i32(kv), torch.empty((3, heads, 512), dtype=BF, device=DEV)
+    lse = torch.empty((3, heads), device=DEV)
+    ws = torch.empty(plan.workspace_bytes, dtype=torch.uint8, device=DEV)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        api.paged_latent_decode_run(plan, q, pages, table, seq_lens_kv=lens, out=out, lse=lse,
+                                    workspace=ws)
+    for now in (kv, [100, 0, 2999], [5999, 17, 1]):
+        lens.copy_(i32(now))
+        out.fill_(float("nan"))
+        graph.replay()
+        plan.check()
+        ref = ref_decode(q, pages, table, now, [0, 1, 2, 3], 512, 0.04, False, 1.0, BF)
+        assert_within(out, lse, ref)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for stream in (side, side.cuda_stream):
+        got = api.paged_latent_decode_run(plan, q, pages, table, seq_lens_kv=lens, stream=stream)
+        torch.full((plan.workspace_bytes // 4,), float("nan"), device=DEV)   # not the call's memory
+        side.synchronize()
+        assert torch.equal(got[0], out) and torch.equal(got[1], lse)
+
+
 def test_decode_plan_update_and_refusals():
     kv = [300, 40]
     q, pages, table = decode_inputs([300, 40, 999], [0, 1, 2, 3], 16, 256, 16, BF)
@@ -498,6 +547,36 @@ def test_prefill_ignores_what_lies_in_other_requests():
     picked, ref = ref_prefill(q, kv[..., :128], rope, kv[..., 128:], qo, ko, 192 ** -0.5, False,
                               1.0, BF)
     assert_within(out[:40], lse[:40], ref)
+
+
+def test_prefill_leaves_rows_behind_the_batch_and_can_be_captured():
+    g = torch.Generator(device=DEV).manual_seed(2)
+    q = torch.randn((300, 3, 192), generator=g, device=DEV).to(BF)
+    kv = torch.randn((400, 3, 256), generator=g, device=DEV).to(BF)
+    rope = torch.randn((400, 64), generator=g, device=DEV).to(BF)
+    qo, ko = [0, 5, 205], [0, 150, 350]
+    plan = api.batch_latent_prefill_plan(qo, ko, num_heads=3, return_lse=True)
+    out = torch.full((300, 3, 128), 7.0, dtype=BF, device=DEV)
+    lse = torch.full((300, 3), 7.0, device=DEV)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        api.batch_latent_prefill_run(plan, q, kv[..., :128], rope, kv[..., 128:], out=out, lse=lse)
+    for _ in range(2):
+        q.mul_(0.5)
+        graph.replay()
+        plan.check()
+        picked, ref = ref_prefill(q, kv[..., :128], rope, kv[..., 128:], qo, ko, 192 ** -0.5, True,
+                                  1.0, BF)
+        assert_within(out[picked], lse[picked], ref)
+        assert bool((out[205:] == 7).all()) and bool((lse[205:] == 7).all())
+
+
+def test_prefill_many_tiles_of_one_request():
+    """Key runs long enough that every ring of the kernel turns many times, odd lengths."""
+    rows = {0, 1, 255, 256, 300, 511, 512, 640}
+    check_prefill([641], [5003], 2, rows=rows, causal=False)
+    check_prefill([641, 2], [5003, 4097], 1, dtype=HF, rows=rows)
 
 
 def test_prefill_refusals():
