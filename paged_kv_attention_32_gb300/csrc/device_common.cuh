@@ -108,27 +108,6 @@ __device__ __forceinline__ void mbar_arrive_expect_tx_cluster(uint32_t bar, uint
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// As mbar_wait, acquiring what other CTAs of the cluster released.
-__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, int32_t* status) {
-  uint64_t t0 = 0;
-  while (true) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    if (ok) return true;
-    const uint64_t now = global_timer_ns();
-    if (t0 == 0) t0 = now;
-    if (now - t0 > kWaitLimitNs) {
-      if (status) atomicOr(status, STATUS_WAIT_TIMEOUT);
-      return false;
-    }
-  }
-}
 // 3-D tiled load into this CTA's shared memory, completing on a barrier of either
 // CTA of a pair (address from map_to_rank).
 __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar,

@@ -86,10 +86,6 @@ __device__ __forceinline__ void let_copies_land() {
   }
 }
 
-__device__ __forceinline__ bool warp_wait_pair(uint32_t bar, uint32_t parity, int32_t* status) {
-  return __all_sync(0xffffffffu, mbar_wait_cluster(bar, parity, status));
-}
-
 template <int DL, bool F16>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 latent_decode_pair_kernel(const __grid_constant__ LatentArgs a, const __grid_constant__ PairMaps maps) {
@@ -238,12 +234,12 @@ latent_decode_pair_kernel(const __grid_constant__ LatentArgs a, const __grid_con
       for (int item = item0; ok && item < item1; ++item) {
         const Piece pc(a, item, rb, 2 * kRows);
         if (pc.n == 0) continue;
-        ok = warp_wait_pair(bar(R_QFULL), (uint32_t)(I & 1), a.status);
+        ok = warp_wait(bar(R_QFULL), (uint32_t)(I & 1), a.status);
         ++I;
         for (int j = 0; ok && j < pc.n; ++j, ++T) {
           // P(T - 2) written means S(T - 2) read: this S buffer is free
-          ok = (T < 2 || warp_wait_pair(bar(R_PFULL + (T & 1)), (uint32_t)(((T >> 1) - 1) & 1), a.status)) &&
-               warp_wait_pair(bar(R_KFULL + kp.slot), kp.parity, a.status);
+          ok = (T < 2 || warp_wait(bar(R_PFULL + (T & 1)), (uint32_t)(((T >> 1) - 1) & 1), a.status)) &&
+               warp_wait(bar(R_KFULL + kp.slot), kp.parity, a.status);
           if (!ok) break;
           tc_fence_after();
           const uint32_t d = tmem + G::kColS + (uint32_t)(T & 1) * 32u;
@@ -271,9 +267,9 @@ latent_decode_pair_kernel(const __grid_constant__ LatentArgs a, const __grid_con
         const Piece pc(a, item, rb, 2 * kRows);
         if (pc.n == 0) continue;
         for (int j = 0; j < pc.n; ++j, ++T) {
-          ok = warp_wait_pair(bar(R_VFULL + vp.slot), vp.parity, a.status) &&
-               warp_wait_pair(bar(R_PFULL + (T & 1)), (uint32_t)((T >> 1) & 1), a.status);
-          if (ok && j == 0 && I > 0) ok = warp_wait_pair(bar(R_OFREE), (uint32_t)((I - 1) & 1), a.status);
+          ok = warp_wait(bar(R_VFULL + vp.slot), vp.parity, a.status) &&
+               warp_wait(bar(R_PFULL + (T & 1)), (uint32_t)((T >> 1) & 1), a.status);
+          if (ok && j == 0 && I > 0) ok = warp_wait(bar(R_OFREE), (uint32_t)((I - 1) & 1), a.status);
           if (!ok) break;
           tc_fence_after();
           const uint64_t p = dp + (uint32_t)(T & 1) * (G::kP / 16);

@@ -76,11 +76,6 @@ static_assert(B_COUNT * 8 + 4 <= 256, "barriers and the TMEM address slot");
 template <bool F16> constexpr uint32_t kIdescQK = idesc_bf16_f32(256, 64, 0, 0, F16);
 template <bool F16> constexpr uint32_t kIdescPV = idesc_bf16_f32(256, kDV, 0, 1, F16);
 
-// Bounded wait of a whole warp on a barrier that both CTAs arrive on.
-__device__ __forceinline__ bool warp_wait_cluster(uint32_t bar, uint32_t parity, int32_t* status) {
-  return __all_sync(0xffffffffu, mbar_wait_cluster(bar, parity, status));
-}
-
 // A position in a ring of N slots and the parity of its current round.
 template <int N>
 struct RingPos {
@@ -211,7 +206,7 @@ latent_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_consta
       RingPos<kVStages> vp;
       auto issue_qk = [&](int j) -> bool {   // S of tile j into buffer j & 1
         const uint32_t d = tmem + (uint32_t)(j & 1) * 64u;
-        if (!warp_wait_cluster(bar(B_KFULL + kp.slot), kp.parity, a.status)) return false;
+        if (!warp_wait(bar(B_KFULL + kp.slot), kp.parity, a.status)) return false;
         tc_fence_after();
 #pragma unroll
         for (int blk = 0; blk < kQBlocks; ++blk)
@@ -224,12 +219,12 @@ latent_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_consta
         kp.next();
         return true;
       };
-      bool ok = warp_wait_cluster(bar(B_Q), 0, a.status);
+      bool ok = warp_wait(bar(B_Q), 0, a.status);
       for (int j = 0; ok && j < n_kv && j < 2; ++j) ok = issue_qk(j);
       for (int j = 0; ok && j < n_kv; ++j) {
         const int st = j & 1;
-        ok = warp_wait_cluster(bar(B_VFULL + vp.slot), vp.parity, a.status) &&
-             warp_wait_cluster(bar(B_PFULL + st), (uint32_t)((j >> 1) & 1), a.status);
+        ok = warp_wait(bar(B_VFULL + vp.slot), vp.parity, a.status) &&
+             warp_wait(bar(B_PFULL + st), (uint32_t)((j >> 1) & 1), a.status);
         if (!ok) break;
         tc_fence_after();
         // 4 k-steps of 16 keys: P columns +8, V rows +16 (2048 bytes)
