@@ -129,10 +129,12 @@ latent_decode_pair_kernel(const __grid_constant__ LatentArgs a, const __grid_con
     for (int i = 0; i < 3; ++i) tmem_slot[1 + i] = 0;   // failure flags
     fence_barrier_init();
   }
+  __syncwarp();
+  cluster_arrive();
   if (warp == 1) tmem_alloc_pair(smem_u32(tmem_slot), 512);
   tc_fence_before();
   __syncthreads();
-  cluster_sync();   // both CTAs' barriers stand before anyone arrives on them
+  cluster_wait();   // both CTAs' barriers stand before anyone arrives on them
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   // the merge's CTAs may start taking free SMs; they wait for this grid's end

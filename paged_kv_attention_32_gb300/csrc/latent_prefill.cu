@@ -125,10 +125,12 @@ latent_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_consta
     mbar_init(bar(B_TAIL), 1);
     fence_barrier_init();
   }
+  __syncwarp();
+  cluster_arrive();
   if (warp == 5) tmem_alloc_pair(smem_u32(tmem_slot), kTmemCols);
   tc_fence_before();
   __syncthreads();
-  cluster_sync();   // both CTAs' barriers stand before anyone arrives on them
+  cluster_wait();   // both CTAs' barriers stand before anyone arrives on them
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
