@@ -618,115 +618,132 @@ latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant
 }
 
 // The pieces of a cut request: out = sum_c w_c o_c / sum_c w_c with
-// w_c = 2^(lse_c - max).  Bound by latency: a chain of dependent loads per row, so
-// little of it and many CTAs an SM.  A row of up to kLatentFewPieces (nearly all) is one
-// CTA's, four values a thread, and every LSE and four pieces at a time are asked for at once.
-// A row of more is shared out to DL / 32 CTAs of 32 dimensions, whose groups of
-// eight threads deal the pieces out; the planner lists such requests first.  Launched
-// while the decode still runs, it waits for that grid's end.
-
+// w_c = 2^(lse_c - max).  A short chain of dependent loads per row, and few
+// instructions: with four values a thread (each making every weight for itself)
+// the issue slots bounded it (5760 rows of 2-3 pieces of 512 values 9.5 us; with eight 7.0).  A
+// row of up to kLatentFewPieces (nearly all) is one CTA's, every LSE and four
+// pieces at a time asked for at once.  A row of more is shared out to DL / 16
+// CTAs of 16 dimensions, whose groups of four threads deal the pieces out; the
+// planner lists such requests first.  Launched while the decode still runs, it
+// waits for that grid's end.
 template <int DL>
-__global__ void __launch_bounds__(DL / 4, 1280 / (DL / 4))
+__global__ void __launch_bounds__(DL / 8, 1024 / (DL / 8))
 latent_merge_kernel(const __grid_constant__ LatentArgs a) {
-  constexpr int T = DL / 4, GROUPS = T / 8, SLABS = DL / 32;
-  __shared__ float4 s_o[GROUPS - 1][8];
+  constexpr int T = DL / 8, GROUPS = T / 4, SLABS = DL / 16;
+  __shared__ float4 s_o[GROUPS - 1][4];
   const int tid = threadIdx.x, lane = tid & 31;
   const int many_ctas = a.num_many * a.max_rows * SLABS;
   const bool few = (int)blockIdx.x >= many_ctas;
-  const int slab = few ? 0 : blockIdx.x % SLABS;
   const int at = few ? a.num_many * a.max_rows + (int)blockIdx.x - many_ctas : blockIdx.x / SLABS;
-  const int r = at % a.max_rows;
-  const LatentReq rq = a.splits[at / a.max_rows];
+  const int which = at / a.max_rows, r = at - which * a.max_rows;
+  const LatentReq rq = a.splits[which];
   const int rows = rq.q_len * a.num_heads, n = rq.n_parts;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (r >= rows) return;
   const int64_t row = (int64_t)rq.q_start * a.num_heads + r, p0 = (int64_t)rq.part_base + r;
   const float* lse = a.ws_lse + p0;
-  const int x = few ? tid : slab * 8 + (tid & 7);   // this thread's four dimensions
-  const float4* src = reinterpret_cast<const float4*>(a.ws_o + p0 * DL) + x;
+  const float4* part = reinterpret_cast<const float4*>(a.ws_o + p0 * DL);
+  const int64_t step = (int64_t)rows * (DL / 4);   // from piece to piece
+  // A piece without keys (LSE -inf) has no output rows, what lies there is not used.
+  auto lse_of = [&](int c) { return c < n ? __ldcg(lse + (int64_t)c * rows) : neg_inf(); };
   float m = neg_inf(), sum = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  auto add = [&](float w, float4 v) {
+  auto add = [](float4& o, float w, float4 v) {
     o.x += w * v.x;
     o.y += w * v.y;
     o.z += w * v.z;
     o.w += w * v.w;
   };
-  // four pieces c0, c0 + step, ...: a piece without keys (LSE -inf) has no output
-  // rows, what lies there is not used
-  auto lse_of = [&](int c) { return c < n ? __ldcg(lse + (int64_t)c * rows) : neg_inf(); };
-  float s[4];
-  float4 v[4];
-  auto ask = [&](int c0, int step) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int c = c0 + i * step;
-      v[i] = c < n ? __ldcg(src + (int64_t)c * rows * T) : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-  };
-  auto take = [&]() {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (s[i] != neg_inf()) add(ex2(s[i] - m), v[i]);
+  auto store = [&](int x, float4 o) {
+    const float f[4] = {o.x, o.y, o.z, o.w};
+    store_out<4>(a.out, row * DL + x * 4, f, sum > 0.f ? a.output_scale / sum : 0.f, a.out_dtype);
   };
   if (few) {
-    float more[4];   // the LSEs of pieces 4 .. 7
-    ask(0, 1);
+    float4 o0 = make_float4(0.f, 0.f, 0.f, 0.f), o1 = o0, v0[4], v1[4];
+    float s[4], more[kLatentFewPieces - 4];
+    auto ask = [&](int c0) {
+      const float4* src = part + c0 * step + tid;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (c0 + i < n) {
+          v0[i] = __ldcg(src);
+          v1[i] = __ldcg(src + T);
+        }
+        src += step;
+      }
+    };
+    auto take = [&](const float* l, int c0) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (c0 + i < n && l[i] != neg_inf()) {
+          const float w = ex2(l[i] - m);
+          sum += w;
+          add(o0, w, v0[i]);
+          add(o1, w, v1[i]);
+        }
+    };
+    ask(0);
 #pragma unroll
     for (int i = 0; i < 4; ++i) s[i] = lse_of(i);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) more[i] = lse_of(4 + i);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) m = fmaxf(m, fmaxf(s[i], more[i]));
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      sum += s[i] == neg_inf() ? 0.f : ex2(s[i] - m);
-      sum += more[i] == neg_inf() ? 0.f : ex2(more[i] - m);
-    }
-    take();
+    for (int i = 0; i < 4; ++i) m = fmaxf(m, s[i]);
     if (n > 4) {
-      ask(4, 1);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s[i] = more[i];
-      take();
-    }
-  } else {
-    const int g = tid >> 3;
-    ask(g, GROUPS);
-    // each warp for itself: four pieces a lane and round, a running maximum and sum
-    for (int c0 = 0; c0 < n; c0 += 128) {
-      float y[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int c = c0 + 32 * i + lane;
-        y[i] = lse_of(c);
+      for (int i = 0; i < kLatentFewPieces - 4; ++i) {
+        more[i] = lse_of(4 + i);
+        m = fmaxf(m, more[i]);
       }
-      float top = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-      if (top > m) {
-        sum *= m == neg_inf() ? 0.f : ex2(m - top);
-        m = top;
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) sum += y[i] == neg_inf() ? 0.f : ex2(y[i] - m);
     }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    for (int c0 = g; c0 < n; c0 += GROUPS * 4) {
-      if (c0 > g) ask(c0, GROUPS);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s[i] = lse_of(c0 + i * GROUPS);
-      take();
+    take(s, 0);
+    if (n > 4) {
+      ask(4);
+      take(more, 4);
     }
-    if (g > 0) s_o[g - 1][tid & 7] = o;
-    __syncthreads();
-    if (g > 0) return;
-#pragma unroll
-    for (int i = 0; i < GROUPS - 1; ++i) add(1.f, s_o[i][tid]);
+    store(tid, o0);
+    store(tid + T, o1);
+    if (tid == 0 && a.lse != nullptr) a.lse[row] = sum > 0.f ? m + log2f(sum) : neg_inf();
+    return;
   }
-  const float f[4] = {o.x, o.y, o.z, o.w};
-  store_out<4>(a.out, row * DL + x * 4, f, sum > 0.f ? a.output_scale / sum : 0.f, a.out_dtype);
+  const int g = tid >> 2, x = blockIdx.x % SLABS * 4 + (tid & 3);
+  constexpr int W = 8;   // pieces a thread has in flight
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f), v[W];
+  auto ask = [&](int c0) {
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+      if (c0 + i * GROUPS < n) v[i] = __ldcg(part + (int64_t)(c0 + i * GROUPS) * step + x);
+  };
+  ask(g);
+  // each warp for itself: four pieces a lane and round, a running maximum and sum
+  for (int c0 = 0; c0 < n; c0 += 128) {
+    float y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = lse_of(c0 + 32 * i + lane);
+    float top = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    if (top > m) {
+      sum *= m == neg_inf() ? 0.f : ex2(m - top);
+      m = top;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum += y[i] == neg_inf() ? 0.f : ex2(y[i] - m);
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  for (int c0 = g; c0 < n; c0 += GROUPS * W) {
+    if (c0 > g) ask(c0);
+    float s[W];
+#pragma unroll
+    for (int i = 0; i < W; ++i) s[i] = lse_of(c0 + i * GROUPS);
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+      if (s[i] != neg_inf()) add(o, ex2(s[i] - m), v[i]);
+  }
+  if (g > 0) s_o[g - 1][tid & 3] = o;
+  __syncthreads();
+  if (g > 0) return;
+#pragma unroll
+  for (int i = 0; i < GROUPS - 1; ++i) add(o, 1.f, s_o[i][tid]);
+  store(x, o);
   if (x == 0 && a.lse != nullptr) a.lse[row] = sum > 0.f ? m + log2f(sum) : neg_inf();
 }
 
@@ -755,8 +772,8 @@ template <int DL>
 int launch_merge(const LatentArgs& a, cudaStream_t stream) {
   if (a.num_splits > 0) {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(a.num_splits + a.num_many * (DL / 32 - 1)) * (unsigned)a.max_rows);
-    cfg.blockDim = dim3(DL / 4);
+    cfg.gridDim = dim3((unsigned)(a.num_splits + a.num_many * (DL / 16 - 1)) * (unsigned)a.max_rows);
+    cfg.blockDim = dim3(DL / 8);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -154,7 +154,7 @@ int build_latent_plan(pka_latent_plan& p, const pka_latent_desc& d_in, const int
                                                  return r.n_parts > kLatentFewPieces;
                                                }) -
                          p.splits.begin());
-  PKA_CHECK_ARG((int64_t)p.splits.size() * max_rows * (d.latent_dim / 32) <= INT32_MAX,
+  PKA_CHECK_ARG((int64_t)p.splits.size() * max_rows * (d.latent_dim / 16) <= INT32_MAX,
                 "too many rows of cut requests");
   p.partial_rows = (int32_t)prow;
   p.ws_lse_offset = ceil_div(prow * d.latent_dim * 4, 256) * 256;
