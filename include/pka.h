@@ -742,6 +742,8 @@ int paged_latent_decode_plan_check(const pka_latent_plan* plan, void* stream);
  * block_tables, bt_row_stride, seq_lens_kv_dev as for paged_decode_run.
  *            Entries past a request's last page are not read; cache rows past
  *            its last token may hold anything, infinities and NaN included.
+ *            Rows before it enter every query row of the request: a causal row's
+ *            weight of a later key is 0, and 0 times an infinity is NaN.
  *            An entry outside [0, num_pages) reads as zeros, never out of
  *            bounds.
  * out        [total_q, num_heads, latent_dim] contiguous, out_dtype, 16-byte
@@ -797,7 +799,9 @@ int batch_latent_prefill_plan(pka_prefill_plan** plan_out, const pka_latent_pref
  *         base + t*kv_stride_tok + h*kv_stride_head + d, one set of strides for
  *         both (they may be the two parts of one projection's output).
  * k_rope  [total_kv, rope]: (t, d) at k_rope + t*rope_stride + d.
- *         All strides multiples of 8 elements, bases 16-byte aligned.
+ *         All strides multiples of 8 elements, bases 16-byte aligned.  Other
+ *         requests' rows may hold anything; a request's own have to be finite
+ *         for its causal rows before them (0 times an infinity is NaN).
  * out     [total_q, H, value] contiguous, out_dtype, 16-byte aligned.
  * lse     NULL or fp32 [total_q, H] base-2 LSE (required with return_lse).
  */

@@ -62,33 +62,19 @@ enum {
 };
 static_assert(L_COUNT * 8 + 4 + 48 <= 512, "barriers, TMEM address, failure flags");
 
-// Max or sum over the eight lanes that share lane % 4, of C values each.  The
-// lanes trade halves, so that each ends with C / 8 (at least one) totals: value
-// index first_value(lane) on.
-template <int C, typename Op>
-__device__ __forceinline__ void reduce_rows(float* x, int lane, Op op) {
-  int n = C;
+// Max or sum of four values each over the eight lanes that share lane % 4.  The
+// lanes trade halves, so that each ends with one total: value first_value(lane).
+template <typename Op>
+__device__ __forceinline__ float reduce_rows(const float* x, int lane, Op op) {
+  const bool b4 = lane & 16, b3 = lane & 8;
+  float y[2];
 #pragma unroll
-  for (int d = 16; d >= 4; d >>= 1) {
-    if (n > 1) {
-      n >>= 1;
-      const bool up = lane & d;
-#pragma unroll
-      for (int i = 0; i < C / 2; ++i)
-        if (i < n) {
-          const float mine = up ? x[i + n] : x[i], other = up ? x[i] : x[i + n];
-          x[i] = op(mine, __shfl_xor_sync(0xffffffffu, other, d));
-        }
-    } else {
-      x[0] = op(x[0], __shfl_xor_sync(0xffffffffu, x[0], d));
-    }
-  }
+  for (int i = 0; i < 2; ++i)
+    y[i] = op(b4 ? x[i + 2] : x[i], __shfl_xor_sync(0xffffffffu, b4 ? x[i] : x[i + 2], 16));
+  const float z = op(b3 ? y[1] : y[0], __shfl_xor_sync(0xffffffffu, b3 ? y[0] : y[1], 8));
+  return op(z, __shfl_xor_sync(0xffffffffu, z, 4));
 }
-template <int C>
-__device__ __forceinline__ int first_value(int lane) {
-  const int b4 = (lane >> 4) & 1, b3 = (lane >> 3) & 1, b2 = (lane >> 2) & 1;
-  return C == 8 ? 4 * b4 + 2 * b3 + b2 : 2 * b4 + b3;
-}
+__device__ __forceinline__ int first_value(int lane) { return 2 * ((lane >> 4) & 1) + ((lane >> 3) & 1); }
 
 struct LatentMaps {
   CUtensorMap pool, pool_rope, q, q_rope;
@@ -470,23 +456,20 @@ latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant
 #pragma unroll
           for (int q = 0; q < C; ++q)
             mx[q] = fmaxf(x[4 * (q >> 1) + (q & 1)], x[4 * (q >> 1) + 2 + (q & 1)]);
-          reduce_rows<C>(mx, lane, [](float u, float v) { return fmaxf(u, v); });
           float* wm = g_max + (T & 1) * 4 * NG;
-          wm[quad * NG + (lane & 3) * C + first_value<C>(lane)] = mx[0];
+          wm[quad * NG + (lane & 3) * C + first_value(lane)] =
+              reduce_rows(mx, lane, [](float u, float v) { return fmaxf(u, v); });
           bar_sync_group(g);
+          float4 u = *reinterpret_cast<const float4*>(wm + (lane & 3) * C);
 #pragma unroll
-          for (int q = 0; q < C; q += 4) {
-            float4 u = *reinterpret_cast<const float4*>(wm + (lane & 3) * C + q);
-#pragma unroll
-            for (int w = 1; w < 4; ++w) {
-              const float4 v = *reinterpret_cast<const float4*>(wm + w * NG + (lane & 3) * C + q);
-              u = make_float4(fmaxf(u.x, v.x), fmaxf(u.y, v.y), fmaxf(u.z, v.z), fmaxf(u.w, v.w));
-            }
-            mx[q] = u.x;
-            mx[q + 1] = u.y;
-            mx[q + 2] = u.z;
-            mx[q + 3] = u.w;
+          for (int w = 1; w < 4; ++w) {
+            const float4 v = *reinterpret_cast<const float4*>(wm + w * NG + (lane & 3) * C);
+            u = make_float4(fmaxf(u.x, v.x), fmaxf(u.y, v.y), fmaxf(u.z, v.z), fmaxf(u.w, v.w));
           }
+          mx[0] = u.x;
+          mx[1] = u.y;
+          mx[2] = u.z;
+          mx[3] = u.w;
           // Every warp of the group holds the same maxima, so all decide alike.  A row
           // without visible keys so far still has O = 0 and l = 0 and takes its first
           // reference without a rescale.
@@ -567,9 +550,9 @@ latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant
       next_q(item + 1);
 
       // ---- output: O^T / l, one latent dimension per lane of a 128-wide block ----
-      reduce_rows<C>(l, lane, [](float u, float v) { return u + v; });
       float* s_sum = g_max + (T & 1) * 4 * NG;   // the half the last tile did not use
-      s_sum[quad * NG + (lane & 3) * C + first_value<C>(lane)] = l[0];
+      s_sum[quad * NG + (lane & 3) * C + first_value(lane)] =
+          reduce_rows(l, lane, [](float u, float v) { return u + v; });
       if (gt < 4)
 #pragma unroll
         for (int q = 0; q < C; ++q) s_ref[gc + 8 * (q >> 1) + col0 + (q & 1)] = m[q];
@@ -583,9 +566,10 @@ latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant
         const int q = ((gt & 7) >> 1) * C + 2 * (gt >> 3) + (gt & 1);   // column gt in s_sum
         const float sum = (s_sum[q] + s_sum[NG + q]) + (s_sum[2 * NG + q] + s_sum[3 * NG + q]);
         const int n = gc + gt;
-        s_col[n] = sum > 0.f ? (whole ? a.output_scale : 1.f) / sum : 0.f;
+        // != and not >: a sum that is NaN stays one, in the LSE as in the output
+        s_col[n] = sum != 0.f ? (whole ? a.output_scale : 1.f) / sum : 0.f;
         if (n < pc.rows) {
-          const float lse = sum > 0.f ? s_ref[n] + log2f(sum) : neg_inf();
+          const float lse = sum != 0.f ? s_ref[n] + log2f(sum) : neg_inf();
           if (!whole) a.ws_lse[prow + n] = lse;
           else if (a.lse != nullptr) a.lse[orow + n] = lse;
         }
@@ -655,7 +639,7 @@ latent_merge_kernel(const __grid_constant__ LatentArgs a) {
   };
   auto store = [&](int x, float4 o) {
     const float f[4] = {o.x, o.y, o.z, o.w};
-    store_out<4>(a.out, row * DL + x * 4, f, sum > 0.f ? a.output_scale / sum : 0.f, a.out_dtype);
+    store_out<4>(a.out, row * DL + x * 4, f, sum != 0.f ? a.output_scale / sum : 0.f, a.out_dtype);
   };
   if (few) {
     float4 o0 = make_float4(0.f, 0.f, 0.f, 0.f), o1 = o0, v0[4], v1[4];
@@ -700,7 +684,7 @@ latent_merge_kernel(const __grid_constant__ LatentArgs a) {
     }
     store(tid, o0);
     store(tid + T, o1);
-    if (tid == 0 && a.lse != nullptr) a.lse[row] = sum > 0.f ? m + log2f(sum) : neg_inf();
+    if (tid == 0 && a.lse != nullptr) a.lse[row] = sum != 0.f ? m + log2f(sum) : neg_inf();
     return;
   }
   const int g = tid >> 2, x = blockIdx.x % SLABS * 4 + (tid & 3);
@@ -744,7 +728,7 @@ latent_merge_kernel(const __grid_constant__ LatentArgs a) {
 #pragma unroll
   for (int i = 0; i < GROUPS - 1; ++i) add(o, 1.f, s_o[i][tid]);
   store(x, o);
-  if (x == 0 && a.lse != nullptr) a.lse[row] = sum > 0.f ? m + log2f(sum) : neg_inf();
+  if (x == 0 && a.lse != nullptr) a.lse[row] = sum != 0.f ? m + log2f(sum) : neg_inf();
 }
 
 template <int DL, int N, bool F16>

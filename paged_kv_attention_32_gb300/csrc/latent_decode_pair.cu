@@ -448,9 +448,10 @@ latent_decode_pair_kernel(const __grid_constant__ LatentArgs a, const __grid_con
         break;
       }
       const float total = s_sum[row] + s_sum[kRows + row];
-      const float inv = total > 0.f ? (whole ? a.output_scale : 1.f) / total : 0.f;
+      // != and not >: a sum that is NaN stays one, in the LSE as in the output
+      const float inv = total != 0.f ? (whole ? a.output_scale : 1.f) / total : 0.f;
       if (half == 0 && row < live) {
-        const float lse = total > 0.f ? m + log2f(total) : neg_inf();
+        const float lse = total != 0.f ? m + log2f(total) : neg_inf();
         if (!whole) a.ws_lse[prow + row] = lse;
         else if (a.lse != nullptr) a.lse[orow + row] = lse;
       }

@@ -309,7 +309,8 @@ latent_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_consta
     if (ok && n_kv > 0 &&
         warp_wait(bar(B_ODONE + ((n_kv - 1) & 1)), (uint32_t)(((n_kv - 1) >> 1) & 1), a.status)) {
       tc_fence_after();
-      const float inv = l > 0.f ? a.output_scale / l : 0.f;
+      // != and not >: a sum that is NaN stays one, in the LSE as in the output
+      const float inv = l != 0.f ? a.output_scale / l : 0.f;
       if (a.out_dtype == PKA_DTYPE_F32) {
         const int64_t dst = ((int64_t)(q0 + t) * a.num_qo_heads + h) * kDV;
 #pragma unroll 1
@@ -363,7 +364,7 @@ latent_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_consta
         }
       }
       if (row_valid && a.lse != nullptr)
-        a.lse[(int64_t)(q0 + t) * a.num_qo_heads + h] = l > 0.f ? m_ref + log2f(l) : neg_inf();
+        a.lse[(int64_t)(q0 + t) * a.num_qo_heads + h] = l != 0.f ? m_ref + log2f(l) : neg_inf();
     }
   }
 

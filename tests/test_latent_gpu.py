@@ -378,6 +378,27 @@ def test_decode_bad_pages_read_as_zeros(heads):
                                        1.0, BF))
 
 
+@pytest.mark.parametrize("num_sms", [1, 8])      # whole and cut requests
+@pytest.mark.parametrize("heads", [16, 64, 128])
+def test_decode_nan_in_a_cached_row_reaches_its_own_request_only(heads, num_sms):
+    """Output and LSE of the request are NaN, also where only one of its pieces has
+    the row; other requests, in the same CTAs before and behind it, are as ever."""
+    kv = [300, 700, 65, 500]
+    q, pages, table = decode_inputs(kv, list(range(5)), heads, 256, 16, BF)
+    plan = api.paged_latent_decode_plan(kv, num_heads=heads, page_size=16, scale=0.05,
+                                        max_pages_per_seq=table.shape[1], num_pages=pages.shape[0],
+                                        latent_dim=256, return_lse=True, num_sms=num_sms)
+    assert (plan.info["num_split"] >= 1) == (num_sms > 1)
+    good, good_lse = api.paged_latent_decode_run(plan, q, pages, table)
+    pages[int(table[1, 40]), 3, 7] = float("nan")     # token 643 of request 1
+    out, lse = api.paged_latent_decode_run(plan, q, pages, table)
+    plan.check()
+    assert bool(out[1].isnan().all()) and bool(lse[1].isnan().all())
+    for b in (0, 2, 3):
+        assert bool(good[b].isfinite().all())
+        assert torch.equal(out[b], good[b]) and torch.equal(lse[b], good_lse[b])
+
+
 @pytest.mark.parametrize("heads", [16, 128])
 def test_decode_pool_offsets_past_32_bits(heads):
     ps, D = 64, 576
@@ -547,6 +568,21 @@ def test_prefill_ignores_what_lies_in_other_requests():
     picked, ref = ref_prefill(q, kv[..., :128], rope, kv[..., 128:], qo, ko, 192 ** -0.5, False,
                               1.0, BF)
     assert_within(out[:40], lse[:40], ref)
+
+
+def test_prefill_nan_in_a_key_reaches_the_rows_that_see_it():
+    lq = lk = [70, 200]
+    qo = [0, 70, 270]
+    g = torch.Generator(device=DEV).manual_seed(3)
+    q, kn, v, rope = (torch.randn(*s, generator=g, device=DEV).to(BF)
+                      for s in ((270, 2, 192), (270, 2, 128), (270, 2, 128), (270, 64)))
+    plan = api.batch_latent_prefill_plan(qo, qo, num_heads=2, causal=True, return_lse=True)
+    good, good_lse = api.batch_latent_prefill_run(plan, q, kn, rope, v)
+    kn[70 + 130] = float("nan")
+    out, lse = api.batch_latent_prefill_run(plan, q, kn, rope, v)
+    plan.check()
+    assert torch.equal(out[:200], good[:200]) and torch.equal(lse[:200], good_lse[:200])
+    assert bool(out[200:].isnan().all()) and bool(lse[200:].isnan().all())
 
 
 def test_prefill_leaves_rows_behind_the_batch_and_can_be_captured():
