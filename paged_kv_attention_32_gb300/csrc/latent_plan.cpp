@@ -19,7 +19,7 @@ namespace pka {
 
 namespace {
 constexpr int64_t kItemCost = 2;     // a piece's fixed cost, in tiles
-constexpr int64_t kMinPiece = 4;     // tiles below which a request is not cut further
+constexpr int64_t kMinPiece = 2;     // tiles below which a request is not cut further
 constexpr int32_t kMaxRows = 65536;
 constexpr int32_t kMaxSms = 1024;
 }  // namespace
