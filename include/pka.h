@@ -767,6 +767,7 @@ int paged_latent_decode_run(const pka_latent_plan* plan, const void* q, int64_t 
  *
  * nope_dim    128.  rope_dim 64.  value_dim 128.
  * num_heads   query and key/value heads alike.
+ * num_sms     SMs to plan for, 0: the device's (152 in a host-only plan).
  * mask, output_scale, return_lse, flags, dtype, out_dtype as for
  *             batch_prefill_plan; sm_scale NaN selects 1/sqrt(nope + rope).
  */
@@ -782,16 +783,18 @@ typedef struct pka_latent_prefill_desc {
   float sm_scale;
   float output_scale;
   int32_t return_lse;
+  int32_t num_sms;
   int32_t flags;
 } pka_latent_prefill_desc;
 
 /* The plan is a prefill plan: batch_prefill_plan_check and
  * batch_prefill_plan_destroy take it, batch_prefill_run does not.
  * num_tiles_out receives the number of tiles of up to 256 rows of one request
- * and head, a pair of CTAs each. */
+ * and head; pairs of CTAs take them in turn, and tiles are cut along their keys
+ * where the pairs would end unevenly.  workspace_bytes_out: their partial states. */
 int batch_latent_prefill_plan(pka_prefill_plan** plan_out, const pka_latent_prefill_desc* desc,
                               const int32_t* qo_indptr_host, const int32_t* kv_indptr_host,
-                              int32_t* num_tiles_out, void* stream);
+                              size_t* workspace_bytes_out, int32_t* num_tiles_out, void* stream);
 
 /*
  * q       [total_q, H, nope + rope]: (t, h, d) at q + t*q_stride_tok + h*q_stride_head + d.
@@ -804,11 +807,14 @@ int batch_latent_prefill_plan(pka_prefill_plan** plan_out, const pka_latent_pref
  *         for its causal rows before them (0 times an infinity is NaN).
  * out     [total_q, H, value] contiguous, out_dtype, 16-byte aligned.
  * lse     NULL or fp32 [total_q, H] base-2 LSE (required with return_lse).
+ * workspace  at least the plan's workspace_bytes, 256-byte aligned (NULL when they
+ *         are 0).  Runs that may overlap on the GPU need a workspace each.
  */
 int batch_latent_prefill_run(const pka_prefill_plan* plan, const void* q, int64_t q_stride_tok,
                              int64_t q_stride_head, const void* k_nope, const void* k_rope,
                              int64_t rope_stride, const void* v, int64_t kv_stride_tok,
-                             int64_t kv_stride_head, void* out, float* lse, void* stream);
+                             int64_t kv_stride_head, void* out, float* lse, void* workspace,
+                             size_t workspace_bytes, void* stream);
 
 /* ======================================================================== */
 /* Test hook                                                                 */

@@ -121,7 +121,7 @@ class LatentPrefillDesc(ctypes.Structure):
         ("nope_dim", ctypes.c_int32), ("rope_dim", ctypes.c_int32),
         ("value_dim", ctypes.c_int32), ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
         ("mask", ctypes.c_int32), ("sm_scale", ctypes.c_float), ("output_scale", ctypes.c_float),
-        ("return_lse", ctypes.c_int32), ("flags", ctypes.c_int32),
+        ("return_lse", ctypes.c_int32), ("num_sms", ctypes.c_int32), ("flags", ctypes.c_int32),
     ]
 
 
@@ -174,9 +174,9 @@ _SIGS = {
                                                _vp, _vp, _vp, _sz, _vp]),
     "batch_latent_prefill_plan": (ctypes.c_int, [ctypes.POINTER(_vp),
                                                  ctypes.POINTER(LatentPrefillDesc), _pi32, _pi32,
-                                                 _pi32, _vp]),
+                                                 ctypes.POINTER(_sz), _pi32, _vp]),
     "batch_latent_prefill_run": (ctypes.c_int, [_vp, _vp, _i64, _i64, _vp, _vp, _i64, _vp, _i64,
-                                                _i64, _vp, _vp, _vp]),
+                                                _i64, _vp, _vp, _vp, _sz, _vp]),
     "paged_kv_gather": (ctypes.c_int, [_vp, _i64, _i64, _i64, _i32, _i32, _i32, _vp, _i64, _i32,
                                        _i32, _i32, _i32, _vp, _vp]),
     "pka_wait_timeout_probe": (ctypes.c_int, [_vp, _vp, _i64, _vp]),

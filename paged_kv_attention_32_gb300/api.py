@@ -765,9 +765,10 @@ def paged_latent_decode_run(plan, q, pages, block_tables, seq_lens_kv=None, out=
 class LatentPrefillPlan(PrefillPlan):
     """A prefill plan for ``batch_latent_prefill_run``."""
 
-    def __init__(self, handle, desc, num_tiles, total_q, total_kv):
+    def __init__(self, handle, desc, num_tiles, total_q, total_kv, workspace_bytes):
         super().__init__(handle, desc, num_tiles)
         self.total_q, self.total_kv = total_q, total_kv
+        self.workspace_bytes = workspace_bytes
         # what every run compares its tensors with
         self.dtype, self.out_dtype = _TORCH[desc.dtype], _TORCH[desc.out_dtype]
         self.q_row = (desc.num_heads, desc.nope_dim + desc.rope_dim)
@@ -777,8 +778,8 @@ class LatentPrefillPlan(PrefillPlan):
 
 def batch_latent_prefill_plan(qo_indptr, kv_indptr, *, num_heads, nope_dim=128, rope_dim=64,
                               value_dim=128, causal=True, sm_scale=None, output_scale=1.0,
-                              return_lse=False, host_only=False, dtype=torch.bfloat16,
-                              out_dtype=None, stream=None):
+                              return_lse=False, num_sms=0, host_only=False,
+                              dtype=torch.bfloat16, out_dtype=None, stream=None):
     """Plan an expanded latent prefill from host copies of the offsets (see pka.h)."""
     in_code, out_code = _dtype_codes(dtype, out_dtype)
     qo_t, qo_p = _host_i32(qo_indptr)
@@ -790,17 +791,20 @@ def batch_latent_prefill_plan(qo_indptr, kv_indptr, *, num_heads, nope_dim=128, 
         value_dim=value_dim, dtype=in_code, out_dtype=out_code,
         mask=L.PKA_MASK_CAUSAL if causal else L.PKA_MASK_DENSE,
         sm_scale=float("nan") if sm_scale is None else sm_scale, output_scale=output_scale,
-        return_lse=int(bool(return_lse)), flags=L.PKA_PLAN_HOST_ONLY if host_only else 0)
+        return_lse=int(bool(return_lse)), num_sms=num_sms,
+        flags=L.PKA_PLAN_HOST_ONLY if host_only else 0)
     h = ctypes.c_void_p()
+    ws = ctypes.c_size_t()
     nt = ctypes.c_int32()
     rc = L.lib().batch_latent_prefill_plan(ctypes.byref(h), ctypes.byref(d), qo_p, kv_p,
-                                           ctypes.byref(nt),
+                                           ctypes.byref(ws), ctypes.byref(nt),
                                            _stream(stream) if not host_only else None)
     L.check(rc, "batch_latent_prefill_plan")
-    return LatentPrefillPlan(h, d, nt.value, int(qo_t[-1]), int(kv_t[-1]))
+    return LatentPrefillPlan(h, d, nt.value, int(qo_t[-1]), int(kv_t[-1]), ws.value)
 
 
-def batch_latent_prefill_run(plan, q, k_nope, k_rope, v, out=None, lse=None, stream=None):
+def batch_latent_prefill_run(plan, q, k_nope, k_rope, v, out=None, lse=None, workspace=None,
+                             stream=None):
     """Run a planned latent prefill: ``q`` ``[Tq, H, nope + rope]``, ``k_nope``
     ``[Tk, H, nope]`` and ``v`` ``[Tk, H, value]`` with the same strides (the two parts of
     one projection's output, or two tensors alike), ``k_rope`` ``[Tk, rope]`` shared by the
@@ -808,7 +812,8 @@ def batch_latent_prefill_run(plan, q, k_nope, k_rope, v, out=None, lse=None, str
     a given ``out`` past the plan's are left as they were."""
     if stream is not None:
         with _on_stream(stream):
-            return batch_latent_prefill_run(plan, q, k_nope, k_rope, v, out=out, lse=lse)
+            return batch_latent_prefill_run(plan, q, k_nope, k_rope, v, out=out, lse=lse,
+                                            workspace=workspace)
     if not isinstance(plan, LatentPrefillPlan):
         raise ValueError("the plan was not made by batch_latent_prefill_plan")
     _check_tensors(plan.dtype, q=q, k_nope=k_nope, k_rope=k_rope, v=v)
@@ -846,9 +851,18 @@ def batch_latent_prefill_run(plan, q, k_nope, k_rope, v, out=None, lse=None, str
             raise ValueError("lse must be [Tq, H]")
     elif plan.return_lse:
         lse = torch.empty((T, plan.q_row[0]), dtype=torch.float32, device=q.device)
+    ws_bytes = 0
+    if workspace is not None:
+        _check_tensors(workspace.dtype, workspace=workspace)
+        _contiguous(workspace=workspace)
+        ws_bytes = workspace.numel() * workspace.element_size()
+    elif plan.workspace_bytes > 0:
+        ws_bytes = plan.workspace_bytes
+        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
     rc = L.lib().batch_latent_prefill_run(
         plan.handle, q.data_ptr(), q_tok, q_head, k_nope.data_ptr(), k_rope.data_ptr(), rope_tok,
-        v.data_ptr(), k_strides[0], k_strides[1], out.data_ptr(), _ptr(lse), _stream(stream))
+        v.data_ptr(), k_strides[0], k_strides[1], out.data_ptr(), _ptr(lse), _ptr(workspace),
+        ws_bytes, _stream(stream))
     L.check(rc, "batch_latent_prefill_run")
     return (out, lse) if plan.return_lse else out
 

@@ -149,7 +149,9 @@ int upload_prefill_plan(pka_prefill_plan& p, cudaStream_t stream) {
   const size_t off_whi = off_wlo + up256(n_win);
   const size_t n_map = p.row_map.size() * sizeof(int32_t);
   const size_t off_map = off_whi + up256(n_win);
-  const size_t off_status = off_map + up256(n_map);
+  const size_t n_deal[3] = {p.segments.size() * 4, p.part.size() * 4, p.cuts.size() * 4};
+  const size_t off_deal = off_map + up256(n_map);
+  const size_t off_status = off_deal + up256(n_deal[0]) + up256(n_deal[1]) + up256(n_deal[2]);
   const size_t total = off_status + 256;
   PKA_CUDA_TRY(cudaGetDevice(&p.device), "cudaGetDevice");
   PKA_CUDA_TRY(cudaMalloc(&p.dev_buf, total), "cudaMalloc(prefill plan)");
@@ -181,6 +183,14 @@ int upload_prefill_plan(pka_prefill_plan& p, cudaStream_t stream) {
                                  stream),
                  "cudaMemcpyAsync(row order)");
   }
+  const std::vector<int32_t>* deal[3] = {&p.segments, &p.part, &p.cuts};
+  const int32_t** deal_dev[3] = {&p.d_segments, &p.d_part, &p.d_cuts};
+  for (size_t i = 0, off = off_deal; i < 3; off += up256(n_deal[i++])) {
+    *deal_dev[i] = reinterpret_cast<const int32_t*>(base + off);
+    if (n_deal[i])
+      PKA_CUDA_TRY(cudaMemcpyAsync(base + off, deal[i]->data(), n_deal[i], cudaMemcpyHostToDevice, stream),
+                   "cudaMemcpyAsync(dealt tiles)");
+  }
   PKA_CUDA_TRY(cudaMemsetAsync(base + off_status, 0, 256, stream), "cudaMemsetAsync(status)");
   return PKA_OK;
 }
@@ -188,18 +198,21 @@ int upload_prefill_plan(pka_prefill_plan& p, cudaStream_t stream) {
 }  // namespace
 
 int pka::make_prefill_plan(pka_prefill_plan** plan_out, const pka_prefill_desc& desc,
-                           const int32_t* qo, const int32_t* kv, int32_t tile_q, bool by_head,
+                           const int32_t* qo, const int32_t* kv, bool latent,
                            int32_t* num_tiles_out, cudaStream_t stream) {
   *plan_out = nullptr;
   pka_prefill_plan* p = new (std::nothrow) pka_prefill_plan();
   if (p == nullptr) return fail(PKA_ERR_INVALID_ARG, "out of host memory");
-  int rc = build_prefill_plan(*p, desc, qo, kv, nullptr, nullptr, tile_q, by_head);
+  int rc = build_prefill_plan(*p, desc, qo, kv, nullptr, nullptr, latent ? 256 : 128, latent);
+  const int32_t num_tiles = (int32_t)p->tiles.size();
+  p->latent = latent;
+  if (rc == PKA_OK && latent) rc = deal_prefill_tiles(*p);
   if (rc == PKA_OK && !(desc.flags & PKA_PLAN_HOST_ONLY)) rc = upload_prefill_plan(*p, stream);
   if (rc != PKA_OK) {
     batch_prefill_plan_destroy(p);
     return rc;
   }
-  if (num_tiles_out) *num_tiles_out = (int32_t)p->tiles.size();
+  if (num_tiles_out) *num_tiles_out = num_tiles;
   *plan_out = p;
   return PKA_OK;
 }
@@ -572,7 +585,7 @@ int batch_prefill_plan(pka_prefill_plan** plan_out, const pka_prefill_desc* desc
   NvtxRange nvtx_range("pka::batch_prefill_plan");
   clear_error();
   PKA_CHECK_ARG(plan_out != nullptr && desc != nullptr, "plan_out and desc must not be NULL");
-  const int rc = make_prefill_plan(plan_out, *desc, qo_indptr_host, kv_indptr_host, 128, false,
+  const int rc = make_prefill_plan(plan_out, *desc, qo_indptr_host, kv_indptr_host, false,
                                    num_tiles_out, static_cast<cudaStream_t>(stream));
   if (rc == PKA_OK && workspace_bytes_out) *workspace_bytes_out = 0;
   return rc;

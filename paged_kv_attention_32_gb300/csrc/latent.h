@@ -68,6 +68,27 @@ struct LatentArgs {
   int32_t out_dtype;
 };
 
+// The pieces of one tile of a latent prefill that was cut along its keys (32 bytes).
+struct LatentPrefillCut {
+  int32_t head;
+  int32_t q_tile;    // 256-row tile index inside the request
+  int32_t q0;        // the request's first packed query row
+  int32_t lq;        // its query rows
+  int32_t part0;     // first of its partial states (256 rows each)
+  int32_t n_parts;
+  int32_t pad0, pad1;
+};
+
+struct LatentPrefillParts {
+  const int32_t* segments;       // where each pair's tiles but its first begin, then the tile count
+  const int32_t* part;           // per tile its partial state, -1 when it is whole
+  const LatentPrefillCut* cuts;
+  float* ws_o;                   // fp32 partial outputs [parts, 256, 128]
+  float* ws_lse;                 // fp32 partial base-2 LSEs [parts, 256]
+  int32_t num_segments;
+  int32_t num_cuts;
+};
+
 }  // namespace pka
 
 struct pka_latent_plan {
@@ -121,8 +142,8 @@ int launch_latent_append(const void* latent, int64_t latent_stride, const void* 
                          int32_t* status, cudaStream_t stream);
 
 // Expanded prefill over a prefill plan's tiles (heads of 128 + 64 key and 128
-// value dimensions).
-int launch_latent_prefill(const pka_prefill_plan& plan, const PrefillArgs& args,
+// value dimensions) and the merge of those that were cut.
+int launch_latent_prefill(const pka_prefill_plan& plan, const PrefillArgs& args, const LatentPrefillParts& parts,
                           const CUtensorMap& qmap, const CUtensorMap& kmap,
                           const CUtensorMap& rmap, const CUtensorMap& vmap, cudaStream_t stream);
 

@@ -81,6 +81,9 @@ int upload_latent_plan(pka_latent_plan& p, cudaStream_t stream) {
 
 }  // namespace
 
+// Partial outputs and LSEs of a latent prefill's pieces, 256 rows each.
+static size_t prefill_workspace(const pka_prefill_plan& p) { return (size_t)p.num_parts * 256 * 129 * sizeof(float); }
+
 extern "C" {
 
 // ---------------------------------------------------------------------------
@@ -352,7 +355,7 @@ int paged_latent_decode_run(const pka_latent_plan* p, const void* q, int64_t q_s
 
 int batch_latent_prefill_plan(pka_prefill_plan** plan_out, const pka_latent_prefill_desc* desc,
                               const int32_t* qo_indptr_host, const int32_t* kv_indptr_host,
-                              int32_t* num_tiles_out, void* stream) {
+                              size_t* workspace_bytes_out, int32_t* num_tiles_out, void* stream) {
   clear_error();
   PKA_CHECK_ARG(plan_out != nullptr && desc != nullptr, "plan_out and desc must not be NULL");
   *plan_out = nullptr;
@@ -373,15 +376,16 @@ int batch_latent_prefill_plan(pka_prefill_plan** plan_out, const pka_latent_pref
   d.sm_scale = std::isnan(desc->sm_scale) ? 1.0f / std::sqrt(128.0f + kLatentRopeDim) : desc->sm_scale;
   d.output_scale = desc->output_scale;
   d.return_lse = desc->return_lse;
+  d.num_sms = desc->num_sms;
   d.flags = desc->flags;
   d.out_dtype = desc->out_dtype;
   pka_prefill_plan* p = nullptr;
   const int rc = guarded([&] {
-    return make_prefill_plan(&p, d, qo_indptr_host, kv_indptr_host, 256, true,
-                             num_tiles_out, static_cast<cudaStream_t>(stream));
+    return make_prefill_plan(&p, d, qo_indptr_host, kv_indptr_host, true, num_tiles_out,
+                             static_cast<cudaStream_t>(stream));
   });
   if (rc != PKA_OK) return rc;
-  p->latent = true;
+  if (workspace_bytes_out) *workspace_bytes_out = prefill_workspace(*p);
   *plan_out = p;
   return PKA_OK;
 }
@@ -389,7 +393,8 @@ int batch_latent_prefill_plan(pka_prefill_plan** plan_out, const pka_latent_pref
 int batch_latent_prefill_run(const pka_prefill_plan* p, const void* q, int64_t q_stride_tok,
                              int64_t q_stride_head, const void* k_nope, const void* k_rope,
                              int64_t rope_stride, const void* v, int64_t kv_stride_tok,
-                             int64_t kv_stride_head, void* out, float* lse, void* stream) {
+                             int64_t kv_stride_head, void* out, float* lse, void* workspace,
+                             size_t workspace_bytes, void* stream) {
   NvtxRange nvtx_range("pka::batch_latent_prefill_run");
   clear_error();
   PKA_CHECK_ARG(p != nullptr, "plan must not be NULL");
@@ -404,6 +409,12 @@ int batch_latent_prefill_run(const pka_prefill_plan* p, const void* q, int64_t q
   int rc = check_device(p->device);
   if (rc != PKA_OK) return rc;
   if (p->tiles.empty()) return PKA_OK;
+  if (p->num_parts > 0) {
+    PKA_CHECK_ARG(workspace != nullptr && aligned(workspace, 256), "workspace must be 256-byte aligned");
+    if (workspace_bytes < prefill_workspace(*p))
+      return fail(PKA_ERR_WORKSPACE_TOO_SMALL, "workspace has %zu bytes, the plan needs %zu", workspace_bytes,
+                  prefill_workspace(*p));
+  }
   CUtensorMap qmap, kmap, rmap, vmap;
   const uint64_t H = (uint64_t)p->Hq, nk = (uint64_t)p->total_kv;
   const uint32_t qbox[3] = {64, 1, 128}, kbox[3] = {64, 1, 32}, vbox[3] = {64, 1, 64};
@@ -435,7 +446,6 @@ int batch_latent_prefill_run(const pka_prefill_plan* p, const void* q, int64_t q
   a.lse = p->desc.return_lse ? lse : nullptr;
   a.tiles = p->d_tiles;
   a.status = p->d_status;
-  a.num_tiles = (int32_t)p->tiles.size();
   a.num_qo_heads = p->Hq;
   a.num_kv_heads = p->Hkv;
   a.group = 1;
@@ -444,7 +454,15 @@ int batch_latent_prefill_run(const pka_prefill_plan* p, const void* q, int64_t q
   a.scale_log2 = p->scale * 1.4426950408889634f;
   a.output_scale = p->desc.output_scale;
   a.out_dtype = p->desc.out_dtype;
-  return launch_latent_prefill(*p, a, qmap, kmap, rmap, vmap, static_cast<cudaStream_t>(stream));
+  LatentPrefillParts parts{};
+  parts.segments = p->d_segments;
+  parts.part = p->d_part;
+  parts.cuts = reinterpret_cast<const LatentPrefillCut*>(p->d_cuts);
+  parts.ws_o = static_cast<float*>(workspace);
+  parts.ws_lse = parts.ws_o + (size_t)p->num_parts * 256 * 128;
+  parts.num_segments = (int32_t)p->segments.size() - 1;
+  parts.num_cuts = (int32_t)(p->cuts.size() * 4 / sizeof(LatentPrefillCut));
+  return launch_latent_prefill(*p, a, parts, qmap, kmap, rmap, vmap, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

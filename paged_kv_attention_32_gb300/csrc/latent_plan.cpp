@@ -11,6 +11,7 @@
 #include <algorithm>
 #include <cmath>
 #include <climits>
+#include <queue>
 
 #include "host_common.h"
 #include "latent.h"
@@ -22,6 +23,10 @@ constexpr int64_t kItemCost = 2;     // a piece's fixed cost, in tiles
 constexpr int64_t kMinPiece = 2;     // tiles below which a request is not cut further
 constexpr int32_t kMaxRows = 65536;
 constexpr int32_t kMaxSms = 1024;
+// the prefill's, in tiles of 64 keys for 256 rows
+constexpr int64_t kPrefillItemCost = 3;   // a piece's queries in and output out
+constexpr int64_t kPrefillMinPiece = 8;   // below which a tile is not cut further
+constexpr int64_t kPrefillCutCost = 12;   // the merge of pieces, whatever their number
 }  // namespace
 
 int build_latent_plan(pka_latent_plan& p, const pka_latent_desc& d_in, const int32_t* seq,
@@ -159,6 +164,95 @@ int build_latent_plan(pka_latent_plan& p, const pka_latent_desc& d_in, const int
   p.partial_rows = (int32_t)prow;
   p.ws_lse_offset = ceil_div(prow * d.latent_dim * 4, 256) * 256;
   p.workspace_bytes = prow ? p.ws_lse_offset + prow * 4 : 0;
+  return PKA_OK;
+}
+
+// Tiles in their order (by head, so that the tiles of a head run together), each to
+// the pair of CTAs that is free first.  Where that ends unevenly every pair gets the
+// same share instead, and the tile that fills one is cut there: what is left of it
+// goes to the next.
+int deal_prefill_tiles(pka_prefill_plan& p) {
+  PKA_CHECK_ARG(p.desc.num_sms >= 0 && p.desc.num_sms <= kMaxSms, "num_sms must be in [0, %d]", kMaxSms);
+  int sms = p.desc.num_sms;
+  if (sms == 0 && (p.desc.flags & PKA_PLAN_HOST_ONLY)) sms = 152;
+  if (sms == 0) {
+    int dev = 0;
+    PKA_CUDA_TRY(cudaGetDevice(&dev), "cudaGetDevice");
+    PKA_CUDA_TRY(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev),
+                 "cudaDeviceGetAttribute(SM count)");
+    sms = std::min(sms, kMaxSms);
+  }
+  if (p.tiles.empty()) {
+    p.segments.assign(1, 0);
+    return PKA_OK;
+  }
+  struct Piece {
+    int32_t tile, kv0, n;
+  };
+  using Slot = std::pair<int64_t, int32_t>;   // load, index: the least loaded first, then the first
+  std::vector<std::vector<Piece>> slots((size_t)sms);   // pairs of CTAs: two CTAs share an SM
+  const int32_t n_tiles = (int32_t)p.tiles.size();
+  int64_t cost = 0;
+  for (const PrefillTile& t : p.tiles) cost += t.n_kv + kPrefillItemCost;
+  // what every slot may take, INT64_MAX: nothing is cut; the longest load, or -1 if it does not fit
+  auto deal = [&](int64_t target) -> int64_t {
+    for (auto& s : slots) s.clear();
+    std::priority_queue<Slot, std::vector<Slot>, std::greater<Slot>> free;
+    for (int32_t i = 0; i < sms; ++i) free.push({0, i});
+    int64_t longest = 0;
+    for (int32_t i = 0; i < n_tiles; ++i) {
+      int64_t lo = 0;
+      const int64_t n = p.tiles[i].n_kv;
+      while (lo < n) {
+        if (free.empty()) return -1;
+        const Slot s = free.top();
+        free.pop();
+        const int64_t left = n - lo, room = target == INT64_MAX ? left : target - s.first - kPrefillItemCost;
+        if (room < std::min(left, kPrefillMinPiece)) continue;   // full
+        const int64_t take = left - room < kPrefillMinPiece ? left : room;
+        slots[(size_t)s.second].push_back(Piece{i, (int32_t)lo, (int32_t)take});
+        lo += take;
+        const int64_t load = s.first + take + kPrefillItemCost;
+        longest = std::max(longest, load);
+        if (load < target) free.push({load, s.second});
+      }
+    }
+    return longest;
+  };
+  const int64_t whole = deal(INT64_MAX);
+  int64_t target = std::max(ceil_div(cost, sms), kPrefillMinPiece + kPrefillItemCost);
+  if (whole > target + kPrefillCutCost) {
+    int64_t even;
+    while ((even = deal(target)) < 0) target += std::max<int64_t>(1, target / 64);
+    if (even + kPrefillCutCost >= whole) deal(INT64_MAX);   // not worth a merge
+  }
+  std::vector<int32_t> pieces((size_t)n_tiles, 0), first((size_t)n_tiles, -1), next((size_t)n_tiles, 0);
+  for (const auto& s : slots)
+    for (const Piece& c : s) ++pieces[(size_t)c.tile];
+  for (int32_t i = 0; i < n_tiles; ++i)
+    if (pieces[(size_t)i] > 1) {
+      const PrefillTile& t = p.tiles[(size_t)i];
+      first[(size_t)i] = p.num_parts;
+      for (int32_t word : {t.head, t.q_tile, t.q0, t.lq, p.num_parts, pieces[(size_t)i], 0, 0}) p.cuts.push_back(word);
+      p.num_parts += pieces[(size_t)i];
+    }
+  // every pair's first piece, then the others of the first pair, of the second, ...
+  std::vector<PrefillTile> dealt;
+  auto lay = [&](const Piece& c) {
+    dealt.push_back(p.tiles[(size_t)c.tile]);
+    dealt.back().kv0 += c.kv0;
+    dealt.back().n_kv = c.n;
+    p.part.push_back(first[(size_t)c.tile] < 0 ? -1 : first[(size_t)c.tile] + next[(size_t)c.tile]++);
+  };
+  for (const auto& s : slots)
+    if (!s.empty()) lay(s[0]);
+  p.segments.assign(1, (int32_t)dealt.size());
+  for (const auto& s : slots) {
+    if (s.empty()) continue;
+    for (size_t i = 1; i < s.size(); ++i) lay(s[i]);
+    p.segments.push_back((int32_t)dealt.size());
+  }
+  p.tiles = std::move(dealt);
   return PKA_OK;
 }
 

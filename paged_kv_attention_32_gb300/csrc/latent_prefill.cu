@@ -61,15 +61,16 @@ constexpr uint32_t kOffBar = kOffV + kVStages * kVBytes;
 constexpr size_t kSmemBytes = kOffBar + 256;
 static_assert(2 * (kSmemBytes + 1024) <= 228 * 1024, "two CTAs share an SM");
 
-// mbarriers.  Q, K, V and P are waited for by the leader's MMA warp, on the leader's
-// barriers, where both CTAs arrive; the others are signalled in both CTAs by the
-// commits.  Parity waits stay correct because every barrier has one waiting role
-// that waits for its phases in order; the O-done waits for P V of tile j - 1
-// come after S of tile j, issued after P V of tile j - 2.
+// mbarriers.  Q, K, V, P and O-free are waited for by the leader's MMA warp, on the
+// leader's barriers, where both CTAs arrive; the others are signalled in both CTAs by
+// the commits.  T counts a pair's key tiles over all its items: S, P and O barriers
+// T & 1.  No barrier runs a phase past one that somebody still has to see: S(T) is
+// issued behind P V(T - 2), P(T) written once S(T) is complete, the next item's Q
+// copied once this one's last S is complete and its first P V issued once O is free.
 enum {
-  B_Q = 0, B_KFULL = 1, B_KEMPTY = B_KFULL + kKStages, B_VFULL = B_KEMPTY + kKStages,
+  B_QFULL = 0, B_QFREE, B_OFREE, B_KFULL, B_KEMPTY = B_KFULL + kKStages, B_VFULL = B_KEMPTY + kKStages,
   B_VEMPTY = B_VFULL + kVStages, B_SFULL = B_VEMPTY + kVStages, B_PFULL = B_SFULL + 2,
-  B_ODONE = B_PFULL + 2, B_MMADONE = B_ODONE + 2, B_TAIL = B_MMADONE + 1, B_COUNT = B_TAIL + 1
+  B_ODONE = B_PFULL + 2, B_MMADONE = B_ODONE + 2, B_TAIL, B_COUNT
 };
 static_assert(B_COUNT * 8 + 4 <= 256, "barriers and the TMEM address slot");
 
@@ -91,7 +92,8 @@ struct RingPos {
 
 template <bool F16>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 2)
-latent_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant__ CUtensorMap tmq,
+latent_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant__ LatentPrefillParts parts,
+                      const __grid_constant__ CUtensorMap tmq,
                       const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmr,
                       const __grid_constant__ CUtensorMap tmv) {
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -101,13 +103,16 @@ latent_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_consta
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_rank();   // 0: the leader
-  const PrefillTile tile = a.tiles[blockIdx.x >> 1];
-  const int h = tile.head, n_kv = tile.n_kv, kv0 = tile.kv0;
-  const int q0 = tile.q0, Lq = tile.lq, k0 = tile.k0, Lk = tile.lk;
-  const int row0 = tile.q_tile * 2 * kTileQ + (int)rank * kTileQ;   // this CTA's first query row
+  // The pair's first tile lies at its own index, so that its loads need not wait for
+  // the list's; the others one behind the other from more0 on.
+  const int pair = blockIdx.x >> 1, more0 = __ldg(parts.segments + pair);
+  const int n_items = 1 + __ldg(parts.segments + pair + 1) - more0;
+  auto index = [&](int k) -> int { return k == 0 ? pair : more0 + k - 1; };
 
   if (tid == 0) {
-    mbar_init(bar(B_Q), 2);
+    mbar_init(bar(B_QFULL), 2);
+    mbar_init(bar(B_QFREE), 1);
+    mbar_init(bar(B_OFREE), 8);
     for (int s = 0; s < kKStages; ++s) {
       mbar_init(bar(B_KFULL + s), 2);
       mbar_init(bar(B_KEMPTY + s), 1);
@@ -134,65 +139,80 @@ latent_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_consta
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
+  // the merge's CTAs may start taking free SMs; they wait for this grid's end
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
   if (warp == 4) {
     // ---------------- TMA producer ----------------
-    if (lane == 0) {
-      tma_prefetch_desc(&tmq);
-      tma_prefetch_desc(&tmk);
-      tma_prefetch_desc(&tmr);
-      tma_prefetch_desc(&tmv);
-      const uint32_t full = map_to_rank(bar(B_Q), 0);
-      mbar_arrive_expect_tx_cluster(full, kQBlocks * kQBox);
-      for (int blk = 0; blk < kQBlocks; ++blk)
-        tma_load_3d_pair(sbase + kOffQ + (uint32_t)blk * kQBox, &tmq, full, blk * 64, h, q0 + row0);
-    }
-    __syncwarp();
+    if (lane < 4) tma_prefetch_desc(lane == 0 ? &tmq : lane == 1 ? &tmk : lane == 2 ? &tmr : &tmv);
     RingPos<kKStages> kp;
     RingPos<kVStages> vp;
-    auto load_k = [&](int j) -> bool {   // keys 32 rank .. 32 rank + 31 of tile j
-      if (j >= kKStages && !warp_wait(bar(B_KEMPTY + kp.slot), kp.parity ^ 1u, a.status)) return false;
-      if (lane == 0) {
-        const uint32_t dst = sbase + kOffK + (uint32_t)kp.slot * kKBytes;
-        const uint32_t full = map_to_rank(bar(B_KFULL + kp.slot), 0);
-        const int row = k0 + (kv0 + j) * kTileK + (int)rank * 32;
-        mbar_arrive_expect_tx_cluster(full, kKBytes);
-        tma_load_3d_pair(dst, &tmk, full, 0, h, row);
-        tma_load_3d_pair(dst + kKBox, &tmk, full, 64, h, row);
-        tma_load_3d_pair(dst + 2 * kKBox, &tmr, full, 0, 0, row);
-      }
-      __syncwarp();
-      kp.next();
-      return true;
-    };
-    auto load_v = [&](int j) -> bool {   // dimensions 64 rank .. 64 rank + 63 of tile j
-      if (j >= kVStages && !warp_wait(bar(B_VEMPTY + vp.slot), vp.parity ^ 1u, a.status)) return false;
-      const uint32_t off = kOffV + (uint32_t)vp.slot * kVBytes;
-      const uint32_t full = map_to_rank(bar(B_VFULL + vp.slot), 0);
-      const int past = (kv0 + j + 1) * kTileK - Lk;   // rows of the tile past the last key
-      if (lane == 0) {
-        if (past > 0) mbar_arrive_expect_tx(bar(B_TAIL), kVBytes);
-        else mbar_arrive_expect_tx_cluster(full, kVBytes);
-        tma_load_3d_pair(sbase + off, &tmv, past > 0 ? map_to_rank(bar(B_TAIL), rank) : full,
-                         (int)rank * 64, h, k0 + (kv0 + j) * kTileK);
-      }
-      __syncwarp();
-      if (past > 0) {   // the last tile: another request's values, p = 0 there, but 0 * inf is not 0
-        if (!warp_wait(bar(B_TAIL), 0, a.status)) return false;
-        for (int c = lane; c < past * 8; c += 32)
-          *reinterpret_cast<uint4*>(smem + off + (uint32_t)(kTileK - past + (c >> 3)) * 128u +
-                                    (uint32_t)(c & 7) * 16u) = make_uint4(0u, 0u, 0u, 0u);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(full);
-      }
-      vp.next();
-      return true;
-    };
-    // order K0 K1 V0 K2 V1 ...: S of tile j + 2 is issued after P V of tile j
+    int nk = 0, nv = 0, tails = 0;   // stages filled so far, cleared tiles
     bool ok = true;
-    for (int j = 0; ok && j < n_kv + 1; ++j) {
-      if (j < n_kv) ok = load_k(j);
-      if (ok && j > 0) ok = load_v(j - 1);
+    PrefillTile tile = a.tiles[pair];
+    for (int i = 0; ok && i < n_items; ++i) {
+      const PrefillTile next = a.tiles[i + 1 < n_items ? index(i + 1) : pair];
+      const int h = tile.head, n_kv = tile.n_kv, key_tile0 = tile.kv0, Lk = tile.lk;
+      const int row0 = tile.q0 + (tile.q_tile * 2 + (int)rank) * kTileQ;   // this CTA's first query row
+      auto load_q = [&]() -> bool {
+        if (i > 0 && !warp_wait(bar(B_QFREE), (uint32_t)((i - 1) & 1), a.status)) return false;
+        if (lane == 0) {
+          const uint32_t full = map_to_rank(bar(B_QFULL), 0);
+          mbar_arrive_expect_tx_cluster(full, kQBlocks * kQBox);
+          for (int blk = 0; blk < kQBlocks; ++blk)
+            tma_load_3d_pair(sbase + kOffQ + (uint32_t)blk * kQBox, &tmq, full, blk * 64, h, row0);
+        }
+        __syncwarp();
+        return true;
+      };
+      auto load_k = [&](int j) -> bool {   // keys 32 rank .. 32 rank + 31 of tile j
+        if (nk >= kKStages && !warp_wait(bar(B_KEMPTY + kp.slot), kp.parity ^ 1u, a.status)) return false;
+        if (lane == 0) {
+          const uint32_t dst = sbase + kOffK + (uint32_t)kp.slot * kKBytes;
+          const uint32_t full = map_to_rank(bar(B_KFULL + kp.slot), 0);
+          const int row = tile.k0 + (key_tile0 + j) * kTileK + (int)rank * 32;
+          mbar_arrive_expect_tx_cluster(full, kKBytes);
+          tma_load_3d_pair(dst, &tmk, full, 0, h, row);
+          tma_load_3d_pair(dst + kKBox, &tmk, full, 64, h, row);
+          tma_load_3d_pair(dst + 2 * kKBox, &tmr, full, 0, 0, row);
+        }
+        __syncwarp();
+        kp.next();
+        ++nk;
+        return true;
+      };
+      auto load_v = [&](int j) -> bool {   // dimensions 64 rank .. 64 rank + 63 of tile j
+        if (nv >= kVStages && !warp_wait(bar(B_VEMPTY + vp.slot), vp.parity ^ 1u, a.status)) return false;
+        const uint32_t off = kOffV + (uint32_t)vp.slot * kVBytes;
+        const uint32_t full = map_to_rank(bar(B_VFULL + vp.slot), 0);
+        const int past = (key_tile0 + j + 1) * kTileK - Lk;   // rows of the tile past the last key
+        if (lane == 0) {
+          if (past > 0) mbar_arrive_expect_tx(bar(B_TAIL), kVBytes);
+          else mbar_arrive_expect_tx_cluster(full, kVBytes);
+          tma_load_3d_pair(sbase + off, &tmv, past > 0 ? map_to_rank(bar(B_TAIL), rank) : full,
+                           (int)rank * 64, h, tile.k0 + (key_tile0 + j) * kTileK);
+        }
+        __syncwarp();
+        if (past > 0) {   // a last tile: another request's values, p = 0 there, but 0 * inf is not 0
+          if (!warp_wait(bar(B_TAIL), (uint32_t)(tails++ & 1), a.status)) return false;
+          for (int c = lane; c < past * 8; c += 32)
+            *reinterpret_cast<uint4*>(smem + off + (uint32_t)(kTileK - past + (c >> 3)) * 128u +
+                                      (uint32_t)(c & 7) * 16u) = make_uint4(0u, 0u, 0u, 0u);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(full);
+        }
+        vp.next();
+        ++nv;
+        return true;
+      };
+      // order K0 Q K1 V0 K2 V1 ...: S of tile j + 2 is issued after P V of tile j
+      for (int j = 0; ok && j < n_kv + 1; ++j) {
+        if (j < n_kv) ok = load_k(j);
+        if (ok && j == 0) ok = load_q();
+        if (ok && j > 0) ok = load_v(j - 1);
+      }
+      tile = next;
     }
     // When a wait gave up, copies still in flight land before the cluster leaves:
     // their barriers may be the other CTA's, so there is only time to go by.
@@ -206,38 +226,49 @@ latent_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_consta
     if (rank == 0) {
       RingPos<kKStages> kp;
       RingPos<kVStages> vp;
-      auto issue_qk = [&](int j) -> bool {   // S of tile j into buffer j & 1
-        const uint32_t d = tmem + (uint32_t)(j & 1) * 64u;
-        if (!warp_wait(bar(B_KFULL + kp.slot), kp.parity, a.status)) return false;
-        tc_fence_after();
+      int T = 0;   // key tiles before this one
+      bool ok = true;
+      int n_kv = __ldg(&a.tiles[pair].n_kv);
+      for (int i = 0; ok && i < n_items; ++i) {
+        const int next_n = __ldg(&a.tiles[i + 1 < n_items ? index(i + 1) : pair].n_kv);
+        auto issue_qk = [&](int j) -> bool {   // S of tile j into buffer (T + j) & 1
+          if (!warp_wait(bar(B_KFULL + kp.slot), kp.parity, a.status)) return false;
+          tc_fence_after();
+          const int st = (T + j) & 1;
 #pragma unroll
-        for (int blk = 0; blk < kQBlocks; ++blk)
-          umma_pair_ss_k4(d, smem_desc_sw128(sbase + kOffQ + (uint32_t)blk * kQBox, 16u, 1024u),
-                          smem_desc_sw128(sbase + kOffK + (uint32_t)kp.slot * kKBytes + (uint32_t)blk * kKBox,
-                                          16u, 1024u),
-                          kIdescQK<F16>, blk > 0 ? 1u : 0u);
-        umma_pair_commit_elect(bar(B_SFULL + (j & 1)));
-        umma_pair_commit_elect(bar(B_KEMPTY + kp.slot));
-        kp.next();
-        return true;
-      };
-      bool ok = warp_wait(bar(B_Q), 0, a.status);
-      for (int j = 0; ok && j < n_kv && j < 2; ++j) ok = issue_qk(j);
-      for (int j = 0; ok && j < n_kv; ++j) {
-        const int st = j & 1;
-        ok = warp_wait(bar(B_VFULL + vp.slot), vp.parity, a.status) &&
-             warp_wait(bar(B_PFULL + st), (uint32_t)((j >> 1) & 1), a.status);
-        if (!ok) break;
-        tc_fence_after();
-        // 4 k-steps of 16 keys: P columns +8, V rows +16 (2048 bytes)
-        umma_pair_ts_k4<2048 / 16>(tmem + kColO, tmem + (uint32_t)st * 64u,
-                                   smem_desc_sw128(sbase + kOffV + (uint32_t)vp.slot * kVBytes, kVBytes, 1024u),
-                                   kIdescPV<F16>, j > 0 ? 1u : 0u);
-        umma_pair_commit_elect(bar(B_ODONE + st));
-        umma_pair_commit_elect(bar(B_VEMPTY + vp.slot));
-        vp.next();
-        // S buffer st is free again once this P V has read P (issue order)
-        if (j + 2 < n_kv) ok = issue_qk(j + 2);
+          for (int blk = 0; blk < kQBlocks; ++blk)
+            umma_pair_ss_k4(tmem + (uint32_t)st * 64u,
+                            smem_desc_sw128(sbase + kOffQ + (uint32_t)blk * kQBox, 16u, 1024u),
+                            smem_desc_sw128(sbase + kOffK + (uint32_t)kp.slot * kKBytes + (uint32_t)blk * kKBox,
+                                            16u, 1024u),
+                            kIdescQK<F16>, blk > 0 ? 1u : 0u);
+          umma_pair_commit_elect(bar(B_SFULL + st));
+          umma_pair_commit_elect(bar(B_KEMPTY + kp.slot));
+          if (j == n_kv - 1) umma_pair_commit_elect(bar(B_QFREE));
+          kp.next();
+          return true;
+        };
+        ok = warp_wait(bar(B_QFULL), (uint32_t)(i & 1), a.status);
+        for (int j = 0; ok && j < n_kv && j < 2; ++j) ok = issue_qk(j);
+        for (int j = 0; ok && j < n_kv; ++j) {
+          const int st = (T + j) & 1;
+          ok = warp_wait(bar(B_VFULL + vp.slot), vp.parity, a.status) &&
+               warp_wait(bar(B_PFULL + st), (uint32_t)(((T + j) >> 1) & 1), a.status);
+          if (ok && j == 0 && i > 0) ok = warp_wait(bar(B_OFREE), (uint32_t)((i - 1) & 1), a.status);
+          if (!ok) break;
+          tc_fence_after();
+          // 4 k-steps of 16 keys: P columns +8, V rows +16 (2048 bytes)
+          umma_pair_ts_k4<2048 / 16>(tmem + kColO, tmem + (uint32_t)st * 64u,
+                                     smem_desc_sw128(sbase + kOffV + (uint32_t)vp.slot * kVBytes, kVBytes, 1024u),
+                                     kIdescPV<F16>, j > 0 ? 1u : 0u);
+          umma_pair_commit_elect(bar(B_ODONE + st));
+          umma_pair_commit_elect(bar(B_VEMPTY + vp.slot));
+          vp.next();
+          // S buffer st is free again once this P V has read P (issue order)
+          if (j + 2 < n_kv) ok = issue_qk(j + 2);
+        }
+        T += n_kv;
+        n_kv = next_n;
       }
       umma_pair_commit_elect(bar(B_MMADONE));
     }
@@ -245,126 +276,104 @@ latent_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_consta
     warp_wait(bar(B_MMADONE), 0, a.status);
   } else {
     // ---------------- softmax: one thread per query row ----------------
-    const int t = row0 + tid;   // row of the request
-    const bool row_valid = t < Lq;
-    const int hi = a.causal ? min(Lk, Lk - Lq + t + 1) : Lk;   // keys [0, hi) visible
     const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
     const uint32_t o_tm = tmem + lane_off + kColO;
     const float sl2 = a.scale_log2;
-    float m_ref = neg_inf(), l = 0.f;
+    int T = 0;   // key tiles before this one
     bool ok = true;
-    for (int j = 0; j < n_kv; ++j) {
-      const int st = j & 1;
-      if (!(ok = warp_wait(bar(B_SFULL + st), (uint32_t)((j >> 1) & 1), a.status))) break;
-      tc_fence_after();
-      const uint32_t s_tm = tmem + lane_off + (uint32_t)st * 64u;
-      const int key0 = (kv0 + j) * kTileK;
-      const bool masked = __any_sync(0xffffffffu, key0 + kTileK > hi);   // warp-uniform
-      uint32_t ra[32], rb[32];
-      tmem_ld32(s_tm, ra);
-      tmem_ld32(s_tm + 32u, rb);
-      tmem_wait_ld();
-      reg_fence32(ra);
-      reg_fence32(rb);
-      uint32_t w0 = 0xffffffffu, w1 = 0xffffffffu;
-      if (masked) {
-        visible_bits(key0, 0, (unsigned)hi, w0, w1);
-        mask_scores64(ra, rb, w0, w1);
-      }
-      const float mraw = row_max64(ra, rb);
-      const float mx = mraw == neg_inf() ? neg_inf() : mraw * sl2;
-      const bool grow = mx > m_ref + kRescaleThreshold;
-      const float m_new = grow ? mx : m_ref;
-      const bool rescale = grow && m_ref != neg_inf();   // else O and l are still zero
-      const float alpha = rescale ? ex2(m_ref - m_new) : 1.f;
-      if (j > 0 && __any_sync(0xffffffffu, rescale)) {
-        // O holds tiles before j: wait for P V of tile j - 1 before rescaling
-        if (!(ok = warp_wait(bar(B_ODONE + ((j - 1) & 1)), (uint32_t)(((j - 1) >> 1) & 1),
-                             a.status)))
-          break;
+    PrefillTile tile = a.tiles[pair];
+    int part = __ldg(parts.part + pair);
+    for (int i = 0; ok && i < n_items; ++i) {
+      const int after = i + 1 < n_items ? index(i + 1) : pair;
+      const PrefillTile next = a.tiles[after];
+      const int next_part = __ldg(parts.part + after), n_kv = tile.n_kv;
+      const int r = (int)rank * kTileQ + tid;                // row of the tile
+      const int t = tile.q_tile * 2 * kTileQ + r;            // row of the request
+      const int hi = a.causal ? min(tile.lk, tile.lk - tile.lq + t + 1) : tile.lk;   // keys [0, hi) visible
+      float m_ref = neg_inf(), l = 0.f;
+      for (int j = 0; j < n_kv; ++j, ++T) {
+        const int st = T & 1;
+        if (!(ok = warp_wait(bar(B_SFULL + st), (uint32_t)((T >> 1) & 1), a.status))) break;
         tc_fence_after();
-#pragma unroll 1
-        for (int c = 0; c < kDV / 32; ++c) {
-          uint32_t r[32];
-          tmem_ld32_sync(o_tm + (uint32_t)c * 32u, r);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
-          tmem_st32(o_tm + (uint32_t)c * 32u, r);
+        const uint32_t s_tm = tmem + lane_off + (uint32_t)st * 64u;
+        const int key0 = (tile.kv0 + j) * kTileK;
+        const bool masked = __any_sync(0xffffffffu, key0 + kTileK > hi);   // warp-uniform
+        uint32_t ra[32], rb[32];
+        tmem_ld32(s_tm, ra);
+        tmem_ld32(s_tm + 32u, rb);
+        tmem_wait_ld();
+        reg_fence32(ra);
+        reg_fence32(rb);
+        uint32_t w0 = 0xffffffffu, w1 = 0xffffffffu;
+        if (masked) {
+          visible_bits(key0, 0, (unsigned)hi, w0, w1);
+          mask_scores64(ra, rb, w0, w1);
         }
+        const float mraw = row_max64(ra, rb);
+        const float mx = mraw == neg_inf() ? neg_inf() : mraw * sl2;
+        const bool grow = mx > m_ref + kRescaleThreshold;
+        const float m_new = grow ? mx : m_ref;
+        const bool rescale = grow && m_ref != neg_inf();   // else O and l are still zero
+        const float alpha = rescale ? ex2(m_ref - m_new) : 1.f;
+        if (j > 0 && __any_sync(0xffffffffu, rescale)) {
+          // O holds the tiles before: wait for P V of the last of them before rescaling
+          if (!(ok = warp_wait(bar(B_ODONE + (st ^ 1)), (uint32_t)(((T - 1) >> 1) & 1), a.status))) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < kDV / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32_sync(o_tm + (uint32_t)c * 32u, o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+            tmem_st32(o_tm + (uint32_t)c * 32u, o);
+          }
+          tmem_wait_st();
+        }
+        m_ref = m_new;
+        // A row with no visible key so far keeps m_ref = -inf: exp2(-inf) = 0.
+        // Masked scores give 0 through their -inf unless the scale is 0.
+        const float neg_m = m_ref == neg_inf() ? 0.f : -m_ref;
+        const bool zero_again = masked && !(sl2 > 0.f);
+        const float2 sum = zero_again ? exp_tile<true, F16>(ra, rb, sl2, neg_m, w0, w1, s_tm)
+                                      : exp_tile<false, F16>(ra, rb, sl2, neg_m, w0, w1, s_tm);
         tmem_wait_st();
+        l = l * alpha + (sum.x + sum.y);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(map_to_rank(bar(B_PFULL + st), 0));
       }
-      m_ref = m_new;
-      // A row with no visible key so far keeps m_ref = -inf: exp2(-inf) = 0.
-      // Masked scores give 0 through their -inf unless the scale is 0.
-      const float neg_m = m_ref == neg_inf() ? 0.f : -m_ref;
-      const bool zero_again = masked && !(sl2 > 0.f);
-      const float2 sum = zero_again ? exp_tile<true, F16>(ra, rb, sl2, neg_m, w0, w1, s_tm)
-                                    : exp_tile<false, F16>(ra, rb, sl2, neg_m, w0, w1, s_tm);
-      tmem_wait_st();
-      l = l * alpha + (sum.x + sum.y);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_remote(map_to_rank(bar(B_PFULL + st), 0));
-    }
-    if (ok && n_kv > 0 &&
-        warp_wait(bar(B_ODONE + ((n_kv - 1) & 1)), (uint32_t)(((n_kv - 1) >> 1) & 1), a.status)) {
+      if (!ok || !(ok = warp_wait(bar(B_ODONE + ((T - 1) & 1)), (uint32_t)(((T - 1) >> 1) & 1), a.status))) break;
       tc_fence_after();
       // != and not >: a sum that is NaN stays one, in the LSE as in the output
-      const float inv = l != 0.f ? a.output_scale / l : 0.f;
-      if (a.out_dtype == PKA_DTYPE_F32) {
-        const int64_t dst = ((int64_t)(q0 + t) * a.num_qo_heads + h) * kDV;
+      const float inv = l != 0.f ? (part < 0 ? a.output_scale : 1.f) / l : 0.f;
+      const float lse = l != 0.f ? m_ref + log2f(l) : neg_inf();
+      const bool row_valid = t < tile.lq;
+      const int64_t orow = (int64_t)(tile.q0 + t) * a.num_qo_heads + tile.head;
+      const int64_t prow = (int64_t)part * (2 * kTileQ) + r;
 #pragma unroll 1
-        for (int c = 0; c < kDV / 32; ++c) {
-          uint32_t r[32];
-          tmem_ld32_sync(o_tm + (uint32_t)c * 32u, r);
-          if (row_valid) {
+      for (int c = 0; c < kDV / 32; ++c) {
+        uint32_t o[32];
+        tmem_ld32_sync(o_tm + (uint32_t)c * 32u, o);
+        if (row_valid) {
 #pragma unroll
-            for (int qd = 0; qd < 2; ++qd) {
-              float f[16];
+          for (int qd = 0; qd < 2; ++qd) {
+            float f[16];
 #pragma unroll
-              for (int x = 0; x < 16; ++x) f[x] = __uint_as_float(r[16 * qd + x]);
-              store_out<16>(a.out, dst + c * 32 + qd * 16, f, inv, a.out_dtype);
-            }
+            for (int x = 0; x < 16; ++x) f[x] = __uint_as_float(o[16 * qd + x]);
+            if (part < 0) store_out<16>(a.out, orow * kDV + c * 32 + qd * 16, f, inv, a.out_dtype);
+            else store_out<16>(parts.ws_o, prow * kDV + c * 32 + qd * 16, f, inv, PKA_DTYPE_F32);
           }
-        }
-      } else {
-        // each warp stages its 32 rows in the Q buffer (every QK has completed),
-        // 16-byte chunks XOR-swizzled by row, then writes whole 256-byte rows
-        constexpr int kRowBytes = kDV * 2;
-        uint8_t* wbuf = smem + kOffQ + (uint32_t)warp * 32u * kRowBytes;
-        const bool f16o = a.out_dtype == PKA_DTYPE_F16;
-#pragma unroll 1
-        for (int c = 0; c < kDV / 32; ++c) {
-          uint32_t r[32];
-          tmem_ld32_sync(o_tm + (uint32_t)c * 32u, r);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {   // 8 values = one 16-byte chunk
-            uint32_t w[4];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const float lo = __uint_as_float(r[8 * k + 2 * x]) * inv;
-              const float hi2 = __uint_as_float(r[8 * k + 2 * x + 1]) * inv;
-              w[x] = f16o ? pack2<true>(lo, hi2) : pack2<false>(lo, hi2);
-            }
-            *reinterpret_cast<uint4*>(wbuf + lane * kRowBytes + (((c * 4 + k) ^ (lane & 7)) << 4)) =
-                make_uint4(w[0], w[1], w[2], w[3]);
-          }
-        }
-        __syncwarp();
-        const int q = lane % 16;
-#pragma unroll 4
-        for (int r0 = 0; r0 < 32; r0 += 2) {
-          const int rr = r0 + lane / 16, tr = row0 + warp * 32 + rr;
-          const uint4 val =
-              *reinterpret_cast<const uint4*>(wbuf + rr * kRowBytes + ((q ^ (rr & 7)) << 4));
-          if (tr < Lq)
-            *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) +
-                                      ((int64_t)(q0 + tr) * a.num_qo_heads + h) * kRowBytes +
-                                      q * 16) = val;
         }
       }
-      if (row_valid && a.lse != nullptr)
-        a.lse[(int64_t)(q0 + t) * a.num_qo_heads + h] = l != 0.f ? m_ref + log2f(l) : neg_inf();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote(map_to_rank(bar(B_OFREE), 0));
+      if (row_valid) {
+        if (part >= 0) parts.ws_lse[prow] = lse;
+        else if (a.lse != nullptr) a.lse[orow] = lse;
+      }
+      tile = next;
+      part = next_part;
     }
   }
 
@@ -377,20 +386,69 @@ latent_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_consta
   }
 }
 
+// The pieces of the tiles that were cut: out = sum_c w_c o_c / sum_c w_c with
+// w_c = 2^(lse_c - max), a warp a row, four values a lane.  Launched while the
+// prefill still runs, it waits for that grid's end.
+constexpr int kMergeRows = 8;   // rows, and warps, of a CTA
+__global__ void __launch_bounds__(kMergeRows * 32)
+latent_prefill_merge_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant__ LatentPrefillParts parts) {
+  constexpr int kCtas = 2 * kTileQ / kMergeRows;
+  const int lane = threadIdx.x & 31, r = (int)(blockIdx.x % kCtas) * kMergeRows + (threadIdx.x >> 5);
+  const LatentPrefillCut cut = parts.cuts[blockIdx.x / kCtas];
+  const int t = cut.q_tile * 2 * kTileQ + r;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (t >= cut.lq) return;
+  const int64_t p0 = (int64_t)cut.part0 * (2 * kTileQ) + r;
+  float m = neg_inf(), sum = 0.f;
+  for (int c = lane; c < cut.n_parts; c += 32) m = fmaxf(m, __ldcg(parts.ws_lse + p0 + (int64_t)c * (2 * kTileQ)));
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+  float o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int c = 0; c < cut.n_parts; ++c) {
+    const int64_t p = p0 + (int64_t)c * (2 * kTileQ);
+    const float lse = __ldcg(parts.ws_lse + p);
+    const float4 v = __ldcg(reinterpret_cast<const float4*>(parts.ws_o + p * kDV) + lane);
+    if (lse != neg_inf()) {   // else the piece weighs nothing
+      const float w = ex2(lse - m);
+      sum += w;
+      o[0] += w * v.x;
+      o[1] += w * v.y;
+      o[2] += w * v.z;
+      o[3] += w * v.w;
+    }
+  }
+  const int64_t row = (int64_t)(cut.q0 + t) * a.num_qo_heads + cut.head;
+  store_out<4>(a.out, row * kDV + lane * 4, o, sum != 0.f ? a.output_scale / sum : 0.f, a.out_dtype);
+  if (lane == 0 && a.lse != nullptr) a.lse[row] = sum != 0.f ? m + log2f(sum) : neg_inf();
+}
+
 }  // namespace
 
-int launch_latent_prefill(const pka_prefill_plan& plan, const PrefillArgs& args,
+int launch_latent_prefill(const pka_prefill_plan& plan, const PrefillArgs& args, const LatentPrefillParts& parts,
                           const CUtensorMap& qmap, const CUtensorMap& kmap,
                           const CUtensorMap& rmap, const CUtensorMap& vmap, cudaStream_t stream) {
-  if (args.num_tiles == 0) return PKA_OK;
   const bool f16 = plan.desc.dtype == PKA_DTYPE_F16;
   auto kern = f16 ? latent_prefill_kernel<true> : latent_prefill_kernel<false>;
   static std::atomic<uint64_t> smem_set[2];   // per input type: devices whose limit was raised
   cudaError_t e = set_smem_once(kern, (int)kSmemBytes, smem_set[f16]);
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(latent_prefill)");
-  kern<<<2 * args.num_tiles, kThreads, kSmemBytes, stream>>>(args, qmap, kmap, rmap, vmap);
+  kern<<<2 * parts.num_segments, kThreads, kSmemBytes, stream>>>(args, parts, qmap, kmap, rmap, vmap);
   e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "latent_prefill_kernel launch");
+  if (parts.num_cuts > 0) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)parts.num_cuts * (2 * kTileQ / kMergeRows));
+    cfg.blockDim = dim3(kMergeRows * 32);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, latent_prefill_merge_kernel, args, parts);
+    if (e != cudaSuccess) return cuda_fail(e, "latent_prefill_merge_kernel launch");
+  }
   return PKA_OK;
 }
 

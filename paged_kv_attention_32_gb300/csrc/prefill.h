@@ -69,7 +69,16 @@ struct pka_prefill_plan {
   const int32_t* d_row_map = nullptr;
   int32_t* d_status = nullptr;
   int device = -1;
-  bool latent = false;   // made by batch_latent_prefill_plan: run by its own entry point
+  // made by batch_latent_prefill_plan, run by its own entry point: every pair of CTAs'
+  // first tile, then the further ones of each pair; some cut along their keys
+  bool latent = false;
+  int32_t num_parts = 0;
+  std::vector<int32_t> segments;         // where each pair's further tiles begin, then the tile count
+  std::vector<int32_t> part;             // per tile its partial state or -1
+  std::vector<int32_t> cuts;             // LatentPrefillCut, 8 words each
+  const int32_t* d_segments = nullptr;
+  const int32_t* d_part = nullptr;
+  const int32_t* d_cuts = nullptr;
 };
 
 namespace pka {
@@ -82,11 +91,14 @@ int build_prefill_plan(pka_prefill_plan& plan, const pka_prefill_desc& desc, con
                        const int32_t* win_hi = nullptr, int32_t tile_q = 128,
                        bool by_head = false);
 
-// Builds a packed prefill plan of tiles of tile_q rows and, unless it is a
-// host-only one, uploads it (batch_prefill_plan: 128, not by head).
+// Gives the tiles of a plan of 256-row tiles to pairs of CTAs (num_sms from the
+// description, 0: the device's), cut along their keys where that evens them out.
+int deal_prefill_tiles(pka_prefill_plan& plan);
+
+// Builds a packed prefill plan and, unless it is a host-only one, uploads it.
+// latent: tiles of 256 rows by head, dealt out, instead of 128 heaviest first.
 int make_prefill_plan(pka_prefill_plan** plan_out, const pka_prefill_desc& desc, const int32_t* qo,
-                      const int32_t* kv, int32_t tile_q, bool by_head, int32_t* num_tiles_out,
-                      cudaStream_t stream);
+                      const int32_t* kv, bool latent, int32_t* num_tiles_out, cudaStream_t stream);
 
 // Launches the prefill kernel (one query head and 128 rows per CTA, 64-key
 // tiles; head_dim 128 or 256) over the plan's tiles.

@@ -504,7 +504,7 @@ def test_decode_plan_update_and_refusals():
 # ---- expanded prefill ----------------------------------------------------------------
 
 def check_prefill(lq, lk, heads, causal=True, dtype=BF, out_dtype=None, scale=None, out_scale=1.0,
-                  seed=0, rows=None, fused=True):
+                  seed=0, rows=None, fused=True, num_sms=0, cut=None):
     g = torch.Generator(device=DEV).manual_seed(seed)
     qo, ko = [0], [0]
     for a, b in zip(lq, lk):
@@ -517,7 +517,8 @@ def check_prefill(lq, lk, heads, causal=True, dtype=BF, out_dtype=None, scale=No
     rope = torch.randn((ko[-1], 96), generator=g, device=DEV).to(dtype)[:, 16:80]
     plan = api.batch_latent_prefill_plan(qo, ko, num_heads=heads, causal=causal, sm_scale=scale,
                                          output_scale=out_scale, return_lse=True, dtype=dtype,
-                                         out_dtype=out_dtype)
+                                         out_dtype=out_dtype, num_sms=num_sms)
+    assert cut is None or (plan.workspace_bytes > 0) == cut
     out, lse = api.batch_latent_prefill_run(plan, q, k, rope, v)
     plan.check()
     scale = 192 ** -0.5 if scale is None else scale
@@ -542,6 +543,65 @@ def test_prefill_types(dtype, out_dtype):
 @pytest.mark.parametrize("scale", [0.0, 0.3, 3.0])
 def test_prefill_scales(scale):
     check_prefill([100], [150], 2, scale=scale)
+
+
+@pytest.mark.parametrize("num_sms,cut", [(1, False), (2, False), (16, True), (152, True)])
+@pytest.mark.parametrize("causal,dtype,out_dtype", [(True, BF, BF), (False, HF, FP), (True, HF, BF)])
+def test_prefill_tiles_cut_along_their_keys(num_sms, cut, causal, dtype, out_dtype):
+    """From one pair of CTAs that takes every tile in turn to many that share few."""
+    check_prefill([130, 1, 300], [3000, 2000, 777], 3, causal, dtype, out_dtype, out_scale=0.5,
+                  num_sms=num_sms, cut=cut)
+
+
+def test_prefill_of_one_row_behind_many_keys():
+    check_prefill([1], [20000], 1, num_sms=152, cut=True)
+
+
+@pytest.mark.parametrize("scale", [0.0, 3.0])
+def test_prefill_scales_of_cut_tiles(scale):
+    check_prefill([100], [3000], 2, scale=scale, num_sms=16, cut=True)
+
+
+def test_prefill_cut_tiles_given_a_workspace_captured_and_in_two_streams():
+    lq, lk = [200, 40], [2500, 900]
+    qo, ko = [0, 200, 240], [0, 2500, 3400]
+    g = torch.Generator(device=DEV).manual_seed(5)
+    q = torch.randn((240, 2, 192), generator=g, device=DEV).to(BF)
+    kv = torch.randn((3400, 2, 256), generator=g, device=DEV).to(BF)
+    rope = torch.randn((3400, 64), generator=g, device=DEV).to(BF)
+    k, v = kv[..., :128], kv[..., 128:]
+    plan = api.batch_latent_prefill_plan(qo, ko, num_heads=2, return_lse=True, num_sms=24)
+    assert plan.workspace_bytes > 0
+    run = api.batch_latent_prefill_run
+    with pytest.raises(L.PkaError) as e:
+        run(plan, q, k, rope, v, workspace=torch.zeros(16, dtype=torch.uint8, device=DEV))
+    assert e.value.code == L.PKA_ERR_WORKSPACE_TOO_SMALL
+    out, lse = run(plan, q, k, rope, v)
+    _, ref = ref_prefill(q, k, rope, v, qo, ko, 192 ** -0.5, True, 1.0, BF)
+    assert_within(out, lse, ref)
+    states = []
+    for i in range(2):   # each stream has a workspace and outputs of its own
+        states.append((torch.cuda.Stream(),
+                       torch.full((plan.workspace_bytes // 4,), float("nan"), device=DEV),
+                       torch.empty_like(out), torch.empty_like(lse)))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s, ws, o, x in states:
+            run(plan, q, k, rope, v, out=o, lse=x, workspace=ws, stream=s)
+    torch.cuda.synchronize()
+    for _, _, o, x in states:
+        assert torch.equal(o, out) and torch.equal(x, lse)
+    s, ws, o, x = states[0]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(plan, q, k, rope, v, out=o, lse=x, workspace=ws)
+    o.fill_(float("nan"))
+    x.fill_(float("nan"))
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(o, out) and torch.equal(x, lse)
+    plan.check()
 
 
 def test_prefill_long():
