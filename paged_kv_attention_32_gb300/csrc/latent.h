@@ -83,7 +83,7 @@ struct LatentPrefillParts {
   const int32_t* segments;       // where each pair's tiles but its first begin, then the tile count
   const int32_t* part;           // per tile its partial state, -1 when it is whole
   const LatentPrefillCut* cuts;
-  float* ws_o;                   // fp32 partial outputs [parts, 256, 128]
+  float* ws_o;                   // fp32 partial outputs [parts, 128 / 8, 256, 8]
   float* ws_lse;                 // fp32 partial base-2 LSEs [parts, 256]
   int32_t num_segments;
   int32_t num_cuts;

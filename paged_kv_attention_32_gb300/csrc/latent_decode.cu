@@ -1,6 +1,19 @@
 // Absorbed latent decode: s_j = scale * q . row_j over latent_dim + rope_dim
 // values, p = softmax(s), o = sum_j p_j row_j[0 .. latent_dim), all heads over
-// the same cached rows.
+// the same cached rows.  A CTA takes up to 64 query rows (token, head) of a request
+// and streams tiles of 64 keys past them, in the transposed form
+//   S^T = K Q^T      M=64 (keys), N rows, 576 or 320 columns deep
+//   O^T += V^T P^T   M=128 (latent dimensions), N rows, 64 keys deep
+// in which few rows are few columns.  A tile is copied once and is both operands.
+// The softmax keeps a running reference and sum per row in 32 bits; P is rounded to
+// the inputs' type, as they are.  What bounds it is HBM: 2 (latent_dim + 64) bytes a
+// key, however many rows share it.  Measured, 152 requests of 4096 keys in pages of 64:
+// 256 + 64 columns, 8 / 32 / 64 heads 64 / 65 / 68 us (6.2, 6.2, 6.0 TB/s; a copy
+// reaches 6.8); 512 + 64 columns 116 / 117 / 116 us (6.2, 6.2, 6.3 TB/s).  64 ragged
+// requests of 32 heads, 512 + 64: 64.5 us against a floor of 47.4: launch, first tile,
+// output and merge are the difference.
+// Warps: 0 copies, 1 issues S, 2 issues P V, then a group of four per 16 rows for the
+// softmax and the output.  TMEM columns: O^T (latent_dim / 128 blocks of N), two S.
 #include <algorithm>
 #include <type_traits>
 
@@ -214,6 +227,15 @@ latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant
       }
       ++I;
       PageWalk walk(a, pc, lane * a.box_rows, lane < boxes);
+      // With two stages the tile behind them is asked for in L2: one box at a time in
+      // flight a stage is too little for HBM (152 requests of 4096 keys, 64 heads, 512 +
+      // 64: 123 -> 116 us; a request of 131072 among 15 57.2 -> 58.4).  With three and more
+      // stages it costs more than it gives (512 + 64, 8 heads 116 -> 114; 256 + 64 64 -> 68).
+      // The other row blocks read the same keys at about the same time.
+      const bool ask_ahead = NS == 2 && rb == 0;
+      PageWalk ahead = walk;
+      if (ask_ahead)
+        for (int j = 0; j < NS; ++j) ahead.next_tile();
       for (int j = 0; j < pc.n; ++j) {
         const int page = walk.page, slot8 = walk.slot / 8;
         walk.next_tile();
@@ -230,6 +252,13 @@ latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant
           ++blocks;
         }
         if (!ok) break;
+        if (ask_ahead && j + NS < pc.n) {
+          if (lane < boxes) {
+            for (int h = 0; h < NH; ++h) tma_prefetch_5d(&maps.pool, 0, 0, 4 * h, ahead.slot / 8, ahead.page);
+            tma_prefetch_5d(&maps.pool_rope, 0, 0, 4 * NH, ahead.slot / 8, ahead.page);
+          }
+          ahead.next_tile();
+        }
         kp.next();
         ++nk;
       }
@@ -606,15 +635,17 @@ latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant
 // instructions: with four values a thread (each making every weight for itself)
 // the issue slots bounded it (5760 rows of 2-3 pieces of 512 values 9.5 us; with eight 7.0).  A
 // row of up to kLatentFewPieces (nearly all) is one CTA's, every LSE and four
-// pieces at a time asked for at once.  A row of more is shared out to DL / 16
-// CTAs of 16 dimensions, whose groups of four threads deal the pieces out; the
-// planner lists such requests first.  Launched while the decode still runs, it
+// pieces at a time asked for at once.  A row of more is shared out to CTAs of 64
+// dimensions each, whose groups of 16 threads deal the pieces out; the planner lists
+// such requests first.  Measured with 16 / 64 / 128 dimensions a CTA, 64 heads, the whole
+// decode: 16 requests in 9 pieces each 49 / 27 / 25 us, 4 in 38 43 / 31 / 32, one in 152
+// 53 / 53 / 59.  Launched while the decode still runs, it
 // waits for that grid's end.
 template <int DL>
 __global__ void __launch_bounds__(DL / 8, 1024 / (DL / 8))
 latent_merge_kernel(const __grid_constant__ LatentArgs a) {
-  constexpr int T = DL / 8, GROUPS = T / 4, SLABS = DL / 16;
-  __shared__ float4 s_o[GROUPS - 1][4];
+  constexpr int T = DL / 8, QUADS = 16, GROUPS = T / QUADS, SLABS = DL / 4 / QUADS;
+  __shared__ float4 s_o[GROUPS - 1][QUADS];
   const int tid = threadIdx.x, lane = tid & 31;
   const int many_ctas = a.num_many * a.max_rows * SLABS;
   const bool few = (int)blockIdx.x >= many_ctas;
@@ -687,7 +718,7 @@ latent_merge_kernel(const __grid_constant__ LatentArgs a) {
     if (tid == 0 && a.lse != nullptr) a.lse[row] = sum != 0.f ? m + log2f(sum) : neg_inf();
     return;
   }
-  const int g = tid >> 2, x = blockIdx.x % SLABS * 4 + (tid & 3);
+  const int g = tid / QUADS, x = blockIdx.x % SLABS * QUADS + tid % QUADS;
   constexpr int W = 8;   // pieces a thread has in flight
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f), v[W];
   auto ask = [&](int c0) {
@@ -722,7 +753,7 @@ latent_merge_kernel(const __grid_constant__ LatentArgs a) {
     for (int i = 0; i < W; ++i)
       if (s[i] != neg_inf()) add(o, ex2(s[i] - m), v[i]);
   }
-  if (g > 0) s_o[g - 1][tid & 3] = o;
+  if (g > 0) s_o[g - 1][tid % QUADS] = o;
   __syncthreads();
   if (g > 0) return;
 #pragma unroll
@@ -756,7 +787,7 @@ template <int DL>
 int launch_merge(const LatentArgs& a, cudaStream_t stream) {
   if (a.num_splits > 0) {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(a.num_splits + a.num_many * (DL / 16 - 1)) * (unsigned)a.max_rows);
+    cfg.gridDim = dim3((unsigned)(a.num_splits + a.num_many * (DL / 64 - 1)) * (unsigned)a.max_rows);
     cfg.blockDim = dim3(DL / 8);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];

@@ -4,14 +4,17 @@
 //   S = Q K^T    M=128 (rows), N=64 (keys), 576 or 320 columns deep
 //   O += P V     M=128 (rows), N=256 (latent dimensions), 64 keys deep
 //
-// With many rows the work is bound by what the tensor core reads from shared
-// memory.  The transposed kernel (latent_decode.cu) holds a tile once for 64
+// With many rows the work is bound by the shared-memory port.  The transposed kernel (latent_decode.cu) holds a tile once for 64
 // rows and reads 2 + 2 KB for each 64 x 64 x 16 step of S; here a CTA holds its
 // own 64 queries, half of the tile's keys (32) for S and half of the latent
 // dimensions (of all 64 keys) for P V, and the pair reads 3 KB a CTA for twice the
 // rows.  Measured per instruction: M=64 N=64 single 32 cycles; M=128 N=64 in a
 // pair 25, N=256 64.  The two halves overlap in a quarter of the tile, which
-// comes twice (from L2).
+// comes twice (from L2).  A tile's bytes through the port of a CTA: 108 KB of operands
+// of S, 48 of P V, 70 of copies and 8 of P, 1860 cycles at 128 B; the tensor core's own
+// time is 1430.  Measured: 64 ragged requests of 128 heads, 512 + 64 columns, 80 us (floor
+// 49.3, its 335 MB at the copy rate); 32 requests of 4 causal rows of 64 heads 126 us
+// (floor 83.5, its products at the library's rate).
 // Each CTA's warps:
 //   0  copies queries and its half of the keys;   3  its half of the values, which
 //      in the tile that holds the last key it clears past it (0 * inf is not 0)
@@ -163,6 +166,14 @@ latent_decode_pair_kernel(const __grid_constant__ LatentArgs a, const __grid_con
       }
       ++I;
       PageWalk walk(a, pc, (int)rank * 32 + lane * krows, lane < boxes);
+      // With two stages the tile behind them is asked for in L2 (both CTAs' keys are its
+      // values too): 76 requests of 4096 keys, 128 heads, 512 + 64 columns 75.9 -> 68.3 us;
+      // a tile further 68.3, two 70.1.  With four stages it costs more than it gives (256 +
+      // 64: 47.4 -> 48.4).  The other row blocks read the same keys at about the same time.
+      const bool ask_ahead = NS == 2 && rb == 0;
+      PageWalk ahead = walk;
+      if (ask_ahead)
+        for (int j = 0; j < NS; ++j) ahead.next_tile();
       for (int j = 0; j < pc.n; ++j) {
         const int page = walk.page, slot8 = walk.slot / 8;
         walk.next_tile();
@@ -173,6 +184,10 @@ latent_decode_pair_kernel(const __grid_constant__ LatentArgs a, const __grid_con
           tma_load_5d_pair(sbase + G::kOffK + (uint32_t)kp.slot * G::kK + (uint32_t)(lane * krows / 8) * G::kGroup,
                            &maps.keys, lead(R_KFULL + kp.slot), 0, 0, 0, slot8, page);
         __syncwarp();
+        if (ask_ahead && j + NS < pc.n) {
+          if (lane < boxes) tma_prefetch_5d(&maps.keys, 0, 0, 0, ahead.slot / 8, ahead.page);
+          ahead.next_tile();
+        }
         kp.next();
         ++nk;
       }

@@ -1,12 +1,12 @@
-// Host planner of the latent decode.
+// Host planners of the latent decode and prefill.  The decode's:
 //
 // All heads of a request read the same cached row, so a CTA takes a block of
 // up to 64 query rows (token, head), a pair of CTAs one of 128, and streams keys
 // past them.  Key tiles of 64 are dealt to as many segments of equal cost as there
-// are CTAs (pairs) per row block, each one of them for the whole run: requests are laid end to end and cut where a
-// segment is full, so at most two pieces of a segment belong to requests that
-// are cut, whatever the lengths.  A piece costs its tiles plus a fixed part
-// (its queries in, its output out).  The pieces of a cut request meet in a
+// are CTAs (pairs) per row block, each one of them for the whole run: requests are
+// laid end to end and cut where a segment is full, so at most two pieces of a segment
+// belong to requests that are cut, whatever the lengths.  A piece costs its tiles plus
+// a fixed part (its queries in, its output out).  The pieces of a cut request meet in a
 // merge over their base-2 LSEs.
 #include <algorithm>
 #include <cmath>
@@ -19,14 +19,19 @@
 namespace pka {
 
 namespace {
-constexpr int64_t kItemCost = 2;     // a piece's fixed cost, in tiles
-constexpr int64_t kMinPiece = 2;     // tiles below which a request is not cut further
+// A piece's fixed cost, in tiles.  Measured with 0 / 1 / 2 / 4: 64 ragged requests of 32
+// heads 67.7 / 66.9 / 66.7 / 67.0 us, of 128 heads 87.6 / 84.7 / 84.0 / 83.7, one of
+// 131072 keys among 15 59.3 / 57.7 / 57.5 / 58.2.
+constexpr int64_t kItemCost = 2;
+// Tiles below which a request is not cut further.  With 2 / 4 / 8: 4 short requests
+// 7.8 / 8.3 / 10.4 us, 64 ragged ones 65.2 / 66.7 / 68.0.
+constexpr int64_t kMinPiece = 2;
 constexpr int32_t kMaxRows = 65536;
 constexpr int32_t kMaxSms = 1024;
-// the prefill's, in tiles of 64 keys for 256 rows
-constexpr int64_t kPrefillItemCost = 3;   // a piece's queries in and output out
+// the prefill's, in tiles of 64 keys for 256 rows (0.4 us each where pairs share SMs)
+constexpr int64_t kPrefillItemCost = 3;   // a piece's queries in and output out: 1 and 6 measure alike
 constexpr int64_t kPrefillMinPiece = 8;   // below which a tile is not cut further
-constexpr int64_t kPrefillCutCost = 12;   // the merge of pieces, whatever their number
+constexpr int64_t kPrefillCutCost = 12;   // the merge of pieces: 4 to 8 us, whatever their number
 }  // namespace
 
 int build_latent_plan(pka_latent_plan& p, const pka_latent_desc& d_in, const int32_t* seq,
@@ -100,7 +105,12 @@ int build_latent_plan(pka_latent_plan& p, const pka_latent_desc& d_in, const int
                 (long long)max_rows, kMaxRows);
   p.total_q = indptr == nullptr ? B * d.q_len : indptr[B];
   p.max_rows = (int32_t)max_rows;
-  // up to 64 rows a CTA; more go to pairs of CTAs with 64 rows each
+  // The smallest block that holds a request's rows: fewer rows leave shared memory for
+  // more key stages (152 requests of 4096 keys, 512 + 64 columns: 116 us with 16 or 32
+  // rows, 124 with 64; a few short requests 7.8 us with 16 rows, 8.4 with 32).  More than
+  // 64 rows go to pairs of CTAs with 64 each (76 requests, 128 heads: 48.7 us against
+  // 57.9 for two blocks of 64 with 256 + 64 columns, 77 against 116 with 512 + 64); up to
+  // 64 leave half of a pair idle (152 requests, 48 heads: 87 us against 68, 143 against 125).
   p.row_tile = max_rows <= 16 ? 16 : max_rows <= 32 ? 32 : max_rows <= 64 ? 64 : 128;
   p.row_blocks = (int32_t)std::max<int64_t>(1, ceil_div(max_rows, p.row_tile));
 

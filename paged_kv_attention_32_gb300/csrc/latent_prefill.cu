@@ -10,15 +10,22 @@
 // S = Q K^T) and 64 of the value dimensions (half of N in O += P V).  What bounds
 // a single CTA's kernel is the shared-memory port, which the tensor core's
 // operands and the incoming copies share: per tile and CTA 48 KB of Q, 24 of K,
-// 16 of V and 40 of copies; in a pair 48 + 12 + 8 + 20.  Measured, 2 x 1024 rows
-// behind 7168 keys, 32 heads: 261 us with single CTAs, 229 in pairs (1397 TFLOP/s);
-// 8 ragged prompts of 512 to 4096: 445 and 441 (256-row tiles compute more beyond the
-// diagonal).  A pair's tile takes ~760 cycles an SM, the tensor core's own time at
-// N = 64 (12 products of 48 cycles and 4 of 64).
-// The shared rotary keys come in by their own tensor map as the third 64-column
-// block of a K tile: the concatenated key is never written anywhere.
-// Two CTAs of different pairs share an SM (113 KB, 256 TMEM columns each) and hide
-// each other's softmax latency.
+// 16 of V and 40 of copies; in a pair 48 + 12 + 8 + 20.  The shared rotary keys come
+// in by their own tensor map as the third 64-column block of a K tile: the
+// concatenated key is never written anywhere.  Two CTAs of different pairs share an
+// SM (113 KB, 256 TMEM columns each) and hide each other's softmax latency.
+// The host deals the tiles of 256 rows out to one wave of pairs, which take theirs in
+// turn, the next one's queries and keys copied while the last one ends; a tile that
+// fills a pair's share is cut there, along its keys, and its pieces are merged.
+//
+// Measured: 152 tiles of 2048 x 8192 keys 0.84 us a key tile and two pairs of an SM, as
+// many products a second as the library's bf16 product reaches (1890 TFLOP/s): the
+// tensor core bounds it.  2 x 1024 rows behind 7168 keys, 32 heads: 261 us with single
+// CTAs, 225 in pairs that took one tile each, 212 dealt out; 8 ragged prompts of 512 to
+// 4096: 445, 437, 397 (15 % of whose products lie beyond the diagonal); 4 prompts of
+// 512, 128 heads: 68 us, where the ends of the tiles count (74 with 16-byte stores).
+// Not kept: tiles of 128 keys, whose scores take a sixth less of the tensor core's
+// time but leave one S buffer: 232 and 475 us where tiles of 64 then took 225 and 437.
 //   warp 4      TMA producer of this CTA's halves; the tile that holds the last
 //               key it clears past it (0 * inf is not 0) before handing it over;
 //   warp 5      in the leader, issues every tcgen05.mma for both CTAs:
@@ -89,6 +96,18 @@ struct RingPos {
     }
   }
 };
+
+// 32 bytes by one store, or by two where the address is 16-byte aligned only.
+__device__ __forceinline__ void store_sector(void* dst, const uint32_t* w, bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]),
+                 "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    static_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    static_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
 
 template <bool F16>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 2)
@@ -279,6 +298,7 @@ latent_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_consta
     const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
     const uint32_t o_tm = tmem + lane_off + kColO;
     const float sl2 = a.scale_log2;
+    const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
     int T = 0;   // key tiles before this one
     bool ok = true;
     PrefillTile tile = a.tiles[pair];
@@ -349,27 +369,40 @@ latent_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_consta
       const float lse = l != 0.f ? m_ref + log2f(l) : neg_inf();
       const bool row_valid = t < tile.lq;
       const int64_t orow = (int64_t)(tile.q0 + t) * a.num_qo_heads + tile.head;
-      const int64_t prow = (int64_t)part * (2 * kTileQ) + r;
+      // Whole 32-byte sectors, one a store and lane.  A partial state is kept as blocks of
+      // 8 dimensions of all its rows, so that a warp's sectors are one run of 1 KB.
 #pragma unroll 1
-      for (int c = 0; c < kDV / 32; ++c) {
+      for (int c = 0; c < kDV; c += 32) {
         uint32_t o[32];
-        tmem_ld32_sync(o_tm + (uint32_t)c * 32u, o);
-        if (row_valid) {
+        tmem_ld32_sync(o_tm + (uint32_t)c, o);
 #pragma unroll
-          for (int qd = 0; qd < 2; ++qd) {
-            float f[16];
+        for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * inv);
+        if (!row_valid) continue;
+        if (part >= 0) {
+          float* dst = parts.ws_o + ((int64_t)part * kDV + c) * (2 * kTileQ) + r * 8;
 #pragma unroll
-            for (int x = 0; x < 16; ++x) f[x] = __uint_as_float(o[16 * qd + x]);
-            if (part < 0) store_out<16>(a.out, orow * kDV + c * 32 + qd * 16, f, inv, a.out_dtype);
-            else store_out<16>(parts.ws_o, prow * kDV + c * 32 + qd * 16, f, inv, PKA_DTYPE_F32);
+          for (int k = 0; k < 4; ++k) store_sector(dst + k * 8 * (2 * kTileQ), o + 8 * k, true);
+        } else if (a.out_dtype == PKA_DTYPE_F32) {
+          float* dst = static_cast<float*>(a.out) + orow * kDV + c;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) store_sector(dst + 8 * k, o + 8 * k, wide);
+        } else {
+          uint16_t* dst = static_cast<uint16_t*>(a.out) + orow * kDV + c;
+          uint32_t w[16];
+#pragma unroll
+          for (int x = 0; x < 16; ++x) {
+            const float lo = __uint_as_float(o[2 * x]), up = __uint_as_float(o[2 * x + 1]);
+            w[x] = a.out_dtype == PKA_DTYPE_F16 ? pack2<true>(lo, up) : pack2<false>(lo, up);
           }
+          store_sector(dst, w, wide);
+          store_sector(dst + 16, w + 8, wide);
         }
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_remote(map_to_rank(bar(B_OFREE), 0));
       if (row_valid) {
-        if (part >= 0) parts.ws_lse[prow] = lse;
+        if (part >= 0) parts.ws_lse[(int64_t)part * (2 * kTileQ) + r] = lse;
         else if (a.lse != nullptr) a.lse[orow] = lse;
       }
       tile = next;
@@ -387,40 +420,56 @@ latent_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_consta
 }
 
 // The pieces of the tiles that were cut: out = sum_c w_c o_c / sum_c w_c with
-// w_c = 2^(lse_c - max), a warp a row, four values a lane.  Launched while the
-// prefill still runs, it waits for that grid's end.
-constexpr int kMergeRows = 8;   // rows, and warps, of a CTA
-__global__ void __launch_bounds__(kMergeRows * 32)
+// w_c = 2^(lse_c - max).  A warp takes four rows: eight lanes read 128 bytes, 8
+// dimensions of all four, and a row belongs to the eight lanes with its (lane / 2) % 4,
+// 16 dimensions each.  Launched while the prefill still runs, it waits for that grid's
+// end.
+constexpr int kMergeWarps = 4, kMergeRows = 4 * kMergeWarps;
+__global__ void __launch_bounds__(kMergeWarps * 32)
 latent_prefill_merge_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant__ LatentPrefillParts parts) {
   constexpr int kCtas = 2 * kTileQ / kMergeRows;
-  const int lane = threadIdx.x & 31, r = (int)(blockIdx.x % kCtas) * kMergeRows + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, half = lane & 1, quarter = lane >> 3;
+  const int r = (int)(blockIdx.x % kCtas) * kMergeRows + (threadIdx.x >> 5) * 4 + ((lane >> 1) & 3);
   const LatentPrefillCut cut = parts.cuts[blockIdx.x / kCtas];
   const int t = cut.q_tile * 2 * kTileQ + r;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (t >= cut.lq) return;
-  const int64_t p0 = (int64_t)cut.part0 * (2 * kTileQ) + r;
+  if (t - ((lane >> 1) & 3) >= cut.lq) return;   // none of the warp's rows
+  const float* lse = parts.ws_lse + (int64_t)cut.part0 * (2 * kTileQ) + r;
+  const float* src = parts.ws_o + ((int64_t)cut.part0 * kDV + quarter * 8) * (2 * kTileQ) + r * 8 + half * 4;
+  const bool live = t < cut.lq;   // rows past the request's last were never written
   float m = neg_inf(), sum = 0.f;
-  for (int c = lane; c < cut.n_parts; c += 32) m = fmaxf(m, __ldcg(parts.ws_lse + p0 + (int64_t)c * (2 * kTileQ)));
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-  float o[4] = {0.f, 0.f, 0.f, 0.f};
+  if (live)
+    for (int c = quarter * 2 + half; c < cut.n_parts; c += 8) m = fmaxf(m, __ldcg(lse + (int64_t)c * (2 * kTileQ)));
+  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+  if (!live) return;
+  float o[4][4] = {};   // dimensions 32 i + 8 quarter + 4 half on
 #pragma unroll 4
   for (int c = 0; c < cut.n_parts; ++c) {
-    const int64_t p = p0 + (int64_t)c * (2 * kTileQ);
-    const float lse = __ldcg(parts.ws_lse + p);
-    const float4 v = __ldcg(reinterpret_cast<const float4*>(parts.ws_o + p * kDV) + lane);
-    if (lse != neg_inf()) {   // else the piece weighs nothing
-      const float w = ex2(lse - m);
+    const float x = __ldcg(lse + (int64_t)c * (2 * kTileQ));
+    const float* p = src + (int64_t)c * kDV * (2 * kTileQ);
+    float4 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __ldcg(reinterpret_cast<const float4*>(p + i * 32 * (2 * kTileQ)));
+    if (x != neg_inf()) {   // else the piece weighs nothing
+      const float w = ex2(x - m);
       sum += w;
-      o[0] += w * v.x;
-      o[1] += w * v.y;
-      o[2] += w * v.z;
-      o[3] += w * v.w;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        o[i][0] += w * v[i].x;
+        o[i][1] += w * v[i].y;
+        o[i][2] += w * v[i].z;
+        o[i][3] += w * v[i].w;
+      }
     }
   }
   const int64_t row = (int64_t)(cut.q0 + t) * a.num_qo_heads + cut.head;
-  store_out<4>(a.out, row * kDV + lane * 4, o, sum != 0.f ? a.output_scale / sum : 0.f, a.out_dtype);
-  if (lane == 0 && a.lse != nullptr) a.lse[row] = sum != 0.f ? m + log2f(sum) : neg_inf();
+  const float f = sum != 0.f ? a.output_scale / sum : 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    store_out<4>(a.out, row * kDV + i * 32 + quarter * 8 + half * 4, o[i], f, a.out_dtype);
+  if (quarter * 2 + half == 0 && a.lse != nullptr) a.lse[row] = sum != 0.f ? m + log2f(sum) : neg_inf();
 }
 
 }  // namespace
@@ -439,7 +488,7 @@ int launch_latent_prefill(const pka_prefill_plan& plan, const PrefillArgs& args,
   if (parts.num_cuts > 0) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)parts.num_cuts * (2 * kTileQ / kMergeRows));
-    cfg.blockDim = dim3(kMergeRows * 32);
+    cfg.blockDim = dim3(kMergeWarps * 32);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -282,6 +282,15 @@ def test_decode_split_over_the_length(num_sms, heads, dl):
         assert plan.info["num_split"] >= 1
 
 
+@pytest.mark.parametrize("dl", [256, 512])
+@pytest.mark.parametrize("batch,heads", [(1, 16), (5, 64), (24, 64), (3, 128), (24, 100)])
+def test_decode_requests_of_many_pieces(batch, heads, dl):
+    """Few and many rows of ten pieces and more: the merge shares them out differently."""
+    plan, _, _ = check_decode([2600 + 64 * b for b in range(batch)], [1] * batch, heads, dl=dl,
+                              num_sms=min(1024, 20 * batch * (2 if heads > 64 else 1)))
+    assert plan.info["num_split"] == batch and plan.info["num_items"] >= 9 * batch
+
+
 @pytest.mark.parametrize("live", [[2000, 5, 64], [1, 0, 63], [1999, 900, 0], [640, 128, 1]])
 @pytest.mark.parametrize("heads", [16, 64, 128])
 def test_decode_live_lengths(live, heads):
@@ -602,6 +611,22 @@ def test_prefill_cut_tiles_given_a_workspace_captured_and_in_two_streams():
     torch.cuda.synchronize()
     assert torch.equal(o, out) and torch.equal(x, lse)
     plan.check()
+
+
+@pytest.mark.parametrize("out_dtype", [BF, FP])
+def test_prefill_output_that_is_16_byte_aligned_only(out_dtype):
+    g = torch.Generator(device=DEV).manual_seed(6)
+    q, k, v = (torch.randn((150, 3, n), generator=g, device=DEV).to(BF) for n in (192, 128, 128))
+    rope = torch.randn((150, 64), generator=g, device=DEV).to(BF)
+    plan = api.batch_latent_prefill_plan([0, 150], [0, 150], num_heads=3, out_dtype=out_dtype)
+    want = api.batch_latent_prefill_run(plan, q, k, rope, v)
+    shift = 16 // want.element_size()
+    room = torch.zeros(want.numel() + 2 * shift, dtype=out_dtype, device=DEV)
+    out = room[shift:shift + want.numel()].view(want.shape)
+    assert out.data_ptr() % 32 == 16
+    api.batch_latent_prefill_run(plan, q, k, rope, v, out=out)
+    assert torch.equal(out, want)
+    assert bool((room[:shift] == 0).all()) and bool((room[-shift:] == 0).all())
 
 
 def test_prefill_long():
