@@ -740,7 +740,7 @@ int paged_latent_decode_plan_check(const pka_latent_plan* plan, void* stream);
  *            16-byte aligned, strides multiples of 8.
  * pages      the latent pool, stride_page as above.
  * block_tables, bt_row_stride, seq_lens_kv_dev as for paged_decode_run.
- *            Entries past a request's last page are not read; cache rows past
+ *            Entries past a request's last page are not used; cache rows past
  *            its last token may hold anything, infinities and NaN included.
  *            Rows before it enter every query row of the request: a causal row's
  *            weight of a later key is 0, and 0 times an infinity is NaN.

@@ -25,6 +25,16 @@ struct LatentItem {
   int32_t part;      // which of the request's partial states, -1 when it is whole
 };
 
+// The same on the device, with what a CTA needs of the request (32 bytes): one load
+// and not a chain of three behind the launch.
+struct LatentPiece {
+  int32_t request;
+  int32_t tile_lo;
+  int32_t tile_hi;
+  int32_t part;
+  int32_t q_start, q_len, kv_len, part_base;   // of LatentReq
+};
+
 // Per-request data (32 bytes).
 struct LatentReq {
   int32_t q_start;    // first packed query row
@@ -46,9 +56,8 @@ struct LatentArgs {
   float* lse;                    // nullptr: no LSE output
   float* ws_o;                   // fp32 partial outputs [partial_rows, latent_dim]
   float* ws_lse;                 // fp32 partial base-2 LSEs [partial_rows]
-  const LatentItem* items;
-  const int32_t* segments;       // first item of each segment, then the item count
-  const LatentReq* reqs;
+  const LatentPiece* pieces;     // the first of each segment, then its further ones by segment
+  const int32_t* more;           // where each segment's further pieces begin, then their end
   const LatentReq* splits;       // the requests cut into pieces, those of many first
   int32_t* status;
   int32_t num_segments;
@@ -100,12 +109,11 @@ struct pka_latent_plan {
   std::vector<pka::LatentItem> items;
   std::vector<int32_t> segments;
   std::vector<pka::LatentReq> reqs, splits;
-  // one device allocation: items | segments | requests | splits | status word
+  // one device allocation: pieces | further pieces' offsets | splits | status word
   void* dev_buf = nullptr;
   size_t dev_capacity = 0;
-  const pka::LatentItem* d_items = nullptr;
-  const int32_t* d_segments = nullptr;
-  const pka::LatentReq* d_reqs = nullptr;
+  const pka::LatentPiece* d_pieces = nullptr;
+  const int32_t* d_more = nullptr;
   const pka::LatentReq* d_splits = nullptr;
   int32_t* d_status = nullptr;
   int device = -1;

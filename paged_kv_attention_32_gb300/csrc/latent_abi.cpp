@@ -34,12 +34,11 @@ bool overlap(const void* p, size_t n, const void* q, size_t m) {
 // One asynchronous copy of the plan's arrays from a pinned image, which is
 // rewritten only after the copy that last read it has completed.
 int upload_latent_plan(pka_latent_plan& p, cudaStream_t stream) {
-  const size_t n_items = p.items.size() * sizeof(LatentItem);
-  const size_t n_segs = p.segments.size() * sizeof(int32_t);
-  const size_t n_reqs = p.reqs.size() * sizeof(LatentReq);
+  const size_t n_pieces = p.items.size() * sizeof(LatentPiece);
+  const size_t n_more = p.segments.size() * sizeof(int32_t);
   const size_t n_splits = p.splits.size() * sizeof(LatentReq);
-  const size_t off_segs = up256(n_items), off_reqs = off_segs + up256(n_segs);
-  const size_t off_splits = off_reqs + up256(n_reqs), off_status = off_splits + up256(n_splits);
+  const size_t off_more = up256(n_pieces), off_splits = off_more + up256(n_more);
+  const size_t off_status = off_splits + up256(n_splits);
   const size_t total = off_status + 256;
   if (p.stage_done != nullptr)
     PKA_CUDA_TRY(cudaEventSynchronize(p.stage_done), "cudaEventSynchronize(plan upload)");
@@ -59,15 +58,26 @@ int upload_latent_plan(pka_latent_plan& p, cudaStream_t stream) {
     PKA_CUDA_TRY(cudaMallocHost(&p.host_stage, cap), "cudaMallocHost(plan image)");
   }
   uint8_t* base = static_cast<uint8_t*>(p.dev_buf);
-  p.d_items = reinterpret_cast<const LatentItem*>(base);
-  p.d_segments = reinterpret_cast<const int32_t*>(base + off_segs);
-  p.d_reqs = reinterpret_cast<const LatentReq*>(base + off_reqs);
+  p.d_pieces = reinterpret_cast<const LatentPiece*>(base);
+  p.d_more = reinterpret_cast<const int32_t*>(base + off_more);
   p.d_splits = reinterpret_cast<const LatentReq*>(base + off_splits);
   p.d_status = reinterpret_cast<int32_t*>(base + off_status);
   uint8_t* img = static_cast<uint8_t*>(p.host_stage);
-  if (n_items) std::memcpy(img, p.items.data(), n_items);
-  std::memcpy(img + off_segs, p.segments.data(), n_segs);
-  std::memcpy(img + off_reqs, p.reqs.data(), n_reqs);
+  LatentPiece* pieces = reinterpret_cast<LatentPiece*>(img);
+  int32_t* more = reinterpret_cast<int32_t*>(img + off_more);
+  auto piece = [&](int32_t i) {
+    const LatentItem& it = p.items[(size_t)i];
+    const LatentReq& r = p.reqs[(size_t)it.request];
+    return LatentPiece{it.request, it.tile_lo, it.tile_hi, it.part, r.q_start, r.q_len, r.kv_len, r.part_base};
+  };
+  const int32_t segs = (int32_t)p.segments.size() - 1;
+  int32_t at = segs;
+  for (int32_t s = 0; s < segs; ++s) {   // no segment is empty
+    more[s] = at;
+    pieces[s] = piece(p.segments[(size_t)s]);
+    for (int32_t i = p.segments[(size_t)s] + 1; i < p.segments[(size_t)s + 1]; ++i) pieces[at++] = piece(i);
+  }
+  more[segs] = at;
   if (n_splits) std::memcpy(img + off_splits, p.splits.data(), n_splits);
   std::memset(img + off_status, 0, 256);
   PKA_CUDA_TRY(cudaMemcpyAsync(base, img, total, cudaMemcpyHostToDevice, stream),
@@ -326,9 +336,8 @@ int paged_latent_decode_run(const pka_latent_plan* p, const void* q, int64_t q_s
   a.ws_lse = workspace ? reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) +
                                                   p->ws_lse_offset)
                        : nullptr;
-  a.items = p->d_items;
-  a.segments = p->d_segments;
-  a.reqs = p->d_reqs;
+  a.pieces = p->d_pieces;
+  a.more = p->d_more;
   a.splits = p->d_splits;
   a.status = p->d_status;
   a.num_segments = (int32_t)p->segments.size() - 1;

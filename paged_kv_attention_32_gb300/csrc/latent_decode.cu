@@ -169,7 +169,7 @@ latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = tid >> 5;   // 0: copies, 1: S, 2: P V, then the softmax groups
   const int seg = blockIdx.x / a.row_blocks, rb = blockIdx.x % a.row_blocks;
-  const int item0 = __ldg(a.segments + seg), item1 = __ldg(a.segments + seg + 1);
+  const Pieces pieces(a, seg);
 
   if (tid == 0) {
     for (int s = 0; s < 12; ++s) {
@@ -208,8 +208,8 @@ latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant
     Ring<NS> kp;
     int nk = 0, blocks = 0, I = 0;   // stages and blocks asked for so far, pieces
     bool ok = true;
-    for (int item = item0; ok && item < item1; ++item) {
-      const Piece pc(a, item, rb, N);
+    for (int item = 0; ok && pieces.has(item); ++item) {
+      const Piece pc(a, pieces[item], rb, N);
       if (pc.n == 0) continue;
       if (a.q_box > 0) {   // whole groups of 8 heads: the queries come by TMA too
         if (I > 0 && !(ok = warp_wait(bar(L_QFREE), (uint32_t)((I - 1) & 1), a.status))) break;
@@ -237,7 +237,7 @@ latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant
       if (ask_ahead)
         for (int j = 0; j < NS; ++j) ahead.next_tile();
       for (int j = 0; j < pc.n; ++j) {
-        const int page = walk.page, slot8 = walk.slot / 8;
+        const int page = walk.page(), slot8 = walk.slot / 8;
         walk.next_tile();
         const uint32_t dst = sbase + (uint32_t)kp.slot * G::kTile;
         for (int h = 0; h <= NH; ++h) {   // blocks in the order P V lets go of them
@@ -254,8 +254,8 @@ latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant
         if (!ok) break;
         if (ask_ahead && j + NS < pc.n) {
           if (lane < boxes) {
-            for (int h = 0; h < NH; ++h) tma_prefetch_5d(&maps.pool, 0, 0, 4 * h, ahead.slot / 8, ahead.page);
-            tma_prefetch_5d(&maps.pool_rope, 0, 0, 4 * NH, ahead.slot / 8, ahead.page);
+            for (int h = 0; h < NH; ++h) tma_prefetch_5d(&maps.pool, 0, 0, 4 * h, ahead.slot / 8, ahead.page());
+            tma_prefetch_5d(&maps.pool_rope, 0, 0, 4 * NH, ahead.slot / 8, ahead.page());
           }
           ahead.next_tile();
         }
@@ -293,8 +293,8 @@ latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant
     Ring<NS> kp;
     int T = 0, I = 0;   // tiles and non-empty pieces before this one
     bool ok = true;
-    for (int item = item0; ok && item < item1; ++item) {
-      const Piece pc(a, item, rb, N);
+    for (int item = 0; ok && pieces.has(item); ++item) {
+      const Piece pc(a, pieces[item], rb, N);
       if (pc.n == 0) continue;
       ok = warp_wait(bar(L_QFULL), (uint32_t)(I & 1), a.status);
       ++I;
@@ -332,8 +332,8 @@ latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant
     Ring<NS> kp;
     int T = 0, I = 0;
     bool ok = true;
-    for (int item = item0; ok && item < item1; ++item) {
-      const Piece pc(a, item, rb, N);
+    for (int item = 0; ok && pieces.has(item); ++item) {
+      const Piece pc(a, pieces[item], rb, N);
       if (pc.n == 0) continue;
       for (int j = 0; j < pc.n; ++j, ++T) {
         ok = warp_wait(bar(L_PFULL + (T & 1)), (uint32_t)((T >> 1) & 1), a.status);
@@ -395,8 +395,8 @@ latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant
     bool ok = true;
     auto next_q = [&](int item) {
       if (a.q_box > 0) return;
-      for (; item < item1; ++item) {
-        const Piece pc(a, item, rb, N);
+      for (; pieces.has(item); ++item) {
+        const Piece pc(a, pieces[item], rb, N);
         if (pc.n > 0) {
           if (I > 0 && !warp_wait(bar(L_QFREE), (uint32_t)((I - 1) & 1), a.status)) s_fail[2] = 1;
           load_q(pc);
@@ -404,12 +404,12 @@ latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant
         }
       }
     };
-    next_q(item0);
+    next_q(0);
 
     Ring<NS> kp;
     int T = 0;
-    for (int item = item0; ok && item < item1; ++item) {
-      const Piece pc(a, item, rb, N);
+    for (int item = 0; ok && pieces.has(item); ++item) {
+      const Piece pc(a, pieces[item], rb, N);
       if (pc.rows <= 0) continue;
       const bool whole = pc.part < 0;
       const int64_t orow = (int64_t)pc.rq.q_start * a.num_heads + pc.row0;   // first output row
@@ -635,8 +635,8 @@ latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant
 // instructions: with four values a thread (each making every weight for itself)
 // the issue slots bounded it (5760 rows of 2-3 pieces of 512 values 9.5 us; with eight 7.0).  A
 // row of up to kLatentFewPieces (nearly all) is one CTA's, every LSE and four
-// pieces at a time asked for at once.  A row of more is shared out to CTAs of 64
-// dimensions each, whose groups of 16 threads deal the pieces out; the planner lists
+// pieces at a time asked for at once.  A row of more is shared out to 8 CTAs of 64 (32)
+// dimensions, whose four groups of threads deal the pieces out; the planner lists
 // such requests first.  Measured with 16 / 64 / 128 dimensions a CTA, 64 heads, the whole
 // decode: 16 requests in 9 pieces each 49 / 27 / 25 us, 4 in 38 43 / 31 / 32, one in 152
 // 53 / 53 / 59.  Launched while the decode still runs, it
@@ -644,7 +644,8 @@ latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant
 template <int DL>
 __global__ void __launch_bounds__(DL / 8, 1024 / (DL / 8))
 latent_merge_kernel(const __grid_constant__ LatentArgs a) {
-  constexpr int T = DL / 8, QUADS = 16, GROUPS = T / QUADS, SLABS = DL / 4 / QUADS;
+  constexpr int T = DL / 8, GROUPS = 4, QUADS = T / GROUPS, SLABS = 8;
+  static_assert(SLABS * QUADS * 4 == DL, "every dimension once");
   __shared__ float4 s_o[GROUPS - 1][QUADS];
   const int tid = threadIdx.x, lane = tid & 31;
   const int many_ctas = a.num_many * a.max_rows * SLABS;
@@ -787,7 +788,7 @@ template <int DL>
 int launch_merge(const LatentArgs& a, cudaStream_t stream) {
   if (a.num_splits > 0) {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(a.num_splits + a.num_many * (DL / 64 - 1)) * (unsigned)a.max_rows);
+    cfg.gridDim = dim3((unsigned)(a.num_splits + a.num_many * 7) * (unsigned)a.max_rows);   // 8 CTAs a row of many
     cfg.blockDim = dim3(DL / 8);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];

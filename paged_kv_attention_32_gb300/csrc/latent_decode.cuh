@@ -42,21 +42,30 @@ __device__ __forceinline__ bool bar_any_group(int g, bool mine) {
   return any != 0;
 }
 
+// The pieces of a segment.  The first lies at the segment's own index, so that its
+// load does not wait for the list's.
+struct Pieces {
+  int seg, more, count;
+  __device__ __forceinline__ Pieces(const LatentArgs& a, int segment)
+      : seg(segment), more(__ldg(a.more + segment)), count(1 + __ldg(a.more + segment + 1) - more) {}
+  __device__ __forceinline__ int operator[](int i) const { return i == 0 ? seg : more + i - 1; }
+  __device__ __forceinline__ bool has(int i) const { return i == 0 || i < count; }
+};
+
 // What a CTA needs to know of its piece.
 struct Piece {
-  LatentReq rq;
+  LatentPiece rq;
   int request, kv, tile0, n, part, row0, rows;   // rows: live rows of the CTA's row block
   __device__ __forceinline__ Piece(const LatentArgs& a, int item, int row_block, int row_tile) {
-    const LatentItem it = a.items[item];
-    rq = a.reqs[it.request];
-    request = it.request;
-    part = it.part;
+    rq = a.pieces[item];
+    request = rq.request;
+    part = rq.part;
     kv = rq.kv_len;
     if (a.seq_lens_live != nullptr) kv = min(max(__ldg(a.seq_lens_live + request), 0), kv);
     row0 = row_block * row_tile;
     rows = min(row_tile, rq.q_len * a.num_heads - row0);
-    tile0 = it.tile_lo;
-    n = rows > 0 ? max(0, min(it.tile_hi, (kv + kLatentTile - 1) / kLatentTile) - tile0) : 0;
+    tile0 = rq.tile_lo;
+    n = rows > 0 ? max(0, min(rq.tile_hi, (kv + kLatentTile - 1) / kLatentTile) - tile0) : 0;
   }
 };
 
@@ -66,19 +75,22 @@ struct Piece {
 // from there brings zeros.
 struct PageWalk {
   const int32_t* table;
-  int page, slot;                       // of the current tile's token
-  int tok, idx, kv, ps, step_pages, step_slots, none;
+  int raw, slot;                        // table entry and slot of the current tile's token
+  int tok, idx, kv, planned, ps, step_pages, step_slots, none;
   bool in;
   __device__ __forceinline__ PageWalk(const LatentArgs& a, const Piece& pc, int offset, bool active)
       : table(a.block_tables + (int64_t)pc.request * a.bt_row_stride), tok(pc.tile0 * kLatentTile + offset),
-        kv(pc.kv), ps(a.page_size), none(a.num_pages), in(active) {
+        kv(pc.kv), planned(pc.rq.kv_len), ps(a.page_size), none(a.num_pages), in(active) {
     idx = tok / ps;
     slot = tok - idx * ps;
     step_pages = kLatentTile / ps;
     step_slots = kLatentTile - step_pages * ps;
-    page = entry();
+    raw = entry();
   }
-  __device__ __forceinline__ int entry() const { return in && tok < kv ? __ldg(table + idx) : none; }
+  // Asked for by the planned length, which the table covers, so as not to wait for the
+  // live one, and looked at no sooner than it is used.
+  __device__ __forceinline__ int entry() const { return in && tok < planned ? __ldg(table + idx) : none; }
+  __device__ __forceinline__ int page() const { return tok < kv ? raw : none; }
   __device__ __forceinline__ void next_tile() {
     tok += kLatentTile;
     idx += step_pages;
@@ -87,7 +99,7 @@ struct PageWalk {
       slot -= ps;
       ++idx;
     }
-    page = entry();
+    raw = entry();
   }
 };
 

@@ -109,7 +109,7 @@ latent_decode_pair_kernel(const __grid_constant__ LatentArgs a, const __grid_con
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_rank();   // 0: the leader
   const int pair = blockIdx.x >> 1, seg = pair / a.row_blocks, rb = pair % a.row_blocks;
-  const int item0 = __ldg(a.segments + seg), item1 = __ldg(a.segments + seg + 1);
+  const Pieces pieces(a, seg);
 
   if (tid == 0) {
     for (int s = 0; s < 4; ++s) {
@@ -150,8 +150,8 @@ latent_decode_pair_kernel(const __grid_constant__ LatentArgs a, const __grid_con
     Ring<NS> kp;
     int nk = 0, I = 0;   // stages filled so far, pieces
     bool ok = true;
-    for (int item = item0; ok && item < item1; ++item) {
-      const Piece pc(a, item, rb, 2 * kRows);
+    for (int item = 0; ok && pieces.has(item); ++item) {
+      const Piece pc(a, pieces[item], rb, 2 * kRows);
       if (pc.n == 0) continue;
       if (a.q_box > 0) {   // whole groups of 8 heads: the queries come by TMA too
         if (I > 0 && !(ok = warp_wait(bar(R_QFREE), (uint32_t)((I - 1) & 1), a.status))) break;
@@ -175,7 +175,7 @@ latent_decode_pair_kernel(const __grid_constant__ LatentArgs a, const __grid_con
       if (ask_ahead)
         for (int j = 0; j < NS; ++j) ahead.next_tile();
       for (int j = 0; j < pc.n; ++j) {
-        const int page = walk.page, slot8 = walk.slot / 8;
+        const int page = walk.page(), slot8 = walk.slot / 8;
         walk.next_tile();
         if (nk >= NS && !(ok = warp_wait(bar(R_KEMPTY + kp.slot), kp.parity ^ 1u, a.status))) break;
         if (lane == 0 && rank == 0) mbar_arrive_expect_tx(bar(R_KFULL + kp.slot), 2 * G::kK);
@@ -185,7 +185,7 @@ latent_decode_pair_kernel(const __grid_constant__ LatentArgs a, const __grid_con
                            &maps.keys, lead(R_KFULL + kp.slot), 0, 0, 0, slot8, page);
         __syncwarp();
         if (ask_ahead && j + NS < pc.n) {
-          if (lane < boxes) tma_prefetch_5d(&maps.keys, 0, 0, 0, ahead.slot / 8, ahead.page);
+          if (lane < boxes) tma_prefetch_5d(&maps.keys, 0, 0, 0, ahead.slot / 8, ahead.page());
           ahead.next_tile();
         }
         kp.next();
@@ -200,12 +200,12 @@ latent_decode_pair_kernel(const __grid_constant__ LatentArgs a, const __grid_con
     Ring<NS> vp;
     int nv = 0, tails = 0;   // stages filled so far, cleared tiles
     bool ok = true;
-    for (int item = item0; ok && item < item1; ++item) {
-      const Piece pc(a, item, rb, 2 * kRows);
+    for (int item = 0; ok && pieces.has(item); ++item) {
+      const Piece pc(a, pieces[item], rb, 2 * kRows);
       if (pc.n == 0) continue;
       PageWalk walk(a, pc, lane * a.box_rows, lane < boxes);
       for (int j = 0; j < pc.n; ++j) {
-        const int page = walk.page, slot8 = walk.slot / 8;
+        const int page = walk.page(), slot8 = walk.slot / 8;
         walk.next_tile();
         if (nv >= NS && !(ok = warp_wait(bar(R_VEMPTY + vp.slot), vp.parity ^ 1u, a.status))) break;
         const uint32_t off = G::kOffV + (uint32_t)vp.slot * G::kV, full = lead(R_VFULL + vp.slot);
@@ -248,8 +248,8 @@ latent_decode_pair_kernel(const __grid_constant__ LatentArgs a, const __grid_con
       Ring<NS> kp;
       int T = 0, I = 0;   // tiles and non-empty pieces before this one
       bool ok = true;
-      for (int item = item0; ok && item < item1; ++item) {
-        const Piece pc(a, item, rb, 2 * kRows);
+      for (int item = 0; ok && pieces.has(item); ++item) {
+        const Piece pc(a, pieces[item], rb, 2 * kRows);
         if (pc.n == 0) continue;
         ok = warp_wait(bar(R_QFULL), (uint32_t)(I & 1), a.status);
         ++I;
@@ -280,8 +280,8 @@ latent_decode_pair_kernel(const __grid_constant__ LatentArgs a, const __grid_con
       Ring<NS> vp;
       int T = 0, I = 0;
       bool ok = true;
-      for (int item = item0; ok && item < item1; ++item) {
-        const Piece pc(a, item, rb, 2 * kRows);
+      for (int item = 0; ok && pieces.has(item); ++item) {
+        const Piece pc(a, pieces[item], rb, 2 * kRows);
         if (pc.n == 0) continue;
         for (int j = 0; j < pc.n; ++j, ++T) {
           ok = warp_wait(bar(R_VFULL + vp.slot), vp.parity, a.status) &&
@@ -335,8 +335,8 @@ latent_decode_pair_kernel(const __grid_constant__ LatentArgs a, const __grid_con
     bool ok = true;
     auto next_q = [&](int item) {   // the next piece that has tiles, from `item` on
       if (a.q_box > 0) return;
-      for (; item < item1; ++item) {
-        const Piece pc(a, item, rb, 2 * kRows);
+      for (; pieces.has(item); ++item) {
+        const Piece pc(a, pieces[item], rb, 2 * kRows);
         if (pc.n > 0) {
           if (I > 0 && !warp_wait(bar(R_QFREE), (uint32_t)((I - 1) & 1), a.status)) s_fail[2] = 1;
           load_q(pc);
@@ -344,11 +344,11 @@ latent_decode_pair_kernel(const __grid_constant__ LatentArgs a, const __grid_con
         }
       }
     };
-    next_q(item0);
+    next_q(0);
 
     int T = 0;
-    for (int item = item0; ok && item < item1; ++item) {
-      const Piece pc(a, item, rb, 2 * kRows);
+    for (int item = 0; ok && pieces.has(item); ++item) {
+      const Piece pc(a, pieces[item], rb, 2 * kRows);
       if (pc.rows <= 0) continue;
       const bool whole = pc.part < 0;
       const int live = min(kRows, pc.rows - (int)rank * kRows);   // this CTA's rows, may be < 1
