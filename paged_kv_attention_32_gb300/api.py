@@ -477,6 +477,15 @@ def _check_tensors(dtype, **tensors):
                 raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
 
 
+def _fits(dtype, dev, *tensors):
+    """Whether every given tensor has this type and lies on device ``dev``: the test a serving
+    step makes; ``_check_tensors`` says what is wrong."""
+    for t in tensors:
+        if t is not None and (t.dtype is not dtype or t.get_device() != dev):
+            return False
+    return True
+
+
 def _on_stream(stream):
     """Makes ``stream`` current: the caching allocator hands a freed block out again in the
     order of the stream it was made on, so what a call allocates for itself has to come from
@@ -520,10 +529,14 @@ def paged_kv_tables(kv_lens, new_lens, free_pages, free_head, block_tables, *, p
                 kv_lens, new_lens, free_pages, free_head, block_tables, page_size=page_size,
                 num_slots=num_slots, seq_lens=seq_lens, qo_indptr=qo_indptr, slot_map=slot_map,
                 free_head_out=free_head_out, status=status)
-    _check_tensors(torch.int32, kv_lens=kv_lens, new_lens=new_lens, free_pages=free_pages,
-                   free_head=free_head, block_tables=block_tables, seq_lens=seq_lens,
-                   qo_indptr=qo_indptr, free_head_out=free_head_out, status=status)
-    _contiguous(kv_lens=kv_lens, new_lens=new_lens, free_pages=free_pages)
+    dev = torch.cuda.current_device()
+    if not _fits(torch.int32, dev, kv_lens, new_lens, free_pages, free_head, block_tables, seq_lens,
+                 qo_indptr, free_head_out, status):
+        _check_tensors(torch.int32, kv_lens=kv_lens, new_lens=new_lens, free_pages=free_pages,
+                       free_head=free_head, block_tables=block_tables, seq_lens=seq_lens,
+                       qo_indptr=qo_indptr, free_head_out=free_head_out, status=status)
+    if not (kv_lens.is_contiguous() and new_lens.is_contiguous() and free_pages.is_contiguous()):
+        _contiguous(kv_lens=kv_lens, new_lens=new_lens, free_pages=free_pages)
     B = kv_lens.numel()
     if block_tables.dim() != 2 or block_tables.shape[0] != B or new_lens.numel() != B:
         raise ValueError("kv_lens, new_lens and block_tables must have one row per request")
@@ -559,8 +572,9 @@ def paged_kv_tables(kv_lens, new_lens, free_pages, free_head, block_tables, *, p
         kv_lens.data_ptr(), new_lens.data_ptr(), B, free_pages.data_ptr(), free_pages.numel(),
         free_head.data_ptr(), page_size, block_tables.data_ptr(), row if row > width else width,
         width, seq_lens.data_ptr(), qo_indptr.data_ptr(), slot_map.data_ptr(), num_slots,
-        free_head_out.data_ptr(), _ptr(status), _stream(stream))
-    L.check(rc, "paged_kv_tables")
+        free_head_out.data_ptr(), _ptr(status), torch._C._cuda_getCurrentRawStream(dev))
+    if rc:
+        L.check(rc, "paged_kv_tables")
     return KvTables(seq_lens, qo_indptr, slot_map, free_head_out)
 
 
@@ -583,8 +597,11 @@ def paged_latent_append(latent, rope, slot_map, pages, status=None, stream=None)
     dtype = pages.dtype
     if dtype is not torch.bfloat16 and dtype is not torch.float16:
         raise ValueError(f"pages must be bfloat16 or float16, got {dtype}")
-    _check_tensors(dtype, latent=latent, rope=rope, pages=pages)
-    _check_tensors(torch.int64, slot_map=slot_map)
+    dev = torch.cuda.current_device()
+    if not _fits(dtype, dev, latent, rope, pages):
+        _check_tensors(dtype, latent=latent, rope=rope, pages=pages)
+    if not _fits(torch.int64, dev, slot_map):
+        _check_tensors(torch.int64, slot_map=slot_map)
     page_stride = _latent_page_stride(pages)
     n_pages, ps, dim = pages.shape
     if latent.dim() != 2 or (rope is not None and rope.dim() != 2):
@@ -605,12 +622,14 @@ def paged_latent_append(latent, rope, slot_map, pages, status=None, stream=None)
         return pages
     if lc != 1:
         raise ValueError("latent must have a dense last dimension")
-    if status is not None:
+    if not _fits(torch.int32, dev, status):
         _check_tensors(torch.int32, status=status)
     rc = L.lib().paged_latent_append(
         latent.data_ptr(), ls, _ptr(rope), rs, dl, dr, slot_map.data_ptr(), T, pages.data_ptr(),
-        n_pages, ps, page_stride, _DTYPES[dtype], _ptr(status), _stream(stream))
-    L.check(rc, "paged_latent_append")
+        n_pages, ps, page_stride, _DTYPES[dtype], _ptr(status),
+        torch._C._cuda_getCurrentRawStream(dev))
+    if rc:
+        L.check(rc, "paged_latent_append")
     return pages
 
 
@@ -628,6 +647,7 @@ class LatentDecodePlan:
         self.out_row = (desc.num_heads, desc.latent_dim)
         self.pages_shape = (desc.num_pages, desc.page_size, desc.latent_dim + desc.rope_dim)
         self.table_width, self.return_lse = desc.max_pages_per_seq, bool(desc.return_lse)
+        self.batch_size = desc.batch_size
 
     @property
     def info(self):
@@ -658,7 +678,7 @@ class LatentDecodePlan:
             self.handle, seq_t.numel(), seq_p, ind_p, ctypes.byref(ws),
             None if host_only else _stream(stream))
         L.check(rc, "paged_latent_decode_plan_update")
-        self.desc.batch_size = seq_t.numel()
+        self.batch_size = self.desc.batch_size = seq_t.numel()
         self.workspace_bytes = ws.value
         self.total_q = self.info["total_q"]
         return self
@@ -712,13 +732,15 @@ def paged_latent_decode_run(plan, q, pages, block_tables, seq_lens_kv=None, out=
         with _on_stream(stream):
             return paged_latent_decode_run(plan, q, pages, block_tables, seq_lens_kv=seq_lens_kv,
                                            out=out, lse=lse, workspace=workspace)
-    _check_tensors(plan.dtype, q=q, pages=pages)
-    _check_tensors(torch.int32, block_tables=block_tables, seq_lens_kv=seq_lens_kv)
-    need, B = plan.total_q, plan.desc.batch_size
-    if q.dim() != 3 or q.shape[1:] != plan.row or q.shape[0] < need:
-        raise ValueError(f"q must be [>= {need}, {plan.row[0]}, {plan.row[1]}], "
-                         f"got {tuple(q.shape)}")
-    T = q.shape[0]
+    dev = torch.cuda.current_device()
+    if not _fits(plan.dtype, dev, q, pages):
+        _check_tensors(plan.dtype, q=q, pages=pages)
+    if not _fits(torch.int32, dev, block_tables, seq_lens_kv):
+        _check_tensors(torch.int32, block_tables=block_tables, seq_lens_kv=seq_lens_kv)
+    need, B, shape = plan.total_q, plan.batch_size, q.shape
+    if len(shape) != 3 or shape[1:] != plan.row or shape[0] < need:
+        raise ValueError(f"q must be [>= {need}, {plan.row[0]}, {plan.row[1]}], got {tuple(shape)}")
+    T = shape[0]
     q_tok, q_head, q_col = q.stride()
     if q_col != 1:
         raise ValueError("q must have a dense last dimension")
@@ -757,8 +779,10 @@ def paged_latent_decode_run(plan, q, pages, block_tables, seq_lens_kv=None, out=
     rc = L.lib().paged_latent_decode_run(
         plan.handle, q.data_ptr(), q_tok, q_head, pages.data_ptr(), page_stride,
         block_tables.data_ptr(), row if row > width else width, _ptr(seq_lens_kv),
-        out.data_ptr(), _ptr(lse), _ptr(workspace), ws_bytes, _stream(stream))
-    L.check(rc, "paged_latent_decode_run")
+        out.data_ptr(), _ptr(lse), _ptr(workspace), ws_bytes,
+        torch._C._cuda_getCurrentRawStream(dev))
+    if rc:
+        L.check(rc, "paged_latent_decode_run")
     return (out, lse) if plan.return_lse else out
 
 
@@ -816,19 +840,19 @@ def batch_latent_prefill_run(plan, q, k_nope, k_rope, v, out=None, lse=None, wor
                                             workspace=workspace)
     if not isinstance(plan, LatentPrefillPlan):
         raise ValueError("the plan was not made by batch_latent_prefill_plan")
-    _check_tensors(plan.dtype, q=q, k_nope=k_nope, k_rope=k_rope, v=v)
+    dev = torch.cuda.current_device()
+    if not _fits(plan.dtype, dev, q, k_nope, k_rope, v):
+        _check_tensors(plan.dtype, q=q, k_nope=k_nope, k_rope=k_rope, v=v)
     need, need_kv = plan.total_q, plan.total_kv
-    if q.dim() != 3 or q.shape[1:] != plan.q_row or q.shape[0] < need:
-        raise ValueError(f"q must be [>= {need}, {plan.q_row[0]}, {plan.q_row[1]}], "
-                         f"got {tuple(q.shape)}")
-    if k_nope.dim() != 3 or k_nope.shape[1:] != plan.k_row or k_nope.shape[0] < need_kv or \
-            v.dim() != 3 or v.shape[1:] != plan.v_row or v.shape[0] < need_kv:
+    qs, ks, vs, rs = q.shape, k_nope.shape, v.shape, k_rope.shape
+    if len(qs) != 3 or qs[1:] != plan.q_row or qs[0] < need:
+        raise ValueError(f"q must be [>= {need}, {plan.q_row[0]}, {plan.q_row[1]}], got {tuple(qs)}")
+    if len(ks) != 3 or ks[1:] != plan.k_row or ks[0] < need_kv or \
+            len(vs) != 3 or vs[1:] != plan.v_row or vs[0] < need_kv:
         raise ValueError(f"k_nope and v must be [>= {need_kv}, {plan.k_row[0]}, ..] with rows of "
-                         f"{plan.k_row[1]} and {plan.v_row[1]}, got {tuple(k_nope.shape)} and "
-                         f"{tuple(v.shape)}")
-    if k_rope.dim() != 2 or k_rope.shape[1] != plan.rope_dim or k_rope.shape[0] < need_kv:
-        raise ValueError(f"k_rope must be [>= {need_kv}, {plan.rope_dim}], "
-                         f"got {tuple(k_rope.shape)}")
+                         f"{plan.k_row[1]} and {plan.v_row[1]}, got {tuple(ks)} and {tuple(vs)}")
+    if len(rs) != 2 or rs[1] != plan.rope_dim or rs[0] < need_kv:
+        raise ValueError(f"k_rope must be [>= {need_kv}, {plan.rope_dim}], got {tuple(rs)}")
     q_tok, q_head, q_col = q.stride()
     k_strides = k_nope.stride()
     rope_tok, rope_col = k_rope.stride()
@@ -836,7 +860,7 @@ def batch_latent_prefill_run(plan, q, k_nope, k_rope, v, out=None, lse=None, wor
         raise ValueError("q, k_nope and k_rope must have a dense last dimension")
     if k_strides != v.stride():
         raise ValueError("k_nope and v must have the same strides")
-    T = q.shape[0]
+    T = qs[0]
     if out is None:
         out = torch.empty((T,) + plan.v_row, dtype=plan.out_dtype, device=q.device)
     else:
@@ -862,8 +886,9 @@ def batch_latent_prefill_run(plan, q, k_nope, k_rope, v, out=None, lse=None, wor
     rc = L.lib().batch_latent_prefill_run(
         plan.handle, q.data_ptr(), q_tok, q_head, k_nope.data_ptr(), k_rope.data_ptr(), rope_tok,
         v.data_ptr(), k_strides[0], k_strides[1], out.data_ptr(), _ptr(lse), _ptr(workspace),
-        ws_bytes, _stream(stream))
-    L.check(rc, "batch_latent_prefill_run")
+        ws_bytes, torch._C._cuda_getCurrentRawStream(dev))
+    if rc:
+        L.check(rc, "batch_latent_prefill_run")
     return (out, lse) if plan.return_lse else out
 
 
