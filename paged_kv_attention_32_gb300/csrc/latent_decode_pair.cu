@@ -271,7 +271,6 @@ latent_decode_pair_kernel(const __grid_constant__ LatentArgs a, const __grid_con
       }
       umma_pair_commit_elect(bar(R_SDONE));
     }
-    warp_wait(bar(R_SDONE), 0, a.status);   // nothing of this warp's still runs, every commit has landed
   } else if (warp == 2) {
     // ---------------- the leader's: issues O += P V ----------------
     if (rank == 0) {
@@ -303,7 +302,6 @@ latent_decode_pair_kernel(const __grid_constant__ LatentArgs a, const __grid_con
       }
       umma_pair_commit_elect(bar(R_ODONE));
     }
-    warp_wait(bar(R_ODONE), 0, a.status);
   } else {
     // ---------------- softmax and output ----------------
     const int quad = warp & 3;                      // TMEM lanes 32 quad .. + 31
@@ -526,6 +524,12 @@ latent_decode_pair_kernel(const __grid_constant__ LatentArgs a, const __grid_con
 
   tc_fence_before();
   __syncthreads();
+  // Nothing of the pair's still runs on the tensor cores, and every commit has landed here.
+  // Waited for only now: all of a pair's tiles may take longer than any one wait may.
+  if (warp == 1) {
+    warp_wait(bar(R_SDONE), 0, a.status);
+    warp_wait(bar(R_ODONE), 0, a.status);
+  }
   cluster_sync();   // neither CTA's shared memory nor TMEM goes while the pair still uses it
   if (warp == 1) {
     tc_fence_after();

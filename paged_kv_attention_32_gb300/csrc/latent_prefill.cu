@@ -291,8 +291,6 @@ latent_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_consta
       }
       umma_pair_commit_elect(bar(B_MMADONE));
     }
-    // nothing of the pair's still runs on the tensor cores, and every commit has landed here
-    warp_wait(bar(B_MMADONE), 0, a.status);
   } else {
     // ---------------- softmax: one thread per query row ----------------
     const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
@@ -412,6 +410,9 @@ latent_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_consta
 
   tc_fence_before();
   __syncthreads();
+  // Nothing of the pair's still runs on the tensor cores, and every commit has landed here.
+  // Waited for only now: all of a pair's tiles may take longer than any one wait may.
+  if (warp == 5) warp_wait(bar(B_MMADONE), 0, a.status);
   cluster_sync();   // neither CTA's shared memory nor TMEM goes while the pair still uses it
   if (warp == 5) {
     tc_fence_after();

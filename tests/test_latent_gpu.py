@@ -820,3 +820,43 @@ def test_absorbed_decode_agrees_with_expanded_prefill():
     # scores of up to ~200 terms of size ~1 each differ by a few 2^-11 after the scale
     assert float((la[0] - lse[-1]).abs().max()) < 0.02
     assert float((got[0] - out[-1].double()).abs().max()) < 0.02
+
+
+# ---- kernels that run longer than any one of their waits may (2 s) -------------------
+
+def took(run):
+    a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    a.record()
+    r = run()
+    b.record()
+    b.synchronize()
+    return a.elapsed_time(b) / 1e3, r
+
+
+def test_prefill_of_one_pair_that_runs_for_seconds():
+    """384 tiles of 2^20 keys on one pair of CTAs: every wait is for one tile at most."""
+    lq, lk = 384 * 256, 1 << 20
+    g = torch.Generator(device=DEV).manual_seed(0)
+    q, k, v, rope = (torch.randn(s, generator=g, device=DEV).to(BF) for s in
+                     ((lq, 1, 192), (lk, 1, 128), (lk, 1, 128), (lk, 64)))
+    plan = api.batch_latent_prefill_plan([0, lq], [0, lk], num_heads=1, causal=False, num_sms=1)
+    seconds, out = took(lambda: api.batch_latent_prefill_run(plan, q, k, rope, v))
+    plan.check()
+    assert seconds > 2 and bool(out.isfinite().all())
+
+
+@pytest.mark.parametrize("heads", [16, 128])
+def test_decode_of_one_segment_that_runs_for_seconds(heads):
+    """Requests that all see the same pages, one behind the other on one CTA (pair)."""
+    batch, kv = 400, 1 << 20
+    g = torch.Generator(device=DEV).manual_seed(0)
+    pages = torch.randn((64, 256, 320), generator=g, device=DEV).to(BF)
+    table = torch.arange(64, dtype=torch.int32, device=DEV).repeat(batch, kv // (64 * 256))
+    q = torch.randn((1, heads, 320), generator=g, device=DEV).to(BF).repeat(batch, 1, 1)
+    plan = api.paged_latent_decode_plan([kv] * batch, num_heads=heads, page_size=256, scale=0.05,
+                                        max_pages_per_seq=kv // 256, num_pages=64, latent_dim=256,
+                                        num_sms=1, return_lse=True)
+    seconds, (out, lse) = took(lambda: api.paged_latent_decode_run(plan, q, pages, table))
+    plan.check()
+    assert seconds > 2
+    assert bool(out.isfinite().all()) and bool((out == out[0]).all()) and bool((lse == lse[0]).all())
