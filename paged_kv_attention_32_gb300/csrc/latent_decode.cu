@@ -169,9 +169,10 @@ latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = tid >> 5;   // 0: copies, 1: S, 2: P V, then the softmax groups
   const int seg = blockIdx.x / a.row_blocks, rb = blockIdx.x % a.row_blocks;
-  const Pieces pieces(a, seg);
 
-  if (tid == 0) {
+  if (tid == 0) {   // the first piece comes in while the CTA sets up
+    ask_line(a.pieces + seg);
+    ask_line(a.more + seg);
     for (int s = 0; s < 12; ++s) {
       mbar_init(bar(L_KFULL + s), 1);
       mbar_init(bar(L_KEMPTY + s), 1);
@@ -199,6 +200,7 @@ latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant
   const uint32_t tmem = *tmem_slot;
   // the merge's CTAs may start taking free SMs; they wait for this grid's end
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const Pieces pieces(a, seg);
 
   if (warp == 0) {
     // ---------------- TMA producer: lane i copies box i of a tile ----------------

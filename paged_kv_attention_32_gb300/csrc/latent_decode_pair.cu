@@ -109,9 +109,10 @@ latent_decode_pair_kernel(const __grid_constant__ LatentArgs a, const __grid_con
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_rank();   // 0: the leader
   const int pair = blockIdx.x >> 1, seg = pair / a.row_blocks, rb = pair % a.row_blocks;
-  const Pieces pieces(a, seg);
 
-  if (tid == 0) {
+  if (tid == 0) {   // the first piece comes in while the CTA sets up
+    ask_line(a.pieces + seg);
+    ask_line(a.more + seg);
     for (int s = 0; s < 4; ++s) {
       mbar_init(bar(R_KFULL + s), 1);   // the leader expects both CTAs' bytes
       mbar_init(bar(R_KEMPTY + s), 1);
@@ -142,6 +143,7 @@ latent_decode_pair_kernel(const __grid_constant__ LatentArgs a, const __grid_con
   const uint32_t tmem = *tmem_slot;
   // the merge's CTAs may start taking free SMs; they wait for this grid's end
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const Pieces pieces(a, seg);
 
   if (warp == 0) {
     // ---------------- queries and keys: lane i copies box i ----------------

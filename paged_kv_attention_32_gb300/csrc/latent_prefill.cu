@@ -122,13 +122,11 @@ latent_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_consta
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_rank();   // 0: the leader
-  // The pair's first tile lies at its own index, so that its loads need not wait for
-  // the list's; the others one behind the other from more0 on.
-  const int pair = blockIdx.x >> 1, more0 = __ldg(parts.segments + pair);
-  const int n_items = 1 + __ldg(parts.segments + pair + 1) - more0;
-  auto index = [&](int k) -> int { return k == 0 ? pair : more0 + k - 1; };
+  const int pair = blockIdx.x >> 1;
 
-  if (tid == 0) {
+  if (tid == 0) {   // the first tile comes in while the pair sets up
+    ask_line(a.tiles + pair);
+    ask_line(parts.segments + pair);
     mbar_init(bar(B_QFULL), 2);
     mbar_init(bar(B_QFREE), 1);
     mbar_init(bar(B_OFREE), 8);
@@ -160,6 +158,12 @@ latent_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_consta
 
   // the merge's CTAs may start taking free SMs; they wait for this grid's end
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  // The pair's first tile lies at its own index, so that its loads need not wait for
+  // the list's; the others one behind the other from more0 on.
+  const int more0 = __ldg(parts.segments + pair);
+  const int n_items = 1 + __ldg(parts.segments + pair + 1) - more0;
+  auto index = [&](int k) -> int { return k == 0 ? pair : more0 + k - 1; };
 
   if (warp == 4) {
     // ---------------- TMA producer ----------------
