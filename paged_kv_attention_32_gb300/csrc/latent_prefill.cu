@@ -22,8 +22,8 @@
 // many products a second as the library's bf16 product reaches (1890 TFLOP/s): the
 // tensor core bounds it.  2 x 1024 rows behind 7168 keys, 32 heads: 261 us with single
 // CTAs, 225 in pairs that took one tile each, 212 dealt out; 8 ragged prompts of 512 to
-// 4096: 445, 437, 397 (15 % of whose products lie beyond the diagonal); 4 prompts of
-// 512, 128 heads: 68 us, where the ends of the tiles count (74 with 16-byte stores).
+// 4096: 445, 437, 400 (15 % of whose products lie beyond the diagonal); 4 prompts of
+// 512, 128 heads: 66 us, where the ends of the tiles count (74 with 16-byte stores).
 // Not kept: tiles of 128 keys, whose scores take a sixth less of the tensor core's
 // time but leave one S buffer: 232 and 475 us where tiles of 64 then took 225 and 437.
 //   warp 4      TMA producer of this CTA's halves; the tile that holds the last
@@ -450,24 +450,33 @@ latent_prefill_merge_kernel(const __grid_constant__ PrefillArgs a, const __grid_
   m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
   if (!live) return;
   float o[4][4] = {};   // dimensions 32 i + 8 quarter + 4 half on
-#pragma unroll 4
-  for (int c = 0; c < cut.n_parts; ++c) {
-    const float x = __ldcg(lse + (int64_t)c * (2 * kTileQ));
-    const float* p = src + (int64_t)c * kDV * (2 * kTileQ);
-    float4 v[4];
+  // two pieces are asked for at once
+  for (int c0 = 0; c0 < cut.n_parts; c0 += 2) {
+    float x[2];
+    float4 v[2][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = __ldcg(reinterpret_cast<const float4*>(p + i * 32 * (2 * kTileQ)));
-    if (x != neg_inf()) {   // else the piece weighs nothing
-      const float w = ex2(x - m);
-      sum += w;
+    for (int k = 0; k < 2; ++k) {
+      x[k] = neg_inf();
+      if (c0 + k < cut.n_parts) {
+        x[k] = __ldcg(lse + (int64_t)(c0 + k) * (2 * kTileQ));
+        const float* p = src + (int64_t)(c0 + k) * kDV * (2 * kTileQ);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        o[i][0] += w * v[i].x;
-        o[i][1] += w * v[i].y;
-        o[i][2] += w * v[i].z;
-        o[i][3] += w * v[i].w;
+        for (int i = 0; i < 4; ++i) v[k][i] = __ldcg(reinterpret_cast<const float4*>(p + i * 32 * (2 * kTileQ)));
       }
     }
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      if (x[k] != neg_inf()) {   // else the piece weighs nothing
+        const float w = ex2(x[k] - m);
+        sum += w;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          o[i][0] += w * v[k][i].x;
+          o[i][1] += w * v[k][i].y;
+          o[i][2] += w * v[k][i].z;
+          o[i][3] += w * v[k][i].w;
+        }
+      }
   }
   const int64_t row = (int64_t)(cut.q0 + t) * a.num_qo_heads + cut.head;
   const float f = sum != 0.f ? a.output_scale / sum : 0.f;
