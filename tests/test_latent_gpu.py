@@ -408,6 +408,26 @@ def test_decode_nan_in_a_cached_row_reaches_its_own_request_only(heads, num_sms)
         assert torch.equal(out[b], good[b]) and torch.equal(lse[b], good_lse[b])
 
 
+@pytest.mark.parametrize("heads,dl", [(64, 512), (128, 512), (128, 256)])
+def test_decode_bad_pages_far_into_a_request_read_as_zeros(heads, dl):
+    """Entries outside the pool in tiles that are asked for ahead of their copies."""
+    kv = [1000, 640]
+    q, pages, table = decode_inputs(kv, [0, 1, 2], heads, dl, 16, BF)
+    plan = api.paged_latent_decode_plan(kv, num_heads=heads, page_size=16, scale=0.05,
+                                        max_pages_per_seq=table.shape[1], num_pages=pages.shape[0],
+                                        latent_dim=dl, num_sms=2, return_lse=True)
+    bad = [(0, 20, -1), (0, 33, pages.shape[0]), (0, 50, 2 ** 31 - 1), (1, 30, -2 ** 31)]
+    rows = torch.zeros((len(bad), 16, dl + 64), dtype=BF, device=DEV)
+    fixed, pool = table.clone(), torch.cat([pages, rows])
+    for i, (b, j, entry) in enumerate(bad):
+        table[b, j] = entry
+        fixed[b, j] = pages.shape[0] + i
+    out, lse = api.paged_latent_decode_run(plan, q, pages, table)
+    plan.check()
+    ref = ref_decode(q, pool, fixed, kv, [0, 1, 2], dl, 0.05, False, 1.0, BF)
+    assert_within(out, lse, ref)
+
+
 @pytest.mark.parametrize("heads", [16, 128])
 def test_decode_pool_offsets_past_32_bits(heads):
     ps, D = 64, 576

@@ -195,3 +195,26 @@ def test_binding_wants_cuda_tensors(monkeypatch):
         api.paged_latent_append(torch.zeros((1, 64), dtype=torch.bfloat16), None,
                                 torch.zeros(1, dtype=torch.int64),
                                 torch.zeros((1, 8, 64), dtype=torch.bfloat16))
+
+
+@pytest.mark.parametrize("qo,kv,heads,num_sms,cut", [
+    ([0, 300], [0, 300], 4, 152, False),          # short tiles stay whole
+    ([0, 256], [0, 64 * 1000], 1, 1, False),      # one pair takes everything in turn
+    ([0, 256], [0, 64 * 1000], 1, 152, True),     # one tile, shared out
+    ([0, 256], [0, 64 * 1000], 152, 152, False),  # as many equal tiles as pairs
+    ([0, 256], [0, 64 * 1000], 200, 152, True),   # a second round a third full
+    ([0, 0], [0, 5], 3, 152, False),              # no rows
+])
+def test_prefill_plan_cuts_tiles_only_where_pairs_end_unevenly(qo, kv, heads, num_sms, cut):
+    plan = api.batch_latent_prefill_plan(qo, kv, num_heads=heads, causal=False, num_sms=num_sms,
+                                         host_only=True)
+    assert (plan.workspace_bytes > 0) == cut
+    assert plan.workspace_bytes % (256 * 129 * 4) == 0      # whole states: 256 rows and their LSEs
+    assert plan.workspace_bytes // (256 * 129 * 4) <= plan.num_tiles + num_sms
+
+
+@pytest.mark.parametrize("num_sms", [-1, 5000])
+def test_prefill_plan_refuses_sm_counts(num_sms):
+    with pytest.raises(L.PkaError) as e:
+        api.batch_latent_prefill_plan([0, 3], [0, 3], num_heads=1, num_sms=num_sms, host_only=True)
+    assert e.value.code == L.PKA_ERR_INVALID_ARG
