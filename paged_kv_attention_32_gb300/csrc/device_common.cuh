@@ -68,6 +68,7 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
 __device__ __forceinline__ void ask_line(const void* p) {
   uint32_t word;
   asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(word) : "l"(p) : "memory");
+  (void)word;
 }
 
 // Asks for a box in L2 without waiting for it.

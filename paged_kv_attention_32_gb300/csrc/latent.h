@@ -27,7 +27,7 @@ struct LatentItem {
 
 // The same on the device, with what a CTA needs of the request (32 bytes): one load
 // and not a chain of three behind the launch.
-struct LatentPiece {
+struct alignas(16) LatentPiece {
   int32_t request;
   int32_t tile_lo;
   int32_t tile_hi;
