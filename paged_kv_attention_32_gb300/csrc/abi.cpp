@@ -5,6 +5,7 @@
 #include <climits>
 #include <cmath>
 #include <cstring>
+#include <memory>
 #include <new>
 #include <string>
 
@@ -201,19 +202,17 @@ int pka::make_prefill_plan(pka_prefill_plan** plan_out, const pka_prefill_desc& 
                            const int32_t* qo, const int32_t* kv, bool latent,
                            int32_t* num_tiles_out, cudaStream_t stream) {
   *plan_out = nullptr;
-  pka_prefill_plan* p = new (std::nothrow) pka_prefill_plan();
+  std::unique_ptr<pka_prefill_plan, void (*)(pka_prefill_plan*)> p(
+      new (std::nothrow) pka_prefill_plan(), batch_prefill_plan_destroy);
   if (p == nullptr) return fail(PKA_ERR_INVALID_ARG, "out of host memory");
   int rc = build_prefill_plan(*p, desc, qo, kv, nullptr, nullptr, latent ? 256 : 128, latent);
   const int32_t num_tiles = (int32_t)p->tiles.size();
   p->latent = latent;
   if (rc == PKA_OK && latent) rc = deal_prefill_tiles(*p);
   if (rc == PKA_OK && !(desc.flags & PKA_PLAN_HOST_ONLY)) rc = upload_prefill_plan(*p, stream);
-  if (rc != PKA_OK) {
-    batch_prefill_plan_destroy(p);
-    return rc;
-  }
+  if (rc != PKA_OK) return rc;
   if (num_tiles_out) *num_tiles_out = num_tiles;
-  *plan_out = p;
+  *plan_out = p.release();
   return PKA_OK;
 }
 

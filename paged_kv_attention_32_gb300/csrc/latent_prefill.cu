@@ -34,8 +34,9 @@
 //               4 k-steps of 16 keys, P from TMEM);
 //   warps 0-3   softmax, one thread per query row: lazy rescaling of O only when
 //               the row maximum grew by more than 2^8, P in 16 bits over the S
-//               buffer (its rounding enters O like the inputs' own; the sum of
-//               p is taken in 32 bits before it), final O / l and LSE.
+//               buffer (its rounding enters O like the inputs' own, in f16 with
+//               steps of 2^-24 below 2^-14; the sum of p is taken in 32 bits
+//               before it), final O / l and LSE.
 // TMEM columns: S0 [0,64) S1 [64,128) O [128,256).
 #include <cuda_bf16.h>
 
