@@ -594,6 +594,9 @@ def paged_latent_append(latent, rope, slot_map, pages, status=None, stream=None)
     (negative entries skip their row), ``pages`` ``[num_pages, page_size, latent_dim +
     rope_dim]``, updated in place and returned.  A slot past the pool is skipped and
     reported in ``status`` (``check_status``)."""
+    if stream is not None:
+        with _on_stream(stream):
+            return paged_latent_append(latent, rope, slot_map, pages, status=status)
     dtype = pages.dtype
     if dtype is not torch.bfloat16 and dtype is not torch.float16:
         raise ValueError(f"pages must be bfloat16 or float16, got {dtype}")
