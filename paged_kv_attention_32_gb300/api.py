@@ -490,8 +490,8 @@ def _on_stream(stream):
     """Makes ``stream`` current: the caching allocator hands a freed block out again in the
     order of the stream it was made on, so what a call allocates for itself has to come from
     the stream the call runs on."""
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream))
+    if not isinstance(stream, torch.cuda.Stream):   # of 0 ExternalStream would make a new stream
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
     return torch.cuda.stream(stream)
 
 

@@ -63,3 +63,12 @@ def test_append_is_queued_on_the_given_stream(streams, library, stream, handle):
     (name, args), = library.calls
     assert name == "paged_latent_append" and args[-1] == handle
     assert streams.now == 11
+
+
+@pytest.mark.parametrize("given,made", [(0, "default"), (99, "external 99")])
+def test_raw_handles_become_the_stream_they_name(monkeypatch, given, made):
+    """0 is the default stream's handle; torch makes a stream of its own of it."""
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda: "default")
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda h: f"external {h}")
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: s)
+    assert api._on_stream(given) == made

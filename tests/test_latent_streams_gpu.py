@@ -76,3 +76,22 @@ def test_a_step_on_one_given_stream(raw):
     ids = torch.arange(B * 8, device=DEV).view(B, 8)
     assert_within(out, lse, ref_decode(q, dense.view(-1, ps, D), ids, new, list(range(B + 1)), dl,
                                        0.06, False, 1.0, BF))
+
+
+def test_handle_0_is_the_default_stream():
+    """The raw handle that torch gives for its default stream, from under another stream."""
+    rows = torch.randn((40, 320), device=DEV).to(BF)
+    pages = torch.zeros((6, 16, 320), dtype=BF, device=DEV)
+    lens, new, made = i32([0]), i32([0]), i32([40])
+    free, head, table = torch.arange(6, dtype=torch.int32, device=DEV), i32([0]), i32([[-1] * 6])
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    handle = torch.cuda.default_stream().cuda_stream
+    assert handle == 0
+    torch.cuda._sleep(BUSY)
+    new.copy_(made)
+    with torch.cuda.stream(side):
+        t = api.paged_kv_tables(lens, new, free, head, table, page_size=16, num_slots=40, stream=handle)
+        api.paged_latent_append(rows[:, :256], rows[:, 256:], t.slot_map, pages, stream=handle)
+    torch.cuda.default_stream().synchronize()
+    assert torch.equal(pages.view(96, 320)[:40], rows) and t.seq_lens.tolist() == [40]
