@@ -570,7 +570,8 @@ def paged_kv_tables(kv_lens, new_lens, free_pages, free_head, block_tables, *, p
         raise ValueError("free_head_out must hold one entry")
     rc = L.lib().paged_kv_tables(
         kv_lens.data_ptr(), new_lens.data_ptr(), B, free_pages.data_ptr(), free_pages.numel(),
-        free_head.data_ptr(), page_size, block_tables.data_ptr(), row if row > width else width,
+        free_head.data_ptr(), page_size, block_tables.data_ptr(),
+        row if B > 1 or row > width else width,   # one row's stride says nothing
         width, seq_lens.data_ptr(), qo_indptr.data_ptr(), slot_map.data_ptr(), num_slots,
         free_head_out.data_ptr(), _ptr(status), torch._C._cuda_getCurrentRawStream(dev))
     if rc:
@@ -781,7 +782,7 @@ def paged_latent_decode_run(plan, q, pages, block_tables, seq_lens_kv=None, out=
         workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
     rc = L.lib().paged_latent_decode_run(
         plan.handle, q.data_ptr(), q_tok, q_head, pages.data_ptr(), page_stride,
-        block_tables.data_ptr(), row if row > width else width, _ptr(seq_lens_kv),
+        block_tables.data_ptr(), row if B > 1 or row > width else width, _ptr(seq_lens_kv),
         out.data_ptr(), _ptr(lse), _ptr(workspace), ws_bytes,
         torch._C._cuda_getCurrentRawStream(dev))
     if rc:

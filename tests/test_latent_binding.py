@@ -72,3 +72,48 @@ def test_raw_handles_become_the_stream_they_name(monkeypatch, given, made):
     monkeypatch.setattr(torch.cuda, "ExternalStream", lambda h: f"external {h}")
     monkeypatch.setattr(torch.cuda, "stream", lambda s: s)
     assert api._on_stream(given) == made
+
+
+def _plan(batch):
+    return api.paged_latent_decode_plan([20] * batch, num_heads=8, page_size=16, max_pages_per_seq=4,
+                                        num_pages=8, scale=0.1, latent_dim=256, num_sms=8, host_only=True)
+
+
+def _tables(table):
+    z = torch.zeros(table.shape[0], dtype=torch.int32)
+    return api.paged_kv_tables(z, z.clone(), torch.zeros(3, dtype=torch.int32),
+                               torch.zeros(1, dtype=torch.int32), table, page_size=16, num_slots=2)
+
+
+def _decode(table):
+    q, pages = torch.zeros((table.shape[0], 8, 320), dtype=BF), torch.zeros((8, 16, 320), dtype=BF)
+    return api.paged_latent_decode_run(_plan(table.shape[0]), q, pages, table)
+
+
+BASE = torch.zeros(40, dtype=torch.int32)
+
+
+@pytest.mark.parametrize("call,at", [(_tables, 8), (_decode, 7)])
+@pytest.mark.parametrize("rows,stride,given", [
+    (3, 0, 0), (3, 2, 2),              # rows over one another: as they are, for the library to refuse
+    (3, 4, 4), (3, 9, 9),
+    (1, 0, 4), (1, 1, 4), (1, 9, 9),   # of one row the stride says nothing
+])
+def test_table_rows_keep_their_stride(streams, monkeypatch, call, at, rows, stride, given):
+    plan = _plan(rows)
+    r = Recorder()
+    table = BASE.as_strided((rows, 4), (stride, 1))
+    monkeypatch.setattr(api, "paged_latent_decode_plan", lambda *a, **k: plan)
+    with monkeypatch.context() as m:
+        m.setattr(L, "lib", lambda: r)
+        call(table)
+    (name, args), = r.calls
+    assert args[at] == given
+
+
+def test_tables_over_one_another_are_refused(streams):
+    """By the library, before anything is launched: two requests would write one row."""
+    for table in (BASE[:4].expand(3, 4), BASE.as_strided((3, 4), (2, 1))):
+        with pytest.raises(L.PkaError, match="row stride") as e:
+            _tables(table)
+        assert e.value.code == L.PKA_ERR_INVALID_ARG
