@@ -52,15 +52,27 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
+// CLUSTER: acquires at the cluster's scope what arrivals of its other CTAs released;
+// without it only what this CTA did.
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
   uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
+  if constexpr (CLUSTER)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
   return ok != 0;
 }
 
@@ -102,18 +114,26 @@ __device__ __forceinline__ void cluster_arrive() {
 __device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// Arrivals on a barrier of any CTA of the cluster (address from map_to_rank).
+// Arrives on a barrier of any CTA of the cluster (address from map_to_rank) and releases
+// to the cluster what was written to this CTA's shared memory before, by this thread or
+// by others that it synchronised with; whoever waits for it has to acquire at the
+// cluster's scope (mbar_wait<true>), and the writer to fence the async proxy where the
+// tensor core reads.  Restricted to shared memory the release is cheap; one of all
+// memory stalls the arriving warp some 900 cycles (latent decode, 32 requests of 4
+// causal rows of 64 heads, the weights handed over so: 193 us against 129).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile(
+      "fence.release.sync_restrict::shared::cta.cluster;\n\t"
+      "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+      : "memory");
 }
 __device__ __forceinline__ void mbar_arrive_expect_tx_cluster(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(bar),
                "r"(bytes)
                : "memory");
 }
-// The same without releasing ordinary writes to the other CTA (what it announces is
-// in tensor memory, ordered by the tcgen05 fences): the cluster-wide release costs
-// the arriving warp some 900 cycles.
+// An arrival that releases nothing to the other CTA, for what it announces in tensor
+// memory alone (ordered by the tcgen05 fences).
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -141,12 +161,14 @@ __device__ __forceinline__ void tma_load_5d_pair(uint32_t dst, const CUtensorMap
 
 // Waits for phase `parity` of the barrier to complete.  Gives up after
 // limit_ns, OR-ing STATUS_WAIT_TIMEOUT into *status; returns false then.
+// CLUSTER: what the other CTAs of the cluster released is acquired too.
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool mbar_wait_for(uint32_t bar, uint32_t parity, int32_t* status,
                                               uint64_t limit_ns) {
-  if (mbar_try_wait(bar, parity)) return true;
+  if (mbar_try_wait<CLUSTER>(bar, parity)) return true;
   const uint64_t t0 = global_timer_ns();
   while (true) {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (mbar_try_wait<CLUSTER>(bar, parity)) return true;
     if (global_timer_ns() - t0 > limit_ns) {
       if (status) atomicOr(status, STATUS_WAIT_TIMEOUT);
       return false;
@@ -155,8 +177,9 @@ __device__ __forceinline__ bool mbar_wait_for(uint32_t bar, uint32_t parity, int
 }
 
 // Every kernel's wait: mbar_wait_for with the kWaitLimitNs bound.
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, int32_t* status) {
-  return mbar_wait_for(bar, parity, status, kWaitLimitNs);
+  return mbar_wait_for<CLUSTER>(bar, parity, status, kWaitLimitNs);
 }
 
 // ---- TMA -------------------------------------------------------------------

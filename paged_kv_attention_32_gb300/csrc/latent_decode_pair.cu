@@ -254,7 +254,8 @@ latent_decode_pair_kernel(const __grid_constant__ LatentArgs a, const __grid_con
       for (int item = 0; ok && pieces.has(item); ++item) {
         const Piece pc(a, pieces[item], rb, 2 * kRows);
         if (pc.n == 0) continue;
-        ok = warp_wait(bar(R_QFULL), (uint32_t)(I & 1), a.status);
+        // queries by plain loads: ordinary writes, of the other CTA too
+        ok = warp_wait<true>(bar(R_QFULL), (uint32_t)(I & 1), a.status);
         ++I;
         for (int j = 0; ok && j < pc.n; ++j, ++T) {
           // P(T - 2) written means S(T - 2) read: this S buffer is free
@@ -286,8 +287,9 @@ latent_decode_pair_kernel(const __grid_constant__ LatentArgs a, const __grid_con
         const Piece pc(a, pieces[item], rb, 2 * kRows);
         if (pc.n == 0) continue;
         for (int j = 0; j < pc.n; ++j, ++T) {
-          ok = warp_wait(bar(R_VFULL + vp.slot), vp.parity, a.status) &&
-               warp_wait(bar(R_PFULL + (T & 1)), (uint32_t)((T >> 1) & 1), a.status);
+          // cleared values and weights: ordinary writes, of the other CTA too
+          ok = warp_wait<true>(bar(R_VFULL + vp.slot), vp.parity, a.status) &&
+               warp_wait<true>(bar(R_PFULL + (T & 1)), (uint32_t)((T >> 1) & 1), a.status);
           if (ok && j == 0 && I > 0) ok = warp_wait(bar(R_OFREE), (uint32_t)((I - 1) & 1), a.status);
           if (!ok) break;
           tc_fence_after();
@@ -449,7 +451,10 @@ latent_decode_pair_kernel(const __grid_constant__ LatentArgs a, const __grid_con
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_remote(lead(R_PFULL + (T & 1)));
+        if (lane == 0) {
+          if (rank == 0) mbar_arrive(bar(R_PFULL + (T & 1)));
+          else mbar_arrive_cluster(lead(R_PFULL + (T & 1)));
+        }
       }
       if (!ok) break;
       ++I;

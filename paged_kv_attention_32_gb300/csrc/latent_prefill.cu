@@ -276,7 +276,8 @@ latent_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_consta
         for (int j = 0; ok && j < n_kv && j < 2; ++j) ok = issue_qk(j);
         for (int j = 0; ok && j < n_kv; ++j) {
           const int st = (T + j) & 1;
-          ok = warp_wait(bar(B_VFULL + vp.slot), vp.parity, a.status) &&
+          // cleared values: ordinary writes, of the other CTA too; P is in tensor memory
+          ok = warp_wait<true>(bar(B_VFULL + vp.slot), vp.parity, a.status) &&
                warp_wait(bar(B_PFULL + st), (uint32_t)(((T + j) >> 1) & 1), a.status);
           if (ok && j == 0 && i > 0) ok = warp_wait(bar(B_OFREE), (uint32_t)((i - 1) & 1), a.status);
           if (!ok) break;

@@ -11,9 +11,10 @@ namespace pka {
 namespace dev {
 
 // Bounded mbarrier wait taken by the whole warp; true on every lane iff every
-// lane saw the phase complete.
+// lane saw the phase complete.  CLUSTER: see mbar_try_wait.
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int32_t* status) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, status));
+  return __all_sync(0xffffffffu, mbar_wait<CLUSTER>(bar, parity, status));
 }
 
 // Row max of 64 scores (ra: keys 0-31, rb: keys 32-63) as four independent
