@@ -121,6 +121,7 @@ template <typename T, int DL>
 __device__ __forceinline__ void store_columns(uint32_t taddr, const float* factor, int live, T* base,
                                               int lane) {
   uint32_t r[16];
+  __syncwarp();   // lanes that stored the last columns and lanes that did not
   tmem_ld16(taddr, r);
   tmem_wait_ld();
   reg_fence<16>(r);

@@ -476,6 +476,7 @@ latent_decode_pair_kernel(const __grid_constant__ LatentArgs a, const __grid_con
         if (!whole) a.ws_lse[prow + row] = lse;
         else if (a.lse != nullptr) a.lse[orow + row] = lse;
       }
+      __syncwarp();   // the whole warp loads what follows
       tc_fence_after();
       // the P buffer that the last tile did not use is free, the other one as well:
       // its P V is complete, and the next piece's P(T) waits for both groups' output

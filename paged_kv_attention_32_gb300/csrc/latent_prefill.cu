@@ -378,19 +378,19 @@ latent_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_consta
 #pragma unroll 1
       for (int c = 0; c < kDV; c += 32) {
         uint32_t o[32];
+        __syncwarp();   // the lanes whose rows are stored and the others load together
         tmem_ld32_sync(o_tm + (uint32_t)c, o);
 #pragma unroll
         for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * inv);
-        if (!row_valid) continue;
-        if (part >= 0) {
+        if (row_valid && part >= 0) {
           float* dst = parts.ws_o + ((int64_t)part * kDV + c) * (2 * kTileQ) + r * 8;
 #pragma unroll
           for (int k = 0; k < 4; ++k) store_sector(dst + k * 8 * (2 * kTileQ), o + 8 * k, true);
-        } else if (a.out_dtype == PKA_DTYPE_F32) {
+        } else if (row_valid && a.out_dtype == PKA_DTYPE_F32) {
           float* dst = static_cast<float*>(a.out) + orow * kDV + c;
 #pragma unroll
           for (int k = 0; k < 4; ++k) store_sector(dst + 8 * k, o + 8 * k, wide);
-        } else {
+        } else if (row_valid) {
           uint16_t* dst = static_cast<uint16_t*>(a.out) + orow * kDV + c;
           uint32_t w[16];
 #pragma unroll

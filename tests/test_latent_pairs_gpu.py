@@ -83,3 +83,55 @@ def test_prefill_pairs_hand_over_cleared_values(num_sms):
         out, lse = api.batch_latent_prefill_run(plan, q, k, rope, v)
         assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
     plan.check()
+
+
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("past,num_sms,cut", [(900, 2, False), (900, 152, False), (3000, 152, True)])
+def test_prefill_warps_of_which_some_lanes_store(past, num_sms, cut, out_dtype):
+    """Every count of live rows in a warp, of whole tiles and of tiles cut along their keys;
+    rows behind them left as they were."""
+    lq = list(range(1, 34)) + [160, 129]
+    lk = [n + past for n in lq]
+    g = torch.Generator(device=DEV).manual_seed(2)
+    qo, ko = [0], [0]
+    for a, b in zip(lq, lk):
+        qo.append(qo[-1] + a)
+        ko.append(ko[-1] + b)
+    q = torch.randn((qo[-1], 1, 192), generator=g, device=DEV).to(BF)
+    kv = torch.randn((ko[-1], 1, 256), generator=g, device=DEV).to(BF)
+    rope = torch.randn((ko[-1], 64), generator=g, device=DEV).to(BF)
+    plan = api.batch_latent_prefill_plan(qo, ko, num_heads=1, return_lse=True, num_sms=num_sms,
+                                         out_dtype=out_dtype)
+    assert (plan.workspace_bytes > 0) == cut
+    out = torch.full((qo[-1] + 7, 1, 128), 7.0, dtype=out_dtype, device=DEV)
+    lse = torch.full((qo[-1] + 7, 1), 7.0, device=DEV)
+    q = torch.cat([q, q[:7]])
+    api.batch_latent_prefill_run(plan, q, kv[..., :128], rope, kv[..., 128:], out=out, lse=lse)
+    plan.check()
+    n = qo[-1]
+    _, ref = ref_prefill(q[:n], kv[..., :128], rope, kv[..., 128:], qo, ko, 192 ** -0.5, True, 1.0,
+                         out_dtype)
+    assert_within(out[:n], lse[:n], ref)
+    assert bool((out[n:] == 7).all()) and bool((lse[n:] == 7).all())
+
+
+@pytest.mark.parametrize("heads", [1, 9, 15, 31, 47, 63, 65, 90, 97, 127])
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float16, torch.float32])
+def test_decode_warps_of_which_some_lanes_store(heads, out_dtype):
+    kv, dl = [130, 5, 700, 64], 256
+    g = torch.Generator(device=DEV).manual_seed(heads)
+    pages = torch.randn((64, 16, dl + 64), generator=g, device=DEV).to(BF)
+    table = torch.randperm(64, generator=torch.Generator().manual_seed(heads)).to(torch.int32)
+    table = table.repeat(3).view(4, 48).to(DEV)
+    q = torch.randn((6, heads, dl + 64), generator=g, device=DEV).to(BF)
+    for sms in (4, 152):
+        plan = api.paged_latent_decode_plan(kv, num_heads=heads, page_size=16, scale=0.05,
+                                            max_pages_per_seq=48, num_pages=64, latent_dim=dl,
+                                            return_lse=True, out_dtype=out_dtype, num_sms=sms)
+        out = torch.full((6, heads, dl), 7.0, dtype=out_dtype, device=DEV)
+        lse = torch.full((6, heads), 7.0, device=DEV)
+        api.paged_latent_decode_run(plan, q, pages, table, out=out, lse=lse)
+        plan.check()
+        assert_within(out[:4], lse[:4], ref_decode(q, pages, table, kv, list(range(5)), dl, 0.05, False,
+                                                   1.0, out_dtype))
+        assert bool((out[4:] == 7).all()) and bool((lse[4:] == 7).all())
