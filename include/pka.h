@@ -734,7 +734,8 @@ int paged_latent_decode_plan_export(const pka_latent_plan* plan, int32_t* items,
 int paged_latent_decode_plan_check(const pka_latent_plan* plan, void* stream);
 
 /*
- * Run the planned latent decode.
+ * Run the planned latent decode.  A plan without query rows runs nothing and looks at none
+ * of the tensors (empty ones may be NULL).
  * q          the plan's dtype, rows [total_q] x [num_heads] x (latent_dim +
  *            rope_dim), (t, h, d) at q + t*q_stride_tok + h*q_stride_head + d;
  *            16-byte aligned, strides multiples of 8.
@@ -797,6 +798,7 @@ int batch_latent_prefill_plan(pka_prefill_plan** plan_out, const pka_latent_pref
                               size_t* workspace_bytes_out, int32_t* num_tiles_out, void* stream);
 
 /*
+ * Run the planned latent prefill; a plan without query rows as in paged_latent_decode_run.
  * q       [total_q, H, nope + rope]: (t, h, d) at q + t*q_stride_tok + h*q_stride_head + d.
  * k_nope, v  [total_kv, H, nope] and [total_kv, H, value]: (t, h, d) at
  *         base + t*kv_stride_tok + h*kv_stride_head + d, one set of strides for

@@ -61,7 +61,6 @@ struct LatentArgs {
   const LatentReq* splits;       // the requests cut into pieces, those of many first
   int32_t* status;
   int32_t num_segments;
-  int32_t num_items;
   int32_t num_splits;
   int32_t num_many;              // of them with more than kLatentFewPieces
   int32_t row_blocks;            // CTAs side by side over a request's rows

@@ -296,6 +296,7 @@ int paged_latent_decode_run(const pka_latent_plan* p, const void* q, int64_t q_s
   clear_error();
   PKA_CHECK_ARG(p != nullptr, "plan must not be NULL");
   PKA_CHECK_ARG(p->dev_buf != nullptr, "plan was built with PKA_PLAN_HOST_ONLY and cannot run");
+  if (p->items.empty()) return PKA_OK;   // no query rows: q and out may be empty, of address NULL
   const pka_latent_desc& d = p->desc;
   PKA_CHECK_ARG(q && pages && block_tables && out,
                 "q, pages, block_tables and out must not be NULL");
@@ -341,7 +342,6 @@ int paged_latent_decode_run(const pka_latent_plan* p, const void* q, int64_t q_s
   a.splits = p->d_splits;
   a.status = p->d_status;
   a.num_segments = (int32_t)p->segments.size() - 1;
-  a.num_items = (int32_t)p->items.size();
   a.num_splits = (int32_t)p->splits.size();
   a.num_many = p->num_many;
   a.row_blocks = p->row_blocks;
@@ -409,6 +409,7 @@ int batch_latent_prefill_run(const pka_prefill_plan* p, const void* q, int64_t q
   PKA_CHECK_ARG(p != nullptr, "plan must not be NULL");
   PKA_CHECK_ARG(p->latent, "the plan was made by batch_prefill_plan");
   PKA_CHECK_ARG(p->dev_buf != nullptr, "plan was built with PKA_PLAN_HOST_ONLY and cannot run");
+  if (p->tiles.empty()) return PKA_OK;   // no query rows: tensors may be empty, of address NULL
   PKA_CHECK_ARG(q && k_nope && k_rope && v && out,
                 "q, k_nope, k_rope, v and out must not be NULL");
   PKA_CHECK_ARG(!p->desc.return_lse || lse != nullptr, "the plan returns the LSE: lse is NULL");
@@ -417,7 +418,6 @@ int batch_latent_prefill_run(const pka_prefill_plan* p, const void* q, int64_t q
     PKA_CHECK_ARG(s > 0 && s % 8 == 0, "strides must be positive multiples of 8 elements");
   int rc = check_device(p->device);
   if (rc != PKA_OK) return rc;
-  if (p->tiles.empty()) return PKA_OK;
   if (p->num_parts > 0) {
     PKA_CHECK_ARG(workspace != nullptr && aligned(workspace, 256), "workspace must be 256-byte aligned");
     if (workspace_bytes < prefill_workspace(*p))

@@ -857,7 +857,6 @@ int launch_single(const pka_latent_plan& plan, const LatentArgs& args, const voi
 
 int launch_latent_decode(const pka_latent_plan& plan, const LatentArgs& a, const void* pages,
                          int64_t stride_page, cudaStream_t stream) {
-  if (a.num_items == 0) return PKA_OK;
   const int rc = plan.row_tile == 128 ? launch_latent_decode_pair(plan, a, pages, stride_page, stream)
                                       : launch_single(plan, a, pages, stride_page, stream);
   if (rc != PKA_OK) return rc;
