@@ -38,6 +38,7 @@ inline cudaError_t set_smem_once(Kernel kern, int bytes, std::atomic<uint64_t>& 
 }
 
 inline int cuda_fail(cudaError_t e, const char* what) {
+  (void)cudaGetLastError();   // reported here: not again at the next launch
   return fail(PKA_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 

@@ -110,7 +110,7 @@ struct pka_latent_plan {
   std::vector<pka::LatentReq> reqs, splits;
   // one device allocation: pieces | further pieces' offsets | splits | status word
   void* dev_buf = nullptr;
-  size_t dev_capacity = 0;
+  size_t capacity = 0;          // of dev_buf and of host_stage
   const pka::LatentPiece* d_pieces = nullptr;
   const int32_t* d_more = nullptr;
   const pka::LatentReq* d_splits = nullptr;
@@ -118,7 +118,6 @@ struct pka_latent_plan {
   int device = -1;
   // pinned host image of dev_buf; stage_done marks when its last upload has read it
   void* host_stage = nullptr;
-  size_t host_capacity = 0;
   cudaEvent_t stage_done = nullptr;
 };
 

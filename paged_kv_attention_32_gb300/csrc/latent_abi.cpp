@@ -6,6 +6,7 @@
 #include <cstring>
 #include <exception>
 #include <new>
+#include <utility>
 
 #include "host_common.h"
 #include "latent.h"
@@ -31,61 +32,92 @@ bool overlap(const void* p, size_t n, const void* q, size_t m) {
   return n > 0 && m > 0 && a < b + m && b < a + n;
 }
 
-// One asynchronous copy of the plan's arrays from a pinned image, which is
-// rewritten only after the copy that last read it has completed.
-int upload_latent_plan(pka_latent_plan& p, cudaStream_t stream) {
-  const size_t n_pieces = p.items.size() * sizeof(LatentPiece);
-  const size_t n_more = p.segments.size() * sizeof(int32_t);
-  const size_t n_splits = p.splits.size() * sizeof(LatentReq);
+// Makes `next`, whose host arrays are built, the plan *p on the device: in p's buffers, or
+// in larger ones.  Where anything fails p stays the plan that it was.
+// One asynchronous copy of the arrays from a pinned image, which is rewritten only after
+// the copy that last read it has completed.
+int install_latent_plan(pka_latent_plan& p, pka_latent_plan&& next, cudaStream_t stream) {
+  const size_t n_pieces = next.items.size() * sizeof(LatentPiece);
+  const size_t n_more = next.segments.size() * sizeof(int32_t);
+  const size_t n_splits = next.splits.size() * sizeof(LatentReq);
   const size_t off_more = up256(n_pieces), off_splits = off_more + up256(n_more);
   const size_t off_status = off_splits + up256(n_splits);
   const size_t total = off_status + 256;
-  if (p.stage_done != nullptr)
-    PKA_CUDA_TRY(cudaEventSynchronize(p.stage_done), "cudaEventSynchronize(plan upload)");
-  if (p.dev_buf == nullptr || total > p.dev_capacity) {
-    if (p.dev_buf != nullptr) {
-      PKA_CUDA_TRY(cudaFree(p.dev_buf), "cudaFree(latent plan)");
-      p.dev_buf = nullptr;
-    }
-    if (p.host_stage != nullptr) {
-      PKA_CUDA_TRY(cudaFreeHost(p.host_stage), "cudaFreeHost(plan image)");
-      p.host_stage = nullptr;
-    }
-    const size_t cap = std::max<size_t>(4096, total + total / 2);
-    PKA_CUDA_TRY(cudaGetDevice(&p.device), "cudaGetDevice");
-    PKA_CUDA_TRY(cudaMalloc(&p.dev_buf, cap), "cudaMalloc(latent plan)");
-    p.dev_capacity = cap;
-    PKA_CUDA_TRY(cudaMallocHost(&p.host_stage, cap), "cudaMallocHost(plan image)");
-  }
-  uint8_t* base = static_cast<uint8_t*>(p.dev_buf);
-  p.d_pieces = reinterpret_cast<const LatentPiece*>(base);
-  p.d_more = reinterpret_cast<const int32_t*>(base + off_more);
-  p.d_splits = reinterpret_cast<const LatentReq*>(base + off_splits);
-  p.d_status = reinterpret_cast<int32_t*>(base + off_status);
-  uint8_t* img = static_cast<uint8_t*>(p.host_stage);
-  LatentPiece* pieces = reinterpret_cast<LatentPiece*>(img);
-  int32_t* more = reinterpret_cast<int32_t*>(img + off_more);
-  auto piece = [&](int32_t i) {
-    const LatentItem& it = p.items[(size_t)i];
-    const LatentReq& r = p.reqs[(size_t)it.request];
-    return LatentPiece{it.request, it.tile_lo, it.tile_hi, it.part, r.q_start, r.q_len, r.kv_len, r.part_base};
-  };
-  const int32_t segs = (int32_t)p.segments.size() - 1;
-  int32_t at = segs;
-  for (int32_t s = 0; s < segs; ++s) {   // no segment is empty
-    more[s] = at;
-    pieces[s] = piece(p.segments[(size_t)s]);
-    for (int32_t i = p.segments[(size_t)s] + 1; i < p.segments[(size_t)s + 1]; ++i) pieces[at++] = piece(i);
-  }
-  more[segs] = at;
-  if (n_splits) std::memcpy(img + off_splits, p.splits.data(), n_splits);
-  std::memset(img + off_status, 0, 256);
-  PKA_CUDA_TRY(cudaMemcpyAsync(base, img, total, cudaMemcpyHostToDevice, stream),
-               "cudaMemcpyAsync(latent plan)");
   if (p.stage_done == nullptr)
     PKA_CUDA_TRY(cudaEventCreateWithFlags(&p.stage_done, cudaEventDisableTiming),
                  "cudaEventCreate(plan upload)");
-  PKA_CUDA_TRY(cudaEventRecord(p.stage_done, stream), "cudaEventRecord(plan upload)");
+  else
+    PKA_CUDA_TRY(cudaEventSynchronize(p.stage_done), "cudaEventSynchronize(plan upload)");
+  next.dev_buf = p.dev_buf;
+  next.host_stage = p.host_stage;
+  next.capacity = p.capacity;
+  next.device = p.device;
+  next.stage_done = p.stage_done;
+  const bool grow = total > p.capacity;
+  if (grow) {
+    next.capacity = std::max<size_t>(4096, total + total / 2);
+    PKA_CUDA_TRY(cudaGetDevice(&next.device), "cudaGetDevice");
+    PKA_CUDA_TRY(cudaMalloc(&next.dev_buf, next.capacity), "cudaMalloc(latent plan)");
+    const cudaError_t e = cudaMallocHost(&next.host_stage, next.capacity);
+    if (e != cudaSuccess) {
+      cudaFree(next.dev_buf);
+      return cuda_fail(e, "cudaMallocHost(plan image)");
+    }
+  }
+  uint8_t* base = static_cast<uint8_t*>(next.dev_buf);
+  next.d_pieces = reinterpret_cast<const LatentPiece*>(base);
+  next.d_more = reinterpret_cast<const int32_t*>(base + off_more);
+  next.d_splits = reinterpret_cast<const LatentReq*>(base + off_splits);
+  next.d_status = reinterpret_cast<int32_t*>(base + off_status);
+  uint8_t* img = static_cast<uint8_t*>(next.host_stage);
+  LatentPiece* pieces = reinterpret_cast<LatentPiece*>(img);
+  int32_t* more = reinterpret_cast<int32_t*>(img + off_more);
+  auto piece = [&](int32_t i) {
+    const LatentItem& it = next.items[(size_t)i];
+    const LatentReq& r = next.reqs[(size_t)it.request];
+    return LatentPiece{it.request, it.tile_lo, it.tile_hi, it.part, r.q_start, r.q_len, r.kv_len, r.part_base};
+  };
+  const int32_t segs = (int32_t)next.segments.size() - 1;
+  int32_t at = segs;
+  for (int32_t s = 0; s < segs; ++s) {   // no segment is empty
+    const size_t first = (size_t)next.segments[(size_t)s];
+    more[s] = at;
+    pieces[s] = piece((int32_t)first);
+    for (int32_t i = (int32_t)first + 1; i < next.segments[(size_t)s + 1]; ++i) pieces[at++] = piece(i);
+  }
+  more[segs] = at;
+  if (n_splits) std::memcpy(img + off_splits, next.splits.data(), n_splits);
+  std::memset(img + off_status, 0, 256);
+  cudaError_t e = cudaMemcpyAsync(base, img, total, cudaMemcpyHostToDevice, stream);
+  if (e != cudaSuccess) {
+    if (grow) {
+      cudaFree(next.dev_buf);
+      cudaFreeHost(next.host_stage);
+    }
+    return cuda_fail(e, "cudaMemcpyAsync(latent plan)");
+  }
+  // from here on the device has the new plan; a copy that no event follows is waited for
+  e = cudaEventRecord(next.stage_done, stream);
+  if (e != cudaSuccess) {
+    (void)cudaGetLastError();
+    e = cudaStreamSynchronize(stream);
+  }
+  if (grow) {
+    cudaFree(p.dev_buf);
+    cudaFreeHost(p.host_stage);
+  }
+  p = std::move(next);
+  return e == cudaSuccess ? PKA_OK : cuda_fail(e, "cudaEventRecord(plan upload)");
+}
+
+// Builds a plan and makes it *p; p stays the plan that it was where that fails.
+int make_latent_plan(pka_latent_plan& p, const pka_latent_desc& desc, const int32_t* seq_lens_kv,
+                     const int32_t* qo_indptr, cudaStream_t stream) {
+  pka_latent_plan next;
+  const int rc = build_latent_plan(next, desc, seq_lens_kv, qo_indptr);
+  if (rc != PKA_OK) return rc;
+  if (!(desc.flags & PKA_PLAN_HOST_ONLY)) return install_latent_plan(p, std::move(next), stream);
+  p = std::move(next);
   return PKA_OK;
 }
 
@@ -198,9 +230,9 @@ int paged_latent_decode_plan(pka_latent_plan** plan_out, const pka_latent_desc* 
   *plan_out = nullptr;
   pka_latent_plan* p = new (std::nothrow) pka_latent_plan();
   if (p == nullptr) return fail(PKA_ERR_INVALID_ARG, "out of host memory");
-  int rc = guarded([&] { return build_latent_plan(*p, *desc, seq_lens_kv_host, qo_indptr_host); });
-  if (rc == PKA_OK && !(desc->flags & PKA_PLAN_HOST_ONLY))
-    rc = upload_latent_plan(*p, static_cast<cudaStream_t>(stream));
+  const int rc = guarded([&] {
+    return make_latent_plan(*p, *desc, seq_lens_kv_host, qo_indptr_host, static_cast<cudaStream_t>(stream));
+  });
   if (rc != PKA_OK) {
     paged_latent_decode_plan_destroy(p);
     return rc;
@@ -222,25 +254,12 @@ int paged_latent_decode_plan_update(pka_latent_plan* p, int32_t batch_size,
     const int rc = check_device(p->device);
     if (rc != PKA_OK) return rc;
   }
-  int rc = guarded([&] {
+  const int rc = guarded([&] {
     pka_latent_desc d = p->desc;
     d.batch_size = batch_size;
-    pka_latent_plan fresh;
-    const int r = build_latent_plan(fresh, d, seq_lens_kv_host, qo_indptr_host);
-    if (r != PKA_OK) return r;   // the old plan stays as it was
-    fresh.dev_buf = p->dev_buf;
-    fresh.dev_capacity = p->dev_capacity;
-    fresh.device = p->device;
-    fresh.host_stage = p->host_stage;
-    fresh.stage_done = p->stage_done;
-    *p = std::move(fresh);
-    return PKA_OK;
+    return make_latent_plan(*p, d, seq_lens_kv_host, qo_indptr_host, static_cast<cudaStream_t>(stream));
   });
   if (rc != PKA_OK) return rc;
-  if (!host_only) {
-    rc = upload_latent_plan(*p, static_cast<cudaStream_t>(stream));
-    if (rc != PKA_OK) return rc;
-  }
   if (workspace_bytes_out) *workspace_bytes_out = (size_t)p->workspace_bytes;
   return PKA_OK;
 }
