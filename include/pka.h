@@ -647,7 +647,9 @@ int paged_latent_append(const void* latent, int64_t latent_stride, const void* r
  * behind it, per row and head
  *   s_j = scale * q . pages[token j],  p = softmax(s),
  *   out = output_scale * sum_j p_j * pages[token j][0 .. latent_dim)
- * which the caller multiplies by the value projection.
+ * which the caller multiplies by the value projection.  Scores, p and every sum are 32
+ * bits; p is rounded to dtype on its way into the last sum, in f16 to steps of 2^-31 of
+ * the row's largest p where it is below 2^-21 of it (batch_latent_prefill alike).
  *
  * batch_size  B.  num_heads 1 .. 1024: all heads share the one cached row.
  * latent_dim  256 or 512.  rope_dim 64.

@@ -17,6 +17,14 @@ constexpr int kLatentTile = 64;        // keys per tile of the latent decode
 constexpr int kLatentRopeDim = 64;
 constexpr int kLatentFewPieces = 8;    // pieces that one CTA merges for a whole row
 
+// A weight is held as 2^(score - reference + shift) on its way into P V.  A reference is at
+// most 2^8 below the row's largest weight, so in f16, which ends at 2^16, there is room for
+// 2^7 more: weights then keep f16's full precision down to 2^-21 of the largest and come in
+// steps of 2^-31 of it below (without it 2^-14 and 2^-24: 20000 keys of 2^-25 each were lost
+// from the output, not from the sum).  bf16 has the exponents of 32 bits.
+template <bool F16>
+constexpr float kLatentWeightShift = F16 ? 7.f : 0.f;
+
 // A run of key tiles of one request (16 bytes, one aligned load).
 struct LatentItem {
   int32_t request;

@@ -6,8 +6,7 @@
 //   O^T += V^T P^T   M=128 (latent dimensions), N rows, 64 keys deep
 // in which few rows are few columns.  A tile is copied once and is both operands.
 // The softmax keeps a running reference and sum per row in 32 bits; P is rounded to
-// the inputs' type, as they are (in f16 weights below 2^-14 of the reference's to steps
-// of 2^-24).  What bounds it is HBM: 2 (latent_dim + 64) bytes a
+// the inputs' type, as they are.  What bounds it is HBM: 2 (latent_dim + 64) bytes a
 // key, however many rows share it.  Measured, 152 requests of 4096 keys in pages of 64:
 // 256 + 64 columns, 8 / 32 / 64 heads 64 / 65 / 68 us (6.2, 6.2, 6.0 TB/s; a copy
 // reaches 6.8); 512 + 64 columns 116 / 117 / 116 us (6.2, 6.2, 6.3 TB/s).  64 ragged
@@ -547,7 +546,7 @@ latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant
         // p = exp2(x - m), summed in 32 bits, rounded to the inputs' format for P V
 #pragma unroll
         for (int q = 0; q < C; ++q) {
-          const float neg = m[q] == neg_inf() ? 0.f : -m[q];
+          const float neg = m[q] == neg_inf() ? 0.f : kLatentWeightShift<F16> - m[q];
           const int i = 4 * (q >> 1) + (q & 1);
           x[i] = ex2(x[i] + neg);
           x[i + 2] = ex2(x[i + 2] + neg);
@@ -588,7 +587,7 @@ latent_decode_kernel(const __grid_constant__ LatentArgs a, const __grid_constant
           reduce_rows(l, lane, [](float u, float v) { return u + v; });
       if (gt < 4)
 #pragma unroll
-        for (int q = 0; q < C; ++q) s_ref[gc + 8 * (q >> 1) + col0 + (q & 1)] = m[q];
+        for (int q = 0; q < C; ++q) s_ref[gc + 8 * (q >> 1) + col0 + (q & 1)] = m[q] - kLatentWeightShift<F16>;
       if (!warp_wait(bar(L_PV + ((T - 1) & 1)), (uint32_t)(((T - 1) >> 1) & 1), a.status)) s_fail[2] = 1;
       bar_sync_group(g);
       if (s_fail[2]) {

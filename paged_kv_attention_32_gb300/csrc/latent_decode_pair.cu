@@ -429,7 +429,7 @@ latent_decode_pair_kernel(const __grid_constant__ LatentArgs a, const __grid_con
           bar_sync_group(0);   // s_max is free again
         }
         // p = exp2(x - m), summed in 32 bits, rounded to the inputs' format for P V
-        const float neg = m == neg_inf() ? 0.f : -m;
+        const float neg = m == neg_inf() ? 0.f : kLatentWeightShift<F16> - m;
         float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
@@ -472,7 +472,7 @@ latent_decode_pair_kernel(const __grid_constant__ LatentArgs a, const __grid_con
       // != and not >: a sum that is NaN stays one, in the LSE as in the output
       const float inv = total != 0.f ? (whole ? a.output_scale : 1.f) / total : 0.f;
       if (half == 0 && row < live) {
-        const float lse = total != 0.f ? m + log2f(total) : neg_inf();
+        const float lse = total != 0.f ? m - kLatentWeightShift<F16> + log2f(total) : neg_inf();
         if (!whole) a.ws_lse[prow + row] = lse;
         else if (a.lse != nullptr) a.lse[orow + row] = lse;
       }

@@ -34,9 +34,8 @@
 //               4 k-steps of 16 keys, P from TMEM);
 //   warps 0-3   softmax, one thread per query row: lazy rescaling of O only when
 //               the row maximum grew by more than 2^8, P in 16 bits over the S
-//               buffer (its rounding enters O like the inputs' own, in f16 with
-//               steps of 2^-24 below 2^-14; the sum of p is taken in 32 bits
-//               before it), final O / l and LSE.
+//               buffer (its rounding enters O like the inputs' own; the sum of p is
+//               taken in 32 bits before it), final O / l and LSE.
 // TMEM columns: S0 [0,64) S1 [64,128) O [128,256).
 #include <cuda_bf16.h>
 
@@ -356,7 +355,7 @@ latent_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_consta
         m_ref = m_new;
         // A row with no visible key so far keeps m_ref = -inf: exp2(-inf) = 0.
         // Masked scores give 0 through their -inf unless the scale is 0.
-        const float neg_m = m_ref == neg_inf() ? 0.f : -m_ref;
+        const float neg_m = m_ref == neg_inf() ? 0.f : kLatentWeightShift<F16> - m_ref;
         const bool zero_again = masked && !(sl2 > 0.f);
         const float2 sum = zero_again ? exp_tile<true, F16>(ra, rb, sl2, neg_m, w0, w1, s_tm)
                                       : exp_tile<false, F16>(ra, rb, sl2, neg_m, w0, w1, s_tm);
@@ -370,7 +369,7 @@ latent_prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_consta
       tc_fence_after();
       // != and not >: a sum that is NaN stays one, in the LSE as in the output
       const float inv = l != 0.f ? (part < 0 ? a.output_scale : 1.f) / l : 0.f;
-      const float lse = l != 0.f ? m_ref + log2f(l) : neg_inf();
+      const float lse = l != 0.f ? m_ref - kLatentWeightShift<F16> + log2f(l) : neg_inf();
       const bool row_valid = t < tile.lq;
       const int64_t orow = (int64_t)(tile.q0 + t) * a.num_qo_heads + tile.head;
       // Whole 32-byte sectors, one a store and lane.  A partial state is kept as blocks of
