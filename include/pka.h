@@ -661,7 +661,10 @@ int paged_latent_append(const void* latent, int64_t latent_stride, const void* r
  * scale       finite; there is no default, the absorbed form hides
  *             the head size it stands for.
  * freeze_seq_lens  nonzero: the plan keeps the host lengths.  Zero: a run reads
- *             the live lengths, each clamped to [0, the planned length].
+ *             the live lengths, each clamped to [0, the planned length]; the work
+ *             stays dealt out as for the planned ones, so the nearer they are the
+ *             evener it is (64 requests of 512 to 8192 keys, 32 heads: 64 us planned
+ *             for their own lengths, 86 us for 8192 each).
  * dtype       PKA_DTYPE_BF16 or PKA_DTYPE_F16: q and the pool.
  * out_dtype   PKA_DTYPE_BF16, PKA_DTYPE_F16 or PKA_DTYPE_F32.
  */
@@ -707,12 +710,20 @@ typedef struct pka_latent_plan_info {
  *                  (and at most 2^31 - 257).
  * qo_indptr_host   NULL (fixed q_len) or [B+1]: cumulative query offsets from
  *                  0, non-decreasing.  A request without rows writes nothing.
+ *                  Row blocks are laid out for the request with the most rows and
+ *                  the SMs shared out over them: requests of very unequal rows run
+ *                  faster from a plan for each kind (64 requests of 4096 keys and 128
+ *                  heads, 1 row each 78 us, one of them with 4 rows 197 us).
  */
 int paged_latent_decode_plan(pka_latent_plan** plan_out, const pka_latent_desc* desc,
                              const int32_t* seq_lens_kv_host, const int32_t* qo_indptr_host,
                              size_t* workspace_bytes_out, void* stream);
 
-/* Re-plan in place for a new batch, as paged_decode_plan_update does. */
+/*
+ * Re-plan in place for a new batch, as paged_decode_plan_update does.  A captured run
+ * keeps the grid and the addresses of the plan as it was: after an update capture it
+ * again, and do not replay the old graph.
+ */
 int paged_latent_decode_plan_update(pka_latent_plan* plan, int32_t batch_size,
                                     const int32_t* seq_lens_kv_host,
                                     const int32_t* qo_indptr_host, size_t* workspace_bytes_out,

@@ -671,7 +671,8 @@ class LatentDecodePlan:
         return [tuple(r) for r in items[: inf["num_items"]].tolist()], segs.tolist()
 
     def update(self, seq_lens_kv, qo_indptr=None, stream=None):
-        """Re-plan in place for a new batch (``paged_latent_decode_plan_update``)."""
+        """Re-plan in place for a new batch (``paged_latent_decode_plan_update``); graphs that
+        captured a run of the plan are not replayed after it."""
         seq_t, seq_p = _host_i32(seq_lens_kv)
         ind_t, ind_p = _host_i32(qo_indptr)
         if ind_t is not None and ind_t.numel() != seq_t.numel() + 1:

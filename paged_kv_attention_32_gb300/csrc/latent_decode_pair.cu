@@ -12,10 +12,10 @@
 // pair 25, N=256 64.  The two halves overlap in a quarter of the tile, which
 // comes twice (from L2).  A tile's bytes through the port of a CTA: 108 KB of operands
 // of S, 48 of P V, 70 of copies and 8 of P, 1860 cycles at 128 B; the tensor core's own
-// time is 1430.  Measured: 64 ragged requests of 128 heads, 512 + 64 columns, 79 us (floor
-// 49.3, its 335 MB at the copy rate); 32 requests of 4 causal rows of 64 heads 127 us
+// time is 1430.  Measured: 64 ragged requests of 128 heads, 512 + 64 columns, 77 us (floor
+// 49.3, its 335 MB at the copy rate); 32 requests of 4 causal rows of 64 heads 125 us
 // (floor 83.5, its products at the library's rate).  256 + 64 columns, 76 requests of
-// 4096 keys, 128 heads: 50 us, of which 199 MB are 29.
+// 4096 keys, 128 heads: 54 us, of which 199 MB are 29.
 // Each CTA's warps:
 //   0  copies queries and its half of the keys;   3  its half of the values, which
 //      in the tile that holds the last key it clears past it (0 * inf is not 0)
