@@ -120,7 +120,7 @@ __device__ __forceinline__ void cluster_wait() {
 // cluster's scope (mbar_wait<true>), and the writer to fence the async proxy where the
 // tensor core reads.  Restricted to shared memory the release is cheap; one of all
 // memory stalls the arriving warp some 900 cycles (latent decode, 32 requests of 4
-// causal rows of 64 heads, the weights handed over so: 193 us against 129).
+// causal rows of 64 heads, the weights handed over so: 193 us against 125).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
   asm volatile(
       "fence.release.sync_restrict::shared::cta.cluster;\n\t"
