@@ -28,6 +28,12 @@
  *       all heads, written to a paged pool and decoded over it.
  *   batch_latent_prefill_plan / batch_latent_prefill_run
  *       its expanded form: ragged prefill with a shared rotary key part.
+ *   paged_rope_append
+ *       a step's keys and queries rotated by their positions, keys and values
+ *       written to the paged K/V pools.
+ *   paged_kv_fork / paged_kv_free / paged_kv_compact / paged_kv_copy
+ *       requests forked over shared pages, released, the pool compacted, and
+ *       pages copied.
  *   paged_kv_gather
  *       test hook: copies paged K or V rows to a dense buffer through the same
  *       page addressing the decode kernels use.
@@ -76,9 +82,9 @@ extern "C" {
 #define PKA_ERR_UNSUPPORTED (-2)          /* valid on the pages, not built here        */
 #define PKA_ERR_WORKSPACE_TOO_SMALL (-3)  /* workspace_bytes below the plan's need     */
 #define PKA_ERR_CUDA (-4)                 /* a CUDA runtime/driver call failed         */
-#define PKA_ERR_DEVICE_BOUNDS (-5)        /* a block-table or slot entry outside the pool */
+#define PKA_ERR_DEVICE_BOUNDS (-5)        /* a table, slot or row entry out of its range  */
 #define PKA_ERR_DEVICE_TIMEOUT (-6)       /* a kernel gave up on a bounded wait        */
-#define PKA_ERR_DEVICE_CAPACITY (-7)      /* paged_kv_tables: a step that does not fit */
+#define PKA_ERR_DEVICE_CAPACITY (-7)      /* page tables: a step that does not fit     */
 
 /* ---- enums ------------------------------------------------------------- */
 #define PKA_DTYPE_BF16 0
@@ -605,10 +611,158 @@ int paged_kv_tables(const int32_t* kv_lens, const int32_t* new_lens, int32_t bat
 /*
  * Wait for `stream`, then read and clear a caller-owned status word, as
  * paged_decode_plan_check does for a plan's: PKA_OK, PKA_ERR_DEVICE_CAPACITY
- * (paged_kv_tables), PKA_ERR_DEVICE_BOUNDS (paged_latent_append) or
- * PKA_ERR_DEVICE_TIMEOUT.  Synchronises; not for capture.
+ * (paged_kv_tables and the page operations), PKA_ERR_DEVICE_BOUNDS (those,
+ * paged_latent_append and paged_rope_append) or PKA_ERR_DEVICE_TIMEOUT.  Synchronises; not for capture.
  */
 int pka_status_check(int32_t* status_dev, void* stream);
+
+/* ======================================================================== */
+/* The K/V page pool: rows written, pages shared, released and moved         */
+/* ======================================================================== */
+
+#define PKA_ROPE_HALVES 0      /* pair j of a rotated row: values j and j + rotary_dim / 2 */
+#define PKA_ROPE_NEIGHBOURS 1  /* pair j: values 2 j and 2 j + 1                            */
+
+/*
+ * Write a step's new keys and values to the paged pools, keys (and queries)
+ * rotated on the way.  The first rotary_dim values of a head's row are pairs;
+ * frequency j turns pair j by the angle position * inv_freq[j],
+ *   (x0, x1) -> (x0 cos - x1 sin, x1 cos + x0 sin),
+ * reduced to a fraction of a turn in 64 bits, the rotation in 32, rounded once.
+ * Values behind rotary_dim, and v, stay as they are.
+ *
+ * q            NULL (num_qo_heads 0) or rows [num_tokens] x [num_qo_heads] x D,
+ *              (t, h, d) at q + t*q_stride_tok + h*q_stride_head + d; written
+ *              rotated to q_out, which has strides of its own and may be q
+ *              itself (same strides) but not overlap it otherwise.
+ * k, v         rows [num_tokens] x [num_kv_heads] x D, one set of strides; not
+ *              in the pools, nor overlapped by q_out.
+ * head_dim     D; must be 128.
+ * positions    int32 [num_axes, num_tokens] device, rows positions_stride
+ *              apart: each token's position on every axis (one axis: its place in the
+ *              sequence; three: time, height and width of an image's or video's
+ *              patch).  Any value, negative ones included.
+ * inv_freq     float64 [rotary_dim / 2] device: radians per position.
+ * rotary_dim   a multiple of 16 in [0, D]; 0 rotates nothing and needs none of
+ *              positions, inv_freq, sections and pairs.
+ * num_axes     1 .. 4.  sections_host [num_axes]: the first sections[0]
+ *              frequencies take their positions from axis 0, the next
+ *              sections[1] from axis 1 and so on; their sum is rotary_dim / 2.
+ * pairs        PKA_ROPE_HALVES or PKA_ROPE_NEIGHBOURS.
+ * slot_map     int64 [num_tokens] device: page * page_size + slot in page
+ *              (paged_kv_tables).  A negative entry skips the token's k and v;
+ *              its q is rotated all the same.  An entry at or past num_pages *
+ *              page_size does too and sets the slot bit of the status word
+ *              (PKA_ERR_DEVICE_BOUNDS).  Entries must be distinct.
+ * k_pages, v_pages, stride_page, stride_head  HND pools as for paged_decode_run.
+ * dtype        PKA_DTYPE_BF16 or PKA_DTYPE_F16: q, q_out, k, v and the pools, all
+ *              16-byte aligned with strides that are multiples of 8.
+ * status       NULL or int32 [1] device status word (pka_status_check).
+ */
+int paged_rope_append(const void* q, int64_t q_stride_tok, int64_t q_stride_head, void* q_out,
+                      int64_t q_out_stride_tok, int64_t q_out_stride_head, int32_t num_qo_heads,
+                      const void* k, const void* v, int64_t kv_stride_tok, int64_t kv_stride_head,
+                      int32_t num_kv_heads, int32_t head_dim, const int32_t* positions,
+                      int64_t positions_stride, const double* inv_freq, int32_t rotary_dim,
+                      int32_t num_axes, const int32_t* sections_host, int32_t pairs,
+                      const int64_t* slot_map, int64_t num_tokens, void* k_pages, void* v_pages,
+                      int64_t num_pages, int32_t page_size, int64_t stride_page, int64_t stride_head,
+                      int32_t dtype, int32_t* status, void* stream);
+
+/*
+ * The operations below change who holds which page.  No page carries a count:
+ * a request's row holds the pages in its first ceil(kv_len / page_size)
+ * entries, and a page is in use while some row holds it.  A prefix that is to
+ * outlive its requests is kept in a row of its own.  kv_lens, free_pages with
+ * free_head, block_tables with bt_row_stride and max_pages_per_seq, page_size
+ * and status as for paged_kv_tables (batch_size <= 16384); all arrays int32 on
+ * the device.  A refused call sets its bit in the status word and changes
+ * nothing but its outputs, which then say so.  All may be captured.
+ *
+ * Fork: row children[i] becomes a copy of row parents[i].  It shares the
+ * parent's full pages; where the parent's last page is not full the child gets
+ * a page of the free list (in the order of the forks) for a copy of it, so
+ * that each may append to its own.
+ * parents, children  [num_forks] rows.  A child is named once and is no parent;
+ *              what its row held before is forgotten, not released.
+ *              num_forks <= batch_size.
+ * seq_lens     [batch_size], out: kv_lens, a child's replaced by its parent's.
+ * src_pages, dst_pages  [num_forks], out: the pages to copy (paged_kv_copy), -1
+ *              where there is none.
+ * free_head_out  [1], out: free_head plus the pages taken.
+ * Refused: rows out of range, a child named twice or also a parent
+ * (PKA_ERR_DEVICE_BOUNDS); too few free pages, a parent's length outside its
+ * row (PKA_ERR_DEVICE_CAPACITY).  seq_lens then repeats kv_lens, free_head_out
+ * free_head, and the moves are -1.
+ */
+int paged_kv_fork(const int32_t* parents, const int32_t* children, int32_t num_forks,
+                  const int32_t* kv_lens, int32_t batch_size, const int32_t* free_pages,
+                  int32_t num_free, const int32_t* free_head, int32_t page_size,
+                  int32_t* block_tables, int64_t bt_row_stride, int32_t max_pages_per_seq,
+                  int32_t* seq_lens, int32_t* src_pages, int32_t* dst_pages,
+                  int32_t* free_head_out, int32_t* status, void* stream);
+
+/*
+ * Release: the pages that a released row holds and no other row does go back to
+ * the free list, in ascending order, right below its head:
+ * free_pages[free_head - n .. free_head) for n of them.
+ * rows         [num_rows] distinct rows, num_rows <= batch_size.
+ * num_pages    pages of the pool, at most 2^22.
+ * seq_lens     [batch_size], out: kv_lens, 0 for the released rows.
+ * free_head_out  [1], out: free_head - n.
+ * Refused: rows out of range or named twice, a table entry outside the pool
+ * (PKA_ERR_DEVICE_BOUNDS); a length outside its row, a list without room below
+ * its head (PKA_ERR_DEVICE_CAPACITY).
+ */
+int paged_kv_free(const int32_t* rows, int32_t num_rows, const int32_t* kv_lens,
+                  int32_t batch_size, int32_t* free_pages, int32_t num_free,
+                  const int32_t* free_head, int32_t page_size, const int32_t* block_tables,
+                  int64_t bt_row_stride, int32_t max_pages_per_seq, int64_t num_pages,
+                  int32_t* seq_lens, int32_t* free_head_out, int32_t* status, void* stream);
+
+/*
+ * Compaction: of the pages in use and the free ones together, the lowest become
+ * the pages in use and the others the free list, in ascending order.  Pages
+ * that are in neither stay out of it.  The i-th page in use that has to move, in
+ * ascending order, goes to the i-th free page that is to be in use.
+ * num_pages    pages of the pool, at most 2^22.
+ * block_tables_out  [batch_size, max_pages_per_seq], rows bt_out_row_stride
+ *              apart: the tables with the moved pages' new places; entries behind
+ *              a row's pages as they were.  May be block_tables itself.
+ * free_pages_out  [num_free]: as many free pages as before from free_head on, and
+ *              the entries before it as they were.  May be free_pages itself.
+ * src_pages, dst_pages  [max_moves], out: the pages to copy (paged_kv_copy), -1
+ *              behind the last.  num_moves [1], out: how many.
+ * Refused: an entry outside the pool, a free page that is in use or listed
+ * twice (PKA_ERR_DEVICE_BOUNDS); a length outside its row, more than max_moves
+ * moves (PKA_ERR_DEVICE_CAPACITY).  The outputs then repeat the inputs, without
+ * moves.
+ */
+int paged_kv_compact(const int32_t* kv_lens, int32_t batch_size, const int32_t* free_pages,
+                     int32_t num_free, const int32_t* free_head, int32_t page_size,
+                     const int32_t* block_tables, int64_t bt_row_stride,
+                     int32_t max_pages_per_seq, int64_t num_pages, int32_t* block_tables_out,
+                     int64_t bt_out_row_stride, int32_t* free_pages_out, int32_t* src_pages,
+                     int32_t* dst_pages, int32_t max_moves, int32_t* num_moves, int32_t* status,
+                     void* stream);
+
+/*
+ * Copy page src_pages[i] to page dst_pages[i] in each of num_pools pools.
+ * pools        [num_pools] host array of device pointers, 16-byte aligned:
+ *              K, V or latent pools of any type, of one layer or of all.
+ * page_strides, page_bytes  [num_pools] host arrays: bytes from page to page and of
+ *              a page, multiples of 16.
+ * src_pages, dst_pages  [num_entries] device; an entry with a negative page is
+ *              skipped, one with a page at or past num_pages too, setting the page bit
+ *              of the status word (PKA_ERR_DEVICE_BOUNDS).  A destination must
+ *              not be the source or destination of another entry.
+ * count        NULL or [1] device: only the first count entries (at most
+ *              num_entries) are looked at.
+ */
+int paged_kv_copy(void* const* pools, const int64_t* page_strides, const int64_t* page_bytes,
+                  int32_t num_pools, int64_t num_pages, const int32_t* src_pages,
+                  const int32_t* dst_pages, int32_t num_entries, const int32_t* count,
+                  int32_t* status, void* stream);
 
 /* ======================================================================== */
 /* Latent attention                                                          */

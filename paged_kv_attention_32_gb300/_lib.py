@@ -22,6 +22,7 @@ PKA_ERR_DEVICE_CAPACITY = -7
 PKA_DTYPE_BF16, PKA_DTYPE_F16, PKA_DTYPE_F32 = 0, 1, 2
 PKA_MASK_DENSE, PKA_MASK_CAUSAL, PKA_MASK_VARIABLE_WINDOW = 0, 1, 2
 PKA_PLAN_HOST_ONLY = 1
+PKA_ROPE_HALVES, PKA_ROPE_NEIGHBOURS = 0, 1
 PKA_KERNEL_CUDA_CORE, PKA_KERNEL_MMA = 0, 1
 
 # every symbol include/pka.h declares
@@ -36,6 +37,7 @@ EXPORTED = (
     "batch_prefill_plan", "batch_prefill_plan_fixed", "batch_prefill_plan_destroy", "batch_prefill_plan_check",
     "batch_prefill_run",
     "paged_kv_tables", "pka_status_check", "paged_latent_append",
+    "paged_rope_append", "paged_kv_fork", "paged_kv_free", "paged_kv_compact", "paged_kv_copy",
     "paged_latent_decode_plan", "paged_latent_decode_plan_update",
     "paged_latent_decode_plan_destroy", "paged_latent_decode_plan_info",
     "paged_latent_decode_plan_export", "paged_latent_decode_plan_check",
@@ -127,6 +129,7 @@ class LatentPrefillDesc(ctypes.Structure):
 
 _vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 _pi32 = ctypes.POINTER(ctypes.c_int32)
+_pi64 = ctypes.POINTER(ctypes.c_int64)
 
 _SIGS = {
     "pka_last_error": (ctypes.c_char_p, []),
@@ -162,6 +165,18 @@ _SIGS = {
     "pka_status_check": (ctypes.c_int, [_vp, _vp]),
     "paged_latent_append": (ctypes.c_int, [_vp, _i64, _vp, _i64, _i32, _i32, _vp, _i64, _vp, _i64,
                                            _i32, _i64, _i32, _vp, _vp]),
+    "paged_rope_append": (ctypes.c_int, [_vp, _i64, _i64, _vp, _i64, _i64, _i32, _vp, _vp, _i64,
+                                         _i64, _i32, _i32, _vp, _i64, _vp, _i32, _i32, _pi32, _i32,
+                                         _vp, _i64, _vp, _vp, _i64, _i32, _i64, _i64, _i32, _vp,
+                                         _vp]),
+    "paged_kv_fork": (ctypes.c_int, [_vp, _vp, _i32, _vp, _i32, _vp, _i32, _vp, _i32, _vp, _i64,
+                                     _i32, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "paged_kv_free": (ctypes.c_int, [_vp, _i32, _vp, _i32, _vp, _i32, _vp, _i32, _vp, _i64, _i32,
+                                     _i64, _vp, _vp, _vp, _vp]),
+    "paged_kv_compact": (ctypes.c_int, [_vp, _i32, _vp, _i32, _vp, _i32, _vp, _i64, _i32, _i64,
+                                        _vp, _i64, _vp, _vp, _vp, _i32, _vp, _vp, _vp]),
+    "paged_kv_copy": (ctypes.c_int, [ctypes.POINTER(_vp), _pi64, _pi64, _i32, _i64, _vp, _vp, _i32,
+                                     _vp, _vp, _vp]),
     "paged_latent_decode_plan": (ctypes.c_int, [ctypes.POINTER(_vp), ctypes.POINTER(LatentDesc),
                                                 _pi32, _pi32, ctypes.POINTER(_sz), _vp]),
     "paged_latent_decode_plan_update": (ctypes.c_int, [_vp, _i32, _pi32, _pi32,

@@ -637,6 +637,309 @@ def paged_latent_append(latent, rope, slot_map, pages, status=None, stream=None)
     return pages
 
 
+def _page_strides(k_pages, v_pages):
+    """(pages, KV heads, page size, page stride, head stride) of a pair of HND pools."""
+    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape or v_pages.stride() != k_pages.stride():
+        raise ValueError("k_pages and v_pages must be [num_pages, num_kv_heads, page_size, head_dim] "
+                         "with the same strides")
+    n, heads, ps, dim = k_pages.shape
+    page, head, slot, col = k_pages.stride()
+    if col != 1 or slot != dim:
+        raise ValueError("each page's slots must be dense rows of head_dim elements")
+    return n, heads, ps, page, head
+
+
+_ROPE_PAIRS = {"halves": L.PKA_ROPE_HALVES, "neighbours": L.PKA_ROPE_NEIGHBOURS}
+_I32x4 = ctypes.c_int32 * 4
+
+
+def paged_rope_append(k, v, slot_map, k_pages, v_pages, q=None, positions=None, inv_freq=None,
+                      sections=None, pairs="halves", q_out=None, status=None, stream=None):
+    """Write a step's rotated keys and its values to the paged K/V pools (see pka.h): ``k``,
+    ``v`` ``[T, Hkv, D]`` with the same strides, ``slot_map`` int64 ``[T]`` (negative entries
+    skip their token), pools ``[num_pages, Hkv, page_size, D]``, updated in place.
+
+    ``positions`` int32 ``[axes, T]`` (or ``[T]``), ``inv_freq`` float64 ``[rotary_dim / 2]``
+    on the device, ``sections`` frequencies per axis (default: all on the first); without
+    ``inv_freq`` nothing is rotated.  ``pairs``: ``'halves'`` (j and j + rotary_dim / 2) or
+    ``'neighbours'`` (2 j and 2 j + 1).  ``q`` ``[T, Hq, D]``: rotated too and returned, in
+    ``q_out`` (which may be ``q``) or a new tensor; else returns None."""
+    if stream is not None:
+        with _on_stream(stream):
+            return paged_rope_append(k, v, slot_map, k_pages, v_pages, q=q, positions=positions,
+                                     inv_freq=inv_freq, sections=sections, pairs=pairs,
+                                     q_out=q_out, status=status)
+    dtype = k_pages.dtype
+    if dtype is not torch.bfloat16 and dtype is not torch.float16:
+        raise ValueError(f"the pools must be bfloat16 or float16, got {dtype}")
+    dev = torch.cuda.current_device()
+    if not _fits(dtype, dev, k, v, k_pages, v_pages, q, q_out):
+        _check_tensors(dtype, k=k, v=v, k_pages=k_pages, v_pages=v_pages, q=q, q_out=q_out)
+    if not _fits(torch.int64, dev, slot_map):
+        _check_tensors(torch.int64, slot_map=slot_map)
+    if not _fits(torch.int32, dev, positions, status):
+        _check_tensors(torch.int32, positions=positions, status=status)
+    n_pages, heads, ps, page_stride, head_stride = _page_strides(k_pages, v_pages)
+    shape = k.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != k_pages.shape[3] or v.shape != shape:
+        raise ValueError(f"k and v must be [T, {heads}, {k_pages.shape[3]}], got {tuple(shape)} "
+                         f"and {tuple(v.shape)}")
+    T, _, D = shape
+    k_tok, k_head, k_col = k.stride()
+    if T and (k_col != 1 or v.stride() != k.stride()):
+        raise ValueError("k and v must have the same strides and a dense last dimension")
+    if slot_map.numel() != T or not slot_map.is_contiguous():
+        raise ValueError("slot_map needs one contiguous entry per token")
+    Hq = q_tok = q_head = o_tok = o_head = 0
+    if q is not None:
+        if q.dim() != 3 or q.shape[0] != T or q.shape[2] != D or (T and q.stride(2) != 1):
+            raise ValueError(f"q must be [{T}, Hq, {D}] with a dense last dimension")
+        Hq = q.shape[1]
+        q_tok, q_head, _ = q.stride()
+        if q_out is None:
+            q_out = torch.empty((T, Hq, D), dtype=dtype, device=q.device)
+        elif q_out.shape != q.shape or q_out.stride(2) != 1:
+            raise ValueError("q_out must have the shape of q and a dense last dimension")
+        o_tok, o_head, _ = q_out.stride()
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if pairs not in _ROPE_PAIRS:
+        raise ValueError(f"pairs must be 'halves' or 'neighbours', got {pairs!r}")
+    half = axes = pos_stride = 0
+    sec = None
+    if inv_freq is not None:
+        if not _fits(torch.float64, dev, inv_freq):
+            _check_tensors(torch.float64, inv_freq=inv_freq)
+        if not inv_freq.is_contiguous():
+            raise ValueError("inv_freq must be contiguous")
+        half = inv_freq.numel()
+        if positions is None:
+            raise ValueError("a rotation needs positions")
+        axes = 1 if positions.dim() == 1 else positions.shape[0]
+        if positions.dim() > 2 or positions.shape[-1] != T or (T and positions.stride(-1) != 1):
+            raise ValueError(f"positions must be [axes, {T}] or [{T}] with dense rows")
+        pos_stride = positions.stride(0) if axes > 1 else T
+        if sections is None:
+            sections = (half,)
+        if not 1 <= axes <= 4 or len(sections) > axes:
+            raise ValueError("positions need 1 to 4 axes, one for each of the sections")
+        sec = _I32x4(*sections)
+    elif positions is not None or sections is not None:
+        raise ValueError("positions and sections go with inv_freq")
+    rc = L.lib().paged_rope_append(
+        _ptr(q) if Hq else None, q_tok, q_head, _ptr(q_out) if Hq else None, o_tok, o_head, Hq,
+        k.data_ptr(), v.data_ptr(), k_tok, k_head, heads, D, _ptr(positions), pos_stride,
+        _ptr(inv_freq), 2 * half, axes, sec, _ROPE_PAIRS[pairs], slot_map.data_ptr(), T,
+        k_pages.data_ptr(), v_pages.data_ptr(), n_pages, ps, page_stride, head_stride,
+        _DTYPES[dtype], _ptr(status), torch._C._cuda_getCurrentRawStream(dev))
+    if rc:
+        L.check(rc, "paged_rope_append")
+    return q_out
+
+
+def _tables_of(kv_lens, block_tables):
+    """(rows, width, row stride) of the tables, one row per entry of kv_lens."""
+    B = kv_lens.numel()
+    if block_tables.dim() != 2 or block_tables.shape[0] != B or not kv_lens.is_contiguous():
+        raise ValueError("block_tables must have one row per request, kv_lens be contiguous")
+    width = block_tables.shape[1]
+    row, col = block_tables.stride()
+    if col != 1:
+        raise ValueError("block_tables rows must be dense")
+    return B, width, row if B > 1 or row > width else width   # one row's stride says nothing
+
+
+def _out_i32(name, t, like, n):
+    """An int32 output of ``n`` entries: the given one, checked, or a new one."""
+    if t is None:
+        return like.new_empty(n)
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must hold {n} contiguous entries")
+    return t
+
+
+def _one_head(free_head, free_pages):
+    if free_head.numel() != 1 or not free_pages.is_contiguous():
+        raise ValueError("free_head must hold one entry, free_pages be contiguous")
+
+
+KvFork = namedtuple("KvFork", "seq_lens src_pages dst_pages free_head")
+
+
+def paged_kv_fork(parents, children, kv_lens, free_pages, free_head, block_tables, *, page_size,
+                  seq_lens=None, src_pages=None, dst_pages=None, free_head_out=None, status=None,
+                  stream=None):
+    """Make rows ``children`` of ``block_tables`` copies of rows ``parents`` (see pka.h): full
+    pages are shared, a last page that is not full is replaced by a fresh one.  All int32 on the
+    device.  Returns ``KvFork(seq_lens, src_pages, dst_pages, free_head)``: the lengths with the
+    children's, the pages to copy with ``paged_kv_copy`` (-1: none) and the advanced head.  A
+    call that does not fit changes nothing and sets ``status`` (``check_status``)."""
+    if stream is not None:
+        with _on_stream(stream):
+            return paged_kv_fork(parents, children, kv_lens, free_pages, free_head, block_tables,
+                                 page_size=page_size, seq_lens=seq_lens, src_pages=src_pages,
+                                 dst_pages=dst_pages, free_head_out=free_head_out, status=status)
+    dev = torch.cuda.current_device()
+    if not _fits(torch.int32, dev, parents, children, kv_lens, free_pages, free_head, block_tables,
+                 seq_lens, src_pages, dst_pages, free_head_out, status):
+        _check_tensors(torch.int32, parents=parents, children=children, kv_lens=kv_lens,
+                       free_pages=free_pages, free_head=free_head, block_tables=block_tables,
+                       seq_lens=seq_lens, src_pages=src_pages, dst_pages=dst_pages,
+                       free_head_out=free_head_out, status=status)
+    B, width, row = _tables_of(kv_lens, block_tables)
+    _one_head(free_head, free_pages)
+    n = parents.numel()
+    if children.numel() != n or not (parents.is_contiguous() and children.is_contiguous()):
+        raise ValueError("parents and children must be contiguous, one child per parent")
+    seq_lens = _out_i32("seq_lens", seq_lens, kv_lens, B)
+    src_pages = _out_i32("src_pages", src_pages, kv_lens, n)
+    dst_pages = _out_i32("dst_pages", dst_pages, kv_lens, n)
+    free_head_out = _out_i32("free_head_out", free_head_out, kv_lens, 1)
+    rc = L.lib().paged_kv_fork(
+        parents.data_ptr(), children.data_ptr(), n, kv_lens.data_ptr(), B, free_pages.data_ptr(),
+        free_pages.numel(), free_head.data_ptr(), page_size, block_tables.data_ptr(), row, width,
+        seq_lens.data_ptr(), src_pages.data_ptr(), dst_pages.data_ptr(), free_head_out.data_ptr(),
+        _ptr(status), torch._C._cuda_getCurrentRawStream(dev))
+    if rc:
+        L.check(rc, "paged_kv_fork")
+    return KvFork(seq_lens, src_pages, dst_pages, free_head_out)
+
+
+KvFree = namedtuple("KvFree", "seq_lens free_head")
+
+
+def paged_kv_free(rows, kv_lens, free_pages, free_head, block_tables, *, page_size, num_pages,
+                  seq_lens=None, free_head_out=None, status=None, stream=None):
+    """Release ``rows`` (int32, distinct): pages that only they hold go back to ``free_pages``,
+    ascending, right below its head (see pka.h).  Returns ``KvFree(seq_lens, free_head)``: the
+    lengths with the released rows' 0, and the lowered head."""
+    if stream is not None:
+        with _on_stream(stream):
+            return paged_kv_free(rows, kv_lens, free_pages, free_head, block_tables,
+                                 page_size=page_size, num_pages=num_pages, seq_lens=seq_lens,
+                                 free_head_out=free_head_out, status=status)
+    dev = torch.cuda.current_device()
+    if not _fits(torch.int32, dev, rows, kv_lens, free_pages, free_head, block_tables, seq_lens,
+                 free_head_out, status):
+        _check_tensors(torch.int32, rows=rows, kv_lens=kv_lens, free_pages=free_pages,
+                       free_head=free_head, block_tables=block_tables, seq_lens=seq_lens,
+                       free_head_out=free_head_out, status=status)
+    B, width, row = _tables_of(kv_lens, block_tables)
+    _one_head(free_head, free_pages)
+    if not rows.is_contiguous():
+        raise ValueError("rows must be contiguous")
+    seq_lens = _out_i32("seq_lens", seq_lens, kv_lens, B)
+    free_head_out = _out_i32("free_head_out", free_head_out, kv_lens, 1)
+    rc = L.lib().paged_kv_free(
+        rows.data_ptr(), rows.numel(), kv_lens.data_ptr(), B, free_pages.data_ptr(),
+        free_pages.numel(), free_head.data_ptr(), page_size, block_tables.data_ptr(), row, width,
+        num_pages, seq_lens.data_ptr(), free_head_out.data_ptr(), _ptr(status),
+        torch._C._cuda_getCurrentRawStream(dev))
+    if rc:
+        L.check(rc, "paged_kv_free")
+    return KvFree(seq_lens, free_head_out)
+
+
+KvCompaction = namedtuple("KvCompaction", "block_tables free_pages src_pages dst_pages num_moves")
+
+
+def paged_kv_compact(kv_lens, free_pages, free_head, block_tables, *, page_size, num_pages,
+                     block_tables_out=None, free_pages_out=None, src_pages=None, dst_pages=None,
+                     num_moves=None, status=None, stream=None):
+    """Move the pages in use to the lowest places among themselves and the free pages (see
+    pka.h).  Returns ``KvCompaction(block_tables, free_pages, src_pages, dst_pages, num_moves)``:
+    new tables and free list (the given outputs, which may be the inputs), and the pages to copy
+    with ``paged_kv_copy``, whose ``count`` takes ``num_moves``; -1 behind the last.  Given
+    ``src_pages`` and ``dst_pages`` bound the moves; without them there is room for all."""
+    if stream is not None:
+        with _on_stream(stream):
+            return paged_kv_compact(kv_lens, free_pages, free_head, block_tables,
+                                    page_size=page_size, num_pages=num_pages,
+                                    block_tables_out=block_tables_out,
+                                    free_pages_out=free_pages_out, src_pages=src_pages,
+                                    dst_pages=dst_pages, num_moves=num_moves, status=status)
+    dev = torch.cuda.current_device()
+    if not _fits(torch.int32, dev, kv_lens, free_pages, free_head, block_tables, block_tables_out,
+                 free_pages_out, src_pages, dst_pages, num_moves, status):
+        _check_tensors(torch.int32, kv_lens=kv_lens, free_pages=free_pages, free_head=free_head,
+                       block_tables=block_tables, block_tables_out=block_tables_out,
+                       free_pages_out=free_pages_out, src_pages=src_pages, dst_pages=dst_pages,
+                       num_moves=num_moves, status=status)
+    B, width, row = _tables_of(kv_lens, block_tables)
+    _one_head(free_head, free_pages)
+    if block_tables_out is None:
+        block_tables_out, out_row = kv_lens.new_empty((B, width)), width
+    else:
+        if block_tables_out.shape != block_tables.shape:
+            raise ValueError("block_tables_out must have the shape of block_tables")
+        out_row = _tables_of(kv_lens, block_tables_out)[2]
+    n = free_pages.numel()
+    free_pages_out = _out_i32("free_pages_out", free_pages_out, kv_lens, n)
+    most = min(n, num_pages) if src_pages is None else src_pages.numel()
+    src_pages = _out_i32("src_pages", src_pages, kv_lens, most)
+    dst_pages = _out_i32("dst_pages", dst_pages, kv_lens, most)
+    num_moves = _out_i32("num_moves", num_moves, kv_lens, 1)
+    rc = L.lib().paged_kv_compact(
+        kv_lens.data_ptr(), B, free_pages.data_ptr(), n, free_head.data_ptr(), page_size,
+        block_tables.data_ptr(), row, width, num_pages, block_tables_out.data_ptr(), out_row,
+        free_pages_out.data_ptr(), src_pages.data_ptr(), dst_pages.data_ptr(), most,
+        num_moves.data_ptr(), _ptr(status), torch._C._cuda_getCurrentRawStream(dev))
+    if rc:
+        L.check(rc, "paged_kv_compact")
+    return KvCompaction(block_tables_out, free_pages_out, src_pages, dst_pages, num_moves)
+
+
+class KvPools:
+    """Pools that ``paged_kv_copy`` copies pages in, their addresses marshalled once: tensors
+    ``[num_pages, ...]`` of any type (K, V or latent pools, of one layer or of all), each page
+    dense, all with the same number of pages."""
+
+    def __init__(self, pools):
+        self.pools = list(pools)
+        if not self.pools:
+            raise ValueError("at least one pool is needed")
+        self.num_pages = self.pools[0].shape[0]
+        self.device = self.pools[0].get_device()
+        for t in self.pools:
+            if t.dim() < 2 or t.shape[0] != self.num_pages or t.get_device() != self.device:
+                raise ValueError("pools must be [num_pages, ...] with the same number of pages, on "
+                                 "one device")
+            if self.num_pages and not t[0].is_contiguous():
+                raise ValueError("each page of a pool must be dense")
+        n = len(self.pools)
+        size = [t[0].numel() * t.element_size() if self.num_pages else 0 for t in self.pools]
+        self.c = ((ctypes.c_void_p * n)(*(t.data_ptr() for t in self.pools)),
+                  (ctypes.c_int64 * n)(*(t.stride(0) * t.element_size() if self.num_pages > 1 else s
+                                         for t, s in zip(self.pools, size))),
+                  (ctypes.c_int64 * n)(*size), n, self.num_pages)
+
+
+def paged_kv_copy(pools, src_pages, dst_pages, count=None, status=None, stream=None):
+    """Copy page ``src_pages[i]`` to ``dst_pages[i]`` in every pool (see pka.h): ``pools`` a
+    ``KvPools`` or a list of tensors, entries int32 on the device (negative: skipped), ``count``
+    int32 ``[1]`` limits them.  A page outside the pool is skipped and reported in ``status``."""
+    if stream is not None:
+        with _on_stream(stream):
+            return paged_kv_copy(pools, src_pages, dst_pages, count=count, status=status)
+    if not isinstance(pools, KvPools):
+        pools = KvPools(pools)
+    dev = torch.cuda.current_device()
+    if not _fits(torch.int32, dev, src_pages, dst_pages, count, status):
+        _check_tensors(torch.int32, src_pages=src_pages, dst_pages=dst_pages, count=count,
+                       status=status)
+    if pools.device != dev:
+        raise ValueError(f"the pools are on cuda:{pools.device}, the current device is cuda:{dev}")
+    n = src_pages.numel()
+    if dst_pages.numel() != n or not (src_pages.is_contiguous() and dst_pages.is_contiguous()):
+        raise ValueError("src_pages and dst_pages must be contiguous, one of each per entry")
+    if count is not None and count.numel() != 1:
+        raise ValueError("count must hold one entry")
+    rc = L.lib().paged_kv_copy(*pools.c, src_pages.data_ptr(), dst_pages.data_ptr(), n, _ptr(count),
+                               _ptr(status), torch._C._cuda_getCurrentRawStream(dev))
+    if rc:
+        L.check(rc, "paged_kv_copy")
+
+
 class LatentDecodePlan:
     """Owns a ``pka_latent_plan*``; freed with ``paged_latent_decode_plan_destroy``."""
 

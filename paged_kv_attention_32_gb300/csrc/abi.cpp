@@ -58,6 +58,12 @@ int read_status(int32_t* d_status, cudaStream_t stream) {
                 st);
   if (st & STATUS_SLOT_BOUNDS)
     return fail(PKA_ERR_DEVICE_BOUNDS, "a slot map entry is outside the pool (status 0x%x)", st);
+  if (st & STATUS_ROWS)
+    return fail(PKA_ERR_DEVICE_BOUNDS,
+                "a row to fork or release is outside the table, given twice, or parent and child "
+                "at once (status 0x%x)", st);
+  if (st & STATUS_FREE_LIST)
+    return fail(PKA_ERR_DEVICE_BOUNDS, "a page of the free list is in use or listed twice (status 0x%x)", st);
   if (st & STATUS_CAPACITY)
     return fail(PKA_ERR_DEVICE_CAPACITY,
                 "a step's tokens do not fit the free pages, a table row or the slot map, or a "

@@ -6,6 +6,7 @@
 #include <cstdarg>
 #include <cstdint>
 #include <cstdio>
+#include <exception>
 #include <string>
 
 #include <cuda_runtime.h>
@@ -63,6 +64,26 @@ int check_device(int plan_device);
 // Waits for `stream`, reads and clears a device status word, and maps its bits
 // to an error code.
 int read_status(int32_t* d_status, cudaStream_t stream);
+
+// Runs `f`, turning a C++ exception (a host allocation that failed) into an error code.
+template <typename F>
+int guarded(F&& f) {
+  try {
+    return f();
+  } catch (const std::exception& e) {
+    return fail(PKA_ERR_INVALID_ARG, "host error: %s", e.what());
+  }
+}
+
+// A byte range, and whether two share a byte.
+struct Range {
+  const void* p;
+  size_t n;
+};
+inline bool overlap(const Range& x, const Range& y) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(x.p), b = reinterpret_cast<uintptr_t>(y.p);
+  return x.n > 0 && y.n > 0 && a < b + y.n && b < a + x.n;
+}
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 

@@ -16,22 +16,6 @@ using namespace pka;
 
 namespace {
 
-// Runs `f`, turning a C++ exception (a host allocation that failed) into an error code.
-template <typename F>
-int guarded(F&& f) {
-  try {
-    return f();
-  } catch (const std::exception& e) {
-    return fail(PKA_ERR_INVALID_ARG, "host error: %s", e.what());
-  }
-}
-
-// Whether two byte ranges share a byte.
-bool overlap(const void* p, size_t n, const void* q, size_t m) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-  return n > 0 && m > 0 && a < b + m && b < a + n;
-}
-
 // Makes `next`, whose host arrays are built, the plan *p on the device: in p's buffers, or
 // in larger ones.  Where anything fails p stays the plan that it was.
 // One asynchronous copy of the arrays from a pinned image, which is rewritten only after
@@ -157,10 +141,6 @@ int paged_kv_tables(const int32_t* kv_lens, const int32_t* new_lens, int32_t bat
                         (const void*)qo_indptr, (const void*)free_head_out, (const void*)status})
     PKA_CHECK_ARG(aligned(p, 4), "int32 arrays must be 4-byte aligned");
   PKA_CHECK_ARG(aligned(slot_map, 8), "slot_map must be 8-byte aligned");
-  struct Range {
-    const void* p;
-    size_t n;
-  };
   const size_t B = (size_t)batch_size;
   const Range ins[] = {{kv_lens, B * 4}, {new_lens, B * 4}, {free_pages, (size_t)num_free * 4},
                        {free_head, 4}};
@@ -170,9 +150,9 @@ int paged_kv_tables(const int32_t* kv_lens, const int32_t* new_lens, int32_t bat
                         {status, status != nullptr ? size_t(4) : 0}};
   for (const Range& o : outs) {
     for (const Range& i : ins)
-      PKA_CHECK_ARG(!overlap(o.p, o.n, i.p, i.n), "an output overlaps an input");
+      PKA_CHECK_ARG(!overlap(o, i), "an output overlaps an input");
     for (const Range& u : outs)
-      PKA_CHECK_ARG(&u == &o || !overlap(o.p, o.n, u.p, u.n), "two outputs overlap");
+      PKA_CHECK_ARG(&u == &o || !overlap(o, u), "two outputs overlap");
   }
   return launch_kv_tables(kv_lens, new_lens, batch_size, free_pages, num_free, free_head,
                           page_size, block_tables, bt_row_stride, max_pages_per_seq, seq_lens,

@@ -69,7 +69,9 @@ enum : int32_t {
   STATUS_WAIT_TIMEOUT = 1,  // an mbarrier wait hit its iteration limit
   STATUS_PAGE_BOUNDS = 2,   // paged_decode_check_tables found an entry outside [0, num_pages)
   STATUS_CAPACITY = 4,      // paged_kv_tables: a step that does not fit
-  STATUS_SLOT_BOUNDS = 8,   // paged_latent_append: a slot past the pool
+  STATUS_SLOT_BOUNDS = 8,   // paged_latent_append, paged_rope_append: a slot past the pool
+  STATUS_ROWS = 16,         // paged_kv_fork / _free: a row outside the table or given twice
+  STATUS_FREE_LIST = 32,    // paged_kv_compact: a free page that is in use or listed twice
 };
 
 }  // namespace pka
