@@ -19,6 +19,9 @@
  *   paged_decode_step_host
  *       one decode step from host buffers: copies in, re-plan, run, copies
  *       out, queued in order on one stream.
+ *   paged_prefix_decode_plan / paged_prefix_decode_run
+ *       paged decode of requests that begin with the same pages, which are
+ *       attended over once for all of them.
  *   paged_decode_check_tables
  *       validation of the block-table entries a decode run reads.
  *   paged_kv_tables
@@ -440,6 +443,71 @@ int paged_decode_run_noalloc(const pka_plan* plan, const void* q, int64_t q_stri
                              const int32_t* block_tables, int64_t bt_row_stride,
                              const int32_t* seq_lens_kv_dev, const float* sinks, void* out,
                              float* lse, void* stream);
+
+/* ======================================================================== */
+/* Paged decode behind shared prefixes                                       */
+/* ======================================================================== */
+
+typedef struct pka_prefix_plan pka_prefix_plan; /* opaque */
+
+/*
+ * Plan a paged decode whose requests, in groups, begin with the same pages (a
+ * system prompt, a document, the prompt of several sampled continuations; the
+ * rows that paged_kv_fork makes are such).  A group's shared pages are attended over
+ * once, by the query rows of all of its requests together, instead of once per
+ * request; the result is that of paged_decode_run over the same tables.
+ *
+ * desc, seq_lens_kv_host, qo_indptr_host, workspace_bytes_out, stream  as for
+ *              paged_decode_plan.  window_left must be -1 (PKA_ERR_UNSUPPORTED).
+ *              mma_min_rows is not used: the decode is the tensor-core one.
+ * group_indptr_host  [num_groups + 1]: group g is requests group_indptr[g] ..
+ *              group_indptr[g + 1] - 1; from 0 to batch_size, not decreasing.
+ * prefix_pages_host  [num_groups]: leading pages that the rows of the group's
+ *              requests have in common, 0 for none; prefix_pages * page_size
+ *              keys that every query row of the group sees: at most kv_len with
+ *              a dense mask, kv_len - q_len + 1 with a causal one.
+ * The workspace holds the fp32 partial states of the prefixes' pieces too.
+ */
+int paged_prefix_decode_plan(pka_prefix_plan** plan_out, const pka_decode_desc* desc,
+                             const int32_t* seq_lens_kv_host, const int32_t* qo_indptr_host,
+                             const int32_t* group_indptr_host, int32_t num_groups,
+                             const int32_t* prefix_pages_host, size_t* workspace_bytes_out,
+                             void* stream);
+
+/* Re-plan in place for a new batch, as paged_decode_plan_update does: capture
+ * a run again after it, and do not replay the old graph. */
+int paged_prefix_decode_plan_update(pka_prefix_plan* plan, int32_t batch_size,
+                                    const int32_t* seq_lens_kv_host,
+                                    const int32_t* qo_indptr_host,
+                                    const int32_t* group_indptr_host, int32_t num_groups,
+                                    const int32_t* prefix_pages_host, size_t* workspace_bytes_out,
+                                    void* stream);
+
+/* Free a plan (NULL is ignored); no run that uses it may still execute. */
+void paged_prefix_decode_plan_destroy(pka_prefix_plan* plan);
+
+/* The decode part's summary, the number of pieces of prefixes (pairs of CTAs) and,
+ * [batch_size], the pieces that each request's prefix is cut into along its keys, 0
+ * where it has none.  Either of the latter may be NULL. */
+int paged_prefix_decode_plan_info(const pka_prefix_plan* plan, pka_plan_info* info,
+                                  int32_t* num_pieces_out, int32_t* prefix_chunks_out);
+
+/* As paged_decode_plan_check. */
+int paged_prefix_decode_plan_check(const pka_prefix_plan* plan, void* stream);
+
+/*
+ * Run the planned decode; arguments as for paged_decode_run.  The shared pages
+ * are read through the table row of the group's first request.  With live
+ * lengths each must be at least what the prefix needs (see above): a shorter
+ * request sees the whole prefix all the same.  Runs that use one plan must not
+ * overlap on the GPU.
+ */
+int paged_prefix_decode_run(const pka_prefix_plan* plan, const void* q, int64_t q_stride_tok,
+                            int64_t q_stride_head, const void* k_pages, const void* v_pages,
+                            int64_t kv_stride_page, int64_t kv_stride_head,
+                            const int32_t* block_tables, int64_t bt_row_stride,
+                            const int32_t* seq_lens_kv_dev, const float* sinks, void* out,
+                            float* lse, void* workspace, size_t workspace_bytes, void* stream);
 
 /* ======================================================================== */
 /* LSE merge                                                                 */

@@ -33,6 +33,9 @@ EXPORTED = (
     "paged_decode_plan_export", "paged_decode_run", "paged_decode_plan_check",
     "paged_decode_check_tables", "paged_decode_step_host",
     "paged_decode_run_noalloc",
+    "paged_prefix_decode_plan", "paged_prefix_decode_plan_update",
+    "paged_prefix_decode_plan_destroy", "paged_prefix_decode_plan_info",
+    "paged_prefix_decode_plan_check", "paged_prefix_decode_run",
     "attn_merge_lse",
     "batch_prefill_plan", "batch_prefill_plan_fixed", "batch_prefill_plan_destroy", "batch_prefill_plan_check",
     "batch_prefill_run",
@@ -150,6 +153,16 @@ _SIGS = {
                                               _i32, _vp]),
     "paged_decode_run_noalloc": (ctypes.c_int, [_vp, _vp, _i64, _i64, _vp, _vp, _i64, _i64, _vp,
                                                 _i64, _vp, _vp, _vp, _vp, _vp]),
+    "paged_prefix_decode_plan": (ctypes.c_int, [ctypes.POINTER(_vp), ctypes.POINTER(DecodeDesc),
+                                                _pi32, _pi32, _pi32, _i32, _pi32,
+                                                ctypes.POINTER(_sz), _vp]),
+    "paged_prefix_decode_plan_update": (ctypes.c_int, [_vp, _i32, _pi32, _pi32, _pi32, _i32, _pi32,
+                                                       ctypes.POINTER(_sz), _vp]),
+    "paged_prefix_decode_plan_destroy": (None, [_vp]),
+    "paged_prefix_decode_plan_info": (ctypes.c_int, [_vp, ctypes.POINTER(PlanInfo), _pi32, _pi32]),
+    "paged_prefix_decode_plan_check": (ctypes.c_int, [_vp, _vp]),
+    "paged_prefix_decode_run": (ctypes.c_int, [_vp, _vp, _i64, _i64, _vp, _vp, _i64, _i64, _vp,
+                                               _i64, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "attn_merge_lse": (ctypes.c_int, [_vp, _vp, _i32, _i32, _i32, _i32, _vp, _i32, _vp, _vp]),
     "batch_prefill_plan": (ctypes.c_int, [ctypes.POINTER(_vp), ctypes.POINTER(PrefillDesc),
                                           _pi32, _pi32, ctypes.POINTER(_sz), _pi32, _vp]),

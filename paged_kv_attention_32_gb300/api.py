@@ -344,6 +344,175 @@ class DecodeStep:
         return self._result
 
 
+class PrefixDecodePlan:
+    """Owns a ``pka_prefix_plan*``; freed with ``paged_prefix_decode_plan_destroy``."""
+
+    def __init__(self, handle, desc, workspace_bytes):
+        self.prefix_handle = handle
+        self._follow(desc, workspace_bytes)
+
+    def _follow(self, desc, workspace_bytes):
+        self.desc = desc
+        self.workspace_bytes = workspace_bytes
+        # what every run compares its tensors with
+        self.dtype, self.out_dtype = _TORCH[desc.dtype], _TORCH[desc.out_dtype]
+        self.batch_size, self.table_width = desc.batch_size, desc.max_pages_per_seq
+        self.row = (desc.num_qo_heads, desc.head_dim)
+        self.pages_shape = (desc.num_pages, desc.num_kv_heads, desc.page_size, desc.head_dim)
+        self.return_lse = bool(desc.return_lse)
+        self.total_q = self.info["total_q"]
+
+    @property
+    def info(self):
+        """The decode part's summary, ``num_pieces`` of prefixes (pairs of CTAs) and
+        ``prefix_chunks``, the pieces that each request's prefix is cut into (0: none)."""
+        inf, pieces = L.PlanInfo(), ctypes.c_int32()
+        chunks = torch.zeros(self.desc.batch_size, dtype=torch.int32)
+        L.check(L.lib().paged_prefix_decode_plan_info(
+            self.prefix_handle, ctypes.byref(inf), ctypes.byref(pieces),
+            ctypes.cast(chunks.data_ptr(), L._pi32)), "plan_info")
+        return dict({f: getattr(inf, f) for f, _ in L.PlanInfo._fields_}, num_pieces=pieces.value,
+                    prefix_chunks=chunks.tolist())
+
+    def update(self, seq_lens_kv, group_indptr, prefix_pages, qo_indptr=None, stream=None):
+        """Re-plan in place for a new batch (``paged_prefix_decode_plan_update``); graphs that
+        captured a run of the plan are not replayed after it."""
+        lens, groups = _prefix_groups(seq_lens_kv, group_indptr, prefix_pages, qo_indptr)
+        ws = ctypes.c_size_t()
+        host_only = bool(self.desc.flags & L.PKA_PLAN_HOST_ONLY)
+        rc = L.lib().paged_prefix_decode_plan_update(
+            self.prefix_handle, lens[0][0].numel(), lens[0][1], lens[1][1], groups[0][1],
+            groups[1][0].numel(), groups[1][1], ctypes.byref(ws),
+            None if host_only else _stream(stream))
+        L.check(rc, "paged_prefix_decode_plan_update")
+        self.desc.batch_size = lens[0][0].numel()
+        self._follow(self.desc, ws.value)
+        return self
+
+    def check(self, stream=None):
+        """Synchronise and read the device status word (raises on a kernel timeout)."""
+        L.check(L.lib().paged_prefix_decode_plan_check(self.prefix_handle, _stream(stream)),
+                "plan_check")
+
+    def __del__(self):
+        h, self.prefix_handle = getattr(self, "prefix_handle", None), None
+        if h:
+            L.lib().paged_prefix_decode_plan_destroy(h)
+
+
+def _prefix_groups(seq_lens_kv, group_indptr, prefix_pages, qo_indptr):
+    """Host arrays of a prefix plan: (lengths, query offsets), (group offsets, pages)."""
+    lens, ind = _host_i32(seq_lens_kv), _host_i32(qo_indptr)
+    groups, pages = _host_i32(group_indptr), _host_i32(prefix_pages)
+    if groups[0].numel() != pages[0].numel() + 1:
+        raise ValueError("group_indptr must have one entry more than prefix_pages")
+    if ind[0] is not None and ind[0].numel() != lens[0].numel() + 1:
+        raise ValueError("qo_indptr must have one entry more than seq_lens_kv")
+    return (lens, ind), (groups, pages)
+
+
+def paged_prefix_decode_plan(seq_lens_kv, group_indptr, prefix_pages, *, num_qo_heads,
+                             num_kv_heads, page_size, max_pages_per_seq, num_pages,
+                             qo_indptr=None, q_len=1, max_q_len=0, causal=False, scale=None,
+                             bmm2_scale=1.0, return_lse=False, freeze_seq_lens=True, num_sms=0,
+                             split_waves=0, min_chunk_tokens=0, host_only=False, head_dim=128,
+                             dtype=torch.bfloat16, out_dtype=None, stream=None):
+    """Plan a paged decode of requests that, in groups, begin with the same pages (see pka.h):
+    requests ``group_indptr[g]`` to ``group_indptr[g + 1] - 1`` share their first
+    ``prefix_pages[g]`` pages, which are read once for all of them.  All host arrays; the other
+    arguments as for ``paged_decode_plan``."""
+    in_code, out_code = _dtype_codes(dtype, out_dtype)
+    lens, groups = _prefix_groups(seq_lens_kv, group_indptr, prefix_pages, qo_indptr)
+    d = L.DecodeDesc(
+        batch_size=lens[0][0].numel(), num_qo_heads=num_qo_heads, num_kv_heads=num_kv_heads,
+        head_dim=head_dim, page_size=page_size, max_pages_per_seq=max_pages_per_seq,
+        num_pages=num_pages, dtype=in_code, out_dtype=out_code, q_len=q_len, max_q_len=max_q_len,
+        mask=L.PKA_MASK_CAUSAL if causal else L.PKA_MASK_DENSE, window_left=-1,
+        scale=float("nan") if scale is None else scale, bmm2_scale=bmm2_scale,
+        return_lse=int(bool(return_lse)), freeze_seq_lens=int(bool(freeze_seq_lens)),
+        num_sms=num_sms, split_waves=split_waves, min_chunk_tokens=min_chunk_tokens,
+        flags=L.PKA_PLAN_HOST_ONLY if host_only else 0)
+    h = ctypes.c_void_p()
+    ws = ctypes.c_size_t()
+    rc = L.lib().paged_prefix_decode_plan(
+        ctypes.byref(h), ctypes.byref(d), lens[0][1], lens[1][1], groups[0][1],
+        groups[1][0].numel(), groups[1][1], ctypes.byref(ws),
+        None if host_only else _stream(stream))
+    L.check(rc, "paged_prefix_decode_plan")
+    return PrefixDecodePlan(h, d, ws.value)
+
+
+def paged_prefix_decode_run(plan, q, k_pages, v_pages, block_tables, seq_lens_kv=None, sinks=None,
+                            out=None, lse=None, workspace=None, stream=None):
+    """Run a planned decode behind shared prefixes: ``q`` ``[T, Hq, D]``, pools
+    ``[num_pages, Hkv, page_size, D]``.  Returns ``out`` ``[T, Hq, D]`` (and the base-2 ``lse``
+    ``[T, Hq]`` when the plan returns it), what ``paged_decode_run`` would; rows of a given
+    ``out`` past the plan's are left as they were."""
+    if stream is not None:
+        with _on_stream(stream):
+            return paged_prefix_decode_run(plan, q, k_pages, v_pages, block_tables,
+                                           seq_lens_kv=seq_lens_kv, sinks=sinks, out=out, lse=lse,
+                                           workspace=workspace)
+    if not isinstance(plan, PrefixDecodePlan):
+        raise ValueError("the plan was not made by paged_prefix_decode_plan")
+    dev = torch.cuda.current_device()
+    if not _fits(plan.dtype, dev, q, k_pages, v_pages):
+        _check_tensors(plan.dtype, q=q, k_pages=k_pages, v_pages=v_pages)
+    if not _fits(torch.int32, dev, block_tables, seq_lens_kv):
+        _check_tensors(torch.int32, block_tables=block_tables, seq_lens_kv=seq_lens_kv)
+    need, B, shape = plan.total_q, plan.batch_size, q.shape
+    if len(shape) != 3 or shape[1:] != plan.row or shape[0] < need:
+        raise ValueError(f"q must be [>= {need}, {plan.row[0]}, {plan.row[1]}], got {tuple(shape)}")
+    T = shape[0]
+    q_tok, q_head, q_col = q.stride()
+    if q_col != 1:
+        raise ValueError("q must have a dense last dimension")
+    if k_pages.shape != plan.pages_shape:
+        raise ValueError(f"the pools must be {list(plan.pages_shape)}, got {tuple(k_pages.shape)}")
+    _, _, _, page_stride, head_stride = _page_strides(k_pages, v_pages)
+    if block_tables.dim() != 2 or block_tables.shape[0] < B or \
+            block_tables.shape[1] < plan.table_width or block_tables.stride(1) != 1:
+        raise ValueError("block_tables needs dense rows, one of at least max_pages_per_seq "
+                         "entries per request")
+    row, width = block_tables.stride(0), block_tables.shape[1]
+    if seq_lens_kv is not None and (seq_lens_kv.numel() < B or not seq_lens_kv.is_contiguous()):
+        raise ValueError("seq_lens_kv needs one contiguous entry per request")
+    if sinks is not None:
+        _check_tensors(torch.float32, sinks=sinks)
+        if sinks.numel() != plan.row[0] or not sinks.is_contiguous():
+            raise ValueError("sinks needs one contiguous entry per query head")
+    if out is None:
+        out = torch.empty((T,) + plan.row, dtype=plan.out_dtype, device=q.device)
+    else:
+        _check_tensors(plan.out_dtype, out=out)
+        _contiguous(out=out)
+        if out.dim() != 3 or out.shape[1:] != plan.row or out.shape[0] < need:
+            raise ValueError("out must be [T, num_qo_heads, head_dim]")
+    if lse is not None:
+        _check_tensors(torch.float32, lse=lse)
+        _contiguous(lse=lse)
+        if lse.dim() != 2 or lse.shape[1] != plan.row[0] or lse.shape[0] < need:
+            raise ValueError("lse must be [T, num_qo_heads]")
+    elif plan.return_lse:
+        lse = torch.empty((T, plan.row[0]), dtype=torch.float32, device=q.device)
+    ws_bytes = 0
+    if workspace is not None:
+        _check_tensors(workspace.dtype, workspace=workspace)
+        _contiguous(workspace=workspace)
+        ws_bytes = workspace.numel() * workspace.element_size()
+    elif plan.workspace_bytes > 0:
+        ws_bytes = plan.workspace_bytes
+        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+    rc = L.lib().paged_prefix_decode_run(
+        plan.prefix_handle, q.data_ptr(), q_tok, q_head, k_pages.data_ptr(), v_pages.data_ptr(),
+        page_stride, head_stride, block_tables.data_ptr(),
+        row if B > 1 or row > width else width, _ptr(seq_lens_kv), _ptr(sinks), out.data_ptr(),
+        _ptr(lse), _ptr(workspace), ws_bytes, torch._C._cuda_getCurrentRawStream(dev))
+    if rc:
+        L.check(rc, "paged_prefix_decode_run")
+    return (out, lse) if plan.return_lse else out
+
+
 def attn_merge_lse(v_states, s_states, out_dtype=torch.bfloat16, v_out=None, s_out=None,
                    stream=None):
     """Merge ``[N, S, H, D]`` fp32 states by their ``[N, S, H]`` base-2 LSEs."""

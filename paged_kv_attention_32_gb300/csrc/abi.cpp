@@ -75,16 +75,18 @@ int read_status(int32_t* d_status, cudaStream_t stream) {
 
 using namespace pka;
 
-namespace {
-
-int upload_decode_plan(pka_plan& p, cudaStream_t stream) {
+int pka::upload_decode_plan(pka_plan& p, cudaStream_t stream) {
   const size_t n_items = p.items.size() * sizeof(WorkItem);
   const size_t n_reqs = p.reqs.size() * sizeof(ReqInfo);
   const size_t n_cnt = (size_t)p.num_merge_counters * sizeof(int32_t);
   const size_t off_reqs = up256(n_items);
   const size_t off_status = off_reqs + up256(n_reqs);
   const size_t off_cnt = off_status + 256;   // merge counters, zero between runs
-  const size_t total = off_cnt + up256(n_cnt);
+  const size_t n_pre = p.prefix_items.size() * sizeof(PrefixItem);
+  const size_t n_tok = p.prefix_tokens.size() * sizeof(PrefixToken);
+  const size_t off_pre = off_cnt + up256(n_cnt);
+  const size_t off_tok = off_pre + up256(n_pre);
+  const size_t total = off_tok + up256(n_tok);
   if (p.dev_buf == nullptr || total > p.dev_capacity) {
     // a replan that outgrows the buffer reallocates it with headroom
     if (p.dev_buf != nullptr) {
@@ -102,6 +104,8 @@ int upload_decode_plan(pka_plan& p, cudaStream_t stream) {
   p.d_reqs = reinterpret_cast<const ReqInfo*>(base + off_reqs);
   p.d_status = reinterpret_cast<int32_t*>(base + off_status);
   p.d_merge_cnt = reinterpret_cast<int32_t*>(base + off_cnt);
+  p.d_prefix_items = reinterpret_cast<const PrefixItem*>(base + off_pre);
+  p.d_prefix_tokens = reinterpret_cast<const PrefixToken*>(base + off_tok);
   // One asynchronous copy from a pinned image of the buffer.  The image is
   // rewritten only after the copy that last read it has completed (stage_done);
   // stream order keeps the upload behind runs already queued on the same stream.
@@ -124,7 +128,9 @@ int upload_decode_plan(pka_plan& p, cudaStream_t stream) {
     uint8_t* img = static_cast<uint8_t*>(p.host_stage);
     if (n_items) std::memcpy(img, p.items.data(), n_items);
     std::memcpy(img + off_reqs, p.reqs.data(), n_reqs);
-    std::memset(img + off_status, 0, total - off_status);   // status word and counters
+    std::memset(img + off_status, 0, off_pre - off_status);   // status word and counters
+    if (n_pre) std::memcpy(img + off_pre, p.prefix_items.data(), n_pre);
+    if (n_tok) std::memcpy(img + off_tok, p.prefix_tokens.data(), n_tok);
     PKA_CUDA_TRY(cudaMemcpyAsync(base, img, total, cudaMemcpyHostToDevice, stream),
                  "cudaMemcpyAsync(plan)");
     if (p.stage_done == nullptr)
@@ -141,10 +147,46 @@ int upload_decode_plan(pka_plan& p, cudaStream_t stream) {
   PKA_CUDA_TRY(cudaMemcpyAsync(base + off_reqs, p.reqs.data(), n_reqs, cudaMemcpyHostToDevice,
                                stream),
                "cudaMemcpyAsync(plan requests)");
-  PKA_CUDA_TRY(cudaMemsetAsync(base + off_status, 0, total - off_status, stream),
+  if (n_pre)
+    PKA_CUDA_TRY(cudaMemcpyAsync(base + off_pre, p.prefix_items.data(), n_pre, cudaMemcpyHostToDevice, stream),
+                 "cudaMemcpyAsync(prefix items)");
+  if (n_tok)
+    PKA_CUDA_TRY(cudaMemcpyAsync(base + off_tok, p.prefix_tokens.data(), n_tok, cudaMemcpyHostToDevice, stream),
+                 "cudaMemcpyAsync(prefix tokens)");
+  PKA_CUDA_TRY(cudaMemsetAsync(base + off_status, 0, off_pre - off_status, stream),
                "cudaMemsetAsync(status and counters)");
   return PKA_OK;
 }
+
+int pka::replace_decode_plan(pka_plan& p, pka_plan&& fresh, cudaStream_t stream) {
+  const bool host_only = p.desc.flags & PKA_PLAN_HOST_ONLY;
+  if (!host_only) {
+    const int rc = check_device(p.device);
+    if (rc != PKA_OK) return rc;
+  }
+  fresh.dev_buf = p.dev_buf;
+  fresh.dev_capacity = p.dev_capacity;
+  fresh.device = p.device;
+  fresh.host_stage = p.host_stage;
+  fresh.host_capacity = p.host_capacity;
+  fresh.stage_done = p.stage_done;
+  p.dev_buf = nullptr;
+  p.host_stage = nullptr;
+  p.stage_done = nullptr;
+  p = std::move(fresh);
+  return host_only ? PKA_OK : upload_decode_plan(p, stream);
+}
+
+void pka::release_decode_plan(pka_plan& p) {
+  if (p.stage_done != nullptr) {
+    cudaEventSynchronize(p.stage_done);   // the image is not freed under a pending copy
+    cudaEventDestroy(p.stage_done);
+  }
+  if (p.host_stage != nullptr) cudaFreeHost(p.host_stage);
+  if (p.dev_buf != nullptr) cudaFree(p.dev_buf);
+}
+
+namespace {
 
 int upload_prefill_plan(pka_prefill_plan& p, cudaStream_t stream) {
   const size_t n_tiles = p.tiles.size() * sizeof(PrefillTile);
@@ -264,38 +306,15 @@ int paged_decode_plan_update(pka_plan* p, int32_t batch_size, const int32_t* seq
   pka_plan fresh;
   int rc = build_decode_plan(fresh, d, seq_lens_kv_host, qo_indptr_host);
   if (rc != PKA_OK) return rc;   // the old plan stays as it was
-  if (!(p->desc.flags & PKA_PLAN_HOST_ONLY)) {
-    int dev = -1;
-    PKA_CUDA_TRY(cudaGetDevice(&dev), "cudaGetDevice");
-    PKA_CHECK_ARG(dev == p->device, "plan was made on device %d, current device is %d", p->device,
-                  dev);
-  }
-  fresh.dev_buf = p->dev_buf;
-  fresh.dev_capacity = p->dev_capacity;
-  fresh.device = p->device;
-  fresh.host_stage = p->host_stage;
-  fresh.host_capacity = p->host_capacity;
-  fresh.stage_done = p->stage_done;
-  p->dev_buf = nullptr;
-  p->host_stage = nullptr;
-  p->stage_done = nullptr;
-  *p = std::move(fresh);
-  if (!(p->desc.flags & PKA_PLAN_HOST_ONLY)) {
-    rc = upload_decode_plan(*p, static_cast<cudaStream_t>(stream));
-    if (rc != PKA_OK) return rc;
-  }
+  rc = replace_decode_plan(*p, std::move(fresh), static_cast<cudaStream_t>(stream));
+  if (rc != PKA_OK) return rc;
   if (workspace_bytes_out) *workspace_bytes_out = (size_t)p->workspace_bytes;
   return PKA_OK;
 }
 
 void paged_decode_plan_destroy(pka_plan* plan) {
   if (plan == nullptr) return;
-  if (plan->stage_done != nullptr) {
-    cudaEventSynchronize(plan->stage_done);   // the image is not freed under a pending copy
-    cudaEventDestroy(plan->stage_done);
-  }
-  if (plan->host_stage != nullptr) cudaFreeHost(plan->host_stage);
-  if (plan->dev_buf != nullptr) cudaFree(plan->dev_buf);
+  release_decode_plan(*plan);
   delete plan;
 }
 
@@ -341,15 +360,15 @@ int paged_decode_plan_export(const pka_plan* p, int32_t* items, int32_t* n_chunk
   return PKA_OK;
 }
 
-int paged_decode_run(const pka_plan* p, const void* q, int64_t q_stride_tok,
-                     int64_t q_stride_head, const void* k_pages, const void* v_pages,
-                     int64_t kv_stride_page, int64_t kv_stride_head,
-                     const int32_t* block_tables, int64_t bt_row_stride,
-                     const int32_t* seq_lens_kv_dev, const float* sinks, void* out, float* lse,
-                     void* workspace, size_t workspace_bytes, void* stream) {
-  NvtxRange nvtx_range("pka::paged_decode_run");
-  clear_error();
-  PKA_CHECK_ARG(p != nullptr, "plan must not be NULL");
+}  // extern "C"
+
+int pka::prepare_decode_run(const pka_plan* p, const void* q, int64_t q_stride_tok,
+                            int64_t q_stride_head, const void* k_pages, const void* v_pages,
+                            int64_t kv_stride_page, int64_t kv_stride_head,
+                            const int32_t* block_tables, int64_t bt_row_stride,
+                            const int32_t* seq_lens_kv_dev, const float* sinks, void* out, float* lse,
+                            void* workspace, size_t workspace_bytes, DecodeArgs* args,
+                            CUtensorMap* kmap, CUtensorMap* vmap) {
   PKA_CHECK_ARG(p->dev_buf != nullptr, "plan was built with PKA_PLAN_HOST_ONLY and cannot run");
   PKA_CHECK_ARG(q && k_pages && v_pages && block_tables && out,
                 "q, k_pages, v_pages, block_tables and out must not be NULL");
@@ -374,15 +393,14 @@ int paged_decode_run(const pka_plan* p, const void* q, int64_t q_stride_tok,
   int rc = check_device(p->device);
   if (rc != PKA_OK) return rc;
 
-  CUtensorMap kmap, vmap;
-  rc = encode_kv_pool_map(&kmap, k_pages, p->desc.num_pages, p->Hkv, p->ps, p->D, kv_stride_page,
+  rc = encode_kv_pool_map(kmap, k_pages, p->desc.num_pages, p->Hkv, p->ps, p->D, kv_stride_page,
                           kv_stride_head);
   if (rc != PKA_OK) return rc;
-  rc = encode_kv_pool_map(&vmap, v_pages, p->desc.num_pages, p->Hkv, p->ps, p->D, kv_stride_page,
+  rc = encode_kv_pool_map(vmap, v_pages, p->desc.num_pages, p->Hkv, p->ps, p->D, kv_stride_page,
                           kv_stride_head);
   if (rc != PKA_OK) return rc;
 
-  DecodeArgs a{};
+  DecodeArgs& a = *args;
   a.q = q;
   a.q_stride_tok = q_stride_tok;
   a.q_stride_head = q_stride_head;
@@ -413,6 +431,26 @@ int paged_decode_run(const pka_plan* p, const void* q, int64_t q_stride_tok,
   a.bmm2_scale = p->desc.bmm2_scale;
   a.in_f16 = p->desc.dtype == PKA_DTYPE_F16;
   a.out_dtype = p->desc.out_dtype;
+  return PKA_OK;
+}
+
+extern "C" {
+
+int paged_decode_run(const pka_plan* p, const void* q, int64_t q_stride_tok,
+                     int64_t q_stride_head, const void* k_pages, const void* v_pages,
+                     int64_t kv_stride_page, int64_t kv_stride_head,
+                     const int32_t* block_tables, int64_t bt_row_stride,
+                     const int32_t* seq_lens_kv_dev, const float* sinks, void* out, float* lse,
+                     void* workspace, size_t workspace_bytes, void* stream) {
+  NvtxRange nvtx_range("pka::paged_decode_run");
+  clear_error();
+  PKA_CHECK_ARG(p != nullptr, "plan must not be NULL");
+  DecodeArgs a{};
+  CUtensorMap kmap, vmap;
+  const int rc = prepare_decode_run(p, q, q_stride_tok, q_stride_head, k_pages, v_pages, kv_stride_page,
+                                    kv_stride_head, block_tables, bt_row_stride, seq_lens_kv_dev, sinks, out,
+                                    lse, workspace, workspace_bytes, &a, &kmap, &vmap);
+  if (rc != PKA_OK) return rc;
   return launch_decode(*p, a, kmap, vmap, static_cast<cudaStream_t>(stream));
 }
 

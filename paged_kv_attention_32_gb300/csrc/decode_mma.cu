@@ -141,6 +141,14 @@ decode_mma_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant__ 
         break;
       const int tok0 = (unit0 + warp + k * kWarps) * kUnit;
       const bool full_unit = tok0 >= all_lo && tok0 + kUnit <= all_hi;
+      if (tok0 + kUnit > kv_len) {
+        // slots past the last key may hold anything: p = 0 there, but 0 * inf is not 0.  It
+        // is the warp's last unit, so no copy comes into this stage again.
+        uint8_t* v = my_stages + st * kStageBytes + 2 * kBoxBytes + (lane >> 3) * kBoxBytes + (lane & 7) * 16;
+        if (lane < 16)
+          for (int j = kv_len - tok0; j < kUnit; ++j) *reinterpret_cast<uint4*>(v + j * 128) = make_uint4(0u, 0u, 0u, 0u);
+        __syncwarp();
+      }
       tw.step(stage_u32 + st * kStageBytes, tok0, full_unit, sl2, lane);
       __syncwarp();
       if (k + NSTAGE < my_units) issue(k + NSTAGE);
@@ -185,6 +193,21 @@ int launch_mma(const DecodeArgs& args, const CUtensorMap& kmap, const CUtensorMa
   const int mt = (args.rows_per_cta + 15) / 16;
   const int64_t grid = (int64_t)args.num_items * mt;
   if (grid > 0x7fffffff) return fail(PKA_ERR_INVALID_ARG, "decode grid too large");
+  if (args.behind_prefix) {   // starts while the prefix kernel ends; only its merges wait for it
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kWarps * 32);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kern, args, kmap, vmap);
+    if (e != cudaSuccess) return cuda_fail(e, "decode_mma_kernel launch");
+    return PKA_OK;
+  }
   kern<<<(unsigned)grid, kWarps * 32, smem, stream>>>(args, kmap, vmap);
   e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "decode_mma_kernel launch");

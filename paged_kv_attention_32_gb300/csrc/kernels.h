@@ -10,6 +10,14 @@
 
 namespace pka {
 
+// The checks of a decode run and what it launches with: arguments and both pools' maps.
+int prepare_decode_run(const pka_plan* plan, const void* q, int64_t q_stride_tok,
+                       int64_t q_stride_head, const void* k_pages, const void* v_pages,
+                       int64_t kv_stride_page, int64_t kv_stride_head, const int32_t* block_tables,
+                       int64_t bt_row_stride, const int32_t* seq_lens_kv_dev, const float* sinks,
+                       void* out, float* lse, void* workspace, size_t workspace_bytes,
+                       DecodeArgs* args, CUtensorMap* kmap, CUtensorMap* vmap);
+
 // Decode kernel (CUDA-core or mma variant, as the plan chose); the partials of
 // a split request are merged inside it by the last chunk CTA of each group.
 int launch_decode(const pka_plan& plan, const DecodeArgs& args, const CUtensorMap& kmap,

@@ -54,16 +54,16 @@ int encode_bf16_map(CUtensorMap* map, const void* base, int rank, const uint64_t
 
 namespace {
 int encode_pool_map_uncached(CUtensorMap* map, const void* pool, int64_t num_pages,
-                             int32_t num_heads, int32_t page_size, int32_t head_dim,
-                             int64_t stride_page, int64_t stride_head) {
+                             int32_t num_heads, int32_t page_size, int64_t stride_page,
+                             int64_t stride_head, int32_t rows, int32_t halves) {
   // The 128 columns are split as (d_lo 0..63, d_hi 0..1) and d_hi is placed
   // after the slot dimension: (d_lo, slot, d_hi, head, page).  A box of
   // {64, 16, 2, 1, 1} then lands in shared memory as the two 64-column halves
   // of 16 token rows one after the other -- a whole 16-token unit in one copy.
+  // (encode_kv_box_map: other rows, one half or both.)
   const uint64_t dims[5] = {64, (uint64_t)page_size, 2, (uint64_t)num_heads, (uint64_t)num_pages};
-  const uint64_t strides[4] = {(uint64_t)head_dim * 2, 128, (uint64_t)stride_head * 2,
-                               (uint64_t)stride_page * 2};
-  const uint32_t box[5] = {64, 16, 2, 1, 1};
+  const uint64_t strides[4] = {256, 128, (uint64_t)stride_head * 2, (uint64_t)stride_page * 2};
+  const uint32_t box[5] = {64, (uint32_t)rows, (uint32_t)halves, 1, 1};
   return encode_bf16_map(map, pool, 5, dims, strides, box);
 }
 
@@ -73,13 +73,13 @@ int encode_pool_map_uncached(CUtensorMap* map, const void* pool, int64_t num_pag
 struct PoolMapKey {
   const void* pool;
   int64_t num_pages, stride_page, stride_head;
-  int32_t num_heads, page_size;
+  int32_t num_heads, page_size, rows, halves;
   bool operator==(const PoolMapKey& o) const {
     return pool == o.pool && num_pages == o.num_pages && stride_page == o.stride_page &&
-           stride_head == o.stride_head && num_heads == o.num_heads && page_size == o.page_size;
+           stride_head == o.stride_head && num_heads == o.num_heads && page_size == o.page_size && rows == o.rows && halves == o.halves;
   }
 };
-constexpr int kPoolMapCache = 4;
+constexpr int kPoolMapCache = 8;
 struct PoolMapCache {
   PoolMapKey key[kPoolMapCache] = {};
   CUtensorMap map[kPoolMapCache];
@@ -92,17 +92,23 @@ thread_local PoolMapCache t_pool_maps;
 int encode_kv_pool_map(CUtensorMap* map, const void* pool, int64_t num_pages, int32_t num_heads,
                        int32_t page_size, int32_t head_dim, int64_t stride_page,
                        int64_t stride_head) {
-  PKA_CHECK_ARG(stride_head > 0 && stride_page > 0, "K/V strides must be positive");
   PKA_CHECK_ARG(head_dim == 128, "the K/V pool map takes head_dim 128 (got %d)", head_dim);
-  const PoolMapKey key{pool, num_pages, stride_page, stride_head, num_heads, page_size};
+  return encode_kv_box_map(map, pool, num_pages, num_heads, page_size, stride_page, stride_head, 16, 2);
+}
+
+int encode_kv_box_map(CUtensorMap* map, const void* pool, int64_t num_pages, int32_t num_heads,
+                      int32_t page_size, int64_t stride_page, int64_t stride_head, int32_t rows,
+                      int32_t halves) {
+  PKA_CHECK_ARG(stride_head > 0 && stride_page > 0, "K/V strides must be positive");
+  const PoolMapKey key{pool, num_pages, stride_page, stride_head, num_heads, page_size, rows, halves};
   PoolMapCache& c = t_pool_maps;
   for (int i = 0; i < kPoolMapCache; ++i)
     if (c.used[i] && c.key[i] == key) {
       *map = c.map[i];
       return PKA_OK;
     }
-  const int rc = encode_pool_map_uncached(map, pool, num_pages, num_heads, page_size, head_dim,
-                                          stride_page, stride_head);
+  const int rc = encode_pool_map_uncached(map, pool, num_pages, num_heads, page_size, stride_page,
+                                          stride_head, rows, halves);
   if (rc == PKA_OK) {
     c.key[c.next] = key;
     c.map[c.next] = *map;

@@ -25,4 +25,10 @@ int encode_kv_pool_map(CUtensorMap* map, const void* pool, int64_t num_pages, in
                        int32_t page_size, int32_t head_dim, int64_t stride_page,
                        int64_t stride_head);
 
+// The same pool with boxes of `rows` slots (16, 32 or 64, dividing page_size) of one
+// 64-column half, or of both, one behind the other.
+int encode_kv_box_map(CUtensorMap* map, const void* pool, int64_t num_pages, int32_t num_heads,
+                      int32_t page_size, int64_t stride_page, int64_t stride_head, int32_t rows,
+                      int32_t halves);
+
 }  // namespace pka
