@@ -11,10 +11,10 @@
 //
 // A fork needs no wait between CTAs: each checks all forks and counts the fresh pages
 // before its own itself, as they read only what none of them writes.  Release and
-// compaction are one cluster of 8 CTAs whose shared memories hold the pool's bits
-// between them, a contiguous range of pages each, so that setting a bit is one write to
-// another CTA's shared memory, ranks are scans of bit counts, and one launch does it all.
-// Launch, table reads and the cluster barriers between the steps bound them.
+// compaction are one CTA, or for large tables a cluster of 16, that mark pages each in a copy
+// of its own of the pool's bits, join the copies by slices over their shared memories, and rank pages by
+// scans of bit counts: one launch does it all.  Launch, table reads and the cluster
+// barriers between the steps bound them.
 #include <algorithm>
 
 #include "device_common.cuh"
@@ -39,22 +39,22 @@ __device__ __forceinline__ uint64_t warp_scan(uint64_t x, int lane) {
 }
 
 // Exclusive prefix of `x` over the block's WARPS * 32 threads, and the sum of all.
+// sums: [WARPS + 1] in shared memory.
 template <int WARPS>
-__device__ __forceinline__ uint64_t block_scan(uint64_t x, uint64_t* warp_sums, uint64_t& all) {
+__device__ __forceinline__ uint64_t block_scan(uint64_t x, uint64_t* sums, uint64_t& all) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint64_t inc = warp_scan(x, lane);
   __syncthreads();   // an earlier scan's sums have been read
-  if (lane == 31) warp_sums[warp] = inc;
+  if (lane == 31) sums[warp] = inc;
   __syncthreads();
-  uint64_t before = 0;
-  all = 0;
-#pragma unroll
-  for (int w = 0; w < WARPS; ++w) {
-    const uint64_t s = warp_sums[w];
-    if (w < warp) before += s;
-    all += s;
+  if (warp == 0) {
+    const uint64_t s = lane < WARPS ? sums[lane] : 0, t = warp_scan(s, lane);
+    if (lane < WARPS) sums[lane] = t - s;
+    if (lane == 31) sums[WARPS] = t;
   }
-  return before + inc - x;
+  __syncthreads();
+  all = sums[WARPS];
+  return sums[warp] + inc - x;
 }
 
 __device__ __forceinline__ int pages_of(int len, int ps) {
@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(kForkThreads) kv_fork_kernel(const __grid_cons
   uint32_t* fresh = smem + 2 * n;                              // [n] fresh pages taken before
   uint32_t* is_parent = smem + 3 * n;                          // a bit per row
   uint32_t* is_child = is_parent + words;
-  __shared__ uint64_t warp_sums[kForkThreads / 32];
+  __shared__ uint64_t warp_sums[kForkThreads / 32 + 1];
   __shared__ int s_bad, s_full;
   const int tid = threadIdx.x, lane = tid & 31;
   const int64_t head = __ldg(a.free_head);
@@ -160,37 +160,32 @@ __global__ void __launch_bounds__(kForkThreads) kv_fork_kernel(const __grid_cons
 
 // ---- bits of a pool over the shared memories of a cluster ----------------------
 
-constexpr int kCluster = 8, kThreads = 1024, kWarps = kThreads / 32;
-constexpr int kPiece = 256;   // table entries a warp takes at a time
+constexpr int kMaxCluster = 16, kThreads = 1024, kWarps = kThreads / 32;
+// Table entries up to which one CTA does without the others: their barriers and joined bits
+// cost more than its share of the reads.
+constexpr int64_t kFewEntries = 32768;
+constexpr int kPiece = 512;   // table entries a warp takes at a time
+constexpr int kDynamicSmem = 222 * 1024;
 
-__device__ __forceinline__ void bit_set(uint32_t addr, uint32_t bit) {
-  asm volatile("red.relaxed.cluster.shared::cluster.or.b32 [%0], %1;" ::"r"(addr), "r"(bit) : "memory");
+__device__ __forceinline__ void flag_set(uint32_t addr, uint32_t bits) {
+  asm volatile("red.relaxed.cluster.shared::cluster.or.b32 [%0], %1;" ::"r"(addr), "r"(bits) : "memory");
 }
-__device__ __forceinline__ uint32_t bit_test_set(uint32_t addr, uint32_t bit) {
-  uint32_t old;
-  asm volatile("atom.relaxed.cluster.shared::cluster.or.b32 %0, [%1], %2;" : "=r"(old) : "r"(addr), "r"(bit) : "memory");
-  return old & bit;
-}
-__device__ __forceinline__ uint32_t load_remote(uint32_t addr) {
-  uint32_t x;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x) : "r"(addr) : "memory");
+__device__ __forceinline__ uint4 load_remote4(uint32_t addr) {
+  uint4 x;
+  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+               : "r"(addr)
+               : "memory");
   return x;
 }
 
-// Every thread of the cluster, whole warps again after branches that lanes took apart.
+// Every thread of the NC CTAs, whole warps again after branches that lanes took apart.
+template <int NC>
 __device__ __forceinline__ void sync_all() {
   __syncwarp();
-  cluster_sync();
+  if constexpr (NC > 1) cluster_sync();
+  else __syncthreads();
 }
-
-// The words of one bit per page: word w lies in CTA w >> shift of the cluster.
-struct PageBits {
-  int shift;
-  __device__ __forceinline__ uint32_t addr(const uint32_t* mine, int page) const {
-    const uint32_t w = (uint32_t)page >> 5;
-    return map_to_rank(smem_u32(mine + (w & ((1u << shift) - 1u))), w >> shift);
-  }
-};
 
 // The lowest `n` set bits of `x`.
 __device__ __forceinline__ uint32_t lowest(uint32_t x, int64_t n) {
@@ -202,60 +197,146 @@ __device__ __forceinline__ uint32_t lowest(uint32_t x, int64_t n) {
 
 // What the CTAs of the cluster tell each other: a flag anybody may set, and their counts.
 struct ClusterBoard {
-  uint64_t counts[2][kCluster];
+  uint64_t counts[2][kMaxCluster];
   int32_t flags;
-  uint64_t warp_sums[kWarps];
+  uint64_t warp_sums[kWarps + 1];
 };
 
 // Each CTA's `mine` into slot `which` of everybody's board; to be read behind a cluster barrier.
+template <int NC>
 __device__ __forceinline__ void publish(ClusterBoard& board, int which, uint32_t rank, uint64_t mine) {
-  if (threadIdx.x < kCluster) {
+  if (threadIdx.x < NC) {
     const uint32_t to = map_to_rank(smem_u32(&board.counts[which][rank]), threadIdx.x);
     asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(to), "l"(mine) : "memory");
   }
 }
+template <int NC>
 __device__ __forceinline__ void raise_flag(ClusterBoard& board, int32_t bits) {
 #pragma unroll 1
-  for (uint32_t r = 0; r < kCluster; ++r) bit_set(map_to_rank(smem_u32(&board.flags), r), (uint32_t)bits);
+  for (uint32_t r = 0; r < NC; ++r) flag_set(map_to_rank(smem_u32(&board.flags), r), (uint32_t)bits);
 }
 
-// Calls `f(row, column, entry)` for the first `entries_of(row)` table entries of every row, 8
-// loads a lane at a time, spread over the cluster's warps.
-template <typename Rows, typename F>
+// Calls `f(row, tag, column, entry)` for the first n table entries of every row, (n, tag) =
+// `row_of(row)`: 16 loads a lane at a time, spread over the warps of the NC CTAs; a row's
+// length is asked for while the piece before is under way.  (Half the piece, with the next
+// one's loads on their way too: 64 rows of 257 entries 4.4 us instead of 2.9.)
+struct RowPart {
+  int n, tag;
+};
+template <int NC, typename Rows, typename F>
 __device__ __forceinline__ void for_entries(const int32_t* tables, int64_t row_stride, int batch, int width,
-                                            uint32_t rank, Rows&& entries_of, F&& f) {
-  const int lane = threadIdx.x & 31, warp = (int)rank * kWarps + (threadIdx.x >> 5);
+                                            uint32_t rank, Rows&& row_of, F&& f) {
+  constexpr int kWarpsAll = NC * kWarps;
+  const int lane = threadIdx.x & 31, warp = (int)(threadIdx.x >> 5) * NC + (int)rank;
   const int pieces = (width + kPiece - 1) / kPiece;
   const int64_t items = (int64_t)batch * pieces;
-  for (int64_t item = warp; item < items; item += kCluster * kWarps) {
-    const int b = (int)(item / pieces), j0 = (int)(item % pieces) * kPiece;
-    const int n = entries_of(b);
-    if (j0 >= n) continue;
+  if (warp >= items) return;
+  int b = warp / pieces, piece = warp % pieces;
+  RowPart row = row_of(b);
+  const int step_b = kWarpsAll / pieces, step_piece = kWarpsAll % pieces;
+  for (int64_t item = warp; item < items; item += kWarpsAll) {
+    int b2 = b + step_b, piece2 = piece + step_piece;
+    if (piece2 >= pieces) {
+      piece2 -= pieces;
+      ++b2;
+    }
+    const int j0 = piece * kPiece + lane;
+    const int32_t* from = tables + b * row_stride;
     int32_t x[kPiece / 32];
 #pragma unroll
     for (int k = 0; k < kPiece / 32; ++k)
-      if (j0 + 32 * k + lane < n) x[k] = tables[b * row_stride + j0 + 32 * k + lane];
+      if (j0 + 32 * k < row.n) x[k] = from[j0 + 32 * k];
+    const RowPart next = b2 < batch ? row_of(b2) : RowPart{0, 0};
 #pragma unroll
     for (int k = 0; k < kPiece / 32; ++k)
-      if (j0 + 32 * k + lane < n) f(b, j0 + 32 * k + lane, x[k]);
+      if (j0 + 32 * k < row.n) f(b, row.tag, j0 + 32 * k, x[k]);
+    b = b2;
+    piece = piece2;
+    row = next;
+  }
+}
+
+// Two bits per page, held twice: marks of a CTA's own over a range of the pool, set by ordinary
+// shared-memory atomics (one to another CTA's shared memory takes some 4 cycles a lane: 2048
+// rows of 270000 pages 181 us), and slices, a contiguous part of the pool per CTA, into which
+// the marks of all CTAs are joined.  A pool of more pages than the marks hold takes several
+// ranges, with the tables read once for each.
+struct PageBits {
+  uint32_t* slice[2];   // [per] words of this CTA's
+  uint32_t* mark[2];    // [range] words
+  int per, words, range;   // per and range are whole vectors of four
+};
+template <int NC>
+__device__ __forceinline__ PageBits page_bits(uint32_t* smem, int num_pages) {
+  PageBits p;
+  p.words = (num_pages + 31) / 32;
+  p.per = ((p.words + NC - 1) / NC + 3) & ~3;
+  p.slice[0] = smem;
+  p.slice[1] = smem + p.per;
+  p.mark[0] = smem + 2 * p.per;
+  p.range = min((kDynamicSmem / 4 - 2 * p.per) / 2 & ~3, (p.words + 3) & ~3);
+  p.mark[1] = p.mark[0] + p.range;
+  return p;
+}
+// Clears the marks; the CTA's threads are to meet before any is set.
+__device__ __forceinline__ void clear_marks(const PageBits& p) {
+  uint4* m = reinterpret_cast<uint4*>(p.mark[0]);
+  for (int i = threadIdx.x; i < p.range / 2; i += kThreads) m[i] = make_uint4(0u, 0u, 0u, 0u);
+}
+// Joins everybody's marks of the words from `first` on into the slices.  TWICE: bits of the
+// second kind that two CTAs have are reported.
+template <int NC, bool TWICE>
+__device__ __forceinline__ bool join_marks(const PageBits& p, int first, uint32_t rank) {
+  const int mine = (int)rank * p.per, w0 = max(mine, first), w1 = min(min(mine + p.per, first + p.range), p.words);
+  bool twice = false;
+  for (int i = threadIdx.x; i < (w1 - w0 + 3) / 4 * 2; i += kThreads) {
+    const int kind = i & 1, w = w0 + (i >> 1) * 4;
+    const uint32_t at = smem_u32(p.mark[kind] + (w - first));
+    uint4 x[NC];
+#pragma unroll
+    for (int r = 0; r < NC; ++r) x[r] = load_remote4(map_to_rank(at, (uint32_t)r));
+    uint4 any = make_uint4(0u, 0u, 0u, 0u);
+    uint32_t again = 0u;
+#pragma unroll
+    for (int r = 0; r < NC; ++r) {
+      if (TWICE) again |= (any.x & x[r].x) | (any.y & x[r].y) | (any.z & x[r].z) | (any.w & x[r].w);
+      any.x |= x[r].x;
+      any.y |= x[r].y;
+      any.z |= x[r].z;
+      any.w |= x[r].w;
+    }
+    if (TWICE && kind == 1 && again != 0u) twice = true;
+    *reinterpret_cast<uint4*>(p.slice[kind] + (w - mine)) = any;
+  }
+  return twice;
+}
+
+// Writes the ids of the pages in `bits` to list[before of the word ..): a word a warp, a bit a
+// lane.  bits and before [words] in shared memory, word w's bit 0 is page 32 (word0 + w).
+__device__ __forceinline__ void write_pages(int32_t* list, const uint32_t* bits, const uint32_t* before, int words,
+                                            int word0) {
+  const int lane = threadIdx.x & 31;
+  for (int w = threadIdx.x >> 5; w < words; w += kWarps) {
+    const uint32_t x = bits[w];
+    if (x >> lane & 1u) list[before[w] + __popc(x & ((1u << lane) - 1u))] = (word0 + w) * 32 + lane;
   }
 }
 
 // ---- release ------------------------------------------------------------------
 
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
-kv_free_kernel(const __grid_constant__ ReleaseArgs a, int shift) {
-  extern __shared__ uint32_t smem[];
+template <int NC>
+__global__ void __launch_bounds__(kThreads, 1) kv_free_kernel(const __grid_constant__ ReleaseArgs a) {
+  extern __shared__ __align__(16) uint32_t smem[];
   __shared__ ClusterBoard board;
+  __shared__ uint32_t released[kPageOpRows / 32];   // a bit per row, every CTA for itself
   const int tid = threadIdx.x;
-  const uint32_t rank = cluster_rank();
-  const int words = 1 << shift;
-  uint32_t* gone = smem;            // pages of released rows
-  uint32_t* kept = smem + words;    // of the others
-  uint32_t* released = smem + 2 * words;   // a bit per row, every CTA for itself
-  const int row_words = (a.batch + 31) / 32;
+  const uint32_t rank = NC > 1 ? cluster_rank() : 0u;
+  const PageBits bits = page_bits<NC>(smem, a.num_pages);
+  const int word0 = (int)rank * bits.per;   // the slice's first word
   const int head = __ldg(a.free_head);
-  for (int w = tid; w < 2 * words + row_words; w += kThreads) smem[w] = 0u;
+  for (int w = tid; w < (a.batch + 31) / 32; w += kThreads) released[w] = 0u;
+  for (int w = tid; w < 2 * bits.per; w += kThreads) smem[w] = 0u;
+  clear_marks(bits);
   if (tid == 0) board.flags = 0;
   __syncthreads();
   int flags = 0;
@@ -271,60 +352,78 @@ kv_free_kernel(const __grid_constant__ ReleaseArgs a, int shift) {
   if (flags != 0) atomicOr(&board.flags, flags);   // each CTA finds the same
   __syncthreads();
   const bool fits = board.flags == 0;
-  sync_all();   // everybody's bits are zero, and the check is over
-  const PageBits bits{shift};
-  if (fits) {
-    for_entries(a.tables, a.row_stride, a.batch, a.width, rank,
-                [&](int b) { return pages_of(__ldg(a.kv_lens + b), a.page_size); },
-                [&](int b, int, int page) {
-                  if (page < 0 || page >= a.num_pages) raise_flag(board, STATUS_PAGE_BOUNDS);
-                  else bit_set(bits.addr(released[b >> 5] >> (b & 31) & 1u ? gone : kept, page), 1u << (page & 31));
+  sync_all<NC>();   // the check is over: flags may come from other CTAs
+  for (int first = 0; fits && first < bits.words; first += bits.range) {
+    if (first > 0) {
+      clear_marks(bits);
+      __syncthreads();
+    }
+    for_entries<NC>(a.tables, a.row_stride, a.batch, a.width, rank,
+                [&](int b) {
+                  return RowPart{pages_of(__ldg(a.kv_lens + b), a.page_size),
+                                 (released[b >> 5] >> (b & 31) & 1u) ? bits.range : 0};   // which marks
+                },
+                [&](int, int tag, int, int page) {
+                  const int w = (page >> 5) - first;
+                  if (page < 0 || page >= a.num_pages) raise_flag<NC>(board, STATUS_PAGE_BOUNDS);
+                  else if (w >= 0 && w < bits.range) atomicOr(bits.mark[0] + tag + w, 1u << (page & 31));
                 });
+    sync_all<NC>();
+    join_marks<NC, false>(bits, first, rank);
+    sync_all<NC>();
   }
-  sync_all();
 
   // the freed pages, in ascending order
-  const int per_thread = (words + kThreads - 1) / kThreads, w0 = tid * per_thread;
+  const int words = bits.per, per_thread = (words + kThreads - 1) / kThreads, w0 = tid * per_thread;
+  uint32_t *kept = bits.slice[0], *gone = bits.slice[1];
   uint64_t mine = 0, all;
   for (int w = w0; w < min(w0 + per_thread, words); ++w) mine += __popc(gone[w] & ~kept[w]);
   const uint64_t before = block_scan<kWarps>(mine, board.warp_sums, all);
-  publish(board, 0, rank, all);
-  sync_all();
+  publish<NC>(board, 0, rank, all);
+  sync_all<NC>();
   int64_t freed = 0, at = 0;
-  for (uint32_t r = 0; r < kCluster; ++r) {
+  for (uint32_t r = 0; r < NC; ++r) {
     if (r < rank) at += (int64_t)board.counts[0][r];
     freed += (int64_t)board.counts[0][r];
   }
   flags = board.flags;
   if (flags == 0 && freed > head) flags = STATUS_CAPACITY;
   if (flags == 0) {
-    int64_t to = head - freed + at + (int64_t)before;
-    for (int w = w0; w < min(w0 + per_thread, words); ++w)
-      for (uint32_t m = gone[w] & ~kept[w]; m != 0u; m &= m - 1u)
-        a.free_pages[to++] = (((int)rank << shift) + w) * 32 + __ffs(m) - 1;
+    uint32_t n = (uint32_t)before;
+    for (int w = w0; w < min(w0 + per_thread, words); ++w) {
+      const uint32_t m = gone[w] & ~kept[w];
+      gone[w] = m;
+      kept[w] = n;
+      n += __popc(m);
+    }
+    __syncthreads();
+    write_pages(a.free_pages + (head - freed + at), gone, kept, words, word0);
   }
   if (rank == 0 && tid == 0) {
     *a.free_head_out = flags == 0 ? (int32_t)(head - freed) : head;
     if (flags != 0 && a.status != nullptr) atomicOr(a.status, flags);
   }
-  for (int b = (int)rank * kThreads + tid; b < a.batch; b += kCluster * kThreads)
+  for (int b = (int)rank * kThreads + tid; b < a.batch; b += NC * kThreads)
     a.seq_lens[b] = flags == 0 && (released[b >> 5] >> (b & 31) & 1u) ? 0 : __ldg(a.kv_lens + b);
 }
 
 // ---- compaction -----------------------------------------------------------------
 
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
-kv_compact_kernel(const __grid_constant__ CompactArgs a, int shift) {
-  extern __shared__ uint32_t smem[];
+constexpr uint32_t kAbove = 0x80000000u;
+
+template <int NC>
+__global__ void __launch_bounds__(kThreads, 1) kv_compact_kernel(const __grid_constant__ CompactArgs a) {
+  extern __shared__ __align__(16) uint32_t smem[];
   __shared__ ClusterBoard board;
   const int tid = threadIdx.x;
-  const uint32_t rank = cluster_rank();
-  const int words = 1 << shift;
-  uint32_t* used = smem;               // pages in the tables, then those of them that move
-  uint32_t* open = smem + words;       // pages in the free list
-  uint32_t* moved = smem + 2 * words;  // moving pages before each word
+  const uint32_t rank = NC > 1 ? cluster_rank() : 0u;
+  const PageBits bits = page_bits<NC>(smem, a.num_pages);
+  const int word0 = (int)rank * bits.per;   // the slice's first word
+  uint32_t* used = bits.slice[0];    // pages in the tables, then those of them that move
+  uint32_t* open = bits.slice[1];    // pages in the free list, then the moving pages before each word
   const int head = __ldg(a.free_head);
-  for (int w = tid; w < 2 * words; w += kThreads) smem[w] = 0u;
+  for (int w = tid; w < 2 * bits.per; w += kThreads) smem[w] = 0u;
+  clear_marks(bits);
   if (tid == 0) board.flags = 0;
   __syncthreads();
   int flags = 0;
@@ -336,35 +435,42 @@ kv_compact_kernel(const __grid_constant__ CompactArgs a, int shift) {
   if (flags != 0) atomicOr(&board.flags, flags);   // each CTA finds the same
   __syncthreads();
   const bool fits = board.flags == 0;
-  sync_all();   // everybody's bits are zero, and the check is over
-  const PageBits bits{shift};
-  auto entries_of = [&](int b) { return pages_of(__ldg(a.kv_lens + b), a.page_size); };
-  if (fits) {
-    for_entries(a.tables, a.row_stride, a.batch, a.width, rank, entries_of, [&](int, int, int page) {
-      if (page < 0 || page >= a.num_pages) raise_flag(board, STATUS_PAGE_BOUNDS);
-      else bit_set(bits.addr(used, page), 1u << (page & 31));
-    });
-    for (int64_t i = head + (int64_t)rank * kThreads + tid; i < a.num_free; i += kCluster * kThreads) {
-      const int page = a.free_pages[i];
-      if (page < 0 || page >= a.num_pages) raise_flag(board, STATUS_PAGE_BOUNDS);
-      else if (bit_test_set(bits.addr(open, page), 1u << (page & 31))) raise_flag(board, STATUS_FREE_LIST);
+  sync_all<NC>();   // the check is over: flags may come from other CTAs
+  auto entries_of = [&](int b) { return RowPart{pages_of(__ldg(a.kv_lens + b), a.page_size), 0}; };
+  for (int first = 0; fits && first < bits.words; first += bits.range) {
+    if (first > 0) {
+      clear_marks(bits);
+      __syncthreads();
     }
+    for_entries<NC>(a.tables, a.row_stride, a.batch, a.width, rank, entries_of, [&](int, int, int, int page) {
+      const int w = (page >> 5) - first;
+      if (page < 0 || page >= a.num_pages) raise_flag<NC>(board, STATUS_PAGE_BOUNDS);
+      else if (w >= 0 && w < bits.range) atomicOr(bits.mark[0] + w, 1u << (page & 31));
+    });
+    for (int64_t i = head + (int64_t)rank * kThreads + tid; i < a.num_free; i += NC * kThreads) {
+      const int page = a.free_pages[i], w = (page >> 5) - first;
+      if (page < 0 || page >= a.num_pages) raise_flag<NC>(board, STATUS_PAGE_BOUNDS);
+      else if (w >= 0 && w < bits.range && (atomicOr(bits.mark[1] + w, 1u << (page & 31)) >> (page & 31) & 1u))
+        raise_flag<NC>(board, STATUS_FREE_LIST);
+    }
+    sync_all<NC>();
+    if (join_marks<NC, true>(bits, first, rank)) raise_flag<NC>(board, STATUS_FREE_LIST);
+    sync_all<NC>();
   }
-  sync_all();
 
   // U and U + F before each word
-  const int per_thread = (words + kThreads - 1) / kThreads, w0 = tid * per_thread;
+  const int words = bits.per, per_thread = (words + kThreads - 1) / kThreads, w0 = tid * per_thread;
   const int w1 = min(w0 + per_thread, words);
   uint64_t mine = 0, all;
   for (int w = w0; w < w1; ++w) {
-    if (used[w] & open[w]) raise_flag(board, STATUS_FREE_LIST);   // in use and free
+    if (used[w] & open[w]) raise_flag<NC>(board, STATUS_FREE_LIST);   // in use and free
     mine += (uint64_t)__popc(used[w]) << 32 | (uint64_t)__popc(used[w] | open[w]);
   }
   uint64_t before = block_scan<kWarps>(mine, board.warp_sums, all);
-  publish(board, 0, rank, all);
-  sync_all();
+  publish<NC>(board, 0, rank, all);
+  sync_all<NC>();
   uint64_t base = 0, sum = 0;
-  for (uint32_t r = 0; r < kCluster; ++r) {
+  for (uint32_t r = 0; r < NC; ++r) {
     if (r < rank) base += board.counts[0][r];
     sum += board.counts[0][r];
   }
@@ -380,10 +486,10 @@ kv_compact_kernel(const __grid_constant__ CompactArgs a, int shift) {
     mine += (uint64_t)__popc(used[w] & ~low) << 32 | (uint64_t)__popc(open[w] & low);
   }
   before = block_scan<kWarps>(mine, board.warp_sums, all);
-  publish(board, 1, rank, all);
-  sync_all();
+  publish<NC>(board, 1, rank, all);
+  sync_all<NC>();
   base = sum = 0;
-  for (uint32_t r = 0; r < kCluster; ++r) {
+  for (uint32_t r = 0; r < NC; ++r) {
     if (r < rank) base += board.counts[1][r];
     sum += board.counts[1][r];
   }
@@ -391,19 +497,33 @@ kv_compact_kernel(const __grid_constant__ CompactArgs a, int shift) {
   flags = board.flags;
   if (flags == 0 && moves > a.max_moves) flags = STATUS_CAPACITY;
   if (flags == 0) {
-    int64_t m = (int64_t)((base + before) >> 32), h = (int64_t)((base + before) & 0xffffffffull);
+    // Below the word where the pages in use end every free page is a hole and none moves, above
+    // it all in use move and all pages are free afterwards: one list for holes and free pages.
+    uint32_t m = (uint32_t)((base + before) >> 32), h = (uint32_t)(base + before);
+    uint32_t *list = bits.mark[0], *at = bits.mark[1];
     z = z0;
     for (int w = w0; w < w1; ++w) {
       const uint32_t both = used[w] | open[w], low = lowest(both, in_use - z);
-      const int page0 = (((int)rank << shift) + w) * 32;
-      uint32_t x = both & ~low;   // free afterwards
-      for (int64_t to = head + z + __popc(low) - in_use; x != 0u; x &= x - 1u) a.free_pages_out[to++] = page0 + __ffs(x) - 1;
-      for (x = open[w] & low; x != 0u; x &= x - 1u) a.dst_pages[h++] = page0 + __ffs(x) - 1;
-      moved[w] = (uint32_t)m;
-      x = used[w] & ~low;
-      used[w] = x;
-      for (; x != 0u; x &= x - 1u) a.src_pages[m++] = page0 + __ffs(x) - 1;
+      const uint32_t hole = open[w] & low, move = used[w] & ~low;
+      const bool above = z >= in_use;
+      list[w] = above ? both : hole;
+      at[w] = above ? (uint32_t)(z - in_use) | kAbove : h;
+      if (!above)   // the rest of the one word that holds the end
+        for (uint32_t x = both & ~low, i = 0; x != 0u; x &= x - 1u, ++i)
+          a.free_pages_out[head + i] = (word0 + w) * 32 + __ffs(x) - 1;
+      open[w] = m;
+      used[w] = move;
+      h += __popc(hole);
+      m += __popc(move);
       z += __popc(both);
+    }
+    __syncthreads();
+    write_pages(a.src_pages, used, open, words, word0);
+    for (int w = tid >> 5, lane = tid & 31; w < words; w += kWarps) {
+      const uint32_t x = list[w], n = at[w];
+      if (x >> lane & 1u)
+        (n & kAbove ? a.free_pages_out + head : a.dst_pages)[(n & ~kAbove) + __popc(x & ((1u << lane) - 1u))] =
+            (word0 + w) * 32 + lane;
     }
   }
   const int me = (int)rank * kThreads + tid;
@@ -411,36 +531,47 @@ kv_compact_kernel(const __grid_constant__ CompactArgs a, int shift) {
     *a.num_moves = flags == 0 ? (int32_t)moves : 0;
     if (flags != 0 && a.status != nullptr) atomicOr(a.status, flags);
   }
-  for (int64_t i = (flags == 0 ? moves : 0) + me; i < a.max_moves; i += kCluster * kThreads)
+  for (int64_t i = (flags == 0 ? moves : 0) + me; i < a.max_moves; i += NC * kThreads)
     a.src_pages[i] = a.dst_pages[i] = -1;
   if (a.free_pages_out != a.free_pages)   // what lies before the list's head, or all of it
-    for (int64_t i = me; i < (flags == 0 ? head : a.num_free); i += kCluster * kThreads)
+    for (int64_t i = me; i < (flags == 0 ? head : a.num_free); i += NC * kThreads)
       a.free_pages_out[i] = a.free_pages[i];
-  sync_all();   // the moves are written, in global memory and in everybody's bits
+  sync_all<NC>();   // the moves are written, in global memory and in everybody's slices
 
+  // the tables, each CTA with its own copy of a range of the slices
   const bool in_place = a.tables_out == a.tables;
-  if (flags != 0 && in_place) return;
-  for_entries(a.tables, a.row_stride, a.batch, a.width, rank, [&](int) { return a.width; },
-              [&](int b, int j, int page) {
-                int to = page;
-                if (flags == 0 && j < entries_of(b)) {
-                  const uint32_t word = load_remote(bits.addr(used, page)), bit = 1u << (page & 31);
-                  if (word & bit) to = __ldcg(a.dst_pages + load_remote(bits.addr(moved, page)) + __popc(word & (bit - 1u)));
-                }
-                if (!in_place || to != page) a.tables_out[b * a.out_row_stride + j] = to;
-              });
-  sync_all();   // nobody's bits go while others read them
+  if (flags == 0 || !in_place) {
+    for (int first = 0; first < bits.words; first += bits.range) {
+      if (first > 0) __syncthreads();   // the range before is done with
+      for (int i = tid; flags == 0 && i < bits.range / 2; i += kThreads) {
+        const int kind = i & 1, w = first + (i >> 1) * 4;
+        if (w < bits.words) {
+          const int owner = w / words;
+          *reinterpret_cast<uint4*>(bits.mark[kind] + (w - first)) =
+              load_remote4(map_to_rank(smem_u32(bits.slice[kind] + (w - owner * words)), (uint32_t)owner));
+        }
+      }
+      __syncthreads();
+      for_entries<NC>(a.tables, a.row_stride, a.batch, a.width, rank, [&](int b) { return RowPart{a.width, flags == 0 ? entries_of(b).n : 0}; },
+                  [&](int b, int tag, int j, int page) {
+                    const bool live = j < tag;
+                    const int w = live ? (page >> 5) - first : 0;
+                    if (live ? w < 0 || w >= bits.range : first > 0) return;   // another range's
+                    int to = page;
+                    if (live) {
+                      const uint32_t word = bits.mark[0][w], bit = 1u << (page & 31);
+                      if (word & bit) to = __ldcg(a.dst_pages + bits.mark[1][w] + __popc(word & (bit - 1u)));
+                    }
+                    if (!in_place || to != page) a.tables_out[b * a.out_row_stride + j] = to;
+                  });
+    }
+  }
+  sync_all<NC>();   // nobody's slices go while others read them
 }
 
-// log2 of the words a CTA holds of `num_pages` bits.
-int word_shift(int32_t num_pages) {
-  const int64_t words = ceil_div(ceil_div(num_pages, 32), kCluster);
-  int shift = 0;
-  while ((int64_t(1) << shift) < words) ++shift;
-  return shift;
-}
-
-constexpr int kMaxWords = (int)(kPageOpPages / 32 / kCluster);
+static_assert(kPageOpPages / 32 / kMaxCluster * 8 <= kDynamicSmem / 2, "slices of the largest pool leave room for marks");
+// One CTA holds a pool's bits twice over up to here.
+constexpr int64_t kFewPages = (int64_t)kDynamicSmem / 16 * 32 - 4096;
 
 }  // namespace
 
@@ -458,27 +589,52 @@ int launch_kv_fork(const ForkArgs& a, cudaStream_t stream) {
   return PKA_OK;
 }
 
-int launch_kv_free(const ReleaseArgs& a, cudaStream_t stream) {
-  const int shift = word_shift(a.num_pages);
-  static std::atomic<uint64_t> smem_set{0};
-  cudaError_t e = set_smem_once(kv_free_kernel, kMaxWords * 8 + kPageOpRows / 8, smem_set);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(kv_free)");
-  const size_t smem = ((size_t)2 << shift) * 4 + (size_t)((a.batch + 31) / 32) * 4;
-  kv_free_kernel<<<kCluster, kThreads, smem, stream>>>(a, shift);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return cuda_fail(e, "kv_free_kernel launch");
+// Launches NC CTAs, as a cluster where they are several (16 are more than is portable: asked
+// for once per kernel and device).
+template <int NC, typename Kernel, typename Args>
+static int launch_cluster(Kernel kern, const Args& a, std::atomic<uint64_t>& done, const char* what,
+                          cudaStream_t stream) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  const uint64_t bit = dev < 64 ? (uint64_t(1) << dev) : 0;
+  if (e == cudaSuccess && !(bit != 0 && (done.load(std::memory_order_acquire) & bit))) {
+    if (NC > 8) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kDynamicSmem);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_acq_rel);
+  }
+  if (e != cudaSuccess) return cuda_fail(e, what);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(NC);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kDynamicSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = NC;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = NC > 1 ? 1 : 0;
+  e = cudaLaunchKernelEx(&cfg, kern, a);
+  if (e != cudaSuccess) return cuda_fail(e, what);
   return PKA_OK;
 }
 
+static bool few(int32_t batch, int32_t width, int32_t num_pages) {
+  return (int64_t)batch * width <= kFewEntries && num_pages <= kFewPages;
+}
+
+int launch_kv_free(const ReleaseArgs& a, cudaStream_t stream) {
+  static std::atomic<uint64_t> done[2];
+  if (few(a.batch, a.width, a.num_pages))
+    return launch_cluster<1>(kv_free_kernel<1>, a, done[0], "kv_free_kernel launch", stream);
+  return launch_cluster<kMaxCluster>(kv_free_kernel<kMaxCluster>, a, done[1], "kv_free_kernel launch", stream);
+}
+
 int launch_kv_compact(const CompactArgs& a, cudaStream_t stream) {
-  const int shift = word_shift(a.num_pages);
-  static std::atomic<uint64_t> smem_set{0};
-  cudaError_t e = set_smem_once(kv_compact_kernel, kMaxWords * 12, smem_set);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(kv_compact)");
-  kv_compact_kernel<<<kCluster, kThreads, ((size_t)3 << shift) * 4, stream>>>(a, shift);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return cuda_fail(e, "kv_compact_kernel launch");
-  return PKA_OK;
+  static std::atomic<uint64_t> done[2];
+  if (few(a.batch, a.width, a.num_pages))
+    return launch_cluster<1>(kv_compact_kernel<1>, a, done[0], "kv_compact_kernel launch", stream);
+  return launch_cluster<kMaxCluster>(kv_compact_kernel<kMaxCluster>, a, done[1], "kv_compact_kernel launch", stream);
 }
 
 }  // namespace pka

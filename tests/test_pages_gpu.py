@@ -337,3 +337,37 @@ def test_streams():
     side.synchronize()
     want = ref.compact(kv, free, head, tables, 16)
     assert got.block_tables.tolist() == want[0] and got.free_pages.tolist() == want[1]
+
+
+@pytest.mark.parametrize("pages", [1, 31, 32, 33, 700000, 1100000, 3000001])
+def test_pools_of_several_ranges(pages):
+    """Pools of one page, of a word and a bit more, and of more pages than a CTA marks at once,
+    whose ids lie all over them."""
+    r = random.Random(pages)
+    batch, width, ps = 30, 80, 2
+    ids = r.sample(range(pages), min(pages, 2400))
+    kv, tables, at = [], [], 0
+    for b in range(batch):
+        n = min(r.randint(0, width), len(ids) - at)
+        kv.append(n * ps)
+        tables.append(ids[at:at + n] + [-2 ** 31] * (width - n))
+        at += n
+    spare = ids[at:]
+    free = [-1] * at + spare
+    rows = [b for b in range(batch) if b % 3 == 0]
+    f, st = dev(free), status()
+    got = api.paged_kv_free(dev(rows), dev(kv), f, dev([at]), dev(tables), page_size=ps, num_pages=pages, status=st)
+    want = ref.release(rows, kv, free, at, tables, ps)
+    assert f.tolist() == want[0] and got.seq_lens.tolist() == want[1] and got.free_head.tolist() == [want[2]]
+    got = api.paged_kv_compact(dev(kv), dev(free), dev([at]), dev(tables), page_size=ps, num_pages=pages, status=st)
+    api.check_status(st)
+    new, lst, src, dst = ref.compact(kv, free, at, tables, ps)
+    assert got.block_tables.tolist() == new and got.free_pages.tolist() == lst
+    assert got.src_pages.tolist()[:len(src)] == src and got.dst_pages.tolist()[:len(dst)] == dst
+    if pages > 2400:   # the same free page twice, seen by different CTAs or by one
+        for i, j in ((at, at + 1), (at, len(free) - 1)):
+            twice = list(free)
+            twice[i] = twice[j]
+            got = api.paged_kv_compact(dev(kv), dev(twice), dev([at]), dev(tables), page_size=ps, num_pages=pages,
+                                       status=st)
+            assert code_of(st) == L.PKA_ERR_DEVICE_BOUNDS and got.block_tables.tolist() == tables
