@@ -459,20 +459,22 @@ typedef struct pka_prefix_plan pka_prefix_plan; /* opaque */
  *
  * desc, seq_lens_kv_host, qo_indptr_host, workspace_bytes_out, stream  as for
  *              paged_decode_plan.  window_left must be -1 (PKA_ERR_UNSUPPORTED).
- *              mma_min_rows is not used: the decode is the tensor-core one.
  * group_indptr_host  [num_groups + 1]: group g is requests group_indptr[g] ..
  *              group_indptr[g + 1] - 1; from 0 to batch_size, not decreasing.
  * prefix_pages_host  [num_groups]: leading pages that the rows of the group's
  *              requests have in common, 0 for none; prefix_pages * page_size
  *              keys that every query row of the group sees: at most kv_len with
  *              a dense mask, kv_len - q_len + 1 with a causal one.
- * The workspace holds the fp32 partial states of the prefixes' pieces too.
+ * min_shared_bytes  where sharing keeps fewer bytes of K and V than this from being
+ *              read again, the run is that of paged_decode_plan (split_waves,
+ *              min_chunk_tokens and mma_min_rows are used then only); else the
+ *              workspace holds the fp32 partial states of all pieces.  Negative: 48 MB.
  */
 int paged_prefix_decode_plan(pka_prefix_plan** plan_out, const pka_decode_desc* desc,
                              const int32_t* seq_lens_kv_host, const int32_t* qo_indptr_host,
                              const int32_t* group_indptr_host, int32_t num_groups,
-                             const int32_t* prefix_pages_host, size_t* workspace_bytes_out,
-                             void* stream);
+                             const int32_t* prefix_pages_host, int64_t min_shared_bytes,
+                             size_t* workspace_bytes_out, void* stream);
 
 /* Re-plan in place for a new batch, as paged_decode_plan_update does: capture
  * a run again after it, and do not replay the old graph. */
@@ -486,11 +488,33 @@ int paged_prefix_decode_plan_update(pka_prefix_plan* plan, int32_t batch_size,
 /* Free a plan (NULL is ignored); no run that uses it may still execute. */
 void paged_prefix_decode_plan_destroy(pka_prefix_plan* plan);
 
-/* The decode part's summary, the number of pieces of prefixes (pairs of CTAs) and,
- * [batch_size], the pieces that each request's prefix is cut into along its keys, 0
- * where it has none.  Either of the latter may be NULL. */
-int paged_prefix_decode_plan_info(const pka_prefix_plan* plan, pka_plan_info* info,
-                                  int32_t* num_pieces_out, int32_t* prefix_chunks_out);
+/* Summary of a prefix plan. */
+typedef struct pka_prefix_plan_info {
+  int32_t shared;             /* 0: too little to share, the run is a paged_decode_run   */
+  int32_t num_prefix_pieces;  /* runs of 64-key tiles of a prefix, for one KV head and up
+                                 to 256 query rows                                       */
+  int32_t num_own_pieces;     /* runs of 16-key units of a request, for one KV head and up
+                                 to 16 query rows                                        */
+  int32_t num_pairs;          /* pairs of CTAs that take the former                      */
+  int32_t num_warps;          /* warps that take the latter                              */
+  int32_t dense;              /* the prefixes' products take longer than all reads      */
+  int32_t partial_rows;       /* fp32 partial rows in the workspace                      */
+  int32_t total_q;
+  int32_t num_sms;
+  int64_t workspace_bytes;
+} pka_prefix_plan_info;
+
+int paged_prefix_decode_plan_info(const pka_prefix_plan* plan, pka_prefix_plan_info* info);
+
+/*
+ * Copy the plan's host arrays out (for tests of the planner): prefix_pieces
+ * [num_prefix_pieces * 6] int32 (table row, KV head, first query row of the group, first
+ * 64-key tile, end tile, first partial row), own_pieces [num_own_pieces * 6] (request, KV
+ * head, first query row of the request, first 16-key unit, end unit, first partial row).
+ * Either may be NULL.
+ */
+int paged_prefix_decode_plan_export(const pka_prefix_plan* plan, int32_t* prefix_pieces,
+                                    int32_t* own_pieces);
 
 /* As paged_decode_plan_check. */
 int paged_prefix_decode_plan_check(const pka_prefix_plan* plan, void* stream);

@@ -35,7 +35,8 @@ EXPORTED = (
     "paged_decode_run_noalloc",
     "paged_prefix_decode_plan", "paged_prefix_decode_plan_update",
     "paged_prefix_decode_plan_destroy", "paged_prefix_decode_plan_info",
-    "paged_prefix_decode_plan_check", "paged_prefix_decode_run",
+    "paged_prefix_decode_plan_export", "paged_prefix_decode_plan_check",
+    "paged_prefix_decode_run",
     "attn_merge_lse",
     "batch_prefill_plan", "batch_prefill_plan_fixed", "batch_prefill_plan_destroy", "batch_prefill_plan_check",
     "batch_prefill_run",
@@ -72,6 +73,16 @@ class PlanInfo(ctypes.Structure):
         ("rows_per_cta", ctypes.c_int32), ("num_sms", ctypes.c_int32),
         ("split_waves", ctypes.c_int32), ("min_chunk_tokens", ctypes.c_int32),
         ("total_q", ctypes.c_int32),
+    ]
+
+
+class PrefixPlanInfo(ctypes.Structure):
+    _fields_ = [
+        ("shared", ctypes.c_int32), ("num_prefix_pieces", ctypes.c_int32),
+        ("num_own_pieces", ctypes.c_int32), ("num_pairs", ctypes.c_int32),
+        ("num_warps", ctypes.c_int32), ("dense", ctypes.c_int32),
+        ("partial_rows", ctypes.c_int32), ("total_q", ctypes.c_int32),
+        ("num_sms", ctypes.c_int32), ("workspace_bytes", ctypes.c_int64),
     ]
 
 
@@ -154,12 +165,13 @@ _SIGS = {
     "paged_decode_run_noalloc": (ctypes.c_int, [_vp, _vp, _i64, _i64, _vp, _vp, _i64, _i64, _vp,
                                                 _i64, _vp, _vp, _vp, _vp, _vp]),
     "paged_prefix_decode_plan": (ctypes.c_int, [ctypes.POINTER(_vp), ctypes.POINTER(DecodeDesc),
-                                                _pi32, _pi32, _pi32, _i32, _pi32,
+                                                _pi32, _pi32, _pi32, _i32, _pi32, _i64,
                                                 ctypes.POINTER(_sz), _vp]),
     "paged_prefix_decode_plan_update": (ctypes.c_int, [_vp, _i32, _pi32, _pi32, _pi32, _i32, _pi32,
                                                        ctypes.POINTER(_sz), _vp]),
     "paged_prefix_decode_plan_destroy": (None, [_vp]),
-    "paged_prefix_decode_plan_info": (ctypes.c_int, [_vp, ctypes.POINTER(PlanInfo), _pi32, _pi32]),
+    "paged_prefix_decode_plan_info": (ctypes.c_int, [_vp, ctypes.POINTER(PrefixPlanInfo)]),
+    "paged_prefix_decode_plan_export": (ctypes.c_int, [_vp, _pi32, _pi32]),
     "paged_prefix_decode_plan_check": (ctypes.c_int, [_vp, _vp]),
     "paged_prefix_decode_run": (ctypes.c_int, [_vp, _vp, _i64, _i64, _vp, _vp, _i64, _i64, _vp,
                                                _i64, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),

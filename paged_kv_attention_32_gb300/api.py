@@ -364,15 +364,22 @@ class PrefixDecodePlan:
 
     @property
     def info(self):
-        """The decode part's summary, ``num_pieces`` of prefixes (pairs of CTAs) and
-        ``prefix_chunks``, the pieces that each request's prefix is cut into (0: none)."""
-        inf, pieces = L.PlanInfo(), ctypes.c_int32()
-        chunks = torch.zeros(self.desc.batch_size, dtype=torch.int32)
-        L.check(L.lib().paged_prefix_decode_plan_info(
-            self.prefix_handle, ctypes.byref(inf), ctypes.byref(pieces),
-            ctypes.cast(chunks.data_ptr(), L._pi32)), "plan_info")
-        return dict({f: getattr(inf, f) for f, _ in L.PlanInfo._fields_}, num_pieces=pieces.value,
-                    prefix_chunks=chunks.tolist())
+        inf = L.PrefixPlanInfo()
+        L.check(L.lib().paged_prefix_decode_plan_info(self.prefix_handle, ctypes.byref(inf)),
+                "plan_info")
+        return {f: getattr(inf, f) for f, _ in L.PrefixPlanInfo._fields_}
+
+    def export(self):
+        """Host copies of the plan's pieces: of prefixes (table row, KV head, first query row of
+        the group, first 64-key tile, end tile, first partial row) and of the requests' own keys
+        (request, KV head, first query row, first 16-key unit, end unit, first partial row)."""
+        inf = self.info
+        sizes = inf["num_prefix_pieces"], inf["num_own_pieces"]
+        pieces = [torch.zeros((max(1, n), 6), dtype=torch.int32) for n in sizes]
+        L.check(L.lib().paged_prefix_decode_plan_export(
+            self.prefix_handle, *(ctypes.cast(p.data_ptr(), L._pi32) for p in pieces)),
+            "plan_export")
+        return [[tuple(r) for r in p[:n].tolist()] for p, n in zip(pieces, sizes)]
 
     def update(self, seq_lens_kv, group_indptr, prefix_pages, qo_indptr=None, stream=None):
         """Re-plan in place for a new batch (``paged_prefix_decode_plan_update``); graphs that
@@ -415,11 +422,13 @@ def paged_prefix_decode_plan(seq_lens_kv, group_indptr, prefix_pages, *, num_qo_
                              num_kv_heads, page_size, max_pages_per_seq, num_pages,
                              qo_indptr=None, q_len=1, max_q_len=0, causal=False, scale=None,
                              bmm2_scale=1.0, return_lse=False, freeze_seq_lens=True, num_sms=0,
-                             split_waves=0, min_chunk_tokens=0, host_only=False, head_dim=128,
-                             dtype=torch.bfloat16, out_dtype=None, stream=None):
+                             split_waves=0, min_chunk_tokens=0, mma_min_rows=0, min_shared_bytes=-1,
+                             host_only=False, head_dim=128, dtype=torch.bfloat16, out_dtype=None,
+                             stream=None):
     """Plan a paged decode of requests that, in groups, begin with the same pages (see pka.h):
     requests ``group_indptr[g]`` to ``group_indptr[g + 1] - 1`` share their first
-    ``prefix_pages[g]`` pages, which are read once for all of them.  All host arrays; the other
+    ``prefix_pages[g]`` pages, which are read once for all of them where that keeps at least
+    ``min_shared_bytes`` (negative: 48 MB) from being read again.  All host arrays; the other
     arguments as for ``paged_decode_plan``."""
     in_code, out_code = _dtype_codes(dtype, out_dtype)
     lens, groups = _prefix_groups(seq_lens_kv, group_indptr, prefix_pages, qo_indptr)
@@ -431,12 +440,12 @@ def paged_prefix_decode_plan(seq_lens_kv, group_indptr, prefix_pages, *, num_qo_
         scale=float("nan") if scale is None else scale, bmm2_scale=bmm2_scale,
         return_lse=int(bool(return_lse)), freeze_seq_lens=int(bool(freeze_seq_lens)),
         num_sms=num_sms, split_waves=split_waves, min_chunk_tokens=min_chunk_tokens,
-        flags=L.PKA_PLAN_HOST_ONLY if host_only else 0)
+        mma_min_rows=mma_min_rows, flags=L.PKA_PLAN_HOST_ONLY if host_only else 0)
     h = ctypes.c_void_p()
     ws = ctypes.c_size_t()
     rc = L.lib().paged_prefix_decode_plan(
         ctypes.byref(h), ctypes.byref(d), lens[0][1], lens[1][1], groups[0][1],
-        groups[1][0].numel(), groups[1][1], ctypes.byref(ws),
+        groups[1][0].numel(), groups[1][1], min_shared_bytes, ctypes.byref(ws),
         None if host_only else _stream(stream))
     L.check(rc, "paged_prefix_decode_plan")
     return PrefixDecodePlan(h, d, ws.value)

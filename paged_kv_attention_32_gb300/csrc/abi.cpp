@@ -82,11 +82,7 @@ int pka::upload_decode_plan(pka_plan& p, cudaStream_t stream) {
   const size_t off_reqs = up256(n_items);
   const size_t off_status = off_reqs + up256(n_reqs);
   const size_t off_cnt = off_status + 256;   // merge counters, zero between runs
-  const size_t n_pre = p.prefix_items.size() * sizeof(PrefixItem);
-  const size_t n_tok = p.prefix_tokens.size() * sizeof(PrefixToken);
-  const size_t off_pre = off_cnt + up256(n_cnt);
-  const size_t off_tok = off_pre + up256(n_pre);
-  const size_t total = off_tok + up256(n_tok);
+  const size_t total = off_cnt + up256(n_cnt);
   if (p.dev_buf == nullptr || total > p.dev_capacity) {
     // a replan that outgrows the buffer reallocates it with headroom
     if (p.dev_buf != nullptr) {
@@ -104,8 +100,6 @@ int pka::upload_decode_plan(pka_plan& p, cudaStream_t stream) {
   p.d_reqs = reinterpret_cast<const ReqInfo*>(base + off_reqs);
   p.d_status = reinterpret_cast<int32_t*>(base + off_status);
   p.d_merge_cnt = reinterpret_cast<int32_t*>(base + off_cnt);
-  p.d_prefix_items = reinterpret_cast<const PrefixItem*>(base + off_pre);
-  p.d_prefix_tokens = reinterpret_cast<const PrefixToken*>(base + off_tok);
   // One asynchronous copy from a pinned image of the buffer.  The image is
   // rewritten only after the copy that last read it has completed (stage_done);
   // stream order keeps the upload behind runs already queued on the same stream.
@@ -128,9 +122,7 @@ int pka::upload_decode_plan(pka_plan& p, cudaStream_t stream) {
     uint8_t* img = static_cast<uint8_t*>(p.host_stage);
     if (n_items) std::memcpy(img, p.items.data(), n_items);
     std::memcpy(img + off_reqs, p.reqs.data(), n_reqs);
-    std::memset(img + off_status, 0, off_pre - off_status);   // status word and counters
-    if (n_pre) std::memcpy(img + off_pre, p.prefix_items.data(), n_pre);
-    if (n_tok) std::memcpy(img + off_tok, p.prefix_tokens.data(), n_tok);
+    std::memset(img + off_status, 0, total - off_status);   // status word and counters
     PKA_CUDA_TRY(cudaMemcpyAsync(base, img, total, cudaMemcpyHostToDevice, stream),
                  "cudaMemcpyAsync(plan)");
     if (p.stage_done == nullptr)
@@ -147,15 +139,21 @@ int pka::upload_decode_plan(pka_plan& p, cudaStream_t stream) {
   PKA_CUDA_TRY(cudaMemcpyAsync(base + off_reqs, p.reqs.data(), n_reqs, cudaMemcpyHostToDevice,
                                stream),
                "cudaMemcpyAsync(plan requests)");
-  if (n_pre)
-    PKA_CUDA_TRY(cudaMemcpyAsync(base + off_pre, p.prefix_items.data(), n_pre, cudaMemcpyHostToDevice, stream),
-                 "cudaMemcpyAsync(prefix items)");
-  if (n_tok)
-    PKA_CUDA_TRY(cudaMemcpyAsync(base + off_tok, p.prefix_tokens.data(), n_tok, cudaMemcpyHostToDevice, stream),
-                 "cudaMemcpyAsync(prefix tokens)");
-  PKA_CUDA_TRY(cudaMemsetAsync(base + off_status, 0, off_pre - off_status, stream),
+  PKA_CUDA_TRY(cudaMemsetAsync(base + off_status, 0, total - off_status, stream),
                "cudaMemsetAsync(status and counters)");
   return PKA_OK;
+}
+
+void pka::keep_decode_buffers(pka_plan& plan, pka_plan& from) {
+  plan.dev_buf = from.dev_buf;
+  plan.dev_capacity = from.dev_capacity;
+  plan.device = from.device;
+  plan.host_stage = from.host_stage;
+  plan.host_capacity = from.host_capacity;
+  plan.stage_done = from.stage_done;
+  from.dev_buf = nullptr;
+  from.host_stage = nullptr;
+  from.stage_done = nullptr;
 }
 
 int pka::replace_decode_plan(pka_plan& p, pka_plan&& fresh, cudaStream_t stream) {
@@ -164,15 +162,7 @@ int pka::replace_decode_plan(pka_plan& p, pka_plan&& fresh, cudaStream_t stream)
     const int rc = check_device(p.device);
     if (rc != PKA_OK) return rc;
   }
-  fresh.dev_buf = p.dev_buf;
-  fresh.dev_capacity = p.dev_capacity;
-  fresh.device = p.device;
-  fresh.host_stage = p.host_stage;
-  fresh.host_capacity = p.host_capacity;
-  fresh.stage_done = p.stage_done;
-  p.dev_buf = nullptr;
-  p.host_stage = nullptr;
-  p.stage_done = nullptr;
+  keep_decode_buffers(fresh, p);
   p = std::move(fresh);
   return host_only ? PKA_OK : upload_decode_plan(p, stream);
 }
@@ -367,9 +357,7 @@ int pka::prepare_decode_run(const pka_plan* p, const void* q, int64_t q_stride_t
                             int64_t kv_stride_page, int64_t kv_stride_head,
                             const int32_t* block_tables, int64_t bt_row_stride,
                             const int32_t* seq_lens_kv_dev, const float* sinks, void* out, float* lse,
-                            void* workspace, size_t workspace_bytes, DecodeArgs* args,
-                            CUtensorMap* kmap, CUtensorMap* vmap) {
-  PKA_CHECK_ARG(p->dev_buf != nullptr, "plan was built with PKA_PLAN_HOST_ONLY and cannot run");
+                            DecodeArgs* args, CUtensorMap* kmap, CUtensorMap* vmap) {
   PKA_CHECK_ARG(q && k_pages && v_pages && block_tables && out,
                 "q, k_pages, v_pages, block_tables and out must not be NULL");
   PKA_CHECK_ARG(p->desc.freeze_seq_lens || seq_lens_kv_dev != nullptr,
@@ -384,16 +372,7 @@ int pka::prepare_decode_run(const pka_plan* p, const void* q, int64_t q_stride_t
                 "K/V strides must be multiples of 8 elements");
   PKA_CHECK_ARG(bt_row_stride >= p->C, "bt_row_stride (%lld) is smaller than the table width %d",
                 (long long)bt_row_stride, p->C);
-  if (p->workspace_bytes > 0) {
-    if (workspace == nullptr || workspace_bytes < (size_t)p->workspace_bytes)
-      return fail(PKA_ERR_WORKSPACE_TOO_SMALL, "workspace of %zu bytes, the plan needs %lld",
-                  workspace_bytes, (long long)p->workspace_bytes);
-    PKA_CHECK_ARG(aligned(workspace, 256), "workspace must be 256-byte aligned");
-  }
-  int rc = check_device(p->device);
-  if (rc != PKA_OK) return rc;
-
-  rc = encode_kv_pool_map(kmap, k_pages, p->desc.num_pages, p->Hkv, p->ps, p->D, kv_stride_page,
+  int rc = encode_kv_pool_map(kmap, k_pages, p->desc.num_pages, p->Hkv, p->ps, p->D, kv_stride_page,
                           kv_stride_head);
   if (rc != PKA_OK) return rc;
   rc = encode_kv_pool_map(vmap, v_pages, p->desc.num_pages, p->Hkv, p->ps, p->D, kv_stride_page,
@@ -410,16 +389,6 @@ int pka::prepare_decode_run(const pka_plan* p, const void* q, int64_t q_stride_t
   a.sinks = sinks;
   a.out = out;
   a.lse = p->desc.return_lse ? lse : nullptr;
-  a.ws_o = static_cast<float*>(workspace);
-  a.ws_lse = workspace ? reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) +
-                                                  p->ws_lse_offset)
-                       : nullptr;
-  a.items = p->d_items;
-  a.reqs = p->d_reqs;
-  a.merge_cnt = p->d_merge_cnt;
-  a.status = p->d_status;
-  a.num_items = (int32_t)p->items.size();
-  a.tiles_per_item = p->kernel == PKA_KERNEL_MMA ? (p->rows_per_cta + 15) / 16 : 1;
   a.num_qo_heads = p->Hq;
   a.num_kv_heads = p->Hkv;
   a.group = p->G;
@@ -434,6 +403,40 @@ int pka::prepare_decode_run(const pka_plan* p, const void* q, int64_t q_stride_t
   return PKA_OK;
 }
 
+int pka::run_decode_plan(const pka_plan& plan, const void* q, int64_t q_stride_tok,
+                         int64_t q_stride_head, const void* k_pages, const void* v_pages,
+                         int64_t kv_stride_page, int64_t kv_stride_head,
+                         const int32_t* block_tables, int64_t bt_row_stride,
+                         const int32_t* seq_lens_kv_dev, const float* sinks, void* out, float* lse,
+                         void* workspace, size_t workspace_bytes, void* stream) {
+  const pka_plan* p = &plan;
+  PKA_CHECK_ARG(p->dev_buf != nullptr, "plan was built with PKA_PLAN_HOST_ONLY and cannot run");
+  DecodeArgs a{};
+  CUtensorMap kmap, vmap;
+  int rc = prepare_decode_run(p, q, q_stride_tok, q_stride_head, k_pages, v_pages, kv_stride_page, kv_stride_head,
+                              block_tables, bt_row_stride, seq_lens_kv_dev, sinks, out, lse, &a, &kmap, &vmap);
+  if (rc != PKA_OK) return rc;
+  if (p->workspace_bytes > 0) {
+    if (workspace == nullptr || workspace_bytes < (size_t)p->workspace_bytes)
+      return fail(PKA_ERR_WORKSPACE_TOO_SMALL, "workspace of %zu bytes, the plan needs %lld",
+                  workspace_bytes, (long long)p->workspace_bytes);
+    PKA_CHECK_ARG(aligned(workspace, 256), "workspace must be 256-byte aligned");
+  }
+  rc = check_device(p->device);
+  if (rc != PKA_OK) return rc;
+  a.ws_o = static_cast<float*>(workspace);
+  a.ws_lse = workspace ? reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) +
+                                                  p->ws_lse_offset)
+                       : nullptr;
+  a.items = p->d_items;
+  a.reqs = p->d_reqs;
+  a.merge_cnt = p->d_merge_cnt;
+  a.status = p->d_status;
+  a.num_items = (int32_t)p->items.size();
+  a.tiles_per_item = p->kernel == PKA_KERNEL_MMA ? (p->rows_per_cta + 15) / 16 : 1;
+  return launch_decode(*p, a, kmap, vmap, static_cast<cudaStream_t>(stream));
+}
+
 extern "C" {
 
 int paged_decode_run(const pka_plan* p, const void* q, int64_t q_stride_tok,
@@ -445,13 +448,9 @@ int paged_decode_run(const pka_plan* p, const void* q, int64_t q_stride_tok,
   NvtxRange nvtx_range("pka::paged_decode_run");
   clear_error();
   PKA_CHECK_ARG(p != nullptr, "plan must not be NULL");
-  DecodeArgs a{};
-  CUtensorMap kmap, vmap;
-  const int rc = prepare_decode_run(p, q, q_stride_tok, q_stride_head, k_pages, v_pages, kv_stride_page,
-                                    kv_stride_head, block_tables, bt_row_stride, seq_lens_kv_dev, sinks, out,
-                                    lse, workspace, workspace_bytes, &a, &kmap, &vmap);
-  if (rc != PKA_OK) return rc;
-  return launch_decode(*p, a, kmap, vmap, static_cast<cudaStream_t>(stream));
+  return run_decode_plan(*p, q, q_stride_tok, q_stride_head, k_pages, v_pages, kv_stride_page, kv_stride_head,
+                         block_tables, bt_row_stride, seq_lens_kv_dev, sinks, out, lse, workspace, workspace_bytes,
+                         stream);
 }
 
 namespace {

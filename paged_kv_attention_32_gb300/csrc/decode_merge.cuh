@@ -6,8 +6,6 @@
 // cudnn_batch_decode_with_kv_cache describes: weights 2^(lse_i - m) with m
 // the largest LSE, the sink added once to the denominator.)  This saves a
 // second kernel launch that would have to wait for the whole decode grid.
-// Behind a shared prefix a row's first states are that prefix's pieces, written by
-// the kernel before; the request's own chunk CTAs alone are counted.
 #pragma once
 
 #include "device_common.cuh"
@@ -96,14 +94,12 @@ __device__ __forceinline__ void split_merge_if_last(const DecodeArgs& a, const R
     int32_t* cnt = a.merge_cnt + rq.cnt_base + hk * a.tiles_per_item + tile;
     int32_t old;
     asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(old) : "l"(cnt) : "memory");
-    const bool last = old == rq.n_items - 1;
+    const bool last = old == rq.n_chunks - 1;
     if (last) *cnt = 0;   // every chunk has counted: ready for the next run
     s_last = last;
   }
   __syncthreads();
   if (!s_last) return;
-  // the pieces of a shared prefix come from the kernel before, which may still run
-  if (a.behind_prefix) asm volatile("griddepcontrol.wait;" ::: "memory");
   // a group of at most 8 rows with a long chunk list: 16 threads per row and
   // 8 chunks per round (fewer rounds of memory latency); else 8 threads per
   // row and 4 chunks per round

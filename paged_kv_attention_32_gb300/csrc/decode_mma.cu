@@ -193,21 +193,6 @@ int launch_mma(const DecodeArgs& args, const CUtensorMap& kmap, const CUtensorMa
   const int mt = (args.rows_per_cta + 15) / 16;
   const int64_t grid = (int64_t)args.num_items * mt;
   if (grid > 0x7fffffff) return fail(PKA_ERR_INVALID_ARG, "decode grid too large");
-  if (args.behind_prefix) {   // starts while the prefix kernel ends; only its merges wait for it
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(kWarps * 32);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, kern, args, kmap, vmap);
-    if (e != cudaSuccess) return cuda_fail(e, "decode_mma_kernel launch");
-    return PKA_OK;
-  }
   kern<<<(unsigned)grid, kWarps * 32, smem, stream>>>(args, kmap, vmap);
   e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "decode_mma_kernel launch");

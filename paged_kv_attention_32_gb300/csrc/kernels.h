@@ -10,13 +10,21 @@
 
 namespace pka {
 
-// The checks of a decode run and what it launches with: arguments and both pools' maps.
+// The checks of a decode run's tensors and what it launches with: arguments, but for the plan's
+// arrays and the workspace, and both pools' maps.
 int prepare_decode_run(const pka_plan* plan, const void* q, int64_t q_stride_tok,
                        int64_t q_stride_head, const void* k_pages, const void* v_pages,
                        int64_t kv_stride_page, int64_t kv_stride_head, const int32_t* block_tables,
                        int64_t bt_row_stride, const int32_t* seq_lens_kv_dev, const float* sinks,
-                       void* out, float* lse, void* workspace, size_t workspace_bytes,
-                       DecodeArgs* args, CUtensorMap* kmap, CUtensorMap* vmap);
+                       void* out, float* lse, DecodeArgs* args, CUtensorMap* kmap,
+                       CUtensorMap* vmap);
+
+// paged_decode_run of a plan that is on the device.
+int run_decode_plan(const pka_plan& plan, const void* q, int64_t q_stride_tok,
+                    int64_t q_stride_head, const void* k_pages, const void* v_pages,
+                    int64_t kv_stride_page, int64_t kv_stride_head, const int32_t* block_tables,
+                    int64_t bt_row_stride, const int32_t* seq_lens_kv_dev, const float* sinks,
+                    void* out, float* lse, void* workspace, size_t workspace_bytes, void* stream);
 
 // Decode kernel (CUDA-core or mma variant, as the plan chose); the partials of
 // a split request are merged inside it by the last chunk CTA of each group.

@@ -18,33 +18,9 @@ struct ReqInfo {
   int32_t q_len;      // query rows of the request
   int32_t kv_len;     // key count seen by the planner (upper bound when not frozen)
   int32_t part_base;  // first fp32 partial row, -1 when the request is not split
-  int32_t n_chunks;   // partial states of a row: the chunks of its request's keys
+  int32_t n_chunks;   // chunks the request's key range was cut into
   int32_t cnt_base;   // split requests: first of its merge counters (one per KV head and tile)
-  int32_t n_items;    // of the chunks, those that decode CTAs make (the last ones; the
-                      // others are pieces of a shared prefix)
-  int32_t pad;
-};
-
-// A piece of a shared prefix for one KV head and up to 256 query rows of its group of
-// requests (48 bytes, three aligned loads).
-struct alignas(16) PrefixItem {
-  int32_t row;        // the table row that lists the prefix's pages
-  int32_t kv_head;
-  int32_t tile_lo;    // 64-key tiles [tile_lo, tile_hi)
-  int32_t tile_hi;
-  int32_t keys;       // of the whole prefix
-  int32_t chunk;      // which of the rows' partial states
-  int32_t q_start;    // the group's first packed query row
-  int32_t rows;       // its query rows times the heads of the KV head's group
-  int32_t row0;       // the first of them here
-  int32_t pad0, pad1, pad2;
-};
-
-// Where a packed query row's partial states lie: state c of head h is row
-// part0 + c * stride + h.
-struct PrefixToken {
-  int32_t part0;
-  int32_t stride;
+  int32_t pad1, pad2;
 };
 
 // One decode work item = one CTA: (request, kv head, chunk, pages [lo, hi)).
@@ -86,7 +62,6 @@ struct DecodeArgs {
   float bmm2_scale;
   int32_t in_f16;                // q/K/V are IEEE half (else bf16)
   int32_t out_dtype;             // PKA_DTYPE_BF16 / F16 / F32
-  int32_t behind_prefix;         // the prefix kernel, before this one, writes some of the partials
 };
 
 // Device error word bits (OR-ed by kernels, read by paged_decode_status).
@@ -114,17 +89,13 @@ struct pka_plan {
   std::vector<int32_t> page_lo, page_hi, order;
   std::vector<pka::WorkItem> items;
   int32_t num_merge_counters = 0;   // split requests: Hkv x tiles per item each
-  std::vector<pka::PrefixItem> prefix_items;     // shared prefixes (paged_prefix_decode_plan)
-  std::vector<pka::PrefixToken> prefix_tokens;   // per packed query row when there are any
-  // one device allocation holding items | reqs | status word | merge counters | prefix arrays
+  // one device allocation holding items | reqs | status word | merge counters
   void* dev_buf = nullptr;
   size_t dev_capacity = 0;    // bytes of dev_buf (reused by paged_decode_plan_update)
   const pka::WorkItem* d_items = nullptr;
   const pka::ReqInfo* d_reqs = nullptr;
   int32_t* d_status = nullptr;
   int32_t* d_merge_cnt = nullptr;
-  const pka::PrefixItem* d_prefix_items = nullptr;
-  const pka::PrefixToken* d_prefix_tokens = nullptr;
   int device = -1;
   // pinned host image of dev_buf: a replan writes it and uploads it with one
   // asynchronous copy; stage_done marks when that copy has read it
@@ -139,20 +110,17 @@ namespace pka {
 // visited pages per request, chunk choice under the CTA target, longest-first
 // item order, partial-row bases and workspace size.  Returns PKA_OK or an
 // error code (message recorded).
-//
-// shared: nullptr, or what the requests' shared prefixes leave to the decode.
-struct SharedPrefix {
-  const int32_t* pages;    // [B] leading pages that are not the decode's
-  const int32_t* chunks;   // [B] partial states that come from elsewhere, before the decode's own
-};
 int build_decode_plan(pka_plan& plan, const pka_decode_desc& desc, const int32_t* seq_lens_kv,
-                      const int32_t* qo_indptr, const SharedPrefix* shared = nullptr);
+                      const int32_t* qo_indptr);
 
 // Puts the plan's arrays on the device, in the plan's buffers.
 int upload_decode_plan(pka_plan& plan, cudaStream_t stream);
 
 // Rebuilt arrays `fresh` into the plan's buffers and `plan` (paged_decode_plan_update).
 int replace_decode_plan(pka_plan& plan, pka_plan&& fresh, cudaStream_t stream);
+
+// Gives `plan` the buffers of `from`, which keeps none.
+void keep_decode_buffers(pka_plan& plan, pka_plan& from);
 
 // Frees what a plan holds.
 void release_decode_plan(pka_plan& plan);

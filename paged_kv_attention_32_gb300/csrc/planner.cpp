@@ -60,7 +60,7 @@ int32_t env_int(const char* name, int32_t fallback) {
 }  // namespace
 
 int build_decode_plan(pka_plan& p, const pka_decode_desc& d_in, const int32_t* seq,
-                      const int32_t* indptr, const SharedPrefix* shared) {
+                      const int32_t* indptr) {
   pka_decode_desc d = d_in;
   PKA_CHECK_ARG(d.batch_size >= 1, "batch_size must be >= 1 (got %d)", d.batch_size);
   PKA_CHECK_ARG(seq != nullptr, "seq_lens_kv_host is NULL");
@@ -169,7 +169,6 @@ int build_decode_plan(pka_plan& p, const pka_decode_desc& d_in, const int32_t* s
     const int64_t kv_lo = windowed ? std::max<int64_t>(0, n - qlen[b] - d.window_left) : 0;
     p.page_lo[b] = (int32_t)(kv_lo / ps);
     p.page_hi[b] = (int32_t)ceil_div(n, ps);
-    if (shared != nullptr) p.page_lo[b] = std::max(p.page_lo[b], shared->pages[b]);
     npages[b] = p.page_hi[b] - p.page_lo[b];
   }
 
@@ -179,8 +178,7 @@ int build_decode_plan(pka_plan& p, const pka_decode_desc& d_in, const int32_t* s
     for (int32_t b = 0; b < B; ++b) tiles[b] = ceil_div((int64_t)p.G * qlen[b], 16);
   int64_t tiles_sum = 0;
   for (int32_t b = 0; b < B; ++b) tiles_sum += tiles[b];
-  // a request may have no page of its own behind a shared prefix: it still has an item
-  const int64_t max_np = std::max<int64_t>(1, *std::max_element(npages.begin(), npages.end()));
+  const int64_t max_np = *std::max_element(npages.begin(), npages.end());
   const int64_t target = (int64_t)d.split_waves * d.num_sms;
   int64_t chunk = max_np;
   if (tiles_sum * Hkv < target) {
@@ -244,15 +242,12 @@ int build_decode_plan(pka_plan& p, const pka_decode_desc& d_in, const int32_t* s
 
   // ---- items ----
   std::vector<int32_t> nch(B);
-  for (int32_t b = 0; b < B; ++b) nch[b] = (int32_t)std::max<int64_t>(1, npages[b] > 0 ? ceil_div(npages[b], cb[b]) : 1);
-  // partial states that the items' come behind
-  auto before = [&](int32_t b) { return shared != nullptr ? shared->chunks[b] : 0; };
+  for (int32_t b = 0; b < B; ++b) nch[b] = (int32_t)ceil_div(npages[b], cb[b]);
   int64_t n_items = 0;
   for (int32_t b = 0; b < B; ++b) n_items += (int64_t)nch[b] * Hkv;
   PKA_CHECK_ARG(n_items <= (int64_t)INT32_MAX, "too many work items");
   for (int32_t b = 0; b < B; ++b)
-    PKA_CHECK_ARG((int64_t)nch[b] + before(b) < (shared != nullptr ? 32768 : 65536),
-                  "request %d needs %d chunks (limit %d)", b, nch[b] + before(b), shared != nullptr ? 32767 : 65535);
+    PKA_CHECK_ARG(nch[b] < 65536, "request %d needs %d chunks (limit 65535)", b, nch[b]);
   PKA_CHECK_ARG(Hkv < 65536, "num_kv_heads must be < 65536");
   p.items.resize((size_t)n_items);
   WorkItem* item = p.items.data();
@@ -262,7 +257,7 @@ int build_decode_plan(pka_plan& p, const pka_decode_desc& d_in, const int32_t* s
     for (int32_t ci = 0; ci < n; ++ci) {
       const int32_t lo = lo0 + (int32_t)(ci * c);
       const int32_t hi = (int32_t)std::min<int64_t>(lo0 + (ci + 1) * c, hi0);
-      for (int32_t hk = 0; hk < Hkv; ++hk) *item++ = WorkItem{b, ((before(b) + ci) << 16) | hk, lo, hi};
+      for (int32_t hk = 0; hk < Hkv; ++hk) *item++ = WorkItem{b, (ci << 16) | hk, lo, hi};
     }
   }
 
@@ -279,12 +274,11 @@ int build_decode_plan(pka_plan& p, const pka_decode_desc& d_in, const int32_t* s
     r.q_start = qstart[b];
     r.q_len = qlen[b];
     r.kv_len = seq[b];
-    r.n_chunks = before(b) + nch[b];
-    r.n_items = nch[b];
+    r.n_chunks = nch[b];
     r.cnt_base = -1;
-    if (r.n_chunks > 1) {
+    if (nch[b] > 1) {
       r.part_base = (int32_t)prow;
-      prow += (int64_t)r.n_chunks * qlen[b] * Hq;
+      prow += (int64_t)nch[b] * qlen[b] * Hq;
       r.cnt_base = (int32_t)counters;
       counters += (int64_t)Hkv * tiles_per_item;
       ++n_split;

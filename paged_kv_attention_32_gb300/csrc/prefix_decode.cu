@@ -8,21 +8,27 @@
 // with the states of the request's own keys.  Every row sees the whole prefix, so the only
 // mask is the piece's end.
 //
-// A pair of CTAs (cta_group::2, one cluster, two SMs) takes 256 rows, 128 each, and walks
-// the keys in tiles of 64.  Each CTA holds its own queries and only half of every tile: 32
-// of the keys (half of B's N in S = Q K^T) and 64 of the value dimensions (half of N in
-// O += P V), which halves what the shared-memory port moves for K and V and the copies.
-// Two CTAs of different pairs share an SM and hide each other's softmax and start.
-//   warp 4      copies this CTA's half of the keys, page by page (TMA);
-//   warp 6      its half of the values;
-//   warp 5      in the leader, issues every tcgen05.mma for both CTAs: S_b (M=256, N=64,
-//               8 k-steps) into one of two S buffers, two tiles ahead of the softmax, and
-//               O += P V (M=256, N=128, 4 k-steps of 16 keys, P from TMEM);
+// A pair of CTAs (cta_group::2, one cluster, two SMs) takes 256 rows, 128 each, and walks the
+// keys in tiles of 64.  Each CTA holds its own queries and only half of every tile: 32 of the
+// keys (half of B's N in S = Q K^T) and 64 of the value dimensions (half of N in O += P V),
+// which halves what the shared-memory port moves for K and V and the copies.  The host deals
+// the work out evenly to one wave of pairs, which take their pieces in turn, the next one's
+// queries and keys copied while the last one ends.
 //   warps 0-3   gather the query rows (any token and head strides, any group size), then
 //               softmax, one thread per row: O rescaled only when the row maximum grew by
 //               more than 2^8, P in 16 bits over the S buffer (its rounding enters O like
-//               the inputs' own; the sum of p is taken in 32 bits before it).
-// TMEM columns: S0 [0,64) S1 [64,128) O [128,256).
+//               the inputs' own; the sum of p is taken in 32 bits before it);
+//   warp 4      copies this CTA's half of the keys, page by page (TMA);
+//   warp 5      the leader's issues every tcgen05.mma for both CTAs: S_b (M=256, N=64, 8
+//               k-steps) into a ring of S buffers, and O += P V (M=256, N=128, 4 k-steps of
+//               16 keys, P from TMEM);
+//   warp 6      copies this CTA's half of the values.
+// Two shapes.  DENSE, where the products bound the whole: two CTAs of different pairs share an
+// SM and hide each other's softmax, with two S buffers each.  Else, where memory does: one
+// CTA an SM with four S buffers, beside a CTA of the kernel over the requests' own keys, so
+// that both read at once.
+// Measured and not kept, 65536 keys and 1024 rows of 8 heads: one CTA with two row tiles and
+// one issuing warp 212 us, the same with two threads a row 240, DENSE 172.
 #include <cuda_bf16.h>
 
 #include "device_common.cuh"
@@ -42,30 +48,44 @@ constexpr int kTileQ = 128, kTileK = kPrefixTile, kD = 128;
 constexpr uint32_t kQBox = 16384;           // 128 rows x 128 bytes
 constexpr uint32_t kKBox = 4096;            // 32 keys x 128 bytes
 constexpr uint32_t kKBytes = 2 * kKBox, kVBytes = 8192;   // a CTA's half of a tile
-constexpr int kStages = 5;
-constexpr int kThreads = 224;
 constexpr float kRescaleThreshold = 8.0f;
-constexpr uint32_t kColO = 128, kTmemCols = 256;
+constexpr int kThreads = 224;
 
-constexpr uint32_t kOffQ = 0;
-constexpr uint32_t kOffK = 2 * kQBox;
-constexpr uint32_t kOffV = kOffK + kStages * kKBytes;
-constexpr uint32_t kOffBar = kOffV + kStages * kVBytes;
-constexpr size_t kSmemBytes = kOffBar + 256;
-static_assert(2 * (kSmemBytes + 1024) <= 228 * 1024, "two CTAs share an SM");
-
-// Q, K, V and P are waited for by the leader's MMA warp, on the leader's barriers, where
-// both CTAs arrive; the others are signalled in both CTAs by the commits.  Tile j uses S, P
-// and O barriers j & 1.  No barrier runs a phase past one that somebody still has to see:
-// S(j) is issued behind P V(j - 2), and P(j) is written once S(j) is complete.
-enum {
-  B_QFULL = 0, B_KFULL, B_KEMPTY = B_KFULL + kStages, B_VFULL = B_KEMPTY + kStages, B_VEMPTY = B_VFULL + kStages,
-  B_SFULL = B_VEMPTY + kStages, B_PFULL = B_SFULL + 2, B_ODONE = B_PFULL + 2, B_MMADONE = B_ODONE + 2, B_COUNT
+template <bool DENSE>
+struct Geo {
+  static constexpr int kStages = 5, kScores = DENSE ? 2 : 4, kRegs = 128;
+  static constexpr uint32_t kOffK = 2 * kQBox, kOffV = kOffK + kStages * kKBytes;
+  static constexpr uint32_t kOffBar = kOffV + kStages * kVBytes;
+  static constexpr size_t kSmemBytes = kOffBar + 512;
+  static constexpr uint32_t kColO = kScores * 64, kTmemCols = kColO + kD <= 256 ? 256 : 512;
+  // Q, K, V, P and O-free are waited for by the leader's MMA warp, on the leader's barriers,
+  // where both CTAs arrive; the others are signalled in both CTAs by the commits.  T counts a
+  // pair's key tiles over all its pieces: S, P and O barriers T % kScores.  No barrier runs a
+  // phase past one that somebody still has to see: S(T) is issued behind P V(T - kScores), P(T)
+  // written once S(T) is complete, the next piece's Q written once this one's last S is
+  // complete and its first P V issued once O is free.
+  static constexpr int kQFull = 0, kOFree = 1, kMmaDone = 2, kKFull = 3, kKEmpty = kKFull + kStages,
+                       kVFull = kKEmpty + kStages, kVEmpty = kVFull + kStages, kSFull = kVEmpty + kStages,
+                       kPFull = kSFull + kScores, kODone = kPFull + kScores, kCount = kODone + kScores;
+  static_assert(kCount * 8 + 4 <= 512, "barriers and the TMEM address slot");
 };
-static_assert(B_COUNT * 8 + 4 <= 256, "barriers and the TMEM address slot");
+static_assert(2 * (Geo<true>::kSmemBytes + 1024) <= 228 * 1024, "two CTAs share an SM");
 
 template <bool F16> constexpr uint32_t kIdescQK = idesc_bf16_f32(256, 64, 0, 0, F16);
 template <bool F16> constexpr uint32_t kIdescPV = idesc_bf16_f32(256, kD, 0, 1, F16);
+
+// A position in a ring of N and the parity of its current round.
+template <int N>
+struct RingPos {
+  int slot = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == N) {
+      slot = 0;
+      parity ^= 1u;
+    }
+  }
+};
 
 __device__ __forceinline__ void store_sector(float* dst, const uint32_t* w) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]),
@@ -73,85 +93,92 @@ __device__ __forceinline__ void store_sector(float* dst, const uint32_t* w) {
                : "memory");
 }
 
-template <bool F16>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 2)
+template <bool F16, bool DENSE>
+__global__ void __cluster_dims__(2, 1, 1) __maxnreg__(Geo<DENSE>::kRegs)
 prefix_kernel(const __grid_constant__ PrefixArgs a, const __grid_constant__ CUtensorMap tmk,
               const __grid_constant__ CUtensorMap tmv) {
+  using Gm = Geo<DENSE>;
+  constexpr int kStages = Gm::kStages, kScores = Gm::kScores;
+  constexpr uint32_t kOffK = Gm::kOffK, kOffV = Gm::kOffV;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffBar + B_COUNT * 8);
-  auto bar = [&](int i) -> uint32_t { return sbase + kOffBar + 8u * (uint32_t)i; };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Gm::kOffBar + Gm::kCount * 8);
+  auto bar = [&](int i) -> uint32_t { return sbase + Gm::kOffBar + 8u * (uint32_t)i; };
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_rank();   // 0: the leader
-  const PrefixItem it = a.items[blockIdx.x >> 1];
+  const int pair = blockIdx.x >> 1;
 
-  if (tid == 0) {
-    mbar_init(bar(B_QFULL), 8);             // the pair's softmax warps
+  if (tid == 0) {   // the list comes in while the pair sets up
+    ask_line(a.segments + pair);
+    mbar_init(bar(Gm::kQFull), 8);   // the pair's softmax warps
+    mbar_init(bar(Gm::kOFree), 8);
+    mbar_init(bar(Gm::kMmaDone), 1);
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(bar(B_KFULL + s), 2);
-      mbar_init(bar(B_KEMPTY + s), 1);
-      mbar_init(bar(B_VFULL + s), 2);
-      mbar_init(bar(B_VEMPTY + s), 1);
+      mbar_init(bar(Gm::kKFull + s), 2);
+      mbar_init(bar(Gm::kKEmpty + s), 1);
+      mbar_init(bar(Gm::kVFull + s), 2);
+      mbar_init(bar(Gm::kVEmpty + s), 1);
     }
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(bar(B_SFULL + s), 1);
-      mbar_init(bar(B_PFULL + s), 8);
-      mbar_init(bar(B_ODONE + s), 1);
+    for (int s = 0; s < kScores; ++s) {
+      mbar_init(bar(Gm::kSFull + s), 1);
+      mbar_init(bar(Gm::kPFull + s), 8);
+      mbar_init(bar(Gm::kODone + s), 1);
     }
-    mbar_init(bar(B_MMADONE), 1);
     fence_barrier_init();
   }
   __syncwarp();
   cluster_arrive();
-  if (warp == 5) tmem_alloc_pair(smem_u32(tmem_slot), kTmemCols);
+  if (warp == 5) tmem_alloc_pair(smem_u32(tmem_slot), Gm::kTmemCols);
   tc_fence_before();
   __syncthreads();
   cluster_wait();   // both CTAs' barriers stand before anyone arrives on them
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  // the decode's CTAs may start taking free SMs; their merges wait for this grid's end
+  // the other kernel's CTAs may start; the merge behind it waits for this grid's end
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  const int n_kv = it.tile_hi - it.tile_lo;
+  const int first = __ldg(a.segments + pair), end = __ldg(a.segments + pair + 1);
   if (warp == 4 || warp == 6) {
     // ---------------- producers: one lane per copy of a tile ----------------
     const bool is_v = warp == 6;
     const CUtensorMap* map = is_v ? &tmv : &tmk;
     if (lane == 0) tma_prefetch_desc(map);
-    const int full0 = is_v ? B_VFULL : B_KFULL, empty0 = is_v ? B_VEMPTY : B_KEMPTY;
+    const int full0 = is_v ? Gm::kVFull : Gm::kKFull, empty0 = is_v ? Gm::kVEmpty : Gm::kKEmpty;
     // K: 32 keys of both halves, V: 64 keys of one half; a lane's 16-key unit in the tile,
     // half and place in the stage
     const int copies = is_v ? kTileK / a.v_rows : a.k_rows == 32 ? 1 : 4;
     const int unit = is_v ? lane * (a.v_rows / 16) : (int)rank * 2 + (lane & 1);
     const int half = is_v ? (int)rank : lane >> 1;
     const uint32_t off = is_v ? kOffV + (uint32_t)unit * 2048u : kOffK + (uint32_t)(lane >> 1) * kKBox + (uint32_t)(lane & 1) * 2048u;
-    const int32_t* row = a.block_tables + (int64_t)it.row * a.bt_row_stride;
-    const int units = it.keys / 16;
-    // page of this lane's unit of tile j: past the prefix one past the pool, which reads as zeros
-    auto page_of = [&](int j) -> int {
-      const int u = (it.tile_lo + j) * (kTileK / 16) + unit;
-      return lane < copies && j < n_kv && u < units ? __ldg(row + u / a.page_units) : a.num_pages;
-    };
-    int page = page_of(0), stage = 0;
-    uint32_t parity = 0;
+    RingPos<kStages> pos;
+    int filled = 0;
     bool ok = true;
-    for (int j = 0; j < n_kv; ++j) {
-      const int next = page_of(j + 1);
-      if (j >= kStages && !(ok = warp_wait(bar(empty0 + stage), parity ^ 1u, a.status))) break;
-      const uint32_t full = map_to_rank(bar(full0 + stage), 0);
-      if (lane == 0) mbar_arrive_expect_tx_cluster(full, kKBytes);
-      __syncwarp();
-      if (lane < copies) {
+    for (int i = first; ok && i < end; ++i) {
+      const PrefixItem it = a.items[i];
+      const int32_t* row = a.block_tables + (int64_t)it.row * a.bt_row_stride;
+      const int units = it.keys / 16, n_kv = it.tile_hi - it.tile_lo;
+      // page of this lane's unit of tile j: past the prefix one past the pool, which reads as zeros
+      auto page_of = [&](int j) -> int {
         const int u = (it.tile_lo + j) * (kTileK / 16) + unit;
-        tma_load_5d_pair(sbase + off + (uint32_t)stage * kKBytes, map, full, 0, (u % a.page_units) * 16, half,
-                         it.kv_head, page);
-      }
-      __syncwarp();
-      page = next;
-      if (++stage == kStages) {
-        stage = 0;
-        parity ^= 1u;
+        return lane < copies && j < n_kv && u < units ? __ldg(row + u / a.page_units) : a.num_pages;
+      };
+      int page = page_of(0);
+      for (int j = 0; j < n_kv; ++j) {
+        const int next = page_of(j + 1);
+        if (filled >= kStages && !(ok = warp_wait(bar(empty0 + pos.slot), pos.parity ^ 1u, a.status))) break;
+        const uint32_t full = map_to_rank(bar(full0 + pos.slot), 0);
+        if (lane == 0) mbar_arrive_expect_tx_cluster(full, kKBytes);
+        __syncwarp();
+        if (lane < copies) {
+          const int u = (it.tile_lo + j) * (kTileK / 16) + unit;
+          tma_load_5d_pair(sbase + off + (uint32_t)pos.slot * kKBytes, map, full, 0, (u % a.page_units) * 16, half,
+                           it.kv_head, page);
+        }
+        __syncwarp();
+        page = next;
+        pos.next();
+        ++filled;
       }
     }
     // When a wait gave up, copies still in flight land before the cluster leaves:
@@ -164,155 +191,172 @@ prefix_kernel(const __grid_constant__ PrefixArgs a, const __grid_constant__ CUte
   } else if (warp == 5) {
     // ---------------- MMA issuer, the leader's: one elected lane issues for the pair ----
     if (rank == 0) {
-      int ks = 0, vs = 0;
-      uint32_t kpar = 0, vpar = 0;
-      auto issue_qk = [&](int j) -> bool {   // S of tile j into buffer j & 1
-        if (!warp_wait(bar(B_KFULL + ks), kpar, a.status)) return false;
-        tc_fence_after();
-        const int st = j & 1;
+      RingPos<kStages> kp, vp;
+      RingPos<kScores> sp, pp;   // the next S to issue and the next P to wait for
+      bool ok = true;
+      for (int i = first; ok && i < end; ++i) {
+        const int n_kv = __ldg(&a.items[i].tile_hi) - __ldg(&a.items[i].tile_lo);
+        auto issue_qk = [&]() -> bool {   // S of the next key tile into the next buffer
+          if (!warp_wait(bar(Gm::kKFull + kp.slot), kp.parity, a.status)) return false;
+          tc_fence_after();
 #pragma unroll
-        for (int blk = 0; blk < 2; ++blk)
-          umma_pair_ss_k4(tmem + (uint32_t)st * 64u,
-                          smem_desc_sw128(sbase + kOffQ + (uint32_t)blk * kQBox, 16u, 1024u),
-                          smem_desc_sw128(sbase + kOffK + (uint32_t)ks * kKBytes + (uint32_t)blk * kKBox, 16u, 1024u),
-                          kIdescQK<F16>, blk > 0 ? 1u : 0u);
-        umma_pair_commit_elect(bar(B_SFULL + st));
-        umma_pair_commit_elect(bar(B_KEMPTY + ks));
-        if (++ks == kStages) {
-          ks = 0;
-          kpar ^= 1u;
+          for (int blk = 0; blk < 2; ++blk)
+            umma_pair_ss_k4(tmem + (uint32_t)sp.slot * 64u,
+                            smem_desc_sw128(sbase + (uint32_t)blk * kQBox, 16u, 1024u),
+                            smem_desc_sw128(sbase + kOffK + (uint32_t)kp.slot * kKBytes + (uint32_t)blk * kKBox, 16u,
+                                            1024u),
+                            kIdescQK<F16>, blk > 0 ? 1u : 0u);
+          umma_pair_commit_elect(bar(Gm::kSFull + sp.slot));
+          umma_pair_commit_elect(bar(Gm::kKEmpty + kp.slot));
+          kp.next();
+          sp.next();
+          return true;
+        };
+        // queries: ordinary writes, of the other CTA too
+        ok = warp_wait<true>(bar(Gm::kQFull), (uint32_t)((i - first) & 1), a.status);
+        for (int j = 0; ok && j < n_kv && j < kScores; ++j) ok = issue_qk();
+        for (int j = 0; ok && j < n_kv; ++j) {
+          ok = warp_wait(bar(Gm::kVFull + vp.slot), vp.parity, a.status) &&
+               warp_wait(bar(Gm::kPFull + pp.slot), pp.parity, a.status);
+          if (ok && j == 0 && i > first) ok = warp_wait(bar(Gm::kOFree), (uint32_t)((i - first - 1) & 1), a.status);
+          if (!ok) break;
+          tc_fence_after();
+          // 4 k-steps of 16 keys: P columns +8, V rows +16 (2048 bytes)
+          umma_pair_ts_k4<2048 / 16>(tmem + Gm::kColO, tmem + (uint32_t)pp.slot * 64u,
+                                     smem_desc_sw128(sbase + kOffV + (uint32_t)vp.slot * kVBytes, kVBytes, 1024u),
+                                     kIdescPV<F16>, j > 0 ? 1u : 0u);
+          umma_pair_commit_elect(bar(Gm::kODone + pp.slot));
+          umma_pair_commit_elect(bar(Gm::kVEmpty + vp.slot));
+          vp.next();
+          pp.next();
+          // the S buffer is free again once this P V has read P (issue order)
+          if (j + kScores < n_kv) ok = issue_qk();
         }
-        return true;
-      };
-      // queries: ordinary writes, of the other CTA too
-      bool ok = warp_wait<true>(bar(B_QFULL), 0, a.status);
-      for (int j = 0; ok && j < n_kv && j < 2; ++j) ok = issue_qk(j);
-      for (int j = 0; ok && j < n_kv; ++j) {
-        const int st = j & 1;
-        ok = warp_wait(bar(B_VFULL + vs), vpar, a.status) &&
-             warp_wait(bar(B_PFULL + st), (uint32_t)((j >> 1) & 1), a.status);
-        if (!ok) break;
-        tc_fence_after();
-        // 4 k-steps of 16 keys: P columns +8, V rows +16 (2048 bytes)
-        umma_pair_ts_k4<2048 / 16>(tmem + kColO, tmem + (uint32_t)st * 64u,
-                                   smem_desc_sw128(sbase + kOffV + (uint32_t)vs * kVBytes, kVBytes, 1024u),
-                                   kIdescPV<F16>, j > 0 ? 1u : 0u);
-        umma_pair_commit_elect(bar(B_ODONE + st));
-        umma_pair_commit_elect(bar(B_VEMPTY + vs));
-        if (++vs == kStages) {
-          vs = 0;
-          vpar ^= 1u;
-        }
-        // S buffer st is free again once this P V has read P (issue order)
-        if (j + 2 < n_kv) ok = issue_qk(j + 2);
       }
-      umma_pair_commit_elect(bar(B_MMADONE));
+      umma_pair_commit_elect(bar(Gm::kMmaDone));
     }
   } else {
     // ---------------- softmax: one thread per query row ----------------
-    const int r = it.row0 + (int)rank * kTileQ + tid;
-    const bool live = r < it.rows;
-    const int token = it.q_start + r / a.group, head = it.kv_head * a.group + r % a.group;
-    // a warp's rows, two at a time, 16 lanes a row; zeros where there is none
-    const int64_t src = live ? (int64_t)token * a.q_stride_tok + (int64_t)head * a.q_stride_head : -1;
+    const int mine = (int)rank * kTileQ + tid;
+    // the query rows of a piece into shared memory, two at a time, 16 lanes a row; zeros
+    // where there is none
+    auto gather = [&](int i) {
+      const PrefixItem it = a.items[i];
+      const int r = it.row0 + mine;
+      const int64_t src = r < it.rows ? (int64_t)(it.q_start + r / a.group) * a.q_stride_tok +
+                                            (int64_t)(it.kv_head * a.group + r % a.group) * a.q_stride_head
+                                      : -1;
 #pragma unroll 4
-    for (int i = 0; i < 16; ++i) {
-      const int rr = 2 * i + (lane >> 4), c = lane & 15;
-      const int64_t at = __shfl_sync(0xffffffffu, src, rr);
-      uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (at >= 0) v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at) + c);
-      v.x ^= a.negate;
-      v.y ^= a.negate;
-      v.z ^= a.negate;
-      v.w ^= a.negate;
-      *reinterpret_cast<uint4*>(smem + kOffQ + (uint32_t)(c >> 3) * kQBox +
-                                swz128((uint32_t)(warp * 32 + rr), (uint32_t)(c & 7))) = v;
-    }
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive_cluster(map_to_rank(bar(B_QFULL), 0));
-
-    const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
-    const uint32_t o_tm = tmem + lane_off + kColO;
-    const float sl2 = a.scale_log2;   // >= 0
-    const bool any_live = __any_sync(0xffffffffu, live);
-    float m_ref = neg_inf(), l = 0.f;
-    bool ok = true;
-    for (int j = 0; j < n_kv; ++j) {
-      const int st = j & 1;
-      if (!(ok = warp_wait(bar(B_SFULL + st), (uint32_t)((j >> 1) & 1), a.status))) break;
-      if (any_live) {   // else P may be anything: rows stay apart
-        tc_fence_after();
-        const uint32_t s_tm = tmem + lane_off + (uint32_t)st * 64u;
-        const int key0 = (it.tile_lo + j) * kTileK;
-        const bool masked = key0 + kTileK > it.keys;
-        uint32_t ra[32], rb[32];
-        tmem_ld32(s_tm, ra);
-        tmem_ld32(s_tm + 32u, rb);
-        tmem_wait_ld();
-        reg_fence32(ra);
-        reg_fence32(rb);
-        uint32_t w0 = 0xffffffffu, w1 = 0xffffffffu;
-        if (masked) {
-          visible_bits(key0, 0, (unsigned)it.keys, w0, w1);
-          mask_scores64(ra, rb, w0, w1);
-        }
-        const float mraw = row_max64(ra, rb);
-        const float mx = mraw == neg_inf() ? neg_inf() : mraw * sl2;
-        const bool grow = mx > m_ref + kRescaleThreshold;
-        const float m_new = grow ? mx : m_ref;
-        const bool rescale = grow && m_ref != neg_inf();   // else O and l are still zero
-        const float alpha = rescale ? ex2(m_ref - m_new) : 1.f;
-        if (j > 0 && __any_sync(0xffffffffu, rescale)) {
-          // O holds the tiles before: wait for P V of the last of them before rescaling
-          if (!(ok = warp_wait(bar(B_ODONE + (st ^ 1)), (uint32_t)(((j - 1) >> 1) & 1), a.status))) break;
-          tc_fence_after();
-#pragma unroll 1
-          for (int c = 0; c < kD / 32; ++c) {
-            uint32_t o[32];
-            tmem_ld32_sync(o_tm + (uint32_t)c * 32u, o);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-            tmem_st32(o_tm + (uint32_t)c * 32u, o);
-          }
-          tmem_wait_st();
-        }
-        m_ref = m_new;
-        // A row whose scores are all -inf keeps m_ref = -inf: exp2(-inf) = 0.  Masked scores
-        // give 0 through their -inf unless the scale is 0.
-        const float neg_m = m_ref == neg_inf() ? 0.f : kLatentWeightShift<F16> - m_ref;
-        const bool zero_again = masked && !(sl2 > 0.f);
-        const float2 sum = zero_again ? exp_tile<true, F16>(ra, rb, sl2, neg_m, w0, w1, s_tm)
-                                      : exp_tile<false, F16>(ra, rb, sl2, neg_m, w0, w1, s_tm);
-        tmem_wait_st();
-        l = l * alpha + (sum.x + sum.y);
-        tc_fence_before();
+      for (int k = 0; k < 16; ++k) {
+        const int rr = 2 * k + (lane >> 4), c = lane & 15;
+        const int64_t at = __shfl_sync(0xffffffffu, src, rr);
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (at >= 0) v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at) + c);
+        v.x ^= a.negate;
+        v.y ^= a.negate;
+        v.z ^= a.negate;
+        v.w ^= a.negate;
+        *reinterpret_cast<uint4*>(smem + (uint32_t)(c >> 3) * kQBox + swz128((uint32_t)(warp * 32 + rr), (uint32_t)(c & 7))) = v;
       }
+      fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive_remote(map_to_rank(bar(B_PFULL + st), 0));
-    }
-    if (ok && any_live && warp_wait(bar(B_ODONE + ((n_kv - 1) & 1)), (uint32_t)(((n_kv - 1) >> 1) & 1), a.status)) {
-      tc_fence_after();
-      // != and not >: a sum that is NaN stays one, in the LSE as in the output
-      const float inv = l != 0.f ? 1.f / l : 0.f;
-      int64_t part = 0;
-      if (live) {
-        const PrefixToken t = a.tokens[token];
-        part = (int64_t)t.part0 + (int64_t)it.chunk * t.stride + head;
-      }
+      if (lane == 0) mbar_arrive_cluster(map_to_rank(bar(Gm::kQFull), 0));
+    };
+    const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
+    const uint32_t o_tm = tmem + lane_off + Gm::kColO;
+    const float sl2 = a.scale_log2;   // >= 0
+    RingPos<kScores> sp;
+    uint32_t last_o = 0, last_parity = 0;   // O barrier of the tile before and its parity
+    bool ok = true;
+    if (first < end) gather(first);
+    for (int i = first; ok && i < end; ++i) {
+      const PrefixItem it = a.items[i];
+      const int n_kv = it.tile_hi - it.tile_lo;
+      const bool live = it.row0 + mine < it.rows, any_live = __any_sync(0xffffffffu, live);
+      float m_ref = neg_inf(), l = 0.f;
+      for (int j = 0; j < n_kv; ++j) {
+        if (!(ok = warp_wait(bar(Gm::kSFull + sp.slot), sp.parity, a.status))) break;
+        if (any_live) {   // else P may be anything: rows stay apart
+          tc_fence_after();
+          const uint32_t s_tm = tmem + lane_off + (uint32_t)sp.slot * 64u;
+          const int key0 = (it.tile_lo + j) * kTileK;
+          const bool masked = key0 + kTileK > it.keys;
+          uint32_t ra[32], rb[32];
+          tmem_ld32(s_tm, ra);
+          tmem_ld32(s_tm + 32u, rb);
+          tmem_wait_ld();
+          reg_fence32(ra);
+          reg_fence32(rb);
+          uint32_t w0 = 0xffffffffu, w1 = 0xffffffffu;
+          if (masked) {
+            visible_bits(key0, 0, (unsigned)it.keys, w0, w1);
+            mask_scores64(ra, rb, w0, w1);
+          }
+          const float mraw = row_max64(ra, rb);
+          const float mx = mraw == neg_inf() ? neg_inf() : mraw * sl2;
+          const bool grow = mx > m_ref + kRescaleThreshold;
+          const float m_new = grow ? mx : m_ref;
+          const bool rescale = grow && m_ref != neg_inf();   // else O and l are still zero
+          const float alpha = rescale ? ex2(m_ref - m_new) : 1.f;
+          if (j > 0 && __any_sync(0xffffffffu, rescale)) {
+            // O holds the tiles before: wait for P V of the last of them before rescaling
+            if (!(ok = warp_wait(last_o, last_parity, a.status))) break;
+            tc_fence_after();
 #pragma unroll 1
-      for (int c = 0; c < kD; c += 32) {
-        uint32_t o[32];
-        __syncwarp();   // the lanes whose rows are stored and the others load together
-        tmem_ld32_sync(o_tm + (uint32_t)c, o);
+            for (int c = 0; c < kD; c += 16) {   // 16 at a time: the scores stay in registers
+              uint32_t o[16];
+              tmem_ld16(o_tm + (uint32_t)c, o);
+              tmem_wait_ld();
+              reg_fence<16>(o);
 #pragma unroll
-        for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * inv);
-        if (live) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) store_sector(a.ws_o + part * kD + c + 8 * k, o + 8 * k);
+              for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * alpha);
+              tmem_st16(o_tm + (uint32_t)c, o);
+            }
+            tmem_wait_st();
+          }
+          m_ref = m_new;
+          // A row whose scores are all -inf keeps m_ref = -inf: exp2(-inf) = 0.  Masked scores
+          // give 0 through their -inf unless the scale is 0.
+          const float neg_m = m_ref == neg_inf() ? 0.f : kLatentWeightShift<F16> - m_ref;
+          const bool zero_again = masked && !(sl2 > 0.f);
+          const float2 sum = zero_again ? exp_tile<true, F16>(ra, rb, sl2, neg_m, w0, w1, s_tm)
+                                        : exp_tile<false, F16>(ra, rb, sl2, neg_m, w0, w1, s_tm);
+          tmem_wait_st();
+          l = l * alpha + (sum.x + sum.y);
+          tc_fence_before();
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(map_to_rank(bar(Gm::kPFull + sp.slot), 0));
+        last_o = bar(Gm::kODone + sp.slot);
+        last_parity = sp.parity;
+        sp.next();
       }
-      if (live) a.ws_lse[part] = l != 0.f ? m_ref - kLatentWeightShift<F16> + log2f(l) : neg_inf();
+      if (!ok) break;
+      // every S of this piece is complete: its queries make room for the next one's
+      if (i + 1 < end) gather(i + 1);
+      if (!(ok = warp_wait(last_o, last_parity, a.status))) break;
+      tc_fence_after();
+      if (any_live) {
+        // != and not >: a sum that is NaN stays one, in the LSE as in the output
+        const float inv = l != 0.f ? 1.f / l : 0.f;
+        const int64_t state = (int64_t)it.state + mine;
+#pragma unroll 1
+        for (int c = 0; c < kD; c += 32) {
+          uint32_t o[32];
+          __syncwarp();   // the lanes whose rows are stored and the others load together
+          tmem_ld32_sync(o_tm + (uint32_t)c, o);
+#pragma unroll
+          for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * inv);
+          if (live) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) store_sector(a.ws_o + state * kD + c + 8 * x, o + 8 * x);
+          }
+        }
+        if (live) a.ws_lse[state] = l != 0.f ? m_ref - kLatentWeightShift<F16> + log2f(l) : neg_inf();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote(map_to_rank(bar(Gm::kOFree), 0));
     }
   }
 
@@ -321,26 +365,32 @@ prefix_kernel(const __grid_constant__ PrefixArgs a, const __grid_constant__ CUte
   __syncthreads();
   // Nothing of the pair's still runs on the tensor cores, and every commit has landed here.
   // Waited for only now: all of a pair's tiles may take longer than any one wait may.
-  if (warp == 5) warp_wait(bar(B_MMADONE), 0, a.status);
+  if (warp == 5) warp_wait(bar(Gm::kMmaDone), 0, a.status);
   cluster_sync();   // neither CTA's shared memory nor TMEM goes while the pair still uses it
   if (warp == 5) {
     tc_fence_after();
-    tmem_dealloc_pair(tmem, kTmemCols);
+    tmem_dealloc_pair(tmem, Gm::kTmemCols);
   }
+}
+
+template <bool F16, bool DENSE>
+int launch(const PrefixArgs& args, const CUtensorMap& kmap, const CUtensorMap& vmap, cudaStream_t stream) {
+  auto kern = prefix_kernel<F16, DENSE>;
+  static std::atomic<uint64_t> smem_set{0};   // devices whose limit was raised
+  cudaError_t e = set_smem_once(kern, (int)Geo<DENSE>::kSmemBytes, smem_set, true);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(prefix)");
+  kern<<<2 * args.num_pairs, kThreads, Geo<DENSE>::kSmemBytes, stream>>>(args, kmap, vmap);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e, "prefix_kernel launch");
+  return PKA_OK;
 }
 
 }  // namespace
 
-int launch_prefix(const PrefixArgs& args, bool f16, const CUtensorMap& kmap, const CUtensorMap& vmap,
+int launch_prefix(const PrefixArgs& args, bool f16, bool dense, const CUtensorMap& kmap, const CUtensorMap& vmap,
                   cudaStream_t stream) {
-  auto kern = f16 ? prefix_kernel<true> : prefix_kernel<false>;
-  static std::atomic<uint64_t> smem_set[2];   // per input type: devices whose limit was raised
-  cudaError_t e = set_smem_once(kern, (int)kSmemBytes, smem_set[f16]);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(prefix)");
-  kern<<<2 * args.num_items, kThreads, kSmemBytes, stream>>>(args, kmap, vmap);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return cuda_fail(e, "prefix_kernel launch");
-  return PKA_OK;
+  if (dense) return f16 ? launch<true, true>(args, kmap, vmap, stream) : launch<false, true>(args, kmap, vmap, stream);
+  return f16 ? launch<true, false>(args, kmap, vmap, stream) : launch<false, false>(args, kmap, vmap, stream);
 }
 
 }  // namespace pka

@@ -2,11 +2,11 @@
 //
 // A group of requests that begin with the same pages attends to them once: the query
 // rows of all its requests, times the heads of a KV head's group, are the rows of one
-// product with the prefix's keys, in tiles of 256 rows and 64 keys.  A prefix is cut along
-// its keys into chunks alike for every group, KV head and row tile, c tiles each, where
-// (waves of pairs of CTAs) * (c + what a piece costs besides its tiles) is least; each
-// chunk is one partial state of the group's rows.  What the requests have behind the
-// prefix is planned as decode work, whose states come behind those.
+// product with the prefix's keys.  The products (group, KV head, row tile) are laid end to
+// end and dealt out evenly, in tiles of 64 keys, to one wave of pairs of CTAs; what the
+// requests have behind the prefix (request, KV head, 16 rows) is cut into pieces of up to 16
+// units of 16 keys, which the warps of one wave of CTAs take as they come.  Every piece
+// writes a partial state of its rows, and a merge takes all of a row's.
 #include <algorithm>
 #include <cmath>
 #include <vector>
@@ -18,13 +18,37 @@ namespace pka {
 
 namespace {
 
-// What a piece costs besides its tiles (start, query rows, partial states), in tiles.
-constexpr int64_t kPieceTiles = 8;
+// Bytes of K and V that sharing keeps from being read again, from which it is done: below, the
+// two further launches and the states cost more than reading a prefix, most of it from L2,
+// for every request.
+constexpr int64_t kWorthBytes = 48 << 20;
+constexpr int64_t kMinPrefixTiles = 3;   // a piece is no shorter, its row tile's keys allowing
+constexpr int64_t kMinOwnUnits = 6, kMaxOwnUnits = 16;   // of 16 keys, in a piece of a request
+
+// Cuts runs of work laid end to end into `parts` even shares.
+class Dealer {
+ public:
+  Dealer(int64_t total, int64_t parts, int64_t least) : total_(total), parts_(parts), least_(least) {}
+  // The share that takes the next piece of a run of `left` units, and how many of them.
+  int64_t take(int64_t left, int64_t* units) {
+    auto room = [&] { return (part_ + 1) * total_ / parts_ - done_; };
+    while (room() < std::min(least_, left) && part_ + 1 < parts_) ++part_;
+    int64_t n = part_ + 1 == parts_ ? left : std::min(left, std::max(room(), std::min(least_, left)));
+    if (left - n < least_) n = left;
+    done_ += n;
+    *units = n;
+    return part_;
+  }
+
+ private:
+  int64_t total_, parts_, least_, part_ = 0, done_ = 0;
+};
 
 }  // namespace
 
-int build_prefix_plan(pka_plan& p, const pka_decode_desc& d_in, const int32_t* seq, const int32_t* indptr,
-                      const int32_t* group_indptr, int32_t num_groups, const int32_t* prefix_pages) {
+int build_prefix_plan(pka_prefix_plan& p, const pka_decode_desc& d_in, const int32_t* seq, const int32_t* indptr,
+                      const int32_t* group_indptr, int32_t num_groups, const int32_t* prefix_pages,
+                      int64_t min_shared_bytes) {
   PKA_CHECK_ARG(num_groups >= 1 && group_indptr != nullptr && prefix_pages != nullptr,
                 "num_groups must be >= 1, group_indptr and prefix_pages not NULL");
   const int32_t B = d_in.batch_size;
@@ -37,78 +61,129 @@ int build_prefix_plan(pka_plan& p, const pka_decode_desc& d_in, const int32_t* s
                 group_indptr[num_groups]);
   if (d_in.window_left != -1)
     return fail(PKA_ERR_UNSUPPORTED, "a window over a shared prefix is not built (window_left %d)", d_in.window_left);
-  pka_decode_desc d = d_in;
-  d.mma_min_rows = 1;   // the tensor-core decode, which may start before the prefix kernel ends
-
-  // a plan without sharing first: it checks the arguments, and gives the query rows
-  int rc = build_decode_plan(p, d, seq, indptr);
+  const int rc = build_decode_plan(p.base, d_in, seq, indptr);
   if (rc != PKA_OK) return rc;
-  const int32_t G = p.G, Hkv = p.Hkv, Hq = p.Hq, ps = p.ps;
-  for (int32_t g = 0; g < num_groups; ++g)
-    for (int32_t b = group_indptr[g]; b < group_indptr[g + 1]; ++b) {
-      const int64_t first_row = (int64_t)seq[b] - (d.mask == PKA_MASK_CAUSAL ? p.reqs[b].q_len - 1 : 0);
-      PKA_CHECK_ARG((int64_t)prefix_pages[g] * ps <= first_row,
-                    "request %d: its first row sees %lld keys, the shared prefix has %lld", b, (long long)first_row,
-                    (long long)prefix_pages[g] * ps);
-    }
-
-  // ---- which groups share, and in how many pieces ----
-  struct Shared {
-    int32_t group;
-    int64_t tiles, row_tiles, rows;
-  };
-  std::vector<Shared> shared;
-  int64_t most_tiles = 0;
+  const pka_decode_desc& d = p.base.desc;
+  const int32_t G = p.base.G, Hkv = p.base.Hkv, ps = p.base.ps;
+  const std::vector<ReqInfo>& reqs = p.base.reqs;
+  int64_t saved = 0, most_rows = 0;
   for (int32_t g = 0; g < num_groups; ++g) {
     const int32_t b0 = group_indptr[g], b1 = group_indptr[g + 1];
-    if (b1 - b0 < 2 || prefix_pages[g] == 0) continue;   // nothing to read once instead of twice
-    const ReqInfo& last = p.reqs[b1 - 1];
-    const int64_t rows = (int64_t)(last.q_start + last.q_len - p.reqs[b0].q_start) * G;
-    PKA_CHECK_ARG(rows <= INT32_MAX, "group %d has too many query rows", g);
-    const int64_t tiles = ceil_div((int64_t)prefix_pages[g] * ps, kPrefixTile);
-    shared.push_back(Shared{g, tiles, ceil_div(rows, kPrefixRows), rows});
-    most_tiles = std::max(most_tiles, tiles);
-  }
-  if (shared.empty()) return PKA_OK;
-  const int64_t pairs = p.desc.num_sms;   // two CTAs an SM, two CTAs a pair
-  int64_t best = 0, chunk = 1;
-  for (int64_t c = 1; c <= most_tiles; c = std::max(c + 1, c * 65 / 64)) {
-    int64_t n = 0;
-    for (const Shared& s : shared) n += Hkv * s.row_tiles * ceil_div(s.tiles, c);
-    const int64_t cost = ceil_div(n, pairs) * (c + kPieceTiles);
-    if (best == 0 || cost < best) {
-      best = cost;
-      chunk = c;
+    const int64_t keys = (int64_t)prefix_pages[g] * ps;
+    for (int32_t b = b0; b < b1; ++b) {
+      const int64_t first_row = (int64_t)seq[b] - (d.mask == PKA_MASK_CAUSAL ? reqs[b].q_len - 1 : 0);
+      PKA_CHECK_ARG(keys <= first_row, "request %d: its first row sees %lld keys, the shared prefix has %lld", b,
+                    (long long)first_row, (long long)keys);
+    }
+    if (b1 - b0 >= 2 && keys > 0) {
+      saved += (b1 - b0 - 1) * keys * Hkv * 512;
+      most_rows = std::max(most_rows, (int64_t)(reqs[b1 - 1].q_start + reqs[b1 - 1].q_len - reqs[b0].q_start) * G);
     }
   }
-  std::vector<int32_t> pages(B, 0), chunks(B, 0);
-  for (const Shared& s : shared)
-    for (int32_t b = group_indptr[s.group]; b < group_indptr[s.group + 1]; ++b) {
-      pages[b] = prefix_pages[s.group];
-      chunks[b] = (int32_t)std::min<int64_t>(ceil_div(s.tiles, chunk), INT32_MAX);
-    }
+  p.min_shared_bytes = min_shared_bytes;
+  p.shared = saved > 0 && saved >= (min_shared_bytes >= 0 ? min_shared_bytes : kWorthBytes);
+  if (!p.shared) {
+    p.workspace_bytes = p.base.workspace_bytes;
+    p.partial_rows = p.base.partial_rows;
+    return PKA_OK;
+  }
+  PKA_CHECK_ARG(most_rows <= INT32_MAX, "a group has too many query rows");
+  p.tokens.assign((size_t)p.base.total_q, TokenStates{0, 0, 0, -1, 0, 0, 0, 0});
+  std::vector<int32_t> own_page(B, 0);
+  int64_t states = 0;
 
-  // ---- the requests' own keys, and where every state goes ----
-  const SharedPrefix behind{pages.data(), chunks.data()};
-  rc = build_decode_plan(p, d, seq, indptr, &behind);
-  if (rc != PKA_OK) return rc;
-  p.prefix_tokens.assign((size_t)p.total_q, PrefixToken{0, 0});
-  for (int32_t b = 0; b < B; ++b) {
-    const ReqInfo& r = p.reqs[b];
-    if (chunks[b] == 0) continue;
-    for (int32_t i = 0; i < r.q_len; ++i) p.prefix_tokens[r.q_start + i] = PrefixToken{r.part_base + i * Hq, r.q_len * Hq};
-  }
-  for (const Shared& s : shared) {
-    const int32_t b0 = group_indptr[s.group];
-    const int64_t n = ceil_div(s.tiles, chunk);
-    for (int64_t ci = 0; ci < n; ++ci)
+  // ---- the shared prefixes ----
+  int64_t total = 0, bytes = 0;
+  for (int pass = 0; pass < 2; ++pass) {   // the work, then its pieces
+    if (pass == 1) {
+      // A tile of 256 rows and 64 keys is 16.8 MFLOP, at 1900 TFLOP/s 8.8 ns of the GPU; where
+      // all of them take longer than the bytes, at 6.7 TB/s, the products bound the whole.
+      for (int32_t b = 0; b < B; ++b) bytes += (seq[b] - (int64_t)own_page[b] * ps) * Hkv * 512;
+      p.dense = (double)total * 8.8e-9 > (double)bytes / 6.7e12;
+    }
+    Dealer deal(total, std::max(1, p.dense ? d.num_sms : d.num_sms / 2), kMinPrefixTiles);
+    int64_t last_pair = -1;
+    for (int32_t g = 0; g < num_groups; ++g) {
+      const int32_t b0 = group_indptr[g], b1 = group_indptr[g + 1];
+      if (b1 - b0 < 2 || prefix_pages[g] == 0) continue;
+      const int32_t q0 = reqs[b0].q_start;
+      const int64_t rows = (int64_t)(reqs[b1 - 1].q_start + reqs[b1 - 1].q_len - q0) * G;
+      const int64_t keys = (int64_t)prefix_pages[g] * ps, tiles = ceil_div(keys, kPrefixTile);
+      const int64_t row_tiles = ceil_div(rows, kPrefixRows);
+      if (pass == 0) {
+        total += Hkv * tiles * row_tiles;
+        bytes += keys * Hkv * 512;
+        for (int32_t b = b0; b < b1; ++b) own_page[b] = prefix_pages[g];
+        continue;
+      }
+      for (int32_t b = b0; b < b1; ++b)
+        for (int32_t i = 0; i < reqs[b].q_len; ++i) {
+          TokenStates& t = p.tokens[reqs[b].q_start + i];
+          t.pre_row = (reqs[b].q_start + i - q0) * G;
+          t.pre_run = (int32_t)p.runs.size();
+          t.pre_tiles = (int32_t)row_tiles;
+        }
       for (int32_t hk = 0; hk < Hkv; ++hk)
-        for (int64_t rt = 0; rt < s.row_tiles; ++rt)
-          p.prefix_items.push_back(PrefixItem{b0, hk, (int32_t)(s.tiles * ci / n), (int32_t)(s.tiles * (ci + 1) / n),
-                                              prefix_pages[s.group] * ps, (int32_t)ci, p.reqs[b0].q_start,
-                                              (int32_t)s.rows, (int32_t)(rt * kPrefixRows), 0, 0, 0});
+        for (int64_t rt = 0; rt < row_tiles; ++rt) {
+          const int64_t here = std::min<int64_t>(kPrefixRows, rows - rt * kPrefixRows);
+          StateRun run{(int32_t)states, 0, (int32_t)here, 0};
+          for (int64_t t = 0; t < tiles; ++run.count) {
+            int64_t n = 0;
+            const int64_t pair = deal.take(tiles - t, &n);
+            for (; last_pair < pair; ++last_pair) p.pair_segments.push_back((int32_t)p.items.size());
+            PKA_CHECK_ARG(states + here <= INT32_MAX, "too many partial rows");
+            p.items.push_back(PrefixItem{b0, hk, (int32_t)t, (int32_t)(t + n), (int32_t)keys, q0, (int32_t)rows,
+                                         (int32_t)(rt * kPrefixRows), (int32_t)states, 0, 0, 0});
+            states += here;
+            t += n;
+          }
+          p.runs.push_back(run);
+        }
+    }
   }
-  PKA_CHECK_ARG(p.prefix_items.size() <= (size_t)INT32_MAX / 2, "too many pieces of prefixes");
+  p.pair_segments.push_back((int32_t)p.items.size());
+
+  // ---- the requests' own keys ----
+  const int64_t upp = ps / 16;
+  int64_t units = 0;
+  for (int32_t b = 0; b < B; ++b)
+    units += std::max<int64_t>(0, ceil_div(seq[b], 16) - own_page[b] * upp) * Hkv *
+             ceil_div((int64_t)G * reqs[b].q_len, kOwnRows);
+  const int64_t warps = (int64_t)d.num_sms * kOwnCtas * kOwnWarps;
+  const int64_t most = std::min(std::max(units * 2 / (3 * warps), kMinOwnUnits), kMaxOwnUnits);
+  for (int32_t b = 0; b < B; ++b) {
+    const int64_t u0 = own_page[b] * upp, u1 = ceil_div(seq[b], 16), rows = (int64_t)G * reqs[b].q_len;
+    const int64_t row_tiles = ceil_div(rows, kOwnRows), n = ceil_div(std::max<int64_t>(0, u1 - u0), most);
+    PKA_CHECK_ARG((int64_t)p.runs.size() + Hkv * row_tiles <= INT32_MAX, "too many row tiles");
+    for (int32_t i = 0; i < reqs[b].q_len; ++i) {
+      TokenStates& t = p.tokens[reqs[b].q_start + i];
+      t.own_row = i * G;
+      t.own_run = (int32_t)p.runs.size();
+      t.own_tiles = (int32_t)row_tiles;
+    }
+    for (int32_t hk = 0; hk < Hkv; ++hk)
+      for (int64_t rt = 0; rt < row_tiles; ++rt) {
+        const int64_t here = std::min<int64_t>(kOwnRows, rows - rt * kOwnRows);
+        p.runs.push_back(StateRun{(int32_t)states, (int32_t)n, (int32_t)here, 0});
+        PKA_CHECK_ARG(states + n * here <= INT32_MAX, "too many partial rows");
+        for (int64_t k = 0; k < n; ++k, states += here)
+          p.pieces.push_back(OwnPiece{b, hk | (int32_t)rt << 16, (int32_t)(u0 + (u1 - u0) * k / n),
+                                      (int32_t)(u0 + (u1 - u0) * (k + 1) / n), (int32_t)states, reqs[b].q_start,
+                                      reqs[b].q_len, reqs[b].kv_len});
+      }
+  }
+  // the longest first, equal ones in the order of the requests
+  std::stable_sort(p.pieces.begin(), p.pieces.end(), [](const OwnPiece& x, const OwnPiece& y) {
+    return x.unit_hi - x.unit_lo > y.unit_hi - y.unit_lo;
+  });
+  const int64_t n_pieces = (int64_t)p.pieces.size();
+  p.own_ctas = (int32_t)std::max<int64_t>(1, std::min<int64_t>((int64_t)d.num_sms * kOwnCtas, ceil_div(n_pieces, kOwnWarps)));
+  // CTAs that find no place beside the prefix kernel start late: they begin with what is left
+  p.own_static = (int32_t)std::min<int64_t>(n_pieces, std::min<int64_t>(p.own_ctas, d.num_sms) * kOwnWarps);
+  PKA_CHECK_ARG(p.items.size() < (size_t)INT32_MAX / 2 && p.pieces.size() < (size_t)INT32_MAX / 2, "too many pieces");
+  p.partial_rows = (int32_t)states;
+  p.ws_lse_offset = (int64_t)up256((size_t)states * 512);
+  p.workspace_bytes = p.ws_lse_offset + states * 4;
   return PKA_OK;
 }
 

@@ -49,7 +49,7 @@ def make(groups, *, heads, kv_heads, ps, q_lens=None, dtype=torch.bfloat16, seed
 
 def plan_of(c, **kw):
     a = dict(num_qo_heads=c["heads"], num_kv_heads=c["kv_heads"], page_size=c["ps"], max_pages_per_seq=c["width"],
-             num_pages=c["k"].shape[0], qo_indptr=c["qo"], scale=c["scale"], return_lse=True, dtype=c["dtype"])
+             num_pages=c["k"].shape[0], qo_indptr=c["qo"], scale=c["scale"], return_lse=True, dtype=c["dtype"], min_shared_bytes=0)
     a.update(kw)
     return api.paged_prefix_decode_plan(c["kv"], c["groups"], c["pre"], **a)
 
@@ -76,7 +76,7 @@ def close(got, want, v, dtype, out_dtype):
 
 def check(c, causal=False, out_dtype=None, sinks=None, bmm2_scale=1.0, plan=None, pieces=True, **kw):
     p = plan or plan_of(c, causal=causal, out_dtype=out_dtype, bmm2_scale=bmm2_scale)
-    assert (p.info["num_pieces"] > 0) == pieces
+    assert bool(p.info["shared"]) == pieces
     got = api.paged_prefix_decode_run(p, c["q"], c["k"], c["v"], table(c), sinks=sinks, **kw)
     p.check()
     want = ref.decode(c["q"], c["k"], c["v"], c["tables"], c["kv"], c["qo"], causal=causal, scale=c["scale"],
