@@ -1,14 +1,16 @@
 """ctypes declarations of the C ABI in ``include/pka.h``.
 
-Loads the in-tree ``_lib/libpka.so``; there is no fallback: if the library is
-missing or does not load, every call raises.
+Loads the in-tree ``_lib/libpka.so``, and the native part of the binding beside it; there
+is no fallback: if either is missing or does not load, every call raises.
 """
 
 import ctypes
+import importlib.util
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_lib", "libpka.so")
+BINDING_PATH = os.path.join(_HERE, "_lib", "_pka_binding.so")
 
 PKA_OK = 0
 PKA_ERR_INVALID_ARG = -1
@@ -252,3 +254,22 @@ def check(code, where):
     if code != PKA_OK:
         raise PkaError(code, where)
     return code
+
+
+_binding = None
+
+
+def binding():
+    """The native marshalling module ``_pka_binding``.  Raises if it is not built."""
+    global _binding
+    if _binding is None:
+        lib()
+        spec = importlib.util.spec_from_file_location("_pka_binding", BINDING_PATH)
+        if not os.path.exists(BINDING_PATH):
+            raise RuntimeError(
+                f"{BINDING_PATH} is missing: build it with `python -m paged_kv_attention_32_gb300.build`")
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.init(check)
+        _binding = module
+    return _binding

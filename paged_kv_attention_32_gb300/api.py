@@ -354,13 +354,13 @@ class PrefixDecodePlan:
     def _follow(self, desc, workspace_bytes):
         self.desc = desc
         self.workspace_bytes = workspace_bytes
-        # what every run compares its tensors with
-        self.dtype, self.out_dtype = _TORCH[desc.dtype], _TORCH[desc.out_dtype]
-        self.batch_size, self.table_width = desc.batch_size, desc.max_pages_per_seq
-        self.row = (desc.num_qo_heads, desc.head_dim)
-        self.pages_shape = (desc.num_pages, desc.num_kv_heads, desc.page_size, desc.head_dim)
-        self.return_lse = bool(desc.return_lse)
+        self.batch_size = desc.batch_size
         self.total_q = self.info["total_q"]
+        # what every run compares its tensors with
+        self.facts = (self.prefix_handle.value, self.total_q, desc.batch_size, desc.num_qo_heads,
+                      desc.head_dim, desc.num_pages, desc.num_kv_heads, desc.page_size,
+                      desc.max_pages_per_seq, desc.dtype, desc.out_dtype, desc.return_lse,
+                      workspace_bytes)
 
     @property
     def info(self):
@@ -464,62 +464,8 @@ def paged_prefix_decode_run(plan, q, k_pages, v_pages, block_tables, seq_lens_kv
                                            workspace=workspace)
     if not isinstance(plan, PrefixDecodePlan):
         raise ValueError("the plan was not made by paged_prefix_decode_plan")
-    dev = torch.cuda.current_device()
-    if not _fits(plan.dtype, dev, q, k_pages, v_pages):
-        _check_tensors(plan.dtype, q=q, k_pages=k_pages, v_pages=v_pages)
-    if not _fits(torch.int32, dev, block_tables, seq_lens_kv):
-        _check_tensors(torch.int32, block_tables=block_tables, seq_lens_kv=seq_lens_kv)
-    need, B, shape = plan.total_q, plan.batch_size, q.shape
-    if len(shape) != 3 or shape[1:] != plan.row or shape[0] < need:
-        raise ValueError(f"q must be [>= {need}, {plan.row[0]}, {plan.row[1]}], got {tuple(shape)}")
-    T = shape[0]
-    q_tok, q_head, q_col = q.stride()
-    if q_col != 1:
-        raise ValueError("q must have a dense last dimension")
-    if k_pages.shape != plan.pages_shape:
-        raise ValueError(f"the pools must be {list(plan.pages_shape)}, got {tuple(k_pages.shape)}")
-    _, _, _, page_stride, head_stride = _page_strides(k_pages, v_pages)
-    if block_tables.dim() != 2 or block_tables.shape[0] < B or \
-            block_tables.shape[1] < plan.table_width or block_tables.stride(1) != 1:
-        raise ValueError("block_tables needs dense rows, one of at least max_pages_per_seq "
-                         "entries per request")
-    row, width = block_tables.stride(0), block_tables.shape[1]
-    if seq_lens_kv is not None and (seq_lens_kv.numel() < B or not seq_lens_kv.is_contiguous()):
-        raise ValueError("seq_lens_kv needs one contiguous entry per request")
-    if sinks is not None:
-        _check_tensors(torch.float32, sinks=sinks)
-        if sinks.numel() != plan.row[0] or not sinks.is_contiguous():
-            raise ValueError("sinks needs one contiguous entry per query head")
-    if out is None:
-        out = torch.empty((T,) + plan.row, dtype=plan.out_dtype, device=q.device)
-    else:
-        _check_tensors(plan.out_dtype, out=out)
-        _contiguous(out=out)
-        if out.dim() != 3 or out.shape[1:] != plan.row or out.shape[0] < need:
-            raise ValueError("out must be [T, num_qo_heads, head_dim]")
-    if lse is not None:
-        _check_tensors(torch.float32, lse=lse)
-        _contiguous(lse=lse)
-        if lse.dim() != 2 or lse.shape[1] != plan.row[0] or lse.shape[0] < need:
-            raise ValueError("lse must be [T, num_qo_heads]")
-    elif plan.return_lse:
-        lse = torch.empty((T, plan.row[0]), dtype=torch.float32, device=q.device)
-    ws_bytes = 0
-    if workspace is not None:
-        _check_tensors(workspace.dtype, workspace=workspace)
-        _contiguous(workspace=workspace)
-        ws_bytes = workspace.numel() * workspace.element_size()
-    elif plan.workspace_bytes > 0:
-        ws_bytes = plan.workspace_bytes
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
-    rc = L.lib().paged_prefix_decode_run(
-        plan.prefix_handle, q.data_ptr(), q_tok, q_head, k_pages.data_ptr(), v_pages.data_ptr(),
-        page_stride, head_stride, block_tables.data_ptr(),
-        row if B > 1 or row > width else width, _ptr(seq_lens_kv), _ptr(sinks), out.data_ptr(),
-        _ptr(lse), _ptr(workspace), ws_bytes, torch._C._cuda_getCurrentRawStream(dev))
-    if rc:
-        L.check(rc, "paged_prefix_decode_run")
-    return (out, lse) if plan.return_lse else out
+    return L.binding().prefix_decode_run(plan.facts, q, k_pages, v_pages, block_tables, seq_lens_kv,
+                                         sinks, out, lse, workspace)
 
 
 def attn_merge_lse(v_states, s_states, out_dtype=torch.bfloat16, v_out=None, s_out=None,
@@ -815,20 +761,7 @@ def paged_latent_append(latent, rope, slot_map, pages, status=None, stream=None)
     return pages
 
 
-def _page_strides(k_pages, v_pages):
-    """(pages, KV heads, page size, page stride, head stride) of a pair of HND pools."""
-    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape or v_pages.stride() != k_pages.stride():
-        raise ValueError("k_pages and v_pages must be [num_pages, num_kv_heads, page_size, head_dim] "
-                         "with the same strides")
-    n, heads, ps, dim = k_pages.shape
-    page, head, slot, col = k_pages.stride()
-    if col != 1 or slot != dim:
-        raise ValueError("each page's slots must be dense rows of head_dim elements")
-    return n, heads, ps, page, head
-
-
 _ROPE_PAIRS = {"halves": L.PKA_ROPE_HALVES, "neighbours": L.PKA_ROPE_NEIGHBOURS}
-_I32x4 = ctypes.c_int32 * 4
 
 
 def paged_rope_append(k, v, slot_map, k_pages, v_pages, q=None, positions=None, inv_freq=None,
@@ -847,98 +780,10 @@ def paged_rope_append(k, v, slot_map, k_pages, v_pages, q=None, positions=None, 
             return paged_rope_append(k, v, slot_map, k_pages, v_pages, q=q, positions=positions,
                                      inv_freq=inv_freq, sections=sections, pairs=pairs,
                                      q_out=q_out, status=status)
-    dtype = k_pages.dtype
-    if dtype is not torch.bfloat16 and dtype is not torch.float16:
-        raise ValueError(f"the pools must be bfloat16 or float16, got {dtype}")
-    dev = torch.cuda.current_device()
-    if not _fits(dtype, dev, k, v, k_pages, v_pages, q, q_out):
-        _check_tensors(dtype, k=k, v=v, k_pages=k_pages, v_pages=v_pages, q=q, q_out=q_out)
-    if not _fits(torch.int64, dev, slot_map):
-        _check_tensors(torch.int64, slot_map=slot_map)
-    if not _fits(torch.int32, dev, positions, status):
-        _check_tensors(torch.int32, positions=positions, status=status)
-    n_pages, heads, ps, page_stride, head_stride = _page_strides(k_pages, v_pages)
-    shape = k.shape
-    if len(shape) != 3 or shape[1] != heads or shape[2] != k_pages.shape[3] or v.shape != shape:
-        raise ValueError(f"k and v must be [T, {heads}, {k_pages.shape[3]}], got {tuple(shape)} "
-                         f"and {tuple(v.shape)}")
-    T, _, D = shape
-    k_tok, k_head, k_col = k.stride()
-    if T and (k_col != 1 or v.stride() != k.stride()):
-        raise ValueError("k and v must have the same strides and a dense last dimension")
-    if slot_map.numel() != T or not slot_map.is_contiguous():
-        raise ValueError("slot_map needs one contiguous entry per token")
-    Hq = q_tok = q_head = o_tok = o_head = 0
-    if q is not None:
-        if q.dim() != 3 or q.shape[0] != T or q.shape[2] != D or (T and q.stride(2) != 1):
-            raise ValueError(f"q must be [{T}, Hq, {D}] with a dense last dimension")
-        Hq = q.shape[1]
-        q_tok, q_head, _ = q.stride()
-        if q_out is None:
-            q_out = torch.empty((T, Hq, D), dtype=dtype, device=q.device)
-        elif q_out.shape != q.shape or q_out.stride(2) != 1:
-            raise ValueError("q_out must have the shape of q and a dense last dimension")
-        o_tok, o_head, _ = q_out.stride()
-    elif q_out is not None:
-        raise ValueError("q_out without q")
     if pairs not in _ROPE_PAIRS:
         raise ValueError(f"pairs must be 'halves' or 'neighbours', got {pairs!r}")
-    half = axes = pos_stride = 0
-    sec = None
-    if inv_freq is not None:
-        if not _fits(torch.float64, dev, inv_freq):
-            _check_tensors(torch.float64, inv_freq=inv_freq)
-        if not inv_freq.is_contiguous():
-            raise ValueError("inv_freq must be contiguous")
-        half = inv_freq.numel()
-        if positions is None:
-            raise ValueError("a rotation needs positions")
-        axes = 1 if positions.dim() == 1 else positions.shape[0]
-        if positions.dim() > 2 or positions.shape[-1] != T or (T and positions.stride(-1) != 1):
-            raise ValueError(f"positions must be [axes, {T}] or [{T}] with dense rows")
-        pos_stride = positions.stride(0) if axes > 1 else T
-        if sections is None:
-            sections = (half,)
-        if not 1 <= axes <= 4 or len(sections) > axes:
-            raise ValueError("positions need 1 to 4 axes, one for each of the sections")
-        sec = _I32x4(*sections)
-    elif positions is not None or sections is not None:
-        raise ValueError("positions and sections go with inv_freq")
-    rc = L.lib().paged_rope_append(
-        _ptr(q) if Hq else None, q_tok, q_head, _ptr(q_out) if Hq else None, o_tok, o_head, Hq,
-        k.data_ptr(), v.data_ptr(), k_tok, k_head, heads, D, _ptr(positions), pos_stride,
-        _ptr(inv_freq), 2 * half, axes, sec, _ROPE_PAIRS[pairs], slot_map.data_ptr(), T,
-        k_pages.data_ptr(), v_pages.data_ptr(), n_pages, ps, page_stride, head_stride,
-        _DTYPES[dtype], _ptr(status), torch._C._cuda_getCurrentRawStream(dev))
-    if rc:
-        L.check(rc, "paged_rope_append")
-    return q_out
-
-
-def _tables_of(kv_lens, block_tables):
-    """(rows, width, row stride) of the tables, one row per entry of kv_lens."""
-    B = kv_lens.numel()
-    if block_tables.dim() != 2 or block_tables.shape[0] != B or not kv_lens.is_contiguous():
-        raise ValueError("block_tables must have one row per request, kv_lens be contiguous")
-    width = block_tables.shape[1]
-    row, col = block_tables.stride()
-    if col != 1:
-        raise ValueError("block_tables rows must be dense")
-    return B, width, row if B > 1 or row > width else width   # one row's stride says nothing
-
-
-def _out_i32(name, t, like, n):
-    """An int32 output of ``n`` entries: the given one, checked, or a new one."""
-    if t is None:
-        return like.new_empty(n)
-    if t.numel() != n or not t.is_contiguous():
-        raise ValueError(f"{name} must hold {n} contiguous entries")
-    return t
-
-
-def _one_head(free_head, free_pages):
-    if free_head.numel() != 1 or not free_pages.is_contiguous():
-        raise ValueError("free_head must hold one entry, free_pages be contiguous")
+    return L.binding().rope_append(k, v, slot_map, k_pages, v_pages, q, positions, inv_freq,
+                                   sections, _ROPE_PAIRS[pairs], q_out, status)
 
 
 KvFork = namedtuple("KvFork", "seq_lens src_pages dst_pages free_head")
@@ -957,30 +802,9 @@ def paged_kv_fork(parents, children, kv_lens, free_pages, free_head, block_table
             return paged_kv_fork(parents, children, kv_lens, free_pages, free_head, block_tables,
                                  page_size=page_size, seq_lens=seq_lens, src_pages=src_pages,
                                  dst_pages=dst_pages, free_head_out=free_head_out, status=status)
-    dev = torch.cuda.current_device()
-    if not _fits(torch.int32, dev, parents, children, kv_lens, free_pages, free_head, block_tables,
-                 seq_lens, src_pages, dst_pages, free_head_out, status):
-        _check_tensors(torch.int32, parents=parents, children=children, kv_lens=kv_lens,
-                       free_pages=free_pages, free_head=free_head, block_tables=block_tables,
-                       seq_lens=seq_lens, src_pages=src_pages, dst_pages=dst_pages,
-                       free_head_out=free_head_out, status=status)
-    B, width, row = _tables_of(kv_lens, block_tables)
-    _one_head(free_head, free_pages)
-    n = parents.numel()
-    if children.numel() != n or not (parents.is_contiguous() and children.is_contiguous()):
-        raise ValueError("parents and children must be contiguous, one child per parent")
-    seq_lens = _out_i32("seq_lens", seq_lens, kv_lens, B)
-    src_pages = _out_i32("src_pages", src_pages, kv_lens, n)
-    dst_pages = _out_i32("dst_pages", dst_pages, kv_lens, n)
-    free_head_out = _out_i32("free_head_out", free_head_out, kv_lens, 1)
-    rc = L.lib().paged_kv_fork(
-        parents.data_ptr(), children.data_ptr(), n, kv_lens.data_ptr(), B, free_pages.data_ptr(),
-        free_pages.numel(), free_head.data_ptr(), page_size, block_tables.data_ptr(), row, width,
-        seq_lens.data_ptr(), src_pages.data_ptr(), dst_pages.data_ptr(), free_head_out.data_ptr(),
-        _ptr(status), torch._C._cuda_getCurrentRawStream(dev))
-    if rc:
-        L.check(rc, "paged_kv_fork")
-    return KvFork(seq_lens, src_pages, dst_pages, free_head_out)
+    return KvFork._make(L.binding().kv_fork(
+        parents, children, kv_lens, free_pages, free_head, block_tables, page_size, seq_lens,
+        src_pages, dst_pages, free_head_out, status))
 
 
 KvFree = namedtuple("KvFree", "seq_lens free_head")
@@ -996,26 +820,9 @@ def paged_kv_free(rows, kv_lens, free_pages, free_head, block_tables, *, page_si
             return paged_kv_free(rows, kv_lens, free_pages, free_head, block_tables,
                                  page_size=page_size, num_pages=num_pages, seq_lens=seq_lens,
                                  free_head_out=free_head_out, status=status)
-    dev = torch.cuda.current_device()
-    if not _fits(torch.int32, dev, rows, kv_lens, free_pages, free_head, block_tables, seq_lens,
-                 free_head_out, status):
-        _check_tensors(torch.int32, rows=rows, kv_lens=kv_lens, free_pages=free_pages,
-                       free_head=free_head, block_tables=block_tables, seq_lens=seq_lens,
-                       free_head_out=free_head_out, status=status)
-    B, width, row = _tables_of(kv_lens, block_tables)
-    _one_head(free_head, free_pages)
-    if not rows.is_contiguous():
-        raise ValueError("rows must be contiguous")
-    seq_lens = _out_i32("seq_lens", seq_lens, kv_lens, B)
-    free_head_out = _out_i32("free_head_out", free_head_out, kv_lens, 1)
-    rc = L.lib().paged_kv_free(
-        rows.data_ptr(), rows.numel(), kv_lens.data_ptr(), B, free_pages.data_ptr(),
-        free_pages.numel(), free_head.data_ptr(), page_size, block_tables.data_ptr(), row, width,
-        num_pages, seq_lens.data_ptr(), free_head_out.data_ptr(), _ptr(status),
-        torch._C._cuda_getCurrentRawStream(dev))
-    if rc:
-        L.check(rc, "paged_kv_free")
-    return KvFree(seq_lens, free_head_out)
+    return KvFree._make(L.binding().kv_free(
+        rows, kv_lens, free_pages, free_head, block_tables, page_size, num_pages, seq_lens,
+        free_head_out, status))
 
 
 KvCompaction = namedtuple("KvCompaction", "block_tables free_pages src_pages dst_pages num_moves")
@@ -1036,35 +843,9 @@ def paged_kv_compact(kv_lens, free_pages, free_head, block_tables, *, page_size,
                                     block_tables_out=block_tables_out,
                                     free_pages_out=free_pages_out, src_pages=src_pages,
                                     dst_pages=dst_pages, num_moves=num_moves, status=status)
-    dev = torch.cuda.current_device()
-    if not _fits(torch.int32, dev, kv_lens, free_pages, free_head, block_tables, block_tables_out,
-                 free_pages_out, src_pages, dst_pages, num_moves, status):
-        _check_tensors(torch.int32, kv_lens=kv_lens, free_pages=free_pages, free_head=free_head,
-                       block_tables=block_tables, block_tables_out=block_tables_out,
-                       free_pages_out=free_pages_out, src_pages=src_pages, dst_pages=dst_pages,
-                       num_moves=num_moves, status=status)
-    B, width, row = _tables_of(kv_lens, block_tables)
-    _one_head(free_head, free_pages)
-    if block_tables_out is None:
-        block_tables_out, out_row = kv_lens.new_empty((B, width)), width
-    else:
-        if block_tables_out.shape != block_tables.shape:
-            raise ValueError("block_tables_out must have the shape of block_tables")
-        out_row = _tables_of(kv_lens, block_tables_out)[2]
-    n = free_pages.numel()
-    free_pages_out = _out_i32("free_pages_out", free_pages_out, kv_lens, n)
-    most = min(n, num_pages) if src_pages is None else src_pages.numel()
-    src_pages = _out_i32("src_pages", src_pages, kv_lens, most)
-    dst_pages = _out_i32("dst_pages", dst_pages, kv_lens, most)
-    num_moves = _out_i32("num_moves", num_moves, kv_lens, 1)
-    rc = L.lib().paged_kv_compact(
-        kv_lens.data_ptr(), B, free_pages.data_ptr(), n, free_head.data_ptr(), page_size,
-        block_tables.data_ptr(), row, width, num_pages, block_tables_out.data_ptr(), out_row,
-        free_pages_out.data_ptr(), src_pages.data_ptr(), dst_pages.data_ptr(), most,
-        num_moves.data_ptr(), _ptr(status), torch._C._cuda_getCurrentRawStream(dev))
-    if rc:
-        L.check(rc, "paged_kv_compact")
-    return KvCompaction(block_tables_out, free_pages_out, src_pages, dst_pages, num_moves)
+    return KvCompaction._make(L.binding().kv_compact(
+        kv_lens, free_pages, free_head, block_tables, page_size, num_pages, block_tables_out,
+        free_pages_out, src_pages, dst_pages, num_moves, status))
 
 
 class KvPools:
@@ -1089,7 +870,8 @@ class KvPools:
         self.c = ((ctypes.c_void_p * n)(*(t.data_ptr() for t in self.pools)),
                   (ctypes.c_int64 * n)(*(t.stride(0) * t.element_size() if self.num_pages > 1 else s
                                          for t, s in zip(self.pools, size))),
-                  (ctypes.c_int64 * n)(*size), n, self.num_pages)
+                  (ctypes.c_int64 * n)(*size))
+        self.facts = tuple(ctypes.addressof(x) for x in self.c) + (n, self.num_pages, self.device)
 
 
 def paged_kv_copy(pools, src_pages, dst_pages, count=None, status=None, stream=None):
@@ -1101,21 +883,7 @@ def paged_kv_copy(pools, src_pages, dst_pages, count=None, status=None, stream=N
             return paged_kv_copy(pools, src_pages, dst_pages, count=count, status=status)
     if not isinstance(pools, KvPools):
         pools = KvPools(pools)
-    dev = torch.cuda.current_device()
-    if not _fits(torch.int32, dev, src_pages, dst_pages, count, status):
-        _check_tensors(torch.int32, src_pages=src_pages, dst_pages=dst_pages, count=count,
-                       status=status)
-    if pools.device != dev:
-        raise ValueError(f"the pools are on cuda:{pools.device}, the current device is cuda:{dev}")
-    n = src_pages.numel()
-    if dst_pages.numel() != n or not (src_pages.is_contiguous() and dst_pages.is_contiguous()):
-        raise ValueError("src_pages and dst_pages must be contiguous, one of each per entry")
-    if count is not None and count.numel() != 1:
-        raise ValueError("count must hold one entry")
-    rc = L.lib().paged_kv_copy(*pools.c, src_pages.data_ptr(), dst_pages.data_ptr(), n, _ptr(count),
-                               _ptr(status), torch._C._cuda_getCurrentRawStream(dev))
-    if rc:
-        L.check(rc, "paged_kv_copy")
+    L.binding().kv_copy(*pools.facts, src_pages, dst_pages, count, status)
 
 
 class LatentDecodePlan:
