@@ -246,17 +246,21 @@ prefix_kernel(const __grid_constant__ PrefixArgs a, const __grid_constant__ CUte
       const int64_t src = r < it.rows ? (int64_t)(it.q_start + r / a.group) * a.q_stride_tok +
                                             (int64_t)(it.kv_head * a.group + r % a.group) * a.q_stride_head
                                       : -1;
-#pragma unroll 4
+uint4 v[16];   // all asked for at once
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const int64_t at = __shfl_sync(0xffffffffu, src, 2 * k + (lane >> 4));
+        v[k] = make_uint4(0u, 0u, 0u, 0u);
+        if (at >= 0) v[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at) + (lane & 15));
+      }
+#pragma unroll
       for (int k = 0; k < 16; ++k) {
         const int rr = 2 * k + (lane >> 4), c = lane & 15;
-        const int64_t at = __shfl_sync(0xffffffffu, src, rr);
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (at >= 0) v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at) + c);
-        v.x ^= a.negate;
-        v.y ^= a.negate;
-        v.z ^= a.negate;
-        v.w ^= a.negate;
-        *reinterpret_cast<uint4*>(smem + (uint32_t)(c >> 3) * kQBox + swz128((uint32_t)(warp * 32 + rr), (uint32_t)(c & 7))) = v;
+        v[k].x ^= a.negate;
+        v[k].y ^= a.negate;
+        v[k].z ^= a.negate;
+        v[k].w ^= a.negate;
+        *reinterpret_cast<uint4*>(smem + (uint32_t)(c >> 3) * kQBox + swz128((uint32_t)(warp * 32 + rr), (uint32_t)(c & 7))) = v[k];
       }
       fence_proxy_async_smem();
       __syncwarp();

@@ -25,13 +25,17 @@ constexpr int64_t kWorthBytes = 48 << 20;
 constexpr int64_t kMinPrefixTiles = 3;   // a piece is no shorter, its row tile's keys allowing
 constexpr int64_t kMinOwnUnits = 6, kMaxOwnUnits = 16;   // of 16 keys, in a piece of a request
 
-// Cuts runs of work laid end to end into `parts` even shares.
+// Cuts runs of work laid end to end into `parts` shares: even ones, or, with `skewed`, 17 to 15
+// between the first half of the parts and the second.  Of two CTAs of the prefix kernel that
+// share an SM the one that started first gets the tensor core more often (65536 keys, 1024 rows
+// of 8 heads: even shares end after 180 and 213 us).
 class Dealer {
  public:
-  Dealer(int64_t total, int64_t parts, int64_t least) : total_(total), parts_(parts), least_(least) {}
+  Dealer(int64_t total, int64_t parts, int64_t least, bool skewed)
+      : total_(total), parts_(parts), least_(least), half_(skewed ? parts / 2 : 0) {}
   // The share that takes the next piece of a run of `left` units, and how many of them.
   int64_t take(int64_t left, int64_t* units) {
-    auto room = [&] { return (part_ + 1) * total_ / parts_ - done_; };
+    auto room = [&] { return total_ * upto(part_ + 1) / upto(parts_) - done_; };
     while (room() < std::min(least_, left) && part_ + 1 < parts_) ++part_;
     int64_t n = part_ + 1 == parts_ ? left : std::min(left, std::max(room(), std::min(least_, left)));
     if (left - n < least_) n = left;
@@ -41,7 +45,8 @@ class Dealer {
   }
 
  private:
-  int64_t total_, parts_, least_, part_ = 0, done_ = 0;
+  int64_t upto(int64_t part) const { return part <= half_ ? 17 * part : 15 * part + 2 * half_; }
+  int64_t total_, parts_, least_, half_, part_ = 0, done_ = 0;
 };
 
 }  // namespace
@@ -101,7 +106,7 @@ int build_prefix_plan(pka_prefix_plan& p, const pka_decode_desc& d_in, const int
       for (int32_t b = 0; b < B; ++b) bytes += (seq[b] - (int64_t)own_page[b] * ps) * Hkv * 512;
       p.dense = (double)total * 8.8e-9 > (double)bytes / 6.7e12;
     }
-    Dealer deal(total, std::max(1, p.dense ? d.num_sms : d.num_sms / 2), kMinPrefixTiles);
+    Dealer deal(total, std::max(1, p.dense ? d.num_sms : d.num_sms / 2), kMinPrefixTiles, p.dense);
     int64_t last_pair = -1;
     for (int32_t g = 0; g < num_groups; ++g) {
       const int32_t b0 = group_indptr[g], b1 = group_indptr[g + 1];
