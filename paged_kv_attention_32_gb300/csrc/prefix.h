@@ -62,8 +62,8 @@ struct PrefixArgs {
   int64_t q_stride_tok, q_stride_head;
   const int32_t* block_tables;
   int64_t bt_row_stride;
-  const PrefixItem* items;
-  const int32_t* segments;       // [pairs + 1]: each pair's first item
+  const PrefixItem* items;       // the first of each pair, then the further ones by pair
+  const int32_t* more;           // [pairs + 1]: where each pair's further items begin, then their end
   float* ws_o;                   // fp32 partial outputs [partial_rows, 128]
   float* ws_lse;                 // fp32 partial base-2 LSEs [partial_rows]
   int32_t* status;
@@ -119,19 +119,19 @@ struct pka_prefix_plan {
   int32_t partial_rows = 0;
   int64_t workspace_bytes = 0, ws_lse_offset = 0;
   std::vector<pka::PrefixItem> items;
-  std::vector<int32_t> pair_segments;
+  std::vector<int32_t> more;
   int32_t own_ctas = 0, own_static = 0;
   std::vector<pka::OwnPiece> pieces;
   std::vector<pka::StateRun> runs;
   std::vector<pka::TokenStates> tokens;
-  // one device allocation: items | pieces | runs | tokens | segments | status word, count
+  // one device allocation: items | pieces | runs | tokens | more | status word, count
   void* dev_buf = nullptr;
   size_t capacity = 0;         // of dev_buf and of host_stage
   const pka::PrefixItem* d_items = nullptr;
   const pka::OwnPiece* d_pieces = nullptr;
   const pka::StateRun* d_runs = nullptr;
   const pka::TokenStates* d_tokens = nullptr;
-  const int32_t* d_pair_segments = nullptr;
+  const int32_t* d_more = nullptr;
   int32_t* d_status = nullptr;   // with the count of pieces taken behind it
   int device = -1;
   // pinned host image of dev_buf; stage_done marks when its last upload has read it

@@ -22,10 +22,10 @@ int install_prefix_plan(pka_prefix_plan& p, pka_prefix_plan&& next, cudaStream_t
                          next.pieces.size() * sizeof(OwnPiece),
                          next.runs.size() * sizeof(StateRun),
                          next.tokens.size() * sizeof(TokenStates),
-                         next.pair_segments.size() * sizeof(int32_t),
+                         next.more.size() * sizeof(int32_t),
                          256};
   const void* from[] = {next.items.data(), next.pieces.data(), next.runs.data(), next.tokens.data(),
-                        next.pair_segments.data()};
+                        next.more.data()};
   size_t off[6], total = 0;
   for (int i = 0; i < 6; ++i) {
     off[i] = total;
@@ -56,7 +56,7 @@ int install_prefix_plan(pka_prefix_plan& p, pka_prefix_plan&& next, cudaStream_t
   next.d_pieces = reinterpret_cast<const OwnPiece*>(base + off[1]);
   next.d_runs = reinterpret_cast<const StateRun*>(base + off[2]);
   next.d_tokens = reinterpret_cast<const TokenStates*>(base + off[3]);
-  next.d_pair_segments = reinterpret_cast<const int32_t*>(base + off[4]);
+  next.d_more = reinterpret_cast<const int32_t*>(base + off[4]);
   next.d_status = reinterpret_cast<int32_t*>(base + off[5]);
   uint8_t* img = static_cast<uint8_t*>(next.host_stage);
   for (int i = 0; i < 5; ++i)
@@ -196,7 +196,7 @@ int paged_prefix_decode_plan_info(const pka_prefix_plan* p, pka_prefix_plan_info
   info->shared = p->shared;
   info->num_prefix_pieces = (int32_t)p->items.size();
   info->num_own_pieces = (int32_t)p->pieces.size();
-  info->num_pairs = p->shared ? (int32_t)p->pair_segments.size() - 1 : 0;
+  info->num_pairs = p->shared ? (int32_t)p->more.size() - 1 : 0;
   info->num_warps = p->shared ? p->own_ctas * kOwnWarps : 0;
   info->dense = p->shared && p->dense;
   info->partial_rows = p->partial_rows;
@@ -283,11 +283,11 @@ int paged_prefix_decode_run(const pka_prefix_plan* p, const void* q, int64_t q_s
   x.block_tables = block_tables;
   x.bt_row_stride = bt_row_stride;
   x.items = p->d_items;
-  x.segments = p->d_pair_segments;
+  x.more = p->d_more;
   x.ws_o = ws_o;
   x.ws_lse = ws_lse;
   x.status = p->d_status;
-  x.num_pairs = (int32_t)p->pair_segments.size() - 1;
+  x.num_pairs = (int32_t)p->more.size() - 1;
   x.group = base.G;
   x.page_units = base.ps / 16;
   x.k_rows = k_rows;

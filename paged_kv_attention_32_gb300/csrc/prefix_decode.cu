@@ -108,9 +108,32 @@ prefix_kernel(const __grid_constant__ PrefixArgs a, const __grid_constant__ CUte
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_rank();   // 0: the leader
   const int pair = blockIdx.x >> 1;
+  // the other kernel's CTAs may start; the merge behind it waits for this grid's end
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
+  // A pair's first piece lies at its own index, so that its loads need not wait for the
+  // list's; the others one behind the other from more0 on.
+  const int mine = (int)rank * kTileQ + (tid & (kTileQ - 1));   // softmax: the thread's row of a piece
+  uint4 rows[16];   // two lanes' worth of a warp's 32 query rows, 16 bytes each
+  // asks for the query rows of a piece, two at a time, 16 lanes a row; zeros where there is none
+  auto ask_rows = [&](int i) {
+    const PrefixItem it = a.items[i];
+    const int r = it.row0 + mine;
+    const int64_t src = r < it.rows ? (int64_t)(it.q_start + r / a.group) * a.q_stride_tok +
+                                          (int64_t)(it.kv_head * a.group + r % a.group) * a.q_stride_head
+                                    : -1;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const int64_t at = __shfl_sync(0xffffffffu, src, 2 * k + (lane >> 4));
+      rows[k] = make_uint4(0u, 0u, 0u, 0u);
+      if (at >= 0) rows[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at) + (lane & 15));
+    }
+  };
+  // The first ones before anything else: behind the first keys and values of all CTAs they
+  // would wait 5 us for memory.
+  if (warp < 4) ask_rows(pair);
   if (tid == 0) {   // the list comes in while the pair sets up
-    ask_line(a.segments + pair);
+    ask_line(a.more + pair);
     mbar_init(bar(Gm::kQFull), 8);   // the pair's softmax warps
     mbar_init(bar(Gm::kOFree), 8);
     mbar_init(bar(Gm::kMmaDone), 1);
@@ -135,10 +158,10 @@ prefix_kernel(const __grid_constant__ PrefixArgs a, const __grid_constant__ CUte
   cluster_wait();   // both CTAs' barriers stand before anyone arrives on them
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  // the other kernel's CTAs may start; the merge behind it waits for this grid's end
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  const int first = __ldg(a.segments + pair), end = __ldg(a.segments + pair + 1);
+  const int more0 = __ldg(a.more + pair);
+  const int n_items = 1 + __ldg(a.more + pair + 1) - more0;
+  auto index = [&](int i) -> int { return i == 0 ? pair : more0 + i - 1; };
   if (warp == 4 || warp == 6) {
     // ---------------- producers: one lane per copy of a tile ----------------
     const bool is_v = warp == 6;
@@ -154,8 +177,9 @@ prefix_kernel(const __grid_constant__ PrefixArgs a, const __grid_constant__ CUte
     RingPos<kStages> pos;
     int filled = 0;
     bool ok = true;
-    for (int i = first; ok && i < end; ++i) {
-      const PrefixItem it = a.items[i];
+    PrefixItem it = a.items[pair];
+    for (int i = 0; ok && i < n_items; ++i) {
+      const PrefixItem behind = a.items[i + 1 < n_items ? index(i + 1) : pair];
       const int32_t* row = a.block_tables + (int64_t)it.row * a.bt_row_stride;
       const int units = it.keys / 16, n_kv = it.tile_hi - it.tile_lo;
       // page of this lane's unit of tile j: past the prefix one past the pool, which reads as zeros
@@ -180,6 +204,7 @@ prefix_kernel(const __grid_constant__ PrefixArgs a, const __grid_constant__ CUte
         pos.next();
         ++filled;
       }
+      it = behind;
     }
     // When a wait gave up, copies still in flight land before the cluster leaves:
     // their barriers may be the other CTA's, so there is only time to go by.
@@ -194,8 +219,8 @@ prefix_kernel(const __grid_constant__ PrefixArgs a, const __grid_constant__ CUte
       RingPos<kStages> kp, vp;
       RingPos<kScores> sp, pp;   // the next S to issue and the next P to wait for
       bool ok = true;
-      for (int i = first; ok && i < end; ++i) {
-        const int n_kv = __ldg(&a.items[i].tile_hi) - __ldg(&a.items[i].tile_lo);
+      for (int i = 0; ok && i < n_items; ++i) {
+        const int n_kv = __ldg(&a.items[index(i)].tile_hi) - __ldg(&a.items[index(i)].tile_lo);
         auto issue_qk = [&]() -> bool {   // S of the next key tile into the next buffer
           if (!warp_wait(bar(Gm::kKFull + kp.slot), kp.parity, a.status)) return false;
           tc_fence_after();
@@ -213,12 +238,12 @@ prefix_kernel(const __grid_constant__ PrefixArgs a, const __grid_constant__ CUte
           return true;
         };
         // queries: ordinary writes, of the other CTA too
-        ok = warp_wait<true>(bar(Gm::kQFull), (uint32_t)((i - first) & 1), a.status);
+        ok = warp_wait<true>(bar(Gm::kQFull), (uint32_t)(i & 1), a.status);
         for (int j = 0; ok && j < n_kv && j < kScores; ++j) ok = issue_qk();
         for (int j = 0; ok && j < n_kv; ++j) {
           ok = warp_wait(bar(Gm::kVFull + vp.slot), vp.parity, a.status) &&
                warp_wait(bar(Gm::kPFull + pp.slot), pp.parity, a.status);
-          if (ok && j == 0 && i > first) ok = warp_wait(bar(Gm::kOFree), (uint32_t)((i - first - 1) & 1), a.status);
+          if (ok && j == 0 && i > 0) ok = warp_wait(bar(Gm::kOFree), (uint32_t)((i - 1) & 1), a.status);
           if (!ok) break;
           tc_fence_after();
           // 4 k-steps of 16 keys: P columns +8, V rows +16 (2048 bytes)
@@ -237,30 +262,16 @@ prefix_kernel(const __grid_constant__ PrefixArgs a, const __grid_constant__ CUte
     }
   } else {
     // ---------------- softmax: one thread per query row ----------------
-    const int mine = (int)rank * kTileQ + tid;
-    // the query rows of a piece into shared memory, two at a time, 16 lanes a row; zeros
-    // where there is none
-    auto gather = [&](int i) {
-      const PrefixItem it = a.items[i];
-      const int r = it.row0 + mine;
-      const int64_t src = r < it.rows ? (int64_t)(it.q_start + r / a.group) * a.q_stride_tok +
-                                            (int64_t)(it.kv_head * a.group + r % a.group) * a.q_stride_head
-                                      : -1;
-uint4 v[16];   // all asked for at once
-#pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        const int64_t at = __shfl_sync(0xffffffffu, src, 2 * k + (lane >> 4));
-        v[k] = make_uint4(0u, 0u, 0u, 0u);
-        if (at >= 0) v[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at) + (lane & 15));
-      }
+    // the query rows asked for into shared memory
+    auto give_rows = [&]() {
 #pragma unroll
       for (int k = 0; k < 16; ++k) {
         const int rr = 2 * k + (lane >> 4), c = lane & 15;
-        v[k].x ^= a.negate;
-        v[k].y ^= a.negate;
-        v[k].z ^= a.negate;
-        v[k].w ^= a.negate;
-        *reinterpret_cast<uint4*>(smem + (uint32_t)(c >> 3) * kQBox + swz128((uint32_t)(warp * 32 + rr), (uint32_t)(c & 7))) = v[k];
+        rows[k].x ^= a.negate;
+        rows[k].y ^= a.negate;
+        rows[k].z ^= a.negate;
+        rows[k].w ^= a.negate;
+        *reinterpret_cast<uint4*>(smem + (uint32_t)(c >> 3) * kQBox + swz128((uint32_t)(warp * 32 + rr), (uint32_t)(c & 7))) = rows[k];
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -272,9 +283,9 @@ uint4 v[16];   // all asked for at once
     RingPos<kScores> sp;
     uint32_t last_o = 0, last_parity = 0;   // O barrier of the tile before and its parity
     bool ok = true;
-    if (first < end) gather(first);
-    for (int i = first; ok && i < end; ++i) {
-      const PrefixItem it = a.items[i];
+    give_rows();
+    for (int i = 0; ok && i < n_items; ++i) {
+      const PrefixItem it = a.items[index(i)];
       const int n_kv = it.tile_hi - it.tile_lo;
       const bool live = it.row0 + mine < it.rows, any_live = __any_sync(0xffffffffu, live);
       float m_ref = neg_inf(), l = 0.f;
@@ -337,7 +348,10 @@ uint4 v[16];   // all asked for at once
       }
       if (!ok) break;
       // every S of this piece is complete: its queries make room for the next one's
-      if (i + 1 < end) gather(i + 1);
+      if (i + 1 < n_items) {
+        ask_rows(index(i + 1));
+        give_rows();
+      }
       if (!(ok = warp_wait(last_o, last_parity, a.status))) break;
       tc_fence_after();
       if (any_live) {

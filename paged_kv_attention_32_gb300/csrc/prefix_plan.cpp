@@ -99,6 +99,8 @@ int build_prefix_plan(pka_prefix_plan& p, const pka_decode_desc& d_in, const int
 
   // ---- the shared prefixes ----
   int64_t total = 0, bytes = 0;
+  std::vector<PrefixItem> in_turn;
+  std::vector<int32_t> by_pair;
   for (int pass = 0; pass < 2; ++pass) {   // the work, then its pieces
     if (pass == 1) {
       // A tile of 256 rows and 64 keys is 16.8 MFLOP, at 1900 TFLOP/s 8.8 ns of the GPU; where
@@ -107,7 +109,6 @@ int build_prefix_plan(pka_prefix_plan& p, const pka_decode_desc& d_in, const int
       p.dense = (double)total * 8.8e-9 > (double)bytes / 6.7e12;
     }
     Dealer deal(total, std::max(1, p.dense ? d.num_sms : d.num_sms / 2), kMinPrefixTiles, p.dense);
-    int64_t last_pair = -1;
     for (int32_t g = 0; g < num_groups; ++g) {
       const int32_t b0 = group_indptr[g], b1 = group_indptr[g + 1];
       if (b1 - b0 < 2 || prefix_pages[g] == 0) continue;
@@ -135,9 +136,9 @@ int build_prefix_plan(pka_prefix_plan& p, const pka_decode_desc& d_in, const int
           for (int64_t t = 0; t < tiles; ++run.count) {
             int64_t n = 0;
             const int64_t pair = deal.take(tiles - t, &n);
-            for (; last_pair < pair; ++last_pair) p.pair_segments.push_back((int32_t)p.items.size());
             PKA_CHECK_ARG(states + here <= INT32_MAX, "too many partial rows");
-            p.items.push_back(PrefixItem{b0, hk, (int32_t)t, (int32_t)(t + n), (int32_t)keys, q0, (int32_t)rows,
+            by_pair.push_back((int32_t)pair);
+            in_turn.push_back(PrefixItem{b0, hk, (int32_t)t, (int32_t)(t + n), (int32_t)keys, q0, (int32_t)rows,
                                          (int32_t)(rt * kPrefixRows), (int32_t)states, 0, 0, 0});
             states += here;
             t += n;
@@ -146,7 +147,16 @@ int build_prefix_plan(pka_prefix_plan& p, const pka_decode_desc& d_in, const int
         }
     }
   }
-  p.pair_segments.push_back((int32_t)p.items.size());
+  // each pair's first piece at the pair's own index, those behind it in turn (no pair is idle)
+  std::vector<PrefixItem> further;
+  for (size_t i = 0; i < in_turn.size(); ++i) {
+    const bool first = i == 0 || by_pair[i] != by_pair[i - 1];
+    if (first) p.more.push_back((int32_t)further.size());
+    (first ? p.items : further).push_back(in_turn[i]);
+  }
+  p.more.push_back((int32_t)further.size());
+  for (int32_t& m : p.more) m += (int32_t)p.items.size();
+  p.items.insert(p.items.end(), further.begin(), further.end());
 
   // ---- the requests' own keys ----
   const int64_t upp = ps / 16;
