@@ -468,7 +468,8 @@ typedef struct pka_prefix_plan pka_prefix_plan; /* opaque */
  * min_shared_bytes  where sharing keeps fewer bytes of K and V than this from being
  *              read again, the run is that of paged_decode_plan (split_waves,
  *              min_chunk_tokens and mma_min_rows are used then only); else the
- *              workspace holds the fp32 partial states of all pieces.  Negative: 48 MB.
+ *              workspace holds the fp32 partial states of all pieces.  Negative: shared
+ *              where by measured rates it is the faster.
  */
 int paged_prefix_decode_plan(pka_prefix_plan** plan_out, const pka_decode_desc* desc,
                              const int32_t* seq_lens_kv_host, const int32_t* qo_indptr_host,

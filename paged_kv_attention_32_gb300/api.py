@@ -428,8 +428,8 @@ def paged_prefix_decode_plan(seq_lens_kv, group_indptr, prefix_pages, *, num_qo_
     """Plan a paged decode of requests that, in groups, begin with the same pages (see pka.h):
     requests ``group_indptr[g]`` to ``group_indptr[g + 1] - 1`` share their first
     ``prefix_pages[g]`` pages, which are read once for all of them where that keeps at least
-    ``min_shared_bytes`` (negative: 48 MB) from being read again.  All host arrays; the other
-    arguments as for ``paged_decode_plan``."""
+    ``min_shared_bytes`` from being read again (negative: where it is the faster by measured
+    rates).  All host arrays; the other arguments as for ``paged_decode_plan``."""
     in_code, out_code = _dtype_codes(dtype, out_dtype)
     lens, groups = _prefix_groups(seq_lens_kv, group_indptr, prefix_pages, qo_indptr)
     d = L.DecodeDesc(

@@ -96,6 +96,7 @@ struct PrefixMergeArgs {
   void* out;
   float* lse;
   int32_t total_q, num_qo_heads, group;
+  int32_t most_states;           // that a row has
   float bmm2_scale;
   int32_t out_dtype;
 };
@@ -116,7 +117,7 @@ struct pka_prefix_plan {
   bool shared = false;
   int64_t min_shared_bytes = -1;   // as given
   bool dense = false;          // the prefixes' products take longer than all reads
-  int32_t partial_rows = 0;
+  int32_t partial_rows = 0, most_states = 0;   // states in all, and at most of one row
   int64_t workspace_bytes = 0, ws_lse_offset = 0;
   std::vector<pka::PrefixItem> items;
   std::vector<int32_t> more;

@@ -123,6 +123,7 @@ int make_prefix_plan(pka_prefix_plan& p, const pka_decode_desc& desc, const int3
   p.items.clear();
   p.pieces.clear();
   p.partial_rows = next.partial_rows;
+  p.most_states = next.most_states;
   p.workspace_bytes = next.workspace_bytes;
   return PKA_OK;
 }
@@ -307,6 +308,7 @@ int paged_prefix_decode_run(const pka_prefix_plan* p, const void* q, int64_t q_s
   m.total_q = base.total_q;
   m.num_qo_heads = base.Hq;
   m.group = base.G;
+  m.most_states = p->most_states;
   m.bmm2_scale = base.desc.bmm2_scale;
   m.out_dtype = base.desc.out_dtype;
   rc = launch_prefix(x, own.decode.in_f16 != 0, p->dense, kbox, vbox, stream);

@@ -243,11 +243,22 @@ __global__ void __maxnreg__(kOwnRegs) prefix_own_kernel(const __grid_constant__ 
 
 constexpr int kMergeWarps = 4, kMergeLoads = 8;
 constexpr int kMergeCtas = 152 * 7;   // one wave
+// Eight warps a row where few rows have many states (38 states of 16 rows of 8 heads: 10 us with a
+// warp a row, 3 with eight; 4 requests of 8 heads on 2 behind 16384 keys 30.1 to 17.8 us in all).
+constexpr int kSplitWarps = 8, kSplitRows = 152 * 3;
 
-__global__ void __launch_bounds__(kMergeWarps * 32, 7) prefix_merge_kernel(const __grid_constant__ PrefixMergeArgs a) {
-  const int lane = threadIdx.x & 31;
-  const int64_t rows = (int64_t)a.total_q * a.num_qo_heads, step = (int64_t)gridDim.x * kMergeWarps;
-  int64_t row = (int64_t)blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
+// A warp takes a row (W = 1), or W warps do, eight states each in turn.
+template <int W>
+__global__ void __launch_bounds__(W == 1 ? kMergeWarps * 32 : W * 32, W == 1 ? 7 : 3)
+    prefix_merge_kernel(const __grid_constant__ PrefixMergeArgs a) {
+  struct Part {
+    alignas(16) float o[128];
+    float m, sum;
+  };
+  __shared__ Part part[W == 1 ? 1 : W];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w = W == 1 ? 0 : warp;
+  const int64_t rows = (int64_t)a.total_q * a.num_qo_heads, step = (int64_t)gridDim.x * (W == 1 ? kMergeWarps : 1);
+  int64_t row = W == 1 ? (int64_t)blockIdx.x * kMergeWarps + warp : (int64_t)blockIdx.x;
   // where a row's states are: the request's own first
   struct Place {
     int own, pre;        // row in the runs' tiles
@@ -270,10 +281,12 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 7) prefix_merge_kernel(const
   };
   Place now = place(row);
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (row == 0 && lane == 0) *a.next = 0;   // every piece has been taken
+  if (row == 0 && w == 0 && lane == 0) *a.next = 0;   // every piece has been taken
   for (; row < rows; row += step) {
-    const int n = now.r0.count + now.r1.count;
-    auto at = [&](int k) -> int64_t {
+    const int all = now.r0.count + now.r1.count, left = all % (W * kMergeLoads) - w * kMergeLoads;
+    const int n = W == 1 ? all : all / (W * kMergeLoads) * kMergeLoads + min(max(left, 0), kMergeLoads);   // this warp's
+    auto at = [&](int i) -> int64_t {
+      const int k = W == 1 ? i : (i / kMergeLoads * W + w) * kMergeLoads + i % kMergeLoads;
       return k < now.r0.count ? now.r0.base + (int64_t)k * now.r0.rows + now.own
                               : now.r1.base + (int64_t)(k - now.r0.count) * now.r1.rows + now.pre;
     };
@@ -321,6 +334,38 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 7) prefix_merge_kernel(const
       }
     }
     next = place(row + step);
+    if (W > 1) {
+      *reinterpret_cast<float4*>(part[w].o + lane * 4) = o;
+      if (lane == 0) {
+        part[w].m = m;
+        part[w].sum = sum;
+      }
+      __syncthreads();
+      if (w == 0) {
+#pragma unroll
+        for (int i = 1; i < W; ++i) m = fmaxf(m, part[i].m);
+        sum = 0.f;
+        o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+          // without a maximum a part holds zeros, or NaN that are kept
+          const float f = part[i].m != neg_inf() ? ex2(part[i].m - m) : part[i].sum == 0.f ? 0.f : 1.f;
+          const float4 v = *reinterpret_cast<const float4*>(part[i].o + lane * 4);
+          if (f != 0.f) {
+            sum += f * part[i].sum;
+            o.x += f * v.x;
+            o.y += f * v.y;
+            o.z += f * v.z;
+            o.w += f * v.w;
+          }
+        }
+      }
+      __syncthreads();
+      if (w != 0) {
+        now = next;
+        continue;
+      }
+    }
     const int h = (int)(row % a.num_qo_heads);
     float denom = sum;
     if (a.sinks != nullptr && m != neg_inf()) denom += ex2(__ldg(a.sinks + h) * kLog2e - m);
@@ -371,8 +416,13 @@ int launch_prefix_own(const OwnArgs& a, const CUtensorMap& kmap, const CUtensorM
 int launch_prefix_merge(const PrefixMergeArgs& a, cudaStream_t stream) {
   const int64_t rows = (int64_t)a.total_q * a.num_qo_heads;
   cudaLaunchAttribute attr;
-  const cudaLaunchConfig_t cfg = behind(std::min<int64_t>(ceil_div(rows, kMergeWarps), kMergeCtas), kMergeWarps * 32, 0, stream, &attr);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, prefix_merge_kernel, a);
+  // Few rows of many states get eight warps each: a warp alone reads them eight at a time.
+  const bool split = rows <= kSplitRows && a.most_states > kMergeLoads;
+  const cudaLaunchConfig_t cfg = split ? behind(rows, kSplitWarps * 32, 0, stream, &attr)
+                                       : behind(std::min<int64_t>(ceil_div(rows, kMergeWarps), kMergeCtas),
+                                                kMergeWarps * 32, 0, stream, &attr);
+  const cudaError_t e = split ? cudaLaunchKernelEx(&cfg, prefix_merge_kernel<kSplitWarps>, a)
+                              : cudaLaunchKernelEx(&cfg, prefix_merge_kernel<1>, a);
   if (e != cudaSuccess) return cuda_fail(e, "prefix_merge_kernel launch");
   return PKA_OK;
 }

@@ -18,10 +18,17 @@ namespace pka {
 
 namespace {
 
-// Bytes of K and V that sharing keeps from being read again, from which it is done: below, the
-// two further launches and the states cost more than reading a prefix, most of it from L2,
-// for every request.
-constexpr int64_t kWorthBytes = 48 << 20;
+// Sharing saves what reading a prefix for every request costs, at 14 TB/s for the most part from
+// L2, and costs its tiles (a pair takes 16 heads or rows of a head for the time of 256) and two
+// launches with the join of the states: 5 us.  32 heads on 8, shared and not: 4 requests behind
+// 16384 keys 32.9 and 28.7 us, behind 65536 62.3 and 75.9; 16 behind 1024 16.9 and 15.8, behind
+// 4096 21.3 and 29.3; 64 behind 256 25.5 and 29.0.
+constexpr double kReadAgain = 14e12, kTileCost = 5.5e-9, kShareCost = 5e-6;
+// Without DENSE a piece has no fewer tiles than this; with it so many fall on each pair, or the
+// states cost what two CTAs an SM gain (32 heads on 8, with and without: 16 requests behind 4096
+// keys, 3 tiles a pair, 28.2 and 21.3 us; 4 behind 16384, 13, 32.9 and 34.8; 4 behind 65536, 54,
+// 62.3 and 88.7; 8 heads on 2, 16 behind 65536, 13, 37.5 and 35.0).
+constexpr int64_t kMinDenseTiles = 32;
 constexpr int64_t kMinPrefixTiles = 3;   // a piece is no shorter, its row tile's keys allowing
 constexpr int64_t kMinOwnUnits = 6, kMaxOwnUnits = 16;   // of 16 keys, in a piece of a request
 
@@ -71,7 +78,7 @@ int build_prefix_plan(pka_prefix_plan& p, const pka_decode_desc& d_in, const int
   const pka_decode_desc& d = p.base.desc;
   const int32_t G = p.base.G, Hkv = p.base.Hkv, ps = p.base.ps;
   const std::vector<ReqInfo>& reqs = p.base.reqs;
-  int64_t saved = 0, most_rows = 0;
+  int64_t saved = 0, again = 0, all_tiles = 0, most_rows = 0;
   for (int32_t g = 0; g < num_groups; ++g) {
     const int32_t b0 = group_indptr[g], b1 = group_indptr[g + 1];
     const int64_t keys = (int64_t)prefix_pages[g] * ps;
@@ -81,12 +88,18 @@ int build_prefix_plan(pka_prefix_plan& p, const pka_decode_desc& d_in, const int
                     (long long)first_row, (long long)keys);
     }
     if (b1 - b0 >= 2 && keys > 0) {
+      const int64_t rows = (int64_t)(reqs[b1 - 1].q_start + reqs[b1 - 1].q_len - reqs[b0].q_start) * G;
+      int64_t passes = 0;   // of the decode without sharing over the prefix
+      for (int32_t b = b0; b < b1; ++b) passes += ceil_div((int64_t)reqs[b].q_len * G, p.base.rows_per_cta);
       saved += (b1 - b0 - 1) * keys * Hkv * 512;
-      most_rows = std::max(most_rows, (int64_t)(reqs[b1 - 1].q_start + reqs[b1 - 1].q_len - reqs[b0].q_start) * G);
+      again += (passes - 1) * keys * Hkv * 512;
+      all_tiles += Hkv * ceil_div(keys, kPrefixTile) * ceil_div(rows, kPrefixRows);
+      most_rows = std::max(most_rows, rows);
     }
   }
   p.min_shared_bytes = min_shared_bytes;
-  p.shared = saved > 0 && saved >= (min_shared_bytes >= 0 ? min_shared_bytes : kWorthBytes);
+  p.shared = saved > 0 && (min_shared_bytes >= 0 ? saved >= min_shared_bytes
+                                                 : (double)again / kReadAgain > (double)all_tiles * kTileCost + kShareCost);
   if (!p.shared) {
     p.workspace_bytes = p.base.workspace_bytes;
     p.partial_rows = p.base.partial_rows;
@@ -99,16 +112,19 @@ int build_prefix_plan(pka_prefix_plan& p, const pka_decode_desc& d_in, const int
 
   // ---- the shared prefixes ----
   int64_t total = 0, bytes = 0;
+  int32_t most_pre = 0, most_own = 0;
   std::vector<PrefixItem> in_turn;
   std::vector<int32_t> by_pair;
   for (int pass = 0; pass < 2; ++pass) {   // the work, then its pieces
     if (pass == 1) {
       // A tile of 256 rows and 64 keys is 16.8 MFLOP, at 1900 TFLOP/s 8.8 ns of the GPU; where
-      // all of them take longer than the bytes, at 6.7 TB/s, the products bound the whole.
+      // many of them take longer than the bytes, at 6.7 TB/s, the products bound the whole.
       for (int32_t b = 0; b < B; ++b) bytes += (seq[b] - (int64_t)own_page[b] * ps) * Hkv * 512;
-      p.dense = (double)total * 8.8e-9 > (double)bytes / 6.7e12;
+      p.dense = total >= kMinDenseTiles * d.num_sms && (double)total * 8.8e-9 > (double)bytes / 6.7e12;
     }
-    Dealer deal(total, std::max(1, p.dense ? d.num_sms : d.num_sms / 2), kMinPrefixTiles, p.dense);
+    // where memory bounds the whole, a sixth of the SMs is left to the requests' own keys from the
+    // start (76 pairs of 152 SMs: 64 requests behind 8192 keys 48.0 us, 64 pairs 45.5)
+    Dealer deal(total, std::max(1, p.dense ? d.num_sms : d.num_sms * 27 / 64), kMinPrefixTiles, p.dense);
     for (int32_t g = 0; g < num_groups; ++g) {
       const int32_t b0 = group_indptr[g], b1 = group_indptr[g + 1];
       if (b1 - b0 < 2 || prefix_pages[g] == 0) continue;
@@ -143,6 +159,7 @@ int build_prefix_plan(pka_prefix_plan& p, const pka_decode_desc& d_in, const int
             states += here;
             t += n;
           }
+          most_pre = std::max(most_pre, run.count);
           p.runs.push_back(run);
         }
     }
@@ -176,6 +193,7 @@ int build_prefix_plan(pka_prefix_plan& p, const pka_decode_desc& d_in, const int
       t.own_run = (int32_t)p.runs.size();
       t.own_tiles = (int32_t)row_tiles;
     }
+    most_own = std::max(most_own, (int32_t)n);
     for (int32_t hk = 0; hk < Hkv; ++hk)
       for (int64_t rt = 0; rt < row_tiles; ++rt) {
         const int64_t here = std::min<int64_t>(kOwnRows, rows - rt * kOwnRows);
@@ -197,6 +215,7 @@ int build_prefix_plan(pka_prefix_plan& p, const pka_decode_desc& d_in, const int
   p.own_static = (int32_t)std::min<int64_t>(n_pieces, std::min<int64_t>(p.own_ctas, d.num_sms) * kOwnWarps);
   PKA_CHECK_ARG(p.items.size() < (size_t)INT32_MAX / 2 && p.pieces.size() < (size_t)INT32_MAX / 2, "too many pieces");
   p.partial_rows = (int32_t)states;
+  p.most_states = most_pre + most_own;
   p.ws_lse_offset = (int64_t)up256((size_t)states * 512);
   p.workspace_bytes = p.ws_lse_offset + states * 4;
   return PKA_OK;

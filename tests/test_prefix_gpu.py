@@ -103,6 +103,26 @@ def test_prefix_lengths(pages):
     check(make([(pages, [20] * 6 + [300])], heads=8, kv_heads=2, ps=16, seed=pages))
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("sms,dense", [(1, 1), (2, 1), (3, 0), (152, 0)])
+def test_shapes_of_the_prefix_kernel(sms, dense, dtype):
+    """Many tiles a CTA take two CTAs an SM, few one: the same batch on few SMs and on all."""
+    c = make([(60, [1 + i % 8 for i in range(150)])], heads=8, kv_heads=2, ps=16, dtype=dtype)
+    p = plan_of(c, num_sms=sms)
+    assert p.info["dense"] == dense
+    check(c, plan=p)
+
+
+@pytest.mark.parametrize("sinks", [False, True])
+@pytest.mark.parametrize("kv_heads", [1, 2, 8])
+def test_rows_of_many_states(kv_heads, sinks):
+    """Few rows behind many keys: several warps join a row's states.  More rows: one does."""
+    c = make([(512, [700, 1, 5000])], heads=8, kv_heads=kv_heads, ps=16, seed=kv_heads)
+    check(c, sinks=torch.randn(8, device="cuda") if sinks else None)
+    c = make([(512, [700, 1, 5000] + [20] * 57)], heads=8, kv_heads=kv_heads, ps=16, seed=kv_heads)
+    check(c, sinks=torch.randn(8, device="cuda") if sinks else None)
+
+
 @pytest.mark.parametrize("requests", [2, 63, 64, 65, 150])
 def test_row_tiles(requests):
     """Rows that fill part of a CTA's 128, of a pair's 256, and several pairs."""

@@ -77,7 +77,7 @@ def test_little_to_share_is_plain_decode():
     assert plan(lens, groups, pages, min_shared_bytes=-1).info["shared"] == 0
     assert plan(lens, groups, pages, min_shared_bytes=7 * 2048 * 1024).info["shared"] == 1
     assert plan(lens, groups, pages, min_shared_bytes=7 * 2048 * 1024 + 1).info["shared"] == 0
-    assert plan(lens, groups, pages, num_qo_heads=32, num_kv_heads=8, min_shared_bytes=-1).info["shared"] == 1
+    assert plan([8300] * 8, groups, [512], num_qo_heads=32, num_kv_heads=8, min_shared_bytes=-1).info["shared"] == 1
 
 
 @pytest.mark.parametrize("seed", range(12))
@@ -156,7 +156,7 @@ def test_even_shares():
 
     p = plan([8192 + 500] * 64, [0, 64], [512], num_qo_heads=32, num_kv_heads=8, max_pages_per_seq=600, num_pages=30000)
     i = p.info
-    assert i["dense"] == 0 and i["num_pairs"] == 76 and i["num_warps"] == 152 * 12
+    assert i["dense"] == 0 and i["num_pairs"] == 64 and i["num_warps"] == 152 * 12
 
 
 def test_update_keeps_the_plan_where_it_refuses():
