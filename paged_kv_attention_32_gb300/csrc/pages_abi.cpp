@@ -108,13 +108,27 @@ int paged_rope_append(const void* q, int64_t q_stride_tok, int64_t q_stride_head
                     aligned(v_pages, 16) && aligned(slot_map, 8) && aligned(status, 4),
                 "q, k, v and the pools must be 16-byte aligned, slot_map 8-byte aligned");
   if (num_tokens == 0) return PKA_OK;
-  if (q != nullptr && !(q_out == q && q_out_stride_tok == q_stride_tok && q_out_stride_head == q_stride_head)) {
-    auto bytes = [&](int64_t tok, int64_t head) -> Range {
-      return {nullptr, (size_t)((num_tokens - 1) * tok + (num_qo_heads - 1) * head + head_dim) * 2};
+  // what is written: no row of it twice
+  auto rows_apart = [](int64_t n, int64_t outer, int64_t m, int64_t inner, int64_t row) {
+    return (n <= 1 || outer >= row) && (m <= 1 || inner >= row);
+  };
+  PKA_CHECK_ARG(rows_apart(num_pages, stride_page, num_kv_heads, stride_head, (int64_t)page_size * head_dim),
+                "pages of %d rows overlap: stride_page %lld, stride_head %lld", page_size, (long long)stride_page,
+                (long long)stride_head);
+  PKA_CHECK_ARG(k_pages != v_pages, "k_pages and v_pages must be two pools");
+  if (q != nullptr) {
+    PKA_CHECK_ARG(rows_apart(num_tokens, q_out_stride_tok, num_qo_heads, q_out_stride_head, head_dim),
+                  "rows of q_out overlap");
+    auto range = [&](const void* p, int64_t tok, int64_t head, int32_t heads) -> Range {
+      return {p, (size_t)((num_tokens - 1) * tok + (heads - 1) * head + head_dim) * 2};
     };
-    const Range in{q, bytes(q_stride_tok, q_stride_head).n};
-    const Range out{q_out, bytes(q_out_stride_tok, q_out_stride_head).n};
-    PKA_CHECK_ARG(!overlap(in, out), "q_out overlaps q without being q");
+    const Range out = range(q_out, q_out_stride_tok, q_out_stride_head, num_qo_heads);
+    // over q itself its rows may lie between those of k and v
+    if (q_out != q || q_out_stride_tok != q_stride_tok || q_out_stride_head != q_stride_head)
+      PKA_CHECK_ARG(!overlap(out, range(q, q_stride_tok, q_stride_head, num_qo_heads)) &&
+                        !overlap(out, range(k, kv_stride_tok, kv_stride_head, num_kv_heads)) &&
+                        !overlap(out, range(v, kv_stride_tok, kv_stride_head, num_kv_heads)),
+                    "q_out overlaps q, k or v without being q");
   }
   a.q = q;
   a.q_stride_tok = q_stride_tok;

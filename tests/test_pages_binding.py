@@ -140,6 +140,14 @@ def sections(*x):
     (dict(ps=0), L.PKA_ERR_INVALID_ARG),
     (dict(q_out=P + 1024), L.PKA_ERR_INVALID_ARG),            # over q without being q
     (dict(q_out=P, o_tok=1024), L.PKA_ERR_INVALID_ARG),
+    (dict(q_out=P + 131072), L.PKA_ERR_INVALID_ARG),          # over k, over v
+    (dict(q_out=P + 196608 + 512), L.PKA_ERR_INVALID_ARG),
+    (dict(o_tok=0), L.PKA_ERR_INVALID_ARG),                   # rows written twice
+    (dict(o_head=64), L.PKA_ERR_INVALID_ARG),
+    (dict(q_out=P, o_tok=512, o_head=0, q_head=0), L.PKA_ERR_INVALID_ARG),
+    (dict(head=1024), L.PKA_ERR_INVALID_ARG),
+    (dict(page=1024), L.PKA_ERR_INVALID_ARG),
+    (dict(vp=P + 262144), L.PKA_ERR_INVALID_ARG),             # keys and values to one pool
 ])
 def test_rope_append_refuses(kw, code):
     assert rope(**kw) == code
