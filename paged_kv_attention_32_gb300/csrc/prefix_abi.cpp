@@ -80,6 +80,7 @@ int install_prefix_plan(pka_prefix_plan& p, pka_prefix_plan&& next, cudaStream_t
     cudaFree(p.dev_buf);
     cudaFreeHost(p.host_stage);
   }
+  keep_decode_buffers(next.base, p.base);   // for a batch that shares nothing
   p = std::move(next);
   return e == cudaSuccess ? PKA_OK : cuda_fail(e, "cudaEventRecord(plan upload)");
 }
@@ -96,16 +97,7 @@ int make_prefix_plan(pka_prefix_plan& p, const pka_decode_desc& desc, const int3
     p = std::move(next);
     return PKA_OK;
   }
-  if (next.shared) {
-    // the decode's own buffers stay for a batch that shares nothing
-    pka_plan old = std::move(p.base);
-    pka_plan fresh = std::move(next.base);
-    keep_decode_buffers(fresh, old);
-    next.base = std::move(fresh);
-    rc = install_prefix_plan(p, std::move(next), stream);
-    if (rc != PKA_OK) p.base = std::move(old);
-    return rc;
-  }
+  if (next.shared) return install_prefix_plan(p, std::move(next), stream);
   if (p.base.dev_buf == nullptr) {
     PKA_CUDA_TRY(cudaGetDevice(&next.base.device), "cudaGetDevice");
     rc = upload_decode_plan(next.base, stream);
@@ -114,11 +106,14 @@ int make_prefix_plan(pka_prefix_plan& p, const pka_decode_desc& desc, const int3
       return rc;
     }
     p.base = std::move(next.base);
+    p.shared = false;
   } else {
+    rc = check_device(p.base.device);
+    if (rc != PKA_OK) return rc;
+    p.shared = false;   // as base says, also where its upload fails
     rc = replace_decode_plan(p.base, std::move(next.base), stream);
     if (rc != PKA_OK) return rc;
   }
-  p.shared = false;
   p.min_shared_bytes = next.min_shared_bytes;
   p.items.clear();
   p.pieces.clear();

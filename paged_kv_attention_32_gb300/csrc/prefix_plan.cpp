@@ -78,7 +78,8 @@ int build_prefix_plan(pka_prefix_plan& p, const pka_decode_desc& d_in, const int
   const pka_decode_desc& d = p.base.desc;
   const int32_t G = p.base.G, Hkv = p.base.Hkv, ps = p.base.ps;
   const std::vector<ReqInfo>& reqs = p.base.reqs;
-  int64_t saved = 0, again = 0, all_tiles = 0, most_rows = 0;
+  double saved = 0, again = 0, all_tiles = 0;   // bytes, and tiles
+  int64_t most_rows = 0;
   for (int32_t g = 0; g < num_groups; ++g) {
     const int32_t b0 = group_indptr[g], b1 = group_indptr[g + 1];
     const int64_t keys = (int64_t)prefix_pages[g] * ps;
@@ -91,15 +92,16 @@ int build_prefix_plan(pka_prefix_plan& p, const pka_decode_desc& d_in, const int
       const int64_t rows = (int64_t)(reqs[b1 - 1].q_start + reqs[b1 - 1].q_len - reqs[b0].q_start) * G;
       int64_t passes = 0;   // of the decode without sharing over the prefix
       for (int32_t b = b0; b < b1; ++b) passes += ceil_div((int64_t)reqs[b].q_len * G, p.base.rows_per_cta);
-      saved += (b1 - b0 - 1) * keys * Hkv * 512;
-      again += (passes - 1) * keys * Hkv * 512;
-      all_tiles += Hkv * ceil_div(keys, kPrefixTile) * ceil_div(rows, kPrefixRows);
+      const double bytes = (double)keys * Hkv * 512;
+      saved += (b1 - b0 - 1) * bytes;
+      again += (double)(passes - 1) * bytes;
+      all_tiles += (double)Hkv * ceil_div(keys, kPrefixTile) * ceil_div(rows, kPrefixRows);
       most_rows = std::max(most_rows, rows);
     }
   }
   p.min_shared_bytes = min_shared_bytes;
-  p.shared = saved > 0 && (min_shared_bytes >= 0 ? saved >= min_shared_bytes
-                                                 : (double)again / kReadAgain > (double)all_tiles * kTileCost + kShareCost);
+  p.shared = saved > 0 && (min_shared_bytes >= 0 ? saved >= (double)min_shared_bytes
+                                                 : again / kReadAgain > all_tiles * kTileCost + kShareCost);
   if (!p.shared) {
     p.workspace_bytes = p.base.workspace_bytes;
     p.partial_rows = p.base.partial_rows;
@@ -187,6 +189,8 @@ int build_prefix_plan(pka_prefix_plan& p, const pka_decode_desc& d_in, const int
     const int64_t u0 = own_page[b] * upp, u1 = ceil_div(seq[b], 16), rows = (int64_t)G * reqs[b].q_len;
     const int64_t row_tiles = ceil_div(rows, kOwnRows), n = ceil_div(std::max<int64_t>(0, u1 - u0), most);
     PKA_CHECK_ARG((int64_t)p.runs.size() + Hkv * row_tiles <= INT32_MAX, "too many row tiles");
+    if (row_tiles > 0x7fff || Hkv > 0xffff)
+      return fail(PKA_ERR_UNSUPPORTED, "request %d has %lld query rows of %d KV heads", b, (long long)rows, Hkv);
     for (int32_t i = 0; i < reqs[b].q_len; ++i) {
       TokenStates& t = p.tokens[reqs[b].q_start + i];
       t.own_row = i * G;

@@ -1,11 +1,13 @@
 """Decode behind shared prefixes against 64-bit attention over every request's own table."""
 
+import ctypes
 import math
 import random
 
 import pytest
 import torch
 
+from paged_kv_attention_32_gb300 import _lib as L
 from paged_kv_attention_32_gb300 import api
 from tests import prefix_ref as ref
 
@@ -37,9 +39,8 @@ def make(groups, *, heads, kv_heads, ps, q_lens=None, dtype=torch.bfloat16, seed
             mine = ids[at:at + need[b] - pages]
             at += len(mine)
             tables.append(shared + mine + [-3] * (width - need[b]))
-    L = q_lens or [1] * len(kv)
     qo = [0]
-    for n in L:
+    for n in q_lens or [1] * len(kv):
         qo.append(qo[-1] + n)
     k, v = (torch.randn((total, kv_heads, ps, D), generator=g, device="cuda").to(dtype) for _ in range(2))
     q = torch.randn((qo[-1], heads, D), generator=g, device="cuda").to(dtype)
@@ -261,6 +262,48 @@ def test_update_and_rows_behind_the_last():
     want = ref.decode(f["q"][:T], f["k"], f["v"], f["tables"], f["kv"], f["qo"], causal=False, scale=f["scale"])
     close((got[0][:T], got[1][:T]), want, f["v"], f["dtype"], f["dtype"])
     assert bool((out[T:] == 7).all()) and bool((lse[T:] == 7).all())
+
+
+def test_update_between_shared_and_not():
+    """A plan that comes to share nothing, and again something: each time as a plan of its own."""
+    c = make([(30, [40, 30, 300]), (5, [9, 9])], heads=8, kv_heads=2, ps=16, seed=1)
+    p = plan_of(c)
+    for _ in range(2):
+        check(c, plan=p)
+        p.update(c["kv"], c["groups"], [0, 0], qo_indptr=c["qo"])
+        check(c, plan=p, pieces=False)
+        p.update(c["kv"], c["groups"], c["pre"], qo_indptr=c["qo"])
+    p.update(c["kv"], [0, 0, 5], [0, 0], qo_indptr=c["qo"])
+    p.update(c["kv"], [0, 2, 5], [30, 0], qo_indptr=c["qo"])
+    check(c, plan=p)
+    none = plan_of(c | {"pre": [0, 0]})
+    none.update(c["kv"], c["groups"], c["pre"], qo_indptr=c["qo"])
+    check(c, plan=none)
+
+
+@pytest.mark.parametrize("shared", [False, True])
+def test_update_that_fails_keeps_the_plan(shared):
+    """An update that needs more memory while a stream of this thread captures is refused by CUDA: the
+    plan runs as before, shared or not, and later updates work."""
+    cudart = ctypes.CDLL("libcudart.so.13")
+    c = make([(30, [40, 30, 300]), (5, [9, 9])], heads=8, kv_heads=2, ps=16, seed=1)
+    p = plan_of(c if shared else c | {"pre": [0, 0]})
+    check(c, plan=p, pieces=shared)
+    info, ws = p.info, p.workspace_bytes
+    torch.cuda.synchronize()
+    s, graph = torch.cuda.Stream(), ctypes.c_void_p()
+    n = 4096
+    assert cudart.cudaStreamBeginCapture(ctypes.c_void_p(s.cuda_stream), 1) == 0
+    try:
+        with pytest.raises(L.PkaError):
+            p.update([480] * n, [0, n], [30], stream=s)
+    finally:
+        cudart.cudaStreamEndCapture(ctypes.c_void_p(s.cuda_stream), ctypes.byref(graph))
+        cudart.cudaGetLastError()
+    assert p.info == info and p.workspace_bytes == ws
+    check(c, plan=p, pieces=shared)
+    p.update(c["kv"], c["groups"], c["pre"], qo_indptr=c["qo"])
+    check(c, plan=p)
 
 
 def test_captured_and_replayed():

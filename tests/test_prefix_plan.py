@@ -28,6 +28,7 @@ def plan(lens, groups, pages, **kw):
     (dict(page_size=24), L.PKA_ERR_UNSUPPORTED),
     (dict(head_dim=64), L.PKA_ERR_UNSUPPORTED),
     (dict(num_qo_heads=7), L.PKA_ERR_INVALID_ARG),
+    (dict(num_qo_heads=64, num_kv_heads=1, q_len=8192), L.PKA_ERR_UNSUPPORTED),   # 2^19 rows of a KV head
 ])
 def test_refusals(kw, code):
     a = dict(lens=[170, 200, 200, 200], groups=[0, 4], pages=[4])
