@@ -4,8 +4,8 @@
 // For the rows r = (token, head of the KV head's group) of a group of requests and the
 // prefix's keys j of one piece
 //   s_j = scale * q_r . k_j,  m = max s, l = sum exp(s - m),  o = sum exp(s - m) v / l,
-// stored as a 32-bit partial state (o and the base-2 LSE) that the decode kernel merges
-// with the states of the request's own keys.  Every row sees the whole prefix, so the only
+// stored as a 32-bit partial state (o and the base-2 LSE) that the merge kernel joins with
+// the states of the requests' own keys.  Every row sees the whole prefix, so the only
 // mask is the piece's end.
 //
 // A pair of CTAs (cta_group::2, one cluster, two SMs) takes 256 rows, 128 each, and walks the
@@ -27,8 +27,13 @@
 // SM and hide each other's softmax, with two S buffers each.  Else, where memory does: one
 // CTA an SM with four S buffers, beside a CTA of the kernel over the requests' own keys, so
 // that both read at once.
-// Measured and not kept, 65536 keys and 1024 rows of 8 heads: one CTA with two row tiles and
-// one issuing warp 212 us, the same with two threads a row 240, DENSE 172.
+// Measured: DENSE, 65536 keys and 1024 rows of 8 heads, 275 GFLOP: 177 to 200 us from the first
+// CTA to the last, 1380 to 1550 TFLOP/s.  Softmax and tensor core bound it together: of the 8
+// softmax warps of an SM each waits for its S while the others' exponentials run, and the
+// tensor pipe is busy half the time at a quarter of the keys.  Else, 8192 keys and 256 rows of
+// 8 heads, 34 MB: 24 us alone, all of it behind 137 MB of the other kernel's reads.
+// Not kept, the first case: one CTA an SM with two row tiles and one issuing warp 212 us, the
+// same with two threads a row 240.
 #include <cuda_bf16.h>
 
 #include "device_common.cuh"

@@ -107,7 +107,7 @@ int build_prefix_plan(pka_prefix_plan& p, const pka_decode_desc& d_in, const int
     p.partial_rows = p.base.partial_rows;
     return PKA_OK;
   }
-  PKA_CHECK_ARG(most_rows <= INT32_MAX, "a group has too many query rows");
+  PKA_CHECK_ARG(most_rows <= INT32_MAX - kPrefixRows, "a group has too many query rows");
   p.tokens.assign((size_t)p.base.total_q, TokenStates{0, 0, 0, -1, 0, 0, 0, 0});
   std::vector<int32_t> own_page(B, 0);
   int64_t states = 0;

