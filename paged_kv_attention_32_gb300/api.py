@@ -2,7 +2,8 @@
 
 Argument marshalling only: tensors are turned into device pointers, strides
 and sizes, outputs are allocated with torch when the caller passes none, and
-every computation happens in ``libpka.so``.  There is no CPU path.
+every computation happens in ``libpka.so``.  There is no CPU path.  The page-pool
+and shared-prefix calls are marshalled natively (``binding/binding.cpp``).
 """
 
 import ctypes

@@ -27,7 +27,7 @@ def free(**kw):
 
 def compact(**kw):
     a = dict(kv=P + 128, batch=4, free=P + 256, num_free=8, head=P + 320, ps=16, tables=P + 512, row=4, width=4,
-             pages=100, tables_out=P + 2048, out_row=4, free_out=P + 3072, src=P + 1152, dst=P + 1216, moves=8,
+             pages=100, tables_out=P + 2048, out_row=4, free_out=P + 3328, src=P + 1152, dst=P + 1216, moves=8,
              count=P + 1280, status=None)
     a.update(kw)
     return L.lib().paged_kv_compact(*a.values(), None)
