@@ -27,7 +27,7 @@ def make(groups, *, heads, kv_heads, ps, q_lens=None, dtype=torch.bfloat16, seed
         indptr.append(indptr[-1] + len(own))
         kv += [pages * ps + n for n in own]
     need = [-(-n // ps) for n in kv]
-    total = sum(need) + 5
+    total = sum(need) + 5 + sum(pages for pages, own in groups if not own)
     ids = list(range(total))
     r.shuffle(ids)
     tables, at = [], 0
