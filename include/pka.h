@@ -22,7 +22,7 @@
  *   paged_prefix_decode_plan / paged_prefix_decode_run
  *       paged decode of requests that begin with the same pages, which are
  *       attended over once for all of them.
- *   paged_decode_check_tables
+ *   paged_decode_check_tables / paged_prefix_decode_check_tables
  *       validation of the block-table entries a decode run reads.
  *   paged_kv_tables
  *       block tables, slot maps and lengths of a step, made on the GPU.
@@ -519,6 +519,16 @@ int paged_prefix_decode_plan_export(const pka_prefix_plan* plan, int32_t* prefix
 
 /* As paged_decode_plan_check. */
 int paged_prefix_decode_plan_check(const pka_prefix_plan* plan, void* stream);
+
+/*
+ * As paged_decode_check_tables for the entries of every request's row, and where the plan
+ * shares, whether the rows of each group begin with the same prefix_pages entries: a run
+ * reads only the first one's.  paged_prefix_decode_plan_check reports either
+ * (PKA_ERR_DEVICE_BOUNDS).
+ */
+int paged_prefix_decode_check_tables(const pka_prefix_plan* plan, const int32_t* block_tables,
+                                     int64_t bt_row_stride, const int32_t* seq_lens_kv_dev,
+                                     void* stream);
 
 /*
  * Run the planned decode; arguments as for paged_decode_run.  The shared pages

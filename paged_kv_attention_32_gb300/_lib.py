@@ -38,7 +38,7 @@ EXPORTED = (
     "paged_prefix_decode_plan", "paged_prefix_decode_plan_update",
     "paged_prefix_decode_plan_destroy", "paged_prefix_decode_plan_info",
     "paged_prefix_decode_plan_export", "paged_prefix_decode_plan_check",
-    "paged_prefix_decode_run",
+    "paged_prefix_decode_check_tables", "paged_prefix_decode_run",
     "attn_merge_lse",
     "batch_prefill_plan", "batch_prefill_plan_fixed", "batch_prefill_plan_destroy", "batch_prefill_plan_check",
     "batch_prefill_run",
@@ -175,6 +175,7 @@ _SIGS = {
     "paged_prefix_decode_plan_info": (ctypes.c_int, [_vp, ctypes.POINTER(PrefixPlanInfo)]),
     "paged_prefix_decode_plan_export": (ctypes.c_int, [_vp, _pi32, _pi32]),
     "paged_prefix_decode_plan_check": (ctypes.c_int, [_vp, _vp]),
+    "paged_prefix_decode_check_tables": (ctypes.c_int, [_vp, _vp, _i64, _vp, _vp]),
     "paged_prefix_decode_run": (ctypes.c_int, [_vp, _vp, _i64, _i64, _vp, _vp, _i64, _i64, _vp,
                                                _i64, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "attn_merge_lse": (ctypes.c_int, [_vp, _vp, _i32, _i32, _i32, _i32, _vp, _i32, _vp, _vp]),

@@ -398,9 +398,28 @@ class PrefixDecodePlan:
         return self
 
     def check(self, stream=None):
-        """Synchronise and read the device status word (raises on a kernel timeout)."""
+        """Synchronise and read the device status word (raises on a kernel timeout, or on what
+        ``check_tables`` found)."""
         L.check(L.lib().paged_prefix_decode_plan_check(self.prefix_handle, _stream(stream)),
                 "plan_check")
+
+    def check_tables(self, block_tables, seq_lens_kv=None, stream=None):
+        """Validate on the device the block-table entries a run of this plan reads, and that the
+        rows of a group begin with the same pages (``paged_prefix_decode_check_tables``);
+        ``check()`` then raises on bad ones."""
+        _check_tensors(torch.int32, block_tables=block_tables, seq_lens_kv=seq_lens_kv)
+        if block_tables.dim() != 2 or block_tables.shape[0] < self.batch_size or (
+                block_tables.shape[1] > 1 and block_tables.stride(1) != 1):
+            raise ValueError("block_tables needs dense rows, one per request")
+        if seq_lens_kv is not None and (seq_lens_kv.numel() < self.batch_size
+                                        or not seq_lens_kv.is_contiguous()):
+            raise ValueError("seq_lens_kv needs one contiguous entry per request")
+        rows = max(block_tables.stride(0), block_tables.shape[1])   # one row's stride says nothing
+        if block_tables.shape[0] > 1:
+            rows = block_tables.stride(0)
+        L.check(L.lib().paged_prefix_decode_check_tables(
+            self.prefix_handle, _ptr(block_tables), rows, _ptr(seq_lens_kv), _stream(stream)),
+            "paged_prefix_decode_check_tables")
 
     def __del__(self):
         h, self.prefix_handle = getattr(self, "prefix_handle", None), None

@@ -64,6 +64,9 @@ int read_status(int32_t* d_status, cudaStream_t stream) {
                 "at once (status 0x%x)", st);
   if (st & STATUS_FREE_LIST)
     return fail(PKA_ERR_DEVICE_BOUNDS, "a page of the free list is in use or listed twice (status 0x%x)", st);
+  if (st & STATUS_PREFIX)
+    return fail(PKA_ERR_DEVICE_BOUNDS,
+                "requests of a group do not begin with the pages that they are to share (status 0x%x)", st);
   if (st & STATUS_CAPACITY)
     return fail(PKA_ERR_DEVICE_CAPACITY,
                 "a step's tokens do not fit the free pages, a table row or the slot map, or a "

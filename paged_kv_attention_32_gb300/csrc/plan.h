@@ -72,6 +72,7 @@ enum : int32_t {
   STATUS_SLOT_BOUNDS = 8,   // paged_latent_append, paged_rope_append: a slot past the pool
   STATUS_ROWS = 16,         // paged_kv_fork / _free: a row outside the table or given twice
   STATUS_FREE_LIST = 32,    // paged_kv_compact: a free page that is in use or listed twice
+  STATUS_PREFIX = 64,       // paged_prefix_decode_check_tables: a group's rows begin with other pages
 };
 
 }  // namespace pka

@@ -57,6 +57,12 @@ struct alignas(16) TokenStates {
   int32_t pad0, pad1;
 };
 
+// What the table row of a request is to hold: its pages, of which the first `shared` are those of
+// row `first`.
+struct alignas(16) RowPages {
+  int32_t first, shared, pages, pad;
+};
+
 struct PrefixArgs {
   const void* q;
   int64_t q_stride_tok, q_stride_head;
@@ -109,6 +115,12 @@ int launch_prefix(const PrefixArgs& args, bool f16, bool dense, const CUtensorMa
 int launch_prefix_own(const OwnArgs& args, const CUtensorMap& kmap, const CUtensorMap& vmap, cudaStream_t stream);
 int launch_prefix_merge(const PrefixMergeArgs& args, cudaStream_t stream);
 
+// Sets STATUS_PAGE_BOUNDS for an entry outside the pool, STATUS_PREFIX for one that a group's rows
+// are to share and do not.
+int launch_prefix_check(const RowPages* rows, int32_t batch, const int32_t* tables, int64_t row_stride,
+                        const int32_t* seq_lens_live, int32_t page_size, int32_t num_pages, int32_t* status,
+                        cudaStream_t stream);
+
 }  // namespace pka
 
 struct pka_prefix_plan {
@@ -125,7 +137,8 @@ struct pka_prefix_plan {
   std::vector<pka::OwnPiece> pieces;
   std::vector<pka::StateRun> runs;
   std::vector<pka::TokenStates> tokens;
-  // one device allocation: items | pieces | runs | tokens | more | status word, count
+  std::vector<pka::RowPages> rows;
+  // one device allocation: items | pieces | runs | tokens | more | rows | status word, count
   void* dev_buf = nullptr;
   size_t capacity = 0;         // of dev_buf and of host_stage
   const pka::PrefixItem* d_items = nullptr;
@@ -133,6 +146,7 @@ struct pka_prefix_plan {
   const pka::StateRun* d_runs = nullptr;
   const pka::TokenStates* d_tokens = nullptr;
   const int32_t* d_more = nullptr;
+  const pka::RowPages* d_rows = nullptr;
   int32_t* d_status = nullptr;   // with the count of pieces taken behind it
   int device = -1;
   // pinned host image of dev_buf; stage_done marks when its last upload has read it

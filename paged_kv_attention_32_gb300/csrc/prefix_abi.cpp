@@ -23,11 +23,13 @@ int install_prefix_plan(pka_prefix_plan& p, pka_prefix_plan&& next, cudaStream_t
                          next.runs.size() * sizeof(StateRun),
                          next.tokens.size() * sizeof(TokenStates),
                          next.more.size() * sizeof(int32_t),
+                         next.rows.size() * sizeof(RowPages),
                          256};
   const void* from[] = {next.items.data(), next.pieces.data(), next.runs.data(), next.tokens.data(),
-                        next.more.data()};
-  size_t off[6], total = 0;
-  for (int i = 0; i < 6; ++i) {
+                        next.more.data(), next.rows.data()};
+  constexpr int kArrays = 6;
+  size_t off[kArrays + 1], total = 0;
+  for (int i = 0; i <= kArrays; ++i) {
     off[i] = total;
     total += up256(size[i]);
   }
@@ -57,11 +59,12 @@ int install_prefix_plan(pka_prefix_plan& p, pka_prefix_plan&& next, cudaStream_t
   next.d_runs = reinterpret_cast<const StateRun*>(base + off[2]);
   next.d_tokens = reinterpret_cast<const TokenStates*>(base + off[3]);
   next.d_more = reinterpret_cast<const int32_t*>(base + off[4]);
-  next.d_status = reinterpret_cast<int32_t*>(base + off[5]);
+  next.d_rows = reinterpret_cast<const RowPages*>(base + off[5]);
+  next.d_status = reinterpret_cast<int32_t*>(base + off[kArrays]);
   uint8_t* img = static_cast<uint8_t*>(next.host_stage);
-  for (int i = 0; i < 5; ++i)
+  for (int i = 0; i < kArrays; ++i)
     if (size[i] > 0) std::memcpy(img + off[i], from[i], size[i]);
-  std::memset(img + off[5], 0, 256);
+  std::memset(img + off[kArrays], 0, 256);
   cudaError_t e = cudaMemcpyAsync(base, img, total, cudaMemcpyHostToDevice, stream);
   if (e != cudaSuccess) {
     if (grow) {
@@ -225,6 +228,23 @@ int paged_prefix_decode_plan_check(const pka_prefix_plan* p, void* stream) {
   const int rc = check_device(p->device);
   if (rc != PKA_OK) return rc;
   return read_status(p->d_status, static_cast<cudaStream_t>(stream));
+}
+
+int paged_prefix_decode_check_tables(const pka_prefix_plan* p, const int32_t* block_tables, int64_t bt_row_stride,
+                                     const int32_t* seq_lens_kv_dev, void* stream) {
+  NvtxRange nvtx_range("pka::paged_prefix_decode_check_tables");
+  clear_error();
+  PKA_CHECK_ARG(p != nullptr, "plan must not be NULL");
+  if (!p->shared) return paged_decode_check_tables(&p->base, block_tables, bt_row_stride, seq_lens_kv_dev, stream);
+  PKA_CHECK_ARG(p->dev_buf != nullptr, "plan has no device state");
+  PKA_CHECK_ARG(block_tables != nullptr, "block_tables must not be NULL");
+  PKA_CHECK_ARG(bt_row_stride >= p->base.C, "bt_row_stride (%lld) is smaller than the table width %d",
+                (long long)bt_row_stride, p->base.C);
+  const int rc = check_device(p->device);
+  if (rc != PKA_OK) return rc;
+  return launch_prefix_check(p->d_rows, (int32_t)p->rows.size(), block_tables, bt_row_stride,
+                             p->base.desc.freeze_seq_lens ? nullptr : seq_lens_kv_dev, p->base.ps,
+                             (int32_t)p->base.desc.num_pages, p->d_status, static_cast<cudaStream_t>(stream));
 }
 
 int paged_prefix_decode_run(const pka_prefix_plan* p, const void* q, int64_t q_stride_tok, int64_t q_stride_head,

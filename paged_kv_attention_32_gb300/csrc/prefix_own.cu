@@ -379,6 +379,29 @@ __global__ void __launch_bounds__(W == 1 ? kMergeWarps * 32 : W * 32, W == 1 ? 7
   }
 }
 
+// ---- what the tables hold -----------------------------------------------------------
+
+// A CTA a request.
+__global__ void __launch_bounds__(128) prefix_check_kernel(const RowPages* rows, const int32_t* tables,
+                                                           int64_t row_stride, const int32_t* seq_lens_live,
+                                                           int32_t page_size, int32_t num_pages, int32_t* status) {
+  const RowPages r = rows[blockIdx.x];
+  int n = r.pages;
+  if (seq_lens_live != nullptr) {   // the shared pages are read all the same
+    const int live = max(__ldg(seq_lens_live + blockIdx.x), 0);
+    n = max(r.shared, min(n, (int)((live + (int64_t)page_size - 1) / page_size)));
+  }
+  const int32_t* row = tables + (int64_t)blockIdx.x * row_stride;
+  const int32_t* first = tables + (int64_t)r.first * row_stride;
+  int bad = 0;
+  for (int j = threadIdx.x; j < n; j += blockDim.x) {
+    const int32_t page = __ldg(row + j);
+    if ((uint32_t)page >= (uint32_t)num_pages) bad |= STATUS_PAGE_BOUNDS;
+    if (j < r.shared && page != __ldg(first + j)) bad |= STATUS_PREFIX;
+  }
+  if (bad != 0) atomicOr(status, bad);
+}
+
 cudaLaunchConfig_t behind(int64_t grid, int threads, size_t smem, cudaStream_t stream, cudaLaunchAttribute* attr) {
   attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr->val.programmaticStreamSerializationAllowed = 1;
@@ -426,6 +449,15 @@ int launch_prefix_merge(const PrefixMergeArgs& a, cudaStream_t stream) {
   const cudaError_t e = split ? cudaLaunchKernelEx(&cfg, prefix_merge_kernel<kSplitWarps>, a)
                               : cudaLaunchKernelEx(&cfg, prefix_merge_kernel<1>, a);
   if (e != cudaSuccess) return cuda_fail(e, "prefix_merge_kernel launch");
+  return PKA_OK;
+}
+
+int launch_prefix_check(const RowPages* rows, int32_t batch, const int32_t* tables, int64_t row_stride,
+                        const int32_t* seq_lens_live, int32_t page_size, int32_t num_pages, int32_t* status,
+                        cudaStream_t stream) {
+  prefix_check_kernel<<<batch, 128, 0, stream>>>(rows, tables, row_stride, seq_lens_live, page_size, num_pages, status);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e, "prefix_check_kernel launch");
   return PKA_OK;
 }
 

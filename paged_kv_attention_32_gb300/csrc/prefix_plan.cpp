@@ -209,6 +209,9 @@ int build_prefix_plan(pka_prefix_plan& p, const pka_decode_desc& d_in, const int
                                       reqs[b].q_len, reqs[b].kv_len});
       }
   }
+  for (int32_t g = 0; g < num_groups; ++g)
+    for (int32_t b = group_indptr[g]; b < group_indptr[g + 1]; ++b)
+      p.rows.push_back(RowPages{group_indptr[g], own_page[b], (int32_t)ceil_div(seq[b], ps), 0});
   // the longest first, equal ones in the order of the requests
   std::stable_sort(p.pieces.begin(), p.pieces.end(), [](const OwnPiece& x, const OwnPiece& y) {
     return x.unit_hi - x.unit_lo > y.unit_hi - y.unit_lo;

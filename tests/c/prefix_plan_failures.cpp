@@ -27,7 +27,7 @@ std::string g_error;
 pka::PrefixArgs g_prefix;
 pka::OwnArgs g_own;
 pka::PrefixMergeArgs g_merge;
-int g_merges = 0, g_plain = 0;
+int g_merges = 0, g_plain = 0, g_checks = 0;
 
 #define REQUIRE(cond)                                                          \
   do {                                                                         \
@@ -123,6 +123,10 @@ cudaError_t cudaStreamSynchronize(cudaStream_t) { return cudaSuccess; }
 cudaError_t cudaGetLastError() { return cudaSuccess; }
 const char* cudaGetErrorString(cudaError_t) { return "refused"; }
 int paged_decode_plan_check(const pka_plan*, void*) { return PKA_OK; }
+int paged_decode_check_tables(const pka_plan* p, const int32_t*, int64_t, const int32_t*, void*) {
+  REQUIRE(p->dev_buf != nullptr);
+  return PKA_OK;
+}
 }
 
 namespace pka {
@@ -190,6 +194,13 @@ int launch_prefix_merge(const PrefixMergeArgs& a, cudaStream_t) {
   ++g_merges;
   return PKA_OK;
 }
+int launch_prefix_check(const RowPages* rows, int32_t batch, const int32_t*, int64_t, const int32_t*, int32_t, int32_t,
+                        int32_t* status, cudaStream_t) {
+  REQUIRE(inside(rows, batch * sizeof(RowPages)) && status == g_prefix.status);
+  for (int32_t b = 0; b < batch; ++b) REQUIRE(rows[b].first <= b && rows[b].shared <= rows[b].pages);
+  ++g_checks;
+  return PKA_OK;
+}
 }  // namespace pka
 
 namespace {
@@ -214,6 +225,9 @@ void runs_as(const pka_prefix_plan* p, const Batch& b) {
   pka_prefix_plan_info info;
   REQUIRE(run(p) == PKA_OK && paged_prefix_decode_plan_info(p, &info) == PKA_OK);
   REQUIRE(info.shared == (int)b.shared && info.total_q == (int)b.lens.size());
+  const int checks = g_checks;
+  REQUIRE(paged_prefix_decode_check_tables(p, reinterpret_cast<int32_t*>(g_any), 64, nullptr, nullptr) == PKA_OK);
+  REQUIRE(g_checks == checks + (b.shared ? 1 : 0));
   if (!b.shared) {
     REQUIRE(g_plain == plain + 1 && g_merges == merges);
     return;

@@ -224,6 +224,49 @@ def test_table_entries_outside_the_pool_read_as_zeros():
     close(got, want, c["v"], c["dtype"], c["dtype"])
 
 
+@pytest.mark.parametrize("shared", [False, True])
+def test_check_tables(shared):
+    """An entry outside the pool in any row, rows that do not begin alike; entries that no run reads."""
+    c = make([(6, [20, 40, 1]), (0, [30]), (3, [0, 16])], heads=4, kv_heads=2, ps=16, seed=2, spare_cols=2)
+    p = plan_of(c if shared else c | {"pre": [0, 0, 0]}, freeze_seq_lens=False)
+    live = torch.tensor(c["kv"], dtype=torch.int32, device="cuda")
+    p.check_tables(table(c), live)
+    p.check()
+
+    def fails(row, col, page, lens=live):
+        t = table(c)
+        t[row, col] = page
+        p.check_tables(t, lens)
+        try:
+            p.check()
+        except L.PkaError as e:
+            assert e.code == L.PKA_ERR_DEVICE_BOUNDS
+            p.check()   # read and cleared
+            return True
+        return False
+
+    n = c["k"].shape[0]
+    for row, col in ((0, 0), (0, 5), (1, 8), (2, 6), (3, 1), (4, 2), (5, 3)):
+        assert fails(row, col, n) and fails(row, col, -1)
+        assert not fails(row, col, c["tables"][row][col])
+    assert not fails(1, 9, n) and not fails(4, 3, -1)        # behind the row's pages
+    other = c["tables"][3][0]
+    assert fails(1, 3, other) == shared and fails(5, 2, other) == shared
+    assert not fails(1, 6, other)                            # a request's own page
+    # a request that has become shorter: its own pages are not read, the shared ones are
+    short = live.clone()
+    short[1] = 97
+    assert not fails(1, 8, n, short) and fails(1, 6, n, short)
+    short[1] = 1
+    assert fails(1, 5, n, short) == shared
+    with pytest.raises(ValueError):
+        p.check_tables(table(c)[:5], live)
+    with pytest.raises(ValueError):
+        p.check_tables(table(c), live[:4])
+    with pytest.raises(ValueError):
+        p.check_tables(table(c).long(), live)
+
+
 def test_live_lengths():
     """Planned for the longest; each run reads the lengths as they are."""
     c = make([(20, [400, 300, 350]), (6, [100, 90])], heads=8, kv_heads=2, ps=16, seed=7)
