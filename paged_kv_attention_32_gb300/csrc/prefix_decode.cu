@@ -14,24 +14,27 @@
 // which halves what the shared-memory port moves for K and V and the copies.  The host deals
 // the work out evenly to one wave of pairs, which take their pieces in turn, the next one's
 // queries and keys copied while the last one ends.
-//   warps 0-3   gather the query rows (any token and head strides, any group size), then
-//               softmax, one thread per row: O rescaled only when the row maximum grew by
-//               more than 2^8, P in 16 bits over the S buffer (its rounding enters O like
+//   softmax     groups of four warps: gather the query rows (any token and head strides, any
+//               group size), then one thread per row: O rescaled only when the row maximum grew
+//               by more than 2^8, P in 16 bits over the S buffer (its rounding enters O like
 //               the inputs' own; the sum of p is taken in 32 bits before it);
-//   warp 4      copies this CTA's half of the keys, page by page (TMA);
-//   warp 5      the leader's issues every tcgen05.mma for both CTAs: S_b (M=256, N=64, 8
+//   one warp    copies this CTA's half of the keys, page by page (TMA);
+//   one warp    the leader's issues every tcgen05.mma for both CTAs: S_b (M=256, N=64, 8
 //               k-steps) into a ring of S buffers, and O += P V (M=256, N=128, 4 k-steps of
 //               16 keys, P from TMEM);
-//   warp 6      copies this CTA's half of the values.
+//   one warp    copies this CTA's half of the values.
 // Two shapes.  DENSE, where the products bound the whole: two CTAs of different pairs share an
 // SM and hide each other's softmax, with two S buffers each.  Else, where memory does: one
 // CTA an SM with four S buffers, beside a CTA of the kernel over the requests' own keys, so
-// that both read at once.
+// that both read at once; two softmax groups take the tiles in turn, each with its own maximum,
+// sum and O, joined at a piece's end (with one group 4 requests of 32 heads on 8 behind 16384
+// keys 34.8 us in all, 64 behind 4096 32.3; with two 32.8 and 29.8).
 // Measured: DENSE, 65536 keys and 1024 rows of 8 heads, 275 GFLOP: 177 to 200 us from the first
 // CTA to the last, 1380 to 1550 TFLOP/s.  Softmax and tensor core bound it together: of the 8
 // softmax warps of an SM each waits for its S while the others' exponentials run, and the
 // tensor pipe is busy half the time at a quarter of the keys.  Else, 8192 keys and 256 rows of
-// 8 heads, 34 MB: 24 us alone, all of it behind 137 MB of the other kernel's reads.
+// 8 heads, 34 MB, beside the other kernel's 137: 20 to 24 us (24 to 28 with one softmax group),
+// both 33, 5.2 TB/s.
 // Not kept, the first case: one CTA an SM with two row tiles and one issuing warp 212 us, the
 // same with two threads a row 240.
 #include <cuda_bf16.h>
@@ -54,15 +57,18 @@ constexpr uint32_t kQBox = 16384;           // 128 rows x 128 bytes
 constexpr uint32_t kKBox = 4096;            // 32 keys x 128 bytes
 constexpr uint32_t kKBytes = 2 * kKBox, kVBytes = 8192;   // a CTA's half of a tile
 constexpr float kRescaleThreshold = 8.0f;
-constexpr int kThreads = 224;
 
 template <bool DENSE>
 struct Geo {
-  static constexpr int kStages = 5, kScores = DENSE ? 2 : 4, kRegs = 128;
+  static constexpr int kStages = DENSE ? 5 : 7, kScores = DENSE ? 2 : 4;
+  // groups of four softmax warps that take the tiles of a piece in turn, each with its own O
+  static constexpr int kGroups = DENSE ? 1 : 2, kSoft = 4 * kGroups, kThreads = (kSoft + 3) * 32;
+  static constexpr int kRegs = DENSE ? 128 : 112;   // 112: a CTA of the own keys' kernel fits beside
   static constexpr uint32_t kOffK = 2 * kQBox, kOffV = kOffK + kStages * kKBytes;
   static constexpr uint32_t kOffBar = kOffV + kStages * kVBytes;
-  static constexpr size_t kSmemBytes = kOffBar + 512;
-  static constexpr uint32_t kColO = kScores * 64, kTmemCols = kColO + kD <= 256 ? 256 : 512;
+  static constexpr uint32_t kOffSums = kOffBar + 512;   // each group's maximum and sum of every row
+  static constexpr size_t kSmemBytes = kOffSums + (kGroups > 1 ? kGroups * kTileQ * 8 : 0);
+  static constexpr uint32_t kColO = kScores * 64, kTmemCols = kColO + kGroups * kD <= 256 ? 256 : 512;
   // Q, K, V, P and O-free are waited for by the leader's MMA warp, on the leader's barriers,
   // where both CTAs arrive; the others are signalled in both CTAs by the commits.  T counts a
   // pair's key tiles over all its pieces: S, P and O barriers T % kScores.  No barrier runs a
@@ -98,12 +104,25 @@ __device__ __forceinline__ void store_sector(float* dst, const uint32_t* w) {
                : "memory");
 }
 
+// Waits at named barrier ID for its N threads; whether all of them are well.
+template <int ID, int N>
+__device__ __forceinline__ bool all_meet(bool well) {
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+      "barrier.cta.red.and.pred p, %2, %3, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(all)
+      : "r"((uint32_t)well), "n"(ID), "n"(N)
+      : "memory");
+  return all != 0u;
+}
+
 template <bool F16, bool DENSE>
 __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(Geo<DENSE>::kRegs)
 prefix_kernel(const __grid_constant__ PrefixArgs a, const __grid_constant__ CUtensorMap tmk,
               const __grid_constant__ CUtensorMap tmv) {
   using Gm = Geo<DENSE>;
-  constexpr int kStages = Gm::kStages, kScores = Gm::kScores;
+  constexpr int kStages = Gm::kStages, kScores = Gm::kScores, kGroups = Gm::kGroups, kSoft = Gm::kSoft;
   constexpr uint32_t kOffK = Gm::kOffK, kOffV = Gm::kOffV;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
@@ -119,8 +138,11 @@ prefix_kernel(const __grid_constant__ PrefixArgs a, const __grid_constant__ CUte
   // A pair's first piece lies at its own index, so that its loads need not wait for the
   // list's; the others one behind the other from more0 on.
   const int mine = (int)rank * kTileQ + (tid & (kTileQ - 1));   // softmax: the thread's row of a piece
-  uint4 rows[16];   // two lanes' worth of a warp's 32 query rows, 16 bytes each
-  // asks for the query rows of a piece, two at a time, 16 lanes a row; zeros where there is none
+  const int group = kGroups > 1 ? warp >> 2 : 0, rows4 = (warp & 3) * 32;   // softmax: its group, its first row of the CTA's
+  constexpr int kAsk = 16 / kGroups;   // rows that a lane brings 16 bytes of
+  uint4 rows[kAsk];
+  // asks for the query rows of a piece, the groups' warps for a part each, two rows at a time, 16 lanes
+  // a row; zeros where there is none
   auto ask_rows = [&](int i) {
     const PrefixItem it = a.items[i];
     const int r = it.row0 + mine;
@@ -128,19 +150,19 @@ prefix_kernel(const __grid_constant__ PrefixArgs a, const __grid_constant__ CUte
                                           (int64_t)(it.kv_head * a.group + r % a.group) * a.q_stride_head
                                     : -1;
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const int64_t at = __shfl_sync(0xffffffffu, src, 2 * k + (lane >> 4));
+    for (int k = 0; k < kAsk; ++k) {
+      const int64_t at = __shfl_sync(0xffffffffu, src, 2 * (group * kAsk + k) + (lane >> 4));
       rows[k] = make_uint4(0u, 0u, 0u, 0u);
       if (at >= 0) rows[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at) + (lane & 15));
     }
   };
   // The first ones before anything else: behind the first keys and values of all CTAs they
   // would wait 5 us for memory.
-  if (warp < 4) ask_rows(pair);
+  if (warp < kSoft) ask_rows(pair);
   if (tid == 0) {   // the list comes in while the pair sets up
     ask_line(a.more + pair);
-    mbar_init(bar(Gm::kQFull), 8);   // the pair's softmax warps
-    mbar_init(bar(Gm::kOFree), 8);
+    mbar_init(bar(Gm::kQFull), 2 * kSoft);   // the pair's softmax warps
+    mbar_init(bar(Gm::kOFree), 2 * kSoft);
     mbar_init(bar(Gm::kMmaDone), 1);
     for (int s = 0; s < kStages; ++s) {
       mbar_init(bar(Gm::kKFull + s), 2);
@@ -150,14 +172,14 @@ prefix_kernel(const __grid_constant__ PrefixArgs a, const __grid_constant__ CUte
     }
     for (int s = 0; s < kScores; ++s) {
       mbar_init(bar(Gm::kSFull + s), 1);
-      mbar_init(bar(Gm::kPFull + s), 8);
+      mbar_init(bar(Gm::kPFull + s), 8);   // of one group
       mbar_init(bar(Gm::kODone + s), 1);
     }
     fence_barrier_init();
   }
   __syncwarp();
   cluster_arrive();
-  if (warp == 5) tmem_alloc_pair(smem_u32(tmem_slot), Gm::kTmemCols);
+  if (warp == kSoft + 1) tmem_alloc_pair(smem_u32(tmem_slot), Gm::kTmemCols);
   tc_fence_before();
   __syncthreads();
   cluster_wait();   // both CTAs' barriers stand before anyone arrives on them
@@ -167,9 +189,9 @@ prefix_kernel(const __grid_constant__ PrefixArgs a, const __grid_constant__ CUte
   const int more0 = __ldg(a.more + pair);
   const int n_items = 1 + __ldg(a.more + pair + 1) - more0;
   auto index = [&](int i) -> int { return i == 0 ? pair : more0 + i - 1; };
-  if (warp == 4 || warp == 6) {
+  if (warp == kSoft || warp == kSoft + 2) {
     // ---------------- producers: one lane per copy of a tile ----------------
-    const bool is_v = warp == 6;
+    const bool is_v = warp == kSoft + 2;
     const CUtensorMap* map = is_v ? &tmv : &tmk;
     if (lane == 0) tma_prefetch_desc(map);
     const int full0 = is_v ? Gm::kVFull : Gm::kKFull, empty0 = is_v ? Gm::kVEmpty : Gm::kKEmpty;
@@ -218,7 +240,7 @@ prefix_kernel(const __grid_constant__ PrefixArgs a, const __grid_constant__ CUte
       while (global_timer_ns() - t0 < 1000000ull) {
       }
     }
-  } else if (warp == 5) {
+  } else if (warp == kSoft + 1) {
     // ---------------- MMA issuer, the leader's: one elected lane issues for the pair ----
     if (rank == 0) {
       RingPos<kStages> kp, vp;
@@ -252,9 +274,9 @@ prefix_kernel(const __grid_constant__ PrefixArgs a, const __grid_constant__ CUte
           if (!ok) break;
           tc_fence_after();
           // 4 k-steps of 16 keys: P columns +8, V rows +16 (2048 bytes)
-          umma_pair_ts_k4<2048 / 16>(tmem + Gm::kColO, tmem + (uint32_t)pp.slot * 64u,
+          umma_pair_ts_k4<2048 / 16>(tmem + Gm::kColO + (uint32_t)(j % kGroups * kD), tmem + (uint32_t)pp.slot * 64u,
                                      smem_desc_sw128(sbase + kOffV + (uint32_t)vp.slot * kVBytes, kVBytes, 1024u),
-                                     kIdescPV<F16>, j > 0 ? 1u : 0u);
+                                     kIdescPV<F16>, j >= kGroups ? 1u : 0u);
           umma_pair_commit_elect(bar(Gm::kODone + pp.slot));
           umma_pair_commit_elect(bar(Gm::kVEmpty + vp.slot));
           vp.next();
@@ -270,23 +292,36 @@ prefix_kernel(const __grid_constant__ PrefixArgs a, const __grid_constant__ CUte
     // the query rows asked for into shared memory
     auto give_rows = [&]() {
 #pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        const int rr = 2 * k + (lane >> 4), c = lane & 15;
+      for (int k = 0; k < kAsk; ++k) {
+        const int rr = 2 * (group * kAsk + k) + (lane >> 4), c = lane & 15;
         rows[k].x ^= a.negate;
         rows[k].y ^= a.negate;
         rows[k].z ^= a.negate;
         rows[k].w ^= a.negate;
-        *reinterpret_cast<uint4*>(smem + (uint32_t)(c >> 3) * kQBox + swz128((uint32_t)(warp * 32 + rr), (uint32_t)(c & 7))) = rows[k];
+        *reinterpret_cast<uint4*>(smem + (uint32_t)(c >> 3) * kQBox + swz128((uint32_t)(rows4 + rr), (uint32_t)(c & 7))) = rows[k];
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(map_to_rank(bar(Gm::kQFull), 0));
     };
-    const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
-    const uint32_t o_tm = tmem + lane_off + Gm::kColO;
+    const uint32_t lane_off = (uint32_t)rows4 << 16;
+    const uint32_t o_tm = tmem + lane_off + Gm::kColO + (uint32_t)(group * kD);   // the group's O
     const float sl2 = a.scale_log2;   // >= 0
     RingPos<kScores> sp;
-    uint32_t last_o = 0, last_parity = 0;   // O barrier of the tile before and its parity
+    uint32_t last_o = 0, last_parity = 0;   // O barrier of the group's tile before and its parity
+    float2* sums = reinterpret_cast<float2*>(smem + Gm::kOffSums) + (tid & (kTileQ - 1));
+    // The groups' warps with the same rows meet, also when a wait of one gave up: none is left
+    // waiting for the others.  Whether all are well.
+    auto meet = [&](bool well) -> bool {
+      if (kGroups == 1) return well;
+      __syncwarp();
+      switch (warp & 3) {
+        case 0: return all_meet<1, kGroups * 32>(well);
+        case 1: return all_meet<2, kGroups * 32>(well);
+        case 2: return all_meet<3, kGroups * 32>(well);
+        default: return all_meet<4, kGroups * 32>(well);
+      }
+    };
     bool ok = true;
     give_rows();
     for (int i = 0; ok && i < n_items; ++i) {
@@ -295,6 +330,10 @@ prefix_kernel(const __grid_constant__ PrefixArgs a, const __grid_constant__ CUte
       const bool live = it.row0 + mine < it.rows, any_live = __any_sync(0xffffffffu, live);
       float m_ref = neg_inf(), l = 0.f;
       for (int j = 0; j < n_kv; ++j) {
+        if (kGroups > 1 && j % kGroups != group) {   // another's
+          sp.next();
+          continue;
+        }
         if (!(ok = warp_wait(bar(Gm::kSFull + sp.slot), sp.parity, a.status))) break;
         if (any_live) {   // else P may be anything: rows stay apart
           tc_fence_after();
@@ -318,8 +357,8 @@ prefix_kernel(const __grid_constant__ PrefixArgs a, const __grid_constant__ CUte
           const float m_new = grow ? mx : m_ref;
           const bool rescale = grow && m_ref != neg_inf();   // else O and l are still zero
           const float alpha = rescale ? ex2(m_ref - m_new) : 1.f;
-          if (j > 0 && __any_sync(0xffffffffu, rescale)) {
-            // O holds the tiles before: wait for P V of the last of them before rescaling
+          if (j >= kGroups && __any_sync(0xffffffffu, rescale)) {
+            // O holds the group's tiles before: wait for P V of the last of them before rescaling
             if (!(ok = warp_wait(last_o, last_parity, a.status))) break;
             tc_fence_after();
 #pragma unroll 1
@@ -351,31 +390,59 @@ prefix_kernel(const __grid_constant__ PrefixArgs a, const __grid_constant__ CUte
         last_parity = sp.parity;
         sp.next();
       }
-      if (!ok) break;
       // every S of this piece is complete: its queries make room for the next one's
+      if constexpr (kGroups > 1) ok = meet(ok);
+      if (!ok) break;
       if (i + 1 < n_items) {
         ask_rows(index(i + 1));
         give_rows();
       }
-      if (!(ok = warp_wait(last_o, last_parity, a.status))) break;
+      if constexpr (kGroups > 1) {
+        sums[group * kTileQ] = make_float2(m_ref, l);
+        ok = meet(group >= n_kv || warp_wait(last_o, last_parity, a.status));   // without a tile there is no O
+      } else {
+        ok = warp_wait(last_o, last_parity, a.status);
+      }
+      if (!ok) break;
       tc_fence_after();
       if (any_live) {
-        // != and not >: a sum that is NaN stays one, in the LSE as in the output
-        const float inv = l != 0.f ? 1.f / l : 0.f;
+        float scale[kGroups] = {};   // of each group's O
+        if constexpr (kGroups == 1) {
+          // != and not >: a sum that is NaN stays one, in the LSE as in the output
+          scale[0] = l != 0.f ? 1.f / l : 0.f;
+        } else {
+          const float2 x = sums[0], y = sums[kTileQ];
+          m_ref = fmaxf(x.x, y.x);
+          scale[0] = x.x == neg_inf() ? 0.f : ex2(x.x - m_ref);
+          scale[1] = y.x == neg_inf() ? 0.f : ex2(y.x - m_ref);
+          l = x.y * scale[0] + y.y * scale[1];
+          const float inv = l != 0.f ? 1.f / l : 0.f;
+          scale[0] *= inv;
+          scale[1] *= inv;
+        }
         const int64_t state = (int64_t)it.state + mine;
+        const int c0 = group * (kD / kGroups);   // the dimensions that this warp stores
+        const uint32_t o0 = tmem + lane_off + Gm::kColO;
 #pragma unroll 1
-        for (int c = 0; c < kD; c += 32) {
+        for (int c = c0; c < c0 + kD / kGroups; c += 32) {
           uint32_t o[32];
           __syncwarp();   // the lanes whose rows are stored and the others load together
-          tmem_ld32_sync(o_tm + (uint32_t)c, o);
+          tmem_ld32_sync(o0 + (uint32_t)c, o);
 #pragma unroll
-          for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * inv);
+          for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * scale[0]);
+          if (kGroups > 1 && n_kv > 1) {
+            uint32_t o1[32];
+            tmem_ld32_sync(o0 + (uint32_t)(kD + c), o1);
+#pragma unroll
+            for (int x = 0; x < 32; ++x)
+              o[x] = __float_as_uint(__uint_as_float(o[x]) + __uint_as_float(o1[x]) * scale[kGroups - 1]);
+          }
           if (live) {
 #pragma unroll
             for (int x = 0; x < 4; ++x) store_sector(a.ws_o + state * kD + c + 8 * x, o + 8 * x);
           }
         }
-        if (live) a.ws_lse[state] = l != 0.f ? m_ref - kLatentWeightShift<F16> + log2f(l) : neg_inf();
+        if (live && group == 0) a.ws_lse[state] = l != 0.f ? m_ref - kLatentWeightShift<F16> + log2f(l) : neg_inf();
       }
       tc_fence_before();
       __syncwarp();
@@ -388,9 +455,9 @@ prefix_kernel(const __grid_constant__ PrefixArgs a, const __grid_constant__ CUte
   __syncthreads();
   // Nothing of the pair's still runs on the tensor cores, and every commit has landed here.
   // Waited for only now: all of a pair's tiles may take longer than any one wait may.
-  if (warp == 5) warp_wait(bar(Gm::kMmaDone), 0, a.status);
+  if (warp == kSoft + 1) warp_wait(bar(Gm::kMmaDone), 0, a.status);
   cluster_sync();   // neither CTA's shared memory nor TMEM goes while the pair still uses it
-  if (warp == 5) {
+  if (warp == kSoft + 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, Gm::kTmemCols);
   }
@@ -402,7 +469,7 @@ int launch(const PrefixArgs& args, const CUtensorMap& kmap, const CUtensorMap& v
   static std::atomic<uint64_t> smem_set{0};   // devices whose limit was raised
   cudaError_t e = set_smem_once(kern, (int)Geo<DENSE>::kSmemBytes, smem_set, true);
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(prefix)");
-  kern<<<2 * args.num_pairs, kThreads, Geo<DENSE>::kSmemBytes, stream>>>(args, kmap, vmap);
+  kern<<<2 * args.num_pairs, Geo<DENSE>::kThreads, Geo<DENSE>::kSmemBytes, stream>>>(args, kmap, vmap);
   e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "prefix_kernel launch");
   return PKA_OK;

@@ -21,13 +21,14 @@ namespace {
 // Sharing saves what reading a prefix for every request costs, at 14 TB/s for the most part from
 // L2, and costs its tiles (a pair takes 16 heads or rows of a head for the time of 256) and two
 // launches with the join of the states: 5 us.  32 heads on 8, shared and not: 4 requests behind
-// 16384 keys 32.9 and 28.7 us, behind 65536 62.3 and 75.9; 16 behind 1024 16.9 and 15.8, behind
-// 4096 21.3 and 29.3; 64 behind 256 25.5 and 29.0.
+// 16384 keys 32.7 and 28.3 us, behind 65536 63.5 and 76.0; 16 behind 1024 16.4 and 14.4, behind
+// 4096 19.8 and 28.7; 64 behind 256 23.8 and 29.1.
 constexpr double kReadAgain = 14e12, kTileCost = 5.5e-9, kShareCost = 5e-6;
 // Without DENSE a piece has no fewer tiles than this; with it so many fall on each pair, or the
 // states cost what two CTAs an SM gain (32 heads on 8, with and without: 16 requests behind 4096
-// keys, 3 tiles a pair, 28.2 and 21.3 us; 4 behind 16384, 13, 32.9 and 34.8; 4 behind 65536, 54,
-// 62.3 and 88.7; 8 heads on 2, 16 behind 65536, 13, 37.5 and 35.0).
+// keys, 3 tiles a pair, 27.4 and 20.1 us; 4 behind 16384, 13, 32.9 and 32.8; behind 32768, 27,
+// 43.3 and 51.3; behind 65536, 54, 63.1 and 87.9; 16 heads on 1, 64 behind 65536, 27, 61.0 and
+// 55.3).
 constexpr int64_t kMinDenseTiles = 32;
 constexpr int64_t kMinPrefixTiles = 3;   // a piece is no shorter, its row tile's keys allowing
 constexpr int64_t kMinOwnUnits = 6, kMaxOwnUnits = 16;   // of 16 keys, in a piece of a request
@@ -119,13 +120,15 @@ int build_prefix_plan(pka_prefix_plan& p, const pka_decode_desc& d_in, const int
   std::vector<int32_t> by_pair;
   for (int pass = 0; pass < 2; ++pass) {   // the work, then its pieces
     if (pass == 1) {
-      // A tile of 256 rows and 64 keys is 16.8 MFLOP, at 1900 TFLOP/s 8.8 ns of the GPU; where
-      // many of them take longer than the bytes, at 6.7 TB/s, the products bound the whole.
+      // A tile of 256 rows and 64 keys (8.4 MFLOP) takes 8.8 ns of the GPU without DENSE, in which one
+      // CTA an SM waits for itself; where many of them take longer than the bytes, at 6.7 TB/s, the
+      // products bound the whole.
       for (int32_t b = 0; b < B; ++b) bytes += (seq[b] - (int64_t)own_page[b] * ps) * Hkv * 512;
       p.dense = total >= kMinDenseTiles * d.num_sms && (double)total * 8.8e-9 > (double)bytes / 6.7e12;
     }
     // where memory bounds the whole, a sixth of the SMs is left to the requests' own keys from the
-    // start (76 pairs of 152 SMs: 64 requests behind 8192 keys 48.0 us, 64 pairs 45.5)
+    // start (76 pairs of 152 SMs: 64 requests behind 8192 keys 48.0 us, 64 pairs 45.5; with two softmax
+    // groups 75 pairs 38.4 us, 64 34.8 where their own keys are few)
     Dealer deal(total, std::max(1, p.dense ? d.num_sms : d.num_sms * 27 / 64), kMinPrefixTiles, p.dense);
     for (int32_t g = 0; g < num_groups; ++g) {
       const int32_t b0 = group_indptr[g], b1 = group_indptr[g + 1];
