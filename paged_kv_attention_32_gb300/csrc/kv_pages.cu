@@ -16,7 +16,7 @@
 // scans of bit counts: one launch does it all.  Latency bounds them: a launch, two waits for
 // memory in turn (lengths, then entries) and the cluster barriers between the steps; for
 // large tables the shared-memory atomics (about 17 cycles a warp's 32 marks).  Fork of 448
-// rows 7 us; release from 64 rows 6.7 us from start to end, from 2048 rows, 530000 entries,
+// rows 7 us; release from 64 rows 6.4 us from start to end, from 2048 rows, 530000 entries,
 // 26 us, of which 10 go to the marks, 6 to joining them; compaction of 256 rows 21 us.
 #include <algorithm>
 
@@ -166,8 +166,8 @@ __global__ void __launch_bounds__(kForkThreads) kv_fork_kernel(const __grid_cons
 constexpr int kMaxCluster = 16, kThreads = 1024, kWarps = kThreads / 32;
 // Table entries up to which one CTA does without the others, whose barriers and joined bits
 // then cost more than its share of the reads.  One CTA and 16: release from 16384 entries 10.3
-// and 12.4 us, from 32768 14.4 and 12.3; compaction, with the copies, of 2016 18.4 and 22.6, of
-// 8032 26.8 and 26.7, of 16384 44.0 and 34.9.
+// and 12.4 us, from 24576 11.9 and 12.4, from 32768 14.0 and 12.4; compaction, with the copies, of
+// 2016 15.8 and 21.9, of 8032 24.7 and 26.7, of 12048 36.8 and 32.0.
 constexpr int64_t kFewToFree = 24576, kFewToCompact = 8192;
 constexpr int kPiece = 512;   // table entries a warp takes at a time
 constexpr int kDynamicSmem = 222 * 1024;
@@ -195,6 +195,7 @@ __device__ __forceinline__ void sync_all() {
 // The lowest `n` set bits of `x`.
 __device__ __forceinline__ uint32_t lowest(uint32_t x, int64_t n) {
   if (n <= 0) return 0u;
+  if (n >= __popc(x)) return x;
   uint32_t left = x;
   for (; n > 0 && left != 0u; --n) left &= left - 1u;
   return x & ~left;
@@ -266,10 +267,11 @@ __device__ __forceinline__ void for_entries(const int32_t* tables, int64_t row_s
 // shared-memory atomics (one to another CTA's shared memory takes some 4 cycles a lane: 2048
 // rows of 270000 pages 181 us), and slices, a contiguous part of the pool per CTA, into which
 // the marks of all CTAs are joined.  A pool of more pages than the marks hold takes several
-// ranges, with the tables read once for each.
+// ranges, with the tables read once for each.  One CTA alone marks in its slice.
 struct PageBits {
   uint32_t* slice[2];   // [per] words of this CTA's
-  uint32_t* mark[2];    // [range] words
+  uint32_t* mark[2];    // [range] words, one behind the other
+  uint32_t* spare[2];   // [per] words, or more; the marks are lost
   int per, words, range;   // per and range are whole vectors of four
 };
 template <int NC>
@@ -279,8 +281,10 @@ __device__ __forceinline__ PageBits page_bits(uint32_t* smem, int num_pages) {
   p.per = ((p.words + NC - 1) / NC + 3) & ~3;
   p.slice[0] = smem;
   p.slice[1] = smem + p.per;
-  p.mark[0] = smem + 2 * p.per;
-  p.range = min((kDynamicSmem / 4 - 2 * p.per) / 2 & ~3, (p.words + 3) & ~3);
+  p.range = NC == 1 ? p.per : min((kDynamicSmem / 4 - 2 * p.per) / 2 & ~3, (p.words + 3) & ~3);
+  p.spare[0] = smem + 2 * p.per;
+  p.spare[1] = p.spare[0] + p.range;
+  p.mark[0] = NC == 1 ? p.slice[0] : p.spare[0];
   p.mark[1] = p.mark[0] + p.range;
   return p;
 }
@@ -342,7 +346,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_free_kernel(const __grid_const
   const int word0 = (int)rank * bits.per;   // the slice's first word
   const int head = __ldg(a.free_head);
   for (int w = tid; w < (a.batch + 31) / 32; w += kThreads) released[w] = 0u;
-  for (int w = tid; w < 2 * bits.per; w += kThreads) smem[w] = 0u;
+  if (NC > 1)
+    for (int w = tid; w < 2 * bits.per; w += kThreads) smem[w] = 0u;
   clear_marks(bits);
   if (tid == 0) board.flags = 0;
   __syncthreads();
@@ -376,8 +381,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_free_kernel(const __grid_const
                   else if (w >= 0 && w < bits.range) atomicOr(bits.mark[0] + tag + w, 1u << (page & 31));
                 });
     sync_all<NC>();
-    join_marks<NC, false>(bits, first, rank);
-    sync_all<NC>();
+    if constexpr (NC > 1) {
+      join_marks<NC, false>(bits, first, rank);
+      sync_all<NC>();
+    }
   }
 
   // the freed pages, in ascending order
@@ -429,7 +436,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_compact_kernel(const __grid_co
   uint32_t* used = bits.slice[0];    // pages in the tables, then those of them that move
   uint32_t* open = bits.slice[1];    // pages in the free list, then the moving pages before each word
   const int head = __ldg(a.free_head);
-  for (int w = tid; w < 2 * bits.per; w += kThreads) smem[w] = 0u;
+  if (NC > 1)
+    for (int w = tid; w < 2 * bits.per; w += kThreads) smem[w] = 0u;
   clear_marks(bits);
   if (tid == 0) board.flags = 0;
   __syncthreads();
@@ -444,6 +452,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_compact_kernel(const __grid_co
   const bool fits = board.flags == 0;
   sync_all<NC>();   // the check is over: flags may come from other CTAs
   auto entries_of = [&](int b) { return RowPart{pages_of(__ldg(a.kv_lens + b), a.page_size), 0}; };
+  // what lies before the list's head stays: each thread's first entry is asked for early
+  const int me = (int)rank * kThreads + tid;
+  const bool other_list = a.free_pages_out != a.free_pages;
+  const int32_t before_head = other_list && fits && me < head ? a.free_pages[me] : 0;
   for (int first = 0; fits && first < bits.words; first += bits.range) {
     if (first > 0) {
       clear_marks(bits);
@@ -461,8 +473,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_compact_kernel(const __grid_co
         raise_flag<NC>(board, STATUS_FREE_LIST);
     }
     sync_all<NC>();
-    if (join_marks<NC, true>(bits, first, rank)) raise_flag<NC>(board, STATUS_FREE_LIST);
-    sync_all<NC>();
+    if constexpr (NC > 1) {
+      if (join_marks<NC, true>(bits, first, rank)) raise_flag<NC>(board, STATUS_FREE_LIST);
+      sync_all<NC>();
+    }
   }
 
   // U and U + F before each word
@@ -507,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_compact_kernel(const __grid_co
     // Below the word where the pages in use end every free page is a hole and none moves, above
     // it all in use move and all pages are free afterwards: one list for holes and free pages.
     uint32_t m = (uint32_t)((base + before) >> 32), h = (uint32_t)(base + before);
-    uint32_t *list = bits.mark[0], *at = bits.mark[1];
+    uint32_t *list = bits.spare[0], *at = bits.spare[1];
     z = z0;
     for (int w = w0; w < w1; ++w) {
       const uint32_t both = used[w] | open[w], low = lowest(both, in_use - z);
@@ -533,25 +547,26 @@ __global__ void __launch_bounds__(kThreads, 1) kv_compact_kernel(const __grid_co
             (word0 + w) * 32 + lane;
     }
   }
-  const int me = (int)rank * kThreads + tid;
   if (me == 0) {
     *a.num_moves = flags == 0 ? (int32_t)moves : 0;
     if (flags != 0 && a.status != nullptr) atomicOr(a.status, flags);
   }
   for (int64_t i = (flags == 0 ? moves : 0) + me; i < a.max_moves; i += NC * kThreads)
     a.src_pages[i] = a.dst_pages[i] = -1;
-  if (a.free_pages_out != a.free_pages)   // what lies before the list's head, or all of it
-    for (int64_t i = me; i < (flags == 0 ? head : a.num_free); i += NC * kThreads)
+  if (other_list) {   // before the head, or where the call is refused all of it
+    if (fits && me < head) a.free_pages_out[me] = before_head;
+    for (int64_t i = fits && me < head ? me + NC * kThreads : me; i < (flags == 0 ? head : a.num_free); i += NC * kThreads)
       a.free_pages_out[i] = a.free_pages[i];
+  }
   sync_all<NC>();   // the moves are written, in global memory and in everybody's slices
 
   // the tables, each CTA with its own copy of a range of the slices
   const bool in_place = a.tables_out == a.tables;
   if (flags == 0 || !in_place) {
     for (int first = 0; first < bits.words; first += bits.range) {
-      if (first > 0) __syncthreads();   // the range before is done with
+      if (NC > 1 && first > 0) __syncthreads();   // the range before is done with
       const int vectors = bits.range / 2, start = (int)((int64_t)vectors * rank / NC);   // as in join_marks
-      for (int n = tid; flags == 0 && n < vectors; n += kThreads) {
+      for (int n = tid; NC > 1 && flags == 0 && n < vectors; n += kThreads) {
         const int i = n + start < vectors ? n + start : n + start - vectors;
         const int kind = i & 1, w = first + (i >> 1) * 4;
         if (w < bits.words) {
@@ -560,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_compact_kernel(const __grid_co
               load_remote4(map_to_rank(smem_u32(bits.slice[kind] + (w - owner * words)), (uint32_t)owner));
         }
       }
-      __syncthreads();
+      if (NC > 1) __syncthreads();
       for_entries<NC>(a.tables, a.row_stride, a.batch, a.width, rank, [&](int b) { return RowPart{a.width, flags == 0 ? entries_of(b).n : 0}; },
                   [&](int b, int tag, int j, int page) {
                     const bool live = j < tag;
