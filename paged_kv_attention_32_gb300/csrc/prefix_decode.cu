@@ -81,6 +81,10 @@ struct Geo {
   static_assert(kCount * 8 + 4 <= 512, "barriers and the TMEM address slot");
 };
 static_assert(2 * (Geo<true>::kSmemBytes + 1024) <= 228 * 1024, "two CTAs share an SM");
+// All of an SM's tensor memory: no CTA of another pair may wait for it beside one that waits for
+// its own other half elsewhere.
+static_assert(Geo<false>::kTmemCols == 512 && Geo<false>::kSmemBytes + Geo<true>::kSmemBytes > 228 * 1024,
+              "no pair's CTA beside this one");
 
 template <bool F16> constexpr uint32_t kIdescQK = idesc_bf16_f32(256, 64, 0, 0, F16);
 template <bool F16> constexpr uint32_t kIdescPV = idesc_bf16_f32(256, kD, 0, 1, F16);
