@@ -15,9 +15,9 @@
 // of its own of the pool's bits, join the copies by slices over their shared memories, and rank pages by
 // scans of bit counts: one launch does it all.  Latency bounds them: a launch, two waits for
 // memory in turn (lengths, then entries) and the cluster barriers between the steps; for
-// large tables the shared-memory atomics (about 17 cycles a warp's 32 marks).  Fork of 448
-// rows 7 us; release from 64 rows 6.4 us from start to end, from 2048 rows, 530000 entries,
-// 26 us, of which 10 go to the marks, 6 to joining them; compaction of 256 rows 21 us.
+// large tables the entries that 16 SMs' registers hold on their way.  Fork of 448 rows 7 us;
+// release from 64 rows 6.4 us from start to end, from 2048 rows, 530000 entries, 20 us, of which
+// 5 go to the marks, 5 to joining them; compaction of 256 rows 20 us.
 #include <algorithm>
 
 #include "device_common.cuh"
@@ -169,7 +169,6 @@ constexpr int kMaxCluster = 16, kThreads = 1024, kWarps = kThreads / 32;
 // and 12.4 us, from 24576 11.9 and 12.4, from 32768 14.0 and 12.4; compaction, with the copies, of
 // 2016 15.8 and 21.9, of 8032 24.7 and 26.7, of 12048 36.8 and 32.0.
 constexpr int64_t kFewToFree = 24576, kFewToCompact = 8192;
-constexpr int kPiece = 512;   // table entries a warp takes at a time
 constexpr int kDynamicSmem = 222 * 1024;
 
 __device__ __forceinline__ void flag_set(uint32_t addr, uint32_t bits) {
@@ -223,21 +222,24 @@ __device__ __forceinline__ void raise_flag(ClusterBoard& board, int32_t bits) {
 }
 
 // Calls `f(row, tag, column, entry)` for the first n table entries of every row, (n, tag) =
-// `row_of(row)`: pieces of a row to the warps of the NC CTAs in turn, 16 loads a lane at a time.
-// A warp asks for the lengths of its next 32 pieces at once and passes over those that are empty
-// (each length asked for while the piece before is under way: a release from 2048 rows 33.8 us
-// instead of 32.8).  Half the piece, with the next one's loads on their way too: 64 rows of 257
-// entries 4.4 us instead of 2.9.
+// `row_of(row)`, and returns what any of a thread's calls did: pieces of a row to the warps of
+// the NC CTAs in turn, AT_ONCE of them in 16 loads a lane.  A warp asks for the lengths of its
+// next 32 pieces at once and passes over those that are empty (each length asked for while the
+// piece before is under way: a release from 2048 rows 33.8 us instead of 32.8).  Two pieces of
+// 256 entries at once keep more loads on their way where rows end anywhere (the same release 24.8
+// us, one piece of 512 29.1, four of 128 25.9); one of 512 is faster where whole rows fit (a
+// release from 64 rows of 257 9.7 and 10.4, compaction of 256 rows by 2 us).
 struct RowPart {
   int n, tag;
 };
-template <int NC, typename Rows, typename F>
-__device__ __forceinline__ void for_entries(const int32_t* tables, int64_t row_stride, int batch, int width,
+template <int NC, int AT_ONCE, typename Rows, typename F>
+__device__ __forceinline__ int for_entries(const int32_t* tables, int64_t row_stride, int batch, int width,
                                             uint32_t rank, Rows&& row_of, F&& f) {
-  constexpr int kWarpsAll = NC * kWarps;
+  constexpr int kWarpsAll = NC * kWarps, kPiece = 512 / AT_ONCE;
   const int lane = threadIdx.x & 31;
   const int pieces = (width + kPiece - 1) / kPiece;
   const int64_t items = (int64_t)batch * pieces;
+  int flags = 0;
   for (int64_t item = (int64_t)(threadIdx.x >> 5) * NC + rank; item < items; item += 32 * kWarpsAll) {
     const int64_t mine = item + (int64_t)lane * kWarpsAll;   // this lane's piece
     int b_of = 0, j_of = 0;
@@ -247,20 +249,29 @@ __device__ __forceinline__ void for_entries(const int32_t* tables, int64_t row_s
       j_of = (int)(mine % pieces) * kPiece;
       row = row_of(b_of);
     }
-    for (uint32_t todo = __ballot_sync(FULL, j_of < row.n); todo != 0u; todo &= todo - 1u) {
-      const int from_lane = __ffs(todo) - 1;
-      const int b = __shfl_sync(FULL, b_of, from_lane), n = __shfl_sync(FULL, row.n, from_lane);
-      const int tag = __shfl_sync(FULL, row.tag, from_lane), j0 = __shfl_sync(FULL, j_of, from_lane) + lane;
-      const int32_t* from = tables + b * row_stride;
-      int32_t x[kPiece / 32];
+    for (uint32_t todo = __ballot_sync(FULL, j_of < row.n); todo != 0u;) {
+      int b[AT_ONCE], n[AT_ONCE], tag[AT_ONCE], j0[AT_ONCE], x[AT_ONCE][kPiece / 32];
 #pragma unroll
-      for (int k = 0; k < kPiece / 32; ++k)
-        if (j0 + 32 * k < n) x[k] = from[j0 + 32 * k];
+      for (int i = 0; i < AT_ONCE; ++i) {   // none left: no entries
+        const int from_lane = todo != 0u ? __ffs(todo) - 1 : 0;
+        b[i] = __shfl_sync(FULL, b_of, from_lane);
+        n[i] = todo != 0u ? __shfl_sync(FULL, row.n, from_lane) : 0;
+        tag[i] = __shfl_sync(FULL, row.tag, from_lane);
+        j0[i] = __shfl_sync(FULL, j_of, from_lane) + lane;
+        todo &= todo - 1u;
+        const int32_t* from = tables + b[i] * row_stride;
 #pragma unroll
-      for (int k = 0; k < kPiece / 32; ++k)
-        if (j0 + 32 * k < n) f(b, tag, j0 + 32 * k, x[k]);
+        for (int k = 0; k < kPiece / 32; ++k)
+          if (j0[i] + 32 * k < n[i]) x[i][k] = from[j0[i] + 32 * k];
+      }
+#pragma unroll
+      for (int i = 0; i < AT_ONCE; ++i)
+#pragma unroll
+        for (int k = 0; k < kPiece / 32; ++k)
+          if (j0[i] + 32 * k < n[i]) flags |= f(b[i], tag[i], j0[i] + 32 * k, x[i][k]);
     }
   }
+  return flags;
 }
 
 // Two bits per page, held twice: marks of a CTA's own over a range of the pool, set by ordinary
@@ -269,7 +280,7 @@ __device__ __forceinline__ void for_entries(const int32_t* tables, int64_t row_s
 // the marks of all CTAs are joined.  A pool of more pages than the marks hold takes several
 // ranges, with the tables read once for each.  One CTA alone marks in its slice.
 struct PageBits {
-  uint32_t* slice[2];   // [per] words of this CTA's
+  uint32_t* slice[2];   // [per] words of this CTA's, one behind the other
   uint32_t* mark[2];    // [range] words, one behind the other
   uint32_t* spare[2];   // [per] words, or more; the marks are lost
   int per, words, range;   // per and range are whole vectors of four
@@ -302,7 +313,7 @@ __device__ __forceinline__ bool join_marks(const PageBits& p, int first, uint32_
   bool twice = false;
   for (int i = threadIdx.x; i < (w1 - w0 + 3) / 4 * 2; i += kThreads) {
     const int kind = i & 1, w = w0 + (i >> 1) * 4;
-    const uint32_t at = smem_u32(p.mark[kind] + (w - first));
+    const uint32_t at = smem_u32(p.mark[0] + kind * p.range + (w - first));
     uint4 x[NC];
 #pragma unroll
     for (int r = 0; r < NC; ++r) x[r] = load_remote4(map_to_rank(at, (rank + (uint32_t)r) % NC));
@@ -317,7 +328,7 @@ __device__ __forceinline__ bool join_marks(const PageBits& p, int first, uint32_
       any.w |= x[r].w;
     }
     if (TWICE && kind == 1 && again != 0u) twice = true;
-    *reinterpret_cast<uint4*>(p.slice[kind] + (w - mine)) = any;
+    *reinterpret_cast<uint4*>(p.slice[0] + kind * p.per + (w - mine)) = any;
   }
   return twice;
 }
@@ -370,16 +381,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv_free_kernel(const __grid_const
       clear_marks(bits);
       __syncthreads();
     }
-    for_entries<NC>(a.tables, a.row_stride, a.batch, a.width, rank,
-                [&](int b) {
-                  return RowPart{pages_of(__ldg(a.kv_lens + b), a.page_size),
-                                 (released[b >> 5] >> (b & 31) & 1u) ? bits.range : 0};   // which marks
-                },
-                [&](int, int tag, int, int page) {
-                  const int w = (page >> 5) - first;
-                  if (page < 0 || page >= a.num_pages) raise_flag<NC>(board, STATUS_PAGE_BOUNDS);
-                  else if (w >= 0 && w < bits.range) atomicOr(bits.mark[0] + tag + w, 1u << (page & 31));
-                });
+    const int found = for_entries<NC, NC == 1 ? 1 : 2>(
+        a.tables, a.row_stride, a.batch, a.width, rank,
+        [&](int b) {
+          return RowPart{pages_of(__ldg(a.kv_lens + b), a.page_size),
+                         (released[b >> 5] >> (b & 31) & 1u) ? bits.range : 0};   // which marks
+        },
+        [&](int, int tag, int, int page) -> int {
+          const int w = (page >> 5) - first;
+          if ((uint32_t)page >= (uint32_t)a.num_pages) return STATUS_PAGE_BOUNDS;
+          if ((uint32_t)w < (uint32_t)bits.range) atomicOr(bits.mark[0] + tag + w, 1u << (page & 31));
+          return 0;
+        });
+    if (found != 0) raise_flag<NC>(board, found);
     sync_all<NC>();
     if constexpr (NC > 1) {
       join_marks<NC, false>(bits, first, rank);
@@ -461,17 +475,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv_compact_kernel(const __grid_co
       clear_marks(bits);
       __syncthreads();
     }
-    for_entries<NC>(a.tables, a.row_stride, a.batch, a.width, rank, entries_of, [&](int, int, int, int page) {
+    int found = for_entries<NC, 1>(a.tables, a.row_stride, a.batch, a.width, rank, entries_of, [&](int, int, int, int page) -> int {
       const int w = (page >> 5) - first;
-      if (page < 0 || page >= a.num_pages) raise_flag<NC>(board, STATUS_PAGE_BOUNDS);
-      else if (w >= 0 && w < bits.range) atomicOr(bits.mark[0] + w, 1u << (page & 31));
+      if ((uint32_t)page >= (uint32_t)a.num_pages) return STATUS_PAGE_BOUNDS;
+      if ((uint32_t)w < (uint32_t)bits.range) atomicOr(bits.mark[0] + w, 1u << (page & 31));
+      return 0;
     });
     for (int64_t i = head + (int64_t)rank * kThreads + tid; i < a.num_free; i += NC * kThreads) {
       const int page = a.free_pages[i], w = (page >> 5) - first;
-      if (page < 0 || page >= a.num_pages) raise_flag<NC>(board, STATUS_PAGE_BOUNDS);
+      if (page < 0 || page >= a.num_pages) found |= STATUS_PAGE_BOUNDS;
       else if (w >= 0 && w < bits.range && (atomicOr(bits.mark[1] + w, 1u << (page & 31)) >> (page & 31) & 1u))
-        raise_flag<NC>(board, STATUS_FREE_LIST);
+        found |= STATUS_FREE_LIST;
     }
+    if (found != 0) raise_flag<NC>(board, found);
     sync_all<NC>();
     if constexpr (NC > 1) {
       if (join_marks<NC, true>(bits, first, rank)) raise_flag<NC>(board, STATUS_FREE_LIST);
@@ -571,22 +587,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv_compact_kernel(const __grid_co
         const int kind = i & 1, w = first + (i >> 1) * 4;
         if (w < bits.words) {
           const int owner = w / words;
-          *reinterpret_cast<uint4*>(bits.mark[kind] + (w - first)) =
-              load_remote4(map_to_rank(smem_u32(bits.slice[kind] + (w - owner * words)), (uint32_t)owner));
+          *reinterpret_cast<uint4*>(bits.mark[0] + kind * bits.range + (w - first)) =
+              load_remote4(map_to_rank(smem_u32(bits.slice[0] + kind * bits.per + (w - owner * words)), (uint32_t)owner));
         }
       }
       if (NC > 1) __syncthreads();
-      for_entries<NC>(a.tables, a.row_stride, a.batch, a.width, rank, [&](int b) { return RowPart{a.width, flags == 0 ? entries_of(b).n : 0}; },
-                  [&](int b, int tag, int j, int page) {
+      for_entries<NC, 1>(a.tables, a.row_stride, a.batch, a.width, rank, [&](int b) { return RowPart{a.width, flags == 0 ? entries_of(b).n : 0}; },
+                  [&](int b, int tag, int j, int page) -> int {
                     const bool live = j < tag;
                     const int w = live ? (page >> 5) - first : 0;
-                    if (live ? w < 0 || w >= bits.range : first > 0) return;   // another range's
+                    if (live ? w < 0 || w >= bits.range : first > 0) return 0;   // another range's
                     int to = page;
                     if (live) {
                       const uint32_t word = bits.mark[0][w], bit = 1u << (page & 31);
                       if (word & bit) to = __ldcg(a.dst_pages + bits.mark[1][w] + __popc(word & (bit - 1u)));
                     }
                     if (!in_place || to != page) a.tables_out[b * a.out_row_stride + j] = to;
+                    return 0;
                   });
     }
   }
