@@ -78,73 +78,91 @@ int read_status(int32_t* d_status, cudaStream_t stream) {
 
 using namespace pka;
 
-int pka::upload_decode_plan(pka_plan& p, cudaStream_t stream) {
-  const size_t n_items = p.items.size() * sizeof(WorkItem);
-  const size_t n_reqs = p.reqs.size() * sizeof(ReqInfo);
-  const size_t n_cnt = (size_t)p.num_merge_counters * sizeof(int32_t);
+namespace {
+
+// Puts the arrays of `next` on the device, in the buffers of `old` or, where they do not fit, in
+// larger ones; `next` then has the buffers and `old` none.  Where anything fails `old` stays the
+// plan that it was, on the device too, and `next` has none.
+int place_decode_plan(pka_plan& next, pka_plan& old, cudaStream_t stream) {
+  const size_t n_items = next.items.size() * sizeof(WorkItem);
+  const size_t n_reqs = next.reqs.size() * sizeof(ReqInfo);
+  const size_t n_cnt = (size_t)next.num_merge_counters * sizeof(int32_t);
   const size_t off_reqs = up256(n_items);
   const size_t off_status = off_reqs + up256(n_reqs);
   const size_t off_cnt = off_status + 256;   // merge counters, zero between runs
   const size_t total = off_cnt + up256(n_cnt);
-  if (p.dev_buf == nullptr || total > p.dev_capacity) {
-    // a replan that outgrows the buffer reallocates it with headroom
-    if (p.dev_buf != nullptr) {
-      PKA_CUDA_TRY(cudaFree(p.dev_buf), "cudaFree(decode plan)");
-      p.dev_buf = nullptr;
-      p.dev_capacity = 0;
-    }
-    const size_t cap = p.dev_capacity == 0 && total < 4096 ? 4096 : total + total / 2;
-    PKA_CUDA_TRY(cudaGetDevice(&p.device), "cudaGetDevice");
-    PKA_CUDA_TRY(cudaMalloc(&p.dev_buf, cap), "cudaMalloc(decode plan)");
-    p.dev_capacity = cap;
-  }
-  uint8_t* base = static_cast<uint8_t*>(p.dev_buf);
-  p.d_items = reinterpret_cast<const WorkItem*>(base);
-  p.d_reqs = reinterpret_cast<const ReqInfo*>(base + off_reqs);
-  p.d_status = reinterpret_cast<int32_t*>(base + off_status);
-  p.d_merge_cnt = reinterpret_cast<int32_t*>(base + off_cnt);
   // One asynchronous copy from a pinned image of the buffer.  The image is
   // rewritten only after the copy that last read it has completed (stage_done);
   // stream order keeps the upload behind runs already queued on the same stream.
-  if (p.host_stage != nullptr && p.stage_done != nullptr)
-    PKA_CUDA_TRY(cudaEventSynchronize(p.stage_done), "cudaEventSynchronize(plan upload)");
-  if (p.host_stage == nullptr || total > p.host_capacity) {
-    if (p.host_stage != nullptr) {
-      PKA_CUDA_TRY(cudaFreeHost(p.host_stage), "cudaFreeHost(plan image)");
-      p.host_stage = nullptr;
-      p.host_capacity = 0;
-    }
-    if (cudaMallocHost(&p.host_stage, p.dev_capacity) == cudaSuccess) {
-      p.host_capacity = p.dev_capacity;
-    } else {
-      (void)cudaGetLastError();   // no pinned memory: copy from the pageable vectors
-      p.host_stage = nullptr;
+  if (old.stage_done == nullptr)
+    PKA_CUDA_TRY(cudaEventCreateWithFlags(&old.stage_done, cudaEventDisableTiming), "cudaEventCreate(plan upload)");
+  else
+    PKA_CUDA_TRY(cudaEventSynchronize(old.stage_done), "cudaEventSynchronize(plan upload)");
+  void* dev_buf = old.dev_buf;
+  size_t dev_capacity = old.dev_capacity;
+  int device = old.device;
+  const bool grow = dev_buf == nullptr || total > dev_capacity;
+  if (grow) {   // with headroom for later updates
+    dev_capacity = dev_buf == nullptr && total < 4096 ? 4096 : total + total / 2;
+    PKA_CUDA_TRY(cudaGetDevice(&device), "cudaGetDevice");
+    PKA_CUDA_TRY(cudaMalloc(&dev_buf, dev_capacity), "cudaMalloc(decode plan)");
+  }
+  void* host_stage = old.host_stage;
+  size_t host_capacity = old.host_capacity;
+  const bool new_stage = host_stage == nullptr || total > host_capacity;
+  std::unique_ptr<uint8_t[]> pageable;
+  if (new_stage) {
+    host_capacity = dev_capacity;
+    if (cudaMallocHost(&host_stage, host_capacity) != cudaSuccess) {
+      (void)cudaGetLastError();   // no pinned memory: a copy from pageable memory has read it when the call returns
+      host_stage = nullptr;
+      host_capacity = 0;
+      pageable.reset(new (std::nothrow) uint8_t[total]);
+      if (pageable == nullptr) {
+        if (grow) (void)cudaFree(dev_buf);
+        return fail(PKA_ERR_INVALID_ARG, "out of host memory");
+      }
     }
   }
-  if (p.host_stage != nullptr) {
-    uint8_t* img = static_cast<uint8_t*>(p.host_stage);
-    if (n_items) std::memcpy(img, p.items.data(), n_items);
-    std::memcpy(img + off_reqs, p.reqs.data(), n_reqs);
-    std::memset(img + off_status, 0, total - off_status);   // status word and counters
-    PKA_CUDA_TRY(cudaMemcpyAsync(base, img, total, cudaMemcpyHostToDevice, stream),
-                 "cudaMemcpyAsync(plan)");
-    if (p.stage_done == nullptr)
-      PKA_CUDA_TRY(cudaEventCreateWithFlags(&p.stage_done, cudaEventDisableTiming),
-                   "cudaEventCreate(plan upload)");
-    PKA_CUDA_TRY(cudaEventRecord(p.stage_done, stream), "cudaEventRecord(plan upload)");
-    return PKA_OK;
+  uint8_t* img = host_stage != nullptr ? static_cast<uint8_t*>(host_stage) : pageable.get();
+  if (n_items) std::memcpy(img, next.items.data(), n_items);
+  std::memcpy(img + off_reqs, next.reqs.data(), n_reqs);
+  std::memset(img + off_status, 0, total - off_status);   // status word and counters
+  const cudaError_t e = cudaMemcpyAsync(dev_buf, img, total, cudaMemcpyHostToDevice, stream);
+  if (e != cudaSuccess) {
+    const int rc = cuda_fail(e, "cudaMemcpyAsync(plan)");
+    if (grow) (void)cudaFree(dev_buf);
+    if (new_stage) (void)cudaFreeHost(host_stage);
+    return rc;
   }
-  // Copies from pageable host vectors are staged before cudaMemcpyAsync returns,
-  // so a later replan may overwrite them.
-  if (n_items)
-    PKA_CUDA_TRY(cudaMemcpyAsync(base, p.items.data(), n_items, cudaMemcpyHostToDevice, stream),
-                 "cudaMemcpyAsync(plan items)");
-  PKA_CUDA_TRY(cudaMemcpyAsync(base + off_reqs, p.reqs.data(), n_reqs, cudaMemcpyHostToDevice,
-                               stream),
-               "cudaMemcpyAsync(plan requests)");
-  PKA_CUDA_TRY(cudaMemsetAsync(base + off_status, 0, total - off_status, stream),
-               "cudaMemsetAsync(status and counters)");
+  // from here on the device has the new plan; a copy that no event follows is waited for
+  if (host_stage != nullptr && cudaEventRecord(old.stage_done, stream) != cudaSuccess) {
+    (void)cudaGetLastError();
+    (void)cudaStreamSynchronize(stream);
+  }
+  if (grow && cudaFree(old.dev_buf) != cudaSuccess) (void)cudaGetLastError();
+  if (new_stage && cudaFreeHost(old.host_stage) != cudaSuccess) (void)cudaGetLastError();
+  old.dev_buf = dev_buf;
+  old.dev_capacity = dev_capacity;
+  old.device = device;
+  old.host_stage = host_stage;
+  old.host_capacity = host_capacity;
+  keep_decode_buffers(next, old);
+  uint8_t* base = static_cast<uint8_t*>(next.dev_buf);
+  next.d_items = reinterpret_cast<const WorkItem*>(base);
+  next.d_reqs = reinterpret_cast<const ReqInfo*>(base + off_reqs);
+  next.d_status = reinterpret_cast<int32_t*>(base + off_status);
+  next.d_merge_cnt = reinterpret_cast<int32_t*>(base + off_cnt);
   return PKA_OK;
+}
+
+}  // namespace
+
+int pka::upload_decode_plan(pka_plan& p, cudaStream_t stream) {
+  pka_plan none;
+  const int rc = place_decode_plan(p, none, stream);
+  release_decode_plan(none);   // where it failed
+  return rc;
 }
 
 void pka::keep_decode_buffers(pka_plan& plan, pka_plan& from) {
@@ -160,14 +178,13 @@ void pka::keep_decode_buffers(pka_plan& plan, pka_plan& from) {
 }
 
 int pka::replace_decode_plan(pka_plan& p, pka_plan&& fresh, cudaStream_t stream) {
-  const bool host_only = p.desc.flags & PKA_PLAN_HOST_ONLY;
-  if (!host_only) {
-    const int rc = check_device(p.device);
+  if (!(p.desc.flags & PKA_PLAN_HOST_ONLY)) {
+    int rc = check_device(p.device);
+    if (rc == PKA_OK) rc = place_decode_plan(fresh, p, stream);
     if (rc != PKA_OK) return rc;
   }
-  keep_decode_buffers(fresh, p);
   p = std::move(fresh);
-  return host_only ? PKA_OK : upload_decode_plan(p, stream);
+  return PKA_OK;
 }
 
 void pka::release_decode_plan(pka_plan& p) {

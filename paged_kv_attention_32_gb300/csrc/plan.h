@@ -114,10 +114,11 @@ namespace pka {
 int build_decode_plan(pka_plan& plan, const pka_decode_desc& desc, const int32_t* seq_lens_kv,
                       const int32_t* qo_indptr);
 
-// Puts the plan's arrays on the device, in the plan's buffers.
+// Puts the arrays of a plan without buffers on the device; the plan has none where that fails.
 int upload_decode_plan(pka_plan& plan, cudaStream_t stream);
 
-// Rebuilt arrays `fresh` into the plan's buffers and `plan` (paged_decode_plan_update).
+// Makes `fresh`, whose host arrays are built, the plan, in the plan's buffers or larger ones
+// (paged_decode_plan_update).  Where anything fails the plan stays as it was.
 int replace_decode_plan(pka_plan& plan, pka_plan&& fresh, cudaStream_t stream);
 
 // Gives `plan` the buffers of `from`, which keeps none.

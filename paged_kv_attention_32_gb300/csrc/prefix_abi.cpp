@@ -80,8 +80,8 @@ int install_prefix_plan(pka_prefix_plan& p, pka_prefix_plan&& next, cudaStream_t
     e = cudaStreamSynchronize(stream);
   }
   if (grow) {
-    cudaFree(p.dev_buf);
-    cudaFreeHost(p.host_stage);
+    if (cudaFree(p.dev_buf) != cudaSuccess) (void)cudaGetLastError();
+    if (cudaFreeHost(p.host_stage) != cudaSuccess) (void)cudaGetLastError();
   }
   keep_decode_buffers(next.base, p.base);   // for a batch that shares nothing
   p = std::move(next);
@@ -109,14 +109,12 @@ int make_prefix_plan(pka_prefix_plan& p, const pka_decode_desc& desc, const int3
       return rc;
     }
     p.base = std::move(next.base);
-    p.shared = false;
   } else {
     rc = check_device(p.base.device);
-    if (rc != PKA_OK) return rc;
-    p.shared = false;   // as base says, also where its upload fails
-    rc = replace_decode_plan(p.base, std::move(next.base), stream);
+    if (rc == PKA_OK) rc = replace_decode_plan(p.base, std::move(next.base), stream);
     if (rc != PKA_OK) return rc;
   }
+  p.shared = false;   // only now: what fails leaves the plan as it was
   p.min_shared_bytes = next.min_shared_bytes;
   p.items.clear();
   p.pieces.clear();
