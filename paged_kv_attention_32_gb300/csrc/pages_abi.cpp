@@ -83,7 +83,7 @@ int paged_rope_append(const void* q, int64_t q_stride_tok, int64_t q_stride_head
                 "rotary_dim must be a multiple of 16 in [0, head_dim] (got %d)", rotary_dim);
   RopeArgs a{};
   if (rotary_dim > 0) {
-    PKA_CHECK_ARG(positions != nullptr && inv_freq != nullptr && sections_host != nullptr,
+    PKA_CHECK_ARG((num_tokens == 0 || positions != nullptr) && inv_freq != nullptr && sections_host != nullptr,
                   "a rotation needs positions, inv_freq and sections");
     PKA_CHECK_ARG(pairs == PKA_ROPE_HALVES || pairs == PKA_ROPE_NEIGHBOURS, "unknown pairs %d", pairs);
     PKA_CHECK_ARG(num_axes >= 1 && num_axes <= kRopeAxes, "num_axes must be in [1, %d] (got %d)", kRopeAxes, num_axes);
