@@ -1,6 +1,8 @@
 // extern "C" entry points of the page pool: argument checks and launches.
+#include <algorithm>
 #include <climits>
 #include <initializer_list>
+#include <utility>
 
 #include "host_common.h"
 #include "pages.h"
@@ -49,6 +51,31 @@ int check_pool_pages(int64_t num_pages) {
   if (num_pages > kPageOpPages)
     return fail(PKA_ERR_UNSUPPORTED, "num_pages %lld is above %lld", (long long)num_pages, (long long)kPageOpPages);
   return PKA_OK;
+}
+
+// Whether at + i * step lies within (-row, row) for an i with |i| < n, not 0 where `other` is set.
+bool step_hits(__int128 at, int64_t n, int64_t step, int64_t row, bool other) {
+  const auto hits = [&](__int128 i) {
+    i = std::max<__int128>(-(__int128)(n - 1), std::min<__int128>(i, n - 1));
+    const __int128 d = at + i * step;
+    return (i != 0 || !other) && d > -(__int128)row && d < row;
+  };
+  const __int128 q = step > 0 ? -at / step : 0;   // the sum is nearest to 0 at q or beside it
+  return hits(q - 1) || hits(q) || hits(q + 1);
+}
+
+// Whether two of n x m rows of `row` elements, at i * outer + j * inner, share an element: at once where one
+// stride has room for all of the other's rows, else in a step for each of the smaller count.
+bool rows_meet(int64_t n, int64_t outer, int64_t m, int64_t inner, int64_t row) {
+  if (n > m) {
+    std::swap(n, m);
+    std::swap(outer, inner);
+  }
+  if (n > 1 && m > 1 && inner >= row && outer >= (__int128)(m - 1) * inner + row) return false;
+  if (n > 1 && m > 1 && outer >= row && inner >= (__int128)(n - 1) * outer + row) return false;
+  for (int64_t i = 0; i < n; ++i)   // two rows that are i apart along the one, anything along the other
+    if (step_hits((__int128)i * outer, m, inner, row, i == 0)) return true;
+  return false;
 }
 
 }  // namespace
@@ -108,16 +135,13 @@ int paged_rope_append(const void* q, int64_t q_stride_tok, int64_t q_stride_head
                     aligned(v_pages, 16) && aligned(slot_map, 8) && aligned(status, 4),
                 "q, k, v and the pools must be 16-byte aligned, slot_map 8-byte aligned");
   if (num_tokens == 0) return PKA_OK;
-  // what is written: no row of it twice
-  auto rows_apart = [](int64_t n, int64_t outer, int64_t m, int64_t inner, int64_t row) {
-    return (n <= 1 || outer >= row) && (m <= 1 || inner >= row);
-  };
-  PKA_CHECK_ARG(rows_apart(num_pages, stride_page, num_kv_heads, stride_head, (int64_t)page_size * head_dim),
+  // what is written: no element of it twice
+  PKA_CHECK_ARG(!rows_meet(num_pages, stride_page, num_kv_heads, stride_head, (int64_t)page_size * head_dim),
                 "pages of %d rows overlap: stride_page %lld, stride_head %lld", page_size, (long long)stride_page,
                 (long long)stride_head);
   PKA_CHECK_ARG(k_pages != v_pages, "k_pages and v_pages must be two pools");
   if (q != nullptr) {
-    PKA_CHECK_ARG(rows_apart(num_tokens, q_out_stride_tok, num_qo_heads, q_out_stride_head, head_dim),
+    PKA_CHECK_ARG(!rows_meet(num_tokens, q_out_stride_tok, num_qo_heads, q_out_stride_head, head_dim),
                   "rows of q_out overlap");
     auto range = [&](const void* p, int64_t tok, int64_t head, int32_t heads) -> Range {
       return {p, (size_t)((num_tokens - 1) * tok + (heads - 1) * head + head_dim) * 2};

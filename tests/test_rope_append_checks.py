@@ -1,4 +1,12 @@
-"""What the rotated append takes and refuses on the host, beyond single arguments (no GPU needed)."""
+"""What the rotated append takes and refuses on the host, beyond single arguments (no GPU needed).
+
+A call that is taken would go on to the launch; without a GPU that fails with PKA_ERR_CUDA, and where
+there is one nothing may run at these addresses, so such calls are made without a GPU only."""
+
+import random
+
+import pytest
+import torch
 
 from paged_kv_attention_32_gb300 import _lib as L
 from tests.test_pages_binding import rope
@@ -12,3 +20,49 @@ def test_no_tokens_need_no_positions():
     # what the call would rotate by is looked at all the same
     for kw in (dict(freq=None), dict(sections=None), dict(axes=0), dict(pairs=2)):
         assert rope(**(none | kw)) == L.PKA_ERR_INVALID_ARG
+
+
+def rows_meet(n, outer, m, inner, row):
+    """By listing all rows."""
+    starts = sorted(i * outer + j * inner for i in range(n) for j in range(m))
+    return any(b - a < row for a, b in zip(starts, starts[1:]))
+
+
+# tokens, token stride, heads, head stride of q_out (rows of 128), or pages and heads of pools (rows of 2048)
+LAYOUTS = [
+    (5, 128, 3, 128), (5, 256, 3, 128), (5, 384, 3, 128), (5, 392, 3, 128), (3, 128, 5, 384), (3, 128, 5, 256),
+    (4, 256, 4, 384), (3, 256, 3, 384), (2, 256, 5, 384), (4, 640, 3, 256), (4, 120, 1, 0), (1, 0, 4, 120),
+    (1, 0, 4, 128), (4, 128, 1, 0), (1, 8, 1, 8), (2, 0, 3, 128), (3, 128, 2, 0), (3, 136, 2, 4096), (100, 130 * 8, 9, 128),
+]
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="a call that is taken would run at these addresses")
+@pytest.mark.parametrize("pools", [False, True])
+def test_rows_written_twice(pools):
+    """Outputs are refused where two of their rows share an element, and nowhere else."""
+    r = random.Random(3)
+    drawn = [(r.randint(1, 7), 8 * r.randint(0, 160), r.randint(1, 7), 8 * r.randint(0, 160)) for _ in range(400)]
+    seen = set()
+    for n, outer, m, inner in LAYOUTS + drawn:
+        if pools:
+            outer, inner = 16 * outer, 16 * inner
+            kw = dict(Hq=0, q=None, q_out=None, Hkv=m, pages=n, page=outer, head=inner, kp=1 << 40, vp=1 << 50)
+            want = rows_meet(n, outer, m, inner, 2048)
+        else:
+            kw = dict(T=n, Hq=m, q_out=1 << 40, o_tok=outer, o_head=inner)
+            want = rows_meet(n, outer, m, inner, 128)
+        code = rope(**kw)
+        assert (code == L.PKA_ERR_INVALID_ARG) == want, (n, outer, m, inner, code)
+        seen.add(want)
+    assert seen == {True, False}
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="a call that is taken would run at these addresses")
+def test_rows_of_the_largest_layouts():
+    """Strides and counts whose products pass 64 bits, and the longest search."""
+    far = dict(Hq=0, q=None, q_out=None, kp=1 << 40, vp=1 << 50)
+    assert rope(**far, pages=2 ** 31 - 1, Hkv=65536, page=2 ** 62, head=2 ** 61) == L.PKA_ERR_INVALID_ARG
+    assert rope(**far, pages=2 ** 31 - 1, Hkv=3, page=2 ** 62, head=2 ** 60) != L.PKA_ERR_INVALID_ARG
+    # heads a page and a half apart over pages: rows meet only where three pages are two heads
+    assert rope(**far, pages=2 ** 31 - 1, Hkv=65536, page=4096, head=6144) == L.PKA_ERR_INVALID_ARG
+    assert rope(**far, pages=3, Hkv=65536, page=4096, head=6144) != L.PKA_ERR_INVALID_ARG
