@@ -78,6 +78,35 @@ bool rows_meet(int64_t n, int64_t outer, int64_t m, int64_t inner, int64_t row) 
   return false;
 }
 
+// n x m rows of `row` units of 16 bits, at p + i * outer + j * inner.
+struct Rows {
+  const void* p;
+  int64_t n, outer, m, inner, row;
+};
+__int128 apart(const Rows& x, const Rows& y) {
+  return ((__int128)reinterpret_cast<uintptr_t>(y.p) - (__int128)reinterpret_cast<uintptr_t>(x.p)) / 2;
+}
+__int128 last(int64_t n, int64_t stride) { return (__int128)(n - 1) * stride; }   // where the last of n begins
+
+// Whether rows of x and of y, which are laid out alike, share a unit.
+bool pools_meet(const Rows& x, const Rows& y) {
+  const __int128 d = apart(x, y);
+  const __int128 inner = last(x.m, x.inner) + x.row, outer = last(x.n, x.outer) + x.row;   // along one of them
+  if ((d < 0 ? -d : d) >= inner + outer - x.row) return false;
+  // what is in turn along one stride: y's between x's all along
+  const auto between = [&](int64_t stride, __int128 size) {
+    if (stride <= 0) return false;
+    const int64_t at = (int64_t)(((int64_t)d % stride + stride) % stride);
+    return at >= size && at + size <= stride;
+  };
+  if (between(x.outer, inner) || between(x.inner, outer)) return false;
+  const bool few = x.n < x.m;   // in a step for each of the smaller count, and back
+  const int64_t n = few ? x.n : x.m, far = few ? x.outer : x.inner, m = few ? x.m : x.n, step = few ? x.inner : x.outer;
+  for (int64_t i = 1 - n; i < n; ++i)
+    if (step_hits(d + (__int128)i * far, m, step, x.row, false)) return true;
+  return false;
+}
+
 }  // namespace
 
 extern "C" {
@@ -139,7 +168,10 @@ int paged_rope_append(const void* q, int64_t q_stride_tok, int64_t q_stride_head
   PKA_CHECK_ARG(!rows_meet(num_pages, stride_page, num_kv_heads, stride_head, (int64_t)page_size * head_dim),
                 "pages of %d rows overlap: stride_page %lld, stride_head %lld", page_size, (long long)stride_page,
                 (long long)stride_head);
-  PKA_CHECK_ARG(k_pages != v_pages, "k_pages and v_pages must be two pools");
+  const auto pool = [&](const void* p) {
+    return Rows{p, num_pages, stride_page, num_kv_heads, stride_head, (int64_t)page_size * head_dim};
+  };
+  PKA_CHECK_ARG(!pools_meet(pool(k_pages), pool(v_pages)), "k_pages and v_pages overlap");
   if (q != nullptr) {
     PKA_CHECK_ARG(!rows_meet(num_tokens, q_out_stride_tok, num_qo_heads, q_out_stride_head, head_dim),
                   "rows of q_out overlap");

@@ -66,3 +66,35 @@ def test_rows_of_the_largest_layouts():
     # heads a page and a half apart over pages: rows meet only where three pages are two heads
     assert rope(**far, pages=2 ** 31 - 1, Hkv=65536, page=4096, head=6144) == L.PKA_ERR_INVALID_ARG
     assert rope(**far, pages=3, Hkv=65536, page=4096, head=6144) != L.PKA_ERR_INVALID_ARG
+
+
+def starts(at, n, outer, m, inner):
+    return [at + i * outer + j * inner for i in range(n) for j in range(m)]
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="a call that is taken would run at these addresses")
+def test_pools_that_share_rows():
+    """Key and value pools are refused where a page's rows of the one are rows of the other, and taken where
+    they lie between each other: halves of a page, of a head, of the whole, alternating heads."""
+    r = random.Random(5)
+    row = 2048   # 16 slots of 128 values
+    seen = set()
+    named = [(5, 2 * 3 * row, 3, row, 3 * row, False), (5, 6 * row, 3, 2 * row, row, False), (5, 3 * row, 3, row, 15 * row, False),
+             (4, row, 3, 8 * row, 4 * row, False), (4, 2 * row, 3, 8 * row, row, False),
+             (5, 3 * row, 3, row, 12 * row, True), (5, 3 * row, 3, row, row, True), (5, 3 * row, 3, row, 8, True),
+             (5, 6 * row, 3, row, 3 * row - 8, True), (1, 0, 1, 0, row, False), (1, 8, 1, 8, row - 8, True)]
+    named += [
+        (r.randint(1, 6), r.choice([128, 8, 1]) * 8 * r.randint(0, 200), r.randint(1, 6),
+         r.choice([128, 8, 1]) * 8 * r.randint(0, 200), r.choice([128, 8, 1]) * 8 * r.randint(-400, 400), None)
+        for _ in range(3000)]
+    for n, outer, m, inner, at, meet in named:
+        if rows_meet(n, outer, m, inner, row):
+            continue
+        k, v = sorted(starts(0, n, outer, m, inner)), starts(at, n, outer, m, inner)
+        want = any(abs(x - y) < row for x in k for y in v)
+        assert meet is None or meet == want
+        base = 1 << 40
+        code = rope(Hq=0, q=None, q_out=None, Hkv=m, pages=n, page=outer, head=inner, kp=base, vp=base + 2 * at)
+        assert (code == L.PKA_ERR_INVALID_ARG) == want, (n, outer, m, inner, at, code)
+        seen.add(want)
+    assert seen == {True, False}
