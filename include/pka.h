@@ -737,9 +737,8 @@ int pka_status_check(int32_t* status_dev, void* stream);
  * q            NULL (num_qo_heads 0) or rows [num_tokens] x [num_qo_heads] x D,
  *              (t, h, d) at q + t*q_stride_tok + h*q_stride_head + d; written
  *              rotated to q_out, which has strides of its own and may be q
- *              itself (same strides) but not overlap it otherwise.
- * k, v         rows [num_tokens] x [num_kv_heads] x D, one set of strides; not
- *              in the pools, nor overlapped by q_out.
+ *              itself (same strides).
+ * k, v         rows [num_tokens] x [num_kv_heads] x D, one set of strides.
  * head_dim     D; must be 128.
  * positions    int32 [num_axes, num_tokens] device, rows positions_stride
  *              apart: each token's position on every axis (one axis: its place in the
@@ -758,6 +757,8 @@ int pka_status_check(int32_t* status_dev, void* stream);
  *              page_size does too and sets the slot bit of the status word
  *              (PKA_ERR_DEVICE_BOUNDS).  Entries must be distinct.
  * k_pages, v_pages, stride_page, stride_head  HND pools as for paged_decode_run.
+ * What is written (q_out, both pools) has no element twice and none of an input but
+ * q_out of q; rows that only lie between others' rows are fine.  Else PKA_ERR_INVALID_ARG.
  * dtype        PKA_DTYPE_BF16 or PKA_DTYPE_F16: q, q_out, k, v and the pools, all
  *              16-byte aligned with strides that are multiples of 8.
  * status       NULL or int32 [1] device status word (pka_status_check).

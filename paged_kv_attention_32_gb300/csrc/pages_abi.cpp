@@ -88,22 +88,39 @@ __int128 apart(const Rows& x, const Rows& y) {
 }
 __int128 last(int64_t n, int64_t stride) { return (__int128)(n - 1) * stride; }   // where the last of n begins
 
-// Whether rows of x and of y, which are laid out alike, share a unit.
-bool pools_meet(const Rows& x, const Rows& y) {
+// Whether rows of x and of y share a unit.
+bool rows_meet(const Rows& x, const Rows& y) {
   const __int128 d = apart(x, y);
-  const __int128 inner = last(x.m, x.inner) + x.row, outer = last(x.n, x.outer) + x.row;   // along one of them
-  if ((d < 0 ? -d : d) >= inner + outer - x.row) return false;
-  // what is in turn along one stride: y's between x's all along
-  const auto between = [&](int64_t stride, __int128 size) {
-    if (stride <= 0) return false;
-    const int64_t at = (int64_t)(((int64_t)d % stride + stride) % stride);
-    return at >= size && at + size <= stride;
+  const __int128 end_x = last(x.n, x.outer) + last(x.m, x.inner) + x.row;
+  const __int128 end_y = last(y.n, y.outer) + last(y.m, y.inner) + y.row;
+  if (d >= end_x || -d >= end_y) return false;
+  // in turn along a stride that both have: y's between x's all along
+  const auto between = [&](int64_t stride, __int128 size_x, __int128 size_y) {
+    const int64_t at = (int64_t)((d % stride + stride) % stride);
+    return at >= size_x && at + size_y <= stride;
   };
-  if (between(x.outer, inner) || between(x.inner, outer)) return false;
-  const bool few = x.n < x.m;   // in a step for each of the smaller count, and back
-  const int64_t n = few ? x.n : x.m, far = few ? x.outer : x.inner, m = few ? x.m : x.n, step = few ? x.inner : x.outer;
-  for (int64_t i = 1 - n; i < n; ++i)
-    if (step_hits(d + (__int128)i * far, m, step, x.row, false)) return true;
+  if (x.outer == y.outer && x.outer > 0 && between(x.outer, last(x.m, x.inner) + x.row, last(y.m, y.inner) + y.row))
+    return false;
+  if (x.inner == y.inner && x.inner > 0 && between(x.inner, last(x.n, x.outer) + x.row, last(y.n, y.outer) + y.row))
+    return false;
+  if (x.n == y.n && x.outer == y.outer && x.m == y.m && x.inner == y.inner && x.row == y.row) {
+    const bool few = x.n < x.m;   // in a step for each of the smaller count, and back
+    const int64_t n = few ? x.n : x.m, far = few ? x.outer : x.inner, m = few ? x.m : x.n, step = few ? x.inner : x.outer;
+    for (int64_t i = 1 - n; i < n; ++i)
+      if (step_hits(d + (__int128)i * far, m, step, x.row, false)) return true;
+    return false;
+  }
+  // rows that lie in the other's gaps, or meet them: each of x with each of y's smaller count
+  const bool few = y.m < y.n;
+  const int64_t n = few ? y.m : y.n, far = few ? y.inner : y.outer, m = few ? y.n : y.m, step = few ? y.outer : y.inner;
+  for (int64_t i = 0; i < x.n; ++i)
+    for (int64_t j = 0; j < x.m; ++j)
+      for (int64_t k = 0; k < n; ++k) {
+        // the first of m rows, `step` apart from 0 on, that ends behind where x's begins
+        const __int128 at = (__int128)i * x.outer + (__int128)j * x.inner - d - (__int128)k * far;
+        const __int128 first = at < y.row || step == 0 ? 0 : (at - y.row) / step + 1;
+        if (first < m && first * step + y.row > at && first * step < at + x.row) return true;
+      }
   return false;
 }
 
@@ -171,20 +188,28 @@ int paged_rope_append(const void* q, int64_t q_stride_tok, int64_t q_stride_head
   const auto pool = [&](const void* p) {
     return Rows{p, num_pages, stride_page, num_kv_heads, stride_head, (int64_t)page_size * head_dim};
   };
-  PKA_CHECK_ARG(!pools_meet(pool(k_pages), pool(v_pages)), "k_pages and v_pages overlap");
+  const auto rows = [&](const void* p, int64_t tok, int64_t head, int32_t heads) {
+    return Rows{p, num_tokens, tok, heads, head, head_dim};
+  };
+  const Rows k_pool = pool(k_pages), v_pool = pool(v_pages), out = rows(q_out, q_out_stride_tok, q_out_stride_head, num_qo_heads);
+  PKA_CHECK_ARG(!rows_meet(k_pool, v_pool), "k_pages and v_pages overlap");
+  const Rows ins[] = {rows(q, q_stride_tok, q_stride_head, num_qo_heads),
+                      rows(k, kv_stride_tok, kv_stride_head, num_kv_heads),
+                      rows(v, kv_stride_tok, kv_stride_head, num_kv_heads),
+                      {slot_map, 1, 0, 1, 0, 4 * num_tokens},
+                      {rotary_dim > 0 ? positions : nullptr, num_axes, num_axes > 1 ? 2 * positions_stride : 0, 1, 0, 2 * num_tokens},
+                      {rotary_dim > 0 ? inv_freq : nullptr, 1, 0, 1, 0, 2 * (int64_t)rotary_dim},
+                      {status, 1, 0, 1, 0, 2}};
+  for (const Rows& in : ins)
+    PKA_CHECK_ARG(in.p == nullptr || (!rows_meet(in, k_pool) && !rows_meet(in, v_pool)), "an input lies in a pool");
   if (q != nullptr) {
     PKA_CHECK_ARG(!rows_meet(num_tokens, q_out_stride_tok, num_qo_heads, q_out_stride_head, head_dim),
                   "rows of q_out overlap");
-    auto range = [&](const void* p, int64_t tok, int64_t head, int32_t heads) -> Range {
-      return {p, (size_t)((num_tokens - 1) * tok + (heads - 1) * head + head_dim) * 2};
-    };
-    const Range out = range(q_out, q_out_stride_tok, q_out_stride_head, num_qo_heads);
-    // over q itself its rows may lie between those of k and v
-    if (q_out != q || q_out_stride_tok != q_stride_tok || q_out_stride_head != q_stride_head)
-      PKA_CHECK_ARG(!overlap(out, range(q, q_stride_tok, q_stride_head, num_qo_heads)) &&
-                        !overlap(out, range(k, kv_stride_tok, kv_stride_head, num_kv_heads)) &&
-                        !overlap(out, range(v, kv_stride_tok, kv_stride_head, num_kv_heads)),
-                    "q_out overlaps q, k or v without being q");
+    PKA_CHECK_ARG(!rows_meet(out, k_pool) && !rows_meet(out, v_pool), "q_out lies in a pool");
+    // q itself it may be, all of it
+    const bool in_place = q_out == q && q_out_stride_tok == q_stride_tok && q_out_stride_head == q_stride_head;
+    for (const Rows& in : ins)
+      PKA_CHECK_ARG(in.p == nullptr || (in_place && &in == ins) || !rows_meet(in, out), "q_out overlaps an input without being q");
   }
   a.q = q;
   a.q_stride_tok = q_stride_tok;

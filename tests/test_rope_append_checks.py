@@ -98,3 +98,56 @@ def test_pools_that_share_rows():
         assert (code == L.PKA_ERR_INVALID_ARG) == want, (n, outer, m, inner, at, code)
         seen.add(want)
     assert seen == {True, False}
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="a call that is taken would run at these addresses")
+def test_inputs_among_what_is_written():
+    """Inputs in a pool or under q_out are refused, by the byte; those in the gaps between rows are taken,
+    and so is q_out over all of q."""
+    def spans(at, n, outer, m, inner, size):
+        return [(x, x + size) for x in starts(at, n, 2 * outer, m, 2 * inner)]
+
+    r = random.Random(7)
+    K, V, Q, base = 1 << 40, 1 << 41, 1 << 42, 1 << 43   # apart from each other and from all else
+    seen = {}
+    for turn in range(6000):
+        T, Hq, Hkv, pages = (r.randint(1, 4) for _ in range(4))
+        step = lambda row: 8 * r.choice([row // 8, r.randint(row // 8, row // 2)])   # noqa: E731
+        page, head = (16 * 128 * Hkv + 8 * r.randint(0, 400), 16 * 128) if r.random() < 0.5 else (
+            16 * 128, 16 * 128 * pages + 8 * r.randint(0, 400))
+        kw = dict(T=T, Hq=Hq, Hkv=Hkv, pages=pages, page=page, head=head, kp=K, vp=V, q=base, k=base + (1 << 24),
+                  v=base + (2 << 24), pos=base + (3 << 24), freq=base + (4 << 24), slots=base + (5 << 24),
+                  status=base + (6 << 24), q_out=Q, axes=2, pos_row=T + r.randint(0, 9))
+        kw["q_head"], kw["o_head"], kw["kv_head"] = step(128), step(128), step(128)
+        for tok, h, n in (("q_tok", "q_head", Hq), ("o_tok", "o_head", Hq), ("kv_tok", "kv_head", Hkv)):
+            kw[tok] = kw[h] * (n - 1) + step(128)
+        name, align = r.choice([("q", 16), ("k", 16), ("v", 16), ("pos", 4), ("freq", 8), ("slots", 8), ("status", 4),
+                                ("q_out", 16)])
+        into = r.choice([K, V, Q])
+        if name == "q_out" and into == Q:
+            into = kw[r.choice("qkv")]
+        span = 2 * (kw["o_tok"] * T if into == Q else page * pages + head * Hkv if into in (K, V) else 512 * T)
+        kw[name] = into + align * r.randint(-40, span // align)
+        if turn % 20 == 0:   # in place, with k and v beside q in a fused projection, or a row too far in
+            kw.update(q=base, q_out=base, k=base + 256 * Hq - 256 * (turn % 40 == 0), v=base + 256 * (Hq + Hkv), o_head=128,
+                      q_head=128, kv_head=128, pos=base + (3 << 24), freq=base + (4 << 24), slots=base + (5 << 24),
+                      status=base + (6 << 24), **{x: 128 * (Hq + 2 * Hkv) for x in ("q_tok", "o_tok", "kv_tok")})
+            name = "fused"
+        ins = {"q": spans(kw["q"], T, kw["q_tok"], Hq, kw["q_head"], 256),
+               "k": spans(kw["k"], T, kw["kv_tok"], Hkv, kw["kv_head"], 256),
+               "v": spans(kw["v"], T, kw["kv_tok"], Hkv, kw["kv_head"], 256),
+               "pos": [(kw["pos"] + 4 * a * kw["pos_row"], kw["pos"] + 4 * a * kw["pos_row"] + 4 * T) for a in (0, 1)],
+               "freq": [(kw["freq"], kw["freq"] + 512)], "slots": [(kw["slots"], kw["slots"] + 8 * T)],
+               "status": [(kw["status"], kw["status"] + 4)]}
+        pools = [spans(x, pages, page, Hkv, head, 4096) for x in (K, V)]
+        out = spans(kw["q_out"], T, kw["o_tok"], Hq, kw["o_head"], 256)
+        if (kw["q"], kw["q_tok"], kw["q_head"]) == (kw["q_out"], kw["o_tok"], kw["o_head"]):
+            pairs = [(x, out) for n, x in ins.items() if n != "q"]
+        else:
+            pairs = [(x, out) for x in ins.values()]
+        pairs += [(x, p) for x in (out, *ins.values()) for p in pools]
+        want = any(a < d and c < b for x, y in pairs for a, b in x for c, d in y)
+        code = rope(**kw)
+        assert (code == L.PKA_ERR_INVALID_ARG) == want, (kw, code)
+        seen.setdefault(name, set()).add(want)
+    assert all(x == {True, False} for x in seen.values()) and len(seen) == 9
