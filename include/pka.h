@@ -741,7 +741,7 @@ int pka_status_check(int32_t* status_dev, void* stream);
  * k, v         rows [num_tokens] x [num_kv_heads] x D, one set of strides.
  * head_dim     D; must be 128.
  * positions    int32 [num_axes, num_tokens] device, rows positions_stride
- *              apart: each token's position on every axis (one axis: its place in the
+ *              apart (0: one row for all axes): each token's position on every axis (one axis: its place in the
  *              sequence; three: time, height and width of an image's or video's
  *              patch).  Any value, negative ones included.
  * inv_freq     float64 [rotary_dim / 2] device: radians per position.

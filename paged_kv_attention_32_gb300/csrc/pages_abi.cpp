@@ -170,7 +170,7 @@ int paged_rope_append(const void* q, int64_t q_stride_tok, int64_t q_stride_head
     }
     PKA_CHECK_ARG(end == rotary_dim / 2, "the sections cover %lld frequencies, rotary_dim has %d", (long long)end,
                   rotary_dim / 2);
-    PKA_CHECK_ARG(num_axes == 1 || positions_stride >= num_tokens, "positions rows of %lld entries, row stride %lld",
+    PKA_CHECK_ARG(num_axes == 1 || positions_stride == 0 || positions_stride >= num_tokens, "positions rows of %lld entries, row stride %lld",
                   (long long)num_tokens, (long long)positions_stride);
     PKA_CHECK_ARG(aligned(positions, 4) && aligned(inv_freq, 8), "positions or inv_freq is not aligned");
   }

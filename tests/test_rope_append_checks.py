@@ -22,6 +22,12 @@ def test_no_tokens_need_no_positions():
         assert rope(**(none | kw)) == L.PKA_ERR_INVALID_ARG
 
 
+@pytest.mark.skipif(torch.cuda.is_available(), reason="a call that is taken would run at these addresses")
+def test_one_row_of_positions_for_all_axes():
+    assert rope(pos_row=0) == rope(pos_row=8) == L.PKA_ERR_CUDA
+    assert rope(pos_row=1) == rope(pos_row=-8) == L.PKA_ERR_INVALID_ARG
+
+
 def rows_meet(n, outer, m, inner, row):
     """By listing all rows."""
     starts = sorted(i * outer + j * inner for i in range(n) for j in range(m))
