@@ -153,6 +153,21 @@ PyObject* pack(std::initializer_list<at::Tensor> list) {
   return tuple;
 }
 
+// The stride of a dimension; of one of size 1, whose own says nothing, that of a dense tensor.
+int64_t stride_of(const at::Tensor& t, int64_t d) {
+  if (t.size(d) > 1) return t.stride(d);
+  int64_t n = 1;
+  for (int64_t i = d + 1; i < t.dim(); ++i) n *= std::max<int64_t>(1, t.size(i));
+  return n;
+}
+// The same shape, and rows at the same places.
+bool alike(const at::Tensor& x, const at::Tensor& y) {
+  if (!x.sizes().equals(y.sizes())) return false;
+  for (int64_t d = 0; d < x.dim(); ++d)
+    if (x.size(d) > 1 && x.stride(d) != y.stride(d)) return false;
+  return true;
+}
+
 // Rows, width and row stride of block tables.
 struct Tables {
   int32_t rows, width;
@@ -173,11 +188,11 @@ struct Pools {
   int32_t heads, page_size, dim;
 };
 Pools pools_of(const at::Tensor& k, const at::Tensor& v) {
-  if (k.dim() != 4 || !v.sizes().equals(k.sizes()) || !v.strides().equals(k.strides()))
+  if (k.dim() != 4 || !alike(k, v))
     bad("k_pages and v_pages must be [num_pages, num_kv_heads, page_size, head_dim] with the same strides");
-  Pools p{k.size(0), k.stride(0), k.stride(1), Args::fit32("num_kv_heads", k.size(1)),
+  Pools p{k.size(0), stride_of(k, 0), stride_of(k, 1), Args::fit32("num_kv_heads", k.size(1)),
           Args::fit32("page_size", k.size(2)), Args::fit32("head_dim", k.size(3))};
-  if (k.stride(3) != 1 || k.stride(2) != p.dim) bad("each page's slots must be dense rows of head_dim elements");
+  if (k.stride(3) != 1 || stride_of(k, 2) != p.dim) bad("each page's slots must be dense rows of head_dim elements");
   return p;
 }
 
@@ -216,7 +231,7 @@ PyObject* rope_append(Args a) {
   if (k.dim() != 3 || k.size(1) != p.heads || k.size(2) != p.dim || !v.sizes().equals(k.sizes()))
     bad("k and v must be [T, " + std::to_string(p.heads) + ", " + std::to_string(p.dim) + "]");
   const int64_t T = k.size(0);
-  if (T > 0 && (k.stride(2) != 1 || !v.strides().equals(k.strides())))
+  if (T > 0 && (k.stride(2) != 1 || !alike(k, v)))
     bad("k and v must have the same strides and a dense last dimension");
   if (slots.numel() != T || !slots.is_contiguous()) bad("slot_map needs one contiguous entry per token");
   at::Tensor out;
@@ -233,10 +248,10 @@ PyObject* rope_append(Args a) {
         bad("q_out must have the shape of q and a dense last dimension");
       out = *q_out;
     }
-    strides[0] = q->stride(0);
-    strides[1] = q->stride(1);
-    strides[2] = out.stride(0);
-    strides[3] = out.stride(1);
+    strides[0] = stride_of(*q, 0);
+    strides[1] = stride_of(*q, 1);
+    strides[2] = stride_of(out, 0);
+    strides[3] = stride_of(out, 1);
   } else if (q_out != nullptr) {
     bad("q_out without q");
   }
@@ -261,7 +276,7 @@ PyObject* rope_append(Args a) {
   }
   const bool any = heads > 0 && T > 0;
   const int rc = paged_rope_append(any ? q->data_ptr() : nullptr, strides[0], strides[1], any ? out.data_ptr() : nullptr,
-                                   strides[2], strides[3], any ? heads : 0, ptr(k), ptr(v), k.stride(0), k.stride(1),
+                                   strides[2], strides[3], any ? heads : 0, ptr(k), ptr(v), stride_of(k, 0), stride_of(k, 1),
                                    p.heads, p.dim, static_cast<const int32_t*>(pos != nullptr ? pos->data_ptr() : nullptr),
                                    pos_stride, static_cast<const double*>(ptr(freq)), 2 * half, axes, section, pairs,
                                    static_cast<const int64_t*>(ptr(slots)), T, ptr(kp), ptr(vp), p.pages, p.page_size,
@@ -460,7 +475,7 @@ PyObject* prefix_decode_run(PyObject* plan, Args a) {
     w = new_tensor({f[12]}, at::kByte, dev);
   }
   const int rc = paged_prefix_decode_run(
-      reinterpret_cast<const pka_prefix_plan*>(f[0]), ptr(q), q.stride(0), q.stride(1), ptr(kp), ptr(vp), p.page_stride,
+      reinterpret_cast<const pka_prefix_plan*>(f[0]), ptr(q), stride_of(q, 0), stride_of(q, 1), ptr(kp), ptr(vp), p.page_stride,
       p.head_stride, static_cast<int32_t*>(ptr(tables)), row, static_cast<int32_t*>(ptr(lens)),
       static_cast<float*>(ptr(sinks)), ptr(o), l.defined() ? static_cast<float*>(ptr(l)) : nullptr,
       w.defined() ? ptr(w) : nullptr, w.defined() ? w.nbytes() : 0, current_stream());
