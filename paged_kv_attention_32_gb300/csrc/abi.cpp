@@ -119,7 +119,7 @@ int place_decode_plan(pka_plan& next, pka_plan& old, cudaStream_t stream) {
       host_capacity = 0;
       pageable.reset(new (std::nothrow) uint8_t[total]);
       if (pageable == nullptr) {
-        if (grow) (void)cudaFree(dev_buf);
+        if (grow) ignored(cudaFree(dev_buf));
         return fail(PKA_ERR_INVALID_ARG, "out of host memory");
       }
     }
@@ -131,8 +131,8 @@ int place_decode_plan(pka_plan& next, pka_plan& old, cudaStream_t stream) {
   const cudaError_t e = cudaMemcpyAsync(dev_buf, img, total, cudaMemcpyHostToDevice, stream);
   if (e != cudaSuccess) {
     const int rc = cuda_fail(e, "cudaMemcpyAsync(plan)");
-    if (grow) (void)cudaFree(dev_buf);
-    if (new_stage) (void)cudaFreeHost(host_stage);
+    if (grow) ignored(cudaFree(dev_buf));
+    if (new_stage) ignored(cudaFreeHost(host_stage));
     return rc;
   }
   // from here on the device has the new plan; a copy that no event follows is waited for
@@ -140,8 +140,8 @@ int place_decode_plan(pka_plan& next, pka_plan& old, cudaStream_t stream) {
     (void)cudaGetLastError();
     (void)cudaStreamSynchronize(stream);
   }
-  if (grow && cudaFree(old.dev_buf) != cudaSuccess) (void)cudaGetLastError();
-  if (new_stage && cudaFreeHost(old.host_stage) != cudaSuccess) (void)cudaGetLastError();
+  if (grow) ignored(cudaFree(old.dev_buf));
+  if (new_stage) ignored(cudaFreeHost(old.host_stage));
   old.dev_buf = dev_buf;
   old.dev_capacity = dev_capacity;
   old.device = device;
@@ -189,11 +189,11 @@ int pka::replace_decode_plan(pka_plan& p, pka_plan&& fresh, cudaStream_t stream)
 
 void pka::release_decode_plan(pka_plan& p) {
   if (p.stage_done != nullptr) {
-    cudaEventSynchronize(p.stage_done);   // the image is not freed under a pending copy
-    cudaEventDestroy(p.stage_done);
+    ignored(cudaEventSynchronize(p.stage_done));   // the image is not freed under a pending copy
+    ignored(cudaEventDestroy(p.stage_done));
   }
-  if (p.host_stage != nullptr) cudaFreeHost(p.host_stage);
-  if (p.dev_buf != nullptr) cudaFree(p.dev_buf);
+  if (p.host_stage != nullptr) ignored(cudaFreeHost(p.host_stage));
+  if (p.dev_buf != nullptr) ignored(cudaFree(p.dev_buf));
 }
 
 namespace {
@@ -688,7 +688,7 @@ int batch_prefill_plan_fixed(pka_prefill_plan** plan_out, const pka_prefill_desc
 
 void batch_prefill_plan_destroy(pka_prefill_plan* plan) {
   if (plan == nullptr) return;
-  if (plan->dev_buf != nullptr) cudaFree(plan->dev_buf);
+  if (plan->dev_buf != nullptr) ignored(cudaFree(plan->dev_buf));
   delete plan;
 }
 

@@ -46,6 +46,12 @@ inline int cuda_fail(cudaError_t e, const char* what) {
   return fail(PKA_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
+// For waits and releases that nothing depends on: what CUDA refuses there (it does while a
+// stream of this thread captures) is not found by the next launch either.
+inline void ignored(cudaError_t e) {
+  if (e != cudaSuccess) (void)cudaGetLastError();
+}
+
 inline bool aligned(const void* p, uintptr_t n) {
   return (reinterpret_cast<uintptr_t>(p) % n) == 0;
 }

@@ -44,8 +44,9 @@ int install_latent_plan(pka_latent_plan& p, pka_latent_plan&& next, cudaStream_t
     PKA_CUDA_TRY(cudaMalloc(&next.dev_buf, next.capacity), "cudaMalloc(latent plan)");
     const cudaError_t e = cudaMallocHost(&next.host_stage, next.capacity);
     if (e != cudaSuccess) {
-      cudaFree(next.dev_buf);
-      return cuda_fail(e, "cudaMallocHost(plan image)");
+      const int rc = cuda_fail(e, "cudaMallocHost(plan image)");
+      ignored(cudaFree(next.dev_buf));
+      return rc;
     }
   }
   uint8_t* base = static_cast<uint8_t*>(next.dev_buf);
@@ -75,8 +76,8 @@ int install_latent_plan(pka_latent_plan& p, pka_latent_plan&& next, cudaStream_t
   cudaError_t e = cudaMemcpyAsync(base, img, total, cudaMemcpyHostToDevice, stream);
   if (e != cudaSuccess) {
     if (grow) {
-      cudaFree(next.dev_buf);
-      cudaFreeHost(next.host_stage);
+      ignored(cudaFree(next.dev_buf));
+      ignored(cudaFreeHost(next.host_stage));
     }
     return cuda_fail(e, "cudaMemcpyAsync(latent plan)");
   }
@@ -87,8 +88,8 @@ int install_latent_plan(pka_latent_plan& p, pka_latent_plan&& next, cudaStream_t
     e = cudaStreamSynchronize(stream);
   }
   if (grow) {
-    cudaFree(p.dev_buf);
-    cudaFreeHost(p.host_stage);
+    ignored(cudaFree(p.dev_buf));
+    ignored(cudaFreeHost(p.host_stage));
   }
   p = std::move(next);
   return e == cudaSuccess ? PKA_OK : cuda_fail(e, "cudaEventRecord(plan upload)");
@@ -247,11 +248,11 @@ int paged_latent_decode_plan_update(pka_latent_plan* p, int32_t batch_size,
 void paged_latent_decode_plan_destroy(pka_latent_plan* plan) {
   if (plan == nullptr) return;
   if (plan->stage_done != nullptr) {
-    cudaEventSynchronize(plan->stage_done);   // the image is not freed under a pending copy
-    cudaEventDestroy(plan->stage_done);
+    ignored(cudaEventSynchronize(plan->stage_done));   // the image is not freed under a pending copy
+    ignored(cudaEventDestroy(plan->stage_done));
   }
-  if (plan->host_stage != nullptr) cudaFreeHost(plan->host_stage);
-  if (plan->dev_buf != nullptr) cudaFree(plan->dev_buf);
+  if (plan->host_stage != nullptr) ignored(cudaFreeHost(plan->host_stage));
+  if (plan->dev_buf != nullptr) ignored(cudaFree(plan->dev_buf));
   delete plan;
 }
 

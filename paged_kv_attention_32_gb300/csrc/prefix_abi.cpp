@@ -49,8 +49,9 @@ int install_prefix_plan(pka_prefix_plan& p, pka_prefix_plan&& next, cudaStream_t
     PKA_CUDA_TRY(cudaMalloc(&next.dev_buf, next.capacity), "cudaMalloc(prefix plan)");
     const cudaError_t e = cudaMallocHost(&next.host_stage, next.capacity);
     if (e != cudaSuccess) {
-      cudaFree(next.dev_buf);
-      return cuda_fail(e, "cudaMallocHost(plan image)");
+      const int rc = cuda_fail(e, "cudaMallocHost(plan image)");
+      ignored(cudaFree(next.dev_buf));
+      return rc;
     }
   }
   uint8_t* base = static_cast<uint8_t*>(next.dev_buf);
@@ -68,8 +69,8 @@ int install_prefix_plan(pka_prefix_plan& p, pka_prefix_plan&& next, cudaStream_t
   cudaError_t e = cudaMemcpyAsync(base, img, total, cudaMemcpyHostToDevice, stream);
   if (e != cudaSuccess) {
     if (grow) {
-      cudaFree(next.dev_buf);
-      cudaFreeHost(next.host_stage);
+      ignored(cudaFree(next.dev_buf));
+      ignored(cudaFreeHost(next.host_stage));
     }
     return cuda_fail(e, "cudaMemcpyAsync(prefix plan)");
   }
@@ -80,8 +81,8 @@ int install_prefix_plan(pka_prefix_plan& p, pka_prefix_plan&& next, cudaStream_t
     e = cudaStreamSynchronize(stream);
   }
   if (grow) {
-    if (cudaFree(p.dev_buf) != cudaSuccess) (void)cudaGetLastError();
-    if (cudaFreeHost(p.host_stage) != cudaSuccess) (void)cudaGetLastError();
+    ignored(cudaFree(p.dev_buf));
+    ignored(cudaFreeHost(p.host_stage));
   }
   keep_decode_buffers(next.base, p.base);   // for a batch that shares nothing
   p = std::move(next);
@@ -177,11 +178,11 @@ int paged_prefix_decode_plan_update(pka_prefix_plan* p, int32_t batch_size, cons
 void paged_prefix_decode_plan_destroy(pka_prefix_plan* p) {
   if (p == nullptr) return;
   if (p->stage_done != nullptr) {
-    cudaEventSynchronize(p->stage_done);   // the image is not freed under a pending copy
-    cudaEventDestroy(p->stage_done);
+    ignored(cudaEventSynchronize(p->stage_done));   // the image is not freed under a pending copy
+    ignored(cudaEventDestroy(p->stage_done));
   }
-  if (p->host_stage != nullptr) cudaFreeHost(p->host_stage);
-  if (p->dev_buf != nullptr) cudaFree(p->dev_buf);
+  if (p->host_stage != nullptr) ignored(cudaFreeHost(p->host_stage));
+  if (p->dev_buf != nullptr) ignored(cudaFree(p->dev_buf));
   release_decode_plan(p->base);
   delete p;
 }

@@ -41,8 +41,11 @@ int g_plain = 0, g_merges = 0;
     }                                                                                    \
   } while (0)
 
+// "capture": what a thread may not call while a stream of it captures.
 bool refused(const char* name) {
-  if (g_refuse != name) return false;
+  const bool unsafe = std::strcmp(name, "cudaMalloc") == 0 || std::strcmp(name, "cudaMallocHost") == 0 ||
+                      std::strcmp(name, "cudaFree") == 0 || std::strcmp(name, "cudaEventSynchronize") == 0;
+  if (g_refuse != name && !(g_refuse == "capture" && unsafe)) return false;
   ++g_refused;
   return g_last = true;
 }
@@ -268,6 +271,13 @@ void runs_as(const pka_prefix_plan* p, const Batch& b) {
 
 void nothing_left() { REQUIRE(g_device.size() == g_kept && g_pinned.empty() && g_events == 0); }
 
+void forget_kept() {
+  nothing_left();
+  for (const auto& [q, n] : g_device) std::free(const_cast<void*>(q));
+  g_device.clear();
+  g_kept = 0;
+}
+
 pka_decode_desc g_desc;
 
 int make(const Batch& b, pka_plan** p) {
@@ -294,7 +304,7 @@ void destroy(pka_plan* p) { paged_decode_plan_destroy(p); }
 void destroy(pka_prefix_plan* p) { paged_prefix_decode_plan_destroy(p); }
 
 const char* const kCalls[] = {"cudaMalloc",      "cudaMallocHost",  "cudaMemcpyAsync",      "cudaMemsetAsync", "cudaGetDevice",
-                              "cudaEventCreate", "cudaEventRecord", "cudaEventSynchronize", "cudaFree"};
+                              "cudaEventCreate", "cudaEventRecord", "cudaEventSynchronize", "cudaFree",        "capture"};
 
 // Plans of Plan's kind made, and updated from each batch to each, while each call is refused.
 template <typename Plan>
@@ -306,13 +316,20 @@ void refuse_all(const std::vector<Batch>& batches) {
       g_refused = 0;
       const int rc = make(b, &p);
       g_refuse.clear();
+      REQUIRE(!g_last);   // told of by the code
       REQUIRE(rc == PKA_OK || (rc == PKA_ERR_CUDA && p == nullptr && g_refused > 0));
       if (rc == PKA_OK) {
         runs_as(p, b);
         destroy(p);
       }
-      g_last = false;
       nothing_left();
+      // a plan destroyed then: its memory may stay, an error that the next launch would find may not
+      REQUIRE(make(b, &p) == PKA_OK);
+      g_refuse = call;
+      destroy(p);
+      g_refuse.clear();
+      REQUIRE(!g_last && g_pinned.empty() && g_events == 0);
+      forget_kept();
     }
 
   // from a new plan, and from one that has been every other batch and so has the largest buffers
@@ -341,9 +358,7 @@ void refuse_all(const std::vector<Batch>& batches) {
           }
           destroy(p);
           nothing_left();
-          for (const auto& [q, n] : g_device) std::free(const_cast<void*>(q));
-          g_device.clear();
-          g_kept = 0;
+          forget_kept();
         }
 }
 
