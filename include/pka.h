@@ -287,6 +287,9 @@ int paged_decode_plan_export(const pka_plan* plan, int32_t* items, int32_t* n_ch
  *                 token t of request b is in page block_tables[b, t/page_size],
  *                 slot t % page_size (batch_decode_with_paged_kv_cache,
  *                 block_tables).  Entries past a request's last page are not read.
+ *                 Slots past its last key may hold anything; values of keys of its
+ *                 own that the mask hides from some of its rows have to be finite
+ *                 (their weight is 0, and 0 times an infinity is NaN).
  * seq_lens_kv_dev int32 [B] device; read only when the plan is not frozen
  *                 (may be NULL for a frozen plan).
  * sinks           NULL or fp32 [Hq] device: per-head sink logits joining each
@@ -467,9 +470,11 @@ typedef struct pka_prefix_plan pka_prefix_plan; /* opaque */
  *              a dense mask, kv_len - q_len + 1 with a causal one.
  * min_shared_bytes  where sharing keeps fewer bytes of K and V than this from being
  *              read again, the run is that of paged_decode_plan (split_waves,
- *              min_chunk_tokens and mma_min_rows are used then only); else the
- *              workspace holds the fp32 partial states of all pieces.  Negative: shared
- *              where by measured rates it is the faster.
+ *              min_chunk_tokens and mma_min_rows are used then only); else it is
+ *              on tensor cores whatever mma_min_rows says, which round each weight to
+ *              the input type (half a step; the CUDA-core decode keeps 32 bits),
+ *              and the workspace holds the fp32 partial states of all pieces.
+ *              Negative: shared where by measured rates it is the faster.
  */
 int paged_prefix_decode_plan(pka_prefix_plan** plan_out, const pka_decode_desc* desc,
                              const int32_t* seq_lens_kv_host, const int32_t* qo_indptr_host,

@@ -17,7 +17,10 @@
 // memory in turn (lengths, then entries) and the cluster barriers between the steps; for
 // large tables the entries that 16 SMs' registers hold on their way.  Fork of 448 rows 7 us;
 // release from 64 rows 6.4 us from start to end, from 2048 rows, 530000 entries, 20 us, of which
-// 5 go to the marks, 5 to joining them; compaction of 256 rows 20 us.
+// 5 go to the marks, 5 to joining them; compaction of 256 rows 20 us.  Beyond that time goes with
+// the entries on 16 SMs, and with the ranges of the pool, each of which reads the tables again:
+// release from 16384 rows of 512 entries 74 us in a pool of 2^19 pages, 603 in one of 2^22 (seven
+// ranges), compaction 164 and 1625; from 2048 rows in a pool of 2^22 pages 224 and 883.
 #include <algorithm>
 
 #include "device_common.cuh"

@@ -31,7 +31,7 @@ constexpr unsigned FULL = 0xffffffffu;
 constexpr int kStages = 2;
 constexpr int kUnit = kMmaUnitTok;
 constexpr int kThreads = kOwnWarps * 32;
-constexpr int kOwnRegs = 168;   // three CTAs an SM, or one beside the prefix kernel's 8 warps of 128
+constexpr int kOwnRegs = 168;   // three CTAs an SM, or one beside the prefix kernel's 11 warps of 112
 
 // As tma_load_kv_pair_elect; what it brings is the first to leave L2 again: it is read once,
 // and the partial states that the merge reads are to stay.
