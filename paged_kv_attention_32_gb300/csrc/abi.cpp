@@ -7,7 +7,7 @@
 #include <cstring>
 #include <memory>
 #include <new>
-#include <string>
+#include <vector>
 
 #include "host_common.h"
 #include "kernels.h"
@@ -18,22 +18,20 @@
 namespace pka {
 
 namespace {
-thread_local std::string g_last_error;
+thread_local char g_last_error[1024];   // told without an allocation: memory may be what ran out
 }
 
 int fail(int code, const char* fmt, ...) {
-  char buf[1024];
   va_list ap;
   va_start(ap, fmt);
-  vsnprintf(buf, sizeof(buf), fmt, ap);
+  vsnprintf(g_last_error, sizeof(g_last_error), fmt, ap);
   va_end(ap);
-  g_last_error = buf;
   return code;
 }
 
-void clear_error() { g_last_error.clear(); }
+void clear_error() { g_last_error[0] = '\0'; }
 
-const char* last_error() { return g_last_error.c_str(); }
+const char* last_error() { return g_last_error; }
 
 int check_device(int plan_device) {
   int dev = -1;
@@ -293,9 +291,11 @@ int paged_decode_plan(pka_plan** plan_out, const pka_decode_desc* desc,
   *plan_out = nullptr;
   pka_plan* p = new (std::nothrow) pka_plan();
   if (p == nullptr) return fail(PKA_ERR_INVALID_ARG, "out of host memory");
-  int rc = build_decode_plan(*p, *desc, seq_lens_kv_host, qo_indptr_host);
-  if (rc == PKA_OK && !(desc->flags & PKA_PLAN_HOST_ONLY))
-    rc = upload_decode_plan(*p, static_cast<cudaStream_t>(stream));
+  const int rc = guarded([&] {
+    const int built = build_decode_plan(*p, *desc, seq_lens_kv_host, qo_indptr_host);
+    if (built != PKA_OK || (desc->flags & PKA_PLAN_HOST_ONLY)) return built;
+    return upload_decode_plan(*p, static_cast<cudaStream_t>(stream));
+  });
   if (rc != PKA_OK) {
     paged_decode_plan_destroy(p);
     return rc;
@@ -313,11 +313,13 @@ int paged_decode_plan_update(pka_plan* p, int32_t batch_size, const int32_t* seq
   PKA_CHECK_ARG(p != nullptr, "plan must not be NULL");
   pka_decode_desc d = p->desc;
   d.batch_size = batch_size;
-  pka_plan fresh;
-  int rc = build_decode_plan(fresh, d, seq_lens_kv_host, qo_indptr_host);
+  const int rc = guarded([&] {
+    pka_plan fresh;
+    const int built = build_decode_plan(fresh, d, seq_lens_kv_host, qo_indptr_host);
+    if (built != PKA_OK) return built;
+    return replace_decode_plan(*p, std::move(fresh), static_cast<cudaStream_t>(stream));
+  });
   if (rc != PKA_OK) return rc;   // the old plan stays as it was
-  rc = replace_decode_plan(*p, std::move(fresh), static_cast<cudaStream_t>(stream));
-  if (rc != PKA_OK) return rc;
   if (workspace_bytes_out) *workspace_bytes_out = (size_t)p->workspace_bytes;
   return PKA_OK;
 }
@@ -647,8 +649,10 @@ int batch_prefill_plan(pka_prefill_plan** plan_out, const pka_prefill_desc* desc
   NvtxRange nvtx_range("pka::batch_prefill_plan");
   clear_error();
   PKA_CHECK_ARG(plan_out != nullptr && desc != nullptr, "plan_out and desc must not be NULL");
-  const int rc = make_prefill_plan(plan_out, *desc, qo_indptr_host, kv_indptr_host, false,
-                                   num_tiles_out, static_cast<cudaStream_t>(stream));
+  const int rc = guarded([&] {
+    return make_prefill_plan(plan_out, *desc, qo_indptr_host, kv_indptr_host, false, num_tiles_out,
+                             static_cast<cudaStream_t>(stream));
+  });
   if (rc == PKA_OK && workspace_bytes_out) *workspace_bytes_out = 0;
   return rc;
 }
@@ -665,17 +669,18 @@ int batch_prefill_plan_fixed(pka_prefill_plan** plan_out, const pka_prefill_desc
   PKA_CHECK_ARG(seq_len_q >= 1 && seq_len_kv >= 1, "seq_len_q and seq_len_kv must be >= 1");
   PKA_CHECK_ARG((int64_t)desc->batch_size * std::max(seq_len_q, seq_len_kv) <= INT32_MAX,
                 "batch_size * seq_len exceeds 2^31 - 1 rows");
-  std::vector<int32_t> qo(desc->batch_size + 1), kv(desc->batch_size + 1);
-  for (int32_t b = 0; b <= desc->batch_size; ++b) {
-    qo[b] = b * seq_len_q;
-    kv[b] = b * seq_len_kv;
-  }
   pka_prefill_plan* p = new (std::nothrow) pka_prefill_plan();
   if (p == nullptr) return fail(PKA_ERR_INVALID_ARG, "out of host memory");
-  int rc = build_prefill_plan(*p, *desc, qo.data(), kv.data(), window_starts_host,
-                              window_ends_host);
-  if (rc == PKA_OK && !(desc->flags & PKA_PLAN_HOST_ONLY))
-    rc = upload_prefill_plan(*p, static_cast<cudaStream_t>(stream));
+  const int rc = guarded([&] {
+    std::vector<int32_t> qo(desc->batch_size + 1), kv(desc->batch_size + 1);
+    for (int32_t b = 0; b <= desc->batch_size; ++b) {
+      qo[b] = b * seq_len_q;
+      kv[b] = b * seq_len_kv;
+    }
+    const int built = build_prefill_plan(*p, *desc, qo.data(), kv.data(), window_starts_host, window_ends_host);
+    if (built != PKA_OK || (desc->flags & PKA_PLAN_HOST_ONLY)) return built;
+    return upload_prefill_plan(*p, static_cast<cudaStream_t>(stream));
+  });
   if (rc != PKA_OK) {
     batch_prefill_plan_destroy(p);
     return rc;

@@ -2,11 +2,13 @@
 // entry points of abi.cpp and prefix_abi.cpp with their planners over a fake runtime that refuses
 // the calls it is told to.  A plan made in vain leaks nothing.  An update, to a batch that shares or
 // one that does not, succeeds or leaves the plan as it was: either way what a run launches with is
-// one batch's, whole, and no error is left for the next launch to find.
+// one batch's, whole, and no error is left for the next launch to find.  So too where host memory
+// runs out, which no entry point lets out as an exception.
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
 #include <map>
+#include <new>
 #include <string>
 #include <vector>
 
@@ -23,6 +25,7 @@ size_t g_kept = 0;        // of them those whose release was refused
 int g_events = 0;
 std::string g_refuse;     // the call that fails
 int g_refused = 0;
+int64_t g_news = -1;      // host allocations until all fail, -1: none does
 bool g_last = false;      // a refusal that cudaGetLastError would still tell of
 // what the last run launched
 const pka_plan* g_plan = nullptr;
@@ -61,7 +64,10 @@ bool inside(const void* p, size_t n) {
 cudaError_t allocate(std::map<const void*, size_t>& all, void** p, size_t n) {
   *p = std::aligned_alloc(256, (n + 255) / 256 * 256);
   std::memset(*p, 0xee, n);
+  const int64_t news = g_news;   // not the runtime's own
+  g_news = -1;
   all[*p] = n;
+  g_news = news;
   return cudaSuccess;
 }
 
@@ -72,6 +78,16 @@ void release(std::map<const void*, size_t>& all, void* p) {
 }
 
 }  // namespace
+
+void* operator new(size_t n) {
+  if (g_news == 0) throw std::bad_alloc();
+  if (g_news > 0) --g_news;
+  void* p = std::malloc(n > 0 ? n : 1);
+  if (p == nullptr) throw std::bad_alloc();
+  return p;
+}
+void operator delete(void* p) noexcept { std::free(p); }
+void operator delete(void* p, size_t) noexcept { std::free(p); }
 
 extern "C" {
 cudaError_t cudaMalloc(void** p, size_t n) {
@@ -362,6 +378,52 @@ void refuse_all(const std::vector<Batch>& batches) {
         }
 }
 
+// Host memory that runs out at every allocation of a plan in turn.
+template <typename Plan>
+void run_out_all(const Batch& from, const Batch& to) {
+  for (int64_t at = 0, done = 0; !done; ++at) {
+    Plan* p = nullptr;
+    g_news = at;
+    const int rc = make(from, &p);
+    done = g_news > 0;
+    g_news = -1;
+    REQUIRE(rc == PKA_OK ? p != nullptr : rc == PKA_ERR_INVALID_ARG && p == nullptr && !done);
+    if (rc == PKA_OK) {
+      runs_as(p, from);
+      destroy(p);
+    }
+    nothing_left();
+  }
+  Plan* p = nullptr;
+  REQUIRE(make(from, &p) == PKA_OK);
+  for (int64_t at = 0, done = 0; !done; ++at) {
+    g_news = at;
+    const int rc = update(p, to);
+    done = g_news > 0;
+    g_news = -1;
+    REQUIRE(rc == PKA_OK || (rc == PKA_ERR_INVALID_ARG && !done));
+    runs_as(p, rc == PKA_OK ? to : from);
+    if (rc == PKA_OK) REQUIRE(update(p, from) == PKA_OK);
+  }
+  destroy(p);
+  nothing_left();
+}
+
+// The same of the prefill's plans.
+template <typename Make>
+void run_out_prefill(Make make_plan) {
+  for (int64_t at = 0, done = 0; !done; ++at) {
+    pka_prefill_plan* p = nullptr;
+    g_news = at;
+    const int rc = make_plan(&p);
+    done = g_news > 0;
+    g_news = -1;
+    REQUIRE(rc == PKA_OK ? p != nullptr : rc == PKA_ERR_INVALID_ARG && p == nullptr && !done);
+    batch_prefill_plan_destroy(p);
+    nothing_left();
+  }
+}
+
 }  // namespace
 
 int main() {
@@ -384,6 +446,27 @@ int main() {
   for (size_t i = 0; i < none_many.lens.size(); ++i) none_many.lens[i] += (int32_t)(i % 600);
   refuse_all<pka_plan>({few, none, alone, many, none_many});
   refuse_all<pka_prefix_plan>({few, none, other, alone, many, none_many});
+  for (const Batch& from : {few, alone, many})
+    for (const Batch& to : {few, none, other}) {
+      run_out_all<pka_plan>(from, to);
+      run_out_all<pka_prefix_plan>(from, to);
+    }
+  pka_prefill_desc f{};
+  f.batch_size = 3;
+  f.num_qo_heads = kHeads;
+  f.num_kv_heads = kKvHeads;
+  f.head_dim = 128;
+  f.sm_scale = 0.1f;
+  f.output_scale = 1.f;
+  f.window_left = -1;
+  f.mask = PKA_MASK_CAUSAL;
+  const int32_t rows[] = {0, 200, 200, 1000};
+  size_t bytes = 0;
+  int32_t tiles = 0;
+  run_out_prefill([&](pka_prefill_plan** p) { return batch_prefill_plan(p, &f, rows, rows, &bytes, &tiles, nullptr); });
+  run_out_prefill([&](pka_prefill_plan** p) {
+    return batch_prefill_plan_fixed(p, &f, 100, 150, nullptr, nullptr, &bytes, &tiles, nullptr);
+  });
   std::puts("ok");
   return 0;
 }
