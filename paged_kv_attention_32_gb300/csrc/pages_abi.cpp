@@ -105,14 +105,16 @@ bool rows_meet(const Rows& x, const Rows& y) {
     return false;
   if (x.n == y.n && x.outer == y.outer && x.m == y.m && x.inner == y.inner && x.row == y.row) {
     const bool few = x.n < x.m;   // in a step for each of the smaller count, and back
-    const int64_t n = few ? x.n : x.m, far = few ? x.outer : x.inner, m = few ? x.m : x.n, step = few ? x.inner : x.outer;
+    const int64_t n = few ? x.n : x.m, far = few ? x.outer : x.inner;
+    const int64_t m = few ? x.m : x.n, step = few ? x.inner : x.outer;
     for (int64_t i = 1 - n; i < n; ++i)
       if (step_hits(d + (__int128)i * far, m, step, x.row, false)) return true;
     return false;
   }
   // rows that lie in the other's gaps, or meet them: each of x with each of y's smaller count
   const bool few = y.m < y.n;
-  const int64_t n = few ? y.m : y.n, far = few ? y.inner : y.outer, m = few ? y.n : y.m, step = few ? y.outer : y.inner;
+  const int64_t n = few ? y.m : y.n, far = few ? y.inner : y.outer;
+  const int64_t m = few ? y.n : y.m, step = few ? y.outer : y.inner;
   for (int64_t i = 0; i < x.n; ++i)
     for (int64_t j = 0; j < x.m; ++j)
       for (int64_t k = 0; k < n; ++k) {
@@ -170,8 +172,8 @@ int paged_rope_append(const void* q, int64_t q_stride_tok, int64_t q_stride_head
     }
     PKA_CHECK_ARG(end == rotary_dim / 2, "the sections cover %lld frequencies, rotary_dim has %d", (long long)end,
                   rotary_dim / 2);
-    PKA_CHECK_ARG(num_axes == 1 || positions_stride == 0 || positions_stride >= num_tokens, "positions rows of %lld entries, row stride %lld",
-                  (long long)num_tokens, (long long)positions_stride);
+    PKA_CHECK_ARG(num_axes == 1 || positions_stride == 0 || positions_stride >= num_tokens,
+                  "positions rows of %lld entries, row stride %lld", (long long)num_tokens, (long long)positions_stride);
     PKA_CHECK_ARG(aligned(positions, 4) && aligned(inv_freq, 8), "positions or inv_freq is not aligned");
   }
   for (int64_t s : {q_stride_tok, q_stride_head, q_out_stride_tok, q_out_stride_head, kv_stride_tok, kv_stride_head,
@@ -191,13 +193,15 @@ int paged_rope_append(const void* q, int64_t q_stride_tok, int64_t q_stride_head
   const auto rows = [&](const void* p, int64_t tok, int64_t head, int32_t heads) {
     return Rows{p, num_tokens, tok, heads, head, head_dim};
   };
-  const Rows k_pool = pool(k_pages), v_pool = pool(v_pages), out = rows(q_out, q_out_stride_tok, q_out_stride_head, num_qo_heads);
+  const Rows k_pool = pool(k_pages), v_pool = pool(v_pages);
+  const Rows out = rows(q_out, q_out_stride_tok, q_out_stride_head, num_qo_heads);
   PKA_CHECK_ARG(!rows_meet(k_pool, v_pool), "k_pages and v_pages overlap");
   const Rows ins[] = {rows(q, q_stride_tok, q_stride_head, num_qo_heads),
                       rows(k, kv_stride_tok, kv_stride_head, num_kv_heads),
                       rows(v, kv_stride_tok, kv_stride_head, num_kv_heads),
                       {slot_map, 1, 0, 1, 0, 4 * num_tokens},
-                      {rotary_dim > 0 ? positions : nullptr, num_axes, num_axes > 1 ? 2 * positions_stride : 0, 1, 0, 2 * num_tokens},
+                      {rotary_dim > 0 ? positions : nullptr, num_axes, num_axes > 1 ? 2 * positions_stride : 0, 1, 0,
+                       2 * num_tokens},
                       {rotary_dim > 0 ? inv_freq : nullptr, 1, 0, 1, 0, 2 * (int64_t)rotary_dim},
                       {status, 1, 0, 1, 0, 2}};
   for (const Rows& in : ins)
@@ -209,7 +213,8 @@ int paged_rope_append(const void* q, int64_t q_stride_tok, int64_t q_stride_head
     // q itself it may be, all of it
     const bool in_place = q_out == q && q_out_stride_tok == q_stride_tok && q_out_stride_head == q_stride_head;
     for (const Rows& in : ins)
-      PKA_CHECK_ARG(in.p == nullptr || (in_place && &in == ins) || !rows_meet(in, out), "q_out overlaps an input without being q");
+      PKA_CHECK_ARG(in.p == nullptr || (in_place && &in == ins) || !rows_meet(in, out),
+                    "q_out overlaps an input without being q");
   }
   a.q = q;
   a.q_stride_tok = q_stride_tok;

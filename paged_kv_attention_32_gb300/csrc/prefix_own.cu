@@ -5,7 +5,8 @@
 // 16-row tile), which it takes as they come, through the tensor-core step of the paged decode
 // (mma.sync m16n8k16; a tile of up to 8 rows with the keys on the 16-row side).  Its copies
 // run ahead over the borders of the pieces, the next of which is taken a piece early, and
-// nothing waits for another warp: a piece ends with a 32-bit partial state of its rows.
+// nothing waits for another warp: a piece ends with a 32-bit partial state of its rows.  p is
+// rounded to the input type for the product with V, as the tensor core takes it, after its 32-bit sum.
 // HBM bounds it; what an ordinary decode of many short requests loses to CTAs that start
 // and end is the reason for the pieces (64 requests of 64 to 1024 keys: 35 us for 21 us of
 // bytes; in pieces 28 us alone, 4.9 TB/s).  A CTA of 4 warps fits beside a CTA of the prefix
